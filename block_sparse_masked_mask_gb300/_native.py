@@ -1,4 +1,5 @@
-"""ctypes loader for libattnmask.so (the C ABI in include/attn_block_mask.h).
+"""ctypes loader for libattnmask.so (the C ABI in include/attn_block_mask.h and
+include/attn_cache.h).
 
 Argument marshalling only: every step of the computation runs in the CUDA
 library.  There is no fallback: if the library is missing this module raises.
@@ -61,6 +62,30 @@ class AttnBlockMask(ctypes.Structure):
     ]
 
 
+class AttnRopePlan(ctypes.Structure):
+    """Mirror of ``attn_rope_plan`` in include/attn_cache.h."""
+    _fields_ = [("magic", ctypes.c_uint32), ("rotary_dim", c_int32), ("interleaved", c_int32),
+                ("result_factor", ctypes.c_float), ("turn", ctypes.c_uint64 * 64)]
+
+
+class AttnKVCache(ctypes.Structure):
+    """Mirror of ``attn_kv_cache`` in include/attn_cache.h."""
+    _fields_ = [
+        ("k_pages", c_void_p),
+        ("v_pages", c_void_p),
+        ("k_scale", c_void_p),
+        ("v_scale", c_void_p),
+        ("page_table", c_void_p),
+        ("status", c_void_p),
+        ("num_pages", c_int32),
+        ("num_kv_heads", c_int32),
+        ("page_size", c_int32),
+        ("head_dim", c_int32),
+        ("batch", c_int32),
+        ("max_pages", c_int32),
+    ]
+
+
 _lib = None
 
 
@@ -89,6 +114,29 @@ def _configure(L: ctypes.CDLL) -> ctypes.CDLL:
         ctypes.c_int, P(AttnMaskParams), c_void_p, c_void_p, c_void_p, P(AttnBlockMask), c_void_p,
         ctypes.c_size_t, c_void_p]
     L.attn_bwd.restype = ctypes.c_int
+    d, i64 = ctypes.c_double, ctypes.c_int64
+    L.attn_rope_plan_init.argtypes = [P(AttnRopePlan), c_int32, c_int32, d, ctypes.c_int, d, d, d, d, d]
+    L.attn_rope.argtypes = [
+        c_void_p, c_void_p, i64, i64, c_int32, c_void_p, c_void_p, i64, i64, c_int32, ctypes.c_int,
+        c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_int32, P(AttnRopePlan), c_int32, c_void_p]
+    L.attn_cache_append.argtypes = [
+        c_void_p, c_void_p, i64, i64, ctypes.c_int, c_int32, c_void_p, c_void_p, c_int32,
+        P(AttnKVCache), c_void_p]
+    L.attn_cache_fwd_workspace_size.argtypes = [P(AttnKVCache), c_int32, c_int32, c_int32, c_int32,
+                                                P(ctypes.c_size_t)]
+    L.attn_cache_fwd.argtypes = [
+        c_void_p, c_void_p, c_void_p, ctypes.c_int, c_int32, c_int32, ctypes.c_float, c_void_p,
+        c_int32, c_void_p, c_int32, ctypes.c_int, P(AttnKVCache), c_void_p, ctypes.c_size_t, c_void_p]
+    L.attn_cache_weights.argtypes = [
+        c_void_p, c_void_p, ctypes.c_int, c_int32, c_int32, ctypes.c_float, c_void_p, c_int32,
+        c_void_p, c_int32, ctypes.c_int, P(AttnKVCache), c_void_p, c_void_p, i64, c_void_p]
+    L.attn_cache_evict.argtypes = [
+        c_void_p, i64, c_void_p, c_void_p, c_int32, c_int32, c_int32, P(AttnKVCache), P(AttnKVCache),
+        c_void_p, c_void_p, i64, c_void_p, c_void_p]
+    L.attn_cache_get_status.argtypes = [P(AttnKVCache), c_void_p]
+    for f in ("attn_rope_plan_init", "attn_rope", "attn_cache_append", "attn_cache_fwd_workspace_size",
+              "attn_cache_fwd", "attn_cache_weights", "attn_cache_evict", "attn_cache_get_status"):
+        getattr(L, f).restype = ctypes.c_int
     L.attn_get_status.argtypes = [P(AttnBlockMask), c_void_p]
     L.attn_get_status.restype = ctypes.c_int
     L.attn_status_string.argtypes = [ctypes.c_int]

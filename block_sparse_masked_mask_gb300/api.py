@@ -317,3 +317,387 @@ def attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
 def attn_get_status(bm: BlockMask, stream=None) -> int:
     """Synchronise and return the device status code of the mask's error word."""
     return int(_native.lib().attn_get_status(ctypes.byref(bm.struct), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# Rotary positions and the 8-bit key / value cache (include/attn_cache.h)
+# ---------------------------------------------------------------------------
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "ramp": 3}
+
+
+class _Launch:
+    """Where a call runs: its stream's handle, with the tensors' device current
+    and new tensors allocated for that stream.  Costs nothing where the device
+    is current already and no stream is named."""
+
+    def __init__(self, device: torch.device, stream):
+        self._guards = []
+        if device.index != torch.cuda.current_device():
+            self._guards.append(torch.cuda.device(device))
+        self._stream, self._device = stream, device
+
+    def __enter__(self):
+        for g in self._guards:
+            g.__enter__()
+        if self._stream is None:
+            return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        s = self._stream
+        if not hasattr(s, "cuda_stream"):
+            s = torch.cuda.ExternalStream(int(s), device=self._device)
+        g = torch.cuda.stream(s)
+        g.__enter__()
+        self._guards.append(g)
+        return ctypes.c_void_p(s.cuda_stream)
+
+    def __exit__(self, *exc):
+        while self._guards:
+            self._guards.pop().__exit__(*exc)
+
+
+def _need_rows(t, name: str, where: str, dtypes, device=None) -> int:
+    """[tokens, heads, dim] with dense heads, tokens any distance apart (a slice
+    of a wider projection); returns that distance in elements."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise AttnError(1, f"{where}: {name} must be a CUDA tensor")
+    if device is not None and t.device != device:
+        raise AttnError(1, f"{where}: {name} is on {t.device}, expected {device}")
+    if t.dtype not in dtypes:
+        raise AttnError(1, f"{where}: {name} has dtype {t.dtype}, expected one of {dtypes}")
+    if t.dim() != 3:
+        raise AttnError(1, f"{where}: {name} must be [tokens, heads, dim]")
+    n, h, d = t.shape
+    if t.is_contiguous():
+        return h * d
+    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+        raise AttnError(1, f"{where}: the heads of {name} must be dense")
+    if n > 1 and t.stride(0) < h * d:
+        raise AttnError(1, f"{where}: the tokens of {name} overlap")
+    return t.stride(0) if n > 1 else h * d
+
+
+class RopePlan:
+    """A prepared rotation (see ``attn_rope_plan``)."""
+
+    def __init__(self, struct: _native.AttnRopePlan):
+        self.struct = struct
+        self._ref = ctypes.byref(struct)
+        self.rotary_dim = int(struct.rotary_dim)
+
+
+def attn_rope_plan(rotary_dim: int, base: float = 10000.0, interleaved: bool = False,
+                   scaling: str = "none", factor: float = 1.0, original_context: float = 0.0,
+                   alpha: float = 1.0, beta: float = 32.0, result_factor: float = 0.0) -> RopePlan:
+    """Prepare a rotation of the first ``rotary_dim`` dimensions of each head:
+    pairs (i, i + rotary_dim / 2), or neighbours when ``interleaved``.
+
+    ``scaling`` stretches the angles theta_i = base^(-2 i / rotary_dim) to
+    contexts ``factor`` times longer: "linear" divides them, "ntk" raises the
+    base, "ramp" divides only those of pairs that turn less than ``alpha``
+    times in ``original_context`` tokens, blending up to ``beta`` turns.
+    ``result_factor`` multiplies the rotated dimensions (0: 1, or
+    0.1 ln(factor) + 1 for "ramp")."""
+    if scaling not in ROPE_SCALINGS:
+        raise AttnError(1, f"attn_rope_plan: scaling must be one of {sorted(ROPE_SCALINGS)}")
+    out = _native.AttnRopePlan()
+    _check(_native.lib().attn_rope_plan_init(
+        ctypes.byref(out), int(rotary_dim), int(bool(interleaved)), float(base), ROPE_SCALINGS[scaling],
+        float(factor), float(original_context), float(alpha), float(beta), float(result_factor)),
+        "attn_rope_plan")
+    return RopePlan(out)
+
+
+def attn_rope(q: torch.Tensor, k: Optional[torch.Tensor], plan: RopePlan,
+              positions: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None,
+              seq_lens: Optional[torch.Tensor] = None, inverse: bool = False,
+              q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None, stream=None):
+    """Rotate q [T, Hq, D] and k [T, Hk, D] (or None) by their positions;
+    returns (q_out, k_out).
+
+    Positions are ``positions`` (int32 [T]), or follow from ``cu_seqlens``
+    (int32 [B + 1]): the place in the own sequence, behind the
+    ``seq_lens[b] - n`` earlier tokens where ``seq_lens`` (int32 [B]) is given.
+    ``inverse`` turns back: applied to the gradients of the rotated q and k it
+    gives those of q and k.  bf16 or fp32; the tokens of q and k may be apart
+    (slices of one projection).  ``q_out=q`` rotates in place."""
+    where = "attn_rope"
+    qs = _need_rows(q, "q", where, tuple(DTYPES))
+    T, H, D = q.shape
+    dt, dev = (q.dtype,), q.device
+    ks = kos = Hk = 0
+    if k is not None:
+        ks = _need_rows(k, "k", where, dt, dev)
+        if k.shape[0] != T or k.shape[2] != D:
+            raise AttnError(1, f"{where}: k has shape {tuple(k.shape)}, expected [{T}, heads, {D}]")
+        Hk = k.shape[1]
+    elif k_out is not None:
+        raise AttnError(1, f"{where}: k_out without k")
+    if not isinstance(plan, RopePlan):
+        raise AttnError(1, f"{where}: plan must come from attn_rope_plan")
+    batch = 0
+    if positions is not None:
+        _need(positions, "positions", where, (torch.int32,), (T,), dev)
+    elif cu_seqlens is None:
+        raise AttnError(1, f"{where}: positions or cu_seqlens is required")
+    else:
+        _need(cu_seqlens, "cu_seqlens", where, (torch.int32,), device=dev)
+        batch = cu_seqlens.numel() - 1
+        _need(seq_lens, "seq_lens", where, (torch.int32,), (batch,), dev)
+    with _Launch(dev, stream) as s:
+        if q_out is None:
+            q_out, qos = torch.empty((T, H, D), dtype=q.dtype, device=dev), H * D
+        else:
+            qos = _need_rows(q_out, "q_out", where, dt, dev)
+            if q_out.shape != q.shape:
+                raise AttnError(1, f"{where}: q_out has shape {tuple(q_out.shape)}, expected {tuple(q.shape)}")
+        if k is not None:
+            if k_out is None:
+                k_out, kos = torch.empty((T, Hk, D), dtype=q.dtype, device=dev), Hk * D
+            else:
+                kos = _need_rows(k_out, "k_out", where, dt, dev)
+                if k_out.shape != k.shape:
+                    raise AttnError(1, f"{where}: k_out has shape {tuple(k_out.shape)}, expected {tuple(k.shape)}")
+        _check(_native.lib().attn_rope(
+            q.data_ptr(), q_out.data_ptr(), qs, qos, H, k.data_ptr() if Hk else None,
+            k_out.data_ptr() if Hk else None, ks, kos, Hk, DTYPES[q.dtype], T, D,
+            None if positions is None else positions.data_ptr(),
+            None if positions is not None else cu_seqlens.data_ptr(),
+            None if positions is not None or seq_lens is None else seq_lens.data_ptr(), batch,
+            plan._ref, int(bool(inverse)), s), where)
+    return q_out, k_out
+
+
+class KVCache:
+    """A paged key / value cache in e4m3 with one power-of-two scale per page
+    and head: the C struct and the tensors it points into.
+
+    k_pages, v_pages: uint8 or float8_e4m3fn [num_pages, heads, page_size, dim];
+    k_scale, v_scale: fp32 [num_pages, heads]; page_table: int32
+    [batch, max_pages].  The caller owns them, and the sequence lengths;
+    the table may be rewritten between calls."""
+
+    def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, k_scale: torch.Tensor,
+                 v_scale: torch.Tensor, page_table: torch.Tensor, status: Optional[torch.Tensor] = None):
+        where = "KVCache"
+        codes = (torch.uint8, torch.float8_e4m3fn)
+        _need(k_pages, "k_pages", where, codes)
+        if k_pages is None or k_pages.dim() != 4:
+            raise AttnError(1, f"{where}: k_pages must be [num_pages, heads, page_size, dim]")
+        dev = k_pages.device
+        P, H, ps, D = k_pages.shape
+        for name, t, dt, shape in (("v_pages", v_pages, codes, (P, H, ps, D)),
+                                   ("k_scale", k_scale, (torch.float32,), (P, H)),
+                                   ("v_scale", v_scale, (torch.float32,), (P, H)),
+                                   ("page_table", page_table, (torch.int32,), None)):
+            if t is None:
+                raise AttnError(1, f"{where}: {name} is required")
+            _need(t, name, where, dt, shape, dev)
+        if page_table.dim() != 2:
+            raise AttnError(1, f"{where}: page_table must be [batch, max_pages]")
+        _need(status, "status", where, (torch.int32,), (1,), dev)
+        if status is None:
+            status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.k_pages, self.v_pages, self.k_scale, self.v_scale = k_pages, v_pages, k_scale, v_scale
+        self.page_table, self.status = page_table, status
+        self.device, self.num_kv_heads, self.head_dim = dev, H, D
+        self.batch, self.max_pages = page_table.shape
+        self.page_size, self.num_pages = ps, P
+        self.struct = _native.AttnKVCache(
+            k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+            page_table.data_ptr(), status.data_ptr(), P, H, ps, D, self.batch, self.max_pages)
+        self._ref = ctypes.byref(self.struct)
+
+    @classmethod
+    def empty(cls, num_pages: int, num_kv_heads: int, head_dim: int, page_table: torch.Tensor,
+              page_size: int = 64) -> "KVCache":
+        """A cache with new pages (codes 0, scales 1) on the table's device."""
+        dev = page_table.device
+        shape = (num_pages, num_kv_heads, page_size, head_dim)
+        codes = [torch.zeros(shape, dtype=torch.uint8, device=dev) for _ in range(2)]
+        scales = [torch.ones(shape[:2], dtype=torch.float32, device=dev) for _ in range(2)]
+        return cls(*codes, *scales, page_table)
+
+
+def _need_cache(cache, where: str) -> KVCache:
+    if not isinstance(cache, KVCache):
+        raise AttnError(1, f"{where}: cache must be a KVCache")
+    return cache
+
+
+def _need_seqs(cache: KVCache, cu_seqlens, seq_lens, where: str) -> None:
+    if seq_lens is None or cu_seqlens is None:
+        raise AttnError(1, f"{where}: cu_seqlens and seq_lens are required")
+    _need(cu_seqlens, "cu_seqlens", where, (torch.int32,), (cache.batch + 1,), cache.device)
+    _need(seq_lens, "seq_lens", where, (torch.int32,), (cache.batch,), cache.device)
+
+
+def attn_cache_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, cu_seqlens: torch.Tensor,
+                      seq_lens: torch.Tensor, max_new: int, stream=None) -> None:
+    """Quantise the new tokens' keys and values [T, Hk, D] (bf16 or fp32) into
+    the cache.  Sequence b's new tokens are rows cu_seqlens[b] ..
+    cu_seqlens[b + 1] - 1 and become its last ones: ``seq_lens`` counts them in.
+    ``max_new`` bounds each sequence's number of new tokens.  Their pages must
+    belong to the sequence alone."""
+    where = "attn_cache_append"
+    _need_cache(cache, where)
+    ks = _need_rows(k, "k", where, tuple(DTYPES), cache.device)
+    vs = _need_rows(v, "v", where, (k.dtype,), cache.device)
+    if k.shape != v.shape or tuple(k.shape[1:]) != (cache.num_kv_heads, cache.head_dim):
+        raise AttnError(1, f"{where}: k and v must be [tokens, {cache.num_kv_heads}, {cache.head_dim}], got "
+                           f"{tuple(k.shape)} and {tuple(v.shape)}")
+    _need_seqs(cache, cu_seqlens, seq_lens, where)
+    with _Launch(cache.device, stream) as s:
+        _check(_native.lib().attn_cache_append(
+            k.data_ptr(), v.data_ptr(), ks, vs, DTYPES[k.dtype], k.shape[0], cu_seqlens.data_ptr(),
+            seq_lens.data_ptr(), int(max_new), cache._ref, s), where)
+
+
+def _need_queries(q, cache, where: str):
+    _need_cache(cache, where)
+    if q is None:
+        raise AttnError(1, f"{where}: q is required")
+    _need(q, "q", where, tuple(DTYPES), device=cache.device)
+    if q.dtype != torch.bfloat16:
+        raise AttnError(2, f"{where}: dtype must be bfloat16")
+    if q.dim() != 3 or q.shape[2] != cache.head_dim or q.shape[1] % cache.num_kv_heads:
+        raise AttnError(1, f"{where}: q has shape {tuple(q.shape)}, expected [tokens, a multiple of "
+                           f"{cache.num_kv_heads}, {cache.head_dim}]")
+    return q.shape
+
+
+def attn_cache_fwd_workspace_size(cache: KVCache, total_tokens: int, num_heads: int, max_new: int,
+                                  max_seqlen: int) -> int:
+    """Bytes of device workspace ``attn_cache_fwd`` needs at these sizes."""
+    _need_cache(cache, "attn_cache_fwd_workspace_size")
+    out = ctypes.c_size_t()
+    _check(_native.lib().attn_cache_fwd_workspace_size(cache._ref, total_tokens, num_heads, max_new,
+                                                       max_seqlen, ctypes.byref(out)),
+           "attn_cache_fwd_workspace_size")
+    return int(out.value)
+
+
+def attn_cache_fwd(q: torch.Tensor, cache: KVCache, cu_seqlens: torch.Tensor, seq_lens: torch.Tensor,
+                   max_new: int, max_seqlen: int, kind="causal", scale: float = 0.0,
+                   out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None, stream=None):
+    """Attention of the new tokens' queries q [T, H, D] (bf16) over the cache,
+    which holds their keys and values already (``attn_cache_append``); returns
+    (O [T, H, D], LSE [H, T] fp32).
+
+    ``kind`` is "causal" (a query sees the tokens up to its own) or "none" (all
+    of its sequence's).  ``max_new`` and ``max_seqlen`` bound the new tokens and
+    the length of every sequence.  Rows behind the last sequence keep what
+    ``out`` and ``lse`` held.  ``workspace`` (uint8) defaults to a new buffer of
+    ``attn_cache_fwd_workspace_size`` bytes; calls that may overlap need one each."""
+    where = "attn_cache_fwd"
+    T, H, D = _need_queries(q, cache, where)
+    dev = cache.device
+    _need(out, "out", where, (q.dtype,), q.shape, dev)
+    _need(lse, "lse", where, (torch.float32,), (H, T), dev)
+    _need(workspace, "workspace", where, device=dev)
+    _need_seqs(cache, cu_seqlens, seq_lens, where)
+    with _Launch(dev, stream) as s:
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty((H, T), dtype=torch.float32, device=dev)
+        if workspace is None:
+            need = attn_cache_fwd_workspace_size(cache, T, H, int(max_new), int(max_seqlen))
+            if need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws, nbytes = (None, 0) if workspace is None else (workspace.data_ptr(),
+                                                          workspace.numel() * workspace.element_size())
+        _check(_native.lib().attn_cache_fwd(
+            q.data_ptr(), out.data_ptr(), lse.data_ptr(), DTYPES[q.dtype], T, H, float(scale),
+            cu_seqlens.data_ptr(), int(max_new), seq_lens.data_ptr(), int(max_seqlen), _kind(kind),
+            cache._ref, ws, nbytes, s), where)
+    return out, lse
+
+
+def attn_cache_weights(q: torch.Tensor, lse: torch.Tensor, cache: KVCache, cu_seqlens: torch.Tensor,
+                       seq_lens: torch.Tensor, max_new: int, max_seqlen: int, kind="causal",
+                       scale: float = 0.0, prev: Optional[torch.Tensor] = None,
+                       out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The attention weight that each cached token receives from the queries of
+    an ``attn_cache_fwd`` call (its q and LSE, the same kind and scale), summed over
+    the queries and the query heads of each key / value head and added to
+    ``prev``: fp32 [batch, heads, width], width >= max_seqlen.  ``out=prev``
+    adds in place.  Entries behind a sequence's tokens keep what ``out`` held
+    (0 in a new one)."""
+    where = "attn_cache_weights"
+    T, H, D = _need_queries(q, cache, where)
+    dev = cache.device
+    if lse is None:
+        raise AttnError(1, f"{where}: lse is required")
+    _need(lse, "lse", where, (torch.float32,), (H, T), dev)
+    _need_seqs(cache, cu_seqlens, seq_lens, where)
+    _need(prev, "prev", where, (torch.float32,), device=dev)
+    _need(out, "out", where, (torch.float32,), device=dev)
+    like = out if out is not None else prev
+    shape = (cache.batch, cache.num_kv_heads, int(max_seqlen)) if like is None else tuple(like.shape)
+    if len(shape) != 3 or shape[:2] != (cache.batch, cache.num_kv_heads):
+        raise AttnError(1, f"{where}: weights must be [{cache.batch}, {cache.num_kv_heads}, width], got {shape}")
+    _need(prev, "prev", where, shape=shape)
+    with _Launch(dev, stream) as s:
+        if out is None:
+            out = torch.zeros(shape, dtype=torch.float32, device=dev)
+        _check(_native.lib().attn_cache_weights(
+            q.data_ptr(), lse.data_ptr(), DTYPES[q.dtype], T, H, float(scale), cu_seqlens.data_ptr(),
+            int(max_new), seq_lens.data_ptr(), int(max_seqlen), _kind(kind), cache._ref,
+            None if prev is None else prev.data_ptr(), out.data_ptr(), shape[2], s), where)
+    return out
+
+
+def attn_cache_evict(weights: torch.Tensor, cache: KVCache, dst: KVCache, seq_lens: torch.Tensor,
+                     budgets: torch.Tensor, recent: int, max_seqlen: int, max_keep: int,
+                     kept: Optional[torch.Tensor] = None, new_weights: Optional[torch.Tensor] = None,
+                     new_lens: Optional[torch.Tensor] = None, stream=None):
+    """Keep min(seq_lens[b], budgets[b]) tokens of each sequence, for every head
+    by itself: the last ``recent`` ones and, of the others, those with the
+    largest ``weights`` (fp32 [batch, heads, width]; ties to the lower index,
+    -inf first to go), and copy them in order into ``dst``'s pages (a KVCache
+    with a page table of its own; the pools may be the same, the pages not).
+
+    Returns (kept int32 [batch, heads, max_keep] with -1 behind the last,
+    new_weights [batch, heads, max_keep or wider] with 0 behind the last,
+    new_lens int32 [batch])."""
+    where = "attn_cache_evict"
+    _need_cache(cache, where)
+    _need_cache(dst, where)
+    dev, B, H = cache.device, cache.batch, cache.num_kv_heads
+    if dst.device != dev:
+        raise AttnError(1, f"{where}: dst is on {dst.device}, expected {dev}")
+    max_keep = int(max_keep)
+    for name, t in (("weights", weights), ("seq_lens", seq_lens), ("budgets", budgets)):
+        if t is None:
+            raise AttnError(1, f"{where}: {name} is required")
+    _need(weights, "weights", where, (torch.float32,), device=dev)
+    _need(seq_lens, "seq_lens", where, (torch.int32,), (B,), dev)
+    _need(budgets, "budgets", where, (torch.int32,), (B,), dev)
+    _need(kept, "kept", where, (torch.int32,), (B, H, max_keep), dev)
+    _need(new_weights, "new_weights", where, (torch.float32,), device=dev)
+    _need(new_lens, "new_lens", where, (torch.int32,), (B,), dev)
+    for name, t in (("weights", weights), ("new_weights", new_weights)):
+        if t is not None and (t.dim() != 3 or tuple(t.shape[:2]) != (B, H)):
+            raise AttnError(1, f"{where}: {name} must be [{B}, {H}, width], got {tuple(t.shape)}")
+    if max_keep < 0:
+        raise AttnError(1, f"{where}: max_keep is negative")
+    with _Launch(dev, stream) as s:
+        if kept is None:
+            kept = torch.empty((B, H, max_keep), dtype=torch.int32, device=dev)
+        if new_weights is None:
+            new_weights = torch.empty((B, H, max_keep), dtype=torch.float32, device=dev)
+        if new_lens is None:
+            new_lens = torch.empty(B, dtype=torch.int32, device=dev)
+        _check(_native.lib().attn_cache_evict(
+            weights.data_ptr(), weights.shape[2], seq_lens.data_ptr(), budgets.data_ptr(), int(recent),
+            int(max_seqlen), max_keep, cache._ref, dst._ref, kept.data_ptr(), new_weights.data_ptr(),
+            new_weights.shape[2], new_lens.data_ptr(), s), where)
+    return kept, new_weights, new_lens
+
+
+def attn_cache_get_status(cache: KVCache, stream=None) -> int:
+    """Synchronise, then return and clear the cache's device status code."""
+    _need_cache(cache, "attn_cache_get_status")
+    with _Launch(cache.device, stream) as s:
+        return int(_native.lib().attn_cache_get_status(cache._ref, s))

@@ -20,8 +20,9 @@ LIB_NAME = "libattnmask.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 
 SOURCES = ["api.cu", "blockmask.cu", "blockmask_noalloc.cu", "attn_fwd_bf16.cu", "attn_fwd_f32.cu",
-           "attn_bwd_bf16.cu"]
-HEADERS = ["common.cuh", "ptx.cuh", "tile_pipeline.cuh"]
+           "attn_bwd_bf16.cu", "cache_api.cu", "rope.cu", "cache_append.cu", "cache_attn.cu",
+           "cache_weights.cu", "cache_evict.cu"]
+HEADERS = ["common.cuh", "ptx.cuh", "tile_pipeline.cuh", "cache.cuh", "cache_rows.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
@@ -41,7 +42,7 @@ def _nvcc() -> str:
 
 def _inputs():
     return ([os.path.join(CSRC, s) for s in SOURCES + HEADERS] +
-            [os.path.join(INCLUDE, "attn_block_mask.h"), os.path.abspath(__file__)])
+            [os.path.join(INCLUDE, h) for h in ("attn_block_mask.h", "attn_cache.h")] + [os.path.abspath(__file__)])
 
 
 def _stale() -> bool:

@@ -150,7 +150,7 @@ const char* attn_status_string(attn_status s) {
     case ATTN_ERR_MASK_MISMATCH: return "block mask does not match the call";
     case ATTN_ERR_CUDA: return "CUDA error";
     case ATTN_ERR_DEVICE_TIMEOUT: return "a kernel pipeline wait timed out";
-    case ATTN_ERR_DEVICE_INVALID_INPUT: return "device found malformed cu_seqlens";
+    case ATTN_ERR_DEVICE_INVALID_INPUT: return "device found malformed input (cu_seqlens, sequence lengths or page numbers)";
   }
   return "unknown status";
 }

@@ -1,0 +1,75 @@
+// The query side of the mma.sync kernels over the cache (attention by rows of
+// 16, weights): which rows a tile holds, and their fp16 form.
+//
+// Rows.  The queries of one sequence and key / value head are n * G rows, row
+// r = new token r / G, query head h G + r % G; kernels take them 16 at a time.
+//
+// Operands.  m16n8k16: lane = 4 g + t holds, of a 16-wide step of the
+// contracted dimension, the places 2t, 2t + 1, 2t + 8, 2t + 9.  The order of
+// that dimension is free as long as both operands agree, so lane t takes the
+// D / 4 consecutive dimensions from t D / 4, four per step: a token's codes are
+// then read from global memory as they lie, 32 bytes per lane for D = 128.
+#pragma once
+
+#include "cache.cuh"
+
+namespace attnmask {
+namespace {
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+
+// One row's D / 4 dimensions of lane t as fp16 pairs, times a power of two that
+// puts the row's largest magnitude into [1, 2): w[2 s], w[2 s + 1] belong to
+// step s.  Returns that power's inverse.  A row past the last is zero.
+template <int D>
+__device__ __forceinline__ float load_query(const CacheQueryArgs& a, const SeqRows& r, int h, int G, int row, int t,
+                                            uint32_t (&w)[D / 8]) {
+  float f[D / 4];
+  float amax = 0.f;
+  if (row < r.n * G) {
+    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(a.q) +
+                             (int64_t(r.q0 + row / G) * a.num_heads + h * G + row % G) * D + t * (D / 4);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+      const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        f[8 * i + 2 * j] = __uint_as_float(x[j] << 16);
+        f[8 * i + 2 * j + 1] = __uint_as_float(x[j] & 0xFFFF0000u);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < D / 4; ++i) amax = fmaxf(amax, fabsf(f[i]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < D / 4; ++i) f[i] = 0.f;
+  }
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+  const int e = amax > 0.f ? max(-126, min(126, exponent_of(amax))) : 0;
+  const float inv = pow2f(-e);
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) w[i] = pack_half2(f[2 * i] * inv, f[2 * i + 1] * inv);
+  return pow2f(e);
+}
+
+// Tokens [0, visible) that row `row` sees (0 for a row past the last).
+__device__ __forceinline__ int visible_tokens(const SeqRows& r, int G, int row, bool causal) {
+  if (row >= r.n * G) return 0;
+  return causal ? max(0, r.len - r.n + row / G + 1) : r.len;
+}
+
+}  // namespace
+}  // namespace attnmask
