@@ -76,6 +76,19 @@ struct CacheQueryArgs {
   float* workspace;
 };
 
+// How attn_cache_fwd cuts its work: rows (new token, query head of the group) in
+// tiles, tokens in chunks, and where the chunks' results meet.
+struct CacheAttnParams {
+  CacheQueryArgs a;
+  int G;           // query heads per key / value head
+  int tile_rows;   // kFewRows (mma.sync) or kManyRows (tcgen05)
+  int row_tiles, chunk, splits;
+  float scale_log2;
+  float* part_o;   // [splits][total_tokens * num_heads][head_dim]: O before the division
+  float2* part_m;  // [splits][total_tokens * num_heads]: running maximum, sum
+};
+constexpr int kFewRows = 16, kManyRows = 256;
+
 struct EvictArgs {
   const float* weights;
   int64_t weight_stride, new_stride;
@@ -92,6 +105,7 @@ attn_status launch_rope(const RopeArgs& a, const attn_rope_plan& plan, cudaStrea
 attn_status launch_cache_append(const AppendArgs& a, cudaStream_t s);
 uint64_t cache_fwd_workspace(const CacheView& c, int total_tokens, int num_heads, int max_new, int max_seqlen);
 attn_status launch_cache_fwd(const CacheQueryArgs& a, cudaStream_t s);
+attn_status launch_cache_chunk(const CacheAttnParams& p, cudaStream_t s);
 attn_status launch_cache_weights(const CacheQueryArgs& a, cudaStream_t s);
 attn_status launch_cache_evict(const EvictArgs& a, cudaStream_t s);
 

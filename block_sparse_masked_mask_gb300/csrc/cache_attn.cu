@@ -53,36 +53,8 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool o
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n) : "memory");
 }
 
-struct Split {
-  int chunk;   // tokens per chunk, a multiple of kGroup * kWarps
-  int splits;  // chunks per sequence at most
-};
-
-// Chunks: enough CTAs to fill the GPU about twice over (three CTAs per SM fit),
-// but none below 256 tokens, where a CTA's start and end cost more than its
-// reads, and none above 1024, so that sequences of different lengths
-// spread evenly.
-Split choose_split(int64_t tiles, int max_seqlen, int sms) {
-  const int64_t want = (6ll * sms + tiles - 1) / (tiles > 0 ? tiles : 1);
-  int64_t chunk = (int64_t(max_seqlen) + want - 1) / (want > 0 ? want : 1);
-  chunk = chunk < 256 ? 256 : (chunk > 1024 ? 1024 : (chunk + 63) / 64 * 64);
-  Split s;
-  s.chunk = int(chunk);
-  s.splits = int((int64_t(max_seqlen) + chunk - 1) / chunk);
-  if (s.splits < 1) s.splits = 1;
-  return s;
-}
-
-struct AttnParams {
-  CacheQueryArgs a;
-  int G, row_tiles, chunk, splits;
-  float scale_log2;
-  float* part_o;   // [splits][T * H][D], O before the division
-  float2* part_m;  // [splits][T * H]: m, sum
-};
-
 template <int D>
-__global__ void __launch_bounds__(kAttnThreads, 3) cache_attn_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kAttnThreads, 3) cache_attn_kernel(const CacheAttnParams p) {
   using C = AttnCfg<D>;
   extern __shared__ __align__(16) uint8_t smem[];
   const CacheQueryArgs& a = p.a;
@@ -322,7 +294,7 @@ __global__ void __launch_bounds__(kAttnThreads, 3) cache_attn_kernel(const AttnP
 
 // Joins the chunks of each row, one warp per row, in the order of the chunks.
 template <int D>
-__global__ void __launch_bounds__(128) cache_combine_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(128) cache_combine_kernel(const CacheAttnParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const CacheQueryArgs& a = p.a;
   const int b = blockIdx.y, lane = threadIdx.x & 31;
@@ -332,9 +304,9 @@ __global__ void __launch_bounds__(128) cache_combine_kernel(const AttnParams p) 
   if (i >= r.n * a.num_heads) return;
   const int head = i % a.num_heads;
   const int64_t token = r.q0 + i / a.num_heads;
-  // the chunks that this row's tile of 16 had
+  // the chunks that this row's tile had
   const int rg = (i / a.num_heads) * p.G + head % p.G;
-  const int last = min(rg / 16 * 16 + 15, r.n * p.G - 1);
+  const int last = min(rg / p.tile_rows * p.tile_rows + p.tile_rows - 1, r.n * p.G - 1);
   const int limit = visible_tokens(r, p.G, last, a.causal);
   const int n = max(1, (limit + p.chunk - 1) / p.chunk);
   const int64_t step = int64_t(a.total_tokens) * a.num_heads;
@@ -361,30 +333,48 @@ __global__ void __launch_bounds__(128) cache_combine_kernel(const AttnParams p) 
     a.lse[int64_t(head) * a.total_tokens + token] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
-int row_tiles(const CacheView& c, int num_heads, int max_new) {
-  return int((int64_t(max_new) * (num_heads / c.heads) + 15) / 16);
-}
-
-// The number of SMs only sizes the work; the size query runs without a device,
-// so it is that of the GPU this library is built for.
-Split split_of(const CacheView& c, int num_heads, int max_new, int max_seqlen) {
-  constexpr int kSms = 152;
-  return choose_split(int64_t(row_tiles(c, num_heads, max_new)) * c.heads * c.batch, max_seqlen, kSms);
+// Tiles, chunks and their number.  More than 16 rows of a key / value head go to
+// the tcgen05 kernel (cache_chunk.cu), which reads the cache once for 256.
+// Chunks: enough CTAs to fill the GPU about twice over; for few rows none below
+// 256 tokens, where a CTA's start and end cost more than its reads, and none above
+// 1024, so that sequences of different lengths spread evenly; for many rows, one
+// CTA per SM, 1024 to 4096.  The number of SMs only sizes the work, and the
+// size query runs without a device, so it is that of the GPU this library is
+// built for.
+void plan(CacheAttnParams* p) {
+  constexpr int64_t kSms = 152;
+  const CacheQueryArgs& a = p->a;
+  p->G = a.num_heads / a.cache.heads;
+  const int64_t rows = int64_t(a.max_new) * p->G;
+  const bool many = rows > kFewRows;
+  p->tile_rows = many ? kManyRows : kFewRows;
+  p->row_tiles = int((rows + p->tile_rows - 1) / p->tile_rows);
+  const int64_t items = int64_t(p->row_tiles) * a.cache.heads * a.cache.batch;
+  const int64_t fill = (many ? 2 : 6) * kSms, least = many ? 1024 : 256, most = many ? 4096 : 1024;
+  const int64_t want = items > 0 ? (fill + items - 1) / items : 1;
+  int64_t chunk = (int64_t(a.max_seqlen) + want - 1) / want;
+  chunk = (chunk + kTile - 1) / kTile * kTile;
+  chunk = chunk < least ? least : (chunk > most ? most : chunk);
+  p->chunk = int(chunk);
+  p->splits = int((int64_t(a.max_seqlen) + chunk - 1) / chunk);
+  if (p->splits < 1) p->splits = 1;
 }
 
 template <int D>
-cudaError_t launch_d(const AttnParams& p, cudaStream_t s) {
+cudaError_t launch_few(const CacheAttnParams& p, cudaStream_t s) {
   using C = AttnCfg<D>;
-  const CacheQueryArgs& a = p.a;
   cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  const dim3 grid(unsigned(p.splits) * unsigned(p.row_tiles), unsigned(a.cache.heads), unsigned(a.cache.batch));
+  const dim3 grid(unsigned(p.splits) * unsigned(p.row_tiles), unsigned(p.a.cache.heads), unsigned(p.a.cache.batch));
   cache_attn_kernel<D><<<grid, kAttnThreads, C::SMEM, s>>>(p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || p.splits == 1) return e;
-  // the joining kernel is launched early and waits for the first one's end
+  return cudaGetLastError();
+}
+
+// The joining kernel is launched early and waits for the first one's end.
+template <int D>
+cudaError_t launch_combine(const CacheAttnParams& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned((int64_t(a.max_new) * a.num_heads + 3) / 4), unsigned(a.cache.batch));
+  cfg.gridDim = dim3(unsigned((int64_t(p.a.max_new) * p.a.num_heads + 3) / 4), unsigned(p.a.cache.batch));
   cfg.blockDim = dim3(128);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -398,30 +388,35 @@ cudaError_t launch_d(const AttnParams& p, cudaStream_t s) {
 }  // namespace
 
 uint64_t cache_fwd_workspace(const CacheView& c, int total_tokens, int num_heads, int max_new, int max_seqlen) {
-  const Split s = split_of(c, num_heads, max_new, max_seqlen);
-  if (s.splits == 1) return 0;
-  const uint64_t rows = uint64_t(s.splits) * uint64_t(total_tokens) * uint64_t(num_heads);
+  CacheAttnParams p;
+  p.a.cache = c;
+  p.a.num_heads = num_heads;
+  p.a.max_new = max_new;
+  p.a.max_seqlen = max_seqlen;
+  plan(&p);
+  if (p.splits == 1) return 0;
+  const uint64_t rows = uint64_t(p.splits) * uint64_t(total_tokens) * uint64_t(num_heads);
   return rows * uint64_t(c.head_dim) * 4 + rows * 8;
 }
 
 attn_status launch_cache_fwd(const CacheQueryArgs& a, cudaStream_t s) {
-  const Split sp = split_of(a.cache, a.num_heads, a.max_new, a.max_seqlen);
-  AttnParams p;
+  CacheAttnParams p;
   p.a = a;
-  p.G = a.num_heads / a.cache.heads;
-  p.row_tiles = row_tiles(a.cache, a.num_heads, a.max_new);
-  p.chunk = sp.chunk;
-  p.splits = sp.splits;
+  plan(&p);
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.part_o = a.workspace;
-  p.part_m = reinterpret_cast<float2*>(a.workspace + uint64_t(sp.splits) * uint64_t(a.total_tokens) *
+  p.part_m = reinterpret_cast<float2*>(a.workspace + uint64_t(p.splits) * uint64_t(a.total_tokens) *
                                                          uint64_t(a.num_heads) * uint64_t(a.cache.head_dim));
-  cudaError_t e = cudaErrorInvalidValue;
-  switch (a.cache.head_dim) {
-    case 32: e = launch_d<32>(p, s); break;
-    case 64: e = launch_d<64>(p, s); break;
-    case 128: e = launch_d<128>(p, s); break;
+  const int d = a.cache.head_dim;
+  cudaError_t e = cudaSuccess;
+  if (p.tile_rows == kManyRows) {
+    const attn_status st = launch_cache_chunk(p, s);
+    if (st != ATTN_OK) return st;
+  } else {
+    e = d == 32 ? launch_few<32>(p, s) : d == 64 ? launch_few<64>(p, s) : launch_few<128>(p, s);
   }
+  if (e == cudaSuccess && p.splits > 1)
+    e = d == 32 ? launch_combine<32>(p, s) : d == 64 ? launch_combine<64>(p, s) : launch_combine<128>(p, s);
   return e == cudaSuccess ? ATTN_OK : record_cuda_error(e, "attn_cache_fwd launch");
 }
 

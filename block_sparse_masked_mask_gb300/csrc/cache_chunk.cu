@@ -1,0 +1,516 @@
+// Attention over the 8-bit cache for many query rows (chunks of prompts), on
+// the tcgen05 tensor cores.
+//
+// A CTA takes one sequence and key / value head, 256 query rows (two M tiles of
+// 128; rows are numbered new token * G + query head) and a chunk of the
+// tokens, which it walks 128 at a time.  The products bound it: 4 D operations
+// per row and token, while a tile's bytes serve 256 rows.
+//  * S = Q K^T runs on the codes as they lie (kind::f8f6f4): the keys need no
+//    conversion.  A bf16 query has 8 significant bits and e4m3 4, so each row,
+//    scaled by a power of two to a largest value in [128, 256), is the sum of two
+//    e4m3 numbers, q = hi + lo, exact down to 2^-10 of that value and within
+//    2^-18 of it below; S is hi K^T + lo K^T in one accumulator, at the cost
+//    of one fp16 product (e4m3 runs at twice the rate).
+//  * O += P V runs in fp16: weights keep 11 bits, the values are exact.  One
+//    warpgroup turns the codes into fp16 tiles in shared memory, once
+//    for both M tiles.
+//  * The pages' scales and the running maximum are those of cache_attn.cu.
+// Warps (512 threads):
+//   0-3, 4-7   softmax of M tile 0 and 1, one thread per row
+//   8-11       values: codes to fp16 tiles (two slots)
+//   12         TMA of the keys (three slots), pages' scales (four slots)
+//   13, 14     tcgen05 issuers of M tile 0 and 1
+//   15         TMEM allocation
+// The two M tiles share only the tiles read: while one's softmax runs, the
+// tensor cores work for the other.  P of a tile is written over its S, so an
+// M tile's S(j + 1) waits for its P V(j).  TMEM columns: S0 [0, 128), S1
+// [128, 256), O0 [256, 256 + D), O1 [384, 384 + D).
+// Every wait is bounded, as in the other tcgen05 kernels, and ends in
+// ATTN_ERR_DEVICE_TIMEOUT in the cache's status word.  Each role waits only for
+// an earlier tile's events of the others, or for this tile's by a role that
+// comes before it (keys, S, softmax, P V), so the order of tiles carries every
+// wait to its end.
+#include "cache_rows.cuh"
+#include "tile_pipeline.cuh"
+
+namespace attnmask {
+namespace {
+
+constexpr int kChunkThreads = 512;
+constexpr int kWarpValues = 8, kWarpKeys = 12, kWarpIssue = 13, kWarpAlloc = 15;
+constexpr int kRegsSoftmax = 160, kRegsOther = 96;
+static_assert(256 * kRegsSoftmax + 256 * kRegsOther == kChunkThreads * 128, "register split");
+
+template <int D>
+struct ChunkCfg {
+  using V = TileLayout<D>;                     // fp16 value tile: the 16-bit layout
+  static constexpr int KT = kTile * D;         // bytes of a tile of codes (keys, or half a query)
+  static constexpr int VT = V::TILE;
+  static constexpr int NK = 3, NV = 2, NSCL = 4;
+  static constexpr int OFF_Q = 0;              // [M tile][hi, lo]
+  static constexpr int OFF_K = OFF_Q + 4 * KT;
+  static constexpr int OFF_V = OFF_K + NK * KT;
+  static constexpr int OFF_SCL = OFF_V + NV * VT;          // [slot][8 blocks of 16 tokens] float4
+  static constexpr int OFF_BAD = OFF_SCL + NSCL * 8 * 16;  // [slot] bits of blocks without a page
+  static constexpr int B_Q = 0, B_KFULL = 2, B_KEMPTY = B_KFULL + NK, B_VFULL = B_KEMPTY + NK,
+                       B_VEMPTY = B_VFULL + NV, B_SCLFULL = B_VEMPTY + NV, B_SCLFREE = B_SCLFULL + NSCL,
+                       B_SFULL = B_SCLFREE + NSCL, B_PFULL = B_SFULL + 2, B_PDONE = B_PFULL + 2,
+                       B_DRAIN = B_PDONE + 2, NBAR = B_DRAIN + 2;
+  static constexpr int OFF_BAR = (OFF_BAD + NSCL * 4 + 15) & ~15;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int USED = OFF_MISC + 16 + 1024;        // the base is aligned to 1024
+  // one CTA per SM: it takes all of TMEM
+  static constexpr int SMEM = USED > 116 * 1024 ? USED : 116 * 1024;
+  static_assert(SMEM <= 232448, "shared memory budget");
+  // rows of D bytes, swizzled over their own width
+  static constexpr uint32_t SW8 = D == 128 ? ptx::kSwizzle128B : D == 64 ? ptx::kSwizzle64B : ptx::kSwizzle32B;
+  __device__ static uint32_t unit8(int row, int u) {  // byte offset of 16-byte unit u of a row
+    const int x = D == 128 ? (row & 7) : D == 64 ? ((row >> 1) & 3) : ((row >> 2) & 1);
+    return uint32_t(row * D + ((u ^ x) << 4));
+  }
+  __device__ static uint32_t unit16(int row, int u) {  // of the fp16 layout's row chunk
+    const int x = V::ROWB == 128 ? (row & 7) : ((row >> 1) & 3);
+    return uint32_t(row * V::ROWB + ((u ^ x) << 4));
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kChunkThreads, 1)
+    cache_chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CacheAttnParams p) {
+  using C = ChunkCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const CacheQueryArgs& a = p.a;
+  const CacheView& c = a.cache;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int split = blockIdx.x / p.row_tiles, row0 = (blockIdx.x % p.row_tiles) * p.tile_rows;
+  const int h = blockIdx.y, b = blockIdx.z;
+  SeqRows r;
+  if (!load_rows(a.cu, a.lens, b, a.total_tokens, a.max_new, a.max_seqlen, c.status, r)) return;
+  const int rows = min(p.tile_rows, r.n * p.G - row0);
+  if (rows <= 0) return;
+  const int limit = visible_tokens(r, p.G, row0 + rows - 1, a.causal);
+  const int begin = split * p.chunk, end = min(begin + p.chunk, limit);
+  if (split > 0 && begin >= end) return;  // chunk 0 also answers for rows that see nothing
+  const int tiles = end > begin ? (end - begin + kTile - 1) / kTile : 0;
+  const int nm = rows > kTile ? 2 : 1;  // M tiles
+  int32_t* err = c.status;
+
+  const uint32_t raw = ptx::smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* sbase = smem_raw + (base - raw);
+  const uint32_t bars = base + C::OFF_BAR;
+  auto bar = [&](int i) { return bars + 8u * uint32_t(i); };
+  uint32_t* misc = reinterpret_cast<uint32_t*>(sbase + C::OFF_MISC);
+  volatile uint32_t* abort_flag = misc + 1;
+  float4* scl = reinterpret_cast<float4*>(sbase + C::OFF_SCL);
+  uint32_t* bad = reinterpret_cast<uint32_t*>(sbase + C::OFF_BAD);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::NK; ++i) {
+      ptx::mbar_init(bar(C::B_KFULL + i), 1);
+      ptx::mbar_init(bar(C::B_KEMPTY + i), nm);
+    }
+    for (int i = 0; i < C::NV; ++i) {
+      ptx::mbar_init(bar(C::B_VFULL + i), 4);
+      ptx::mbar_init(bar(C::B_VEMPTY + i), nm);
+    }
+    for (int i = 0; i < C::NSCL; ++i) {
+      ptx::mbar_init(bar(C::B_SCLFULL + i), 1);
+      ptx::mbar_init(bar(C::B_SCLFREE + i), 4 * nm);
+    }
+    for (int m = 0; m < 2; ++m) {
+      ptx::mbar_init(bar(C::B_Q + m), 4);
+      ptx::mbar_init(bar(C::B_SFULL + m), 1);
+      ptx::mbar_init(bar(C::B_PFULL + m), 4);
+      ptx::mbar_init(bar(C::B_PDONE + m), 1);
+      ptx::mbar_init(bar(C::B_DRAIN + m), 1);
+    }
+    // an earlier CTA that gave up on a wait makes every later one skip its work
+    *abort_flag = (*reinterpret_cast<volatile int32_t*>(err) & kErrTimeout) ? 1u : 0u;
+    ptx::fence_mbar_init();
+  }
+  if (warp == kWarpAlloc) {
+    ptx::tmem_alloc(ptx::smem_addr(misc), 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = misc[0];
+  const bool skip = *abort_flag != 0u;
+
+  if (skip) {
+    // nothing issued, nothing to drain
+  } else if (warp >= kWarpKeys) {
+    ptx::regs_dec<kRegsOther>();
+    if (warp == kWarpKeys) {
+      // ------------------------------------------------------------ keys, scales
+      // lane i < 8: the i-th 16 tokens of a tile
+      const int step = max(1, (1 << c.page_log2) / 16);  // lanes per page
+      const bool leader = lane < 8 && lane % step == 0;
+      int page = -1;
+      float ks = 0.f, vs = 0.f;
+      auto lookup = [&](int j) {
+        page = -1;
+        ks = vs = 0.f;
+        const int tok = begin + j * kTile + lane * 16;
+        if (lane < 8 && j < tiles && tok < end) {
+          page = load_page(c, b, tok >> c.page_log2);
+          if (page >= 0) {
+            ks = c.k_scale[int64_t(page) * c.heads + h];
+            vs = c.v_scale[int64_t(page) * c.heads + h];
+          }
+        }
+      };
+      if (lane == 0) ptx::prefetch_tensormap(&tmK);
+      lookup(0);
+      int done = 0;
+      for (int j = 0; j < tiles; ++j) {
+        const int ss = j % C::NSCL, slot = j % C::NK;
+        if (j >= C::NSCL &&
+            !warp_wait(bar(C::B_SCLFREE + ss), uint32_t(j / C::NSCL - 1) & 1u, abort_flag, err, 1))
+          break;
+        const int tok = begin + j * kTile + lane * 16;
+        if (lane < 8) {
+          const int x = exponent_of(vs);
+          scl[ss * 8 + lane] = page >= 0 ? make_float4(ks, float(x), pow2f(max(-126, -x)), 0.f)
+                                         : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        const uint32_t missing = __ballot_sync(0xffffffffu, lane < 8 && tok < end && page < 0);
+        if (lane == 0) bad[ss] = missing;
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(C::B_SCLFULL + ss));
+        if (j >= C::NK && !warp_wait(bar(C::B_KEMPTY + slot), uint32_t(j / C::NK - 1) & 1u, abort_flag, err, 2)) break;
+        const bool load = leader && page >= 0;
+        const uint32_t loads = __ballot_sync(0xffffffffu, load);
+        const uint32_t piece = uint32_t(D) << c.page_log2;  // bytes of a page's keys
+        if (lane == 0) ptx::mbar_arrive_expect_tx(bar(C::B_KFULL + slot), piece * __popc(loads));
+        __syncwarp();
+        if (load)
+          ptx::tma_load_4d(base + C::OFF_K + slot * C::KT + lane * 16 * D, &tmK, bar(C::B_KFULL + slot), 0, 0, h, page);
+        done = j + 1;
+        lookup(j + 1);
+      }
+      // do not leave while a copy may still be writing shared memory
+      if (lane == 0) {
+        for (int s = 0; s < C::NK; ++s) {
+          if (done <= s) continue;
+          const int last = s + C::NK * ((done - 1 - s) / C::NK);
+          drain_bar(bar(C::B_KFULL + s), uint32_t(last / C::NK) & 1u, err);
+        }
+      }
+      __syncwarp();
+    } else if (warp < kWarpIssue + nm) {
+      // ------------------------------------------------------------ issuers
+      const int m = warp - kWarpIssue;
+      if (lane == 0) {
+        constexpr uint32_t IDESC_S = ptx::idesc_e4m3_f32(128, 128);
+        constexpr uint32_t IDESC_PV = ptx::idesc_f16_f32(128, D, false, true);
+        const uint32_t s_tmem = tmem + uint32_t(m) * 128u, o_tmem = tmem + 256u + uint32_t(m) * 128u;
+        const uint64_t qhi = ptx::smem_desc(base + C::OFF_Q + (2 * m) * C::KT, 16u, 8 * D, C::SW8);
+        const uint64_t qlo = ptx::smem_desc(base + C::OFF_Q + (2 * m + 1) * C::KT, 16u, 8 * D, C::SW8);
+        const uint64_t kd = ptx::smem_desc(base + C::OFF_K, 16u, 8 * D, C::SW8);
+        const uint64_t vd = v_base<D>(base + C::OFF_V);
+        bool ok = tiles == 0 || wait_bar(bar(C::B_Q + m), 0, abort_flag, err, 3);
+        for (int j = 0; ok && j < tiles; ++j) {
+          const int ks = j % C::NK, vslot = j % C::NV;
+          if (!wait_bar(bar(C::B_KFULL + ks), uint32_t(j / C::NK) & 1u, abort_flag, err, 4)) break;
+          // P(j - 1) lies over S: its product has read it
+          if (j > 0 && !wait_bar(bar(C::B_PDONE + m), uint32_t(j - 1) & 1u, abort_flag, err, 5)) break;
+          ptx::tc_fence_after();
+          const uint64_t kj = kd + uint64_t(ks) * (C::KT >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk) ptx::mma_f8_ss(s_tmem, qhi + 2 * kk, kj + 2 * kk, IDESC_S, kk > 0);
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk) ptx::mma_f8_ss(s_tmem, qlo + 2 * kk, kj + 2 * kk, IDESC_S, 1);
+          ptx::mma_commit(bar(C::B_SFULL + m));
+          ptx::mma_commit(bar(C::B_KEMPTY + ks));
+          if (!wait_bar(bar(C::B_VFULL + vslot), uint32_t(j / C::NV) & 1u, abort_flag, err, 6)) break;
+          if (!wait_bar(bar(C::B_PFULL + m), uint32_t(j) & 1u, abort_flag, err, 7)) break;
+          ptx::tc_fence_after();
+          const uint64_t vj = vd + uint64_t(vslot) * (C::VT >> 4);
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            ptx::mma_ts(o_tmem, s_tmem + uint32_t(kk) * 8u, vj + v_step<D>(kk), IDESC_PV, (j > 0 || kk > 0) ? 1u : 0u);
+          ptx::mma_commit(bar(C::B_PDONE + m));
+          ptx::mma_commit(bar(C::B_VEMPTY + vslot));
+        }
+        // every product this thread issued has finished once this arrives
+        ptx::mma_commit(bar(C::B_DRAIN + m));
+        drain_bar(bar(C::B_DRAIN + m), 0, err);
+      }
+      __syncwarp();
+    }
+  } else if (warp >= kWarpValues) {
+    // ------------------------------------------------------------ values
+    ptx::regs_dec<kRegsOther>();
+    constexpr int PPT = D / 16;  // 16-byte pieces per token = pieces per thread
+    const int ct = threadIdx.x - kWarpValues * 32;
+    uint4 next[PPT];
+    auto fetch = [&](int j) {
+#pragma unroll
+      for (int i = 0; i < PPT; ++i) {
+        const int x = i * 128 + ct, row = x / PPT, piece = x % PPT;
+        const int tok = begin + j * kTile + row;
+        next[i] = make_uint4(0, 0, 0, 0);  // behind the end, or without a page: 0 weights times 0
+        if (j < tiles && tok < end) {
+          const int id = __ldg(c.table + int64_t(b) * c.max_pages + (tok >> c.page_log2));
+          if (unsigned(id) < unsigned(c.num_pages))  // the keys' warp notes bad ones
+            next[i] = __ldg(reinterpret_cast<const uint4*>(
+                c.v_pages + (((int64_t(id) * c.heads + h) << c.page_log2) + (tok & ((1 << c.page_log2) - 1))) * D +
+                piece * 16));
+        }
+      }
+    };
+    fetch(0);
+    for (int j = 0; j < tiles; ++j) {
+      const int slot = j % C::NV;
+      if (j >= C::NV && !warp_wait(bar(C::B_VEMPTY + slot), uint32_t(j / C::NV - 1) & 1u, abort_flag, err, 8)) break;
+      uint8_t* tile = sbase + C::OFF_V + slot * C::VT;
+#pragma unroll
+      for (int i = 0; i < PPT; ++i) {
+        const int x = i * 128 + ct, row = x / PPT, piece = x % PPT;
+        uint8_t* chunk = tile + (piece * 16 / C::V::CE) * C::V::CHUNK;
+        const int u = (piece * 16 % C::V::CE) / 8;  // two units: u, u + 1
+        const uint4 w = next[i];
+        const uint4 lo = make_uint4(half2_of(w.x), half2_of_high(w.x), half2_of(w.y), half2_of_high(w.y));
+        const uint4 hi = make_uint4(half2_of(w.z), half2_of_high(w.z), half2_of(w.w), half2_of_high(w.w));
+        // pieces of the second row chunk store their halves the other way
+        // round: eight lanes of a token then meet eight different bank groups
+        const bool flip = piece * 16 >= C::V::CE;
+        *reinterpret_cast<uint4*>(chunk + C::unit16(row, u + (flip ? 1 : 0))) = flip ? hi : lo;
+        *reinterpret_cast<uint4*>(chunk + C::unit16(row, u + (flip ? 0 : 1))) = flip ? lo : hi;
+      }
+      ptx::fence_proxy_async_smem();
+      warp_arrive(bar(C::B_VFULL + slot), lane);
+      fetch(j + 1);
+    }
+  } else if (warp < 4 * nm) {
+    // ------------------------------------------------------------ softmax
+    ptx::regs_inc<kRegsSoftmax>();
+    const int m = warp >> 2, quarter = warp & 3;
+    const int row = quarter * 32 + lane;          // of the M tile, its TMEM lane
+    const int rg = row0 + m * kTile + row;        // of the sequence and head
+    const uint32_t lane_base = tmem + (uint32_t(quarter * 32) << 16);
+    const uint32_t s_col = lane_base + uint32_t(m) * 128u, o_col = lane_base + 256u + uint32_t(m) * 128u;
+    const bool real = rg < r.n * p.G;
+    const int64_t token = r.q0 + (real ? rg / p.G : 0);
+    const int head = h * p.G + (real ? rg % p.G : 0);
+    const int visible = visible_tokens(r, p.G, rg, a.causal);
+
+    // the row's query as hi + lo
+    float qscale;
+    {
+      uint4 q[D / 8];
+      float amax = 0.f;
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                        (token * a.num_heads + head) * D);
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        q[i] = real ? src[i] : make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
+      }
+      const int e = amax > 0.f ? max(-119, min(126, exponent_of(amax))) : 0;
+      const float f = pow2f(7 - e);
+      // an infinite query has no scores
+      qscale = (amax < INFINITY ? pow2f(e - 7) : __int_as_float(0x7FC00000)) * p.scale_log2;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e4 = 0; e4 < 4; ++e4) {
+          const uint4 v = q[2 * i + (e4 >> 1)];
+          const uint32_t w0 = (e4 & 1) ? v.z : v.x, w1 = (e4 & 1) ? v.w : v.y;
+          const float x0 = __uint_as_float(w0 << 16) * f, x1 = __uint_as_float(w0 & 0xFFFF0000u) * f;
+          const float x2 = __uint_as_float(w1 << 16) * f, x3 = __uint_as_float(w1 & 0xFFFF0000u) * f;
+          const uint32_t h0 = e4m3_pair(x0, x1), h1 = e4m3_pair(x2, x3);
+          uint32_t y0 = half2_of(h0), y1 = half2_of(h1);
+          const float2 z0 = __half22float2(*reinterpret_cast<__half2*>(&y0));
+          const float2 z1 = __half22float2(*reinterpret_cast<__half2*>(&y1));
+          hi[e4] = h0 | (h1 << 16);
+          lo[e4] = e4m3_pair(x0 - z0.x, x1 - z0.y) | (e4m3_pair(x2 - z1.x, x3 - z1.y) << 16);
+        }
+        const uint32_t at = C::OFF_Q + (2 * m) * C::KT + C::unit8(row, i);
+        *reinterpret_cast<uint4*>(sbase + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(sbase + at + C::KT) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+      ptx::fence_proxy_async_smem();
+      warp_arrive(bar(C::B_Q + m), lane);
+    }
+
+    float mx = -INFINITY, l = 0.f;  // running maximum (of score + value exponent), sum
+    bool ok = true;
+    for (int j = 0; j < tiles; ++j) {
+      const int ss = j % C::NSCL;
+      if (!warp_wait(bar(C::B_SCLFULL + ss), uint32_t(j / C::NSCL) & 1u, abort_flag, err, 9)) { ok = false; break; }
+      if (!warp_wait(bar(C::B_SFULL + m), uint32_t(j) & 1u, abort_flag, err, 10)) { ok = false; break; }
+      ptx::tc_fence_after();
+      const int seen = visible - (begin + j * kTile);  // columns [0, seen) are visible
+      const uint32_t missing = bad[ss];
+      const bool masked = __any_sync(0xffffffffu, seen < kTile) || missing != 0;
+      const float4* sc = scl + ss * 8;
+
+      uint32_t pk[kTile / 2];
+      float top, sum;
+      // weights 2^(t - ref) of the row, their sum, the largest t - ref
+      auto weigh = [&](float ref) {
+        top = -INFINITY;
+        sum = 0.f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t s[32];
+          ptx::tmem_ld32(s_col + q * 32, s);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const float4 k = sc[2 * q + half];
+            const float f = qscale * k.x, x = k.y - ref;
+            float part = 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              float t0 = fmaf(__uint_as_float(s[16 * half + i]), f, x);
+              float t1 = fmaf(__uint_as_float(s[16 * half + i + 1]), f, x);
+              if (masked) {
+                const int col = 32 * q + 16 * half + i;
+                const bool gone = (missing >> (2 * q + half)) & 1u;
+                if (gone || col >= seen) t0 = -INFINITY;
+                if (gone || col + 1 >= seen) t1 = -INFINITY;
+              }
+              top = ptx::fmax3(top, t0, t1);
+              t0 = ptx::ex2(t0);
+              t1 = ptx::ex2(t1);
+              part += t0 + t1;
+              pk[16 * q + 8 * half + i / 2] = pack_half2(t0, t1);
+            }
+            sum = fmaf(part, k.z, sum);
+          }
+        }
+      };
+      weigh(mx == -INFINITY ? 0.f : mx);
+      // the reference moves on the first visible token and when a weight
+      // would pass 2^8
+      const bool raise = mx == -INFINITY ? top > -INFINITY : top > 8.f;
+      if (__any_sync(0xffffffffu, raise)) {
+        const float was = mx;
+        if (raise) mx = (was == -INFINITY ? 0.f : was) + top;
+        const float alpha = raise ? (was == -INFINITY ? 0.f : ptx::ex2(was - mx)) : 1.f;
+        l *= alpha;
+        if (j > 0) {  // S(j) was issued after P V(j - 1) had ended
+#pragma unroll 1
+          for (int q = 0; q < D / 16; ++q) {
+            uint32_t v[16];
+            ptx::tmem_ld16(o_col + q * 16, v);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
+            ptx::tmem_st16(o_col + q * 16, v);
+          }
+        }
+        weigh(mx == -INFINITY ? 0.f : mx);
+      }
+      l += sum;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        ptx::tmem_st16(s_col + q * 16, *reinterpret_cast<const uint32_t(*)[16]>(pk + 16 * q));
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        ptx::mbar_arrive(bar(C::B_PFULL + m));
+        ptx::mbar_arrive(bar(C::B_SCLFREE + ss));
+      }
+    }
+    if (ok && tiles > 0) ok = warp_wait(bar(C::B_PDONE + m), uint32_t(tiles - 1) & 1u, abort_flag, err, 11);
+    ptx::tc_fence_after();
+    if (ok) {
+      const bool single = p.splits == 1;
+      const float inv = single ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+      const int64_t at = (int64_t(single ? 0 : split) * a.total_tokens + token) * a.num_heads + head;
+#pragma unroll
+      for (int q = 0; q < D / 16; ++q) {
+        uint32_t v[16];
+        if (tiles > 0) {
+          ptx::tmem_ld16(o_col + q * 16, v);
+          ptx::tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = 0u;
+        }
+        __syncwarp();
+        if (real && single) {
+          uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + at * D + q * 16);
+          uint32_t w[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            w[i] = ptx::pack_bf16(__uint_as_float(v[2 * i]) * inv, __uint_as_float(v[2 * i + 1]) * inv);
+          out[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          out[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        } else if (real) {
+          uint4* out = reinterpret_cast<uint4*>(p.part_o + at * D + q * 16);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) out[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        }
+      }
+      if (real) {
+        if (single)
+          a.lse[int64_t(head) * a.total_tokens + token] =
+              l == 0.f ? -INFINITY : (mx + log2f(l)) * 0.69314718055994531f;
+        else
+          p.part_m[at] = make_float2(mx, l);
+      }
+    }
+  } else {
+    ptx::regs_inc<kRegsSoftmax>();  // no second M tile
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpAlloc) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+attn_status launch_d(const CacheAttnParams& p, cudaStream_t s) {
+  using C = ChunkCfg<D>;
+  const CacheView& c = p.a.cache;
+  // the keys' pages as rows of D bytes: (dimension, slot, head, page), one page
+  // and head per copy
+  CUtensorMap map;
+  auto fn = encode_fn();
+  const int page_size = 1 << c.page_log2;
+  cuuint64_t dims[4] = {cuuint64_t(D), cuuint64_t(page_size), cuuint64_t(c.heads), cuuint64_t(c.num_pages)};
+  cuuint64_t strides[3] = {cuuint64_t(D), cuuint64_t(D) * page_size, cuuint64_t(D) * page_size * c.heads};
+  cuuint32_t box[4] = {cuuint32_t(D), cuuint32_t(page_size), 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUtensorMapSwizzle sw = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                : D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
+  if (!fn || fn(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, c.k_pages, dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return record_cuda_error(cudaErrorInvalidValue, "attn_cache_fwd tensor map encoding");
+  cudaError_t e = cudaFuncSetAttribute(cache_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return record_cuda_error(e, "attn_cache_fwd configure");
+  const dim3 grid(unsigned(p.splits) * unsigned(p.row_tiles), unsigned(c.heads), unsigned(c.batch));
+  cache_chunk_kernel<D><<<grid, kChunkThreads, C::SMEM, s>>>(map, p);
+  e = cudaGetLastError();
+  return e == cudaSuccess ? ATTN_OK : record_cuda_error(e, "attn_cache_fwd launch");
+}
+
+}  // namespace
+
+attn_status launch_cache_chunk(const CacheAttnParams& p, cudaStream_t s) {
+  switch (p.a.cache.head_dim) {
+    case 32: return launch_d<32>(p, s);
+    case 64: return launch_d<64>(p, s);
+    case 128: return launch_d<128>(p, s);
+  }
+  return ATTN_ERR_UNSUPPORTED;
+}
+
+}  // namespace attnmask

@@ -114,13 +114,14 @@ def run_attend(pair, q, cu, lens, causal=True, scale=0.0, max_new=None, max_seql
 def check_attend(pair, q, cu, lens, causal=True, scale=0.0, **kw):
     o, lse = run_attend(pair, q, cu, lens, causal, scale, **kw)
     assert api.attn_cache_get_status(pair.dev) == api.ATTN_OK
-    T = cu[-1]
+    T = int(cu[-1])
+    q = q[:T]
     O, L, terms, spread = pair.ref.attend(q.double().numpy(), cu, lens, causal, scale)
     tol, slack = attend_bounds(pair.ref, O, spread, terms, cu, lens, q.shape[2])
     got = o.double().cpu().numpy()
     err = np.abs(got[:T] - O[:T])
     assert (err <= tol[:T]).all(), f"O: max err {err.max()}, worst ratio {(err / np.maximum(tol[:T], 1e-300)).max()}"
-    gl = lse.double().cpu().numpy()
+    gl = lse.double().cpu().numpy()[:, :T]
     for b in range(len(lens)):
         s = slice(cu[b], cu[b + 1])
         seen = np.isfinite(L[:, s])
@@ -246,9 +247,9 @@ def test_rows_behind_the_last_sequence_and_bounds_above_the_sizes():
     q = randn(9, 4, 128, seed=8)
     q[5:] = float("nan")
     o, lse = torch.full((9, 4, 128), 5.0, dtype=torch.bfloat16, device="cuda"), torch.full((4, 9), 5.0, device="cuda")
-    out, l = check_attend(p, q[:5], cu, lens)
-    run_attend(p, q, cu, lens, max_new=9, max_seqlen=128, out=o, lse=lse)
-    assert torch.equal(o[:5], out) and torch.equal(lse[:, :5], l)
+    check_attend(p, q[:5], cu, lens)
+    # (bounds choose the cut into tiles and with it the order of the sums: within the same tolerance, not bit for bit)
+    check_attend(p, q, cu, lens, max_new=9, max_seqlen=128, out=o, lse=lse)
     assert (o[5:] == 5).all() and (lse[:, 5:] == 5).all()
 
 
