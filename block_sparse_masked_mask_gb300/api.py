@@ -327,32 +327,54 @@ ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "ramp": 3}
 
 
 class _Launch:
-    """Where a call runs: its stream's handle, with the tensors' device current
-    and new tensors allocated for that stream.  Costs nothing where the device
-    is current already and no stream is named."""
+    """Where a call runs when its device is not the current one or it names a
+    stream: the device made current, new tensors allocated for that stream."""
 
     def __init__(self, device: torch.device, stream):
-        self._guards = []
-        if device.index != torch.cuda.current_device():
-            self._guards.append(torch.cuda.device(device))
+        self._guards = [torch.cuda.device(device)]
         self._stream, self._device = stream, device
 
     def __enter__(self):
-        for g in self._guards:
-            g.__enter__()
-        if self._stream is None:
-            return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        self._guards[0].__enter__()
         s = self._stream
+        if s is None:
+            return torch.cuda.current_stream().cuda_stream
         if not hasattr(s, "cuda_stream"):
             s = torch.cuda.ExternalStream(int(s), device=self._device)
         g = torch.cuda.stream(s)
         g.__enter__()
         self._guards.append(g)
-        return ctypes.c_void_p(s.cuda_stream)
+        return s.cuda_stream
 
     def __exit__(self, *exc):
         while self._guards:
             self._guards.pop().__exit__(*exc)
+
+
+class _Here:
+    """The usual case of _Launch: the current device and its current stream."""
+
+    def __init__(self, index: int):
+        self._handle = torch._C._cuda_getCurrentRawStream(index)
+
+    def __enter__(self):
+        return self._handle
+
+    def __exit__(self, *exc):
+        pass
+
+
+def _launch(device: torch.device, stream):
+    if stream is None and device.index == torch.cuda.current_device():
+        return _Here(device.index)
+    return _Launch(device, stream)
+
+
+def _fits(t, dtype, shape, index: int) -> bool:
+    """The quick form of _need: a contiguous CUDA tensor of this type and shape on
+    device `index`.  Where it is False, _need says what is wrong."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.get_device() == index
+            and t.shape == shape and t.is_contiguous())
 
 
 def _need_rows(t, name: str, where: str, dtypes, device=None) -> int:
@@ -360,7 +382,7 @@ def _need_rows(t, name: str, where: str, dtypes, device=None) -> int:
     of a wider projection); returns that distance in elements."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise AttnError(1, f"{where}: {name} must be a CUDA tensor")
-    if device is not None and t.device != device:
+    if device is not None and t.get_device() != device.index:
         raise AttnError(1, f"{where}: {name} is on {t.device}, expected {device}")
     if t.dtype not in dtypes:
         raise AttnError(1, f"{where}: {name} has dtype {t.dtype}, expected one of {dtypes}")
@@ -436,14 +458,17 @@ def attn_rope(q: torch.Tensor, k: Optional[torch.Tensor], plan: RopePlan,
         raise AttnError(1, f"{where}: plan must come from attn_rope_plan")
     batch = 0
     if positions is not None:
-        _need(positions, "positions", where, (torch.int32,), (T,), dev)
+        if not _fits(positions, torch.int32, (T,), dev.index):
+            _need(positions, "positions", where, (torch.int32,), (T,), dev)
     elif cu_seqlens is None:
         raise AttnError(1, f"{where}: positions or cu_seqlens is required")
     else:
-        _need(cu_seqlens, "cu_seqlens", where, (torch.int32,), device=dev)
+        if not (isinstance(cu_seqlens, torch.Tensor) and _fits(cu_seqlens, torch.int32, cu_seqlens.shape, dev.index)):
+            _need(cu_seqlens, "cu_seqlens", where, (torch.int32,), device=dev)
         batch = cu_seqlens.numel() - 1
-        _need(seq_lens, "seq_lens", where, (torch.int32,), (batch,), dev)
-    with _Launch(dev, stream) as s:
+        if seq_lens is not None and not _fits(seq_lens, torch.int32, (batch,), dev.index):
+            _need(seq_lens, "seq_lens", where, (torch.int32,), (batch,), dev)
+    with _launch(dev, stream) as s:
         if q_out is None:
             q_out, qos = torch.empty((T, H, D), dtype=q.dtype, device=dev), H * D
         else:
@@ -499,7 +524,7 @@ class KVCache:
             status = torch.zeros(1, dtype=torch.int32, device=dev)
         self.k_pages, self.v_pages, self.k_scale, self.v_scale = k_pages, v_pages, k_scale, v_scale
         self.page_table, self.status = page_table, status
-        self.device, self.num_kv_heads, self.head_dim = dev, H, D
+        self.device, self.index, self.num_kv_heads, self.head_dim = dev, dev.index, H, D
         self.batch, self.max_pages = page_table.shape
         self.page_size, self.num_pages = ps, P
         self.struct = _native.AttnKVCache(
@@ -527,8 +552,10 @@ def _need_cache(cache, where: str) -> KVCache:
 def _need_seqs(cache: KVCache, cu_seqlens, seq_lens, where: str) -> None:
     if seq_lens is None or cu_seqlens is None:
         raise AttnError(1, f"{where}: cu_seqlens and seq_lens are required")
-    _need(cu_seqlens, "cu_seqlens", where, (torch.int32,), (cache.batch + 1,), cache.device)
-    _need(seq_lens, "seq_lens", where, (torch.int32,), (cache.batch,), cache.device)
+    if not (_fits(cu_seqlens, torch.int32, (cache.batch + 1,), cache.index)
+            and _fits(seq_lens, torch.int32, (cache.batch,), cache.index)):
+        _need(cu_seqlens, "cu_seqlens", where, (torch.int32,), (cache.batch + 1,), cache.device)
+        _need(seq_lens, "seq_lens", where, (torch.int32,), (cache.batch,), cache.device)
 
 
 def attn_cache_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, cu_seqlens: torch.Tensor,
@@ -546,7 +573,7 @@ def attn_cache_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, cu_seqle
         raise AttnError(1, f"{where}: k and v must be [tokens, {cache.num_kv_heads}, {cache.head_dim}], got "
                            f"{tuple(k.shape)} and {tuple(v.shape)}")
     _need_seqs(cache, cu_seqlens, seq_lens, where)
-    with _Launch(cache.device, stream) as s:
+    with _launch(cache.device, stream) as s:
         _check(_native.lib().attn_cache_append(
             k.data_ptr(), v.data_ptr(), ks, vs, DTYPES[k.dtype], k.shape[0], cu_seqlens.data_ptr(),
             seq_lens.data_ptr(), int(max_new), cache._ref, s), where)
@@ -556,7 +583,8 @@ def _need_queries(q, cache, where: str):
     _need_cache(cache, where)
     if q is None:
         raise AttnError(1, f"{where}: q is required")
-    _need(q, "q", where, tuple(DTYPES), device=cache.device)
+    if not (isinstance(q, torch.Tensor) and _fits(q, torch.bfloat16, q.shape, cache.index)):
+        _need(q, "q", where, tuple(DTYPES), device=cache.device)
     if q.dtype != torch.bfloat16:
         raise AttnError(2, f"{where}: dtype must be bfloat16")
     if q.dim() != 3 or q.shape[2] != cache.head_dim or q.shape[1] % cache.num_kv_heads:
@@ -592,11 +620,13 @@ def attn_cache_fwd(q: torch.Tensor, cache: KVCache, cu_seqlens: torch.Tensor, se
     where = "attn_cache_fwd"
     T, H, D = _need_queries(q, cache, where)
     dev = cache.device
-    _need(out, "out", where, (q.dtype,), q.shape, dev)
-    _need(lse, "lse", where, (torch.float32,), (H, T), dev)
+    if out is not None and not _fits(out, q.dtype, q.shape, cache.index):
+        _need(out, "out", where, (q.dtype,), q.shape, dev)
+    if lse is not None and not _fits(lse, torch.float32, (H, T), cache.index):
+        _need(lse, "lse", where, (torch.float32,), (H, T), dev)
     _need(workspace, "workspace", where, device=dev)
     _need_seqs(cache, cu_seqlens, seq_lens, where)
-    with _Launch(dev, stream) as s:
+    with _launch(dev, stream) as s:
         if out is None:
             out = torch.empty_like(q)
         if lse is None:
@@ -629,16 +659,17 @@ def attn_cache_weights(q: torch.Tensor, lse: torch.Tensor, cache: KVCache, cu_se
     dev = cache.device
     if lse is None:
         raise AttnError(1, f"{where}: lse is required")
-    _need(lse, "lse", where, (torch.float32,), (H, T), dev)
+    if not _fits(lse, torch.float32, (H, T), cache.index):
+        _need(lse, "lse", where, (torch.float32,), (H, T), dev)
     _need_seqs(cache, cu_seqlens, seq_lens, where)
-    _need(prev, "prev", where, (torch.float32,), device=dev)
-    _need(out, "out", where, (torch.float32,), device=dev)
     like = out if out is not None else prev
     shape = (cache.batch, cache.num_kv_heads, int(max_seqlen)) if like is None else tuple(like.shape)
     if len(shape) != 3 or shape[:2] != (cache.batch, cache.num_kv_heads):
         raise AttnError(1, f"{where}: weights must be [{cache.batch}, {cache.num_kv_heads}, width], got {shape}")
-    _need(prev, "prev", where, shape=shape)
-    with _Launch(dev, stream) as s:
+    for name, t in (("prev", prev), ("out", out)):
+        if t is not None and not _fits(t, torch.float32, shape, cache.index):
+            _need(t, name, where, (torch.float32,), shape, dev)
+    with _launch(dev, stream) as s:
         if out is None:
             out = torch.zeros(shape, dtype=torch.float32, device=dev)
         _check(_native.lib().attn_cache_weights(
@@ -671,18 +702,21 @@ def attn_cache_evict(weights: torch.Tensor, cache: KVCache, dst: KVCache, seq_le
     for name, t in (("weights", weights), ("seq_lens", seq_lens), ("budgets", budgets)):
         if t is None:
             raise AttnError(1, f"{where}: {name} is required")
-    _need(weights, "weights", where, (torch.float32,), device=dev)
-    _need(seq_lens, "seq_lens", where, (torch.int32,), (B,), dev)
-    _need(budgets, "budgets", where, (torch.int32,), (B,), dev)
-    _need(kept, "kept", where, (torch.int32,), (B, H, max_keep), dev)
-    _need(new_weights, "new_weights", where, (torch.float32,), device=dev)
-    _need(new_lens, "new_lens", where, (torch.int32,), (B,), dev)
+    for name, t, dtype, shape in (("seq_lens", seq_lens, torch.int32, (B,)), ("budgets", budgets, torch.int32, (B,)),
+                                  ("kept", kept, torch.int32, (B, H, max_keep)),
+                                  ("new_lens", new_lens, torch.int32, (B,))):
+        if t is not None and not _fits(t, dtype, shape, cache.index):
+            _need(t, name, where, (dtype,), shape, dev)
     for name, t in (("weights", weights), ("new_weights", new_weights)):
-        if t is not None and (t.dim() != 3 or tuple(t.shape[:2]) != (B, H)):
+        if t is None:
+            continue
+        if not (isinstance(t, torch.Tensor) and _fits(t, torch.float32, t.shape, cache.index)):
+            _need(t, name, where, (torch.float32,), device=dev)
+        if t.dim() != 3 or t.shape[0] != B or t.shape[1] != H:
             raise AttnError(1, f"{where}: {name} must be [{B}, {H}, width], got {tuple(t.shape)}")
     if max_keep < 0:
         raise AttnError(1, f"{where}: max_keep is negative")
-    with _Launch(dev, stream) as s:
+    with _launch(dev, stream) as s:
         if kept is None:
             kept = torch.empty((B, H, max_keep), dtype=torch.int32, device=dev)
         if new_weights is None:
@@ -699,5 +733,5 @@ def attn_cache_evict(weights: torch.Tensor, cache: KVCache, dst: KVCache, seq_le
 def attn_cache_get_status(cache: KVCache, stream=None) -> int:
     """Synchronise, then return and clear the cache's device status code."""
     _need_cache(cache, "attn_cache_get_status")
-    with _Launch(cache.device, stream) as s:
+    with _launch(cache.device, stream) as s:
         return int(_native.lib().attn_cache_get_status(cache._ref, s))

@@ -30,15 +30,15 @@ constexpr int kWarps = 4;
 constexpr int kAttnThreads = 32 * kWarps;
 constexpr int kStages = 4;  // groups in flight per warp
 constexpr int kGroup = 16;  // tokens per group
+constexpr int kMost = 32;   // groups per warp at most: a chunk has 2048 tokens or less
 constexpr float kRaise = 8.f;
 
 template <int D>
 struct AttnCfg {
-  static constexpr int LB = D / 4;           // bytes of a token's keys per lane
-  static constexpr int VB = D / 8;           // bytes of a token's values per lane
-  static constexpr int LANE = 2 * LB + 4 * VB;  // bytes of a group per lane (D)
-  static constexpr int PIECE = VB < 16 ? VB : 16;  // bytes per copy
-  static constexpr int STAGE = 32 * LANE + 32 * 8;  // per warp: codes, then two scales per lane
+  // A lane copies a group in eight pieces: two of the keys of two tokens each,
+  // one of the values of four tokens.
+  static constexpr int PIECE = D / 8;
+  static constexpr int STAGE = 32 * 8 * PIECE;  // per warp
   static constexpr int QUEUE = kWarps * kStages * STAGE;
   static constexpr int MERGE = kWarps * 16 * (D + 2) * 4;
   static constexpr int SMEM = QUEUE > MERGE ? QUEUE : MERGE;
@@ -78,49 +78,44 @@ __global__ void __launch_bounds__(kAttnThreads, 3) cache_attn_kernel(const Cache
   const int mine = groups > warp ? (groups - warp + kWarps - 1) / kWarps : 0;
   const int64_t page_bytes = int64_t(D) << c.page_log2;
 
-  // Page of the warp's i-th group; kept one group ahead of its copies.
-  auto page_of = [&](int i) -> int {
-    if (i >= mine) return -1;
-    return load_page(c, b, (begin + (warp + i * kWarps) * kGroup) >> c.page_log2);
-  };
-  auto issue = [&](int i, int page) {
+  // Lane i looks up the page of the warp's i-th group and its scales (at most
+  // kMost groups per warp), once; they travel by shuffle.  A page that is left
+  // out has scale 0: none of its tokens is visible.
+  int my_page = -1;
+  float my_ks = 0.f, my_vs = 0.f;
+  if (lane < mine) {
+    my_page = load_page(c, b, (begin + (warp + lane * kWarps) * kGroup) >> c.page_log2);
+    if (my_page >= 0) {
+      my_ks = c.k_scale[int64_t(my_page) * c.heads + h];
+      my_vs = c.v_scale[int64_t(my_page) * c.heads + h];
+    }
+  }
+  auto issue = [&](int i) {
+    const int page = __shfl_sync(0xffffffffu, my_page, i & 31);
     if (i < mine) {
       const int tok = begin + (warp + i * kWarps) * kGroup;
       const int slot = tok & ((1 << c.page_log2) - 1);
-      const bool fine = page >= 0;
-      const int64_t base = (int64_t(fine ? page : 0) * c.heads + h) * page_bytes + int64_t(slot) * D;
-      const uint8_t* kp = c.k_pages + base;
-      const uint8_t* vp = c.v_pages + base;
-      const uint32_t dst = queue + (i % kStages) * C::STAGE;
+      const int64_t base = (int64_t(max(page, 0)) * c.heads + h) * page_bytes + int64_t(slot) * D;
+      const uint8_t* kp = c.k_pages + base + g * D + t * C::PIECE;
+      const uint8_t* vp = c.v_pages + base + 2 * t * D + g * C::PIECE;
+      const uint32_t dst = queue + (i % kStages) * C::STAGE + lane * C::PIECE;
+      const int left = page >= 0 ? end - tok : 0;  // tokens of the group; zeros behind them
       // piece j of lane l at (j * 32 + l) * PIECE: no bank conflicts either way
-      int j = 0;
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-        for (int x = 0; x < C::LB / C::PIECE; ++x, ++j) {
-          const int tk = 8 * nt + g;
-          copy_async<C::PIECE>(dst + (j * 32 + lane) * C::PIECE, kp + tk * D + t * C::LB + x * C::PIECE,
-                               fine && tok + tk < end);
-        }
+        for (int x = 0; x < 2; ++x)
+          copy_async<C::PIECE>(dst + (2 * nt + x) * 32 * C::PIECE, kp + nt * 8 * D + x * (D / 2), 8 * nt + g < left);
 #pragma unroll
-      for (int q = 0; q < 4; ++q, ++j) {
-        const int tk = 8 * (q >> 1) + 2 * t + (q & 1);
-        copy_async<C::PIECE>(dst + (j * 32 + lane) * C::PIECE, vp + tk * D + g * C::VB, fine && tok + tk < end);
+      for (int q = 0; q < 4; ++q) {
+        const int tk = 8 * (q >> 1) + (q & 1);
+        copy_async<C::PIECE>(dst + (4 + q) * 32 * C::PIECE, vp + tk * D, tk + 2 * t < left);
       }
-      const int64_t sc = int64_t(fine ? page : 0) * c.heads + h;
-      copy_async<4>(dst + 32 * C::LANE + lane * 4, c.k_scale + sc, fine);
-      copy_async<4>(dst + 32 * C::LANE + 128 + lane * 4, c.v_scale + sc, fine);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-
-  int page = page_of(0);
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) {
-    const int next = page_of(i + 1);
-    issue(i, page);
-    page = next;
-  }
+  for (int i = 0; i < kStages - 1; ++i) issue(i);
 
   // the queries of rows g and g + 8
   uint32_t qa[D / 8], qb[D / 8];
@@ -135,26 +130,22 @@ __global__ void __launch_bounds__(kAttnThreads, 3) cache_attn_kernel(const Cache
   float ma = -INFINITY, mb = -INFINITY, la = 0.f, lb = 0.f;
 
   for (int i = 0; i < mine; ++i) {
-    const int next = page_of(i + kStages);
-    issue(i + kStages - 1, page);
-    page = next;
+    issue(i + kStages - 1);
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-    const uint8_t* st = queue_ptr + (i % kStages) * C::STAGE;
-    const float ks = *reinterpret_cast<const float*>(st + 32 * C::LANE + lane * 4);
-    const float vs = *reinterpret_cast<const float*>(st + 32 * C::LANE + 128 + lane * 4);
+    const uint8_t* st = queue_ptr + (i % kStages) * C::STAGE + lane * C::PIECE;
+    const float ks = __shfl_sync(0xffffffffu, my_ks, i), vs = __shfl_sync(0xffffffffu, my_vs, i);
     const int tok = begin + (warp + i * kWarps) * kGroup;
 
     float s[2][4];
-    int j = 0;
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt) {
       s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
 #pragma unroll
-      for (int x = 0; x < C::LB / C::PIECE; ++x, ++j) {
+      for (int x = 0; x < 2; ++x) {
         uint32_t w[C::PIECE / 4];
-        const uint8_t* at = st + (j * 32 + lane) * C::PIECE;
 #pragma unroll
-        for (int y = 0; y < C::PIECE / 4; ++y) w[y] = reinterpret_cast<const uint32_t*>(at)[y];
+        for (int y = 0; y < C::PIECE / 4; ++y)
+          w[y] = reinterpret_cast<const uint32_t*>(st + (2 * nt + x) * 32 * C::PIECE)[y];
 #pragma unroll
         for (int y = 0; y < C::PIECE / 4; ++y) {
           const int step = x * (C::PIECE / 4) + y;
@@ -163,7 +154,6 @@ __global__ void __launch_bounds__(kAttnThreads, 3) cache_attn_kernel(const Cache
         }
       }
     }
-    // a page that was left out has scale 0: none of its tokens is visible
     const float x = float(exponent_of(vs)), inv_vs = pow2f(max(-126, -exponent_of(vs)));
     const float fa = sa * ks, fb = sb * ks;
     float pw[2][4];
@@ -218,11 +208,10 @@ __global__ void __launch_bounds__(kAttnThreads, 3) cache_attn_kernel(const Cache
     // values: tokens 2t, 2t + 1 and 2t + 8, 2t + 9, dimensions g D/8 ..
     uint32_t v[4][C::PIECE / 4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q, ++j) {
-      const uint8_t* at = st + (j * 32 + lane) * C::PIECE;
+    for (int q = 0; q < 4; ++q)
 #pragma unroll
-      for (int y = 0; y < C::PIECE / 4; ++y) v[q][y] = reinterpret_cast<const uint32_t*>(at)[y];
-    }
+      for (int y = 0; y < C::PIECE / 4; ++y)
+        v[q][y] = reinterpret_cast<const uint32_t*>(st + (4 + q) * 32 * C::PIECE)[y];
 #pragma unroll
     for (int y = 0; y < C::PIECE / 4; ++y) {
       const uint32_t l0 = __byte_perm(v[0][y], v[1][y], 0x5140), l1 = __byte_perm(v[0][y], v[1][y], 0x7362);
@@ -247,10 +236,10 @@ __global__ void __launch_bounds__(kAttnThreads, 3) cache_attn_kernel(const Cache
 #pragma unroll
   for (int k = 0; k < D / 8; ++k) {
     // column 2t (2t + 1) of product k is dimension (2t) D/8 + k ((2t + 1) D/8 + k)
-    mine_o[g * D + 2 * t * C::VB + k] = o[k][0];
-    mine_o[g * D + (2 * t + 1) * C::VB + k] = o[k][1];
-    mine_o[(g + 8) * D + 2 * t * C::VB + k] = o[k][2];
-    mine_o[(g + 8) * D + (2 * t + 1) * C::VB + k] = o[k][3];
+    mine_o[g * D + 2 * t * C::PIECE + k] = o[k][0];
+    mine_o[g * D + (2 * t + 1) * C::PIECE + k] = o[k][1];
+    mine_o[(g + 8) * D + 2 * t * C::PIECE + k] = o[k][2];
+    mine_o[(g + 8) * D + (2 * t + 1) * C::PIECE + k] = o[k][3];
   }
   if (t == 0) {
     ml[(warp * 16 + g) * 2] = ma;
@@ -351,6 +340,7 @@ void plan(CacheAttnParams* p) {
   p->row_tiles = int((rows + p->tile_rows - 1) / p->tile_rows);
   const int64_t items = int64_t(p->row_tiles) * a.cache.heads * a.cache.batch;
   const int64_t fill = (many ? 2 : 6) * kSms, least = many ? 1024 : 256, most = many ? 4096 : 1024;
+  static_assert(1024 <= kMost * kWarps * kGroup, "a warp's groups fit its lanes");
   const int64_t want = items > 0 ? (fill + items - 1) / items : 1;
   int64_t chunk = (int64_t(a.max_seqlen) + want - 1) / want;
   chunk = (chunk + kTile - 1) / kTile * kTile;

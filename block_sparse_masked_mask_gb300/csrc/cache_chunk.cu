@@ -18,18 +18,21 @@
 // Warps (512 threads):
 //   0-3, 4-7   softmax of M tile 0 and 1, one thread per row
 //   8-11       values: codes to fp16 tiles (two slots)
-//   12         TMA of the keys (three slots), pages' scales (four slots)
-//   13, 14     tcgen05 issuers of M tile 0 and 1
-//   15         TMEM allocation
-// The two M tiles share only the tiles read: while one's softmax runs, the
-// tensor cores work for the other.  P of a tile is written over its S, so an
-// M tile's S(j + 1) waits for its P V(j).  TMEM columns: S0 [0, 128), S1
-// [128, 256), O0 [256, 256 + D), O1 [384, 384 + D).
+//   12         pages, scales (four slots) and TMA of the keys (three slots)
+//   13         tcgen05 issuer of S for both M tiles
+//   14, 15     tcgen05 issuers of P V, one per M tile (15 also owns TMEM)
+// Keys and values come in tiles of 128 tokens; the products and the softmax go
+// in steps of 64, with two S buffers per M tile: S of the next step is there
+// when a softmax ends its step, so the softmax and the tensor cores both run
+// without a pause.  P of a step is written over its S; S(i + 2) waits for P V(i).
+// (With one S buffer of 128 tokens per M tile the chain S, softmax, P V of a
+// tile took 6200 cycles, most of it with the tensor cores idle.)
+// TMEM columns: S of M tile m, buffer f at 128 m + 64 f; O at 256 + 128 m.
 // Every wait is bounded, as in the other tcgen05 kernels, and ends in
 // ATTN_ERR_DEVICE_TIMEOUT in the cache's status word.  Each role waits only for
-// an earlier tile's events of the others, or for this tile's by a role that
-// comes before it (keys, S, softmax, P V), so the order of tiles carries every
-// wait to its end.
+// an earlier step's events of the others, or for this step's by a role that
+// comes before it (pages, keys / values, S, softmax, P V), so the order of steps
+// carries every wait to its end.
 #include "cache_rows.cuh"
 #include "tile_pipeline.cuh"
 
@@ -37,9 +40,8 @@ namespace attnmask {
 namespace {
 
 constexpr int kChunkThreads = 512;
-constexpr int kWarpValues = 8, kWarpKeys = 12, kWarpIssue = 13, kWarpAlloc = 15;
-constexpr int kRegsSoftmax = 160, kRegsOther = 96;
-static_assert(256 * kRegsSoftmax + 256 * kRegsOther == kChunkThreads * 128, "register split");
+constexpr int kWarpValues = 8, kWarpKeys = 12, kWarpS = 13, kWarpPV = 14;
+constexpr int kStep = 64;  // tokens per step
 
 template <int D>
 struct ChunkCfg {
@@ -50,13 +52,15 @@ struct ChunkCfg {
   static constexpr int OFF_Q = 0;              // [M tile][hi, lo]
   static constexpr int OFF_K = OFF_Q + 4 * KT;
   static constexpr int OFF_V = OFF_K + NK * KT;
-  static constexpr int OFF_SCL = OFF_V + NV * VT;          // [slot][8 blocks of 16 tokens] float4
-  static constexpr int OFF_BAD = OFF_SCL + NSCL * 8 * 16;  // [slot] bits of blocks without a page
+  // [slot][8 blocks of 16 tokens]: key scale, exponent of the value scale, its
+  // inverse, the page (as an int; -1: none)
+  static constexpr int OFF_SCL = OFF_V + NV * VT;
+  // B_SFULL, B_PFULL, B_PDONE: per M tile and S buffer
   static constexpr int B_Q = 0, B_KFULL = 2, B_KEMPTY = B_KFULL + NK, B_VFULL = B_KEMPTY + NK,
                        B_VEMPTY = B_VFULL + NV, B_SCLFULL = B_VEMPTY + NV, B_SCLFREE = B_SCLFULL + NSCL,
-                       B_SFULL = B_SCLFREE + NSCL, B_PFULL = B_SFULL + 2, B_PDONE = B_PFULL + 2,
-                       B_DRAIN = B_PDONE + 2, NBAR = B_DRAIN + 2;
-  static constexpr int OFF_BAR = (OFF_BAD + NSCL * 4 + 15) & ~15;
+                       B_SFULL = B_SCLFREE + NSCL, B_PFULL = B_SFULL + 4, B_PDONE = B_PFULL + 4,
+                       B_DRAIN = B_PDONE + 4, NBAR = B_DRAIN + 3;
+  static constexpr int OFF_BAR = (OFF_SCL + NSCL * 8 * 16 + 15) & ~15;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int USED = OFF_MISC + 16 + 1024;        // the base is aligned to 1024
   // one CTA per SM: it takes all of TMEM
@@ -92,7 +96,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const int limit = visible_tokens(r, p.G, row0 + rows - 1, a.causal);
   const int begin = split * p.chunk, end = min(begin + p.chunk, limit);
   if (split > 0 && begin >= end) return;  // chunk 0 also answers for rows that see nothing
-  const int tiles = end > begin ? (end - begin + kTile - 1) / kTile : 0;
+  const int steps = end > begin ? (end - begin + kStep - 1) / kStep : 0;
+  const int tiles = (steps + 1) / 2;
   const int nm = rows > kTile ? 2 : 1;  // M tiles
   int32_t* err = c.status;
 
@@ -104,12 +109,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   uint32_t* misc = reinterpret_cast<uint32_t*>(sbase + C::OFF_MISC);
   volatile uint32_t* abort_flag = misc + 1;
   float4* scl = reinterpret_cast<float4*>(sbase + C::OFF_SCL);
-  uint32_t* bad = reinterpret_cast<uint32_t*>(sbase + C::OFF_BAD);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NK; ++i) {
       ptx::mbar_init(bar(C::B_KFULL + i), 1);
-      ptx::mbar_init(bar(C::B_KEMPTY + i), nm);
+      ptx::mbar_init(bar(C::B_KEMPTY + i), 1);
     }
     for (int i = 0; i < C::NV; ++i) {
       ptx::mbar_init(bar(C::B_VFULL + i), 4);
@@ -117,20 +121,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
     for (int i = 0; i < C::NSCL; ++i) {
       ptx::mbar_init(bar(C::B_SCLFULL + i), 1);
-      ptx::mbar_init(bar(C::B_SCLFREE + i), 4 * nm);
+      ptx::mbar_init(bar(C::B_SCLFREE + i), 4 * nm + 4);  // softmax and value warps
     }
-    for (int m = 0; m < 2; ++m) {
-      ptx::mbar_init(bar(C::B_Q + m), 4);
-      ptx::mbar_init(bar(C::B_SFULL + m), 1);
-      ptx::mbar_init(bar(C::B_PFULL + m), 4);
-      ptx::mbar_init(bar(C::B_PDONE + m), 1);
-      ptx::mbar_init(bar(C::B_DRAIN + m), 1);
+    for (int i = 0; i < 4; ++i) {
+      ptx::mbar_init(bar(C::B_SFULL + i), 1);
+      ptx::mbar_init(bar(C::B_PFULL + i), 4);
+      ptx::mbar_init(bar(C::B_PDONE + i), 1);
     }
+    for (int i = 0; i < 2; ++i) ptx::mbar_init(bar(C::B_Q + i), 4);
+    for (int i = 0; i < 3; ++i) ptx::mbar_init(bar(C::B_DRAIN + i), 1);
     // an earlier CTA that gave up on a wait makes every later one skip its work
     *abort_flag = (*reinterpret_cast<volatile int32_t*>(err) & kErrTimeout) ? 1u : 0u;
     ptx::fence_mbar_init();
   }
-  if (warp == kWarpAlloc) {
+  if (warp == kWarpPV + 1) {
     ptx::tmem_alloc(ptx::smem_addr(misc), 512);
     ptx::tmem_relinquish();
   }
@@ -142,129 +146,146 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 
   if (skip) {
     // nothing issued, nothing to drain
-  } else if (warp >= kWarpKeys) {
-    ptx::regs_dec<kRegsOther>();
-    if (warp == kWarpKeys) {
-      // ------------------------------------------------------------ keys, scales
-      // lane i < 8: the i-th 16 tokens of a tile
-      const int step = max(1, (1 << c.page_log2) / 16);  // lanes per page
-      const bool leader = lane < 8 && lane % step == 0;
-      int page = -1;
-      float ks = 0.f, vs = 0.f;
-      auto lookup = [&](int j) {
-        page = -1;
-        ks = vs = 0.f;
-        const int tok = begin + j * kTile + lane * 16;
-        if (lane < 8 && j < tiles && tok < end) {
-          page = load_page(c, b, tok >> c.page_log2);
-          if (page >= 0) {
-            ks = c.k_scale[int64_t(page) * c.heads + h];
-            vs = c.v_scale[int64_t(page) * c.heads + h];
-          }
-        }
-      };
-      if (lane == 0) ptx::prefetch_tensormap(&tmK);
-      lookup(0);
-      int done = 0;
-      for (int j = 0; j < tiles; ++j) {
-        const int ss = j % C::NSCL, slot = j % C::NK;
-        if (j >= C::NSCL &&
-            !warp_wait(bar(C::B_SCLFREE + ss), uint32_t(j / C::NSCL - 1) & 1u, abort_flag, err, 1))
-          break;
-        const int tok = begin + j * kTile + lane * 16;
-        if (lane < 8) {
-          const int x = exponent_of(vs);
-          scl[ss * 8 + lane] = page >= 0 ? make_float4(ks, float(x), pow2f(max(-126, -x)), 0.f)
-                                         : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        const uint32_t missing = __ballot_sync(0xffffffffu, lane < 8 && tok < end && page < 0);
-        if (lane == 0) bad[ss] = missing;
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(C::B_SCLFULL + ss));
-        if (j >= C::NK && !warp_wait(bar(C::B_KEMPTY + slot), uint32_t(j / C::NK - 1) & 1u, abort_flag, err, 2)) break;
-        const bool load = leader && page >= 0;
-        const uint32_t loads = __ballot_sync(0xffffffffu, load);
-        const uint32_t piece = uint32_t(D) << c.page_log2;  // bytes of a page's keys
-        if (lane == 0) ptx::mbar_arrive_expect_tx(bar(C::B_KFULL + slot), piece * __popc(loads));
-        __syncwarp();
-        if (load)
-          ptx::tma_load_4d(base + C::OFF_K + slot * C::KT + lane * 16 * D, &tmK, bar(C::B_KFULL + slot), 0, 0, h, page);
-        done = j + 1;
-        lookup(j + 1);
-      }
-      // do not leave while a copy may still be writing shared memory
-      if (lane == 0) {
-        for (int s = 0; s < C::NK; ++s) {
-          if (done <= s) continue;
-          const int last = s + C::NK * ((done - 1 - s) / C::NK);
-          drain_bar(bar(C::B_KFULL + s), uint32_t(last / C::NK) & 1u, err);
-        }
+  } else if (warp == kWarpKeys) {
+    // -------------------------------------------------------------- pages, scales, keys
+    // Lane i < 8: the i-th 16 tokens of a tile.  Page numbers are read two tiles
+    // ahead, scales one, so that neither read is waited for.
+    const int step = (1 << c.page_log2) / 16;  // lanes per page
+    auto number = [&](int j) {
+      const int tok = begin + j * kTile + lane * 16;
+      return lane < 8 && tok < end ? __ldg(c.table + int64_t(b) * c.max_pages + (tok >> c.page_log2)) : 0;
+    };
+    auto scales = [&](int j, int id) {
+      const int tok = begin + j * kTile + lane * 16;
+      const bool fine = lane < 8 && tok < end && unsigned(id) < unsigned(c.num_pages);
+      const int64_t at = fine ? int64_t(id) * c.heads + h : 0;
+      return make_float2(fine ? __ldg(c.k_scale + at) : 0.f, fine ? __ldg(c.v_scale + at) : 0.f);
+    };
+    if (lane == 0) ptx::prefetch_tensormap(&tmK);
+    int id = number(0), id_next = number(1);
+    float2 sc = scales(0, id);
+    int done = 0;
+    for (int j = 0; j < tiles; ++j) {
+      const int id_after = number(j + 2);
+      const float2 sc_next = scales(j + 1, id_next);
+      const int ss = j % C::NSCL, slot = j % C::NK;
+      const int tok = begin + j * kTile + lane * 16;
+      const bool here = lane < 8 && tok < end, fine = here && unsigned(id) < unsigned(c.num_pages);
+      if (here && !fine) atomicOr(err, kErrBadPage);
+      if (j >= C::NSCL && !warp_wait(bar(C::B_SCLFREE + ss), uint32_t(j / C::NSCL - 1) & 1u, abort_flag, err, 1))
+        break;
+      if (lane < 8) {
+        const int x = exponent_of(sc.y);
+        scl[ss * 8 + lane] = fine ? make_float4(sc.x, float(x), pow2f(max(-126, -x)), __int_as_float(id))
+                                  : make_float4(0.f, 0.f, 0.f, __int_as_float(-1));
       }
       __syncwarp();
-    } else if (warp < kWarpIssue + nm) {
-      // ------------------------------------------------------------ issuers
-      const int m = warp - kWarpIssue;
-      if (lane == 0) {
-        constexpr uint32_t IDESC_S = ptx::idesc_e4m3_f32(128, 128);
-        constexpr uint32_t IDESC_PV = ptx::idesc_f16_f32(128, D, false, true);
-        const uint32_t s_tmem = tmem + uint32_t(m) * 128u, o_tmem = tmem + 256u + uint32_t(m) * 128u;
-        const uint64_t qhi = ptx::smem_desc(base + C::OFF_Q + (2 * m) * C::KT, 16u, 8 * D, C::SW8);
-        const uint64_t qlo = ptx::smem_desc(base + C::OFF_Q + (2 * m + 1) * C::KT, 16u, 8 * D, C::SW8);
-        const uint64_t kd = ptx::smem_desc(base + C::OFF_K, 16u, 8 * D, C::SW8);
-        const uint64_t vd = v_base<D>(base + C::OFF_V);
-        bool ok = tiles == 0 || wait_bar(bar(C::B_Q + m), 0, abort_flag, err, 3);
-        for (int j = 0; ok && j < tiles; ++j) {
-          const int ks = j % C::NK, vslot = j % C::NV;
-          if (!wait_bar(bar(C::B_KFULL + ks), uint32_t(j / C::NK) & 1u, abort_flag, err, 4)) break;
-          // P(j - 1) lies over S: its product has read it
-          if (j > 0 && !wait_bar(bar(C::B_PDONE + m), uint32_t(j - 1) & 1u, abort_flag, err, 5)) break;
-          ptx::tc_fence_after();
-          const uint64_t kj = kd + uint64_t(ks) * (C::KT >> 4);
-#pragma unroll
-          for (int kk = 0; kk < D / 32; ++kk) ptx::mma_f8_ss(s_tmem, qhi + 2 * kk, kj + 2 * kk, IDESC_S, kk > 0);
-#pragma unroll
-          for (int kk = 0; kk < D / 32; ++kk) ptx::mma_f8_ss(s_tmem, qlo + 2 * kk, kj + 2 * kk, IDESC_S, 1);
-          ptx::mma_commit(bar(C::B_SFULL + m));
-          ptx::mma_commit(bar(C::B_KEMPTY + ks));
-          if (!wait_bar(bar(C::B_VFULL + vslot), uint32_t(j / C::NV) & 1u, abort_flag, err, 6)) break;
-          if (!wait_bar(bar(C::B_PFULL + m), uint32_t(j) & 1u, abort_flag, err, 7)) break;
-          ptx::tc_fence_after();
-          const uint64_t vj = vd + uint64_t(vslot) * (C::VT >> 4);
-#pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)
-            ptx::mma_ts(o_tmem, s_tmem + uint32_t(kk) * 8u, vj + v_step<D>(kk), IDESC_PV, (j > 0 || kk > 0) ? 1u : 0u);
-          ptx::mma_commit(bar(C::B_PDONE + m));
-          ptx::mma_commit(bar(C::B_VEMPTY + vslot));
-        }
-        // every product this thread issued has finished once this arrives
-        ptx::mma_commit(bar(C::B_DRAIN + m));
-        drain_bar(bar(C::B_DRAIN + m), 0, err);
-      }
+      if (lane == 0) ptx::mbar_arrive(bar(C::B_SCLFULL + ss));
+      if (j >= C::NK && !warp_wait(bar(C::B_KEMPTY + slot), uint32_t(j / C::NK - 1) & 1u, abort_flag, err, 2)) break;
+      const bool load = fine && lane % step == 0;  // one lane per page
+      const uint32_t loads = __ballot_sync(0xffffffffu, load);
+      const uint32_t piece = uint32_t(D) << c.page_log2;  // bytes of a page's keys
+      if (lane == 0) ptx::mbar_arrive_expect_tx(bar(C::B_KFULL + slot), piece * __popc(loads));
       __syncwarp();
+      if (load)
+        ptx::tma_load_4d(base + C::OFF_K + slot * C::KT + lane * 16 * D, &tmK, bar(C::B_KFULL + slot), 0, 0, h, id);
+      done = j + 1;
+      id = id_next;
+      id_next = id_after;
+      sc = sc_next;
     }
+    // do not leave while a copy may still be writing shared memory
+    if (lane == 0) {
+      for (int s = 0; s < C::NK; ++s) {
+        if (done <= s) continue;
+        const int last = s + C::NK * ((done - 1 - s) / C::NK);
+        drain_bar(bar(C::B_KFULL + s), uint32_t(last / C::NK) & 1u, err);
+      }
+    }
+    __syncwarp();
+  } else if (warp == kWarpS) {
+    // -------------------------------------------------------------- S issuer
+    if (lane == 0) {
+      constexpr uint32_t IDESC = ptx::idesc_e4m3_f32(128, kStep);
+      const uint64_t qd = ptx::smem_desc(base + C::OFF_Q, 16u, 8 * D, C::SW8);
+      const uint64_t kd = ptx::smem_desc(base + C::OFF_K, 16u, 8 * D, C::SW8);
+      bool ok = true;
+      for (int m = 0; m < nm && ok && steps > 0; ++m) ok = wait_bar(bar(C::B_Q + m), 0, abort_flag, err, 3);
+      for (int i = 0; ok && i < steps; ++i) {
+        const int j = i >> 1, ks = j % C::NK, f = i & 1;
+        if (f == 0 && !wait_bar(bar(C::B_KFULL + ks), uint32_t(j / C::NK) & 1u, abort_flag, err, 4)) break;
+        const uint64_t ki = kd + uint64_t((ks * C::KT + f * kStep * D) >> 4);
+        for (int m = 0; m < nm; ++m) {
+          // P(i - 2) lies over this S: its product has read it
+          if (i >= 2 && !wait_bar(bar(C::B_PDONE + 2 * m + f), uint32_t(i / 2 - 1) & 1u, abort_flag, err, 5)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          const uint32_t s_tmem = tmem + uint32_t(128 * m + kStep * f);
+          const uint64_t qhi = qd + uint64_t((2 * m * C::KT) >> 4), qlo = qd + uint64_t(((2 * m + 1) * C::KT) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk) ptx::mma_f8_ss(s_tmem, qhi + 2 * kk, ki + 2 * kk, IDESC, kk > 0);
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk) ptx::mma_f8_ss(s_tmem, qlo + 2 * kk, ki + 2 * kk, IDESC, 1);
+          ptx::mma_commit(bar(C::B_SFULL + 2 * m + f));
+        }
+        if (ok && (f == 1 || i == steps - 1)) ptx::mma_commit(bar(C::B_KEMPTY + ks));
+      }
+      // every product this thread issued has finished once this arrives
+      ptx::mma_commit(bar(C::B_DRAIN + 2));
+      drain_bar(bar(C::B_DRAIN + 2), 0, err);
+    }
+    __syncwarp();
+  } else if (warp >= kWarpPV) {
+    // -------------------------------------------------------------- P V issuers
+    const int m = warp - kWarpPV;
+    if (lane == 0 && m < nm) {
+      constexpr uint32_t IDESC = ptx::idesc_f16_f32(128, D, false, true);
+      const uint32_t o_tmem = tmem + 256u + 128u * uint32_t(m);
+      const uint64_t vd = v_base<D>(base + C::OFF_V);
+      for (int i = 0; i < steps; ++i) {
+        const int j = i >> 1, vs = j % C::NV, f = i & 1;
+        if (f == 0 && !wait_bar(bar(C::B_VFULL + vs), uint32_t(j / C::NV) & 1u, abort_flag, err, 6)) break;
+        if (!wait_bar(bar(C::B_PFULL + 2 * m + f), uint32_t(j) & 1u, abort_flag, err, 7)) break;
+        ptx::tc_fence_after();
+        const uint32_t p_tmem = tmem + uint32_t(128 * m + kStep * f);
+        const uint64_t vi = vd + uint64_t(vs) * (C::VT >> 4) + v_step<D>(f * (kStep / 16));
+#pragma unroll
+        for (int kk = 0; kk < kStep / 16; ++kk)
+          ptx::mma_ts(o_tmem, p_tmem + uint32_t(kk) * 8u, vi + v_step<D>(kk), IDESC, (i > 0 || kk > 0) ? 1u : 0u);
+        ptx::mma_commit(bar(C::B_PDONE + 2 * m + f));
+        if (f == 1 || i == steps - 1) ptx::mma_commit(bar(C::B_VEMPTY + vs));
+      }
+      ptx::mma_commit(bar(C::B_DRAIN + m));
+      drain_bar(bar(C::B_DRAIN + m), 0, err);
+    }
+    __syncwarp();
   } else if (warp >= kWarpValues) {
     // ------------------------------------------------------------ values
-    ptx::regs_dec<kRegsOther>();
     constexpr int PPT = D / 16;  // 16-byte pieces per token = pieces per thread
     const int ct = threadIdx.x - kWarpValues * 32;
     uint4 next[PPT];
-    auto fetch = [&](int j) {
+    auto fetch = [&](int j) -> bool {
+      if (j >= tiles) return true;
+      const int ss = j % C::NSCL;
+      if (!warp_wait(bar(C::B_SCLFULL + ss), uint32_t(j / C::NSCL) & 1u, abort_flag, err, 12)) return false;
 #pragma unroll
       for (int i = 0; i < PPT; ++i) {
         const int x = i * 128 + ct, row = x / PPT, piece = x % PPT;
         const int tok = begin + j * kTile + row;
-        next[i] = make_uint4(0, 0, 0, 0);  // behind the end, or without a page: 0 weights times 0
-        if (j < tiles && tok < end) {
-          const int id = __ldg(c.table + int64_t(b) * c.max_pages + (tok >> c.page_log2));
-          if (unsigned(id) < unsigned(c.num_pages))  // the keys' warp notes bad ones
-            next[i] = __ldg(reinterpret_cast<const uint4*>(
-                c.v_pages + (((int64_t(id) * c.heads + h) << c.page_log2) + (tok & ((1 << c.page_log2) - 1))) * D +
-                piece * 16));
-        }
+        const int id = __float_as_int(scl[ss * 8 + row / 16].w);
+        next[i] = make_uint4(0, 0, 0, 0);  // behind the end, or without a page: weights of 0 times 0
+        if (tok < end && id >= 0)
+          next[i] = __ldg(reinterpret_cast<const uint4*>(
+              c.v_pages + (((int64_t(id) * c.heads + h) << c.page_log2) + (tok & ((1 << c.page_log2) - 1))) * D +
+              piece * 16));
       }
+      warp_arrive(bar(C::B_SCLFREE + ss), lane);
+      return true;
     };
-    fetch(0);
-    for (int j = 0; j < tiles; ++j) {
+    bool ok = fetch(0);
+    for (int j = 0; ok && j < tiles; ++j) {
       const int slot = j % C::NV;
       if (j >= C::NV && !warp_wait(bar(C::B_VEMPTY + slot), uint32_t(j / C::NV - 1) & 1u, abort_flag, err, 8)) break;
       uint8_t* tile = sbase + C::OFF_V + slot * C::VT;
@@ -284,16 +305,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
       ptx::fence_proxy_async_smem();
       warp_arrive(bar(C::B_VFULL + slot), lane);
-      fetch(j + 1);
+      ok = fetch(j + 1);
     }
   } else if (warp < 4 * nm) {
     // ------------------------------------------------------------ softmax
-    ptx::regs_inc<kRegsSoftmax>();
     const int m = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;          // of the M tile, its TMEM lane
     const int rg = row0 + m * kTile + row;        // of the sequence and head
     const uint32_t lane_base = tmem + (uint32_t(quarter * 32) << 16);
-    const uint32_t s_col = lane_base + uint32_t(m) * 128u, o_col = lane_base + 256u + uint32_t(m) * 128u;
+    const uint32_t o_col = lane_base + 256u + uint32_t(m) * 128u;
     const bool real = rg < r.n * p.G;
     const int64_t token = r.q0 + (real ? rg / p.G : 0);
     const int head = h * p.G + (real ? rg % p.G : 0);
@@ -342,89 +362,106 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       warp_arrive(bar(C::B_Q + m), lane);
     }
 
-    float mx = -INFINITY, l = 0.f;  // running maximum (of score + value exponent), sum
+    float mx = -INFINITY;                    // running maximum (of score + value exponent)
+    float2 l2 = make_float2(0.f, 0.f);       // two halves of the sum
     bool ok = true;
-    for (int j = 0; j < tiles; ++j) {
-      const int ss = j % C::NSCL;
-      if (!warp_wait(bar(C::B_SCLFULL + ss), uint32_t(j / C::NSCL) & 1u, abort_flag, err, 9)) { ok = false; break; }
-      if (!warp_wait(bar(C::B_SFULL + m), uint32_t(j) & 1u, abort_flag, err, 10)) { ok = false; break; }
+    for (int i = 0; i < steps; ++i) {
+      const int j = i >> 1, f = i & 1, ss = j % C::NSCL;
+      if (f == 0 && !warp_wait(bar(C::B_SCLFULL + ss), uint32_t(j / C::NSCL) & 1u, abort_flag, err, 9)) {
+        ok = false;
+        break;
+      }
+      if (!warp_wait(bar(C::B_SFULL + 2 * m + f), uint32_t(j) & 1u, abort_flag, err, 10)) { ok = false; break; }
       ptx::tc_fence_after();
-      const int seen = visible - (begin + j * kTile);  // columns [0, seen) are visible
-      const uint32_t missing = bad[ss];
-      const bool masked = __any_sync(0xffffffffu, seen < kTile) || missing != 0;
-      const float4* sc = scl + ss * 8;
-
-      uint32_t pk[kTile / 2];
-      float top, sum;
-      // weights 2^(t - ref) of the row, their sum, the largest t - ref
-      auto weigh = [&](float ref) {
-        top = -INFINITY;
-        sum = 0.f;
+      const uint32_t s_col = lane_base + uint32_t(128 * m + kStep * f);
+      uint32_t s[2][32];
+      ptx::tmem_ld32(s_col, s[0]);
+      ptx::tmem_ld32(s_col + 32, s[1]);
+      const float4* sc = scl + ss * 8 + 4 * f;
+      const int seen = visible - (begin + i * kStep);  // columns [0, seen) are visible
+      bool gone = false;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) gone |= __float_as_int(sc[q].w) < 0 && begin + i * kStep + 16 * q < end;
+      ptx::tmem_wait_ld();
+      if (__any_sync(0xffffffffu, seen < kStep) || gone) {
+        // hidden: the lowest score, whatever lay there
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          uint32_t s[32];
-          ptx::tmem_ld32(s_col + q * 32, s);
-          ptx::tmem_wait_ld();
+          const int n = __float_as_int(sc[q].w) < 0 ? 0 : seen - 16 * q;
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const float4 k = sc[2 * q + half];
-            const float f = qscale * k.x, x = k.y - ref;
-            float part = 0.f;
-#pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              float t0 = fmaf(__uint_as_float(s[16 * half + i]), f, x);
-              float t1 = fmaf(__uint_as_float(s[16 * half + i + 1]), f, x);
-              if (masked) {
-                const int col = 32 * q + 16 * half + i;
-                const bool gone = (missing >> (2 * q + half)) & 1u;
-                if (gone || col >= seen) t0 = -INFINITY;
-                if (gone || col + 1 >= seen) t1 = -INFINITY;
-              }
-              top = ptx::fmax3(top, t0, t1);
-              t0 = ptx::ex2(t0);
-              t1 = ptx::ex2(t1);
-              part += t0 + t1;
-              pk[16 * q + 8 * half + i / 2] = pack_half2(t0, t1);
-            }
-            sum = fmaf(part, k.z, sum);
-          }
+          for (int e = 0; e < 16; ++e)
+            if (e >= n) s[q >> 1][(q & 1) * 16 + e] = 0xFF800000u;  // -inf
         }
-      };
-      weigh(mx == -INFINITY ? 0.f : mx);
-      // the reference moves on the first visible token and when a weight
-      // would pass 2^8
-      const bool raise = mx == -INFINITY ? top > -INFINITY : top > 8.f;
+      }
+      // a block's largest score: its factor is not negative, so the largest product
+      float top = -INFINITY;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t* v = s[q >> 1] + (q & 1) * 16;
+        float t = ptx::fmax3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
+#pragma unroll
+        for (int e = 3; e < 15; e += 2) t = ptx::fmax3(t, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+        t = fmaxf(t, __uint_as_float(v[15]));
+        if (t > -INFINITY) top = fmaxf(top, fmaf(t, qscale * sc[q].x, sc[q].y));
+      }
+      // the reference moves on the first visible token and when a weight would
+      // pass 2^8
+      const bool raise = top > mx + 8.f;
       if (__any_sync(0xffffffffu, raise)) {
-        const float was = mx;
-        if (raise) mx = (was == -INFINITY ? 0.f : was) + top;
-        const float alpha = raise ? (was == -INFINITY ? 0.f : ptx::ex2(was - mx)) : 1.f;
-        l *= alpha;
-        if (j > 0) {  // S(j) was issued after P V(j - 1) had ended
+        const float alpha = raise ? (mx == -INFINITY ? 0.f : ptx::ex2(mx - top)) : 1.f;
+        if (raise) mx = top;
+        l2.x *= alpha;
+        l2.y *= alpha;
+        if (i > 0) {  // O holds the earlier steps' products once the last of them has ended
+          const int was = i - 1;
+          if (!warp_wait(bar(C::B_PDONE + 2 * m + (was & 1)), uint32_t(was >> 1) & 1u, abort_flag, err, 13)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
 #pragma unroll 1
           for (int q = 0; q < D / 16; ++q) {
             uint32_t v[16];
             ptx::tmem_ld16(o_col + q * 16, v);
             ptx::tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
+            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
             ptx::tmem_st16(o_col + q * 16, v);
           }
         }
-        weigh(mx == -INFINITY ? 0.f : mx);
       }
-      l += sum;
+      const float ref = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        ptx::tmem_st16(s_col + q * 16, *reinterpret_cast<const uint32_t(*)[16]>(pk + 16 * q));
+      for (int q = 0; q < 4; ++q) {
+        const float4 k = sc[q];
+        // -inf * 0 (a page left out) would be NaN
+        const float kf = __float_as_int(k.w) < 0 ? 1.f : qscale * k.x, kx = k.y - ref;
+        const float2 f2 = make_float2(kf, kf), x2 = make_float2(kx, kx);
+        float2 part = make_float2(0.f, 0.f);
+        uint32_t* v = s[q >> 1] + (q & 1) * 16;
+        uint32_t pk[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float2 w = ptx::ffma2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), f2, x2);
+          w.x = ptx::ex2(w.x);
+          w.y = ptx::ex2(w.y);
+          part = ptx::fadd2(part, w);
+          pk[e] = pack_half2(w.x, w.y);
+        }
+        l2 = ptx::ffma2(part, make_float2(k.z, k.z), l2);
+        ptx::tmem_st8(s_col + 8 * q, pk);  // over S columns read already
+      }
       ptx::tmem_wait_st();
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        ptx::mbar_arrive(bar(C::B_PFULL + m));
-        ptx::mbar_arrive(bar(C::B_SCLFREE + ss));
+        ptx::mbar_arrive(bar(C::B_PFULL + 2 * m + f));
+        if (f == 1 || i == steps - 1) ptx::mbar_arrive(bar(C::B_SCLFREE + ss));
       }
     }
-    if (ok && tiles > 0) ok = warp_wait(bar(C::B_PDONE + m), uint32_t(tiles - 1) & 1u, abort_flag, err, 11);
+    const float l = l2.x + l2.y;
+    if (ok && steps > 0)
+      ok = warp_wait(bar(C::B_PDONE + 2 * m + ((steps - 1) & 1)), uint32_t((steps - 1) >> 1) & 1u, abort_flag, err, 11);
     ptx::tc_fence_after();
     if (ok) {
       const bool single = p.splits == 1;
@@ -433,7 +470,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
       for (int q = 0; q < D / 16; ++q) {
         uint32_t v[16];
-        if (tiles > 0) {
+        if (steps > 0) {
           ptx::tmem_ld16(o_col + q * 16, v);
           ptx::tmem_wait_ld();
         } else {
@@ -463,13 +500,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           p.part_m[at] = make_float2(mx, l);
       }
     }
-  } else {
-    ptx::regs_inc<kRegsSoftmax>();  // no second M tile
   }
 
   ptx::tc_fence_before();
   __syncthreads();
-  if (warp == kWarpAlloc) {
+  if (warp == kWarpPV + 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, 512);
   }

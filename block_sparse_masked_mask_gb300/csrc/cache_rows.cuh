@@ -6,9 +6,10 @@
 //
 // Operands.  m16n8k16: lane = 4 g + t holds, of a 16-wide step of the
 // contracted dimension, the places 2t, 2t + 1, 2t + 8, 2t + 9.  The order of
-// that dimension is free as long as both operands agree, so lane t takes the
-// D / 4 consecutive dimensions from t D / 4, four per step: a token's codes are
-// then read from global memory as they lie, 32 bytes per lane for D = 128.
+// that dimension is free as long as both operands agree, so lane t takes two
+// pieces of D / 8 consecutive dimensions, at t D / 8 of each half of the head,
+// four dimensions per step: a token's codes are then read as they lie, and the
+// four lanes of a token read whole sectors.
 #pragma once
 
 #include "cache.cuh"
@@ -29,8 +30,8 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
-// One row's D / 4 dimensions of lane t as fp16 pairs, times a power of two that
-// puts the row's largest magnitude into [1, 2): w[2 s], w[2 s + 1] belong to
+// One row's dimensions of lane t (two pieces) as fp16 pairs, times a power of two
+// that puts the row's largest magnitude into [1, 2): w[2 s], w[2 s + 1] belong to
 // step s.  Returns that power's inverse.  A row past the last is zero.
 template <int D>
 __device__ __forceinline__ float load_query(const CacheQueryArgs& a, const SeqRows& r, int h, int G, int row, int t,
@@ -39,17 +40,18 @@ __device__ __forceinline__ float load_query(const CacheQueryArgs& a, const SeqRo
   float amax = 0.f;
   if (row < r.n * G) {
     const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(a.q) +
-                             (int64_t(r.q0 + row / G) * a.num_heads + h * G + row % G) * D + t * (D / 4);
+                             (int64_t(r.q0 + row / G) * a.num_heads + h * G + row % G) * D + t * (D / 8);
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const uint4 v = reinterpret_cast<const uint4*>(p)[i];
-      const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+    for (int x = 0; x < 2; ++x)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        f[8 * i + 2 * j] = __uint_as_float(x[j] << 16);
-        f[8 * i + 2 * j + 1] = __uint_as_float(x[j] & 0xFFFF0000u);
+      for (int i = 0; i < D / 32; ++i) {
+        const uint2 v = reinterpret_cast<const uint2*>(p + x * (D / 2))[i];
+        float* at = f + x * (D / 8) + 4 * i;
+        at[0] = __uint_as_float(v.x << 16);
+        at[1] = __uint_as_float(v.x & 0xFFFF0000u);
+        at[2] = __uint_as_float(v.y << 16);
+        at[3] = __uint_as_float(v.y & 0xFFFF0000u);
       }
-    }
 #pragma unroll
     for (int i = 0; i < D / 4; ++i) amax = fmaxf(amax, fabsf(f[i]));
   } else {

@@ -26,7 +26,7 @@ struct WeightParams {
 
 template <int D>
 __global__ void __launch_bounds__(kWeightThreads, 4) cache_weights_kernel(const WeightParams p) {
-  constexpr int LB = D / 4, WORDS = LB / 4;
+  constexpr int WORDS = D / 16;  // of a token, per lane
   const CacheQueryArgs& a = p.a;
   const CacheView& c = a.cache;
   __shared__ uint4 frag[kWarps][D / 16][32];
@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(kWeightThreads, 4) cache_weights_kernel(const 
   if (cta_tok >= r.len) return;
   const int tok0 = cta_tok + warp * kTokens;
 
-  // keys of tokens tok0 + 8 nt + g, dimensions t D/4 ..
+  // keys of tokens tok0 + 8 nt + g, the lane's two pieces
   uint32_t w[4][WORDS];
   float ks[2] = {0.f, 0.f};
   bool fine[2] = {false, false};
@@ -55,16 +55,20 @@ __global__ void __launch_bounds__(kWeightThreads, 4) cache_weights_kernel(const 
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       const int nt = 2 * half + n;
-      const uint8_t* at = base + (8 * n + g) * D + t * LB;
+      const uint8_t* at = base + (8 * n + g) * D + t * (D / 8);
       const bool on = page >= 0 && tok + 8 * n + g < r.len;
 #pragma unroll
-      for (int i = 0; i < WORDS; i += (WORDS < 4 ? WORDS : 4)) {
-        if constexpr (WORDS >= 4) {
-          const uint4 v = on ? *reinterpret_cast<const uint4*>(at + 4 * i) : make_uint4(0, 0, 0, 0);
-          w[nt][i] = v.x; w[nt][i + 1] = v.y; w[nt][i + 2] = v.z; w[nt][i + 3] = v.w;
+      for (int x = 0; x < 2; ++x) {
+        uint32_t* to = w[nt] + x * (WORDS / 2);
+        const uint8_t* from = at + x * (D / 2);
+        if constexpr (D == 128) {
+          const uint4 v = on ? *reinterpret_cast<const uint4*>(from) : make_uint4(0, 0, 0, 0);
+          to[0] = v.x; to[1] = v.y; to[2] = v.z; to[3] = v.w;
+        } else if constexpr (D == 64) {
+          const uint2 v = on ? *reinterpret_cast<const uint2*>(from) : make_uint2(0, 0);
+          to[0] = v.x; to[1] = v.y;
         } else {
-          const uint2 v = on ? *reinterpret_cast<const uint2*>(at + 4 * i) : make_uint2(0, 0);
-          w[nt][i] = v.x; w[nt][i + 1] = v.y;
+          to[0] = on ? *reinterpret_cast<const uint32_t*>(from) : 0u;
         }
       }
     }

@@ -3,10 +3,11 @@
 // the gradient is the same with -a.
 //
 // One pass: every element is read and written once, so the memory bounds it.
-// The angle's sine and cosine are computed once per token and pair and shared
-// by all heads through shared memory.  A CTA takes one or a few whole tokens
-// (all heads of q and k): its loads are issued before the angles are
-// computed, so the two latencies overlap.
+// A warp takes one token and a share of its heads.  Its lanes compute the
+// token's sines and cosines once, two or so each, and exchange them through
+// shared memory; a lane then keeps those of its own pairs in registers, for it
+// meets the same pairs in every head.  No CTA-wide barrier: the loads of the
+// first heads are in flight while the angles are computed.
 //
 // The angle in turns is position * theta / (2 pi) modulo 1.  The plan holds
 // theta / (2 pi) as a 64-bit fixed-point fraction, and an integer product
@@ -17,15 +18,15 @@
 namespace attnmask {
 namespace {
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeUnroll = 4;      // units in flight per thread
-constexpr int kRopeMaxTokens = 16;  // tokens per CTA
+constexpr int kRopeWarps = 8;
+constexpr int kRopeUnroll = 4;  // units in flight per lane
 
 struct RopeParams {
   RopeArgs a;
-  int rot;            // rotated dimensions
-  int unit_log2;      // log2 of the units per head
-  int tokens_per_cta;
+  int rot;         // rotated dimensions
+  int unit_log2;   // log2 of the units per head
+  int slices;      // warps per token
+  int passes;      // passes of a warp over its heads (32 units each)
   float factor;
   uint64_t turn[ATTN_ROPE_MAX_PAIRS];
 };
@@ -41,28 +42,50 @@ __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float
 __device__ __forceinline__ void from_f(float& d, float x) { d = x; }
 __device__ __forceinline__ void from_f(__nv_bfloat16& d, float x) { d = __float2bfloat16_rn(x); }
 
-// A unit is VP pairs: for the half layout VP elements of each half, for the
-// interleaved one 2 VP consecutive elements.  Units behind rot are copied.
-template <typename T, int VP, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
-  __shared__ float2 cs[kRopeMaxTokens][ATTN_ROPE_MAX_PAIRS];
-  __shared__ int ok[kRopeMaxTokens];
-  const RopeArgs& a = p.a;
-  const int t0 = blockIdx.x * p.tokens_per_cta;
-  const int nt = min(p.tokens_per_cta, a.total_tokens - t0);
-  const int heads = a.num_heads + a.num_kv_heads;
-  const int per_token = heads << p.unit_log2;
-  const int total = nt * per_token;
-  const int turned = p.rot / (2 * VP);  // units of a head that are rotated
+// The position of row t and whether it has one.
+__device__ __forceinline__ bool position_of(const RopeArgs& a, int t, int& pos) {
+  if (a.positions) {
+    pos = a.positions[t];
+    return true;
+  }
+  // the last sequence that starts at or before the row
+  int b0 = 0, b1 = a.batch;
+  while (b0 + 1 < b1) {
+    const int m = (b0 + b1) >> 1;
+    if (a.cu[m] <= t) b0 = m; else b1 = m;
+  }
+  const int s0 = a.cu[b0], s1 = a.cu[b0 + 1];
+  pos = t - s0 + (a.lens ? a.lens[b0] - (s1 - s0) : 0);
+  return t >= s0 && t < s1;
+}
 
-  Vec<T, VP> lo[kRopeUnroll], hi[kRopeUnroll];
-  auto locate = [&](int i, int& t, int& h, int& u) {
-    t = nt == 1 ? 0 : i / per_token;
-    const int r = i - t * per_token;
-    h = r >> p.unit_log2;
-    u = r & ((1 << p.unit_log2) - 1);
-  };
-  auto offsets = [&](int u, int& d0, int& d1) {
+// A unit is VP pairs: for the half layout VP elements of each half, for the
+// interleaved one 2 VP consecutive elements.  Units behind rot are copied.  A
+// pass of a warp covers 32 units: whole heads, or half a head where a head has 64.
+template <typename T, int VP, bool INTER>
+__global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const __grid_constant__ RopeParams p) {
+  __shared__ float2 cs[kRopeWarps][ATTN_ROPE_MAX_PAIRS];
+  const RopeArgs& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t job = int64_t(blockIdx.x) * kRopeWarps + warp;
+  const int t = int(job / p.slices), slice = int(job % p.slices);
+  if (t >= a.total_tokens) return;
+  const int heads = a.num_heads + a.num_kv_heads;
+  const int turned = p.rot / (2 * VP);  // units of a head that are rotated
+  const int units = 1 << p.unit_log2;
+  const T* q = static_cast<const T*>(a.q) + int64_t(t) * a.q_stride;
+  const T* k = static_cast<const T*>(a.k) + int64_t(t) * a.k_stride;
+  T* qo = static_cast<T*>(a.q_out) + int64_t(t) * a.q_out_stride;
+  T* ko = static_cast<T*>(a.k_out) + int64_t(t) * a.k_out_stride;
+
+  // 64 units per head (VP = 1, 128 dimensions): the lane's unit alternates; else
+  // it is the same in every pass
+  const int blocks = units > 32 ? units / 32 : 1;
+  const int per_pass = units > 32 ? 1 : 32 >> p.unit_log2;  // heads
+  const int first = slice * p.passes * per_pass, last = min(heads, first + p.passes * per_pass);
+  for (int block = 0; block < blocks; ++block) {
+    const int u = block * 32 + (lane & (units - 1));
+    int d0, d1;
     if (u >= turned) {
       d0 = p.rot + (u - turned) * 2 * VP;
       d1 = d0 + VP;
@@ -73,87 +96,65 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
       d0 = u * VP;
       d1 = p.rot / 2 + d0;
     }
-  };
-  for (int base = 0; base < total; base += kRopeThreads * kRopeUnroll) {
+    const int h0 = first + (units > 32 ? 0 : lane >> p.unit_log2);
+    Vec<T, VP> x[kRopeUnroll], y[kRopeUnroll];
+    auto load = [&](int h) {
 #pragma unroll
-    for (int j = 0; j < kRopeUnroll; ++j) {
-      const int i = base + j * kRopeThreads + threadIdx.x;
-      if (i >= total) continue;
-      int t, h, u, d0, d1;
-      locate(i, t, h, u);
-      offsets(u, d0, d1);
-      const T* src = h < a.num_heads
-                         ? static_cast<const T*>(a.q) + int64_t(t0 + t) * a.q_stride + h * a.head_dim
-                         : static_cast<const T*>(a.k) + int64_t(t0 + t) * a.k_stride + (h - a.num_heads) * a.head_dim;
-      lo[j] = *reinterpret_cast<const Vec<T, VP>*>(src + d0);
-      hi[j] = *reinterpret_cast<const Vec<T, VP>*>(src + d1);
+      for (int j = 0; j < kRopeUnroll; ++j) {
+        const int i = h + j * per_pass;
+        if (i >= last) continue;
+        const T* src = i < a.num_heads ? q + i * a.head_dim : k + (i - a.num_heads) * a.head_dim;
+        x[j] = *reinterpret_cast<const Vec<T, VP>*>(src + d0);
+        y[j] = *reinterpret_cast<const Vec<T, VP>*>(src + d1);
+      }
+    };
+    load(h0);
+    if (block == 0) {
+      int pos;
+      if (!position_of(a, t, pos)) return;  // the whole warp
+      for (int c = lane; c < p.rot / 2; c += 32) {
+        const int64_t turn = int64_t(uint64_t(int64_t(pos)) * p.turn[c]);
+        float sn, cn;
+        sincospif(float(int32_t(turn >> 32)) * 0x1p-31f, &sn, &cn);
+        cs[warp][c] = make_float2(cn * p.factor, (a.inverse ? -sn : sn) * p.factor);
+      }
+      __syncwarp();
     }
-    if (base == 0) {
-      const int pairs = p.rot / 2;
-      for (int i = threadIdx.x; i < nt * ATTN_ROPE_MAX_PAIRS; i += kRopeThreads) {
-        const int t = i / ATTN_ROPE_MAX_PAIRS, c = i % ATTN_ROPE_MAX_PAIRS;
-        int pos = 0;
-        bool in = true;
-        if (a.positions) {
-          pos = a.positions[t0 + t];
-        } else {
-          // the last sequence that starts at or before the row
-          int b0 = 0, b1 = a.batch;
-          while (b0 + 1 < b1) {
-            const int m = (b0 + b1) >> 1;
-            if (a.cu[m] <= t0 + t) b0 = m; else b1 = m;
+    float2 c[VP];
+#pragma unroll
+    for (int e = 0; e < VP; ++e) c[e] = u < turned ? cs[warp][u * VP + e] : make_float2(1.f, 0.f);
+    for (int h = h0; h < last; h += kRopeUnroll * per_pass) {
+      if (h != h0) load(h);
+#pragma unroll
+      for (int j = 0; j < kRopeUnroll; ++j) {
+        const int i = h + j * per_pass;
+        if (i >= last) continue;
+        if (u < turned) {
+#pragma unroll
+          for (int e = 0; e < VP; ++e) {
+            // the half layout pairs x with y; the interleaved one neighbours
+            T* px = INTER ? (2 * e < VP ? &x[j].x[2 * e] : &y[j].x[2 * e - VP]) : &x[j].x[e];
+            T* py = INTER ? (2 * e + 1 < VP ? &x[j].x[2 * e + 1] : &y[j].x[2 * e + 1 - VP]) : &y[j].x[e];
+            const float fx = to_f(*px), fy = to_f(*py);
+            from_f(*px, fx * c[e].x - fy * c[e].y);
+            from_f(*py, fy * c[e].x + fx * c[e].y);
           }
-          const int s0 = a.cu[b0], s1 = a.cu[b0 + 1];
-          in = t0 + t >= s0 && t0 + t < s1;
-          pos = t0 + t - s0 + (a.lens ? a.lens[b0] - (s1 - s0) : 0);
         }
-        if (c == 0) ok[t] = in;
-        if (c < pairs) {
-          const int64_t turn = int64_t(uint64_t(int64_t(pos)) * p.turn[c]);
-          float sn, cn;
-          sincospif(float(int32_t(turn >> 32)) * 0x1p-31f, &sn, &cn);
-          cs[t][c] = make_float2(cn * p.factor, (a.inverse ? -sn : sn) * p.factor);
-        }
+        T* dst = i < a.num_heads ? qo + i * a.head_dim : ko + (i - a.num_heads) * a.head_dim;
+        *reinterpret_cast<Vec<T, VP>*>(dst + d0) = x[j];
+        *reinterpret_cast<Vec<T, VP>*>(dst + d1) = y[j];
       }
-      __syncthreads();
-    }
-#pragma unroll
-    for (int j = 0; j < kRopeUnroll; ++j) {
-      const int i = base + j * kRopeThreads + threadIdx.x;
-      if (i >= total) continue;
-      int t, h, u, d0, d1;
-      locate(i, t, h, u);
-      offsets(u, d0, d1);
-      if (!ok[t]) continue;
-      Vec<T, VP> x = lo[j], y = hi[j];
-      if (u < turned) {
-#pragma unroll
-        for (int e = 0; e < VP; ++e) {
-          // the half layout pairs lo with hi; the interleaved one neighbours
-          T* px = INTER ? (2 * e < VP ? &x.x[2 * e] : &y.x[2 * e - VP]) : &x.x[e];
-          T* py = INTER ? (2 * e + 1 < VP ? &x.x[2 * e + 1] : &y.x[2 * e + 1 - VP]) : &y.x[e];
-          const float2 c = cs[t][u * VP + e];
-          const float fx = to_f(*px), fy = to_f(*py);
-          from_f(*px, fx * c.x - fy * c.y);
-          from_f(*py, fy * c.x + fx * c.y);
-        }
-      }
-      T* dst = h < a.num_heads
-                   ? static_cast<T*>(a.q_out) + int64_t(t0 + t) * a.q_out_stride + h * a.head_dim
-                   : static_cast<T*>(a.k_out) + int64_t(t0 + t) * a.k_out_stride + (h - a.num_heads) * a.head_dim;
-      *reinterpret_cast<Vec<T, VP>*>(dst + d0) = x;
-      *reinterpret_cast<Vec<T, VP>*>(dst + d1) = y;
     }
   }
 }
 
 template <typename T, int VP>
 cudaError_t launch_vp(const RopeParams& p, bool interleaved, cudaStream_t s) {
-  const unsigned grid = unsigned((p.a.total_tokens + p.tokens_per_cta - 1) / p.tokens_per_cta);
+  const unsigned grid = unsigned((int64_t(p.a.total_tokens) * p.slices + kRopeWarps - 1) / kRopeWarps);
   if (interleaved)
-    rope_kernel<T, VP, true><<<grid, kRopeThreads, 0, s>>>(p);
+    rope_kernel<T, VP, true><<<grid, 32 * kRopeWarps, 0, s>>>(p);
   else
-    rope_kernel<T, VP, false><<<grid, kRopeThreads, 0, s>>>(p);
+    rope_kernel<T, VP, false><<<grid, 32 * kRopeWarps, 0, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -173,17 +174,17 @@ cudaError_t launch_t(RopeParams& p, bool interleaved, cudaStream_t s) {
   while (vp > 1 && (bits & (vp * sizeof(T) - 1))) vp >>= 1;
   p.unit_log2 = 0;
   while ((2 * vp << p.unit_log2) < a.head_dim) ++p.unit_log2;
-  // Tokens per CTA: up to one unrolled pass of units, but enough CTAs for
-  // four per SM while the tokens last.
-  const int per_token = (a.num_heads + a.num_kv_heads) << p.unit_log2;
+  // Warps per token: one, or more while there are fewer warps than the GPU
+  // holds (32 per SM), down to one pass each.
+  const int units = 1 << p.unit_log2, heads = a.num_heads + a.num_kv_heads;
+  const int all = units > 32 ? heads : int((int64_t(heads) * units + 31) / 32);  // passes over a token
   int sms = 0, dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  int tpc = kRopeThreads * kRopeUnroll / per_token;
-  const int spread = a.total_tokens / (4 * sms);
-  tpc = tpc < spread ? tpc : spread;
-  p.tokens_per_cta = tpc < 1 ? 1 : (tpc > kRopeMaxTokens ? kRopeMaxTokens : tpc);
+  const int want = (32 * sms + a.total_tokens - 1) / a.total_tokens;
+  p.passes = (all + want - 1) / want;
+  p.slices = (all + p.passes - 1) / p.passes;
   switch (vp) {
     case 8: if constexpr (kMost >= 8) return launch_vp<T, 8>(p, interleaved, s);
     case 4: return launch_vp<T, 4>(p, interleaved, s);
