@@ -19,8 +19,8 @@
 //   0-3, 4-7   softmax of M tile 0 and 1, one thread per row
 //   8-11       values: codes to fp16 tiles (two slots)
 //   12         pages, scales (four slots) and TMA of the keys (three slots)
-//   13         tcgen05 issuer of S for both M tiles
-//   14, 15     tcgen05 issuers of P V, one per M tile (15 also owns TMEM)
+//   13, 14     tcgen05 issuers of S, one per M tile
+//   15         tcgen05 issuer of P V for both M tiles (also owns TMEM)
 // Keys and values come in tiles of 128 tokens; the products and the softmax go
 // in steps of 64, with two S buffers per M tile: S of the next step is there
 // when a softmax ends its step, so the softmax and the tensor cores both run
@@ -40,7 +40,7 @@ namespace attnmask {
 namespace {
 
 constexpr int kChunkThreads = 512;
-constexpr int kWarpValues = 8, kWarpKeys = 12, kWarpS = 13, kWarpPV = 14;
+constexpr int kWarpValues = 8, kWarpKeys = 12, kWarpS = 13, kWarpPV = 15;
 constexpr int kStep = 64;  // tokens per step
 
 template <int D>
@@ -113,11 +113,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NK; ++i) {
       ptx::mbar_init(bar(C::B_KFULL + i), 1);
-      ptx::mbar_init(bar(C::B_KEMPTY + i), 1);
+      ptx::mbar_init(bar(C::B_KEMPTY + i), nm);
     }
     for (int i = 0; i < C::NV; ++i) {
       ptx::mbar_init(bar(C::B_VFULL + i), 4);
-      ptx::mbar_init(bar(C::B_VEMPTY + i), nm);
+      ptx::mbar_init(bar(C::B_VEMPTY + i), 1);
     }
     for (int i = 0; i < C::NSCL; ++i) {
       ptx::mbar_init(bar(C::B_SCLFULL + i), 1);
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     *abort_flag = (*reinterpret_cast<volatile int32_t*>(err) & kErrTimeout) ? 1u : 0u;
     ptx::fence_mbar_init();
   }
-  if (warp == kWarpPV + 1) {
+  if (warp == kWarpPV) {
     ptx::tmem_alloc(ptx::smem_addr(misc), 512);
     ptx::tmem_relinquish();
   }
@@ -203,59 +203,56 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == kWarpS) {
-    // -------------------------------------------------------------- S issuer
+  } else if (warp == kWarpPV) {
+    // -------------------------------------------------------------- P V issuer
     if (lane == 0) {
-      constexpr uint32_t IDESC = ptx::idesc_e4m3_f32(128, kStep);
-      const uint64_t qd = ptx::smem_desc(base + C::OFF_Q, 16u, 8 * D, C::SW8);
-      const uint64_t kd = ptx::smem_desc(base + C::OFF_K, 16u, 8 * D, C::SW8);
+      constexpr uint32_t IDESC = ptx::idesc_f16_f32(128, D, false, true);
+      const uint64_t vd = v_base<D>(base + C::OFF_V);
       bool ok = true;
-      for (int m = 0; m < nm && ok && steps > 0; ++m) ok = wait_bar(bar(C::B_Q + m), 0, abort_flag, err, 3);
       for (int i = 0; ok && i < steps; ++i) {
-        const int j = i >> 1, ks = j % C::NK, f = i & 1;
-        if (f == 0 && !wait_bar(bar(C::B_KFULL + ks), uint32_t(j / C::NK) & 1u, abort_flag, err, 4)) break;
-        const uint64_t ki = kd + uint64_t((ks * C::KT + f * kStep * D) >> 4);
+        const int j = i >> 1, vs = j % C::NV, f = i & 1;
+        if (f == 0 && !wait_bar(bar(C::B_VFULL + vs), uint32_t(j / C::NV) & 1u, abort_flag, err, 6)) break;
+        const uint64_t vi = vd + uint64_t(vs) * (C::VT >> 4) + v_step<D>(f * (kStep / 16));
         for (int m = 0; m < nm; ++m) {
-          // P(i - 2) lies over this S: its product has read it
-          if (i >= 2 && !wait_bar(bar(C::B_PDONE + 2 * m + f), uint32_t(i / 2 - 1) & 1u, abort_flag, err, 5)) {
-            ok = false;
-            break;
-          }
+          ok = wait_bar(bar(C::B_PFULL + 2 * m + f), uint32_t(j) & 1u, abort_flag, err, 7);
+          if (!ok) break;
           ptx::tc_fence_after();
-          const uint32_t s_tmem = tmem + uint32_t(128 * m + kStep * f);
-          const uint64_t qhi = qd + uint64_t((2 * m * C::KT) >> 4), qlo = qd + uint64_t(((2 * m + 1) * C::KT) >> 4);
+          const uint32_t p_tmem = tmem + uint32_t(128 * m + kStep * f), o_tmem = tmem + uint32_t(256 + 128 * m);
 #pragma unroll
-          for (int kk = 0; kk < D / 32; ++kk) ptx::mma_f8_ss(s_tmem, qhi + 2 * kk, ki + 2 * kk, IDESC, kk > 0);
-#pragma unroll
-          for (int kk = 0; kk < D / 32; ++kk) ptx::mma_f8_ss(s_tmem, qlo + 2 * kk, ki + 2 * kk, IDESC, 1);
-          ptx::mma_commit(bar(C::B_SFULL + 2 * m + f));
+          for (int kk = 0; kk < kStep / 16; ++kk)
+            ptx::mma_ts(o_tmem, p_tmem + uint32_t(kk) * 8u, vi + v_step<D>(kk), IDESC, (i > 0 || kk > 0) ? 1u : 0u);
+          ptx::mma_commit(bar(C::B_PDONE + 2 * m + f));
         }
-        if (ok && (f == 1 || i == steps - 1)) ptx::mma_commit(bar(C::B_KEMPTY + ks));
+        if (ok && (f == 1 || i == steps - 1)) ptx::mma_commit(bar(C::B_VEMPTY + vs));
       }
       // every product this thread issued has finished once this arrives
       ptx::mma_commit(bar(C::B_DRAIN + 2));
       drain_bar(bar(C::B_DRAIN + 2), 0, err);
     }
     __syncwarp();
-  } else if (warp >= kWarpPV) {
-    // -------------------------------------------------------------- P V issuers
-    const int m = warp - kWarpPV;
+  } else if (warp >= kWarpS) {
+    // -------------------------------------------------------------- S issuers
+    const int m = warp - kWarpS;
     if (lane == 0 && m < nm) {
-      constexpr uint32_t IDESC = ptx::idesc_f16_f32(128, D, false, true);
-      const uint32_t o_tmem = tmem + 256u + 128u * uint32_t(m);
-      const uint64_t vd = v_base<D>(base + C::OFF_V);
-      for (int i = 0; i < steps; ++i) {
-        const int j = i >> 1, vs = j % C::NV, f = i & 1;
-        if (f == 0 && !wait_bar(bar(C::B_VFULL + vs), uint32_t(j / C::NV) & 1u, abort_flag, err, 6)) break;
-        if (!wait_bar(bar(C::B_PFULL + 2 * m + f), uint32_t(j) & 1u, abort_flag, err, 7)) break;
+      constexpr uint32_t IDESC = ptx::idesc_e4m3_f32(128, kStep);
+      const uint64_t qhi = ptx::smem_desc(base + C::OFF_Q + 2 * m * C::KT, 16u, 8 * D, C::SW8);
+      const uint64_t qlo = ptx::smem_desc(base + C::OFF_Q + (2 * m + 1) * C::KT, 16u, 8 * D, C::SW8);
+      const uint64_t kd = ptx::smem_desc(base + C::OFF_K, 16u, 8 * D, C::SW8);
+      const bool ok = steps == 0 || wait_bar(bar(C::B_Q + m), 0, abort_flag, err, 3);
+      for (int i = 0; ok && i < steps; ++i) {
+        const int j = i >> 1, ks = j % C::NK, f = i & 1;
+        if (f == 0 && !wait_bar(bar(C::B_KFULL + ks), uint32_t(j / C::NK) & 1u, abort_flag, err, 4)) break;
+        // P(i - 2) lies over this S: its product has read it
+        if (i >= 2 && !wait_bar(bar(C::B_PDONE + 2 * m + f), uint32_t(i / 2 - 1) & 1u, abort_flag, err, 5)) break;
         ptx::tc_fence_after();
-        const uint32_t p_tmem = tmem + uint32_t(128 * m + kStep * f);
-        const uint64_t vi = vd + uint64_t(vs) * (C::VT >> 4) + v_step<D>(f * (kStep / 16));
+        const uint32_t s_tmem = tmem + uint32_t(128 * m + kStep * f);
+        const uint64_t ki = kd + uint64_t((ks * C::KT + f * kStep * D) >> 4);
 #pragma unroll
-        for (int kk = 0; kk < kStep / 16; ++kk)
-          ptx::mma_ts(o_tmem, p_tmem + uint32_t(kk) * 8u, vi + v_step<D>(kk), IDESC, (i > 0 || kk > 0) ? 1u : 0u);
-        ptx::mma_commit(bar(C::B_PDONE + 2 * m + f));
-        if (f == 1 || i == steps - 1) ptx::mma_commit(bar(C::B_VEMPTY + vs));
+        for (int kk = 0; kk < D / 32; ++kk) ptx::mma_f8_ss(s_tmem, qhi + 2 * kk, ki + 2 * kk, IDESC, kk > 0);
+#pragma unroll
+        for (int kk = 0; kk < D / 32; ++kk) ptx::mma_f8_ss(s_tmem, qlo + 2 * kk, ki + 2 * kk, IDESC, 1);
+        ptx::mma_commit(bar(C::B_SFULL + 2 * m + f));
+        if (f == 1 || i == steps - 1) ptx::mma_commit(bar(C::B_KEMPTY + ks));
       }
       ptx::mma_commit(bar(C::B_DRAIN + m));
       drain_bar(bar(C::B_DRAIN + m), 0, err);
@@ -504,7 +501,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 
   ptx::tc_fence_before();
   __syncthreads();
-  if (warp == kWarpPV + 1) {
+  if (warp == kWarpPV) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, 512);
   }
