@@ -76,16 +76,22 @@ struct CacheQueryArgs {
   float* workspace;
 };
 
-// How attn_cache_fwd cuts its work: rows (new token, query head of the group) in
-// tiles, tokens in chunks, and where the chunks' results meet.
+// How attn_cache_fwd cuts its work, and where the pieces' results meet: rows (new
+// token, query head of the group) in tiles and tokens in chunks
+// (tcgen05 kernel), or share the line of all tokens evenly (mma.sync kernel).
 struct CacheAttnParams {
   CacheQueryArgs a;
   int G;           // query heads per key / value head
-  int tile_rows;   // kFewRows (mma.sync) or kManyRows (tcgen05)
-  int row_tiles, chunk, splits;
+  bool many;       // the tcgen05 kernel
+  int row_tiles, chunk, splits;  // many: tiles of kManyRows rows, tokens per chunk, chunks
+  int ctas;        // few: CTAs
   float scale_log2;
-  float* part_o;   // [splits][total_tokens * num_heads][head_dim]: O before the division
-  float2* part_m;  // [splits][total_tokens * num_heads]: running maximum, sum
+  // Results before the division, and (running maximum, sum).
+  //   many: [splits][total_tokens * num_heads] rows
+  //   few:  [2 * ctas][max_new * G] rows: of CTA c, 2 c a segment that goes on
+  //         one of the CTA before, 2 c + 1 one that goes on in the next
+  float* part_o;   // rows of head_dim
+  float2* part_m;
 };
 constexpr int kFewRows = 16, kManyRows = 256;
 
@@ -121,7 +127,8 @@ struct SeqRows {
 // index below is ever formed from them.  max_new and max_len bound what the
 // launch was sized for; max_len is at most max_pages * page_size.
 __device__ __forceinline__ bool load_rows(const int32_t* cu, const int32_t* lens, int b, int total_tokens,
-                                          int max_new, int max_len, int32_t* status, SeqRows& r) {
+                                          int max_new, int max_len, int32_t* status, SeqRows& r,
+                                          bool note = true) {
   const int q0 = cu[b], q1 = cu[b + 1];
   r.q0 = q0;
   r.len = lens[b];
@@ -133,7 +140,7 @@ __device__ __forceinline__ bool load_rows(const int32_t* cu, const int32_t* lens
   if (r.n > max_new) err |= kErrTooManyNew;
   if (r.len < 0) err |= kErrHeld;
   if (r.len > max_len) err |= kErrSeqTooLong;
-  if (err) atomicOr(status, err);
+  if (err && note) atomicOr(status, err);
   return err == 0;
 }
 

@@ -48,9 +48,10 @@ attn_status check_sizes(const attn_kv_cache* c, int32_t total_tokens, int32_t nu
   if (total_tokens < 0 || num_heads < 1 || max_new < 0 || max_seqlen < 0) return ATTN_ERR_INVALID_ARG;
   if (num_heads % c->num_kv_heads != 0) return ATTN_ERR_INVALID_ARG;
   if (int64_t(max_seqlen) > int64_t(c->max_pages) * c->page_size) return ATTN_ERR_INVALID_ARG;
-  // rows of one sequence and of the call, and a launch's blocks, fit 31 bits
+  // rows of one sequence and of the call, units of 64 tokens and a launch's blocks fit 31 bits
   if (int64_t(total_tokens) * num_heads > (int64_t(1) << 30) || int64_t(max_new) * num_heads > (int64_t(1) << 30))
     return ATTN_ERR_UNSUPPORTED;
+  if (int64_t(c->batch) * c->num_kv_heads * (int64_t(max_seqlen) / 64 + 1) > INT_MAX) return ATTN_ERR_UNSUPPORTED;
   const int64_t tiles = (int64_t(max_new) * (num_heads / c->num_kv_heads) + 15) / 16;
   if (tiles * ((int64_t(max_seqlen) + 255) / 256) > (int64_t(1) << 30)) return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;

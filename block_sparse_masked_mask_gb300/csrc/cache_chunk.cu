@@ -87,11 +87,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const CacheQueryArgs& a = p.a;
   const CacheView& c = a.cache;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int split = blockIdx.x / p.row_tiles, row0 = (blockIdx.x % p.row_tiles) * p.tile_rows;
+  const int split = blockIdx.x / p.row_tiles, row0 = (blockIdx.x % p.row_tiles) * kManyRows;
   const int h = blockIdx.y, b = blockIdx.z;
   SeqRows r;
   if (!load_rows(a.cu, a.lens, b, a.total_tokens, a.max_new, a.max_seqlen, c.status, r)) return;
-  const int rows = min(p.tile_rows, r.n * p.G - row0);
+  const int rows = min(kManyRows, r.n * p.G - row0);
   if (rows <= 0) return;
   const int limit = visible_tokens(r, p.G, row0 + rows - 1, a.causal);
   const int begin = split * p.chunk, end = min(begin + p.chunk, limit);

@@ -3,162 +3,260 @@
 // key / value head.
 //
 // The keys are read once (D bytes per token and head), which bounds it for a
-// decode step; the LSE is known, so no second pass and no running maximum.  A
-// warp owns 32 tokens: it holds their keys in registers as the B operand of
-// mma.sync m16n8k16 and walks the query rows 16 at a time, which the CTA's
-// four warps stage in shared memory in operand order.  Every token's sum is
-// formed by one warp in a fixed order: no atomics, repeats are bit-identical.
+// decode step; the LSE is known, so no second pass and no running maximum.  The
+// tokens are divided evenly among the CTAs and queued as in cache_attn.cu; a warp
+// takes 32 of them at a time, holds their keys as fp16 A operands of mma.sync
+// m16n8k16 and walks the query rows 8 at a time, which the CTA has staged in
+// shared memory in operand order, up to 64 rows at once; more rows read the
+// keys again (from L2) for each 64 and add to what the last ones left.
+// Every token's sum is formed by one warp in a fixed order: no atomics, repeats
+// are bit-identical.
 #include "cache_rows.cuh"
 #include "ptx.cuh"
 
 namespace attnmask {
 namespace {
 
-constexpr int kWarps = 4;
 constexpr int kWeightThreads = 32 * kWarps;
-constexpr int kTokens = 32;  // per warp
+constexpr int kStages = 3;     // of the queue, blocks
+constexpr int kBlock = 32;     // tokens a warp takes at a time
+constexpr int kRowTiles = 8;   // of 8 rows, staged at once
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int D>
+struct WeightCfg {
+  static constexpr int PIECE = D / 8;
+  static constexpr int STAGE = 32 * 8 * PIECE;  // per warp: two pieces of four tokens per lane
+  static constexpr int QUEUE = kWarps * kStages * STAGE;
+  static constexpr int FRAG = D / 16 * 32 * 8;  // a row tile's B operands
+  static constexpr int OFF_FRAG = QUEUE;
+  static constexpr int OFF_ROWS = OFF_FRAG + kRowTiles * FRAG;  // per row: scale, LSE, visible
+  static constexpr int SMEM = OFF_ROWS + kRowTiles * 8 * 16;
+};
 
 struct WeightParams {
   CacheQueryArgs a;
-  int G;
+  int G, ctas;
   float scale_log2;
 };
 
+// Units of sequence b and all heads (its tokens, also where it has no query).
+struct WeightUnits {
+  const WeightParams& p;
+  bool note;
+  __device__ int operator()(int b) const {
+    const CacheQueryArgs& a = p.a;
+    SeqRows r;
+    if (!load_rows(a.cu, a.lens, b, a.total_tokens, a.max_new, a.max_seqlen, a.cache.status, r, note)) return 0;
+    return (r.len + kUnit - 1) / kUnit * a.cache.heads;
+  }
+};
+
 template <int D>
-__global__ void __launch_bounds__(kWeightThreads, 4) cache_weights_kernel(const WeightParams p) {
-  constexpr int WORDS = D / 16;  // of a token, per lane
+__global__ void __launch_bounds__(kWeightThreads, 3) cache_weights_kernel(const WeightParams p) {
+  using C = WeightCfg<D>;
+  extern __shared__ __align__(16) uint8_t smem[];
   const CacheQueryArgs& a = p.a;
   const CacheView& c = a.cache;
-  __shared__ uint4 frag[kWarps][D / 16][32];
-  __shared__ float row_scale[kWarps][16], row_lse[kWarps][16];
-  const int h = blockIdx.y, b = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  SeqRows r;
-  if (!load_rows(a.cu, a.lens, b, a.total_tokens, a.max_new, a.max_seqlen, c.status, r)) return;
-  const int cta_tok = blockIdx.x * kWarps * kTokens;
-  if (cta_tok >= r.len) return;
-  const int tok0 = cta_tok + warp * kTokens;
+  const WeightUnits units{p, blockIdx.x == 0};
+  const int total = total_units(units, c.batch, lane);
+  const int piece = (total + p.ctas - 1) / p.ctas;
+  int pos = blockIdx.x * piece;
+  const int stop = min(pos + piece, total);
+  if (pos >= stop) return;
+  int before;
+  int b = find_unit(units, c.batch, lane, pos, before);
 
-  // keys of tokens tok0 + 8 nt + g, the lane's two pieces
-  uint32_t w[4][WORDS];
-  float ks[2] = {0.f, 0.f};
-  bool fine[2] = {false, false};
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int tok = tok0 + 16 * half;
-    int page = -1;
-    if (tok < r.len) page = load_page(c, b, tok >> c.page_log2);
-    fine[half] = page >= 0;
-    if (page >= 0) ks[half] = c.k_scale[int64_t(page) * c.heads + h];
-    const uint8_t* base = c.k_pages + (((int64_t(page >= 0 ? page : 0) * c.heads + h) << c.page_log2) +
-                                       (tok & ((1 << c.page_log2) - 1))) * D;
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const int nt = 2 * half + n;
-      const uint8_t* at = base + (8 * n + g) * D + t * (D / 8);
-      const bool on = page >= 0 && tok + 8 * n + g < r.len;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        uint32_t* to = w[nt] + x * (WORDS / 2);
-        const uint8_t* from = at + x * (D / 2);
-        if constexpr (D == 128) {
-          const uint4 v = on ? *reinterpret_cast<const uint4*>(from) : make_uint4(0, 0, 0, 0);
-          to[0] = v.x; to[1] = v.y; to[2] = v.z; to[3] = v.w;
-        } else if constexpr (D == 64) {
-          const uint2 v = on ? *reinterpret_cast<const uint2*>(from) : make_uint2(0, 0);
-          to[0] = v.x; to[1] = v.y;
-        } else {
-          to[0] = on ? *reinterpret_cast<const uint32_t*>(from) : 0u;
-        }
-      }
+  const uint32_t queue = ptx::smem_addr(smem) + warp * kStages * C::STAGE + lane * C::PIECE;
+  const uint8_t* queue_ptr = smem + warp * kStages * C::STAGE + lane * C::PIECE;
+  uint2* frag = reinterpret_cast<uint2*>(smem + C::OFF_FRAG);    // [row tile][step][lane]
+  float4* row_of = reinterpret_cast<float4*>(smem + C::OFF_ROWS);  // scale, LSE (base 2), visible
+  const int64_t page_bytes = int64_t(D) << c.page_log2;
+
+  while (pos < stop) {
+    // ---- the segment: units u0 .. u1 - 1 of sequence b, head h
+    SeqRows r;
+    const bool good = load_rows(a.cu, a.lens, b, a.total_tokens, a.max_new, a.max_seqlen, c.status, r, false);
+    const int U = good ? (r.len + kUnit - 1) / kUnit : 0;
+    if (U == 0) {
+      ++b;
+      continue;
     }
-  }
+    const int h = (pos - before) / U, u0 = (pos - before) - h * U, u1 = min(U, u0 + stop - pos);
+    const int rows = r.n * p.G;
+    const int begin = u0 * kUnit, end = min(u1 * kUnit, r.len);
+    const int blocks = (end - begin + kBlock - 1) / kBlock;
+    const int mine = blocks > warp ? (blocks - warp + kWarps - 1) / kWarps : 0;
+    auto token_of = [&](int i) { return begin + (warp + i * kWarps) * kBlock; };
+    const float* prev = a.prev;
+    const int64_t out = (int64_t(b) * c.heads + h) * a.weight_stride;
 
-  float sum[4][2];
+    int row0 = 0;
+    do {  // 64 rows at a time, once where there is none
+      // lane 2 i + x: the x-th 16 tokens of the i-th block; 16 blocks at a time, a batch ahead
+      auto pages = [&](int first) {
+        const int i = first + lane / 2, tok = token_of(i) + (lane & 1) * kGroup;
+        return look_up(c, b, h, tok, i < mine && tok < end, false);
+      };
+      PageBatch now = pages(0), next = pages(16);
+      auto issue = [&](int i, bool ahead) {
+        const PageBatch& from = ahead ? next : now;
+        const int page0 = __shfl_sync(0xffffffffu, from.page, (2 * i) & 31);
+        const int page1 = __shfl_sync(0xffffffffu, from.page, (2 * i + 1) & 31);
+        if (i < mine) {
+          const uint32_t dst = queue + (i % kStages) * C::STAGE;
 #pragma unroll
-  for (int nt = 0; nt < 4; ++nt) sum[nt][0] = sum[nt][1] = 0.f;
-  const int rows = r.n * p.G;
-  for (int row0 = 0; row0 < rows; row0 += 16 * kWarps) {
-    {
-      uint32_t qa[D / 8], qb[D / 8];
-      const int ra = row0 + warp * 16 + g, rb = ra + 8;
-      const float sa = load_query<D>(a, r, h, p.G, ra, t, qa), sb = load_query<D>(a, r, h, p.G, rb, t, qb);
-      __syncthreads();  // the last batch has been read
+          for (int half = 0; half < 2; ++half) {
+            const int page = half ? page1 : page0, tok = token_of(i) + half * kGroup;
+            const int slot = tok & ((1 << c.page_log2) - 1);
+            const uint8_t* kp = c.k_pages + (int64_t(max(page, 0)) * c.heads + h) * page_bytes +
+                                int64_t(slot + g) * D + t * C::PIECE;
+            const int left = page >= 0 ? end - tok : 0;
 #pragma unroll
-      for (int s = 0; s < D / 16; ++s) frag[warp][s][lane] = make_uint4(qa[2 * s], qb[2 * s], qa[2 * s + 1], qb[2 * s + 1]);
-      if (t < 2) {
-        const int row = t ? rb : ra;
-        float l = INFINITY;  // a row that does not exist or sees nothing adds 0
-        if (row < rows)
-          l = a.lse[int64_t(h * p.G + row % p.G) * a.total_tokens + r.q0 + row / p.G] * 1.4426950408889634f;
-        row_lse[warp][g + 8 * t] = l == -INFINITY ? INFINITY : l;
-        row_scale[warp][g + 8 * t] = (t ? sb : sa) * p.scale_log2;
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int x = 0; x < 2; ++x)
+                copy_async<C::PIECE>(dst + (4 * half + 2 * n + x) * 32 * C::PIECE, kp + n * 8 * D + x * (D / 2),
+                                     8 * n + g < left);
+          }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+#pragma unroll
+      for (int i = 0; i < kStages - 1; ++i) issue(i, false);
+
+      // ---- the rows: warp w stages tiles w, w + 4
+      const int tiles = min(kRowTiles, (rows - row0 + 7) / 8);
+      __syncthreads();  // the last rows have been read
+      for (int x = warp; x < tiles; x += kWarps) {
+        uint32_t q[D / 8];
+        const int row = row0 + 8 * x + g;
+        const float s = load_query<D>(a, r, h, p.G, row, t, q) * p.scale_log2;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) frag[(x * (D / 16) + k) * 32 + lane] = make_uint2(q[2 * k], q[2 * k + 1]);
+        if (t == 0) {
+          float e = INFINITY;  // a row that does not exist or sees nothing adds 0
+          if (row < rows) e = a.lse[int64_t(h * p.G + row % p.G) * a.total_tokens + r.q0 + row / p.G] * kLog2e;
+          row_of[8 * x + g] = make_float4(s, e == -INFINITY ? INFINITY : e,
+                                          __int_as_float(visible_tokens(r, p.G, row, a.causal)), 0.f);
+        }
       }
       __syncthreads();
-    }
-    const int tiles = min(kWarps, (rows - row0 + 15) / 16);
-    for (int tl = 0; tl < tiles; ++tl) {
-      const int first = row0 + tl * 16, last = min(first + 15, rows - 1);
-      if (visible_tokens(r, p.G, last, a.causal) <= tok0) continue;
-      float s[4][4];
-#pragma unroll
-      for (int nt = 0; nt < 4; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint4 q = frag[tl][k][lane];
-#pragma unroll
-        for (int nt = 0; nt < 4; ++nt) mma16816(s[nt], q.x, q.y, q.z, q.w, half2_of(w[nt][k]), half2_of_high(w[nt][k]));
-      }
-      const float fa = row_scale[tl][g], fb = row_scale[tl][g + 8];
-      const float ea = row_lse[tl][g], eb = row_lse[tl][g + 8];
-      const bool masked = tok0 + kTokens > visible_tokens(r, p.G, first, a.causal) || !fine[0] || !fine[1];
-      const int va = visible_tokens(r, p.G, first + g, a.causal), vb = visible_tokens(r, p.G, first + g + 8, a.causal);
-#pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
-        float x[4] = {fmaf(s[nt][0], fa * ks[nt >> 1], -ea), fmaf(s[nt][1], fa * ks[nt >> 1], -ea),
-                      fmaf(s[nt][2], fb * ks[nt >> 1], -eb), fmaf(s[nt][3], fb * ks[nt >> 1], -eb)};
-        if (masked) {
-          const int col = tok0 + 8 * nt + 2 * t;
-          if (!fine[nt >> 1] || col >= va) x[0] = -INFINITY;
-          if (!fine[nt >> 1] || col + 1 >= va) x[1] = -INFINITY;
-          if (!fine[nt >> 1] || col >= vb) x[2] = -INFINITY;
-          if (!fine[nt >> 1] || col + 1 >= vb) x[3] = -INFINITY;
+      const int least = visible_tokens(r, p.G, row0, a.causal);  // tokens that all these rows see
+      const int most = rows > row0 ? visible_tokens(r, p.G, min(row0 + kRowTiles * 8, rows) - 1, a.causal) : 0;
+
+      for (int i = 0; i < mine; ++i) {
+        if (i > 0 && (i & 15) == 0) {
+          now = next;
+          next = pages(i + 16);
         }
-        sum[nt][0] += ptx::ex2(x[0]) + ptx::ex2(x[2]);
-        sum[nt][1] += ptx::ex2(x[1]) + ptx::ex2(x[3]);
+        issue(i + kStages - 1, ((i + kStages - 1) ^ i) >> 4);
+        const int tok = token_of(i);
+        // what the sums are added to: tokens tok + lane, read early
+        float was = 0.f;
+        if (prev && tok + lane < end) was = prev[out + tok + lane];
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        const uint8_t* st = queue_ptr + (i % kStages) * C::STAGE;
+        const int page0 = __shfl_sync(0xffffffffu, now.page, (2 * i) & 31);
+        const int page1 = __shfl_sync(0xffffffffu, now.page, (2 * i + 1) & 31);
+        const float ks[2] = {__shfl_sync(0xffffffffu, now.k_scale, (2 * i) & 31),
+                             __shfl_sync(0xffffffffu, now.k_scale, (2 * i + 1) & 31)};
+        uint32_t k[2][D / 16][4];  // A operands: tokens 16 half + g, + 8
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int y = 0; y < C::PIECE / 4; ++y) {
+              const uint32_t w0 = reinterpret_cast<const uint32_t*>(st + (4 * half + x) * 32 * C::PIECE)[y];
+              const uint32_t w1 = reinterpret_cast<const uint32_t*>(st + (4 * half + 2 + x) * 32 * C::PIECE)[y];
+              uint32_t* to = k[half][x * (C::PIECE / 4) + y];
+              to[0] = half2_of(w0);
+              to[1] = half2_of(w1);
+              to[2] = half2_of_high(w0);
+              to[3] = half2_of_high(w1);
+            }
+        float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};  // tokens 16 half + g, + 8
+        if (tok < most) {
+          const bool masked = tok + kBlock > least || page0 < 0 || page1 < 0;
+          for (int x = 0; x < tiles; ++x) {
+            float s[2][4];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) s[half][0] = s[half][1] = s[half][2] = s[half][3] = 0.f;
+#pragma unroll
+            for (int y = 0; y < D / 16; ++y) {
+              const uint2 q = frag[(x * (D / 16) + y) * 32 + lane];
+#pragma unroll
+              for (int half = 0; half < 2; ++half)
+                mma16816(s[half], k[half][y][0], k[half][y][1], k[half][y][2], k[half][y][3], q.x, q.y);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float4 row = row_of[8 * x + 2 * t + e];
+              const int visible = __float_as_int(row.z);
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                const float f = row.x * ks[half];
+                float w0 = fmaf(s[half][e], f, -row.y), w1 = fmaf(s[half][2 + e], f, -row.y);
+                if (masked) {
+                  const bool gone = (half ? page1 : page0) < 0;
+                  if (gone || tok + 16 * half + g >= visible) w0 = -INFINITY;
+                  if (gone || tok + 16 * half + g + 8 >= visible) w1 = -INFINITY;
+                }
+                sum[half][0] += ptx::ex2(w0);
+                sum[half][1] += ptx::ex2(w1);
+              }
+            }
+          }
+        }
+        // over the four lanes of a token; lane 4 g + t then stores token 8 t + g
+        float mine_sum = 0.f;
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = sum[half][e];
+            x += __shfl_xor_sync(0xffffffffu, x, 1);
+            x += __shfl_xor_sync(0xffffffffu, x, 2);
+            if (t == 2 * half + e) mine_sum = x;
+          }
+        const int at = 8 * t + g;
+        was = __shfl_sync(0xffffffffu, was, at);
+        if (tok + at < end) a.weights[out + tok + at] = was + mine_sum;
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      row0 += kRowTiles * 8;
+      prev = a.weights;  // (written and read again by the same warp)
+      __syncwarp();
+    } while (row0 < rows);
+    pos += u1 - u0;
+    if (pos == before + U * c.heads) {
+      before = pos;
+      ++b;
     }
   }
-#pragma unroll
-  for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float x = sum[nt][e];
-      x += __shfl_xor_sync(0xffffffffu, x, 4);
-      x += __shfl_xor_sync(0xffffffffu, x, 8);
-      x += __shfl_xor_sync(0xffffffffu, x, 16);
-      const int tok = tok0 + 8 * nt + 2 * t + e;
-      if (g == nt && tok < r.len) {  // one lane of the eight that hold it
-        const int64_t at = (int64_t(b) * c.heads + h) * a.weight_stride + tok;
-        a.weights[at] = (a.prev ? a.prev[at] : 0.f) + x;
-      }
-    }
 }
 
 template <int D>
 cudaError_t launch_d(const WeightParams& p, cudaStream_t s) {
-  const CacheQueryArgs& a = p.a;
-  const dim3 grid(unsigned((a.max_seqlen + kWarps * kTokens - 1) / (kWarps * kTokens)), unsigned(a.cache.heads),
-                  unsigned(a.cache.batch));
-  cache_weights_kernel<D><<<grid, kWeightThreads, 0, s>>>(p);
+  using C = WeightCfg<D>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(cache_weights_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  cache_weights_kernel<D><<<unsigned(p.ctas), kWeightThreads, C::SMEM, s>>>(p);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 attn_status launch_cache_weights(const CacheQueryArgs& a, cudaStream_t s) {
-  WeightParams p{a, a.num_heads / a.cache.heads, a.scale * 1.4426950408889634f};
-  cudaError_t e = cudaErrorInvalidValue;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return record_cuda_error(e, "attn_cache_weights device query");
+  WeightParams p{a, a.num_heads / a.cache.heads, 3 * sms, a.scale * kLog2e};
+  e = cudaErrorInvalidValue;
   switch (a.cache.head_dim) {
     case 32: e = launch_d<32>(p, s); break;
     case 64: e = launch_d<64>(p, s); break;
