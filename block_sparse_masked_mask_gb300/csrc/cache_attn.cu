@@ -7,9 +7,8 @@
 //    (cache_rows.cuh).  A CTA walks its piece segment by segment (one sequence
 //    and head each); its four warps take a segment's groups of 16 tokens in
 //    turn and share nothing until the segment's end.
-//  * Each lane copies (cp.async) exactly the bytes that it will use itself,
-//    kStages - 1 groups ahead, into its own places in shared memory: a queue
-//    that needs no barrier.
+//  * Each warp has a queue of its own in shared memory, filled by cp.async
+//    kStages - 1 groups ahead.
 //  * Codes become fp16 in registers (exact) and feed mma.sync m16n8k16, with the
 //    tokens (and then the dimensions) as M and the rows as N = 8 or 16: a
 //    decode step's few rows waste little of a product.  Lanes take their
@@ -36,10 +35,8 @@ constexpr float kLn2 = 0.69314718055994531f;
 
 template <int D>
 struct AttnCfg {
-  // A lane copies a group in eight pieces: two of the keys of two tokens each,
-  // one of the values of four tokens.
-  static constexpr int PIECE = D / 8;
-  static constexpr int STAGE = 32 * 8 * PIECE;  // per warp
+  using Tile = GroupTile<D>;
+  static constexpr int STAGE = 2 * Tile::BYTES;  // keys, values
   static constexpr int QUEUE = kWarps * kStages * STAGE;
   static constexpr int MERGE = kWarps * kFewRows * D * 4;  // over the queue
   static constexpr int STATS = QUEUE > MERGE ? QUEUE : MERGE;
@@ -82,19 +79,18 @@ __global__ void __launch_bounds__(kAttnThreads, 3) cache_attn_kernel(const Cache
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const AttnUnits units{p, blockIdx.x == 0};
-  const int total = total_units(units, c.batch, lane);
-  const int piece = share(total, p.ctas);
+  const UnitLine line(units, c.batch, lane);
+  const int piece = share(line.total, p.ctas);
   int pos = blockIdx.x * piece;
-  const int stop = min(pos + piece, total);
+  const int stop = min(pos + piece, line.total);
   if (pos >= stop) return;
   int before;
-  int b = find_unit(units, c.batch, lane, pos, before);
+  int b = line.find(units, c.batch, lane, pos, before);
 
-  const uint32_t queue = ptx::smem_addr(smem) + warp * kStages * C::STAGE + lane * C::PIECE;
-  const uint8_t* queue_ptr = smem + warp * kStages * C::STAGE + lane * C::PIECE;
+  uint8_t* queue = smem + warp * kStages * C::STAGE;
+  const uint32_t queue_addr = ptx::smem_addr(queue);
   float* mo = reinterpret_cast<float*>(smem);                  // [warp][8 NT][D]
   float2* ml = reinterpret_cast<float2*>(smem + C::STATS);     // [warp][8 NT]
-  const int64_t page_bytes = int64_t(D) << c.page_log2;
 
   while (pos < stop) {
     // ---- the segment: units u0 .. u1 - 1 of sequence b, head h
@@ -114,34 +110,26 @@ __global__ void __launch_bounds__(kAttnThreads, 3) cache_attn_kernel(const Cache
     auto token_of = [&](int i) { return begin + (warp + i * kWarps) * kGroup; };
 
     // ---- the queue
-    PageBatch now = look_up(c, b, h, token_of(lane), lane < mine, true);
-    PageBatch next = look_up(c, b, h, token_of(32 + lane), 32 + lane < mine, true);
-    auto issue = [&](int i, bool ahead) {  // ahead: of the batch after the current one
-      const int page = __shfl_sync(0xffffffffu, ahead ? next.page : now.page, i & 31);
+    int number = page_number(c, b, token_of(lane), lane < mine);
+    int number_next = page_number(c, b, token_of(32 + lane), 32 + lane < mine);
+    auto issue = [&](int i, int numbers) {
+      const int page = __shfl_sync(0xffffffffu, numbers, i & 31);
       if (i < mine) {
         const int tok = token_of(i);
-        const int slot = tok & ((1 << c.page_log2) - 1);
-        const int64_t base = (int64_t(max(page, 0)) * c.heads + h) * page_bytes + int64_t(slot) * D;
-        const uint8_t* kp = c.k_pages + base + g * D + t * C::PIECE;
-        const uint8_t* vp = c.v_pages + base + 2 * t * D + g * C::PIECE;
-        const uint32_t dst = queue + (i % kStages) * C::STAGE;
-        const int left = page >= 0 ? end - tok : 0;  // tokens of the group; zeros behind them
-        // piece j of lane l at (j * 32 + l) * PIECE: no bank conflicts either way
-#pragma unroll
-        for (int half = 0; half < 2; ++half)
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-            copy_async<C::PIECE>(dst + (2 * half + x) * 32 * C::PIECE, kp + half * 8 * D + x * (D / 2), 8 * half + g < left);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int tk = 8 * (q >> 1) + (q & 1);
-          copy_async<C::PIECE>(dst + (4 + q) * 32 * C::PIECE, vp + tk * D, tk + 2 * t < left);
-        }
+        const bool fine = in_pool(c, page);
+        const int64_t base = (((int64_t(fine ? page : 0) * c.heads + h) << c.page_log2) +
+                              (tok & ((1 << c.page_log2) - 1))) * D;
+        const int left = fine ? end - tok : 0;  // tokens of the group
+        const uint32_t dst = queue_addr + (i % kStages) * C::STAGE;
+        C::Tile::template copy<false>(dst, c.k_pages + base, left, lane);
+        C::Tile::template copy<true>(dst + C::Tile::BYTES, c.v_pages + base, left, lane);
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) issue(i, false);
+    for (int i = 0; i < kStages - 1; ++i) issue(i, number);
+    PageBatch now = with_scales(c, h, number, lane < mine, true);
+    PageBatch next = with_scales(c, h, number_next, 32 + lane < mine, true);
 
     // ---- the queries: B operand of row 8 nt + g; scales and limits of rows 8 nt + 2t, + 1
     uint32_t q[NT][D / 8];
@@ -168,11 +156,15 @@ __global__ void __launch_bounds__(kAttnThreads, 3) cache_attn_kernel(const Cache
     for (int i = 0; i < mine; ++i) {
       if (i > 0 && (i & 31) == 0) {
         now = next;
-        next = look_up(c, b, h, token_of(i + 32 + lane), i + 32 + lane < mine, true);
+        const bool on = i + 32 + lane < mine;
+        next = with_scales(c, h, page_number(c, b, token_of(i + 32 + lane), on), on, true);
       }
-      issue(i + kStages - 1, ((i + kStages - 1) ^ i) >> 5);
+      __syncwarp();  // the slot's last group has been read
+      issue(i + kStages - 1, (((i + kStages - 1) ^ i) >> 5) ? next.number : now.number);
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-      const uint8_t* st = queue_ptr + (i % kStages) * C::STAGE;
+      __syncwarp();  // every lane's copies are here
+      const uint8_t* keys = queue + (i % kStages) * C::STAGE;
+      const uint8_t* values = keys + C::Tile::BYTES;
       const float ks = __shfl_sync(0xffffffffu, now.k_scale, i & 31), vs = __shfl_sync(0xffffffffu, now.v_scale, i & 31);
       const int tok = token_of(i);
 
@@ -182,15 +174,13 @@ __global__ void __launch_bounds__(kAttnThreads, 3) cache_attn_kernel(const Cache
       for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        uint32_t w[2][C::PIECE / 4];
+        uint32_t w[2][D / 32];
 #pragma unroll
         for (int half = 0; half < 2; ++half)
+          C::Tile::template read<false>(keys, 8 * half + g, x * (D / 2) + t * (D / 8), w[half]);
 #pragma unroll
-          for (int y = 0; y < C::PIECE / 4; ++y)
-            w[half][y] = reinterpret_cast<const uint32_t*>(st + (2 * half + x) * 32 * C::PIECE)[y];
-#pragma unroll
-        for (int y = 0; y < C::PIECE / 4; ++y) {
-          const int step = x * (C::PIECE / 4) + y;
+        for (int y = 0; y < D / 32; ++y) {
+          const int step = x * (D / 32) + y;
           const uint32_t a0 = half2_of(w[0][y]), a1 = half2_of(w[1][y]), a2 = half2_of_high(w[0][y]),
                          a3 = half2_of_high(w[1][y]);
 #pragma unroll
@@ -247,14 +237,12 @@ __global__ void __launch_bounds__(kAttnThreads, 3) cache_attn_kernel(const Cache
         w1[nt] = transposed(pack_half2(s[nt][2], s[nt][3]));
       }
       // O: dimensions g D/8 + 2k, + 1 by rows 2t, 2t + 1
-      uint32_t v[4][C::PIECE / 4];
+      uint32_t v[4][D / 32];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
+        C::Tile::template read<true>(values, 8 * (j >> 1) + 2 * t + (j & 1), g * (D / 8), v[j]);
 #pragma unroll
-        for (int y = 0; y < C::PIECE / 4; ++y)
-          v[j][y] = reinterpret_cast<const uint32_t*>(st + (4 + j) * 32 * C::PIECE)[y];
-#pragma unroll
-      for (int y = 0; y < C::PIECE / 4; ++y)
+      for (int y = 0; y < D / 32; ++y)
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
           const uint32_t lo = __byte_perm(v[0][y], v[1][y], z ? 0x7362 : 0x5140);
@@ -278,7 +266,7 @@ __global__ void __launch_bounds__(kAttnThreads, 3) cache_attn_kernel(const Cache
         sum += __shfl_xor_sync(0xffffffffu, sum, 16);
         const int row = warp * 8 * NT + 8 * nt + 2 * t + e;
         if (g == 0) ml[row] = make_float2(m[nt][e], sum);
-        float2* to = reinterpret_cast<float2*>(mo + row * D + g * C::PIECE);
+        float2* to = reinterpret_cast<float2*>(mo + row * D + g * (D / 8));
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) to[k] = make_float2(o[k][nt][e], o[k][nt][2 + e]);
       }
@@ -412,6 +400,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_few_kernel(const C
   // the line before this (sequence, head); the division is the other kernel's
   const AttnUnits units{p, false};
   int all = 0, first = 0;
+#pragma unroll 4
   for (int s = lane; s < a.cache.batch; s += 32) {
     const int n = units(s);
     all += n;

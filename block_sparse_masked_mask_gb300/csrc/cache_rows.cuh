@@ -79,62 +79,120 @@ constexpr int kGroup = 16;   // tokens a warp takes at a time
 constexpr int kWarps = 4;    // per CTA; they take a segment's groups in turn
 static_assert(kUnit == kGroup * kWarps, "a unit is one group per warp");
 
-// A division of the line of units among the CTAs of a launch: `units(b)` is the
-// number of sequence b, all heads.  Called by whole warps.
-template <typename F>
-__device__ __forceinline__ int total_units(const F& units, int batch, int lane) {
-  int n = 0;
-  for (int b = lane; b < batch; b += 32) n += units(b);
+// The line of units: `units(b)` is the number of sequence b, all heads.  Called
+// by whole warps; the first 128 sequences' numbers stay with the lanes.
+struct UnitLine {
+  int n[4];
+  int total;
+
+  template <typename F>
+  __device__ __forceinline__ UnitLine(const F& units, int batch, int lane) {
+    total = 0;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-  return n;
-}
-// The sequence that unit `pos` belongs to (pos is below the total), and the units before it.
-template <typename F>
-__device__ __forceinline__ int find_unit(const F& units, int batch, int lane, int pos, int& before) {
-  before = 0;
-  for (int b0 = 0;; b0 += 32) {
-    int n = b0 + lane < batch ? units(b0 + lane) : 0;
-    const int mine = n;
+    for (int k = 0; k < 4; ++k) n[k] = 32 * k + lane < batch ? units(32 * k + lane) : 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, n, o);
-      if (lane >= o) n += y;
-    }
-    const uint32_t past = __ballot_sync(0xffffffffu, before + n > pos);
-    if (past || b0 + 32 >= batch) {
-      const int at = past ? __ffs(past) - 1 : 31;
-      before += __shfl_sync(0xffffffffu, n - mine, at);
-      return b0 + at;
-    }
-    before += __shfl_sync(0xffffffffu, n, 31);
+    for (int k = 0; k < 4; ++k) total += n[k];
+    for (int b = 128 + lane; b < batch; b += 32) total += units(b);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   }
-}
 
-template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool on) {
-  const int n = on ? BYTES : 0;  // nothing read, zeros stored
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n) : "memory");
-}
+  // The sequence that unit `pos` (below the total) belongs to, and the units before it.
+  template <typename F>
+  __device__ __forceinline__ int find(const F& units, int batch, int lane, int pos, int& before) const {
+    before = 0;
+    for (int b0 = 0;; b0 += 32) {
+      int mine = 0;
+      if (b0 < 128) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (b0 == 32 * k) mine = n[k];
+      } else if (b0 + lane < batch) {
+        mine = units(b0 + lane);
+      }
+      int sum = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += y;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, before + sum > pos);
+      if (past || b0 + 32 >= batch) {
+        const int at = past ? __ffs(past) - 1 : 31;
+        before += __shfl_sync(0xffffffffu, sum - mine, at);
+        return b0 + at;
+      }
+      before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+  }
+};
 
-// Pages of a warp's groups, looked up by its lanes 32 at a time, a batch ahead;
-// they travel by shuffle.  A page outside the pool is -1, with scales 0.
+// Sixteen tokens' codes in shared memory, rows of D bytes as they lie in the page.
+// They are copied 512 consecutive bytes per instruction, lane by lane, and read
+// by the lanes that use them, so a warp meets at a barrier of its own
+// between the two.  (Copies straight to the lane that uses them need none, but
+// the values' rows then come in four pieces of 32 bytes per eight lanes: 5.2
+// instead of 7.0 TB/s.)  The pieces of 16 bytes of a row are permuted so that
+// the readers of keys (lane 4 g + t: row g, D / 8 bytes at t D / 8 of a half) or
+// of values (rows 2t, 2t + 1, piece g of D / 8 bytes) meet as few bank conflicts as
+// the row's length allows.
+template <int D>
+struct GroupTile {
+  static constexpr int BYTES = kGroup * D;
+  template <bool VALUES>
+  __device__ static int turn(int row) {
+    if (VALUES) return D == 128 ? ((row >> 1) & 3) << 1 : D == 64 ? (row >> 1) & 3 : 0;
+    return D == 128 ? (row & 1) << 2 : D == 64 ? ((row >> 1) & 1) << 1 : (row >> 2) & 1;
+  }
+  // Rows [0, left) of `src`; zeros behind them.
+  template <bool VALUES>
+  __device__ static void copy(uint32_t dst, const uint8_t* src, int left, int lane) {
+#pragma unroll
+    for (int j = 0; j < BYTES / 512; ++j) {
+      const int at = j * 512 + lane * 16, row = at / D, unit = at % D / 16;
+      const int n = row < left ? 16 : 0;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + row * D + ((unit ^ turn<VALUES>(row)) << 4)),
+                   "l"(src + at), "r"(n)
+                   : "memory");
+    }
+  }
+  // The D / 8 bytes at `at` of a row, as words.
+  template <bool VALUES>
+  __device__ static void read(const uint8_t* tile, int row, int at, uint32_t (&w)[D / 32]) {
+    const uint8_t* from = tile + row * D + (((at >> 4) ^ turn<VALUES>(row)) << 4) + (at & 15);
+    if constexpr (D == 128) {
+      const uint4 v = *reinterpret_cast<const uint4*>(from);
+      w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+    } else if constexpr (D == 64) {
+      const uint2 v = *reinterpret_cast<const uint2*>(from);
+      w[0] = v.x; w[1] = v.y;
+    } else {
+      w[0] = *reinterpret_cast<const uint32_t*>(from);
+    }
+  }
+};
+
+// Pages of a warp's groups, looked up by its lanes 32 at a time and a batch ahead;
+// they travel by shuffle.  The numbers come first, so that copies can start;
+// a page outside the pool has scales 0 (and is noted in the status word).
 struct PageBatch {
-  int page;
+  int number;
   float k_scale, v_scale;
 };
-__device__ __forceinline__ PageBatch look_up(const CacheView& c, int b, int h, int token, bool on, bool values) {
-  PageBatch p{-1, 0.f, 0.f};
-  if (on) {
-    p.page = load_page(c, b, token >> c.page_log2);
-    if (p.page >= 0) {
-      const int64_t at = int64_t(p.page) * c.heads + h;
-      p.k_scale = c.k_scale[at];
-      if (values) p.v_scale = c.v_scale[at];
-    }
+__device__ __forceinline__ int page_number(const CacheView& c, int b, int token, bool on) {
+  return on ? __ldg(c.table + int64_t(b) * c.max_pages + (token >> c.page_log2)) : 0;
+}
+__device__ __forceinline__ bool in_pool(const CacheView& c, int number) {
+  return unsigned(number) < unsigned(c.num_pages);
+}
+__device__ __forceinline__ PageBatch with_scales(const CacheView& c, int h, int number, bool on, bool values) {
+  PageBatch p{number, 0.f, 0.f};
+  if (on && in_pool(c, number)) {
+    const int64_t at = int64_t(number) * c.heads + h;
+    p.k_scale = __ldg(c.k_scale + at);
+    if (values) p.v_scale = __ldg(c.v_scale + at);
+  } else if (on) {
+    atomicOr(c.status, kErrBadPage);
   }
   return p;
 }

@@ -25,8 +25,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D>
 struct WeightCfg {
-  static constexpr int PIECE = D / 8;
-  static constexpr int STAGE = 32 * 8 * PIECE;  // per warp: two pieces of four tokens per lane
+  using Tile = GroupTile<D>;
+  static constexpr int STAGE = 2 * Tile::BYTES;  // two groups' keys, per warp
   static constexpr int QUEUE = kWarps * kStages * STAGE;
   static constexpr int FRAG = D / 16 * 32 * 8;  // a row tile's B operands
   static constexpr int OFF_FRAG = QUEUE;
@@ -60,19 +60,18 @@ __global__ void __launch_bounds__(kWeightThreads, 3) cache_weights_kernel(const 
   const CacheView& c = a.cache;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const WeightUnits units{p, blockIdx.x == 0};
-  const int total = total_units(units, c.batch, lane);
-  const int piece = (total + p.ctas - 1) / p.ctas;
+  const UnitLine line(units, c.batch, lane);
+  const int piece = (line.total + p.ctas - 1) / p.ctas;
   int pos = blockIdx.x * piece;
-  const int stop = min(pos + piece, total);
+  const int stop = min(pos + piece, line.total);
   if (pos >= stop) return;
   int before;
-  int b = find_unit(units, c.batch, lane, pos, before);
+  int b = line.find(units, c.batch, lane, pos, before);
 
-  const uint32_t queue = ptx::smem_addr(smem) + warp * kStages * C::STAGE + lane * C::PIECE;
-  const uint8_t* queue_ptr = smem + warp * kStages * C::STAGE + lane * C::PIECE;
+  uint8_t* queue = smem + warp * kStages * C::STAGE;
+  const uint32_t queue_addr = ptx::smem_addr(queue);
   uint2* frag = reinterpret_cast<uint2*>(smem + C::OFF_FRAG);    // [row tile][step][lane]
   float4* row_of = reinterpret_cast<float4*>(smem + C::OFF_ROWS);  // scale, LSE (base 2), visible
-  const int64_t page_bytes = int64_t(D) << c.page_log2;
 
   while (pos < stop) {
     // ---- the segment: units u0 .. u1 - 1 of sequence b, head h
@@ -95,36 +94,33 @@ __global__ void __launch_bounds__(kWeightThreads, 3) cache_weights_kernel(const 
     int row0 = 0;
     do {  // 64 rows at a time, once where there is none
       // lane 2 i + x: the x-th 16 tokens of the i-th block; 16 blocks at a time, a batch ahead
-      auto pages = [&](int first) {
-        const int i = first + lane / 2, tok = token_of(i) + (lane & 1) * kGroup;
-        return look_up(c, b, h, tok, i < mine && tok < end, false);
+      auto has = [&](int first) {
+        const int i = first + lane / 2;
+        return i < mine && token_of(i) + (lane & 1) * kGroup < end;
       };
-      PageBatch now = pages(0), next = pages(16);
-      auto issue = [&](int i, bool ahead) {
-        const PageBatch& from = ahead ? next : now;
-        const int page0 = __shfl_sync(0xffffffffu, from.page, (2 * i) & 31);
-        const int page1 = __shfl_sync(0xffffffffu, from.page, (2 * i + 1) & 31);
+      auto numbers = [&](int first) {
+        return page_number(c, b, token_of(first + lane / 2) + (lane & 1) * kGroup, has(first));
+      };
+      auto issue = [&](int i, int from) {
+        const int page[2] = {__shfl_sync(0xffffffffu, from, (2 * i) & 31), __shfl_sync(0xffffffffu, from, (2 * i + 1) & 31)};
         if (i < mine) {
-          const uint32_t dst = queue + (i % kStages) * C::STAGE;
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            const int page = half ? page1 : page0, tok = token_of(i) + half * kGroup;
-            const int slot = tok & ((1 << c.page_log2) - 1);
-            const uint8_t* kp = c.k_pages + (int64_t(max(page, 0)) * c.heads + h) * page_bytes +
-                                int64_t(slot + g) * D + t * C::PIECE;
-            const int left = page >= 0 ? end - tok : 0;
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-              for (int x = 0; x < 2; ++x)
-                copy_async<C::PIECE>(dst + (4 * half + 2 * n + x) * 32 * C::PIECE, kp + n * 8 * D + x * (D / 2),
-                                     8 * n + g < left);
+            const int tok = token_of(i) + half * kGroup;
+            const bool fine = in_pool(c, page[half]);
+            const int64_t base = (((int64_t(fine ? page[half] : 0) * c.heads + h) << c.page_log2) +
+                                  (tok & ((1 << c.page_log2) - 1))) * D;
+            C::Tile::template copy<false>(queue_addr + (i % kStages) * C::STAGE + half * C::Tile::BYTES,
+                                          c.k_pages + base, fine ? end - tok : 0, lane);
           }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
       };
+      const int number = numbers(0), number_next = numbers(16);
 #pragma unroll
-      for (int i = 0; i < kStages - 1; ++i) issue(i, false);
+      for (int i = 0; i < kStages - 1; ++i) issue(i, number);
+      PageBatch now = with_scales(c, h, number, has(0), false);
+      PageBatch next = with_scales(c, h, number_next, has(16), false);
 
       // ---- the rows: warp w stages tiles w, w + 4
       const int tiles = min(kRowTiles, (rows - row0 + 7) / 8);
@@ -149,37 +145,40 @@ __global__ void __launch_bounds__(kWeightThreads, 3) cache_weights_kernel(const 
       for (int i = 0; i < mine; ++i) {
         if (i > 0 && (i & 15) == 0) {
           now = next;
-          next = pages(i + 16);
+          next = with_scales(c, h, numbers(i + 16), has(i + 16), false);
         }
-        issue(i + kStages - 1, ((i + kStages - 1) ^ i) >> 4);
+        __syncwarp();  // the slot's last block has been read
+        issue(i + kStages - 1, (((i + kStages - 1) ^ i) >> 4) ? next.number : now.number);
         const int tok = token_of(i);
         // what the sums are added to: tokens tok + lane, read early
         float was = 0.f;
         if (prev && tok + lane < end) was = prev[out + tok + lane];
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-        const uint8_t* st = queue_ptr + (i % kStages) * C::STAGE;
-        const int page0 = __shfl_sync(0xffffffffu, now.page, (2 * i) & 31);
-        const int page1 = __shfl_sync(0xffffffffu, now.page, (2 * i + 1) & 31);
+        __syncwarp();  // every lane's copies are here
+        const uint8_t* st = queue + (i % kStages) * C::STAGE;
         const float ks[2] = {__shfl_sync(0xffffffffu, now.k_scale, (2 * i) & 31),
                              __shfl_sync(0xffffffffu, now.k_scale, (2 * i + 1) & 31)};
         uint32_t k[2][D / 16][4];  // A operands: tokens 16 half + g, + 8
 #pragma unroll
         for (int half = 0; half < 2; ++half)
 #pragma unroll
-          for (int x = 0; x < 2; ++x)
+          for (int x = 0; x < 2; ++x) {
+            uint32_t w0[D / 32], w1[D / 32];
+            const int at = x * (D / 2) + t * (D / 8);
+            C::Tile::template read<false>(st + half * C::Tile::BYTES, g, at, w0);
+            C::Tile::template read<false>(st + half * C::Tile::BYTES, 8 + g, at, w1);
 #pragma unroll
-            for (int y = 0; y < C::PIECE / 4; ++y) {
-              const uint32_t w0 = reinterpret_cast<const uint32_t*>(st + (4 * half + x) * 32 * C::PIECE)[y];
-              const uint32_t w1 = reinterpret_cast<const uint32_t*>(st + (4 * half + 2 + x) * 32 * C::PIECE)[y];
-              uint32_t* to = k[half][x * (C::PIECE / 4) + y];
-              to[0] = half2_of(w0);
-              to[1] = half2_of(w1);
-              to[2] = half2_of_high(w0);
-              to[3] = half2_of_high(w1);
+            for (int y = 0; y < D / 32; ++y) {
+              uint32_t* to = k[half][x * (D / 32) + y];
+              to[0] = half2_of(w0[y]);
+              to[1] = half2_of(w1[y]);
+              to[2] = half2_of_high(w0[y]);
+              to[3] = half2_of_high(w1[y]);
             }
+          }
         float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};  // tokens 16 half + g, + 8
         if (tok < most) {
-          const bool masked = tok + kBlock > least || page0 < 0 || page1 < 0;
+          const bool masked = tok + kBlock > least || ks[0] == 0.f || ks[1] == 0.f;  // scale 0: left out
           for (int x = 0; x < tiles; ++x) {
             float s[2][4];
 #pragma unroll
@@ -200,7 +199,7 @@ __global__ void __launch_bounds__(kWeightThreads, 3) cache_weights_kernel(const 
                 const float f = row.x * ks[half];
                 float w0 = fmaf(s[half][e], f, -row.y), w1 = fmaf(s[half][2 + e], f, -row.y);
                 if (masked) {
-                  const bool gone = (half ? page1 : page0) < 0;
+                  const bool gone = ks[half] == 0.f;
                   if (gone || tok + 16 * half + g >= visible) w0 = -INFINITY;
                   if (gone || tok + 16 * half + g + 8 >= visible) w1 = -INFINITY;
                 }
