@@ -347,40 +347,35 @@ class _Launch:
         return s.cuda_stream
 
     def __exit__(self, *exc):
+        # (also called without arguments, behind a plain try)
+        exc = exc or (None, None, None)
         while self._guards:
             self._guards.pop().__exit__(*exc)
 
 
-class _Here:
-    """The usual case of _Launch: the current device and its current stream."""
-
-    def __init__(self, index: int):
-        self._handle = torch._C._cuda_getCurrentRawStream(index)
-
-    def __enter__(self):
-        return self._handle
-
-    def __exit__(self, *exc):
-        pass
+_Tensor = torch.Tensor
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _launch(device: torch.device, stream):
-    if stream is None and device.index == torch.cuda.current_device():
-        return _Here(device.index)
+def _elsewhere(device: torch.device, stream):
+    """None in the usual case, where a call runs on the current device and its
+    current stream; otherwise the context it runs in."""
+    if stream is None and device.index == torch._C._cuda_getDevice():
+        return None
     return _Launch(device, stream)
 
 
 def _fits(t, dtype, shape, index: int) -> bool:
     """The quick form of _need: a contiguous CUDA tensor of this type and shape on
     device `index`.  Where it is False, _need says what is wrong."""
-    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.get_device() == index
-            and t.shape == shape and t.is_contiguous())
+    return (type(t) is _Tensor and t.dtype is dtype and t.get_device() == index and t.shape == shape
+            and t.is_contiguous())
 
 
 def _need_rows(t, name: str, where: str, dtypes, device=None) -> int:
     """[tokens, heads, dim] with dense heads, tokens any distance apart (a slice
     of a wider projection); returns that distance in elements."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, _Tensor) or not t.is_cuda:
         raise AttnError(1, f"{where}: {name} must be a CUDA tensor")
     if device is not None and t.get_device() != device.index:
         raise AttnError(1, f"{where}: {name} is on {t.device}, expected {device}")
@@ -468,7 +463,9 @@ def attn_rope(q: torch.Tensor, k: Optional[torch.Tensor], plan: RopePlan,
         batch = cu_seqlens.numel() - 1
         if seq_lens is not None and not _fits(seq_lens, torch.int32, (batch,), dev.index):
             _need(seq_lens, "seq_lens", where, (torch.int32,), (batch,), dev)
-    with _launch(dev, stream) as s:
+    at = _elsewhere(dev, stream)
+    s = _raw_stream(dev.index) if at is None else at.__enter__()
+    try:
         if q_out is None:
             q_out, qos = torch.empty((T, H, D), dtype=q.dtype, device=dev), H * D
         else:
@@ -489,6 +486,9 @@ def attn_rope(q: torch.Tensor, k: Optional[torch.Tensor], plan: RopePlan,
             None if positions is not None else cu_seqlens.data_ptr(),
             None if positions is not None or seq_lens is None else seq_lens.data_ptr(), batch,
             plan._ref, int(bool(inverse)), s), where)
+    finally:
+        if at is not None:
+            at.__exit__()
     return q_out, k_out
 
 
@@ -573,10 +573,15 @@ def attn_cache_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, cu_seqle
         raise AttnError(1, f"{where}: k and v must be [tokens, {cache.num_kv_heads}, {cache.head_dim}], got "
                            f"{tuple(k.shape)} and {tuple(v.shape)}")
     _need_seqs(cache, cu_seqlens, seq_lens, where)
-    with _launch(cache.device, stream) as s:
+    at = _elsewhere(cache.device, stream)
+    s = _raw_stream(cache.device.index) if at is None else at.__enter__()
+    try:
         _check(_native.lib().attn_cache_append(
             k.data_ptr(), v.data_ptr(), ks, vs, DTYPES[k.dtype], k.shape[0], cu_seqlens.data_ptr(),
             seq_lens.data_ptr(), int(max_new), cache._ref, s), where)
+    finally:
+        if at is not None:
+            at.__exit__()
 
 
 def _need_queries(q, cache, where: str):
@@ -626,21 +631,31 @@ def attn_cache_fwd(q: torch.Tensor, cache: KVCache, cu_seqlens: torch.Tensor, se
         _need(lse, "lse", where, (torch.float32,), (H, T), dev)
     _need(workspace, "workspace", where, device=dev)
     _need_seqs(cache, cu_seqlens, seq_lens, where)
-    with _launch(dev, stream) as s:
+    at = _elsewhere(dev, stream)
+    s = _raw_stream(dev.index) if at is None else at.__enter__()
+    try:
         if out is None:
             out = torch.empty_like(q)
         if lse is None:
             lse = torch.empty((H, T), dtype=torch.float32, device=dev)
-        if workspace is None:
-            need = attn_cache_fwd_workspace_size(cache, T, H, int(max_new), int(max_seqlen))
-            if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        ws, nbytes = (None, 0) if workspace is None else (workspace.data_ptr(),
-                                                          workspace.numel() * workspace.element_size())
-        _check(_native.lib().attn_cache_fwd(
-            q.data_ptr(), out.data_ptr(), lse.data_ptr(), DTYPES[q.dtype], T, H, float(scale),
-            cu_seqlens.data_ptr(), int(max_new), seq_lens.data_ptr(), int(max_seqlen), _kind(kind),
-            cache._ref, ws, nbytes, s), where)
+        own = None
+        if workspace is not None:
+            ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        else:
+            ws, nbytes = None, attn_cache_fwd_workspace_size(cache, T, H, max_new, max_seqlen)
+            if nbytes:
+                # what torch.empty draws on, without a tensor around it (a fifth of its time)
+                ws = own = torch._C._cuda_cudaCachingAllocator_raw_alloc(nbytes, s)
+        try:
+            _check(_native.lib().attn_cache_fwd(
+                q.data_ptr(), out.data_ptr(), lse.data_ptr(), 0, T, H, scale, cu_seqlens.data_ptr(), max_new,
+                seq_lens.data_ptr(), max_seqlen, _kind(kind), cache._ref, ws, nbytes, s), where)
+        finally:
+            if own is not None:  # reused in the order of the stream
+                torch._C._cuda_cudaCachingAllocator_raw_delete(own)
+    finally:
+        if at is not None:
+            at.__exit__()
     return out, lse
 
 
@@ -669,13 +684,18 @@ def attn_cache_weights(q: torch.Tensor, lse: torch.Tensor, cache: KVCache, cu_se
     for name, t in (("prev", prev), ("out", out)):
         if t is not None and not _fits(t, torch.float32, shape, cache.index):
             _need(t, name, where, (torch.float32,), shape, dev)
-    with _launch(dev, stream) as s:
+    at = _elsewhere(dev, stream)
+    s = _raw_stream(dev.index) if at is None else at.__enter__()
+    try:
         if out is None:
             out = torch.zeros(shape, dtype=torch.float32, device=dev)
         _check(_native.lib().attn_cache_weights(
             q.data_ptr(), lse.data_ptr(), DTYPES[q.dtype], T, H, float(scale), cu_seqlens.data_ptr(),
             int(max_new), seq_lens.data_ptr(), int(max_seqlen), _kind(kind), cache._ref,
             None if prev is None else prev.data_ptr(), out.data_ptr(), shape[2], s), where)
+    finally:
+        if at is not None:
+            at.__exit__()
     return out
 
 
@@ -716,7 +736,9 @@ def attn_cache_evict(weights: torch.Tensor, cache: KVCache, dst: KVCache, seq_le
             raise AttnError(1, f"{where}: {name} must be [{B}, {H}, width], got {tuple(t.shape)}")
     if max_keep < 0:
         raise AttnError(1, f"{where}: max_keep is negative")
-    with _launch(dev, stream) as s:
+    at = _elsewhere(dev, stream)
+    s = _raw_stream(dev.index) if at is None else at.__enter__()
+    try:
         if kept is None:
             kept = torch.empty((B, H, max_keep), dtype=torch.int32, device=dev)
         if new_weights is None:
@@ -727,11 +749,19 @@ def attn_cache_evict(weights: torch.Tensor, cache: KVCache, dst: KVCache, seq_le
             weights.data_ptr(), weights.shape[2], seq_lens.data_ptr(), budgets.data_ptr(), int(recent),
             int(max_seqlen), max_keep, cache._ref, dst._ref, kept.data_ptr(), new_weights.data_ptr(),
             new_weights.shape[2], new_lens.data_ptr(), s), where)
+    finally:
+        if at is not None:
+            at.__exit__()
     return kept, new_weights, new_lens
 
 
 def attn_cache_get_status(cache: KVCache, stream=None) -> int:
     """Synchronise, then return and clear the cache's device status code."""
     _need_cache(cache, "attn_cache_get_status")
-    with _launch(cache.device, stream) as s:
+    at = _elsewhere(cache.device, stream)
+    s = _raw_stream(cache.device.index) if at is None else at.__enter__()
+    try:
         return int(_native.lib().attn_cache_get_status(cache._ref, s))
+    finally:
+        if at is not None:
+            at.__exit__()

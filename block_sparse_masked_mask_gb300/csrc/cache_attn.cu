@@ -382,16 +382,17 @@ __device__ __forceinline__ void join_row(const CacheAttnParams& p, int n, const 
   if (lane == 0) a.lse[int64_t(head) * a.total_tokens + token] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
-constexpr int kJoinWarps = 8;
+constexpr int kJoinWarps = 8;  // per CTA
 
 // Both joining kernels start while the first one ends; every CTA waits for its
 // end, those with nothing to join too, so that what follows on the stream does.
-// Few rows: a CTA per (sequence, row); 8 warps share its partial results.
-template <int D>
+// Few rows: W warps per row share its partial results (1 or 8).
+template <int D, int W>
 __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_few_kernel(const CacheAttnParams p) {
-  __shared__ float shared[kJoinWarps * (D + 2)];
+  __shared__ float shared[W > 1 ? W * (D + 2) : 1];
   const CacheQueryArgs& a = p.a;
-  const int b = blockIdx.y, i = blockIdx.x, w = threadIdx.x >> 5, lane = threadIdx.x & 31;  // i: token, head
+  const int b = blockIdx.y, w = (threadIdx.x >> 5) % W, lane = threadIdx.x & 31;
+  const int i = blockIdx.x * (kJoinWarps / W) + (threadIdx.x >> 5) / W;  // of the sequence: token, head
   SeqRows r;
   const bool good = load_rows(a.cu, a.lens, b, a.total_tokens, a.max_new, a.max_seqlen, a.cache.status, r, false);
   const bool mine = good && i < r.n * a.num_heads;
@@ -417,7 +418,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_few_kernel(const C
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!mine || c0 == c1) return;  // finished by its CTA
   auto at = [&](int j) { return int64_t(2 * (c0 + j) + (j == 0 ? 1 : 0)) * (a.max_new * p.G) + row; };
-  join_row<D, kJoinWarps>(p, c1 - c0 + 1, at, r.q0 + i / a.num_heads, head, w, lane, shared);
+  join_row<D, W>(p, c1 - c0 + 1, at, r.q0 + i / a.num_heads, head, w, lane, shared);
 }
 
 // Many rows: a warp per row, over the chunks that the row's tile had.
@@ -481,8 +482,14 @@ cudaError_t launch_few(const CacheAttnParams& p, cudaStream_t s) {
 template <int D>
 cudaError_t launch_join(const CacheAttnParams& p, cudaStream_t s) {
   const int64_t rows = int64_t(p.a.max_new) * p.a.num_heads;
+  // A (sequence, head) meets about ctas / (their number) CTAs; where those are
+  // many, a CTA joins each row (one request of 131072 tokens and one head: 128
+  // us with a warp per row, 25 us), else a warp does (64 requests of 8 heads: the
+  // join takes 12 us with a CTA per row, 5 us with a warp).
+  const bool wide = !p.many && int64_t(p.ctas) > 8 * int64_t(p.a.cache.batch) * p.a.cache.heads;
+  const int per_cta = wide ? 1 : kJoinWarps;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(p.many ? (rows + kJoinWarps - 1) / kJoinWarps : rows), unsigned(p.a.cache.batch));
+  cfg.gridDim = dim3(unsigned((rows + per_cta - 1) / per_cta), unsigned(p.a.cache.batch));
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -490,7 +497,8 @@ cudaError_t launch_join(const CacheAttnParams& p, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, p.many ? cache_join_many_kernel<D> : cache_join_few_kernel<D>, p);
+  return cudaLaunchKernelEx(&cfg, p.many ? cache_join_many_kernel<D>
+                                         : wide ? cache_join_few_kernel<D, kJoinWarps> : cache_join_few_kernel<D, 1>, p);
 }
 
 }  // namespace
