@@ -2,13 +2,16 @@
 //
 // Choice, one CTA per (sequence, head): the last tokens are kept in any case;
 // of the others the `want` largest weights.  Weights become 32-bit keys of the
-// same order, and a radix selection fixes the want-th largest key eight bits
-// at a time (a histogram per pass over the weights, which stay in L2).  A last
-// pass in the order of the tokens writes those above the border key, and of
-// those at it the first ones, at the places that a running count gives.
-// Copy, one CTA per (page of the destination, head): the page's scale is the
-// largest of its tokens' scales; codes of smaller scales are shifted.
-#include "cache.cuh"
+// same order, held in shared memory (as many as fit, else read again), and a radix
+// selection fixes the want-th largest key in digits of 11, 11 and 10 bits: the
+// first digit is the exponent and two bits more, so that weights of one size
+// still spread over a few counters.  Each warp then takes a run of consecutive
+// tokens, counts what it keeps (above the border key, and of those at it the first
+// ones) and, knowing the counts of the warps before it, writes it in order.
+// Copy, a CTA per page of the destination and head, 16 bytes per lane and all of
+// a page's loads in flight at once: the page's scale is the largest of its
+// tokens' scales; codes of smaller scales are shifted.
+#include "cache_rows.cuh"
 
 namespace attnmask {
 namespace {
@@ -36,10 +39,37 @@ __device__ __forceinline__ bool load_kept(const EvictArgs& a, int b, int& len, i
   return err == 0;
 }
 
-__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const EvictArgs a) {
+constexpr int kBins = 2048;
+constexpr int kStageMost = 48 * 1024;  // keys in shared memory
+
+// Sum of `x` over the threads before this one (1024 threads), and over all.
+// `sums` holds 32 words; the caller puts a barrier between two uses of it.
+__device__ __forceinline__ int sum_before(int x, int* sums, int& all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int up = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, up, o);
+    if (lane >= o) up += y;
+  }
+  if (lane == 31) sums[warp] = up;
+  __syncthreads();
+  const int s = sums[lane];
+  int w = s;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += y;
+  }
+  all = __shfl_sync(0xffffffffu, w, 31);
+  return __shfl_sync(0xffffffffu, w - s, warp) + up - x;
+}
+
+__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const EvictArgs a, int stage) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  __shared__ int hist[256];
-  __shared__ int warp_sum[32];
+  extern __shared__ uint32_t keys[];  // of the first `stage` tokens
+  __shared__ int hist[kBins];
+  __shared__ int sums[32];
   __shared__ uint32_t border;
   __shared__ int left;  // keys still wanted among those that match the border so far
   const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -50,170 +80,199 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
   float* out = a.new_weights + (int64_t(b) * a.src.heads + h) * a.new_stride;
   if (h == 0 && tid == 0) a.new_lens[b] = keep;
   const int tail = min(a.recent, keep), others = len - tail, want = keep - tail;
-
-  if (tid == 0) {
-    border = 0;
-    left = want;
-  }
-  __syncthreads();
-  if (want < others && want > 0) {
-    for (int pass = 0; pass < 4; ++pass) {
-      const int shift = 24 - 8 * pass;
-      if (tid < 256) hist[tid] = 0;
-      __syncthreads();
-      const uint32_t prefix = border;
-      for (int j = tid; j < others; j += kSelectThreads) {
-        const uint32_t k = order_key(w[j]);
-        if (pass == 0 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255u], 1);
-      }
-      __syncthreads();
-      if (warp == 0) {
-        // digits from 255 down, eight per lane: the one where the count reaches `left`
-        int n[8], mine = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mine += n[i] = hist[255 - (8 * lane + i)];
-        int before = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, before, o);
-          if (lane >= o) before += y;
-        }
-        before -= mine;
-        const int need = left;
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (before < need && before + n[i] >= need) {
-            border = prefix | uint32_t(255 - (8 * lane + i)) << shift;
-            left = need - before;
-          }
-          before += n[i];
-        }
-      }
-      __syncthreads();
-    }
-  }
   const bool all = want >= others;
-  const uint32_t edge = border;
-  const int ties = left;  // of the keys equal to the border, the first `ties`
-  __syncthreads();
+  auto key_of = [&](int j) { return j < stage ? keys[j] : order_key(w[j]); };
 
-  // in the order of the tokens: (kept, at the border) counts in one word
-  int64_t base = 0;  // low half: kept so far; high half: border keys so far
-  for (int j0 = 0; j0 < len; j0 += kSelectThreads) {
-    const int j = j0 + tid;
-    uint32_t k = 0;
-    float x = 0.f;
-    bool above = false, at = false;
-    if (j < len) {
-      x = w[j];
-      k = order_key(x);
-      above = j >= others || all || (want > 0 && k > edge);
-      at = !above && want > 0 && k == edge;
+  if (!all && want > 0) {
+#pragma unroll 4
+    for (int j = tid; j < min(others, stage); j += kSelectThreads) keys[j] = order_key(w[j]);
+    uint32_t prefix = 0;
+    int need = want;
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+      for (int i = tid; i < kBins; i += kSelectThreads) hist[i] = 0;
+      __syncthreads();
+      for (int j = tid; j < others; j += kSelectThreads) {
+        const uint32_t k = key_of(j);
+        if (pass == 0 || (k >> (shift + bits)) == (prefix >> (shift + bits)))
+          atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1)], 1);
+      }
+      __syncthreads();
+      // digits from the highest down, two per thread: the one where the count reaches `need`
+      const int n0 = hist[kBins - 1 - 2 * tid], n1 = hist[kBins - 2 - 2 * tid];
+      int total;
+      const int before = sum_before(n0 + n1, sums, total);
+      if (before < need && before + n0 >= need) {
+        border = prefix | uint32_t(kBins - 1 - 2 * tid) << shift;
+        left = need - before;
+      } else if (before + n0 < need && before + n0 + n1 >= need) {
+        border = prefix | uint32_t(kBins - 2 - 2 * tid) << shift;
+        left = need - before - n0;
+      }
+      __syncthreads();
+      prefix = border;
+      need = left;
     }
-    // border keys before this one
-    const uint32_t lower = (1u << lane) - 1u;
-    const uint32_t tie_mask = __ballot_sync(0xffffffffu, at);
-    if (lane == 0) warp_sum[warp] = __popc(tie_mask);
-    __syncthreads();
-    int tie_before = 0, tie_all = 0;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const int n = warp_sum[i];
-      tie_before += i < warp ? n : 0;
-      tie_all += n;
+  }
+  const uint32_t edge = all || want == 0 ? 0u : border;
+  const int ties = all || want == 0 ? 0 : left;  // of the keys equal to the border, the first `ties`
+
+  // warp w: a run of consecutive tokens, 32 at a time
+  const int run = ((len + kSelectThreads - 1) / kSelectThreads) * 32;
+  const int j0 = warp * run, j1 = min(len, j0 + run);
+  auto classify = [&](int j, uint32_t& above, uint32_t& at) {
+    bool up = false, tie = false;
+    if (j < j1) {
+      if (all || j >= others) {
+        up = true;
+      } else if (want > 0) {
+        const uint32_t k = key_of(j);
+        up = k > edge;
+        tie = k == edge;
+      }
     }
-    __syncthreads();
-    const int tie_rank = int(base >> 32) + tie_before + __popc(tie_mask & lower);
-    const bool take = above || (at && tie_rank < ties);
-    const uint32_t take_mask = __ballot_sync(0xffffffffu, take);
-    if (lane == 0) warp_sum[warp] = __popc(take_mask);
-    __syncthreads();
-    int before = 0, total = 0;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const int n = warp_sum[i];
-      before += i < warp ? n : 0;
-      total += n;
+    above = __ballot_sync(0xffffffffu, up);
+    at = __ballot_sync(0xffffffffu, tie);
+  };
+  int n_above = 0, n_tie = 0;
+  for (int j = j0; j < j1; j += 32) {
+    uint32_t above, at;
+    classify(j + lane, above, at);
+    n_above += __popc(above);
+    n_tie += __popc(at);
+  }
+  int unused;
+  __syncthreads();
+  int tie = sum_before(lane == 0 ? n_tie : 0, sums, unused);  // border keys before this warp's
+  tie = __shfl_sync(0xffffffffu, tie, 0);
+  const int taken = max(0, min(n_tie, ties - tie));           // of this warp's, the first `taken`
+  __syncthreads();
+  int place = sum_before(lane == 0 ? n_above + taken : 0, sums, unused);
+  place = __shfl_sync(0xffffffffu, place, 0);
+  const uint32_t lower = (1u << lane) - 1u;
+  for (int j = j0; j < j1; j += 32) {
+    uint32_t above, at;
+    classify(j + lane, above, at);
+    const bool first = (at >> lane & 1u) && tie + __popc(at & lower) < ties;
+    const uint32_t take = above | __ballot_sync(0xffffffffu, first);
+    if (take >> lane & 1u) {
+      const int to = place + __popc(take & lower);
+      kept[to] = j + lane;
+      out[to] = w[j + lane];
     }
-    __syncthreads();
-    if (take) {
-      const int place = int(uint32_t(base)) + before + __popc(take_mask & lower);
-      kept[place] = j;
-      out[place] = x;
-    }
-    base += (int64_t(tie_all) << 32) + total;
+    place += __popc(take);
+    tie += __popc(at);
   }
   for (int j = keep + tid; j < a.max_keep; j += kSelectThreads) kept[j] = -1;
   for (int64_t j = keep + tid; j < a.new_stride; j += kSelectThreads) out[j] = 0.f;
 }
 
+// Pages of the destination that a sequence fills.
+struct KeptPages {
+  const EvictArgs& a;
+  __device__ int operator()(int b) const {
+    const int len = a.lens[b], budget = a.budgets[b], keep = min(len, budget);
+    if (len < 0 || len > a.max_seqlen || budget < 0 || keep > a.max_keep) return 0;
+    return (keep + (1 << a.src.page_log2) - 1) >> a.src.page_log2;
+  }
+};
+
+// N: 16-byte pieces per thread of a page's keys (and as many of its values)
+template <int N>
 __global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const EvictArgs a) {
+  __shared__ int src_page[2][128], src_slot[2][128];
+  __shared__ int exps[2][2][128];
+  __shared__ int top[2][2];
+  const int page_size = 1 << a.src.page_log2, D = a.src.head_dim, per_row = D / 16;
+  const int h = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
+  const KeptPages pages{a};
+  const UnitLine line(pages, a.src.batch, lane);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  __shared__ int src_page[128], src_slot[128];
-  __shared__ int exps[2][128];
-  __shared__ int top[2];
-  const int page_size = 1 << a.src.page_log2, D = a.src.head_dim;
-  const int i = blockIdx.x, h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
-  int len, keep;
-  if (!load_kept(a, b, len, keep)) return;
-  const int n = min(page_size, keep - (i << a.src.page_log2));  // tokens of this page
-  if (n <= 0) return;
-  const int dst = load_page(a.dst, b, i);
-  if (dst < 0) {
-    if (tid == 0) atomicOr(a.src.status, kErrBadPage);
-    return;
-  }
-  if (tid < 2) top[tid] = -1000;
-  __syncthreads();
-  if (tid < n) {
-    const int j = a.kept[(int64_t(b) * a.src.heads + h) * a.max_keep + (i << a.src.page_log2) + tid];
-    const int page = load_page(a.src, b, j >> a.src.page_log2);
-    src_page[tid] = page;
-    src_slot[tid] = j & (page_size - 1);
-    if (page >= 0) {
-      const int64_t at = int64_t(page) * a.src.heads + h;
-      exps[0][tid] = exponent_of(a.src.k_scale[at]);
-      exps[1][tid] = exponent_of(a.src.v_scale[at]);
-      atomicMax(&top[0], exps[0][tid]);
-      atomicMax(&top[1], exps[1][tid]);
+  int turn = 0;  // the shared arrays alternate, one barrier each
+  for (int pos = blockIdx.x; pos < line.total; pos += gridDim.x, turn ^= 1) {
+    int before;
+    const int b = line.find(pages, a.src.batch, lane, pos, before);
+    const int i = pos - before;
+    const int keep = min(a.lens[b], a.budgets[b]);
+    const int n = min(page_size, keep - (i << a.src.page_log2));  // tokens of this page
+    const int dst = __ldg(a.dst.table + int64_t(b) * a.dst.max_pages + i);
+    const bool fine = unsigned(dst) < unsigned(a.dst.num_pages);
+    if (!fine && tid == 0) {
+      atomicOr(a.src.status, kErrBadPage);
+      atomicOr(a.dst.status, kErrBadPage);
     }
-  }
-  __syncthreads();
-  const int pieces = D / 16;  // 16-byte pieces per token
-  for (int x = tid; x < 2 * n * pieces; x += kGatherThreads) {
-    const int side = x >= n * pieces, y = x - side * n * pieces;
-    const int slot = y / pieces, piece = y % pieces;
-    const int page = src_page[slot];
-    if (page < 0) continue;
-    const uint8_t* from = (side ? a.src.v_pages : a.src.k_pages) +
-                          (((int64_t(page) * a.src.heads + h) << a.src.page_log2) + src_slot[slot]) * D + piece * 16;
-    uint8_t* to = (side ? a.dst.v_pages : a.dst.k_pages) +
-                  (((int64_t(dst) * a.dst.heads + h) << a.dst.page_log2) + slot) * D + piece * 16;
-    uint4 v = *reinterpret_cast<const uint4*>(from);
-    const int shift = top[side] - exps[side][slot];
-    if (shift > 0) {
-      v.x = rescale4(v.x, shift);
-      v.y = rescale4(v.y, shift);
-      v.z = rescale4(v.z, shift);
-      v.w = rescale4(v.w, shift);
+    if (tid < 2) top[turn][tid] = -1000;
+    __syncthreads();  // (also: the pages before the last have been copied)
+    if (tid < n) {
+      const int j = a.kept[(int64_t(b) * a.src.heads + h) * a.max_keep + (i << a.src.page_log2) + tid];
+      const int page = load_page(a.src, b, j >> a.src.page_log2);
+      src_page[turn][tid] = page;
+      src_slot[turn][tid] = j & (page_size - 1);
+      if (page >= 0) {
+        const int64_t at = int64_t(page) * a.src.heads + h;
+        const int ek = exponent_of(a.src.k_scale[at]), ev = exponent_of(a.src.v_scale[at]);
+        exps[turn][0][tid] = ek;
+        exps[turn][1][tid] = ev;
+        atomicMax(&top[turn][0], ek);
+        atomicMax(&top[turn][1], ev);
+      }
     }
-    *reinterpret_cast<uint4*>(to) = v;
+    __syncthreads();
+    if (!fine) continue;
+    uint4 v[2][N];
+#pragma unroll
+    for (int side = 0; side < 2; ++side)
+#pragma unroll
+      for (int y = 0; y < N; ++y) {
+        const int x = y * kGatherThreads + tid, slot = x / per_row, piece = x % per_row;
+        if (slot >= n || src_page[turn][slot] < 0) continue;
+        v[side][y] = *reinterpret_cast<const uint4*>(
+            (side ? a.src.v_pages : a.src.k_pages) +
+            (((int64_t(src_page[turn][slot]) * a.src.heads + h) << a.src.page_log2) + src_slot[turn][slot]) * D +
+            piece * 16);
+      }
+#pragma unroll
+    for (int side = 0; side < 2; ++side)
+#pragma unroll
+      for (int y = 0; y < N; ++y) {
+        const int x = y * kGatherThreads + tid, slot = x / per_row, piece = x % per_row;
+        if (slot >= n || src_page[turn][slot] < 0) continue;
+        uint4 w = v[side][y];
+        const int shift = top[turn][side] - exps[turn][side][slot];
+        if (shift > 0) {
+          w.x = rescale4(w.x, shift);
+          w.y = rescale4(w.y, shift);
+          w.z = rescale4(w.z, shift);
+          w.w = rescale4(w.w, shift);
+        }
+        *reinterpret_cast<uint4*>((side ? a.dst.v_pages : a.dst.k_pages) +
+                                  (((int64_t(dst) * a.dst.heads + h) << a.dst.page_log2) + slot) * D + piece * 16) = w;
+      }
+    if (tid < 2 && top[turn][tid] > -1000)
+      (tid ? a.dst.v_scale : a.dst.k_scale)[int64_t(dst) * a.dst.heads + h] = pow2f(max(-126, top[turn][tid]));
   }
-  if (tid < 2 && top[tid] > -1000)
-    (tid ? a.dst.v_scale : a.dst.k_scale)[int64_t(dst) * a.dst.heads + h] = pow2f(max(-126, top[tid]));
 }
 
 }  // namespace
 
 attn_status launch_cache_evict(const EvictArgs& a, cudaStream_t s) {
-  evict_select_kernel<<<dim3(unsigned(a.src.heads), unsigned(a.src.batch)), kSelectThreads, 0, s>>>(a);
-  cudaError_t e = cudaGetLastError();
+  const int stage = a.max_seqlen < kStageMost ? a.max_seqlen : kStageMost;
+  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStageMost * 4);
+  if (e != cudaSuccess) return record_cuda_error(e, "attn_cache_evict configure");
+  evict_select_kernel<<<dim3(unsigned(a.src.heads), unsigned(a.src.batch)), kSelectThreads, unsigned(stage) * 4, s>>>(a, stage);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return record_cuda_error(e, "attn_cache_evict select launch");
   if (a.max_keep == 0) return ATTN_OK;
+  // Sixteen CTAs per SM at most; they take the pages in turn.
+  const int page_size = 1 << a.src.page_log2;
+  const int64_t pages = int64_t(a.src.batch) * ((int64_t(a.max_keep) + page_size - 1) / page_size);
+  int dev = 0, sms = 0;
+  e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return record_cuda_error(e, "attn_cache_evict device query");
+  const int64_t most = (16ll * sms + a.src.heads - 1) / a.src.heads;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned((a.max_keep + (1 << a.src.page_log2) - 1) >> a.src.page_log2), unsigned(a.src.heads),
-                     unsigned(a.src.batch));
+  cfg.gridDim = dim3(unsigned(pages < most ? pages : most), unsigned(a.src.heads));
   cfg.blockDim = dim3(kGatherThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -221,7 +280,12 @@ attn_status launch_cache_evict(const EvictArgs& a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, evict_gather_kernel, a);
+  switch (page_size * a.src.head_dim / 16 / kGatherThreads) {
+    case 8: e = cudaLaunchKernelEx(&cfg, evict_gather_kernel<8>, a); break;
+    case 4: e = cudaLaunchKernelEx(&cfg, evict_gather_kernel<4>, a); break;
+    case 2: e = cudaLaunchKernelEx(&cfg, evict_gather_kernel<2>, a); break;
+    default: e = cudaLaunchKernelEx(&cfg, evict_gather_kernel<1>, a); break;
+  }
   return e == cudaSuccess ? ATTN_OK : record_cuda_error(e, "attn_cache_evict copy launch");
 }
 

@@ -98,17 +98,14 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const __grid_cons
     }
     const int h0 = first + (units > 32 ? 0 : lane >> p.unit_log2);
     Vec<T, VP> x[kRopeUnroll], y[kRopeUnroll];
-    auto load = [&](int h) {
-#pragma unroll
-      for (int j = 0; j < kRopeUnroll; ++j) {
-        const int i = h + j * per_pass;
-        if (i >= last) continue;
-        const T* src = i < a.num_heads ? q + i * a.head_dim : k + (i - a.num_heads) * a.head_dim;
-        x[j] = *reinterpret_cast<const Vec<T, VP>*>(src + d0);
-        y[j] = *reinterpret_cast<const Vec<T, VP>*>(src + d1);
-      }
+    auto load = [&](int j, int i) {
+      if (i >= last) return;
+      const T* src = i < a.num_heads ? q + i * a.head_dim : k + (i - a.num_heads) * a.head_dim;
+      x[j] = *reinterpret_cast<const Vec<T, VP>*>(src + d0);
+      y[j] = *reinterpret_cast<const Vec<T, VP>*>(src + d1);
     };
-    load(h0);
+#pragma unroll
+    for (int j = 0; j < kRopeUnroll; ++j) load(j, h0 + j * per_pass);
     if (block == 0) {
       int pos;
       if (!position_of(a, t, pos)) return;  // the whole warp
@@ -124,7 +121,6 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const __grid_cons
 #pragma unroll
     for (int e = 0; e < VP; ++e) c[e] = u < turned ? cs[warp][u * VP + e] : make_float2(1.f, 0.f);
     for (int h = h0; h < last; h += kRopeUnroll * per_pass) {
-      if (h != h0) load(h);
 #pragma unroll
       for (int j = 0; j < kRopeUnroll; ++j) {
         const int i = h + j * per_pass;
@@ -143,6 +139,7 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const __grid_cons
         T* dst = i < a.num_heads ? qo + i * a.head_dim : ko + (i - a.num_heads) * a.head_dim;
         *reinterpret_cast<Vec<T, VP>*>(dst + d0) = x[j];
         *reinterpret_cast<Vec<T, VP>*>(dst + d1) = y[j];
+        load(j, i + kRopeUnroll * per_pass);  // the next unit takes its place
       }
     }
   }
