@@ -68,7 +68,7 @@ struct NewPages {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a, int team_log2) {
+__global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 2 ? 4 : 2) append_kernel(const AppendArgs a, int team_log2) {
   const CacheView& c = a.cache;
   const NewPages pages{a, blockIdx.x == 0 && blockIdx.y == 0};
   const UnitLine line(pages, c.batch, threadIdx.x & 31);
@@ -80,8 +80,6 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
   const int held = len - (a.cu[b + 1] - q0);  // tokens that are there already
   const int page_size = 1 << c.page_log2;
   const int i = (held >> c.page_log2) + pos - before;  // this CTA's page of the sequence
-  const int page = load_page(c, b, i);
-  if (page < 0) return;
   const int first = max(held - (i << c.page_log2), 0);  // slots [first, last) are new
   const int last = min(len - (i << c.page_log2), page_size);
   const int per_row = c.head_dim / kChunk;
@@ -92,8 +90,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
   const int h = on ? (values ? hv - c.heads : hv) : 0;
   const T* src = static_cast<const T*>(values ? a.v : a.k);
   const int64_t stride = values ? a.v_stride : a.k_stride;
-  uint8_t* codes = (values ? c.v_pages : c.k_pages) + ((int64_t(page) * c.heads + h) << c.page_log2) * c.head_dim;
-  float* scale = (values ? c.v_scale : c.k_scale) + int64_t(page) * c.heads + h;
+  const int number = __ldg(c.table + int64_t(b) * c.max_pages + i);  // needed only behind the loads
 
   Raw<T> x[kChunks];
   float amax = 0.f;
@@ -106,6 +103,12 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
     else
       x[j].zero();
   }
+  if (!in_pool(c, number)) {
+    atomicOr(c.status, kErrBadPage);
+    return;
+  }
+  uint8_t* codes = (values ? c.v_pages : c.k_pages) + ((int64_t(number) * c.heads + h) << c.page_log2) * c.head_dim;
+  float* scale = (values ? c.v_scale : c.k_scale) + int64_t(number) * c.heads + h;
 #pragma unroll
   for (int j = 0; j < kChunks; ++j) {
     float f[kChunk];

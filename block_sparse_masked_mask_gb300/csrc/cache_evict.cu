@@ -177,79 +177,104 @@ struct KeptPages {
   }
 };
 
-// N: 16-byte pieces per thread of a page's keys (and as many of its values)
+// N: 16-byte pieces per thread of a page's keys (and as many of its values).
+// A CTA takes destination pages in turn; the kept tokens' numbers are read two
+// pages ahead and the source pages' one, so that a page waits for its own codes only.
 template <int N>
 __global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const EvictArgs a) {
   __shared__ int src_page[2][128], src_slot[2][128];
   __shared__ int exps[2][2][128];
   __shared__ int top[2][2];
-  const int page_size = 1 << a.src.page_log2, D = a.src.head_dim, per_row = D / 16;
+  const int log2 = a.src.page_log2, page_size = 1 << log2, D = a.src.head_dim, per_row = D / 16;
   const int h = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
   const KeptPages pages{a};
   const UnitLine line(pages, a.src.batch, lane);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  int turn = 0;  // the shared arrays alternate, one barrier each
-  for (int pos = blockIdx.x; pos < line.total; pos += gridDim.x, turn ^= 1) {
+
+  // The page at a place of the line: its sequence, number, tokens (0: none), and the
+  // token that this thread looks up (-1: none).
+  struct Place {
+    int b, i, n, token;
+  };
+  auto place_at = [&](int pos) {
+    Place p{0, 0, 0, -1};
+    if (pos >= line.total) return p;
     int before;
-    const int b = line.find(pages, a.src.batch, lane, pos, before);
-    const int i = pos - before;
-    const int keep = min(a.lens[b], a.budgets[b]);
-    const int n = min(page_size, keep - (i << a.src.page_log2));  // tokens of this page
-    const int dst = __ldg(a.dst.table + int64_t(b) * a.dst.max_pages + i);
-    const bool fine = unsigned(dst) < unsigned(a.dst.num_pages);
-    if (!fine && tid == 0) {
-      atomicOr(a.src.status, kErrBadPage);
-      atomicOr(a.dst.status, kErrBadPage);
-    }
+    p.b = line.find(pages, a.src.batch, lane, pos, before);
+    p.i = pos - before;
+    p.n = min(page_size, min(a.lens[p.b], a.budgets[p.b]) - (p.i << log2));
+    if (tid < p.n) p.token = a.kept[(int64_t(p.b) * a.src.heads + h) * a.max_keep + (p.i << log2) + tid];
+    return p;
+  };
+  auto number_of = [&](const Place& p) {
+    return p.token < 0 ? 0 : __ldg(a.src.table + int64_t(p.b) * a.src.max_pages + (p.token >> log2));
+  };
+  int pos = blockIdx.x;
+  Place here = place_at(pos), next = place_at(pos + gridDim.x);
+  int number = number_of(here);
+  for (int turn = 0; pos < line.total; turn ^= 1) {  // the shared arrays alternate
+    const int dst = __ldg(a.dst.table + int64_t(here.b) * a.dst.max_pages + here.i);
     if (tid < 2) top[turn][tid] = -1000;
-    __syncthreads();  // (also: the pages before the last have been copied)
-    if (tid < n) {
-      const int j = a.kept[(int64_t(b) * a.src.heads + h) * a.max_keep + (i << a.src.page_log2) + tid];
-      const int page = load_page(a.src, b, j >> a.src.page_log2);
-      src_page[turn][tid] = page;
-      src_slot[turn][tid] = j & (page_size - 1);
-      if (page >= 0) {
-        const int64_t at = int64_t(page) * a.src.heads + h;
-        const int ek = exponent_of(a.src.k_scale[at]), ev = exponent_of(a.src.v_scale[at]);
-        exps[turn][0][tid] = ek;
-        exps[turn][1][tid] = ev;
-        atomicMax(&top[turn][0], ek);
-        atomicMax(&top[turn][1], ev);
-      }
+    if (tid < here.n) {
+      const bool fine = unsigned(number) < unsigned(a.src.num_pages);
+      if (!fine) atomicOr(a.src.status, kErrBadPage);
+      src_page[turn][tid] = fine ? number : -1;
+      src_slot[turn][tid] = here.token & (page_size - 1);
     }
     __syncthreads();
-    if (!fine) continue;
+    const bool fine = unsigned(dst) < unsigned(a.dst.num_pages);
     uint4 v[2][N];
 #pragma unroll
     for (int side = 0; side < 2; ++side)
 #pragma unroll
       for (int y = 0; y < N; ++y) {
         const int x = y * kGatherThreads + tid, slot = x / per_row, piece = x % per_row;
-        if (slot >= n || src_page[turn][slot] < 0) continue;
+        if (slot >= here.n || src_page[turn][slot] < 0) continue;
         v[side][y] = *reinterpret_cast<const uint4*>(
             (side ? a.src.v_pages : a.src.k_pages) +
-            (((int64_t(src_page[turn][slot]) * a.src.heads + h) << a.src.page_log2) + src_slot[turn][slot]) * D +
-            piece * 16);
+            (((int64_t(src_page[turn][slot]) * a.src.heads + h) << log2) + src_slot[turn][slot]) * D + piece * 16);
       }
+    if (tid < here.n && src_page[turn][tid] >= 0) {
+      const int64_t at = int64_t(number) * a.src.heads + h;
+      const int ek = exponent_of(a.src.k_scale[at]), ev = exponent_of(a.src.v_scale[at]);
+      exps[turn][0][tid] = ek;
+      exps[turn][1][tid] = ev;
+      atomicMax(&top[turn][0], ek);
+      atomicMax(&top[turn][1], ev);
+    }
+    const Place after = place_at(pos + 2 * gridDim.x);
+    const int number_next = number_of(next);
+    __syncthreads();
+    if (!fine) {
+      if (tid == 0) {
+        atomicOr(a.src.status, kErrBadPage);
+        atomicOr(a.dst.status, kErrBadPage);
+      }
+    } else {
 #pragma unroll
-    for (int side = 0; side < 2; ++side)
+      for (int side = 0; side < 2; ++side)
 #pragma unroll
-      for (int y = 0; y < N; ++y) {
-        const int x = y * kGatherThreads + tid, slot = x / per_row, piece = x % per_row;
-        if (slot >= n || src_page[turn][slot] < 0) continue;
-        uint4 w = v[side][y];
-        const int shift = top[turn][side] - exps[turn][side][slot];
-        if (shift > 0) {
-          w.x = rescale4(w.x, shift);
-          w.y = rescale4(w.y, shift);
-          w.z = rescale4(w.z, shift);
-          w.w = rescale4(w.w, shift);
+        for (int y = 0; y < N; ++y) {
+          const int x = y * kGatherThreads + tid, slot = x / per_row, piece = x % per_row;
+          if (slot >= here.n || src_page[turn][slot] < 0) continue;
+          uint4 w = v[side][y];
+          const int shift = top[turn][side] - exps[turn][side][slot];
+          if (shift > 0) {
+            w.x = rescale4(w.x, shift);
+            w.y = rescale4(w.y, shift);
+            w.z = rescale4(w.z, shift);
+            w.w = rescale4(w.w, shift);
+          }
+          *reinterpret_cast<uint4*>((side ? a.dst.v_pages : a.dst.k_pages) +
+                                    (((int64_t(dst) * a.dst.heads + h) << log2) + slot) * D + piece * 16) = w;
         }
-        *reinterpret_cast<uint4*>((side ? a.dst.v_pages : a.dst.k_pages) +
-                                  (((int64_t(dst) * a.dst.heads + h) << a.dst.page_log2) + slot) * D + piece * 16) = w;
-      }
-    if (tid < 2 && top[turn][tid] > -1000)
-      (tid ? a.dst.v_scale : a.dst.k_scale)[int64_t(dst) * a.dst.heads + h] = pow2f(max(-126, top[turn][tid]));
+      if (tid < 2 && top[turn][tid] > -1000)
+        (tid ? a.dst.v_scale : a.dst.k_scale)[int64_t(dst) * a.dst.heads + h] = pow2f(max(-126, top[turn][tid]));
+    }
+    pos += gridDim.x;
+    here = next;
+    next = after;
+    number = number_next;
   }
 }
 
