@@ -84,8 +84,8 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
   auto key_of = [&](int j) { return j < stage ? keys[j] : order_key(w[j]); };
 
   if (!all && want > 0) {
-#pragma unroll 4
-    for (int j = tid; j < min(others, stage); j += kSelectThreads) keys[j] = order_key(w[j]);
+#pragma unroll 8
+    for (int j = tid; j < min(others, stage); j += kSelectThreads) keys[j] = order_key(__ldg(w + j));
     uint32_t prefix = 0;
     int need = want;
     for (int pass = 0; pass < 3; ++pass) {
@@ -150,18 +150,25 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
   int place = sum_before(lane == 0 ? n_above + taken : 0, sums, unused);
   place = __shfl_sync(0xffffffffu, place, 0);
   const uint32_t lower = (1u << lane) - 1u;
-  for (int j = j0; j < j1; j += 32) {
-    uint32_t above, at;
-    classify(j + lane, above, at);
-    const bool first = (at >> lane & 1u) && tie + __popc(at & lower) < ties;
-    const uint32_t take = above | __ballot_sync(0xffffffffu, first);
-    if (take >> lane & 1u) {
-      const int to = place + __popc(take & lower);
-      kept[to] = j + lane;
-      out[to] = w[j + lane];
+  for (int j8 = j0; j8 < j1; j8 += 256) {
+    float x[8];  // weights, read together
+#pragma unroll
+    for (int u = 0; u < 8; ++u) x[u] = j8 + 32 * u + lane < j1 ? __ldg(w + j8 + 32 * u + lane) : 0.f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int j = j8 + 32 * u + lane;
+      uint32_t above, at;
+      classify(j, above, at);
+      const bool first = (at >> lane & 1u) && tie + __popc(at & lower) < ties;
+      const uint32_t take = above | __ballot_sync(0xffffffffu, first);
+      if (take >> lane & 1u) {
+        const int to = place + __popc(take & lower);
+        kept[to] = j;
+        out[to] = x[u];
+      }
+      place += __popc(take);
+      tie += __popc(at);
     }
-    place += __popc(take);
-    tie += __popc(at);
   }
   for (int j = keep + tid; j < a.max_keep; j += kSelectThreads) kept[j] = -1;
   for (int64_t j = keep + tid; j < a.new_stride; j += kSelectThreads) out[j] = 0.f;
@@ -182,9 +189,11 @@ struct KeptPages {
 // pages ahead and the source pages' one, so that a page waits for its own codes only.
 template <int N>
 __global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const EvictArgs a) {
+  __shared__ uint4 moved[2 * N * kGatherThreads];  // each thread's own pieces
   __shared__ int src_page[2][128], src_slot[2][128];
   __shared__ int exps[2][2][128];
   __shared__ int top[2][2];
+  const uint32_t codes = uint32_t(__cvta_generic_to_shared(moved + threadIdx.x));
   const int log2 = a.src.page_log2, page_size = 1 << log2, D = a.src.head_dim, per_row = D / 16;
   const int h = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
   const KeptPages pages{a};
@@ -223,17 +232,18 @@ __global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const Evic
     }
     __syncthreads();
     const bool fine = unsigned(dst) < unsigned(a.dst.num_pages);
-    uint4 v[2][N];
 #pragma unroll
     for (int side = 0; side < 2; ++side)
 #pragma unroll
       for (int y = 0; y < N; ++y) {
         const int x = y * kGatherThreads + tid, slot = x / per_row, piece = x % per_row;
         if (slot >= here.n || src_page[turn][slot] < 0) continue;
-        v[side][y] = *reinterpret_cast<const uint4*>(
-            (side ? a.src.v_pages : a.src.k_pages) +
-            (((int64_t(src_page[turn][slot]) * a.src.heads + h) << log2) + src_slot[turn][slot]) * D + piece * 16);
+        copy16_async(codes + (side * N + y) * kGatherThreads * 16,
+                     (side ? a.src.v_pages : a.src.k_pages) +
+                         (((int64_t(src_page[turn][slot]) * a.src.heads + h) << log2) + src_slot[turn][slot]) * D + piece * 16,
+                     true);
       }
+    asm volatile("cp.async.commit_group;" ::: "memory");
     if (tid < here.n && src_page[turn][tid] >= 0) {
       const int64_t at = int64_t(number) * a.src.heads + h;
       const int ek = exponent_of(a.src.k_scale[at]), ev = exponent_of(a.src.v_scale[at]);
@@ -244,6 +254,7 @@ __global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const Evic
     }
     const Place after = place_at(pos + 2 * gridDim.x);
     const int number_next = number_of(next);
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
     if (!fine) {
       if (tid == 0) {
@@ -257,7 +268,7 @@ __global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const Evic
         for (int y = 0; y < N; ++y) {
           const int x = y * kGatherThreads + tid, slot = x / per_row, piece = x % per_row;
           if (slot >= here.n || src_page[turn][slot] < 0) continue;
-          uint4 w = v[side][y];
+          uint4 w = moved[((side * N + y) * kGatherThreads + tid)];
           const int shift = top[turn][side] - exps[turn][side][slot];
           if (shift > 0) {
             w.x = rescale4(w.x, shift);

@@ -127,6 +127,12 @@ struct UnitLine {
   }
 };
 
+// 16 bytes from global to shared memory, or zeros.
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, bool on) {
+  const int n = on ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+
 // Sixteen tokens' codes in shared memory, rows of D bytes as they lie in the page.
 // They are copied 512 consecutive bytes per instruction, lane by lane, and read
 // by the lanes that use them, so a warp meets at a barrier of its own
@@ -150,10 +156,7 @@ struct GroupTile {
 #pragma unroll
     for (int j = 0; j < BYTES / 512; ++j) {
       const int at = j * 512 + lane * 16, row = at / D, unit = at % D / 16;
-      const int n = row < left ? 16 : 0;
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + row * D + ((unit ^ turn<VALUES>(row)) << 4)),
-                   "l"(src + at), "r"(n)
-                   : "memory");
+      copy16_async(dst + row * D + ((unit ^ turn<VALUES>(row)) << 4), src + at, row < left);
     }
   }
   // The D / 8 bytes at `at` of a row, as words.
