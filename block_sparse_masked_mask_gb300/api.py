@@ -354,6 +354,8 @@ class _Launch:
 
 
 _Tensor = torch.Tensor
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_ROW_DTYPES = tuple(DTYPES)
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
@@ -372,13 +374,13 @@ def _fits(t, dtype, shape, index: int) -> bool:
             and t.is_contiguous())
 
 
-def _need_rows(t, name: str, where: str, dtypes, device=None) -> int:
+def _need_rows(t, name: str, where: str, dtypes, index: int = -1) -> int:
     """[tokens, heads, dim] with dense heads, tokens any distance apart (a slice
     of a wider projection); returns that distance in elements."""
     if not isinstance(t, _Tensor) or not t.is_cuda:
         raise AttnError(1, f"{where}: {name} must be a CUDA tensor")
-    if device is not None and t.get_device() != device.index:
-        raise AttnError(1, f"{where}: {name} is on {t.device}, expected {device}")
+    if index >= 0 and t.get_device() != index:
+        raise AttnError(1, f"{where}: {name} is on {t.device}, expected cuda:{index}")
     if t.dtype not in dtypes:
         raise AttnError(1, f"{where}: {name} has dtype {t.dtype}, expected one of {dtypes}")
     if t.dim() != 3:
@@ -438,54 +440,56 @@ def attn_rope(q: torch.Tensor, k: Optional[torch.Tensor], plan: RopePlan,
     gives those of q and k.  bf16 or fp32; the tokens of q and k may be apart
     (slices of one projection).  ``q_out=q`` rotates in place."""
     where = "attn_rope"
-    qs = _need_rows(q, "q", where, tuple(DTYPES))
+    qs = _need_rows(q, "q", where, _ROW_DTYPES)
     T, H, D = q.shape
-    dt, dev = (q.dtype,), q.device
+    dtype, dev = q.dtype, q.device
+    index = dev.index
     ks = kos = Hk = 0
     if k is not None:
-        ks = _need_rows(k, "k", where, dt, dev)
-        if k.shape[0] != T or k.shape[2] != D:
+        ks = _need_rows(k, "k", where, (dtype,), index)
+        n, Hk, d = k.shape
+        if n != T or d != D:
             raise AttnError(1, f"{where}: k has shape {tuple(k.shape)}, expected [{T}, heads, {D}]")
-        Hk = k.shape[1]
     elif k_out is not None:
         raise AttnError(1, f"{where}: k_out without k")
     if not isinstance(plan, RopePlan):
         raise AttnError(1, f"{where}: plan must come from attn_rope_plan")
     batch = 0
     if positions is not None:
-        if not _fits(positions, torch.int32, (T,), dev.index):
-            _need(positions, "positions", where, (torch.int32,), (T,), dev)
+        if cu_seqlens is not None or seq_lens is not None:
+            raise AttnError(1, f"{where}: positions, or cu_seqlens and seq_lens, not both")
+        if not _fits(positions, _I32, (T,), index):
+            _need(positions, "positions", where, (_I32,), (T,), dev)
     elif cu_seqlens is None:
         raise AttnError(1, f"{where}: positions or cu_seqlens is required")
     else:
-        if not (isinstance(cu_seqlens, torch.Tensor) and _fits(cu_seqlens, torch.int32, cu_seqlens.shape, dev.index)):
-            _need(cu_seqlens, "cu_seqlens", where, (torch.int32,), device=dev)
+        if not (isinstance(cu_seqlens, _Tensor) and _fits(cu_seqlens, _I32, cu_seqlens.shape, index)):
+            _need(cu_seqlens, "cu_seqlens", where, (_I32,), device=dev)
         batch = cu_seqlens.numel() - 1
-        if seq_lens is not None and not _fits(seq_lens, torch.int32, (batch,), dev.index):
-            _need(seq_lens, "seq_lens", where, (torch.int32,), (batch,), dev)
+        if seq_lens is not None and not _fits(seq_lens, _I32, (batch,), index):
+            _need(seq_lens, "seq_lens", where, (_I32,), (batch,), dev)
     at = _elsewhere(dev, stream)
-    s = _raw_stream(dev.index) if at is None else at.__enter__()
+    s = _raw_stream(index) if at is None else at.__enter__()
     try:
         if q_out is None:
-            q_out, qos = torch.empty((T, H, D), dtype=q.dtype, device=dev), H * D
+            q_out, qos = torch.empty((T, H, D), dtype=dtype, device=dev), H * D
         else:
-            qos = _need_rows(q_out, "q_out", where, dt, dev)
+            qos = _need_rows(q_out, "q_out", where, (dtype,), index)
             if q_out.shape != q.shape:
                 raise AttnError(1, f"{where}: q_out has shape {tuple(q_out.shape)}, expected {tuple(q.shape)}")
         if k is not None:
             if k_out is None:
-                k_out, kos = torch.empty((T, Hk, D), dtype=q.dtype, device=dev), Hk * D
+                k_out, kos = torch.empty((T, Hk, D), dtype=dtype, device=dev), Hk * D
             else:
-                kos = _need_rows(k_out, "k_out", where, dt, dev)
+                kos = _need_rows(k_out, "k_out", where, (dtype,), index)
                 if k_out.shape != k.shape:
                     raise AttnError(1, f"{where}: k_out has shape {tuple(k_out.shape)}, expected {tuple(k.shape)}")
         _check(_native.lib().attn_rope(
             q.data_ptr(), q_out.data_ptr(), qs, qos, H, k.data_ptr() if Hk else None,
-            k_out.data_ptr() if Hk else None, ks, kos, Hk, DTYPES[q.dtype], T, D,
+            k_out.data_ptr() if Hk else None, ks, kos, Hk, DTYPES[dtype], T, D,
             None if positions is None else positions.data_ptr(),
-            None if positions is not None else cu_seqlens.data_ptr(),
-            None if positions is not None or seq_lens is None else seq_lens.data_ptr(), batch,
-            plan._ref, int(bool(inverse)), s), where)
+            None if cu_seqlens is None else cu_seqlens.data_ptr(),
+            None if seq_lens is None else seq_lens.data_ptr(), batch, plan._ref, 1 if inverse else 0, s), where)
     finally:
         if at is not None:
             at.__exit__()
@@ -552,8 +556,8 @@ def _need_cache(cache, where: str) -> KVCache:
 def _need_seqs(cache: KVCache, cu_seqlens, seq_lens, where: str) -> None:
     if seq_lens is None or cu_seqlens is None:
         raise AttnError(1, f"{where}: cu_seqlens and seq_lens are required")
-    if not (_fits(cu_seqlens, torch.int32, (cache.batch + 1,), cache.index)
-            and _fits(seq_lens, torch.int32, (cache.batch,), cache.index)):
+    if not (_fits(cu_seqlens, _I32, (cache.batch + 1,), cache.index)
+            and _fits(seq_lens, _I32, (cache.batch,), cache.index)):
         _need(cu_seqlens, "cu_seqlens", where, (torch.int32,), (cache.batch + 1,), cache.device)
         _need(seq_lens, "seq_lens", where, (torch.int32,), (cache.batch,), cache.device)
 
@@ -567,18 +571,19 @@ def attn_cache_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, cu_seqle
     belong to the sequence alone."""
     where = "attn_cache_append"
     _need_cache(cache, where)
-    ks = _need_rows(k, "k", where, tuple(DTYPES), cache.device)
-    vs = _need_rows(v, "v", where, (k.dtype,), cache.device)
-    if k.shape != v.shape or tuple(k.shape[1:]) != (cache.num_kv_heads, cache.head_dim):
+    ks = _need_rows(k, "k", where, _ROW_DTYPES, cache.index)
+    vs = _need_rows(v, "v", where, (k.dtype,), cache.index)
+    T, h, d = k.shape
+    if k.shape != v.shape or h != cache.num_kv_heads or d != cache.head_dim:
         raise AttnError(1, f"{where}: k and v must be [tokens, {cache.num_kv_heads}, {cache.head_dim}], got "
                            f"{tuple(k.shape)} and {tuple(v.shape)}")
     _need_seqs(cache, cu_seqlens, seq_lens, where)
     at = _elsewhere(cache.device, stream)
-    s = _raw_stream(cache.device.index) if at is None else at.__enter__()
+    s = _raw_stream(cache.index) if at is None else at.__enter__()
     try:
         _check(_native.lib().attn_cache_append(
-            k.data_ptr(), v.data_ptr(), ks, vs, DTYPES[k.dtype], k.shape[0], cu_seqlens.data_ptr(),
-            seq_lens.data_ptr(), int(max_new), cache._ref, s), where)
+            k.data_ptr(), v.data_ptr(), ks, vs, DTYPES[k.dtype], T, cu_seqlens.data_ptr(),
+            seq_lens.data_ptr(), max_new, cache._ref, s), where)
     finally:
         if at is not None:
             at.__exit__()
@@ -588,14 +593,15 @@ def _need_queries(q, cache, where: str):
     _need_cache(cache, where)
     if q is None:
         raise AttnError(1, f"{where}: q is required")
-    if not (isinstance(q, torch.Tensor) and _fits(q, torch.bfloat16, q.shape, cache.index)):
-        _need(q, "q", where, tuple(DTYPES), device=cache.device)
-    if q.dtype != torch.bfloat16:
-        raise AttnError(2, f"{where}: dtype must be bfloat16")
-    if q.dim() != 3 or q.shape[2] != cache.head_dim or q.shape[1] % cache.num_kv_heads:
-        raise AttnError(1, f"{where}: q has shape {tuple(q.shape)}, expected [tokens, a multiple of "
+    if not (isinstance(q, _Tensor) and _fits(q, _BF16, q.shape, cache.index)):
+        _need(q, "q", where, _ROW_DTYPES, device=cache.device)
+        if q.dtype != _BF16:
+            raise AttnError(2, f"{where}: dtype must be bfloat16")
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != cache.head_dim or shape[1] % cache.num_kv_heads:
+        raise AttnError(1, f"{where}: q has shape {tuple(shape)}, expected [tokens, a multiple of "
                            f"{cache.num_kv_heads}, {cache.head_dim}]")
-    return q.shape
+    return shape
 
 
 def attn_cache_fwd_workspace_size(cache: KVCache, total_tokens: int, num_heads: int, max_new: int,
@@ -625,14 +631,14 @@ def attn_cache_fwd(q: torch.Tensor, cache: KVCache, cu_seqlens: torch.Tensor, se
     where = "attn_cache_fwd"
     T, H, D = _need_queries(q, cache, where)
     dev = cache.device
-    if out is not None and not _fits(out, q.dtype, q.shape, cache.index):
+    if out is not None and not _fits(out, _BF16, q.shape, cache.index):
         _need(out, "out", where, (q.dtype,), q.shape, dev)
-    if lse is not None and not _fits(lse, torch.float32, (H, T), cache.index):
+    if lse is not None and not _fits(lse, _F32, (H, T), cache.index):
         _need(lse, "lse", where, (torch.float32,), (H, T), dev)
     _need(workspace, "workspace", where, device=dev)
     _need_seqs(cache, cu_seqlens, seq_lens, where)
     at = _elsewhere(dev, stream)
-    s = _raw_stream(dev.index) if at is None else at.__enter__()
+    s = _raw_stream(cache.index) if at is None else at.__enter__()
     try:
         if out is None:
             out = torch.empty_like(q)
@@ -685,7 +691,7 @@ def attn_cache_weights(q: torch.Tensor, lse: torch.Tensor, cache: KVCache, cu_se
         if t is not None and not _fits(t, torch.float32, shape, cache.index):
             _need(t, name, where, (torch.float32,), shape, dev)
     at = _elsewhere(dev, stream)
-    s = _raw_stream(dev.index) if at is None else at.__enter__()
+    s = _raw_stream(cache.index) if at is None else at.__enter__()
     try:
         if out is None:
             out = torch.zeros(shape, dtype=torch.float32, device=dev)
@@ -697,6 +703,15 @@ def attn_cache_weights(q: torch.Tensor, lse: torch.Tensor, cache: KVCache, cu_se
         if at is not None:
             at.__exit__()
     return out
+
+
+def _need_weights(t, name: str, cache: KVCache, where: str) -> None:
+    """fp32 [batch, heads, width], any width."""
+    B, H = cache.batch, cache.num_kv_heads
+    if not (isinstance(t, _Tensor) and t.dim() == 3 and _fits(t, _F32, (B, H, t.shape[2]), cache.index)):
+        _need(t, name, where, (_F32,), device=cache.device)
+        if t.dim() != 3 or tuple(t.shape[:2]) != (B, H):
+            raise AttnError(1, f"{where}: {name} must be [{B}, {H}, width], got {tuple(t.shape)}")
 
 
 def attn_cache_evict(weights: torch.Tensor, cache: KVCache, dst: KVCache, seq_lens: torch.Tensor,
@@ -719,25 +734,22 @@ def attn_cache_evict(weights: torch.Tensor, cache: KVCache, dst: KVCache, seq_le
     if dst.device != dev:
         raise AttnError(1, f"{where}: dst is on {dst.device}, expected {dev}")
     max_keep = int(max_keep)
-    for name, t in (("weights", weights), ("seq_lens", seq_lens), ("budgets", budgets)):
-        if t is None:
-            raise AttnError(1, f"{where}: {name} is required")
-    for name, t, dtype, shape in (("seq_lens", seq_lens, torch.int32, (B,)), ("budgets", budgets, torch.int32, (B,)),
-                                  ("kept", kept, torch.int32, (B, H, max_keep)),
-                                  ("new_lens", new_lens, torch.int32, (B,))):
-        if t is not None and not _fits(t, dtype, shape, cache.index):
-            _need(t, name, where, (dtype,), shape, dev)
-    for name, t in (("weights", weights), ("new_weights", new_weights)):
-        if t is None:
-            continue
-        if not (isinstance(t, torch.Tensor) and _fits(t, torch.float32, t.shape, cache.index)):
-            _need(t, name, where, (torch.float32,), device=dev)
-        if t.dim() != 3 or t.shape[0] != B or t.shape[1] != H:
-            raise AttnError(1, f"{where}: {name} must be [{B}, {H}, width], got {tuple(t.shape)}")
+    if weights is None or seq_lens is None or budgets is None:
+        raise AttnError(1, f"{where}: weights, seq_lens and budgets are required")
+    index = cache.index
+    if not (_fits(seq_lens, _I32, (B,), index) and _fits(budgets, _I32, (B,), index)
+            and (kept is None or _fits(kept, _I32, (B, H, max_keep), index))
+            and (new_lens is None or _fits(new_lens, _I32, (B,), index))):
+        for name, t, shape in (("seq_lens", seq_lens, (B,)), ("budgets", budgets, (B,)),
+                               ("kept", kept, (B, H, max_keep)), ("new_lens", new_lens, (B,))):
+            _need(t, name, where, (_I32,), shape, dev)
+    _need_weights(weights, "weights", cache, where)
+    if new_weights is not None:
+        _need_weights(new_weights, "new_weights", cache, where)
     if max_keep < 0:
         raise AttnError(1, f"{where}: max_keep is negative")
     at = _elsewhere(dev, stream)
-    s = _raw_stream(dev.index) if at is None else at.__enter__()
+    s = _raw_stream(cache.index) if at is None else at.__enter__()
     try:
         if kept is None:
             kept = torch.empty((B, H, max_keep), dtype=torch.int32, device=dev)
@@ -759,7 +771,7 @@ def attn_cache_get_status(cache: KVCache, stream=None) -> int:
     """Synchronise, then return and clear the cache's device status code."""
     _need_cache(cache, "attn_cache_get_status")
     at = _elsewhere(cache.device, stream)
-    s = _raw_stream(cache.device.index) if at is None else at.__enter__()
+    s = _raw_stream(cache.index) if at is None else at.__enter__()
     try:
         return int(_native.lib().attn_cache_get_status(cache._ref, s))
     finally:
