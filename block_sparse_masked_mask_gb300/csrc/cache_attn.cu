@@ -78,14 +78,21 @@ __global__ void __launch_bounds__(kAttnThreads, 3) cache_attn_kernel(const Cache
   const CacheView& c = a.cache;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const AttnUnits units{p, blockIdx.x == 0};
-  const UnitLine line(units, c.batch, lane);
-  const int piece = share(line.total, p.ctas);
-  int pos = blockIdx.x * piece;
-  const int stop = min(pos + piece, line.total);
+  int b, pos, stop, before = 0;
+  if (p.whole) {
+    b = blockIdx.x / c.heads;
+    const int U = AttnUnits{p, blockIdx.x % c.heads == 0}(b) / c.heads;
+    pos = (blockIdx.x % c.heads) * U;
+    stop = pos + U;
+  } else {
+    const AttnUnits units{p, blockIdx.x == 0};
+    const UnitLine line(units, c.batch, lane);
+    const int piece = share(line.total, p.ctas);
+    pos = blockIdx.x * piece;
+    stop = min(pos + piece, line.total);
+    if (pos < stop) b = line.find(units, c.batch, lane, pos, before);
+  }
   if (pos >= stop) return;
-  int before;
-  int b = line.find(units, c.batch, lane, pos, before);
 
   uint8_t* queue = smem + warp * kStages * C::STAGE;
   const uint32_t queue_addr = ptx::smem_addr(queue);
@@ -439,9 +446,19 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_many_kernel(const 
   join_row<D, 1>(p, max(1, (limit + p.chunk - 1) / p.chunk), at, token, head, 0, lane, nullptr);
 }
 
+// Whether a CTA takes a (sequence, head) whole, so that nothing is joined: where
+// the sequences are short, and up to 1024 tokens where all of them fill the GPU
+// about once.  Measured, split / whole, D = 128: 8 heads of one sequence, 512
+// tokens 8.4 / 7.6 us, 1024 8.8 / 11.0; of 16 sequences, 512 13.7 / 7.9, 1024 16.3 /
+// 12.2, 2048 21.7 / 19.7; of 64 sequences, 512 22.6 / 20.5, 1024 31.5 / 34.3.
+bool take_whole(const CacheQueryArgs& a) {
+  const int64_t items = int64_t(a.cache.batch) * a.cache.heads;
+  return a.max_seqlen <= 512 || (a.max_seqlen <= 1024 && items >= 64 && items <= 456);
+}
+
 // Which kernel, and its cut.  More than 16 rows of a key / value head go to the
-// tcgen05 kernel (cache_chunk.cu), which reads the cache once for 256; its
-// chunks of 1024 to 4096 tokens fill the GPU about twice over, one CTA per SM.
+// tcgen05 kernel (cache_chunk.cu), which reads the cache once for 256; its chunks
+// fill the GPU once, one CTA per SM, with 256 to 4096 tokens each.
 // The number of SMs only sizes the work, and the size query runs without a
 // device, so it is that of the GPU this library is built for.
 void plan(CacheAttnParams* p) {
@@ -450,22 +467,22 @@ void plan(CacheAttnParams* p) {
   p->G = a.num_heads / a.cache.heads;
   const int64_t rows = int64_t(a.max_new) * p->G;
   p->many = rows > kFewRows;
-  p->ctas = 3 * kSms;  // resident at once
+  p->whole = take_whole(a);
+  p->ctas = p->whole ? a.cache.batch * a.cache.heads : 3 * kSms;  // (three per SM are resident at once)
   p->row_tiles = int((rows + kManyRows - 1) / kManyRows);
   const int64_t items = int64_t(p->row_tiles) * a.cache.heads * a.cache.batch;
-  const int64_t want = items > 0 ? (2 * kSms + items - 1) / items : 1;
-  int64_t chunk = (int64_t(a.max_seqlen) + want - 1) / want;
+  int64_t chunk = (int64_t(a.max_seqlen) * items + kSms - 1) / kSms;
   chunk = (chunk + kTile - 1) / kTile * kTile;
-  chunk = chunk < 1024 ? 1024 : (chunk > 4096 ? 4096 : chunk);
+  chunk = chunk < 256 ? 256 : (chunk > 4096 ? 4096 : chunk);
   p->chunk = int(chunk);
   p->splits = int((int64_t(a.max_seqlen) + chunk - 1) / chunk);
   if (p->splits < 1) p->splits = 1;
 }
 
-// Rows of partial results (few: a head of one unit lies in one CTA's piece).
+// Rows of partial results.
 uint64_t partial_rows(const CacheAttnParams& p) {
   if (p.many) return p.splits == 1 ? 0 : uint64_t(p.splits) * uint64_t(p.a.total_tokens) * uint64_t(p.a.num_heads);
-  return p.a.max_seqlen <= kUnit ? 0 : 2 * uint64_t(p.ctas) * uint64_t(p.a.max_new) * uint64_t(p.G);
+  return p.whole ? 0 : 2 * uint64_t(p.ctas) * uint64_t(p.a.max_new) * uint64_t(p.G);
 }
 
 template <int D>
