@@ -428,22 +428,43 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_few_kernel(const C
   join_row<D, W>(p, c1 - c0 + 1, at, r.q0 + i / a.num_heads, head, w, lane, shared);
 }
 
-// Many rows: a warp per row, over the chunks that the row's tile had.
+// Many rows: a CTA per 32 rows of an item, a warp per row.
 template <int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) cache_join_many_kernel(const CacheAttnParams p) {
+__global__ void __launch_bounds__(32 * kJoinWarps) cache_join_many_kernel(const CacheAttnParams p, int row_tiles) {
   const CacheQueryArgs& a = p.a;
-  const int b = blockIdx.y, lane = threadIdx.x & 31;
-  const int i = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+  const int b = blockIdx.y, h = blockIdx.x / row_tiles, tile = blockIdx.x % row_tiles;
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   SeqRows r;
   const bool good = load_rows(a.cu, a.lens, b, a.total_tokens, a.max_new, a.max_seqlen, a.cache.status, r, false);
+  const int U = good ? tile_units(r, p.G, a.causal, tile) : 0;
+  int piece = 1, first = 0;
+  if (U > 0) {
+    const ManyUnits units{p, false};
+    int all = 0;
+    for (int s = lane; s < a.cache.batch; s += 32) {
+      const int n = units(s);
+      all += n;
+      first += s < b ? n : 0;
+    }
+    for (int t = lane; t < tile; t += 32) first += tile_units(r, p.G, a.causal, t);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      all += __shfl_xor_sync(0xffffffffu, all, o);
+      first += __shfl_xor_sync(0xffffffffu, first, o);
+    }
+    first += h * item_units(r, p.G, a.causal);
+    piece = share_many(all, p.ctas);
+  }
+  const int c0 = first / piece, c1 = (first + U - 1) / piece;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!good || i >= r.n * a.num_heads) return;
-  const int head = i % a.num_heads, row = (i / a.num_heads) * p.G + head % p.G;
-  const int last = min(row / kManyRows * kManyRows + kManyRows - 1, r.n * p.G - 1);
-  const int limit = visible_tokens(r, p.G, last, a.causal);
-  const int64_t token = r.q0 + i / a.num_heads, step = int64_t(a.total_tokens) * a.num_heads;
-  auto at = [&](int j) { return j * step + token * a.num_heads + head; };
-  join_row<D, 1>(p, max(1, (limit + p.chunk - 1) / p.chunk), at, token, head, 0, lane, nullptr);
+  if (U == 0 || c0 == c1) return;  // finished by its CTA
+  const int per_slot = min(kManyRows, a.max_new * p.G);
+  const int rows = min(kManyRows, r.n * p.G - tile * kManyRows), x0 = blockIdx.z * 32;
+  for (int x = x0 + w; x < min(rows, x0 + 32); x += kJoinWarps) {
+    const int row = tile * kManyRows + x;
+    auto at = [&](int j) { return int64_t(2 * (c0 + j) + (j == 0 ? 1 : 0)) * per_slot + x; };
+    join_row<D, 1>(p, c1 - c0 + 1, at, r.q0 + row / p.G, h * p.G + row % p.G, 0, lane, nullptr);
+  }
 }
 
 // Whether a CTA takes a (sequence, head) whole, so that nothing is joined: where
@@ -456,33 +477,25 @@ bool take_whole(const CacheQueryArgs& a) {
   return a.max_seqlen <= 512 || (a.max_seqlen <= 1024 && items >= 64 && items <= 456);
 }
 
-// Which kernel, and its cut.  More than 16 rows of a key / value head go to the
-// tcgen05 kernel (cache_chunk.cu), which reads the cache once for 256; its chunks
-// fill the GPU once, one CTA per SM, with 256 to 4096 tokens each.
-// The number of SMs only sizes the work, and the size query runs without a
-// device, so it is that of the GPU this library is built for.
+// Which kernel, and its CTAs: more than 16 rows of a key / value head go to the
+// tcgen05 kernel (cache_chunk.cu), which reads the cache once for 256, one CTA per
+// SM; else three per SM are resident at once.  The number of SMs only sizes the
+// work, and the size query runs without a device, so it is that of the GPU this
+// library is built for.
 void plan(CacheAttnParams* p) {
   constexpr int kSms = 152;
   const CacheQueryArgs& a = p->a;
   p->G = a.num_heads / a.cache.heads;
-  const int64_t rows = int64_t(a.max_new) * p->G;
-  p->many = rows > kFewRows;
-  p->whole = take_whole(a);
-  p->ctas = p->whole ? a.cache.batch * a.cache.heads : 3 * kSms;  // (three per SM are resident at once)
-  p->row_tiles = int((rows + kManyRows - 1) / kManyRows);
-  const int64_t items = int64_t(p->row_tiles) * a.cache.heads * a.cache.batch;
-  int64_t chunk = (int64_t(a.max_seqlen) * items + kSms - 1) / kSms;
-  chunk = (chunk + kTile - 1) / kTile * kTile;
-  chunk = chunk < 256 ? 256 : (chunk > 4096 ? 4096 : chunk);
-  p->chunk = int(chunk);
-  p->splits = int((int64_t(a.max_seqlen) + chunk - 1) / chunk);
-  if (p->splits < 1) p->splits = 1;
+  p->many = int64_t(a.max_new) * p->G > kFewRows;
+  p->whole = !p->many && take_whole(a);
+  p->ctas = p->many ? kSms : p->whole ? a.cache.batch * a.cache.heads : 3 * kSms;
 }
 
-// Rows of partial results.
+// Rows of partial results.  (Many rows: an item of at most 128 tokens is one unit.)
 uint64_t partial_rows(const CacheAttnParams& p) {
-  if (p.many) return p.splits == 1 ? 0 : uint64_t(p.splits) * uint64_t(p.a.total_tokens) * uint64_t(p.a.num_heads);
-  return p.whole ? 0 : 2 * uint64_t(p.ctas) * uint64_t(p.a.max_new) * uint64_t(p.G);
+  if (p.whole || (p.many && p.a.max_seqlen <= kTile)) return 0;
+  const int64_t rows = int64_t(p.a.max_new) * p.G;
+  return 2 * uint64_t(p.ctas) * uint64_t(rows < kManyRows ? rows : kManyRows);
 }
 
 template <int D>
@@ -498,15 +511,7 @@ cudaError_t launch_few(const CacheAttnParams& p, cudaStream_t s) {
 // The joining kernel is launched early and waits for the first one's end.
 template <int D>
 cudaError_t launch_join(const CacheAttnParams& p, cudaStream_t s) {
-  const int64_t rows = int64_t(p.a.max_new) * p.a.num_heads;
-  // A (sequence, head) meets about ctas / (their number) CTAs; where those are
-  // many, a CTA joins each row (one request of 131072 tokens and one head: 128
-  // us with a warp per row, 25 us), else a warp does (64 requests of 8 heads: the
-  // join takes 12 us with a CTA per row, 5 us with a warp).
-  const bool wide = !p.many && int64_t(p.ctas) > 8 * int64_t(p.a.cache.batch) * p.a.cache.heads;
-  const int per_cta = wide ? 1 : kJoinWarps;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned((rows + per_cta - 1) / per_cta), unsigned(p.a.cache.batch));
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -514,8 +519,20 @@ cudaError_t launch_join(const CacheAttnParams& p, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, p.many ? cache_join_many_kernel<D>
-                                         : wide ? cache_join_few_kernel<D, kJoinWarps> : cache_join_few_kernel<D, 1>, p);
+  if (p.many) {
+    const int row_tiles = int((int64_t(p.a.max_new) * p.G + kManyRows - 1) / kManyRows);
+    cfg.gridDim = dim3(unsigned(row_tiles) * unsigned(p.a.cache.heads), unsigned(p.a.cache.batch), kManyRows / 32);
+    return cudaLaunchKernelEx(&cfg, cache_join_many_kernel<D>, p, row_tiles);
+  }
+  // A (sequence, head) meets about ctas / (their number) CTAs; where those are
+  // many, a CTA joins each row (one request of 131072 tokens and one head: 128
+  // us with a warp per row, 25 us), else a warp does (64 requests of 8 heads: the
+  // join takes 12 us with a CTA per row, 7 us with a warp).
+  const int64_t rows = int64_t(p.a.max_new) * p.a.num_heads;
+  const bool wide = int64_t(p.ctas) > 8 * int64_t(p.a.cache.batch) * p.a.cache.heads;
+  const int per_cta = wide ? 1 : kJoinWarps;
+  cfg.gridDim = dim3(unsigned((rows + per_cta - 1) / per_cta), unsigned(p.a.cache.batch));
+  return cudaLaunchKernelEx(&cfg, wide ? cache_join_few_kernel<D, kJoinWarps> : cache_join_few_kernel<D, 1>, p);
 }
 
 }  // namespace

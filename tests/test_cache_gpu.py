@@ -231,6 +231,25 @@ def test_long_chunks(n):
     check_attend(p, randn(3 * n, 8, 128, seed=n), cu, lens)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dim,page_size,heads,group", [(64, 16, 4, 4), (128, 64, 5, 3)])
+def test_many_items_of_many_rows(dim, page_size, heads, group, causal):
+    """Several tiles of rows per sequence, tiles of one and of two halves in turn,
+    more of them than there are SMs, sequences with no new token or no token between."""
+    n = [(37 * i) % 150 if i % 7 else 0 for i in range(45)]
+    lens = [x + (53 * i) % 700 if i % 11 else x // 2 for i, x in enumerate(n)]
+    p = filled(lens, heads, dim, page_size, seed=23)
+    cu = cu_of(n)
+    check_attend(p, randn(int(cu[-1]), heads * group, dim, seed=3), cu, lens, causal)
+
+
+def test_one_long_item_over_many_ctas():
+    """Few rows above 16 over a long sequence, and a tile and a half of rows."""
+    for rows in (20, 390):
+        p = filled([9001], 1, 64, 64, seed=rows)
+        check_attend(p, randn(rows, 1, 64, seed=rows), cu_of([rows]), [9001])
+
+
 def test_large_scores_and_scales():
     """Scores in the hundreds (a one-hot softmax), a given scale, tiny and huge queries."""
     lens = [333, 80]
