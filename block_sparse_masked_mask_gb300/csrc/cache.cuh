@@ -88,7 +88,7 @@ struct CacheAttnParams {
   // Results before the division, and (running maximum, sum), of the segments that
   // are not a whole item: of CTA c, 2 c one that goes on one of the CTA before,
   // 2 c + 1 one that goes on in the next; min(max_new * G, kManyRows) rows each.
-  float* part_o;   // rows of head_dim
+  float* part_o;   // few: rows of head_dim; many: four dimensions of all rows, then the next four
   float2* part_m;
 };
 constexpr int kFewRows = 16, kManyRows = 256;

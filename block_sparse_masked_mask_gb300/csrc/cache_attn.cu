@@ -428,15 +428,16 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_few_kernel(const C
   join_row<D, W>(p, c1 - c0 + 1, at, r.q0 + i / a.num_heads, head, w, lane, shared);
 }
 
-// Many rows: a CTA per 32 rows of an item, a warp per row.
+// Many rows: a CTA per 32 rows of an item; lanes are rows, warps share the dimensions.
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_many_kernel(const CacheAttnParams p, int row_tiles) {
   const CacheQueryArgs& a = p.a;
   const int b = blockIdx.y, h = blockIdx.x / row_tiles, tile = blockIdx.x % row_tiles;
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int x = blockIdx.z * 32 + lane, row = tile * kManyRows + x;
   SeqRows r;
   const bool good = load_rows(a.cu, a.lens, b, a.total_tokens, a.max_new, a.max_seqlen, a.cache.status, r, false);
-  const int U = good ? tile_units(r, p.G, a.causal, tile) : 0;
+  const int U = good && tile * kManyRows + int(blockIdx.z) * 32 < r.n * p.G ? tile_units(r, p.G, a.causal, tile) : 0;
   int piece = 1, first = 0;
   if (U > 0) {
     const ManyUnits units{p, false};
@@ -452,19 +453,45 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_many_kernel(const 
       all += __shfl_xor_sync(0xffffffffu, all, o);
       first += __shfl_xor_sync(0xffffffffu, first, o);
     }
-    first += h * item_units(r, p.G, a.causal);
+    first += h * item_units_warp(r, p.G, a.causal, lane);
     piece = share_many(all, p.ctas);
   }
   const int c0 = first / piece, c1 = (first + U - 1) / piece;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (U == 0 || c0 == c1) return;  // finished by its CTA
+  if (U == 0 || c0 == c1 || row >= r.n * p.G) return;  // finished by its CTA
   const int per_slot = min(kManyRows, a.max_new * p.G);
-  const int rows = min(kManyRows, r.n * p.G - tile * kManyRows), x0 = blockIdx.z * 32;
-  for (int x = x0 + w; x < min(rows, x0 + 32); x += kJoinWarps) {
-    const int row = tile * kManyRows + x;
-    auto at = [&](int j) { return int64_t(2 * (c0 + j) + (j == 0 ? 1 : 0)) * per_slot + x; };
-    join_row<D, 1>(p, c1 - c0 + 1, at, r.q0 + row / p.G, h * p.G + row % p.G, 0, lane, nullptr);
+  auto slot = [&](int c) { return int64_t(2 * c + (c == c0 ? 1 : 0)) * per_slot; };
+  float m = -INFINITY;
+#pragma unroll 4
+  for (int c = c0; c <= c1; ++c) m = fmaxf(m, p.part_m[slot(c) + x].x);
+  constexpr int Q = D / 4 < kJoinWarps ? 1 : D / 4 / kJoinWarps;  // groups of four dimensions per warp
+  float l = 0.f;
+  float4 o[Q];
+#pragma unroll
+  for (int q = 0; q < Q; ++q) o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float4* part = reinterpret_cast<const float4*>(p.part_o);
+#pragma unroll 2
+  for (int c = c0; c <= c1; ++c) {
+    const float2 s = p.part_m[slot(c) + x];
+    const float f = s.x == -INFINITY ? 0.f : ptx::ex2(s.x - m);
+    l += s.y != s.y ? s.y : f * s.y;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const float4 v = part[slot(c) * (D / 4) + int64_t(w * Q + q) * per_slot + x];
+      o[q].x = fmaf(f, v.x, o[q].x);
+      o[q].y = fmaf(f, v.y, o[q].y);
+      o[q].z = fmaf(f, v.z, o[q].z);
+      o[q].w = fmaf(f, v.w, o[q].w);
+    }
   }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int head = h * p.G + row % p.G;
+  const int64_t token = r.q0 + row / p.G;
+#pragma unroll
+  for (int q = 0; q < Q; ++q)
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + (token * a.num_heads + head) * D + (w * Q + q) * 4) =
+        make_uint2(ptx::pack_bf16(o[q].x * inv, o[q].y * inv), ptx::pack_bf16(o[q].z * inv, o[q].w * inv));
+  if (w == 0) a.lse[int64_t(head) * a.total_tokens + token] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // Whether a CTA takes a (sequence, head) whole, so that nothing is joined: where

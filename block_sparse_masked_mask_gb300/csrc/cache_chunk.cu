@@ -82,7 +82,9 @@ struct ChunkCfg {
                        B_VEMPTY = B_VFULL + NV, B_SCLFULL = B_VEMPTY + NV, B_SCLFREE = B_SCLFULL + NSCL,
                        B_SFULL = B_SCLFREE + NSCL, B_PFULL = B_SFULL + 4, B_PDONE = B_PFULL + 4,
                        B_DRAIN = B_PDONE + 4, NBAR = B_DRAIN + 3;
-  static constexpr int OFF_BAR = (OFF_SCL + NSCL * 8 * 16 + 15) & ~15;
+  static constexpr int STAGE = 16 * D * 2;                // rows of O on their way out, per softmax warp
+  static constexpr int OFF_STAGE = OFF_SCL + NSCL * 8 * 16;
+  static constexpr int OFF_BAR = (OFF_STAGE + 8 * STAGE + 15) & ~15;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int USED = OFF_MISC + 16 + 1024;        // the base is aligned to 1024
   // one CTA per SM: it takes all of TMEM
@@ -131,7 +133,7 @@ struct Walk {
     while (pos < stop) {
       if (b != known) {
         const bool good = load_rows(a.cu, a.lens, b, a.total_tokens, a.max_new, a.max_seqlen, a.cache.status, r, false);
-        all = good ? item_units(r, p.G, a.causal) : 0;
+        all = good ? item_units_warp(r, p.G, a.causal, lane) : 0;
         known = b;
       }
       s.r = r;
@@ -192,27 +194,26 @@ __device__ __noinline__ float put_query(const CacheAttnParams& p, const Segment&
   const int rg = s.row0 + m * kTile + row;  // of the sequence and head
   const bool real = rg < s.r.n * p.G;
   const int64_t at_q = int64_t(s.r.q0 + (real ? rg / p.G : 0)) * a.num_heads + s.h * p.G + (real ? rg % p.G : 0);
-  // read twice, a few registers at a time (the second time from L1)
-  float amax = 0.f;
   const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at_q * D);
-  auto piece = [&](int i) { return real ? __ldg(src + i) : make_uint4(0, 0, 0, 0); };
-#pragma unroll 4
+  uint4 q[D / 8];  // all reads in flight at once
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) q[i] = real ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+  float amax = 0.f;
+#pragma unroll
   for (int i = 0; i < D / 8; ++i) {
-    const uint4 q = piece(i);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
   }
   const int e = amax > 0.f ? max(-119, min(126, exponent_of(amax))) : 0;
   const float f = pow2f(7 - e);
-#pragma unroll 1
+#pragma unroll
   for (int i = 0; i < D / 16; ++i) {
-    const uint4 q[2] = {piece(2 * i), piece(2 * i + 1)};
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int e4 = 0; e4 < 4; ++e4) {
-      const uint4 v = q[e4 >> 1];
+      const uint4 v = q[2 * i + (e4 >> 1)];
       const uint32_t w0 = (e4 & 1) ? v.z : v.x, w1 = (e4 & 1) ? v.w : v.y;
       const float x0 = __uint_as_float(w0 << 16) * f, x1 = __uint_as_float(w0 & 0xFFFF0000u) * f;
       const float x2 = __uint_as_float(w1 << 16) * f, x3 = __uint_as_float(w1 & 0xFFFF0000u) * f;
@@ -660,42 +661,72 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const int64_t token = done.r.q0 + (real ? rg / p.G : 0);
       const int head = done.h * p.G + (real ? rg % p.G : 0);
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      const int64_t at = done.whole ? token * a.num_heads + head
-                                    : int64_t(done.slot) * min(kManyRows, a.max_new * p.G) + m * kTile + row;
+      if (done.whole) {
+        // rows of O as whole rows, 16 at a time through the warp's stage
+        constexpr int CPR = D / 8, RPI = 32 / CPR;  // 16-byte pieces per row, rows per store
+        uint8_t* stage = sbase + C::OFF_STAGE + warp * C::STAGE;
+        uint32_t pk[D / 2];
 #pragma unroll
-      for (int q = 0; q < D / 16; ++q) {
-        uint32_t v[16];
-        if (done.tiles > 0) {
+        for (int q = 0; q < D / 16; ++q) {
+          uint32_t v[16];
+          if (done.tiles > 0) {
+            ptx::tmem_ld16(o_col + q * 16, v);
+            ptx::tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = 0u;
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            pk[8 * q + e] = ptx::pack_bf16(__uint_as_float(v[2 * e]) * inv, __uint_as_float(v[2 * e + 1]) * inv);
+        }
+        const int row_first = done.row0 + m * kTile + quarter * 32;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          if ((lane >> 4) == half) {
+#pragma unroll
+            for (int x = 0; x < CPR; ++x)
+              *reinterpret_cast<uint4*>(stage + (lane & 15) * D * 2 + ((x ^ lane) & (CPR - 1)) * 16) =
+                  make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]);
+          }
+          __syncwarp();
+#pragma unroll 1
+          for (int x = 0; x < 16 / RPI; ++x) {
+            const int r16 = x * RPI + lane / CPR, piece = lane % CPR;
+            const uint4 val = *reinterpret_cast<const uint4*>(stage + r16 * D * 2 + ((piece ^ r16) & (CPR - 1)) * 16);
+            const int rr = row_first + half * 16 + r16;
+            if (rr < done.r.n * p.G)
+              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) +
+                                        (int64_t(done.r.q0 + rr / p.G) * a.num_heads + done.h * p.G + rr % p.G) * D +
+                                        piece * 8) = val;
+          }
+          __syncwarp();
+        }
+        if (real)
+          a.lse[int64_t(head) * a.total_tokens + token] =
+              l == 0.f ? -INFINITY : (mx + log2f(l)) * 0.69314718055994531f;
+      } else {
+        // four dimensions of all rows together: lanes are rows
+        const int per_slot = min(kManyRows, a.max_new * p.G), x = m * kTile + row;
+        float4* to = reinterpret_cast<float4*>(p.part_o) + int64_t(done.slot) * per_slot * (D / 4) + x;
+#pragma unroll
+        for (int q = 0; q < D / 16; ++q) {
+          uint32_t v[16];
           ptx::tmem_ld16(o_col + q * 16, v);
           ptx::tmem_wait_ld();
-        } else {
+          if (real) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = 0u;
+            for (int e = 0; e < 4; ++e)
+              to[int64_t(4 * q + e) * per_slot] =
+                  make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]), __uint_as_float(v[4 * e + 2]),
+                              __uint_as_float(v[4 * e + 3]));
+          }
+          __syncwarp();
         }
-        __syncwarp();
-        if (real && done.whole) {
-          uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + at * D + q * 16);
-          uint32_t w[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            w[i] = ptx::pack_bf16(__uint_as_float(v[2 * i]) * inv, __uint_as_float(v[2 * i + 1]) * inv);
-          out[0] = make_uint4(w[0], w[1], w[2], w[3]);
-          out[1] = make_uint4(w[4], w[5], w[6], w[7]);
-        } else if (real) {
-          uint4* out = reinterpret_cast<uint4*>(p.part_o + at * D + q * 16);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) out[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        }
+        if (real) p.part_m[int64_t(done.slot) * per_slot + x] = make_float2(mx, l);
       }
       // O has been read before the next item's first weights arrive
       ptx::tc_fence_before();
-      if (real) {
-        if (done.whole)
-          a.lse[int64_t(head) * a.total_tokens + token] =
-              l == 0.f ? -INFINITY : (mx + log2f(l)) * 0.69314718055994531f;
-        else
-          p.part_m[at] = make_float2(mx, l);
-      }
     }
   }
 

@@ -223,6 +223,15 @@ __device__ __forceinline__ int item_units(const SeqRows& r, int G, bool causal) 
   for (int i = 0; i < tiles; ++i) n += tile_units(r, G, causal, i);
   return n;
 }
+// The same by a whole warp for one sequence.
+__device__ __forceinline__ int item_units_warp(const SeqRows& r, int G, bool causal, int lane) {
+  const int tiles = (r.n * G + kManyRows - 1) / kManyRows;
+  int n = 0;
+  for (int i = lane; i < tiles; i += 32) n += tile_units(r, G, causal, i);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  return n;
+}
 struct ManyUnits {
   const CacheAttnParams& p;
   bool note;
