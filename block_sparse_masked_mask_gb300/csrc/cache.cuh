@@ -76,19 +76,22 @@ struct CacheQueryArgs {
   float* workspace;
 };
 
-// How attn_cache_fwd divides its work: the tokens (few rows) or tiles (many rows)
-// of all sequences and heads form a line, cut evenly among the CTAs.
+// How attn_cache_fwd cuts its work, and where the pieces' results meet: rows (new
+// token, query head of the group) in tiles and tokens in chunks
+// (tcgen05 kernel), or share the line of all tokens evenly (mma.sync kernel).
 struct CacheAttnParams {
   CacheQueryArgs a;
-  int G;       // query heads per key / value head
-  bool many;   // more than kFewRows rows of a sequence and head: the tcgen05 kernel
-  bool whole;  // few: a CTA per (sequence, head) instead
-  int ctas;
+  int G;           // query heads per key / value head
+  bool many;       // the tcgen05 kernel
+  int row_tiles, chunk, splits;  // many: tiles of kManyRows rows, tokens per chunk, chunks
+  int ctas;        // few: CTAs
+  bool whole;      // few: a CTA per (sequence, head)
   float scale_log2;
-  // Results before the division, and (running maximum, sum), of the segments that
-  // are not a whole item: of CTA c, 2 c one that goes on one of the CTA before,
-  // 2 c + 1 one that goes on in the next; min(max_new * G, kManyRows) rows each.
-  float* part_o;   // few: rows of head_dim; many: four dimensions of all rows, then the next four
+  // Results before the division, and (running maximum, sum).
+  //   many: [splits][total_tokens * num_heads] rows
+  //   few:  [2 * ctas][max_new * G] rows: of CTA c, 2 c a segment that goes on
+  //         one of the CTA before, 2 c + 1 one that goes on in the next
+  float* part_o;   // rows of head_dim
   float2* part_m;
 };
 constexpr int kFewRows = 16, kManyRows = 256;

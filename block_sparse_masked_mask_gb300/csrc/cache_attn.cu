@@ -428,70 +428,22 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_few_kernel(const C
   join_row<D, W>(p, c1 - c0 + 1, at, r.q0 + i / a.num_heads, head, w, lane, shared);
 }
 
-// Many rows: a CTA per 32 rows of an item; lanes are rows, warps share the dimensions.
+// Many rows: a warp per row, over the chunks that the row's tile had.
 template <int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) cache_join_many_kernel(const CacheAttnParams p, int row_tiles) {
+__global__ void __launch_bounds__(32 * kJoinWarps) cache_join_many_kernel(const CacheAttnParams p) {
   const CacheQueryArgs& a = p.a;
-  const int b = blockIdx.y, h = blockIdx.x / row_tiles, tile = blockIdx.x % row_tiles;
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int x = blockIdx.z * 32 + lane, row = tile * kManyRows + x;
+  const int b = blockIdx.y, lane = threadIdx.x & 31;
+  const int i = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
   SeqRows r;
   const bool good = load_rows(a.cu, a.lens, b, a.total_tokens, a.max_new, a.max_seqlen, a.cache.status, r, false);
-  const int U = good && tile * kManyRows + int(blockIdx.z) * 32 < r.n * p.G ? tile_units(r, p.G, a.causal, tile) : 0;
-  int piece = 1, first = 0;
-  if (U > 0) {
-    const ManyUnits units{p, false};
-    int all = 0;
-    for (int s = lane; s < a.cache.batch; s += 32) {
-      const int n = units(s);
-      all += n;
-      first += s < b ? n : 0;
-    }
-    for (int t = lane; t < tile; t += 32) first += tile_units(r, p.G, a.causal, t);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      all += __shfl_xor_sync(0xffffffffu, all, o);
-      first += __shfl_xor_sync(0xffffffffu, first, o);
-    }
-    first += h * item_units_warp(r, p.G, a.causal, lane);
-    piece = share_many(all, p.ctas);
-  }
-  const int c0 = first / piece, c1 = (first + U - 1) / piece;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (U == 0 || c0 == c1 || row >= r.n * p.G) return;  // finished by its CTA
-  const int per_slot = min(kManyRows, a.max_new * p.G);
-  auto slot = [&](int c) { return int64_t(2 * c + (c == c0 ? 1 : 0)) * per_slot; };
-  float m = -INFINITY;
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) m = fmaxf(m, p.part_m[slot(c) + x].x);
-  constexpr int Q = D / 4 < kJoinWarps ? 1 : D / 4 / kJoinWarps;  // groups of four dimensions per warp
-  float l = 0.f;
-  float4 o[Q];
-#pragma unroll
-  for (int q = 0; q < Q; ++q) o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-  const float4* part = reinterpret_cast<const float4*>(p.part_o);
-#pragma unroll 2
-  for (int c = c0; c <= c1; ++c) {
-    const float2 s = p.part_m[slot(c) + x];
-    const float f = s.x == -INFINITY ? 0.f : ptx::ex2(s.x - m);
-    l += s.y != s.y ? s.y : f * s.y;
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      const float4 v = part[slot(c) * (D / 4) + int64_t(w * Q + q) * per_slot + x];
-      o[q].x = fmaf(f, v.x, o[q].x);
-      o[q].y = fmaf(f, v.y, o[q].y);
-      o[q].z = fmaf(f, v.z, o[q].z);
-      o[q].w = fmaf(f, v.w, o[q].w);
-    }
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int head = h * p.G + row % p.G;
-  const int64_t token = r.q0 + row / p.G;
-#pragma unroll
-  for (int q = 0; q < Q; ++q)
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + (token * a.num_heads + head) * D + (w * Q + q) * 4) =
-        make_uint2(ptx::pack_bf16(o[q].x * inv, o[q].y * inv), ptx::pack_bf16(o[q].z * inv, o[q].w * inv));
-  if (w == 0) a.lse[int64_t(head) * a.total_tokens + token] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  if (!good || i >= r.n * a.num_heads) return;
+  const int head = i % a.num_heads, row = (i / a.num_heads) * p.G + head % p.G;
+  const int last = min(row / kManyRows * kManyRows + kManyRows - 1, r.n * p.G - 1);
+  const int limit = visible_tokens(r, p.G, last, a.causal);
+  const int64_t token = r.q0 + i / a.num_heads, step = int64_t(a.total_tokens) * a.num_heads;
+  auto at = [&](int j) { return j * step + token * a.num_heads + head; };
+  join_row<D, 1>(p, max(1, (limit + p.chunk - 1) / p.chunk), at, token, head, 0, lane, nullptr);
 }
 
 // Whether a CTA takes a (sequence, head) whole, so that nothing is joined: where
@@ -504,25 +456,33 @@ bool take_whole(const CacheQueryArgs& a) {
   return a.max_seqlen <= 512 || (a.max_seqlen <= 1024 && items >= 64 && items <= 456);
 }
 
-// Which kernel, and its CTAs: more than 16 rows of a key / value head go to the
-// tcgen05 kernel (cache_chunk.cu), which reads the cache once for 256, one CTA per
-// SM; else three per SM are resident at once.  The number of SMs only sizes the
-// work, and the size query runs without a device, so it is that of the GPU this
-// library is built for.
+// Which kernel, and its cut.  More than 16 rows of a key / value head go to the
+// tcgen05 kernel (cache_chunk.cu), which reads the cache once for 256; its chunks
+// fill the GPU once, one CTA per SM, with 256 to 4096 tokens each.
+// The number of SMs only sizes the work, and the size query runs without a
+// device, so it is that of the GPU this library is built for.
 void plan(CacheAttnParams* p) {
   constexpr int kSms = 152;
   const CacheQueryArgs& a = p->a;
   p->G = a.num_heads / a.cache.heads;
-  p->many = int64_t(a.max_new) * p->G > kFewRows;
-  p->whole = !p->many && take_whole(a);
-  p->ctas = p->many ? kSms : p->whole ? a.cache.batch * a.cache.heads : 3 * kSms;
+  const int64_t rows = int64_t(a.max_new) * p->G;
+  p->many = rows > kFewRows;
+  p->whole = take_whole(a);
+  p->ctas = p->whole ? a.cache.batch * a.cache.heads : 3 * kSms;  // (three per SM are resident at once)
+  p->row_tiles = int((rows + kManyRows - 1) / kManyRows);
+  const int64_t items = int64_t(p->row_tiles) * a.cache.heads * a.cache.batch;
+  int64_t chunk = (int64_t(a.max_seqlen) * items + kSms - 1) / kSms;
+  chunk = (chunk + kTile - 1) / kTile * kTile;
+  chunk = chunk < 256 ? 256 : (chunk > 4096 ? 4096 : chunk);
+  p->chunk = int(chunk);
+  p->splits = int((int64_t(a.max_seqlen) + chunk - 1) / chunk);
+  if (p->splits < 1) p->splits = 1;
 }
 
-// Rows of partial results.  (Many rows: an item of at most 128 tokens is one unit.)
+// Rows of partial results.
 uint64_t partial_rows(const CacheAttnParams& p) {
-  if (p.whole || (p.many && p.a.max_seqlen <= kTile)) return 0;
-  const int64_t rows = int64_t(p.a.max_new) * p.G;
-  return 2 * uint64_t(p.ctas) * uint64_t(rows < kManyRows ? rows : kManyRows);
+  if (p.many) return p.splits == 1 ? 0 : uint64_t(p.splits) * uint64_t(p.a.total_tokens) * uint64_t(p.a.num_heads);
+  return p.whole ? 0 : 2 * uint64_t(p.ctas) * uint64_t(p.a.max_new) * uint64_t(p.G);
 }
 
 template <int D>
@@ -538,7 +498,15 @@ cudaError_t launch_few(const CacheAttnParams& p, cudaStream_t s) {
 // The joining kernel is launched early and waits for the first one's end.
 template <int D>
 cudaError_t launch_join(const CacheAttnParams& p, cudaStream_t s) {
+  const int64_t rows = int64_t(p.a.max_new) * p.a.num_heads;
+  // A (sequence, head) meets about ctas / (their number) CTAs; where those are
+  // many, a CTA joins each row (one request of 131072 tokens and one head: 128
+  // us with a warp per row, 25 us), else a warp does (64 requests of 8 heads: the
+  // join takes 12 us with a CTA per row, 5 us with a warp).
+  const bool wide = !p.many && int64_t(p.ctas) > 8 * int64_t(p.a.cache.batch) * p.a.cache.heads;
+  const int per_cta = wide ? 1 : kJoinWarps;
   cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned((rows + per_cta - 1) / per_cta), unsigned(p.a.cache.batch));
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -546,20 +514,8 @@ cudaError_t launch_join(const CacheAttnParams& p, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (p.many) {
-    const int row_tiles = int((int64_t(p.a.max_new) * p.G + kManyRows - 1) / kManyRows);
-    cfg.gridDim = dim3(unsigned(row_tiles) * unsigned(p.a.cache.heads), unsigned(p.a.cache.batch), kManyRows / 32);
-    return cudaLaunchKernelEx(&cfg, cache_join_many_kernel<D>, p, row_tiles);
-  }
-  // A (sequence, head) meets about ctas / (their number) CTAs; where those are
-  // many, a CTA joins each row (one request of 131072 tokens and one head: 128
-  // us with a warp per row, 25 us), else a warp does (64 requests of 8 heads: the
-  // join takes 12 us with a CTA per row, 7 us with a warp).
-  const int64_t rows = int64_t(p.a.max_new) * p.a.num_heads;
-  const bool wide = int64_t(p.ctas) > 8 * int64_t(p.a.cache.batch) * p.a.cache.heads;
-  const int per_cta = wide ? 1 : kJoinWarps;
-  cfg.gridDim = dim3(unsigned((rows + per_cta - 1) / per_cta), unsigned(p.a.cache.batch));
-  return cudaLaunchKernelEx(&cfg, wide ? cache_join_few_kernel<D, kJoinWarps> : cache_join_few_kernel<D, 1>, p);
+  return cudaLaunchKernelEx(&cfg, p.many ? cache_join_many_kernel<D>
+                                         : wide ? cache_join_few_kernel<D, kJoinWarps> : cache_join_few_kernel<D, 1>, p);
 }
 
 }  // namespace

@@ -206,44 +206,5 @@ __device__ __forceinline__ int visible_tokens(const SeqRows& r, int G, int row, 
   return causal ? max(0, r.len - r.n + row / G + 1) : r.len;
 }
 
-// Many rows (cache_chunk.cu): an item is a tile of kManyRows rows of a sequence and
-// head; its units are the tiles of 128 tokens that some of its rows see, at least
-// one.  0 for a tile past the last.
-__device__ __forceinline__ int tile_units(const SeqRows& r, int G, bool causal, int tile) {
-  const int rows = r.n * G;
-  if (tile * kManyRows >= rows) return 0;
-  const int last = min((tile + 1) * kManyRows, rows) - 1;
-  return max(1, (visible_tokens(r, G, last, causal) + kTile - 1) / kTile);
-}
-// Of all tiles of one head.
-__device__ __forceinline__ int item_units(const SeqRows& r, int G, bool causal) {
-  const int tiles = (r.n * G + kManyRows - 1) / kManyRows;
-  if (!causal) return tiles * tile_units(r, G, causal, 0);
-  int n = 0;
-  for (int i = 0; i < tiles; ++i) n += tile_units(r, G, causal, i);
-  return n;
-}
-// The same by a whole warp for one sequence.
-__device__ __forceinline__ int item_units_warp(const SeqRows& r, int G, bool causal, int lane) {
-  const int tiles = (r.n * G + kManyRows - 1) / kManyRows;
-  int n = 0;
-  for (int i = lane; i < tiles; i += 32) n += tile_units(r, G, causal, i);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-  return n;
-}
-struct ManyUnits {
-  const CacheAttnParams& p;
-  bool note;
-  __device__ int operator()(int b) const {
-    const CacheQueryArgs& a = p.a;
-    SeqRows r;
-    if (!load_rows(a.cu, a.lens, b, a.total_tokens, a.max_new, a.max_seqlen, a.cache.status, r, note)) return 0;
-    return item_units(r, p.G, a.causal) * a.cache.heads;
-  }
-};
-// Units per CTA: an even share, at least two.
-__device__ __forceinline__ int share_many(int total, int ctas) { return max(2, (total + ctas - 1) / ctas); }
-
 }  // namespace
 }  // namespace attnmask
