@@ -22,6 +22,8 @@
 // more than 2^8.
 // A (sequence, head) that lies in one CTA's piece is finished there; the others
 // meet in a second kernel through fp32 partial results, two per CTA at most.
+#include <cmath>
+
 #include "cache_rows.cuh"
 #include "ptx.cuh"
 
@@ -457,8 +459,15 @@ bool take_whole(const CacheQueryArgs& a) {
 }
 
 // Which kernel, and its cut.  More than 16 rows of a key / value head go to the
-// tcgen05 kernel (cache_chunk.cu), which reads the cache once for 256; its chunks
-// fill the GPU once, one CTA per SM, with 256 to 4096 tokens each.
+// tcgen05 kernel (cache_chunk.cu), which reads the cache once for 256, one CTA per
+// SM.  Its chunks are of one size: the least number of chunks (of 4096 tokens at
+// most), or as many as fill the SMs one to four times, whichever is quickest in
+// this estimate, in tokens of a CTA's walk (11 to 20 ns each): a chunk with its
+// start and end (384) times the waves, half rounded up, as sequences differ in
+// length; and the join, with the bytes of its partial results (8 per element, at
+// 5 TB/s).  Measured against chunks of work / SMs tokens: 2 sequences of 4096,
+// 300 new, 4 heads 58 -> 43 us; 8 of up to 9000, up to 200 new, D = 64: 72 -> 46;
+// 1 of 32768, 512 new, 8 heads 303 -> 284.
 // The number of SMs only sizes the work, and the size query runs without a
 // device, so it is that of the GPU this library is built for.
 void plan(CacheAttnParams* p) {
@@ -471,12 +480,26 @@ void plan(CacheAttnParams* p) {
   p->ctas = p->whole ? a.cache.batch * a.cache.heads : 3 * kSms;  // (three per SM are resident at once)
   p->row_tiles = int((rows + kManyRows - 1) / kManyRows);
   const int64_t items = int64_t(p->row_tiles) * a.cache.heads * a.cache.batch;
-  int64_t chunk = (int64_t(a.max_seqlen) * items + kSms - 1) / kSms;
-  chunk = (chunk + kTile - 1) / kTile * kTile;
-  chunk = chunk < 256 ? 256 : (chunk > 4096 ? 4096 : chunk);
-  p->chunk = int(chunk);
-  p->splits = int((int64_t(a.max_seqlen) + chunk - 1) / chunk);
-  if (p->splits < 1) p->splits = 1;
+  p->chunk = 256;
+  p->splits = 1;
+  if (!p->many || items == 0) return;
+  const int64_t least = (int64_t(a.max_seqlen) + 4095) / 4096;
+  double best = INFINITY;
+  for (int fill = 0; fill <= 4; ++fill) {
+    const int64_t n = fill == 0 ? least : fill * kSms / items;
+    if (n < least || n < 1) continue;
+    int64_t chunk = (int64_t(a.max_seqlen) + n - 1) / n;
+    chunk = (chunk + kTile - 1) / kTile * kTile;
+    if (chunk < 256) chunk = 256;
+    const int64_t splits = a.max_seqlen > 0 ? (int64_t(a.max_seqlen) + chunk - 1) / chunk : 1;
+    const double ctas = double(items) * double(splits), waves = ctas / kSms;
+    double cost = (waves > 1 ? (waves + ceil(waves)) / 2 : 1) * double(chunk + 384);
+    if (splits > 1) cost += 400 + double(splits) * a.total_tokens * a.num_heads * a.cache.head_dim / 6400;
+    if (cost >= best) continue;
+    best = cost;
+    p->chunk = int(chunk);
+    p->splits = int(splits);
+  }
 }
 
 // Rows of partial results.

@@ -14,11 +14,18 @@
 //  * O += P V runs in fp16: weights keep 11 bits, the values are exact.  One
 //    warpgroup turns the codes into fp16 tiles in shared memory, once
 //    for both M tiles.
+//  * Up to 128 rows (a draft, the end of a prompt) both M tiles hold the same
+//    queries and take the tiles of tokens in turn, each with its own running
+//    maximum, and the CTA joins them at its end; warps without rows only pass the
+//    steps on.  Such a CTA waits for latencies, and two chains hide each other's:
+//    16 sequences of 8192, 32 rows of 8 heads 137 -> 108 us.
 //  * The pages' scales and the running maximum are those of cache_attn.cu.
 // Warps (512 threads):
 //   0-3, 4-7   softmax of M tile 0 and 1, one thread per row
 //   8-11       values: codes to fp16 tiles (two slots)
-//   12         pages, scales (four slots) and TMA of the keys (three slots)
+//   12         pages, scales (four slots) and TMA of the codes (two slots each
+//              of keys and values; reads by the value warps themselves came a
+//              latency late: the 32 rows above 108 -> 92 us)
 //   13, 14     tcgen05 issuers of S, one per M tile
 //   15         tcgen05 issuer of P V for both M tiles (also owns TMEM)
 // Keys and values come in tiles of 128 tokens; the products and the softmax go
@@ -43,20 +50,38 @@ constexpr int kChunkThreads = 512;
 constexpr int kWarpValues = 8, kWarpKeys = 12, kWarpS = 13, kWarpPV = 15;
 constexpr int kStep = 64;  // tokens per step
 
+// The bounded waits of tile_pipeline.cuh behind one inlined try: five roles run
+// at once, and their loops are fastest when they are short (the instruction
+// caches; with the whole wait inlined everywhere 4 prompts of 300 to 512 tokens
+// took 378 us, so 358).
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, int32_t* err,
+                                       int site) {
+  return wait_bar(bar, parity, abort_flag, err, site);
+}
+__device__ __forceinline__ bool wait_lane(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, int32_t* err,
+                                          int site) {
+  return ptx::mbar_try_wait(bar, parity) || wait_long(bar, parity, abort_flag, err, site);
+}
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, int32_t* err,
+                                          int site) {
+  return __all_sync(0xffffffffu, wait_lane(bar, parity, abort_flag, err, site));
+}
+
 template <int D>
 struct ChunkCfg {
   using V = TileLayout<D>;                     // fp16 value tile: the 16-bit layout
   static constexpr int KT = kTile * D;         // bytes of a tile of codes (keys, or half a query)
   static constexpr int VT = V::TILE;
-  static constexpr int NK = 3, NV = 2, NSCL = 4;
+  static constexpr int NK = 2, NR = 2, NV = 2, NSCL = 4;
   static constexpr int OFF_Q = 0;              // [M tile][hi, lo]
   static constexpr int OFF_K = OFF_Q + 4 * KT;
-  static constexpr int OFF_V = OFF_K + NK * KT;
+  static constexpr int OFF_R = OFF_K + NK * KT;  // the values' codes
+  static constexpr int OFF_V = OFF_R + NR * KT;
   // [slot][8 blocks of 16 tokens]: key scale, exponent of the value scale, its
   // inverse, the page (as an int; -1: none)
   static constexpr int OFF_SCL = OFF_V + NV * VT;
   // B_SFULL, B_PFULL, B_PDONE: per M tile and S buffer
-  static constexpr int B_Q = 0, B_KFULL = 2, B_KEMPTY = B_KFULL + NK, B_VFULL = B_KEMPTY + NK,
+  static constexpr int B_Q = 0, B_KFULL = 2, B_KEMPTY = B_KFULL + NK, B_RFULL = B_KEMPTY + NK, B_REMPTY = B_RFULL + NR, B_VFULL = B_REMPTY + NR,
                        B_VEMPTY = B_VFULL + NV, B_SCLFULL = B_VEMPTY + NV, B_SCLFREE = B_SCLFULL + NSCL,
                        B_SFULL = B_SCLFREE + NSCL, B_PFULL = B_SFULL + 4, B_PDONE = B_PFULL + 4,
                        B_DRAIN = B_PDONE + 4, NBAR = B_DRAIN + 3;
@@ -80,7 +105,8 @@ struct ChunkCfg {
 
 template <int D>
 __global__ void __launch_bounds__(kChunkThreads, 1)
-    cache_chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CacheAttnParams p) {
+    cache_chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                       const __grid_constant__ CacheAttnParams p) {
   using C = ChunkCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -98,7 +124,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   if (split > 0 && begin >= end) return;  // chunk 0 also answers for rows that see nothing
   const int steps = end > begin ? (end - begin + kStep - 1) / kStep : 0;
   const int tiles = (steps + 1) / 2;
-  const int nm = rows > kTile ? 2 : 1;  // M tiles
+  // up to 128 rows: both M tiles hold them, and take the tiles of tokens in turn
+  const bool twin = rows <= kTile;
+  const int users = twin ? 1 : 2;  // M tiles per tile of tokens
   int32_t* err = c.status;
 
   const uint32_t raw = ptx::smem_addr(smem_raw);
@@ -113,7 +141,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NK; ++i) {
       ptx::mbar_init(bar(C::B_KFULL + i), 1);
-      ptx::mbar_init(bar(C::B_KEMPTY + i), nm);
+      ptx::mbar_init(bar(C::B_KEMPTY + i), users);
+    }
+    for (int i = 0; i < C::NR; ++i) {
+      ptx::mbar_init(bar(C::B_RFULL + i), 1);
+      ptx::mbar_init(bar(C::B_REMPTY + i), 4);
     }
     for (int i = 0; i < C::NV; ++i) {
       ptx::mbar_init(bar(C::B_VFULL + i), 4);
@@ -121,7 +153,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
     for (int i = 0; i < C::NSCL; ++i) {
       ptx::mbar_init(bar(C::B_SCLFULL + i), 1);
-      ptx::mbar_init(bar(C::B_SCLFREE + i), 4 * nm + 4);  // softmax and value warps
+      ptx::mbar_init(bar(C::B_SCLFREE + i), 4 * users + 4);  // softmax and value warps
     }
     for (int i = 0; i < 4; ++i) {
       ptx::mbar_init(bar(C::B_SFULL + i), 1);
@@ -161,10 +193,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const int64_t at = fine ? int64_t(id) * c.heads + h : 0;
       return make_float2(fine ? __ldg(c.k_scale + at) : 0.f, fine ? __ldg(c.v_scale + at) : 0.f);
     };
-    if (lane == 0) ptx::prefetch_tensormap(&tmK);
+    if (lane == 0) {
+      ptx::prefetch_tensormap(&tmK);
+      ptx::prefetch_tensormap(&tmV);
+    }
     int id = number(0), id_next = number(1);
     float2 sc = scales(0, id);
-    int done = 0;
+    int done = 0, done_v = 0;
     for (int j = 0; j < tiles; ++j) {
       const int id_after = number(j + 2);
       const float2 sc_next = scales(j + 1, id_next);
@@ -172,7 +207,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const int tok = begin + j * kTile + lane * 16;
       const bool here = lane < 8 && tok < end, fine = here && unsigned(id) < unsigned(c.num_pages);
       if (here && !fine) atomicOr(err, kErrBadPage);
-      if (j >= C::NSCL && !warp_wait(bar(C::B_SCLFREE + ss), uint32_t(j / C::NSCL - 1) & 1u, abort_flag, err, 1))
+      if (j >= C::NSCL && !wait_warp(bar(C::B_SCLFREE + ss), uint32_t(j / C::NSCL - 1) & 1u, abort_flag, err, 1))
         break;
       if (lane < 8) {
         const int x = exponent_of(sc.y);
@@ -181,7 +216,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar(C::B_SCLFULL + ss));
-      if (j >= C::NK && !warp_wait(bar(C::B_KEMPTY + slot), uint32_t(j / C::NK - 1) & 1u, abort_flag, err, 2)) break;
+      if (j >= C::NK && !wait_warp(bar(C::B_KEMPTY + slot), uint32_t(j / C::NK - 1) & 1u, abort_flag, err, 2)) break;
       const bool load = fine && lane % step == 0;  // one lane per page
       const uint32_t loads = __ballot_sync(0xffffffffu, load);
       const uint32_t piece = uint32_t(D) << c.page_log2;  // bytes of a page's keys
@@ -190,6 +225,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (load)
         ptx::tma_load_4d(base + C::OFF_K + slot * C::KT + lane * 16 * D, &tmK, bar(C::B_KFULL + slot), 0, 0, h, id);
       done = j + 1;
+      const int rs = j % C::NR;
+      if (j >= C::NR && !wait_warp(bar(C::B_REMPTY + rs), uint32_t(j / C::NR - 1) & 1u, abort_flag, err, 12)) break;
+      if (lane == 0) ptx::mbar_arrive_expect_tx(bar(C::B_RFULL + rs), piece * __popc(loads));
+      __syncwarp();
+      if (load)
+        ptx::tma_load_4d(base + C::OFF_R + rs * C::KT + lane * 16 * D, &tmV, bar(C::B_RFULL + rs), 0, 0, h, id);
+      done_v = j + 1;
       id = id_next;
       id_next = id_after;
       sc = sc_next;
@@ -201,6 +243,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const int last = s + C::NK * ((done - 1 - s) / C::NK);
         drain_bar(bar(C::B_KFULL + s), uint32_t(last / C::NK) & 1u, err);
       }
+      for (int s = 0; s < C::NR; ++s) {
+        if (done_v <= s) continue;
+        const int last = s + C::NR * ((done_v - 1 - s) / C::NR);
+        drain_bar(bar(C::B_RFULL + s), uint32_t(last / C::NR) & 1u, err);
+      }
     }
     __syncwarp();
   } else if (warp == kWarpPV) {
@@ -211,16 +258,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       bool ok = true;
       for (int i = 0; ok && i < steps; ++i) {
         const int j = i >> 1, vs = j % C::NV, f = i & 1;
-        if (f == 0 && !wait_bar(bar(C::B_VFULL + vs), uint32_t(j / C::NV) & 1u, abort_flag, err, 6)) break;
+        if (f == 0 && !wait_lane(bar(C::B_VFULL + vs), uint32_t(j / C::NV) & 1u, abort_flag, err, 6)) break;
         const uint64_t vi = vd + uint64_t(vs) * (C::VT >> 4) + v_step<D>(f * (kStep / 16));
-        for (int m = 0; m < nm; ++m) {
-          ok = wait_bar(bar(C::B_PFULL + 2 * m + f), uint32_t(j) & 1u, abort_flag, err, 7);
+        const int turn = twin ? j >> 1 : j;  // of the M tile's own
+        for (int m = twin ? j & 1 : 0; m < 2; m += twin ? 2 : 1) {
+          ok = wait_lane(bar(C::B_PFULL + 2 * m + f), uint32_t(turn) & 1u, abort_flag, err, 7);
           if (!ok) break;
           ptx::tc_fence_after();
           const uint32_t p_tmem = tmem + uint32_t(128 * m + kStep * f), o_tmem = tmem + uint32_t(256 + 128 * m);
 #pragma unroll
           for (int kk = 0; kk < kStep / 16; ++kk)
-            ptx::mma_ts(o_tmem, p_tmem + uint32_t(kk) * 8u, vi + v_step<D>(kk), IDESC, (i > 0 || kk > 0) ? 1u : 0u);
+            ptx::mma_ts(o_tmem, p_tmem + uint32_t(kk) * 8u, vi + v_step<D>(kk), IDESC,
+                        (turn > 0 || f > 0 || kk > 0) ? 1u : 0u);
           ptx::mma_commit(bar(C::B_PDONE + 2 * m + f));
         }
         if (ok && (f == 1 || i == steps - 1)) ptx::mma_commit(bar(C::B_VEMPTY + vs));
@@ -233,17 +282,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   } else if (warp >= kWarpS) {
     // -------------------------------------------------------------- S issuers
     const int m = warp - kWarpS;
-    if (lane == 0 && m < nm) {
+    if (lane == 0) {
       constexpr uint32_t IDESC = ptx::idesc_e4m3_f32(128, kStep);
       const uint64_t qhi = ptx::smem_desc(base + C::OFF_Q + 2 * m * C::KT, 16u, 8 * D, C::SW8);
       const uint64_t qlo = ptx::smem_desc(base + C::OFF_Q + (2 * m + 1) * C::KT, 16u, 8 * D, C::SW8);
       const uint64_t kd = ptx::smem_desc(base + C::OFF_K, 16u, 8 * D, C::SW8);
-      const bool ok = steps == 0 || wait_bar(bar(C::B_Q + m), 0, abort_flag, err, 3);
-      for (int i = 0; ok && i < steps; ++i) {
-        const int j = i >> 1, ks = j % C::NK, f = i & 1;
-        if (f == 0 && !wait_bar(bar(C::B_KFULL + ks), uint32_t(j / C::NK) & 1u, abort_flag, err, 4)) break;
-        // P(i - 2) lies over this S: its product has read it
-        if (i >= 2 && !wait_bar(bar(C::B_PDONE + 2 * m + f), uint32_t(i / 2 - 1) & 1u, abort_flag, err, 5)) break;
+      const bool ok = steps == 0 || wait_lane(bar(C::B_Q + m), 0, abort_flag, err, 3);
+      for (int i = twin ? 2 * m : 0; ok && i < steps; i += twin && (i & 1) ? 3 : 1) {
+        const int j = i >> 1, ks = j % C::NK, f = i & 1, turn = twin ? j >> 1 : j;
+        if (f == 0 && !wait_lane(bar(C::B_KFULL + ks), uint32_t(j / C::NK) & 1u, abort_flag, err, 4)) break;
+        // the P before lies over this S: its product has read it
+        if (turn >= 1 && !wait_lane(bar(C::B_PDONE + 2 * m + f), uint32_t(turn - 1) & 1u, abort_flag, err, 5)) break;
         ptx::tc_fence_after();
         const uint32_t s_tmem = tmem + uint32_t(128 * m + kStep * f);
         const uint64_t ki = kd + uint64_t((ks * C::KT + f * kStep * D) >> 4);
@@ -262,29 +311,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     // ------------------------------------------------------------ values
     constexpr int PPT = D / 16;  // 16-byte pieces per token = pieces per thread
     const int ct = threadIdx.x - kWarpValues * 32;
-    uint4 next[PPT];
-    auto fetch = [&](int j) -> bool {
-      if (j >= tiles) return true;
-      const int ss = j % C::NSCL;
-      if (!warp_wait(bar(C::B_SCLFULL + ss), uint32_t(j / C::NSCL) & 1u, abort_flag, err, 12)) return false;
+    for (int j = 0; j < tiles; ++j) {
+      const int rs = j % C::NR, ss = j % C::NSCL, slot = j % C::NV;
+      // (the scales' slot was written before this arrived)
+      if (!wait_warp(bar(C::B_RFULL + rs), uint32_t(j / C::NR) & 1u, abort_flag, err, 12)) break;
+      uint4 next[PPT];
 #pragma unroll
       for (int i = 0; i < PPT; ++i) {
-        const int x = i * 128 + ct, row = x / PPT, piece = x % PPT;
-        const int tok = begin + j * kTile + row;
-        const int id = __float_as_int(scl[ss * 8 + row / 16].w);
-        next[i] = make_uint4(0, 0, 0, 0);  // behind the end, or without a page: weights of 0 times 0
-        if (tok < end && id >= 0)
-          next[i] = __ldg(reinterpret_cast<const uint4*>(
-              c.v_pages + (((int64_t(id) * c.heads + h) << c.page_log2) + (tok & ((1 << c.page_log2) - 1))) * D +
-              piece * 16));
+        const int x = i * 128 + ct, row = x / PPT;
+        next[i] = *reinterpret_cast<const uint4*>(sbase + C::OFF_R + rs * C::KT + x * 16);
+        // behind the end, or without a page: weights of 0 times 0
+        if (begin + j * kTile + row >= end || __float_as_int(scl[ss * 8 + row / 16].w) < 0)
+          next[i] = make_uint4(0, 0, 0, 0);
       }
-      warp_arrive(bar(C::B_SCLFREE + ss), lane);
-      return true;
-    };
-    bool ok = fetch(0);
-    for (int j = 0; ok && j < tiles; ++j) {
-      const int slot = j % C::NV;
-      if (j >= C::NV && !warp_wait(bar(C::B_VEMPTY + slot), uint32_t(j / C::NV - 1) & 1u, abort_flag, err, 8)) break;
+      warp_arrive(bar(C::B_REMPTY + rs), lane);
+      if (lane == 0) ptx::mbar_arrive(bar(C::B_SCLFREE + ss));
+      if (j >= C::NV && !wait_warp(bar(C::B_VEMPTY + slot), uint32_t(j / C::NV - 1) & 1u, abort_flag, err, 8)) break;
       uint8_t* tile = sbase + C::OFF_V + slot * C::VT;
 #pragma unroll
       for (int i = 0; i < PPT; ++i) {
@@ -302,19 +344,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
       ptx::fence_proxy_async_smem();
       warp_arrive(bar(C::B_VFULL + slot), lane);
-      ok = fetch(j + 1);
     }
-  } else if (warp < 4 * nm) {
+  } else {
     // ------------------------------------------------------------ softmax
     const int m = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;          // of the M tile, its TMEM lane
-    const int rg = row0 + m * kTile + row;        // of the sequence and head
+    const int rg = row0 + (twin ? 0 : m * kTile) + row;  // of the sequence and head
     const uint32_t lane_base = tmem + (uint32_t(quarter * 32) << 16);
     const uint32_t o_col = lane_base + 256u + uint32_t(m) * 128u;
     const bool real = rg < r.n * p.G;
     const int64_t token = r.q0 + (real ? rg / p.G : 0);
     const int head = h * p.G + (real ? rg % p.G : 0);
     const int visible = visible_tokens(r, p.G, rg, a.causal);
+    const bool idle = rg - lane >= r.n * p.G;     // a warp without rows only keeps the steps' order
 
     // the row's query as hi + lo
     float qscale;
@@ -362,13 +404,23 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     float mx = -INFINITY;                    // running maximum (of score + value exponent)
     float2 l2 = make_float2(0.f, 0.f);       // two halves of the sum
     bool ok = true;
-    for (int i = 0; i < steps; ++i) {
-      const int j = i >> 1, f = i & 1, ss = j % C::NSCL;
-      if (f == 0 && !warp_wait(bar(C::B_SCLFULL + ss), uint32_t(j / C::NSCL) & 1u, abort_flag, err, 9)) {
+    int last = -1;                           // step of this M tile: its turns' 2 t and 2 t + 1
+    for (int i = twin ? 2 * m : 0; i < steps; i += twin && (i & 1) ? 3 : 1) {
+      const int j = i >> 1, f = i & 1, ss = j % C::NSCL, turn = twin ? j >> 1 : j;
+      if (f == 0 && !wait_warp(bar(C::B_SCLFULL + ss), uint32_t(j / C::NSCL) & 1u, abort_flag, err, 9)) {
         ok = false;
         break;
       }
-      if (!warp_wait(bar(C::B_SFULL + 2 * m + f), uint32_t(j) & 1u, abort_flag, err, 10)) { ok = false; break; }
+      if (!wait_warp(bar(C::B_SFULL + 2 * m + f), uint32_t(turn) & 1u, abort_flag, err, 10)) { ok = false; break; }
+      if (idle) {
+        if (lane == 0) {
+          ptx::mbar_arrive(bar(C::B_PFULL + 2 * m + f));
+          if (f == 1 || i == steps - 1) ptx::mbar_arrive(bar(C::B_SCLFREE + ss));
+        }
+        __syncwarp();
+        last = 2 * turn + f;
+        continue;
+      }
       ptx::tc_fence_after();
       const uint32_t s_col = lane_base + uint32_t(128 * m + kStep * f);
       uint32_t s[2][32];
@@ -409,9 +461,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (raise) mx = top;
         l2.x *= alpha;
         l2.y *= alpha;
-        if (i > 0) {  // O holds the earlier steps' products once the last of them has ended
-          const int was = i - 1;
-          if (!warp_wait(bar(C::B_PDONE + 2 * m + (was & 1)), uint32_t(was >> 1) & 1u, abort_flag, err, 13)) {
+        if (last >= 0) {  // O holds the earlier steps' products once the last of them has ended
+          if (!wait_warp(bar(C::B_PDONE + 2 * m + (last & 1)), uint32_t(last >> 1) & 1u, abort_flag, err, 13)) {
             ok = false;
             break;
           }
@@ -455,12 +506,47 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         ptx::mbar_arrive(bar(C::B_PFULL + 2 * m + f));
         if (f == 1 || i == steps - 1) ptx::mbar_arrive(bar(C::B_SCLFREE + ss));
       }
+      last = 2 * turn + f;
     }
-    const float l = l2.x + l2.y;
-    if (ok && steps > 0)
-      ok = warp_wait(bar(C::B_PDONE + 2 * m + ((steps - 1) & 1)), uint32_t((steps - 1) >> 1) & 1u, abort_flag, err, 11);
+    float l = l2.x + l2.y;
+    if (ok && last >= 0)
+      ok = wait_warp(bar(C::B_PDONE + 2 * m + (last & 1)), uint32_t(last >> 1) & 1u, abort_flag, err, 11);
     ptx::tc_fence_after();
-    if (ok) {
+    // Both M tiles' results become the first's, through shared memory: once
+    // every softmax warp is here, all scores are read, and so are the queries and
+    // keys.  Four dimensions of all rows together: lanes are rows.
+    float4* const other = reinterpret_cast<float4*>(sbase + C::OFF_Q);
+    float2* const other_m = reinterpret_cast<float2*>(sbase + C::OFF_K);
+    float mine = 1.f, its = 0.f;  // factors of the two
+    if (twin) {
+      ptx::named_barrier(1, 256);
+      if (m == 1) {
+        other_m[row] = make_float2(mx, l);
+        if (ok && last >= 0) {
+#pragma unroll 1
+          for (int q = 0; q < D / 16; ++q) {
+            uint32_t v[16];
+            ptx::tmem_ld16(o_col + q * 16, v);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              other[(4 * q + e) * kTile + row] =
+                  make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]), __uint_as_float(v[4 * e + 2]),
+                              __uint_as_float(v[4 * e + 3]));
+          }
+        }
+      }
+      ptx::named_barrier(1, 256);
+      if (m == 0) {
+        const float2 ml = other_m[row];
+        const float top = fmaxf(mx, ml.x);
+        mine = mx == -INFINITY ? 0.f : ptx::ex2(mx - top);
+        its = ml.x == -INFINITY ? 0.f : ptx::ex2(ml.x - top);
+        l = (l != l ? l : mine * l) + (ml.y != ml.y ? ml.y : its * ml.y);  // NaN stays NaN
+        mx = top;
+      }
+    }
+    if (ok && (m == 0 || !twin)) {
       const bool single = p.splits == 1;
       const float inv = single ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
       const int64_t at = (int64_t(single ? 0 : split) * a.total_tokens + token) * a.num_heads + head;
@@ -474,7 +560,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[i] = 0u;
         }
-        __syncwarp();
+        if (twin) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * mine);
+          if (its > 0.f) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float4 x = other[(4 * q + e) * kTile + row];
+              v[4 * e] = __float_as_uint(fmaf(x.x, its, __uint_as_float(v[4 * e])));
+              v[4 * e + 1] = __float_as_uint(fmaf(x.y, its, __uint_as_float(v[4 * e + 1])));
+              v[4 * e + 2] = __float_as_uint(fmaf(x.z, its, __uint_as_float(v[4 * e + 2])));
+              v[4 * e + 3] = __float_as_uint(fmaf(x.w, its, __uint_as_float(v[4 * e + 3])));
+            }
+          }
+        }
         if (real && single) {
           uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + at * D + q * 16);
           uint32_t w[8];
@@ -488,6 +587,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) out[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
         }
+        __syncwarp();
       }
       if (real) {
         if (single)
@@ -513,7 +613,7 @@ attn_status launch_d(const CacheAttnParams& p, cudaStream_t s) {
   const CacheView& c = p.a.cache;
   // the keys' pages as rows of D bytes: (dimension, slot, head, page), one page
   // and head per copy
-  CUtensorMap map;
+  CUtensorMap map, map_v;
   auto fn = encode_fn();
   const int page_size = 1 << c.page_log2;
   cuuint64_t dims[4] = {cuuint64_t(D), cuuint64_t(page_size), cuuint64_t(c.heads), cuuint64_t(c.num_pages)};
@@ -522,14 +622,17 @@ attn_status launch_d(const CacheAttnParams& p, cudaStream_t s) {
   cuuint32_t estr[4] = {1, 1, 1, 1};
   const CUtensorMapSwizzle sw = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
                                 : D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
-  if (!fn || fn(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, c.k_pages, dims, strides, box, estr,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+  auto encode = [&](CUtensorMap* m, const void* pages, CUtensorMapSwizzle swizzle) {
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(pages), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  if (!fn || !encode(&map, c.k_pages, sw) || !encode(&map_v, c.v_pages, CU_TENSOR_MAP_SWIZZLE_NONE))
     return record_cuda_error(cudaErrorInvalidValue, "attn_cache_fwd tensor map encoding");
   cudaError_t e = cudaFuncSetAttribute(cache_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return record_cuda_error(e, "attn_cache_fwd configure");
   const dim3 grid(unsigned(p.splits) * unsigned(p.row_tiles), unsigned(c.heads), unsigned(c.batch));
-  cache_chunk_kernel<D><<<grid, kChunkThreads, C::SMEM, s>>>(map, p);
+  cache_chunk_kernel<D><<<grid, kChunkThreads, C::SMEM, s>>>(map, map_v, p);
   e = cudaGetLastError();
   return e == cudaSuccess ? ATTN_OK : record_cuda_error(e, "attn_cache_fwd launch");
 }
