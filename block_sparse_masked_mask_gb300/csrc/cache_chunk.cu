@@ -317,12 +317,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (!wait_warp(bar(C::B_RFULL + rs), uint32_t(j / C::NR) & 1u, abort_flag, err, 12)) break;
       uint4 next[PPT];
 #pragma unroll
-      for (int i = 0; i < PPT; ++i) {
-        const int x = i * 128 + ct, row = x / PPT;
-        next[i] = *reinterpret_cast<const uint4*>(sbase + C::OFF_R + rs * C::KT + x * 16);
+      for (int i = 0; i < PPT; ++i)
+        next[i] = *reinterpret_cast<const uint4*>(sbase + C::OFF_R + rs * C::KT + (i * 128 + ct) * 16);
+      const bool gone = __float_as_int(scl[ss * 8 + (lane & 7)].w) < 0;
+      if (__any_sync(0xffffffffu, gone) || begin + (j + 1) * kTile > end) {
         // behind the end, or without a page: weights of 0 times 0
-        if (begin + j * kTile + row >= end || __float_as_int(scl[ss * 8 + row / 16].w) < 0)
-          next[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < PPT; ++i) {
+          const int row = (i * 128 + ct) / PPT;
+          if (begin + j * kTile + row >= end || __float_as_int(scl[ss * 8 + row / 16].w) < 0)
+            next[i] = make_uint4(0, 0, 0, 0);
+        }
       }
       warp_arrive(bar(C::B_REMPTY + rs), lane);
       if (lane == 0) ptx::mbar_arrive(bar(C::B_SCLFREE + ss));
