@@ -155,6 +155,10 @@ attn_status attn_rope(const void* q, void* q_out, int64_t q_stride, int64_t q_ou
   const int64_t need_q = int64_t(num_heads) * head_dim, need_k = int64_t(num_kv_heads) * head_dim;
   if (total_tokens > 1 && (q_stride < need_q || q_out_stride < need_q)) return ATTN_ERR_INVALID_ARG;
   if (total_tokens > 1 && num_kv_heads > 0 && (k_stride < need_k || k_out_stride < need_k)) return ATTN_ERR_INVALID_ARG;
+  // in place, a token's row must be its own
+  if (total_tokens > 1 && ((q == q_out && q_stride != q_out_stride) ||
+                           (num_kv_heads > 0 && k == k_out && k_stride != k_out_stride)))
+    return ATTN_ERR_INVALID_ARG;
   if (total_tokens == 0) return ATTN_OK;
   RopeArgs a;
   a.q = q;

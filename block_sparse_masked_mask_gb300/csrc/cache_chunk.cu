@@ -8,8 +8,8 @@
 //  * S = Q K^T runs on the codes as they lie (kind::f8f6f4): the keys need no
 //    conversion.  A bf16 query has 8 significant bits and e4m3 4, so each row,
 //    scaled by a power of two to a largest value in [128, 256), is the sum of two
-//    e4m3 numbers, q = hi + lo, exact down to 2^-10 of that value and within
-//    2^-18 of it below; S is hi K^T + lo K^T in one accumulator, at the cost
+//    e4m3 numbers, q = hi + lo, exact down to 2^-9 of that value and within
+//    2^-17 of it below; S is hi K^T + lo K^T in one accumulator, at the cost
 //    of one fp16 product (e4m3 runs at twice the rate).
 //  * O += P V runs in fp16: weights keep 11 bits, the values are exact.  One
 //    warpgroup turns the codes into fp16 tiles in shared memory, once

@@ -100,8 +100,8 @@ ATTN_API attn_status attn_rope_plan_init(attn_rope_plan* plan, int32_t rotary_di
  * transposed matrix: the gradient of the rotation's input from that of its
  * output.
  *   q, q_out     [total_tokens, num_heads, head_dim]; heads are dense, tokens
- *                q_stride / q_out_stride elements apart.  q_out == q with the
- *                same stride rotates in place; other overlaps are not allowed.
+ *                q_stride / q_out_stride elements apart.  q_out == q rotates in
+ *                place and needs the same stride; no other overlaps.
  *   k, k_out     the same with num_kv_heads; NULL with num_kv_heads = 0
  *   dtype        of all four
  *   head_dim     32, 64 or 128, at least the plan's rotary_dim
@@ -179,10 +179,12 @@ ATTN_API attn_status attn_cache_fwd_workspace_size(const attn_kv_cache* cache, i
  *   workspace    256-byte aligned scratch of attn_cache_fwd_workspace_size()
  *                bytes, for this call alone while it runs; NULL if that is 0
  * Cached numbers inside a sequence must be finite, as for attn_bwd(); what
- * lies behind its end may hold anything.  e4m3 numbers are exact in the fp16
- * that the tensor cores take; q is scaled by a power of two per row and is
- * then exact in fp16 down to 2^-24 of its row's largest value; the weights are
- * rounded to fp16; sums are fp32.  Repeated calls are bit-identical.
+ * lies behind its end may hold anything.  Cached numbers enter the products
+ * exactly.  q is scaled by a power of two per row; up to 16 rows (max_new * G)
+ * it is then exact in fp16 down to 2^-24 of its row's largest value, with more
+ * rows it is the sum of two e4m3 numbers, exact down to 2^-9 of that value and
+ * within 2^-17 of it below.  The weights are rounded to fp16; sums are fp32.
+ * Repeated calls are bit-identical.  o may be q.
  */
 ATTN_API attn_status attn_cache_fwd(const void* q, void* o, float* lse, attn_dtype dtype,
                                     int32_t total_tokens, int32_t num_heads, float scale,

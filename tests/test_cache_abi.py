@@ -93,6 +93,8 @@ def test_rope_refuses_bad_arguments_before_any_launch(native_lib):
     assert call(D=96) == UNSUPPORTED
     assert call(D=32) == INVALID                      # the plan turns 64 dimensions
     assert call(qs=511) == INVALID and call(kos=255) == INVALID
+    assert call(q=fake(0x20000), qo=fake(0x20000), qos=1024) == INVALID  # in place, rows over other rows
+    assert call(k=fake(0x20000), ko=fake(0x20000), ks=1024) == INVALID
     assert call(q=fake(0x10001)) == INVALID and call(pos=fake(0x10002)) == INVALID
     assert call(dtype=1, k=fake(0x10002)) == INVALID
     assert call(plan=ctypes.byref(_native.AttnRopePlan())) == INVALID  # never initialised

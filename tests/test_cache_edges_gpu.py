@@ -1,0 +1,210 @@
+"""The cache operators at their edges: waits that run out, pools above 4 GiB,
+captured calls with a workspace of their own, aliased results, queries of a
+wide range, many short sequences.  Bounds are those of test_cache_gpu."""
+import numpy as np
+import pytest
+import torch
+
+from block_sparse_masked_mask_gb300 import _native, api
+from block_sparse_masked_mask_gb300 import build as B
+from oracle import cache as C
+from test_cache_gpu import Pair, check_attend, cu_of, dev, filled, randn, run_attend, run_evict, table_for
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ waits
+
+@pytest.fixture(scope="module")
+def short_wait_library():
+    return B.build_variant("waitshort", {"ATTN_WAIT_TIMEOUT_NS": "100ull"})
+
+
+@pytest.mark.parametrize("rows", [40, 300])
+def test_short_waits_run_out_and_the_launch_returns(short_wait_library, rows):
+    """With waits of 100 ns the tcgen05 kernel gives up, the status says so, later
+    launches return at once until it has been read, and the context stays usable."""
+    lens = [4000, 2500]
+    p = filled(lens, 2, 128, 64, seed=3)
+    cu, q = cu_of([rows // 2, rows // 2]), randn(rows, 4, 128, seed=1)
+    want = [x.clone() for x in check_attend(p, q, cu, lens)]
+    with _native.use_library(short_wait_library):
+        for _ in range(2):
+            run_attend(p, q, cu, lens)
+        assert api.attn_cache_get_status(p.dev) == api.ATTN_ERR_DEVICE_TIMEOUT
+        assert api.attn_cache_get_status(p.dev) == api.ATTN_OK
+        # single tokens need no such waits
+        one = run_attend(p, q[:2], cu_of([1, 1]), lens)
+        assert api.attn_cache_get_status(p.dev) == api.ATTN_OK
+        one = [x.clone() for x in one]
+    for a, b in zip(one, run_attend(p, q[:2], cu_of([1, 1]), lens)):
+        assert torch.equal(a, b)
+    for a, b in zip(want, run_attend(p, q, cu, lens)):
+        assert torch.equal(a, b)
+    assert api.attn_cache_get_status(p.dev) == api.ATTN_OK
+
+
+# ------------------------------------------------------------------ far pages
+
+class Far(Pair):
+    """A Pair whose device pages are the last ones of a pool above 4 GiB per side
+    (the oracle has them alone)."""
+
+    def __init__(self, lens, heads, dim, page_size, pool, seed, shared=None):
+        rng = np.random.default_rng(seed)
+        self.table, self.pages = table_for(lens, page_size, rng)
+        codes = [rng.integers(0, 256, (self.pages, heads, page_size, dim)).astype(np.uint8) for _ in range(2)]
+        scale = [2.0 ** rng.integers(-3, 4, (self.pages, heads)).astype(np.float64) for _ in range(2)]
+        self.ref = C.Cache(*codes, *scale, self.table)
+        self.first = (shared.first if shared else pool) - self.pages
+        if shared:
+            d = shared.dev
+            bufs = (d.k_pages, d.v_pages, d.k_scale, d.v_scale)
+        else:
+            bufs = [torch.zeros((pool, heads, page_size, dim), dtype=torch.uint8, device="cuda") for _ in range(2)]
+            bufs += [torch.ones((pool, heads), device="cuda") for _ in range(2)]
+        for buf, x in zip(bufs, codes + [s.astype(np.float32) for s in scale]):
+            buf[self.first:self.first + self.pages] = torch.from_numpy(x).cuda()
+        self.dev = api.KVCache(*bufs, torch.from_numpy(self.table + np.int32(self.first)).cuda())
+
+    def check_codes(self):
+        here = slice(self.first, self.first + self.pages)
+        for got, want in ((self.dev.k_pages, self.ref.codes[0]), (self.dev.v_pages, self.ref.codes[1])):
+            assert np.array_equal(got[here].cpu().numpy(), want)
+        for got, want in ((self.dev.k_scale, self.ref.scale[0]), (self.dev.v_scale, self.ref.scale[1])):
+            assert np.array_equal(got[here].cpu().double().numpy(), want)
+
+
+def test_pages_past_32_bits():
+    heads, dim, ps = 8, 128, 128
+    pool = (1 << 32) // (heads * dim * ps) + 64
+    lens = [700, 300]
+    p = Far(lens, heads, dim, ps, pool, seed=1)
+    assert int(p.dev.page_table[0, 0]) * heads * dim * ps > 2 ** 31
+    k, v = randn(1000, heads, dim, seed=1), randn(1000, heads, dim, seed=2)
+    p.append(k, v, cu_of(lens), lens)
+    p.check_codes()
+    _, lse = check_attend(p, randn(2, 16, dim, seed=3), cu_of([1, 1]), lens)
+    check_attend(p, randn(60, 16, dim, seed=4), cu_of([40, 20]), lens)
+    q = randn(2, 16, dim, seed=3)
+    w = api.attn_cache_weights(q.cuda(), lse, p.dev, dev([0, 1, 2]), dev(lens), 1, 700).cpu()
+    ref, _ = p.ref.weights(q.double().numpy(), lse.cpu().numpy(), cu_of([1, 1]), lens)
+    for b, n in enumerate(lens):
+        assert np.abs(w[b, :, :n].double().numpy() - ref[b]).max() <= 1e-4
+    dst = Far([200, 200], heads, dim, ps, pool, seed=2, shared=p)
+    run_evict(p, dst, w, lens, [200, 200], 32)
+    p.check_codes()
+
+
+# ------------------------------------------------------------------ capture
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_captured_calls_draw_workspaces_of_their_own(new):
+    """Two graphs of calls without a workspace argument, replayed alternately and
+    at once on two streams, between eager calls."""
+    cases = []
+    for seed, lens in ((1, [3000, 1500]), (2, [2600, 2900])):
+        p = filled(lens, 2, 128, 64, seed=seed)
+        cu, q = dev(cu_of([new, new])), randn(2 * new, 8, 128, seed=seed).cuda()
+        args = (q, p.dev, cu, dev(lens), new, max(lens))
+        assert api.attn_cache_fwd_workspace_size(p.dev, 2 * new, 8, new, max(lens)) > 0
+        want = [x.clone() for x in api.attn_cache_fwd(*args)]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = api.attn_cache_fwd(*args)
+        cases.append((graph, out, want, args))
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    for together in (False, True, False):
+        for _, out, _, _ in cases:
+            for x in out:
+                x.fill_(9)
+        torch.cuda.synchronize()
+        for side, (graph, out, want, args) in zip(sides, cases):
+            with torch.cuda.stream(side):
+                graph.replay()
+            if not together:
+                torch.cuda.synchronize()
+                junk = torch.full((1 << 22,), 7.0, device="cuda")  # what the allocator holds free is overwritten
+                for a, b in zip(want, api.attn_cache_fwd(*args)):
+                    assert torch.equal(a, b)
+                del junk
+        torch.cuda.synchronize()
+        for _, out, want, _ in cases:
+            assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+# ------------------------------------------------------------------ arguments that the documentation allows
+
+@pytest.mark.parametrize("new", [1, 3, 20, 200])
+@pytest.mark.parametrize("length", [400, 5000])
+def test_results_over_the_queries(new, length):
+    lens = [length, 300]
+    p = filled(lens, 2, 64, 32, seed=7)
+    cu, q = cu_of([new, new]), randn(2 * new, 6, 64, seed=1).cuda()
+    want = [x.clone() for x in run_attend(p, q, cu, lens)]
+    o, lse = run_attend(p, q, cu, lens, out=q)
+    assert o is q and torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+def test_a_page_twice_in_one_sequence():
+    p = filled([192, 64], 2, 64, 64, seed=9)
+    p.table[0, 2] = p.table[0, 0]
+    p.dev.page_table.copy_(torch.from_numpy(p.table))
+    p.ref.table = p.table
+    for new in (1, 30):
+        check_attend(p, randn(2 * new, 4, 64, seed=1), cu_of([new, new]), [192, 64])
+
+
+def test_workspaces_that_do_not_fit():
+    p = filled([3000], 1, 64, 32, seed=2)
+    q, cu, lens = randn(1, 4, 64).cuda(), dev([0, 1]), dev([3000])
+    need = api.attn_cache_fwd_workspace_size(p.dev, 1, 4, 1, 3000)
+    ws = torch.empty(need + 512, dtype=torch.uint8, device="cuda")
+    api.attn_cache_fwd(q, p.dev, cu, lens, 1, 3000, workspace=ws[256:])
+    for bad in (ws[1:], ws[128:], ws[:need].cpu()):
+        with pytest.raises(api.AttnError):
+            api.attn_cache_fwd(q, p.dev, cu, lens, 1, 3000, workspace=bad)
+
+
+@pytest.mark.parametrize("new", [1, 2])
+def test_thousands_of_short_sequences(new):
+    """More sequences than a CTA's threads and than the GPU's CTAs, some empty, some
+    without new tokens."""
+    rng = np.random.default_rng(4)
+    n = rng.integers(0, new + 1, 3000)
+    lens = [int(x) for x in n + rng.integers(0, 40, 3000)]
+    p = filled(lens, 1, 32, 16, seed=11)
+    cu = cu_of(n)
+    q = randn(int(cu[-1]), 2, 32, seed=12)
+    check_attend(p, q, cu, lens, max_new=new)
+    o, lse = run_attend(p, q, cu, lens, max_new=new)
+    w = api.attn_cache_weights(q.cuda(), lse, p.dev, dev(cu), dev(lens), new, max(lens)).cpu()
+    ref, _ = p.ref.weights(q.double().numpy(), lse.cpu().numpy(), cu, lens)
+    for b, L in enumerate(lens):
+        if L:
+            assert np.abs(w[b, :, :L].double().numpy() - ref[b]).max() <= 1e-4
+
+
+@pytest.mark.parametrize("rows", [1, 48, 200])
+def test_queries_of_a_wide_range(rows):
+    """Elements from 2^-14 of the row's largest up: with many rows an element below
+    2^-9 of the largest, m, may be off by 2^-17 m, a score by scale 2^-17 m
+    sum |k|, on top of the usual bounds."""
+    lens = [500]
+    p = filled(lens, 1, 64, 64, seed=21, spread=False)
+    g = torch.Generator().manual_seed(1)
+    q = torch.randn((rows, 1, 64), generator=g) * 2.0 ** torch.randint(-14, 1, (rows, 1, 64), generator=g)
+    q = (4 * q).to(torch.bfloat16)
+    o, lse = run_attend(p, q, cu_of([rows]), lens)
+    O, L, terms, spread = p.ref.attend(q.double().numpy(), cu_of([rows]), lens)
+    K = np.abs(p.ref.numbers(0, 0, 500)).sum(-1).max()
+    m = np.abs(q.double().numpy()).max(-1)
+    off = 0.0 if rows <= 16 else 2.0 ** -17 * m * K / 8  # [rows, 1]
+    A = terms[0].max()
+    rel = 2 * ((64 + 4) * 2.0 ** -24 * A) + 2.0 ** -22 + 2.0 ** -23 * (2 * A + 16) + 500 * 2.0 ** -24
+    assert (np.abs(lse.double().cpu().numpy() - L) <= rel + np.transpose(off + 0 * m) + 2.0 ** -22 * np.abs(L)).all()
+    small = 2.0 ** -25 * p.ref.code_sums(1, 0, 500)[None]
+    # each weight moves by e^+-(off + rel), the sum too
+    tol = (2.0 ** -11 + 3 * rel + 2 * np.expm1(2 * (off + 0 * m))[..., None]) * spread + small
+    tol = tol * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(O)
+    assert (np.abs(o.double().cpu().numpy() - O) <= tol).all()
