@@ -114,6 +114,7 @@ uint64_t cache_fwd_workspace(const CacheView& c, int total_tokens, int num_heads
 attn_status launch_cache_fwd(const CacheQueryArgs& a, cudaStream_t s);
 attn_status launch_cache_chunk(const CacheAttnParams& p, cudaStream_t s);
 attn_status launch_cache_weights(const CacheQueryArgs& a, cudaStream_t s);
+attn_status launch_cache_weights_many(const CacheQueryArgs& a, int sms, cudaStream_t s);
 attn_status launch_cache_evict(const EvictArgs& a, cudaStream_t s);
 
 // ---------------------------------------------------------------- device side

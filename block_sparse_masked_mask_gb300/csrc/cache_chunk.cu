@@ -40,8 +40,7 @@
 // an earlier step's events of the others, or for this step's by a role that
 // comes before it (pages, keys / values, S, softmax, P V), so the order of steps
 // carries every wait to its end.
-#include "cache_rows.cuh"
-#include "tile_pipeline.cuh"
+#include "cache_tiles.cuh"
 
 namespace attnmask {
 namespace {
@@ -50,27 +49,10 @@ constexpr int kChunkThreads = 512;
 constexpr int kWarpValues = 8, kWarpKeys = 12, kWarpS = 13, kWarpPV = 15;
 constexpr int kStep = 64;  // tokens per step
 
-// The bounded waits of tile_pipeline.cuh behind one inlined try: five roles run
-// at once, and their loops are fastest when they are short (the instruction
-// caches; with the whole wait inlined everywhere 4 prompts of 300 to 512 tokens
-// took 378 us, so 358).
-__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, int32_t* err,
-                                       int site) {
-  return wait_bar(bar, parity, abort_flag, err, site);
-}
-__device__ __forceinline__ bool wait_lane(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, int32_t* err,
-                                          int site) {
-  return ptx::mbar_try_wait(bar, parity) || wait_long(bar, parity, abort_flag, err, site);
-}
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, int32_t* err,
-                                          int site) {
-  return __all_sync(0xffffffffu, wait_lane(bar, parity, abort_flag, err, site));
-}
-
 template <int D>
 struct ChunkCfg {
   using V = TileLayout<D>;                     // fp16 value tile: the 16-bit layout
-  static constexpr int KT = kTile * D;         // bytes of a tile of codes (keys, or half a query)
+  static constexpr int KT = CodeTile<D>::BYTES;  // a tile of codes: keys, values or half a query
   static constexpr int VT = V::TILE;
   static constexpr int NK = 2, NR = 2, NV = 2, NSCL = 4;
   static constexpr int OFF_Q = 0;              // [M tile][hi, lo]
@@ -91,12 +73,6 @@ struct ChunkCfg {
   // one CTA per SM: it takes all of TMEM
   static constexpr int SMEM = USED > 116 * 1024 ? USED : 116 * 1024;
   static_assert(SMEM <= 232448, "shared memory budget");
-  // rows of D bytes, swizzled over their own width
-  static constexpr uint32_t SW8 = D == 128 ? ptx::kSwizzle128B : D == 64 ? ptx::kSwizzle64B : ptx::kSwizzle32B;
-  __device__ static uint32_t unit8(int row, int u) {  // byte offset of 16-byte unit u of a row
-    const int x = D == 128 ? (row & 7) : D == 64 ? ((row >> 1) & 3) : ((row >> 2) & 1);
-    return uint32_t(row * D + ((u ^ x) << 4));
-  }
   __device__ static uint32_t unit16(int row, int u) {  // of the fp16 layout's row chunk
     const int x = V::ROWB == 128 ? (row & 7) : ((row >> 1) & 3);
     return uint32_t(row * V::ROWB + ((u ^ x) << 4));
@@ -180,16 +156,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     // nothing issued, nothing to drain
   } else if (warp == kWarpKeys) {
     // -------------------------------------------------------------- pages, scales, keys
-    // Lane i < 8: the i-th 16 tokens of a tile.  Page numbers are read two tiles
-    // ahead, scales one, so that neither read is waited for.
+    // Eight lanes a tile, one per 16 tokens: lanes 8 q .. 8 q + 7 look up the q-th
+    // tile of four.  Page numbers are read two fours ahead, scales one, so that
+    // neither read is waited for.
     const int step = (1 << c.page_log2) / 16;  // lanes per page
-    auto number = [&](int j) {
-      const int tok = begin + j * kTile + lane * 16;
-      return lane < 8 && tok < end ? __ldg(c.table + int64_t(b) * c.max_pages + (tok >> c.page_log2)) : 0;
-    };
+    auto token = [&](int j) { return begin + j * kTile + lane * 16; };  // of the four from j
+    auto number = [&](int j) { return page_number(c, b, token(j), token(j) < end); };
     auto scales = [&](int j, int id) {
-      const int tok = begin + j * kTile + lane * 16;
-      const bool fine = lane < 8 && tok < end && unsigned(id) < unsigned(c.num_pages);
+      const bool fine = token(j) < end && in_pool(c, id);
       const int64_t at = fine ? int64_t(id) * c.heads + h : 0;
       return make_float2(fine ? __ldg(c.k_scale + at) : 0.f, fine ? __ldg(c.v_scale + at) : 0.f);
     };
@@ -197,44 +171,45 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       ptx::prefetch_tensormap(&tmK);
       ptx::prefetch_tensormap(&tmV);
     }
-    int id = number(0), id_next = number(1);
-    float2 sc = scales(0, id);
+    int id = 0, id_next = number(0), id_after = number(4);
+    float2 sc = make_float2(0.f, 0.f), sc_next = scales(0, id_next);
     int done = 0, done_v = 0;
     for (int j = 0; j < tiles; ++j) {
-      const int id_after = number(j + 2);
-      const float2 sc_next = scales(j + 1, id_next);
+      if ((j & 3) == 0) {
+        id = id_next;
+        id_next = id_after;
+        id_after = number(j + 8);
+        sc = sc_next;
+        sc_next = scales(j + 4, id_next);
+      }
       const int ss = j % C::NSCL, slot = j % C::NK;
-      const int tok = begin + j * kTile + lane * 16;
-      const bool here = lane < 8 && tok < end, fine = here && unsigned(id) < unsigned(c.num_pages);
+      const bool mine = lane >> 3 == (j & 3), here = mine && token(j & ~3) < end, fine = here && in_pool(c, id);
       if (here && !fine) atomicOr(err, kErrBadPage);
       if (j >= C::NSCL && !wait_warp(bar(C::B_SCLFREE + ss), uint32_t(j / C::NSCL - 1) & 1u, abort_flag, err, 1))
         break;
-      if (lane < 8) {
+      if (mine) {
         const int x = exponent_of(sc.y);
-        scl[ss * 8 + lane] = fine ? make_float4(sc.x, float(x), pow2f(max(-126, -x)), __int_as_float(id))
+        scl[ss * 8 + (lane & 7)] = fine ? make_float4(sc.x, float(x), pow2f(max(-126, -x)), __int_as_float(id))
                                   : make_float4(0.f, 0.f, 0.f, __int_as_float(-1));
       }
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar(C::B_SCLFULL + ss));
       if (j >= C::NK && !wait_warp(bar(C::B_KEMPTY + slot), uint32_t(j / C::NK - 1) & 1u, abort_flag, err, 2)) break;
-      const bool load = fine && lane % step == 0;  // one lane per page
+      const bool load = fine && lane % step == 0;  // one lane per page (eight lanes are whole pages)
       const uint32_t loads = __ballot_sync(0xffffffffu, load);
       const uint32_t piece = uint32_t(D) << c.page_log2;  // bytes of a page's keys
       if (lane == 0) ptx::mbar_arrive_expect_tx(bar(C::B_KFULL + slot), piece * __popc(loads));
       __syncwarp();
       if (load)
-        ptx::tma_load_4d(base + C::OFF_K + slot * C::KT + lane * 16 * D, &tmK, bar(C::B_KFULL + slot), 0, 0, h, id);
+        ptx::tma_load_4d(base + C::OFF_K + slot * C::KT + (lane & 7) * 16 * D, &tmK, bar(C::B_KFULL + slot), 0, 0, h, id);
       done = j + 1;
       const int rs = j % C::NR;
       if (j >= C::NR && !wait_warp(bar(C::B_REMPTY + rs), uint32_t(j / C::NR - 1) & 1u, abort_flag, err, 12)) break;
       if (lane == 0) ptx::mbar_arrive_expect_tx(bar(C::B_RFULL + rs), piece * __popc(loads));
       __syncwarp();
       if (load)
-        ptx::tma_load_4d(base + C::OFF_R + rs * C::KT + lane * 16 * D, &tmV, bar(C::B_RFULL + rs), 0, 0, h, id);
+        ptx::tma_load_4d(base + C::OFF_R + rs * C::KT + (lane & 7) * 16 * D, &tmV, bar(C::B_RFULL + rs), 0, 0, h, id);
       done_v = j + 1;
-      id = id_next;
-      id_next = id_after;
-      sc = sc_next;
     }
     // do not leave while a copy may still be writing shared memory
     if (lane == 0) {
@@ -284,9 +259,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const int m = warp - kWarpS;
     if (lane == 0) {
       constexpr uint32_t IDESC = ptx::idesc_e4m3_f32(128, kStep);
-      const uint64_t qhi = ptx::smem_desc(base + C::OFF_Q + 2 * m * C::KT, 16u, 8 * D, C::SW8);
-      const uint64_t qlo = ptx::smem_desc(base + C::OFF_Q + (2 * m + 1) * C::KT, 16u, 8 * D, C::SW8);
-      const uint64_t kd = ptx::smem_desc(base + C::OFF_K, 16u, 8 * D, C::SW8);
+      const uint64_t qhi = ptx::smem_desc(base + C::OFF_Q + 2 * m * C::KT, 16u, 8 * D, CodeTile<D>::SW);
+      const uint64_t qlo = ptx::smem_desc(base + C::OFF_Q + (2 * m + 1) * C::KT, 16u, 8 * D, CodeTile<D>::SW);
+      const uint64_t kd = ptx::smem_desc(base + C::OFF_K, 16u, 8 * D, CodeTile<D>::SW);
       const bool ok = steps == 0 || wait_lane(bar(C::B_Q + m), 0, abort_flag, err, 3);
       for (int i = twin ? 2 * m : 0; ok && i < steps; i += twin && (i & 1) ? 3 : 1) {
         const int j = i >> 1, ks = j % C::NK, f = i & 1, turn = twin ? j >> 1 : j;
@@ -363,48 +338,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const int visible = visible_tokens(r, p.G, rg, a.causal);
     const bool idle = rg - lane >= r.n * p.G;     // a warp without rows only keeps the steps' order
 
-    // the row's query as hi + lo
-    float qscale;
-    {
-      uint4 q[D / 8];
-      float amax = 0.f;
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                        (token * a.num_heads + head) * D);
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        q[i] = real ? src[i] : make_uint4(0, 0, 0, 0);
-        const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
-      }
-      const int e = amax > 0.f ? max(-119, min(126, exponent_of(amax))) : 0;
-      const float f = pow2f(7 - e);
-      // an infinite query has no scores
-      qscale = (amax < INFINITY ? pow2f(e - 7) : __int_as_float(0x7FC00000)) * p.scale_log2;
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int e4 = 0; e4 < 4; ++e4) {
-          const uint4 v = q[2 * i + (e4 >> 1)];
-          const uint32_t w0 = (e4 & 1) ? v.z : v.x, w1 = (e4 & 1) ? v.w : v.y;
-          const float x0 = __uint_as_float(w0 << 16) * f, x1 = __uint_as_float(w0 & 0xFFFF0000u) * f;
-          const float x2 = __uint_as_float(w1 << 16) * f, x3 = __uint_as_float(w1 & 0xFFFF0000u) * f;
-          const uint32_t h0 = e4m3_pair(x0, x1), h1 = e4m3_pair(x2, x3);
-          uint32_t y0 = half2_of(h0), y1 = half2_of(h1);
-          const float2 z0 = __half22float2(*reinterpret_cast<__half2*>(&y0));
-          const float2 z1 = __half22float2(*reinterpret_cast<__half2*>(&y1));
-          hi[e4] = h0 | (h1 << 16);
-          lo[e4] = e4m3_pair(x0 - z0.x, x1 - z0.y) | (e4m3_pair(x2 - z1.x, x3 - z1.y) << 16);
-        }
-        const uint32_t at = C::OFF_Q + (2 * m) * C::KT + C::unit8(row, i);
-        *reinterpret_cast<uint4*>(sbase + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(sbase + at + C::KT) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      }
-      ptx::fence_proxy_async_smem();
-      warp_arrive(bar(C::B_Q + m), lane);
-    }
+    const float qscale =
+        p.scale_log2 * split_query<D>(static_cast<const __nv_bfloat16*>(a.q) + (token * a.num_heads + head) * D, real,
+                                      sbase + C::OFF_Q + 2 * m * C::KT, row);
+    ptx::fence_proxy_async_smem();
+    warp_arrive(bar(C::B_Q + m), lane);
 
     float mx = -INFINITY;                    // running maximum (of score + value exponent)
     float2 l2 = make_float2(0.f, 0.f);       // two halves of the sum
@@ -616,23 +554,8 @@ template <int D>
 attn_status launch_d(const CacheAttnParams& p, cudaStream_t s) {
   using C = ChunkCfg<D>;
   const CacheView& c = p.a.cache;
-  // the keys' pages as rows of D bytes: (dimension, slot, head, page), one page
-  // and head per copy
   CUtensorMap map, map_v;
-  auto fn = encode_fn();
-  const int page_size = 1 << c.page_log2;
-  cuuint64_t dims[4] = {cuuint64_t(D), cuuint64_t(page_size), cuuint64_t(c.heads), cuuint64_t(c.num_pages)};
-  cuuint64_t strides[3] = {cuuint64_t(D), cuuint64_t(D) * page_size, cuuint64_t(D) * page_size * c.heads};
-  cuuint32_t box[4] = {cuuint32_t(D), cuuint32_t(page_size), 1, 1};
-  cuuint32_t estr[4] = {1, 1, 1, 1};
-  const CUtensorMapSwizzle sw = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
-                                : D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
-  auto encode = [&](CUtensorMap* m, const void* pages, CUtensorMapSwizzle swizzle) {
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(pages), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-  };
-  if (!fn || !encode(&map, c.k_pages, sw) || !encode(&map_v, c.v_pages, CU_TENSOR_MAP_SWIZZLE_NONE))
+  if (!encode_pages<D>(&map, c, c.k_pages, true) || !encode_pages<D>(&map_v, c, c.v_pages, false))
     return record_cuda_error(cudaErrorInvalidValue, "attn_cache_fwd tensor map encoding");
   cudaError_t e = cudaFuncSetAttribute(cache_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return record_cuda_error(e, "attn_cache_fwd configure");

@@ -203,6 +203,7 @@ ATTN_API attn_status attn_cache_fwd(const void* q, void* o, float* lse, attn_dty
  *                prev == weights adds in place
  *   weights      the same shape; weight_stride >= max_seqlen.  Entries at and
  *                behind seq_lens[b] keep what they held.
+ * q enters as in attn_cache_fwd(), its second form from more than 24 rows on.
  * Sums are fp32 in a fixed order: repeated calls are bit-identical.
  */
 ATTN_API attn_status attn_cache_weights(const void* q, const float* lse, attn_dtype dtype,

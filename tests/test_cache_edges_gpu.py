@@ -20,6 +20,21 @@ def short_wait_library():
     return B.build_variant("waitshort", {"ATTN_WAIT_TIMEOUT_NS": "100ull"})
 
 
+@pytest.mark.parametrize("new", [40, 300])
+def test_short_waits_of_the_weights_run_out(short_wait_library, new):
+    lens = [4000, 2500]
+    p = filled(lens, 2, 128, 64, seed=3)
+    cu, q = cu_of([new // 2, new // 2]), randn(new, 4, 128, seed=1)
+    args = (q.cuda(), run_attend(p, q, cu, lens)[1], p.dev, dev(cu), dev(lens), new // 2, 4000)
+    want = api.attn_cache_weights(*args)
+    with _native.use_library(short_wait_library):
+        for _ in range(2):
+            api.attn_cache_weights(*args)
+        assert api.attn_cache_get_status(p.dev) == api.ATTN_ERR_DEVICE_TIMEOUT
+    assert torch.equal(want, api.attn_cache_weights(*args))
+    assert api.attn_cache_get_status(p.dev) == api.ATTN_OK
+
+
 @pytest.mark.parametrize("rows", [40, 300])
 def test_short_waits_run_out_and_the_launch_returns(short_wait_library, rows):
     """With waits of 100 ns the tcgen05 kernel gives up, the status says so, later
@@ -208,3 +223,59 @@ def test_queries_of_a_wide_range(rows):
     tol = (2.0 ** -11 + 3 * rel + 2 * np.expm1(2 * (off + 0 * m))[..., None]) * spread + small
     tol = tol * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(O)
     assert (np.abs(o.double().cpu().numpy() - O) <= tol).all()
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dim,page_size,heads,group,new", [
+    (128, 64, 2, 1, [25, 0, 3, 25]), (64, 16, 1, 5, [64, 1, 0, 60]), (32, 128, 3, 2, [70, 64, 1, 129]),
+    (128, 32, 1, 8, [64, 9, 33, 0]), (128, 128, 2, 2, [150, 1, 2, 300])])
+def test_weights_of_many_rows(dim, page_size, heads, group, new, causal):
+    """More than 24 rows, in one and in several passes of 128; sequences without
+    queries; sums on top of others, in place too.  Every score may be off by the
+    usual roundings and by scale 2^-17 m sum |k|, m the row's largest element."""
+    lens = [700, 64, 130, 1300]
+    p = filled(lens, heads, dim, page_size, seed=dim + page_size, spread=False)
+    cu = cu_of(new)
+    q = randn(int(cu[-1]), heads * group, dim, seed=5)
+    _, lse = run_attend(p, q, cu, lens, causal)
+    g = torch.Generator().manual_seed(2)
+    before = torch.rand((4, heads, 1301), generator=g)
+    ref, terms = p.ref.weights(q.double().numpy(), lse.cpu().numpy(), cu, lens, causal)
+    args = (q.cuda(), lse, p.dev, dev(cu), dev(lens), max(new), 1300, "causal" if causal else "none")
+    out = torch.full((4, heads, 1301), 3.0, device="cuda")
+    apart = api.attn_cache_weights(*args, prev=before.cuda(), out=out)
+    x = before.cuda()
+    assert torch.equal(api.attn_cache_weights(*args, prev=x, out=x)[:, :, :64], apart[:, :, :64])
+    alone = api.attn_cache_weights(*args)
+    assert api.attn_cache_get_status(p.dev) == api.ATTN_OK
+    for got, was, behind in ((apart, before, 3.0), (x, before, None), (alone, 0 * before, 0.0)):
+        got = got.double().cpu().numpy()
+        for b, n in enumerate(lens):
+            A = terms[b].max(initial=0)
+            m = np.abs(q[cu[b]:cu[b + 1]].double().numpy()).max(initial=0)
+            off = 2.0 ** -17 * m * np.abs(p.ref.numbers(0, b, n)).sum(-1).max() / np.sqrt(dim)
+            rel = 2 * (dim + 4) * 2.0 ** -24 * A + 2.0 ** -22 + 2.0 ** -22 * (2 * A + 16) + new[b] * group * 2.0 ** -24
+            w = was[b, :, :n].double().numpy()
+            err = np.abs(got[b, :, :n] - (w + ref[b]))
+            # a pass of 128 rows adds to what the last one left: a rounding of the sum each
+            assert (err <= (rel + np.expm1(off)) * ref[b] + (-(-new[b] * group // 128) + 1) * 2.0 ** -24 * (w + ref[b])
+                    + 1e-37).all()
+            want = was[b, :, n:got.shape[2]].double().numpy() if behind is None else behind
+            assert (got[b, :, n:] == want).all()
+
+
+def test_weights_of_many_rows_leave_out_bad_pages():
+    p = filled([300, 200], 2, 64, 32, seed=1)
+    cu, lens = dev([0, 40, 80]), dev([300, 200])
+    q = randn(80, 4, 64, seed=1).cuda()
+    lse = torch.zeros((4, 80), device="cuda")
+    good = api.attn_cache_weights(q, lse, p.dev, cu, lens, 40, 300)
+    for bad in (-1, p.dev.num_pages):
+        was = p.dev.page_table[0, 2].item()
+        p.dev.page_table[0, 2] = bad
+        got = api.attn_cache_weights(q, lse, p.dev, cu, lens, 40, 300)
+        assert api.attn_cache_get_status(p.dev) == api.ATTN_ERR_DEVICE_INVALID_INPUT
+        assert (got[0, :, 64:96] == 0).all()
+        got[0, :, 64:96] = good[0, :, 64:96]
+        assert torch.equal(got, good)
+        p.dev.page_table[0, 2] = was
