@@ -17,6 +17,9 @@
 // keys (three slots), 5 tcgen05 issuer and owner of TMEM (two S buffers of 128 columns).
 // Scales lie in a ring of eight slots without a barrier for their reuse: the keys
 // of tile j have waited for the products of j - 3, those for the epilogue of j - 5.
+// Measured (there: with mma.sync, cache_weights.cu), D = 128: 8 sequences of 16 heads,
+// 32 rows 18 us (there 21), 64 rows 22 (32); 4 of 8192, 8 heads, 512 rows 81 (158).
+// The starts bound it: a change of queries costs 3 to 4 us, a tile about 0.6.
 // Every wait is bounded and ends in ATTN_ERR_DEVICE_TIMEOUT; each is for an
 // earlier tile's event of the others, or for this tile's by a role that comes
 // before it (queries, keys, S, epilogue).
