@@ -279,3 +279,40 @@ def test_weights_of_many_rows_leave_out_bad_pages():
         got[0, :, 64:96] = good[0, :, 64:96]
         assert torch.equal(got, good)
         p.dev.page_table[0, 2] = was
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_attention_and_weights_of_many_rows_at_once(dim):
+    """Two streams, both kernels on the tensor cores; captured and replayed with other
+    lengths and queries too."""
+    lens = [3000, 1800, 2500]
+    p = filled(lens, 2, dim, 64, seed=5)
+    cu, q = cu_of([40, 40, 40]), randn(120, 4, dim, seed=1).cuda()
+    d_cu, d_lens = dev(cu), dev(lens)
+    attend = lambda **kw: api.attn_cache_fwd(q, p.dev, d_cu, d_lens, 40, 3000, **kw)  # noqa: E731
+    o, lse = [x.clone() for x in attend()]
+    weigh = lambda **kw: api.attn_cache_weights(q, lse, p.dev, d_cu, d_lens, 40, 3000, **kw)  # noqa: E731
+    w = weigh().clone()
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(10):
+        outs.append((attend(stream=sides[0]), weigh(stream=sides[1])))
+    torch.cuda.synchronize()
+    for (a, b), c in outs:
+        assert torch.equal(a, o) and torch.equal(b, lse) and torch.equal(c, w)
+    assert api.attn_cache_get_status(p.dev) == api.ATTN_OK
+
+    go, glse, gw = torch.empty_like(o), torch.empty_like(lse), torch.zeros_like(w)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        attend(out=go, lse=glse)
+        api.attn_cache_weights(q, glse, p.dev, d_cu, d_lens, 40, 3000, out=gw)
+    new = [40, 1799, 2000]
+    q.copy_(randn(120, 4, dim, seed=2))
+    d_lens.copy_(dev(new))
+    graph.replay()
+    torch.cuda.synchronize()
+    want_o, want_lse = attend()
+    want_w = api.attn_cache_weights(q, want_lse, p.dev, d_cu, d_lens, 40, 3000)
+    assert torch.equal(go, want_o) and torch.equal(glse, want_lse) and torch.equal(gw, want_w)
