@@ -146,15 +146,6 @@ __device__ __forceinline__ bool load_rows(const int32_t* cu, const int32_t* lens
   return err == 0;
 }
 
-// Page `i` of sequence b, or -1 (and a note in the status word) if its number
-// is outside the pool.  i < max_pages is the caller's.
-__device__ __forceinline__ int load_page(const CacheView& c, int b, int i) {
-  const int id = __ldg(c.table + int64_t(b) * c.max_pages + i);
-  if (unsigned(id) < unsigned(c.num_pages)) return id;
-  atomicOr(c.status, kErrBadPage);
-  return -1;
-}
-
 __device__ __forceinline__ float pow2f(int e) {  // -126 <= e <= 127
   return __int_as_float((e + 127) << 23);
 }

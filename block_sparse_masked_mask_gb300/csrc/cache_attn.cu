@@ -462,7 +462,9 @@ bool take_whole(const CacheQueryArgs& a) {
 
 // Which kernel, and its cut.  More than 16 rows of a key / value head go to the
 // tcgen05 kernel (cache_chunk.cu), which reads the cache once for 256, one CTA per
-// SM.  Its chunks are of one size: the least number of chunks (of 4096 tokens at
+// SM: measured here / there, 16 sequences of 8192, 8 heads, 4 rows 54 / 88 us, 16 rows
+// 62 / 89 (there 20 rows 90, 32 rows 90, 128 rows 108); one of 8192, 16 rows 18 / 19.
+// Its chunks are of one size: the least number of chunks (of 4096 tokens at
 // most), or as many as fill the SMs one to four times, whichever is quickest in
 // this estimate, in tokens of a CTA's walk (11 to 20 ns each): a chunk with its
 // start and end (384) times the waves, half rounded up, as sequences differ in

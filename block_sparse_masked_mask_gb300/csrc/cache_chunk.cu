@@ -25,7 +25,7 @@
 //   8-11       values: codes to fp16 tiles (two slots)
 //   12         pages, scales (four slots) and TMA of the codes (two slots each
 //              of keys and values; reads by the value warps themselves came a
-//              latency late: the 32 rows above 108 -> 92 us)
+//              latency late: the 32 rows above 108 -> 91 us)
 //   13, 14     tcgen05 issuers of S, one per M tile
 //   15         tcgen05 issuer of P V for both M tiles (also owns TMEM)
 // Keys and values come in tiles of 128 tokens; the products and the softmax go
@@ -36,7 +36,7 @@
 // tile took 6200 cycles, most of it with the tensor cores idle.)
 // TMEM columns: S of M tile m, buffer f at 128 m + 64 f; O at 256 + 128 m.
 // Measured, D = 128: 4 prompts of 300 to 512 new tokens behind 4096 to 16384, 32 / 8
-// heads 348 us, 42% of the bf16 rate; one of 2048 behind 14336 534 us, 51%.  A tile of
+// heads 334 us, 44% of the bf16 rate; one of 2048 behind 14336 530 us, 51%.  A tile of
 // 256 rows and 128 tokens takes about 3700 cycles: its score products 1570 (49 each,
 // their operands from shared memory; the pipe alone 32), its weight products 1040, and
 // each M tile's chain of products and softmax (1000 cycles per step) goes on through them.
@@ -340,7 +340,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const bool real = rg < r.n * p.G;
     const int64_t token = r.q0 + (real ? rg / p.G : 0);
     const int head = h * p.G + (real ? rg % p.G : 0);
-    const int visible = visible_tokens(r, p.G, rg, a.causal);
+    // (a lane without a row hides nothing: one hidden score sends its warp the slow way)
+    const int visible = real ? visible_tokens(r, p.G, rg, a.causal) : limit;
     const bool idle = rg - lane >= r.n * p.G;     // a warp without rows only keeps the steps' order
 
     const float qscale =
