@@ -85,7 +85,7 @@ struct CacheAttnParams {
   bool many;       // the tcgen05 kernel
   int row_tiles, chunk, splits;  // many: tiles of kManyRows rows, tokens per chunk, chunks
   int ctas;        // few: CTAs
-  bool whole;      // few: a CTA per (sequence, head)
+  int team;        // few: CTAs per (sequence, head), a cluster; 0: the line is cut
   float scale_log2;
   // Results before the division, and (running maximum, sum).
   //   many: [splits][total_tokens * num_heads] rows

@@ -22,8 +22,10 @@
 // more than 2^8.
 // A (sequence, head) that lies in one CTA's piece is finished there; the others
 // meet in a second kernel through fp32 partial results, two per CTA at most.
+// Few or short sequences go another way: a cluster of up to eight CTAs takes each
+// (sequence, head) and joins its results through shared memory (team_of).
 // Measured, 64 requests of 1024 to 16384 tokens, 8 heads, D = 128: 118 us, 84% of the
-// copy rate; 16 of 8192, 16 rows 62 us, 64%; a single one of 2049 tokens 11 us.
+// copy rate; 16 of 8192, 16 rows 62 us, 64%; a single one of 2049 tokens 8.4 us.
 #include <cmath>
 
 #include "cache_rows.cuh"
@@ -34,6 +36,7 @@ namespace {
 
 constexpr int kAttnThreads = 32 * kWarps;
 constexpr int kStages = 4;  // of the queue, groups
+constexpr int kTeam = 8;    // CTAs of a cluster
 constexpr float kRaise = 8.f;
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -44,7 +47,8 @@ struct AttnCfg {
   static constexpr int QUEUE = kWarps * kStages * STAGE;
   static constexpr int MERGE = kWarps * kFewRows * D * 4;  // over the queue
   static constexpr int STATS = QUEUE > MERGE ? QUEUE : MERGE;
-  static constexpr int SMEM = STATS + kWarps * kFewRows * 8;
+  static constexpr int TEAM = STATS + kWarps * kFewRows * 8;  // the CTA's own, for its team
+  static constexpr int SMEM = TEAM + kFewRows * 8;
 };
 
 // Units of sequence b and all heads: of the tokens that some row sees, at least
@@ -73,6 +77,49 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   return y;
 }
 
+// A cluster's results meet in each other's shared memory: every CTA joins its share
+// of the rows' elements, in the order of the ranks.
+template <int D>
+__device__ __forceinline__ void team_join(const CacheAttnParams& p, int b, int h, int rank, const float* mo,
+                                          const float2* own) {
+  const CacheQueryArgs& a = p.a;
+  SeqRows r;
+  load_rows(a.cu, a.lens, b, a.total_tokens, a.max_new, a.max_seqlen, a.cache.status, r, false);
+  const int rows = r.n * p.G;
+  ptx::cluster_sync();
+  for (int at = (rank * kAttnThreads + threadIdx.x) * 4; at < rows * D; at += p.team * kAttnThreads * 4) {
+    const int row = at / D, d = at % D;
+    float2 s[kTeam];
+    float top = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kTeam; ++k) {
+      s[k] = k < p.team ? ptx::load_peer(own + row, k) : make_float2(-INFINITY, 0.f);
+      top = fmaxf(top, s[k].x);
+    }
+    float sum = 0.f;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kTeam; ++k) {
+      const float f = s[k].x == -INFINITY ? 0.f : ptx::ex2(s[k].x - top);
+      sum += s[k].y != s[k].y ? s[k].y : f * s[k].y;
+      if (f > 0.f) {
+        const float4 z = ptx::load_peer(reinterpret_cast<const float4*>(mo + row * D + d), k);
+        y.x = fmaf(f, z.x, y.x);
+        y.y = fmaf(f, z.y, y.y);
+        y.z = fmaf(f, z.z, y.z);
+        y.w = fmaf(f, z.w, y.w);
+      }
+    }
+    const int head = h * p.G + row % p.G;
+    const int64_t token = r.q0 + row / p.G;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + (token * a.num_heads + head) * D + d) =
+        make_uint2(ptx::pack_bf16(y.x * inv, y.y * inv), ptx::pack_bf16(y.z * inv, y.w * inv));
+    if (d == 0) a.lse[int64_t(head) * a.total_tokens + token] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+  }
+  ptx::cluster_sync();  // nobody leaves while others read
+}
+
 // NT: tiles of 8 rows
 template <int D, int NT>
 __global__ void __launch_bounds__(kAttnThreads, 3) cache_attn_kernel(const CacheAttnParams p) {
@@ -83,11 +130,14 @@ __global__ void __launch_bounds__(kAttnThreads, 3) cache_attn_kernel(const Cache
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int b, pos, stop, before = 0;
-  if (p.whole) {
-    b = blockIdx.x / c.heads;
-    const int U = AttnUnits{p, blockIdx.x % c.heads == 0}(b) / c.heads;
-    pos = (blockIdx.x % c.heads) * U;
-    stop = pos + U;
+  const int rank = p.team > 1 ? blockIdx.x % p.team : 0;  // in the cluster
+  if (p.team > 0) {
+    const int item = blockIdx.x / p.team, h = item % c.heads;
+    b = item / c.heads;
+    const int U = AttnUnits{p, h == 0 && rank == 0}(b) / c.heads;
+    if (U == 0) return;  // the whole team
+    pos = h * U + int(int64_t(U) * rank / p.team);
+    stop = h * U + int(int64_t(U) * (rank + 1) / p.team);
   } else {
     const AttnUnits units{p, blockIdx.x == 0};
     const UnitLine line(units, c.batch, lane);
@@ -96,12 +146,14 @@ __global__ void __launch_bounds__(kAttnThreads, 3) cache_attn_kernel(const Cache
     stop = min(pos + piece, line.total);
     if (pos < stop) b = line.find(units, c.batch, lane, pos, before);
   }
-  if (pos >= stop) return;
+  if (pos >= stop && p.team <= 1) return;
 
   uint8_t* queue = smem + warp * kStages * C::STAGE;
   const uint32_t queue_addr = ptx::smem_addr(queue);
   float* mo = reinterpret_cast<float*>(smem);                  // [warp][8 NT][D]
   float2* ml = reinterpret_cast<float2*>(smem + C::STATS);     // [warp][8 NT]
+  float2* own = reinterpret_cast<float2*>(smem + C::TEAM);     // [8 NT]: of the CTA, with its O in mo's first part
+  if (threadIdx.x < kFewRows) own[threadIdx.x] = make_float2(-INFINITY, 0.f);
 
   while (pos < stop) {
     // ---- the segment: units u0 .. u1 - 1 of sequence b, head h
@@ -282,7 +334,7 @@ __global__ void __launch_bounds__(kAttnThreads, 3) cache_attn_kernel(const Cache
         for (int k = 0; k < D / 16; ++k) to[k] = make_float2(o[k][nt][e], o[k][nt][2 + e]);
       }
     __syncthreads();
-    const bool whole = u0 == 0 && u1 == U;
+    const bool whole = p.team <= 1 && u0 == 0 && u1 == U;
     const int slot = 2 * blockIdx.x + (u0 > 0 ? 0 : 1);
     for (int at = threadIdx.x * 4; at < rows * D; at += kAttnThreads * 4) {
       const int row = at / D, d = at % D;
@@ -309,6 +361,9 @@ __global__ void __launch_bounds__(kAttnThreads, 3) cache_attn_kernel(const Cache
         *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + (token * a.num_heads + head) * D + d) =
             make_uint2(ptx::pack_bf16(y.x * inv, y.y * inv), ptx::pack_bf16(y.z * inv, y.w * inv));
         if (d == 0) a.lse[int64_t(head) * a.total_tokens + token] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+      } else if (p.team > 0) {
+        *reinterpret_cast<float4*>(mo + row * D + d) = y;  // (read by this thread alone)
+        if (d == 0) own[row] = make_float2(top, sum);
       } else {
         const int64_t to = int64_t(slot) * (a.max_new * p.G) + row;
         *reinterpret_cast<float4*>(p.part_o + to * D + d) = y;
@@ -317,11 +372,12 @@ __global__ void __launch_bounds__(kAttnThreads, 3) cache_attn_kernel(const Cache
     }
     __syncthreads();  // before the next segment's copies
     pos += u1 - u0;
-    if (pos == before + U * c.heads) {
+    if (pos == before + U * c.heads && p.team == 0) {
       before = pos;
       ++b;
     }
   }
+  if (p.team > 1) team_join<D>(p, b, blockIdx.x / p.team % c.heads, rank, mo, own);
 }
 
 // Joins a row's partial results in their order: `n` of them, the i-th at row
@@ -450,14 +506,22 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_many_kernel(const 
   join_row<D, 1>(p, max(1, (limit + p.chunk - 1) / p.chunk), at, token, head, 0, lane, nullptr);
 }
 
-// Whether a CTA takes a (sequence, head) whole, so that nothing is joined: where
-// the sequences are short, and up to 1024 tokens where all of them fill the GPU
-// about once.  Measured, split / whole, D = 128: 8 heads of one sequence, 512
-// tokens 8.4 / 7.6 us, 1024 8.8 / 11.0; of 16 sequences, 512 13.7 / 7.9, 1024 16.3 /
-// 12.2, 2048 21.7 / 19.7; of 64 sequences, 512 22.6 / 20.5, 1024 31.5 / 34.3.
-bool take_whole(const CacheQueryArgs& a) {
+// CTAs that take a (sequence, head) together, as one cluster whose results meet in
+// shared memory, with one launch and no workspace; 0: the line of all tokens is cut
+// and joined.  As many as the GPU holds at once (456), for up to 1024 tokens each:
+// above that, and for sequences of which one alone is long, the line is more
+// even.  Measured, line / cluster, D = 128, 8 heads: 1 sequence of 700 tokens 10.2 /
+// 7.2 us, 2049 10.9 / 8.4, 8192 13.4 / 13.3, 16384 16.7 / 20.8; with 16 rows, 2049 15.6 /
+// 10.8; 4 of 3000 14.0 / 9.9, of 6000 18.5 / 14.7; 8 of 3000 18.8 / 14.4; 16 of 2000 21.1 /
+// 17.1.  Short sequences are quickest by one CTA: 8 of 300 tokens, by 4 CTAs 7.9 us, by
+// one 6.9; 16 of 700, by two 10.0, by one 9.7; 64 of 700, by one 23, the line 27.
+int team_of(const CacheQueryArgs& a) {
   const int64_t items = int64_t(a.cache.batch) * a.cache.heads;
-  return a.max_seqlen <= 512 || (a.max_seqlen <= 1024 && items >= 64 && items <= 456);
+  if (a.max_seqlen <= 384) return 1;
+  int team = kTeam;
+  while (team > 1 && items * team > 456) team /= 2;
+  if (team <= 2 && a.max_seqlen <= 768) return 1;
+  return items * team <= 456 && a.max_seqlen <= 1024 * team ? team : 0;
 }
 
 // Which kernel, and its cut.  More than 16 rows of a key / value head go to the
@@ -480,8 +544,8 @@ void plan(CacheAttnParams* p) {
   p->G = a.num_heads / a.cache.heads;
   const int64_t rows = int64_t(a.max_new) * p->G;
   p->many = rows > kFewRows;
-  p->whole = take_whole(a);
-  p->ctas = p->whole ? a.cache.batch * a.cache.heads : 3 * kSms;  // (three per SM are resident at once)
+  p->team = team_of(a);
+  p->ctas = p->team ? a.cache.batch * a.cache.heads * p->team : 3 * kSms;  // (three per SM are resident at once)
   p->row_tiles = int((rows + kManyRows - 1) / kManyRows);
   const int64_t items = int64_t(p->row_tiles) * a.cache.heads * a.cache.batch;
   p->chunk = 256;
@@ -509,7 +573,7 @@ void plan(CacheAttnParams* p) {
 // Rows of partial results.
 uint64_t partial_rows(const CacheAttnParams& p) {
   if (p.many) return p.splits == 1 ? 0 : uint64_t(p.splits) * uint64_t(p.a.total_tokens) * uint64_t(p.a.num_heads);
-  return p.whole ? 0 : 2 * uint64_t(p.ctas) * uint64_t(p.a.max_new) * uint64_t(p.G);
+  return p.team ? 0 : 2 * uint64_t(p.ctas) * uint64_t(p.a.max_new) * uint64_t(p.G);
 }
 
 template <int D>
@@ -518,8 +582,18 @@ cudaError_t launch_few(const CacheAttnParams& p, cudaStream_t s) {
   auto kernel = p.a.max_new * p.G <= 8 ? cache_attn_kernel<D, 1> : cache_attn_kernel<D, 2>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  kernel<<<unsigned(p.ctas), kAttnThreads, C::SMEM, s>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(p.ctas));
+  cfg.blockDim = dim3(kAttnThreads);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = unsigned(p.team > 1 ? p.team : 1);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 // The joining kernel is launched early and waits for the first one's end.

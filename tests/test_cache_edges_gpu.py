@@ -118,7 +118,7 @@ def test_captured_calls_draw_workspaces_of_their_own(new):
     """Two graphs of calls without a workspace argument, replayed alternately and
     at once on two streams, between eager calls."""
     cases = []
-    for seed, lens in ((1, [3000, 1500]), (2, [2600, 2900])):
+    for seed, lens in ((1, [9000, 1500]), (2, [8600, 8900])):
         p = filled(lens, 2, 128, 64, seed=seed)
         cu, q = dev(cu_of([new, new])), randn(2 * new, 8, 128, seed=seed).cuda()
         args = (q, p.dev, cu, dev(lens), new, max(lens))
@@ -151,7 +151,7 @@ def test_captured_calls_draw_workspaces_of_their_own(new):
 # ------------------------------------------------------------------ arguments that the documentation allows
 
 @pytest.mark.parametrize("new", [1, 3, 20, 200])
-@pytest.mark.parametrize("length", [400, 5000])
+@pytest.mark.parametrize("length", [400, 5000, 20000])
 def test_results_over_the_queries(new, length):
     lens = [length, 300]
     p = filled(lens, 2, 64, 32, seed=7)
@@ -171,14 +171,14 @@ def test_a_page_twice_in_one_sequence():
 
 
 def test_workspaces_that_do_not_fit():
-    p = filled([3000], 1, 64, 32, seed=2)
-    q, cu, lens = randn(1, 4, 64).cuda(), dev([0, 1]), dev([3000])
-    need = api.attn_cache_fwd_workspace_size(p.dev, 1, 4, 1, 3000)
+    p = filled([9000], 1, 64, 32, seed=2)
+    q, cu, lens = randn(1, 4, 64).cuda(), dev([0, 1]), dev([9000])
+    need = api.attn_cache_fwd_workspace_size(p.dev, 1, 4, 1, 9000)
     ws = torch.empty(need + 512, dtype=torch.uint8, device="cuda")
-    api.attn_cache_fwd(q, p.dev, cu, lens, 1, 3000, workspace=ws[256:])
+    api.attn_cache_fwd(q, p.dev, cu, lens, 1, 9000, workspace=ws[256:])
     for bad in (ws[1:], ws[128:], ws[:need].cpu()):
         with pytest.raises(api.AttnError):
-            api.attn_cache_fwd(q, p.dev, cu, lens, 1, 3000, workspace=bad)
+            api.attn_cache_fwd(q, p.dev, cu, lens, 1, 9000, workspace=bad)
 
 
 @pytest.mark.parametrize("new", [1, 2])
@@ -316,3 +316,25 @@ def test_attention_and_weights_of_many_rows_at_once(dim):
     want_o, want_lse = attend()
     want_w = api.attn_cache_weights(q, want_lse, p.dev, d_cu, d_lens, 40, 3000)
     assert torch.equal(go, want_o) and torch.equal(glse, want_lse) and torch.equal(gw, want_w)
+
+
+@pytest.mark.parametrize("new,group", [(1, 1), (1, 8), (4, 4), (2, 5)])
+@pytest.mark.parametrize("batch,heads,most", [(1, 1, 8192), (1, 1, 8193), (3, 2, 5000), (2, 20, 4096), (5, 20, 2000),
+                                              (20, 10, 900), (20, 10, 1025), (9, 30, 800), (48, 10, 700)])
+def test_sequences_cut_in_every_way(batch, heads, most, new, group):
+    """A (sequence, head) by one CTA, by clusters of 2, 4 and 8, and on the cut line;
+    lengths from 0 up, shorter than the cluster has pieces, uneven."""
+    rng = np.random.default_rng(batch * most)
+    n = [int(x) for x in rng.integers(0, new + 1, batch)]
+    n[0] = new
+    lens = [max(a, int(most * rng.random() ** 3)) for a in n]
+    lens[0] = most
+    if batch > 2:
+        lens[1], lens[2] = max(n[1], 60), n[2]
+    p = filled(lens, heads, 32, 32, seed=batch)
+    cu, q = cu_of(n), randn(sum(n) + 2, heads * group, 32, seed=most)
+    for causal in (True, False):
+        o, lse = check_attend(p, q, cu, lens, causal)
+        for a, b in zip((o, lse), run_attend(p, q, cu, lens, causal)):
+            rows = sum(n)
+            assert torch.equal(a[:rows] if a is o else a[:, :rows], b[:rows] if a is o else b[:, :rows])

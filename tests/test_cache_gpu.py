@@ -564,11 +564,11 @@ def test_the_binding_refuses_what_the_kernels_would_misread():
     for call in bad:
         with pytest.raises(api.AttnError):
             call()
-    big = filled([3000], 1, 64, 32, seed=2)
-    need = api.attn_cache_fwd_workspace_size(big.dev, 1, 4, 1, 3000)
+    big = filled([9000], 1, 64, 32, seed=2)
+    need = api.attn_cache_fwd_workspace_size(big.dev, 1, 4, 1, 9000)
     assert need > 0
     with pytest.raises(api.AttnError) as e:
-        api.attn_cache_fwd(q, big.dev, cu, dev([3000]), 1, 3000,
+        api.attn_cache_fwd(q, big.dev, cu, dev([9000]), 1, 9000,
                            workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
     assert e.value.status == api.ATTN_ERR_WORKSPACE_TOO_SMALL
 
