@@ -85,10 +85,13 @@ __device__ __forceinline__ bool position_of(const RopeArgs& a, int t, int& pos) 
 }
 
 // A unit is VP pairs: for the half layout VP elements of each half, for the
-// interleaved one 2 VP consecutive elements.  Units behind rot are copied.  A
+// interleaved one 2 VP consecutive elements.  What lies behind rot is copied.  A
 // pass of a warp covers 32 units: whole heads, or half a head where a head has 64.
+// PART: an interleaved unit lies partly behind rot, so that any rot is taken by
+// wide accesses (rot = 50, 10400 tokens of 40 heads of 128 bf16: 37 us; by the
+// accesses that divide rot 133).
 // (Three CTAs per SM fit fp32 without spills and are 5% faster; bf16 needs the registers.)
-template <typename T, int VP, bool INTER>
+template <typename T, int VP, bool INTER, bool PART>
 __global__ void __launch_bounds__(32 * kRopeWarps, sizeof(T) == 4 ? 3 : 1) rope_kernel(const __grid_constant__ RopeParams p) {
   __shared__ float2 cs[kRopeWarps][ATTN_ROPE_MAX_PAIRS];
   const RopeArgs& a = p.a;
@@ -97,7 +100,8 @@ __global__ void __launch_bounds__(32 * kRopeWarps, sizeof(T) == 4 ? 3 : 1) rope_
   const int t = int(job / p.slices), slice = int(job % p.slices);
   if (t >= a.total_tokens) return;
   const int heads = a.num_heads + a.num_kv_heads;
-  const int turned = p.rot / (2 * VP);  // units of a head that are rotated
+  // units of a head that are rotated; the last interleaved one may be in part
+  const int turned = (p.rot + (PART ? 2 * VP - 1 : 0)) / (2 * VP);
   const int units = 1 << p.unit_log2;
   const T* q = static_cast<const T*>(a.q) + int64_t(t) * a.q_stride;
   const T* k = static_cast<const T*>(a.k) + int64_t(t) * a.k_stride;
@@ -112,11 +116,11 @@ __global__ void __launch_bounds__(32 * kRopeWarps, sizeof(T) == 4 ? 3 : 1) rope_
   for (int block = 0; block < blocks; ++block) {
     const int u = block * 32 + (lane & (units - 1));
     int d0, d1;
-    if (u >= turned) {
-      d0 = p.rot + (u - turned) * 2 * VP;
-      d1 = d0 + VP;
-    } else if (INTER) {
+    if (INTER) {
       d0 = u * 2 * VP;
+      d1 = d0 + VP;
+    } else if (u >= turned) {
+      d0 = p.rot + (u - turned) * 2 * VP;
       d1 = d0 + VP;
     } else {
       d0 = u * VP;
@@ -145,7 +149,7 @@ __global__ void __launch_bounds__(32 * kRopeWarps, sizeof(T) == 4 ? 3 : 1) rope_
     }
     float2 c[VP];
 #pragma unroll
-    for (int e = 0; e < VP; ++e) c[e] = u < turned ? cs[warp][u * VP + e] : make_float2(1.f, 0.f);
+    for (int e = 0; e < VP; ++e) c[e] = (PART ? u * VP + e < p.rot / 2 : u < turned) ? cs[warp][u * VP + e] : make_float2(1.f, 0.f);
     for (int h = h0; h < last; h += kRopeUnroll * per_pass) {
 #pragma unroll
       for (int j = 0; j < kRopeUnroll; ++j) {
@@ -157,6 +161,7 @@ __global__ void __launch_bounds__(32 * kRopeWarps, sizeof(T) == 4 ? 3 : 1) rope_
             // the half layout pairs x with y; the interleaved one neighbours
             T* px = INTER ? (2 * e < VP ? &x[j].x[2 * e] : &y[j].x[2 * e - VP]) : &x[j].x[e];
             T* py = INTER ? (2 * e + 1 < VP ? &x[j].x[2 * e + 1] : &y[j].x[2 * e + 1 - VP]) : &y[j].x[e];
+            if (PART && u * VP + e >= p.rot / 2) continue;  // copied
             const float fx = to_f(*px), fy = to_f(*py);
             from_f(*px, fx * c[e].x - fy * c[e].y);
             from_f(*py, fy * c[e].x + fx * c[e].y);
@@ -174,19 +179,19 @@ __global__ void __launch_bounds__(32 * kRopeWarps, sizeof(T) == 4 ? 3 : 1) rope_
 template <typename T, int VP>
 cudaError_t launch_vp(const RopeParams& p, bool interleaved, cudaStream_t s) {
   const unsigned grid = unsigned((int64_t(p.a.total_tokens) * p.slices + kRopeWarps - 1) / kRopeWarps);
-  if (interleaved)
-    rope_kernel<T, VP, true><<<grid, 32 * kRopeWarps, 0, s>>>(p);
-  else
-    rope_kernel<T, VP, false><<<grid, 32 * kRopeWarps, 0, s>>>(p);
+  const bool part = p.rot % (2 * VP) != 0;
+  auto kernel = !interleaved ? rope_kernel<T, VP, false, false>
+                             : part ? rope_kernel<T, VP, true, VP != 1> : rope_kernel<T, VP, true, false>;
+  kernel<<<grid, 32 * kRopeWarps, 0, s>>>(p);
   return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t launch_t(RopeParams& p, bool interleaved, cudaStream_t s) {
   const RopeArgs& a = p.a;
-  // The widest access (up to 16 bytes) that pairs, addresses and strides allow.
+  // The widest access (up to 16 bytes) that the halves, addresses and strides allow.
   constexpr int kMost = 16 / sizeof(T);
-  uint64_t bits = uint64_t(p.rot / 2) * sizeof(T);
+  uint64_t bits = interleaved ? 0 : uint64_t(p.rot / 2) * sizeof(T);
   bits |= uint64_t(reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.q_out));
   bits |= uint64_t(a.q_stride | a.q_out_stride) * sizeof(T);
   if (a.num_kv_heads) {
