@@ -19,7 +19,7 @@ namespace attnmask {
 namespace {
 
 constexpr int kRopeWarps = 8;
-constexpr int kRopeUnroll = 4;  // units in flight per lane
+constexpr int kRopeUnroll = 4;  // units in flight per lane (even)
 
 struct RopeParams {
   RopeArgs a;
@@ -84,6 +84,20 @@ __device__ __forceinline__ bool position_of(const RopeArgs& a, int t, int& pos) 
   return t >= s0 && t < s1;
 }
 
+// The warp's table of (cos, sin) for row t, the factor multiplied in; false if the row has no position.
+__device__ __forceinline__ bool angles(const RopeParams& p, int t, int lane, float2* cs) {
+  int pos;
+  if (!position_of(p.a, t, pos)) return false;
+  for (int c = lane; c < p.rot / 2; c += 32) {
+    const int64_t turn = int64_t(uint64_t(int64_t(pos)) * p.turn[c]);
+    float sn, cn;
+    sincospif(float(int32_t(turn >> 32)) * 0x1p-31f, &sn, &cn);
+    cs[c] = make_float2(cn * p.factor, (p.a.inverse ? -sn : sn) * p.factor);
+  }
+  __syncwarp();
+  return true;
+}
+
 // A unit is VP pairs: for the half layout VP elements of each half, for the
 // interleaved one 2 VP consecutive elements.  What lies behind rot is copied.  A
 // pass of a warp covers 32 units: whole heads, or half a head where a head has 64.
@@ -136,17 +150,7 @@ __global__ void __launch_bounds__(32 * kRopeWarps, sizeof(T) == 4 ? 3 : 1) rope_
     };
 #pragma unroll
     for (int j = 0; j < kRopeUnroll; ++j) load(j, h0 + j * per_pass);
-    if (block == 0) {
-      int pos;
-      if (!position_of(a, t, pos)) return;  // the whole warp
-      for (int c = lane; c < p.rot / 2; c += 32) {
-        const int64_t turn = int64_t(uint64_t(int64_t(pos)) * p.turn[c]);
-        float sn, cn;
-        sincospif(float(int32_t(turn >> 32)) * 0x1p-31f, &sn, &cn);
-        cs[warp][c] = make_float2(cn * p.factor, (a.inverse ? -sn : sn) * p.factor);
-      }
-      __syncwarp();
-    }
+    if (block == 0 && !angles(p, t, lane, cs[warp])) return;  // the whole warp
     float2 c[VP];
 #pragma unroll
     for (int e = 0; e < VP; ++e) c[e] = (PART ? u * VP + e < p.rot / 2 : u < turned) ? cs[warp][u * VP + e] : make_float2(1.f, 0.f);
@@ -176,6 +180,70 @@ __global__ void __launch_bounds__(32 * kRopeWarps, sizeof(T) == 4 ? 3 : 1) rope_
   }
 }
 
+// The half layout where rot / 2 is no multiple of a wide access: a lane takes W
+// consecutive elements as they lie, and finds each one's partner, rot / 2 away, in
+// a copy of the warp's heads in shared memory.
+template <typename T, int W>
+__global__ void __launch_bounds__(32 * kRopeWarps) rope_halves_kernel(const __grid_constant__ RopeParams p) {
+  __shared__ float2 cs[kRopeWarps][ATTN_ROPE_MAX_PAIRS];
+  __shared__ alignas(16) T copies[kRopeWarps][2][32 * W];
+  const RopeArgs& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t job = int64_t(blockIdx.x) * kRopeWarps + warp;
+  const int t = int(job / p.slices), slice = int(job % p.slices);
+  if (t >= a.total_tokens) return;
+  const int heads = a.num_heads + a.num_kv_heads, half = p.rot / 2;
+  const int per_pass = 32 >> p.unit_log2;  // heads
+  const int first = slice * p.passes * per_pass, last = min(heads, first + p.passes * per_pass);
+  const int d0 = (lane & ((1 << p.unit_log2) - 1)) * W, h0 = first + (lane >> p.unit_log2);
+  const T* q = static_cast<const T*>(a.q) + int64_t(t) * a.q_stride + d0;
+  const T* k = static_cast<const T*>(a.k) + int64_t(t) * a.k_stride + d0;
+  T* qo = static_cast<T*>(a.q_out) + int64_t(t) * a.q_out_stride + d0;
+  T* ko = static_cast<T*>(a.k_out) + int64_t(t) * a.k_out_stride + d0;
+  Vec<T, W> x[kRopeUnroll];
+  auto load = [&](int j, int i) {
+    if (i < last) load_vec(x[j], i < a.num_heads ? q + i * a.head_dim : k + (i - a.num_heads) * a.head_dim);
+  };
+#pragma unroll
+  for (int j = 0; j < kRopeUnroll; ++j) load(j, h0 + j * per_pass);
+  if (!angles(p, t, lane, cs[warp])) return;  // the whole warp
+  float2 c[W];  // y = x c.x + partner c.y
+  int from[W];  // the partner's place in the copy
+#pragma unroll
+  for (int e = 0; e < W; ++e) {
+    const int d = d0 + e, i = d < half ? d : d - half;
+    c[e] = d < p.rot ? cs[warp][i] : make_float2(1.f, 0.f);
+    if (d < half) c[e].y = -c[e].y;
+    from[e] = lane * W + e + (d < half ? half : d < p.rot ? -half : 0);
+  }
+  const int rounds = (last - first + per_pass - 1) / per_pass;
+  for (int r = 0; r < rounds; r += kRopeUnroll) {
+#pragma unroll
+    for (int j = 0; j < kRopeUnroll; ++j) {
+      if (r + j >= rounds) break;  // the whole warp
+      T* copy = copies[warp][j & 1];
+      *reinterpret_cast<Vec<T, W>*>(copy + lane * W) = x[j];
+      __syncwarp();  // (and the copy before the last one has been read)
+      const int i = h0 + (r + j) * per_pass;
+      Vec<T, W> y;
+#pragma unroll
+      for (int e = 0; e < W; ++e) {
+        y.x[e] = x[j].x[e];
+        if (d0 + e < p.rot) from_f(y.x[e], to_f(x[j].x[e]) * c[e].x + to_f(copy[from[e]]) * c[e].y);
+      }
+      if (i < last) store_vec(i < a.num_heads ? qo + i * a.head_dim : ko + (i - a.num_heads) * a.head_dim, y);
+      load(j, i + kRopeUnroll * per_pass);
+    }
+  }
+}
+
+template <typename T, int W>
+cudaError_t launch_halves(const RopeParams& p, cudaStream_t s) {
+  const unsigned grid = unsigned((int64_t(p.a.total_tokens) * p.slices + kRopeWarps - 1) / kRopeWarps);
+  rope_halves_kernel<T, W><<<grid, 32 * kRopeWarps, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
 template <typename T, int VP>
 cudaError_t launch_vp(const RopeParams& p, bool interleaved, cudaStream_t s) {
   const unsigned grid = unsigned((int64_t(p.a.total_tokens) * p.slices + kRopeWarps - 1) / kRopeWarps);
@@ -191,17 +259,23 @@ cudaError_t launch_t(RopeParams& p, bool interleaved, cudaStream_t s) {
   const RopeArgs& a = p.a;
   // The widest access (up to 16 bytes) that the halves, addresses and strides allow.
   constexpr int kMost = 16 / sizeof(T);
-  uint64_t bits = interleaved ? 0 : uint64_t(p.rot / 2) * sizeof(T);
-  bits |= uint64_t(reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.q_out));
+  uint64_t bits = uint64_t(reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.q_out));
   bits |= uint64_t(a.q_stride | a.q_out_stride) * sizeof(T);
   if (a.num_kv_heads) {
     bits |= uint64_t(reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.k_out));
     bits |= uint64_t(a.k_stride | a.k_out_stride) * sizeof(T);
   }
-  int vp = kMost;
+  int wide = kMost, vp = kMost;
+  while (wide > 1 && (bits & (wide * sizeof(T) - 1))) wide >>= 1;
+  if (!interleaved) bits |= uint64_t(p.rot / 2) * sizeof(T);
   while (vp > 1 && (bits & (vp * sizeof(T) - 1))) vp >>= 1;
+  // Halves at odd places: by wide accesses and shared memory, where pairs would be read
+  // one or two at a time (16 x 650 tokens of 40 heads of 128, pairs / copies: rot = 50 bf16
+  // 71 / 53 us, fp32 82 / 78; rot = 52 78 / 53, 96 / 78; but rot = 40 bf16, by fours, 37 / 52).
+  const bool halves = vp < 4 && wide >= 4 && wide * 32 >= a.head_dim;
+  const int unit = halves ? wide : 2 * vp;  // elements
   p.unit_log2 = 0;
-  while ((2 * vp << p.unit_log2) < a.head_dim) ++p.unit_log2;
+  while ((unit << p.unit_log2) < a.head_dim) ++p.unit_log2;
   // Warps per token: one, or more while there are fewer warps than the GPU
   // holds (32 per SM), down to one pass each.
   const int units = 1 << p.unit_log2, heads = a.num_heads + a.num_kv_heads;
@@ -213,6 +287,11 @@ cudaError_t launch_t(RopeParams& p, bool interleaved, cudaStream_t s) {
   const int want = (32 * sms + a.total_tokens - 1) / a.total_tokens;
   p.passes = (all + want - 1) / want;
   p.slices = (all + p.passes - 1) / p.passes;
+  if (halves) {
+    if constexpr (kMost >= 8)
+      if (wide == 8) return launch_halves<T, 8>(p, s);
+    return launch_halves<T, 4>(p, s);
+  }
   switch (vp) {
     case 8: if constexpr (kMost >= 8) return launch_vp<T, 8>(p, interleaved, s);
     case 4: return launch_vp<T, 4>(p, interleaved, s);

@@ -214,23 +214,28 @@ def test_captured_replay_and_other_stream():
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("D,rot", [(32, 2), (32, 30), (64, 34), (128, 4), (128, 52), (128, 102), (128, 126)])
-def test_interleaved_pairs_that_end_inside_an_access(D, rot, dtype):
-    """What lies behind the rotated dimensions is copied bit for bit, infinities and NaN too."""
+@pytest.mark.parametrize("interleaved", [True, False])
+def test_rotated_widths_that_no_access_divides(D, rot, dtype, interleaved):
+    """What lies behind the rotated dimensions is copied bit for bit, infinities and NaN too;
+    in place as well."""
     T, H = 37, 3
     x = torch.randn((T, H, D), generator=torch.Generator().manual_seed(rot)).to(dtype)
     x[::3, :, rot:] = float("inf")
     x[1::3, :, rot:] = float("nan")
     positions = torch.arange(T, dtype=torch.int32) * 1000
-    plan = api.attn_rope_plan(rot, interleaved=True)
+    plan = api.attn_rope_plan(rot, interleaved=interleaved)
     y, _ = api.attn_rope(x.cuda(), None, plan, positions=positions.cuda())
-    y = y.cpu()
+    same = x.cuda()
+    api.attn_rope(same, None, plan, positions=positions.cuda(), q_out=same)
     as_ints = torch.int16 if dtype == torch.bfloat16 else torch.int32
+    assert torch.equal(same.view(as_ints), y.view(as_ints))
+    y = y.cpu()
     assert torch.equal(y[..., rot:].contiguous().view(as_ints), x[..., rot:].contiguous().view(as_ints))
     part = x.clone()
     part[..., rot:] = 0
     z, _ = api.attn_rope(part.cuda(), None, plan, positions=positions.cuda())
     assert torch.equal(y[..., :rot], z.cpu()[..., :rot])
-    back, _ = api.attn_rope(y.cuda(), None, plan, positions=positions.cuda(), inverse=True, q_out=y.cuda())
+    back, _ = api.attn_rope(y.cuda(), None, plan, positions=positions.cuda(), inverse=True)
     # two rotations: per element two products and a sum, twice, on values up to sqrt(2) max |x|,
     # sines and cosines to 2^-22, each result rounded once
     half_step = torch.finfo(dtype).eps / 2
