@@ -9,7 +9,7 @@
 // the result does not depend on any order.  Bound: each new element is read
 // once (2 or 4 bytes) and written once (1 byte).  A CTA's teams take different
 // heads of one page.  (Held in registers instead, the elements leave room for
-// two CTAs per SM and the latencies of the lookups show: 47 us instead of 37
+// two CTAs per SM and the latencies of the lookups show: 47 us instead of 36
 // for 14000 tokens of 16 heads.)  The pages of all
 // sequences form one line (cache_rows.cuh), a CTA per page, so that ragged
 // batches launch few empty CTAs.
@@ -59,8 +59,10 @@ struct NewPages {
   }
 };
 
+// (Six CTAs per SM: 36.0 us for those 14000 tokens; five, as the compiler would have it,
+// 36.9, seven 38.4.)
 template <typename T>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a, int team_log2) {
+__global__ void __launch_bounds__(kAppendThreads, 6) append_kernel(const AppendArgs a, int team_log2) {
   using C = Chunk<T>;
   extern __shared__ __align__(16) uint8_t smem[];
   const CacheView& c = a.cache;
