@@ -143,8 +143,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
     for (int i = 0; i < 2; ++i) ptx::mbar_init(bar(C::B_Q + i), 4);
     for (int i = 0; i < 3; ++i) ptx::mbar_init(bar(C::B_DRAIN + i), 1);
-    // an earlier CTA that gave up on a wait makes every later one skip its work
-    *abort_flag = (*reinterpret_cast<volatile int32_t*>(err) & kErrTimeout) ? 1u : 0u;
+    // An earlier CTA that gave up on a wait makes every later one skip its work.  No
+    // wait writes the second word, so all warps start or none does: a wait that
+    // runs out while a slower warp is still on its way here must not keep that warp
+    // from the softmax warps' meetings, which have no bound of their own.
+    misc[2] = *abort_flag = (*reinterpret_cast<volatile int32_t*>(err) & kErrTimeout) ? 1u : 0u;
     ptx::fence_mbar_init();
   }
   if (warp == kWarpPV) {
@@ -155,7 +158,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = misc[0];
-  const bool skip = *abort_flag != 0u;
+  const bool skip = misc[2] != 0u;
 
   if (skip) {
     // nothing issued, nothing to drain

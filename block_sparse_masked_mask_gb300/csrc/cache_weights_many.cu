@@ -136,8 +136,9 @@ __global__ void __launch_bounds__(kManyThreads, 2)
       ptx::mbar_init(bar(C::B_SEMPTY + i), 4);
     }
     ptx::mbar_init(bar(C::B_DRAIN), 1);
-    // an earlier CTA that gave up on a wait makes every later one skip its work
-    *abort_flag = (*reinterpret_cast<volatile int32_t*>(err) & kErrTimeout) ? 1u : 0u;
+    // an earlier CTA that gave up on a wait makes every later one skip its work (the second
+    // word, which no wait writes: all warps start or none does)
+    misc[2] = *abort_flag = (*reinterpret_cast<volatile int32_t*>(err) & kErrTimeout) ? 1u : 0u;
     ptx::fence_mbar_init();
   }
   if (warp == kWarpS) {
@@ -150,7 +151,7 @@ __global__ void __launch_bounds__(kManyThreads, 2)
   const uint32_t tmem = misc[0];
   int j = 0;  // tiles so far
 
-  if (*abort_flag != 0u) {
+  if (misc[2] != 0u) {
     // nothing issued, nothing to drain
   } else if (warp == kWarpKeys) {
     // -------------------------------------------------------------- pages, scales, keys
