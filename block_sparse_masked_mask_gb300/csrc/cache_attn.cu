@@ -19,7 +19,11 @@
 // the running maximum of s_j + x_j: weights of all pages share one fp16 range
 // in which those that matter to O are near 1, and the sum of 2^(s_j - m) is that
 // of w_j 2^-x_j, one multiplication.  m moves only when it would grow by
-// more than 2^8.
+// more than 2^8.  That sum does not depend on the values, and its terms span more
+// than an exponential: where exponents of pages lie more than kSpread apart (a page of
+// zeros has 2^-80) they are taken as squares of 2^((s_j - m) / 2), and so are the
+// factors of sums whose reference moves (half_factor).  fp32 holds them: the
+// largest sum is 2^118, and one that a page of 2^120 dominates is 2^-120.
 // A (sequence, head) that lies in one CTA's piece is finished there; the others
 // meet in a second kernel through fp32 partial results, two per CTA at most.
 // Few or short sequences go another way: a cluster of up to eight CTAs takes each
@@ -100,8 +104,8 @@ __device__ __forceinline__ void team_join(const CacheAttnParams& p, int b, int h
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < kTeam; ++k) {
-      const float f = s[k].x == -INFINITY ? 0.f : ptx::ex2(s[k].x - top);
-      sum += s[k].y != s[k].y ? s[k].y : f * s[k].y;
+      const float half = half_factor(s[k].x, top), f = half * half;
+      sum += s[k].y != s[k].y ? s[k].y : s[k].y * half * half;
       if (f > 0.f) {
         const float4 z = ptx::load_peer(reinterpret_cast<const float4*>(mo + row * D + d), k);
         y.x = fmaf(f, z.x, y.x);
@@ -216,9 +220,18 @@ __global__ void __launch_bounds__(kAttnThreads, 3) cache_attn_kernel(const Cache
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) o[k][nt][0] = o[k][nt][1] = o[k][nt][2] = o[k][nt][3] = 0.f;
 
+    // Whether some pages of this batch may lie far below the largest exponent so far:
+    // never while all scales are in [2^-kSpread, 1], values up to 448.
+    bool far = false;
+    auto compare = [&]() {
+      const float v = now.v_scale;  // (0: no page)
+      far = __any_sync(0xffffffffu, v > 1.f || (v < kSpreadScale && v > 0.f)) || far;
+    };
+    compare();
     for (int i = 0; i < mine; ++i) {
       if (i > 0 && (i & 31) == 0) {
         now = next;
+        compare();
         const bool on = i + 32 + lane < mine;
         next = with_scales(c, h, page_number(c, b, token_of(i + 32 + lane), on), on, true);
       }
@@ -250,9 +263,10 @@ __global__ void __launch_bounds__(kAttnThreads, 3) cache_attn_kernel(const Cache
           for (int nt = 0; nt < NT; ++nt) mma16816(s[nt], a0, a1, a2, a3, q[nt][2 * step], q[nt][2 * step + 1]);
         }
       }
-      const float x = float(exponent_of(vs)), inv_vs = pow2f(max(-126, -exponent_of(vs)));
+      const float x = float(exponent_of(vs));
+      float inv_vs = pow2f(max(-126, -exponent_of(vs)));
       const bool masked = tok + kGroup > least || vs == 0.f;  // scale 0: the page was left out
-      bool raise = false;
+      bool raise = far;  // (one check for both rare ways)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -276,15 +290,26 @@ __global__ void __launch_bounds__(kAttnThreads, 3) cache_attn_kernel(const Cache
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
             top = fmaxf(top, m[nt][e]);
-            const float f = m[nt][e] == -INFINITY ? 0.f : ptx::ex2(m[nt][e] - top);
+            const float half = half_factor(m[nt][e], top), f = half * half;
             m[nt][e] = top;
-            l[nt][e] *= f;
+            l[nt][e] = l[nt][e] * half * half;
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
               o[k][nt][e] *= f;
               o[k][nt][2 + e] *= f;
             }
           }
+        if (far) {  // the sums here, and not from the weights
+          inv_vs = 0.f;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float ref = (m[nt][e] == -INFINITY ? 0.f : m[nt][e]) + x;
+              const float y0 = ptx::ex2(0.5f * (s[nt][e] - ref)), y1 = ptx::ex2(0.5f * (s[nt][2 + e] - ref));
+              l[nt][e] = fmaf(y0, y0, fmaf(y1, y1, l[nt][e]));
+            }
+        }
       }
       uint32_t w0[NT], w1[NT];  // weights: tokens 2t, 2t + 1 (and + 8) of row g
 #pragma unroll
@@ -346,8 +371,8 @@ __global__ void __launch_bounds__(kAttnThreads, 3) cache_attn_kernel(const Cache
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float2 s = ml[w * 8 * NT + row];
-        const float f = s.x == -INFINITY ? 0.f : ptx::ex2(s.x - top);
-        sum += s.y != s.y ? s.y : f * s.y;  // a NaN sum stays one even where no maximum was found
+        const float half = half_factor(s.x, top), f = half * half;
+        sum += s.y != s.y ? s.y : s.y * half * half;  // a NaN sum stays one even where no maximum was found
         const float4 z = *reinterpret_cast<const float4*>(mo + (w * 8 * NT + row) * D + d);
         y.x = fmaf(f, z.x, y.x);
         y.y = fmaf(f, z.y, y.y);
@@ -399,11 +424,11 @@ __device__ __forceinline__ void join_row(const CacheAttnParams& p, int n, const 
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     top = fmaxf(top, m);
-    const float f = s.x == -INFINITY ? 0.f : ptx::ex2(s.x - top), old = m == -INFINITY ? 0.f : ptx::ex2(m - top);
-    float sum = s.y != s.y ? s.y : f * s.y;
+    const float half = half_factor(s.x, top), f = half * half, old_half = half_factor(m, top), old = old_half * old_half;
+    float sum = s.y != s.y ? s.y : s.y * half * half;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    l = l * old + sum;
+    l = l * old_half * old_half + sum;
     m = top;
 #pragma unroll
     for (int e = 0; e < E; ++e) x[e] *= old;
@@ -435,8 +460,8 @@ __device__ __forceinline__ void join_row(const CacheAttnParams& p, int n, const 
 #pragma unroll
     for (int y = 0; y < W; ++y) {
       const float* from = shared + y * (D + 2);
-      const float f = from[D] == -INFINITY ? 0.f : ptx::ex2(from[D] - top), s = from[D + 1];
-      l += s != s ? s : f * s;
+      const float half = half_factor(from[D], top), f = half * half, s = from[D + 1];
+      l += s != s ? s : s * half * half;
 #pragma unroll
       for (int e = 0; e < E; ++e) x[e] = fmaf(f, from[lane * E + e], x[e]);
     }

@@ -19,7 +19,8 @@
 //    maximum, and the CTA joins them at its end; warps without rows only pass the
 //    steps on.  Such a CTA waits for latencies, and two chains hide each other's:
 //    16 sequences of 8192, 32 rows of 8 heads 137 -> 108 us.
-//  * The pages' scales and the running maximum are those of cache_attn.cu.
+//  * The pages' scales, the running maximum and the far pages' sums are those of
+//    cache_attn.cu.
 // Warps (512 threads):
 //   0-3, 4-7   softmax of M tile 0 and 1, one thread per row
 //   8-11       values: codes to fp16 tiles (two slots)
@@ -53,6 +54,8 @@ namespace {
 constexpr int kChunkThreads = 512;
 constexpr int kWarpValues = 8, kWarpKeys = 12, kWarpS = 13, kWarpPV = 15;
 constexpr int kStep = 64;  // tokens per step
+constexpr int kNoPage = INT_MIN;  // a block without a page
+constexpr int kFar = 1;           // one whose value exponent lies kSpread below the largest so far
 
 template <int D>
 struct ChunkCfg {
@@ -65,7 +68,7 @@ struct ChunkCfg {
   static constexpr int OFF_R = OFF_K + NK * KT;  // the values' codes
   static constexpr int OFF_V = OFF_R + NR * KT;
   // [slot][8 blocks of 16 tokens]: key scale, exponent of the value scale, its
-  // inverse, the page (as an int; -1: none)
+  // inverse (0: far), and as an int kNoPage, kFar or 0
   static constexpr int OFF_SCL = OFF_V + NV * VT;
   // B_SFULL, B_PFULL, B_PDONE: per M tile and S buffer
   static constexpr int B_Q = 0, B_KFULL = 2, B_KEMPTY = B_KFULL + NK, B_RFULL = B_KEMPTY + NK, B_REMPTY = B_RFULL + NR, B_VFULL = B_REMPTY + NR,
@@ -83,6 +86,26 @@ struct ChunkCfg {
     return uint32_t(row * V::ROWB + ((u ^ x) << 4));
   }
 };
+
+// The sums of a step's far blocks, from the scores as they lie; not inlined, to keep
+// the softmax's loop short.
+__device__ __noinline__ float far_sums(uint32_t s_col, const float4* sc, float qscale, float ref, int seen) {
+  float sum = 0.f;
+#pragma unroll 1
+  for (int q = 0; q < 4; ++q) {
+    if (__float_as_int(sc[q].w) != kFar) continue;
+    const float f = qscale * sc[q].x;
+    uint32_t v[16];
+    ptx::tmem_ld16(s_col + 16 * q, v);
+    ptx::tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const float y = ptx::ex2(0.5f * fmaf(__uint_as_float(v[e]), f, -ref));
+      if (16 * q + e < seen) sum = fmaf(y, y, sum);
+    }
+  }
+  return sum;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kChunkThreads, 1)
@@ -181,6 +204,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
     int id = 0, id_next = number(0), id_after = number(4);
     float2 sc = make_float2(0.f, 0.f), sc_next = scales(0, id_next);
+    int x_top = 0;  // largest exponent of the values so far, if above that of values up to 448
     int done = 0, done_v = 0;
     for (int j = 0; j < tiles; ++j) {
       if ((j & 3) == 0) {
@@ -195,10 +219,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (here && !fine) atomicOr(err, kErrBadPage);
       if (j >= C::NSCL && !wait_warp(bar(C::B_SCLFREE + ss), uint32_t(j / C::NSCL - 1) & 1u, abort_flag, err, 1))
         break;
+      const int x = exponent_of(sc.y);
+      if (__any_sync(0xffffffffu, fine && x > x_top)) x_top = max(x_top, __reduce_max_sync(0xffffffffu, fine ? x : 0));
       if (mine) {
-        const int x = exponent_of(sc.y);
-        scl[ss * 8 + (lane & 7)] = fine ? make_float4(sc.x, float(x), pow2f(max(-126, -x)), __int_as_float(id))
-                                  : make_float4(0.f, 0.f, 0.f, __int_as_float(-1));
+        const bool far = x < x_top - kSpread;
+        scl[ss * 8 + (lane & 7)] =
+            fine ? make_float4(sc.x, float(x), far ? 0.f : pow2f(max(-126, -x)), __int_as_float(far ? kFar : 0))
+                 : make_float4(0.f, 0.f, 0.f, __int_as_float(kNoPage));
       }
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar(C::B_SCLFULL + ss));
@@ -380,11 +407,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       ptx::tmem_ld32(s_col + 32, s[1]);
       const float4* sc = scl + ss * 8 + 4 * f;
       const int seen = visible - (begin + i * kStep);  // columns [0, seen) are visible
-      bool gone = false;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) gone |= __float_as_int(sc[q].w) < 0 && begin + i * kStep + 16 * q < end;
+      const int odd = __float_as_int(sc[0].w) | __float_as_int(sc[1].w) | __float_as_int(sc[2].w) | __float_as_int(sc[3].w);
       ptx::tmem_wait_ld();
-      if (__any_sync(0xffffffffu, seen < kStep) || gone) {
+      if (__any_sync(0xffffffffu, seen < kStep) || odd < 0) {
         // hidden: the lowest score, whatever lay there
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -408,11 +433,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       // the reference moves on the first visible token and when a weight would
       // pass 2^8
       const bool raise = top > mx + 8.f;
-      if (__any_sync(0xffffffffu, raise)) {
-        const float alpha = raise ? (mx == -INFINITY ? 0.f : ptx::ex2(mx - top)) : 1.f;
+      if (__any_sync(0xffffffffu, raise || (odd & kFar))) {
+        const float half = raise ? half_factor(mx, top) : 1.f, alpha = half * half;
         if (raise) mx = top;
-        l2.x *= alpha;
-        l2.y *= alpha;
+        l2.x = l2.x * half * half;
+        l2.y = l2.y * half * half;
         if (last >= 0) {  // O holds the earlier steps' products once the last of them has ended
           if (!wait_warp(bar(C::B_PDONE + 2 * m + (last & 1)), uint32_t(last >> 1) & 1u, abort_flag, err, 13)) {
             ok = false;
@@ -429,6 +454,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             ptx::tmem_st16(o_col + q * 16, v);
           }
         }
+        if (odd & kFar) l2.x += far_sums(s_col, sc, qscale, mx == -INFINITY ? 0.f : mx, seen);
       }
       const float ref = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
@@ -492,9 +518,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (m == 0) {
         const float2 ml = other_m[row];
         const float top = fmaxf(mx, ml.x);
-        mine = mx == -INFINITY ? 0.f : ptx::ex2(mx - top);
-        its = ml.x == -INFINITY ? 0.f : ptx::ex2(ml.x - top);
-        l = (l != l ? l : mine * l) + (ml.y != ml.y ? ml.y : its * ml.y);  // NaN stays NaN
+        const float half = half_factor(mx, top), other_half = half_factor(ml.x, top);
+        mine = half * half;
+        its = other_half * other_half;
+        l = l * half * half + ml.y * other_half * other_half;
         mx = top;
       }
     }

@@ -1,0 +1,67 @@
+"""Cache attention over the whole range that codes, scales and queries may have:
+values of very different size in one sequence.  Bounds are those of test_cache_gpu
+with the terms that grow here written out (exponents of the value scales)."""
+import numpy as np
+import pytest
+
+from block_sparse_masked_mask_gb300 import api
+from test_cache_gpu import Pair, cu_of, randn, run_attend
+
+pytestmark = pytest.mark.gpu
+
+
+def far_bounds(p, O, spread, terms, cu, lens, dim):
+    """A score's base-2 argument carries the value exponent, E at most: two roundings
+    of numbers up to A + E; far weights' sums square one ex2 (2^-21)."""
+    tol, slack = np.zeros(O.shape), []
+    E = 128.0
+    for b, L in enumerate(lens):
+        A = terms[b].max(initial=0)
+        rel = 2 * ((dim + 4) * 2.0 ** -24 * A) + 2.0 ** -21 + 2.0 ** -23 * (2 * A + 2 * E) + L * 2.0 ** -24
+        slack.append(rel)
+        s = slice(cu[b], cu[b + 1])
+        small = 2.0 ** -25 * p.ref.code_sums(1, b, L)
+        tol[s] = (2.0 ** -11 + 3 * rel) * spread[s] + np.repeat(small, O.shape[1] // small.shape[0], 0)[None]
+        tol[s] = tol[s] * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(O[s])
+    return tol, slack
+
+
+# powers of two of the pages' values in turn (None: zeros, whose page has the least
+# scale, 2^-80), and how many pages of each follow one another
+ORDERS = {"zeros_first": ([None, 60], 1), "zeros_last": ([60, None], 1), "runs": ([None, 0, 60], 8),
+          "far": ([110, None, -60, 20], 2), "up": ([-60, None, 0, 60, 110], 3), "down": ([110, 60, 0, -60], 5)}
+
+
+@pytest.mark.parametrize("order", ORDERS)
+@pytest.mark.parametrize("dim,lens,new,group", [
+    (64, [200, 70, 900], 1, 1),       # one CTA or a cluster per sequence
+    (32, [3000, 500], 2, 6),          # clusters, 12 rows
+    (32, [9000, 40], 1, 2),           # the cut line and its join
+    (64, [200, 70, 900], 20, 1),      # tensor cores, both M tiles with the same rows
+    (128, [1100], 70, 4),             # two M tiles
+    (32, [9000, 2500], 40, 1)])       # chunks and their join
+def test_values_of_very_different_size(order, dim, lens, new, group):
+    """The softmax does not depend on the values: a page of zeros next to one of
+    2^60 keeps its share of every sum, and LSE is that of the keys alone."""
+    powers, run = ORDERS[order]
+    p = Pair(lens, 1, dim, 32, seed=1)
+    cu_all, T = cu_of(lens), sum(lens)
+    k, v = 0.5 * randn(T, 1, dim, seed=2), randn(T, 1, dim, seed=3)
+    for b, n in enumerate(lens):
+        for j in range(0, n, 32):
+            x = powers[(j // 32 // run + b) % len(powers)]
+            v[cu_all[b] + j:cu_all[b] + min(n, j + 32)] *= 0.0 if x is None else 2.0 ** x
+    p.append(k, v, cu_all, lens)
+    cu = cu_of([new] * len(lens))
+    q = randn(int(cu[-1]), group, dim, seed=4)
+    O, L, terms, spread = p.ref.attend(q.double().numpy(), cu, lens)
+    tol, slack = far_bounds(p, O, spread, terms, cu, lens, dim)
+    o, lse = run_attend(p, q, cu, lens)
+    assert api.attn_cache_get_status(p.dev) == api.ATTN_OK
+    got = lse.double().cpu().numpy()
+    for b in range(len(lens)):
+        s = slice(cu[b], cu[b + 1])
+        d = np.abs(got[:, s] - L[:, s])
+        assert (d <= slack[b] + 2.0 ** -22 * np.abs(L[:, s])).all(), f"LSE of {b}: {d.max()} vs {slack[b]}"
+    err = np.abs(o.double().cpu().numpy() - O)
+    assert (err <= tol).all(), f"O: worst ratio {(err / tol).max()}"
