@@ -460,8 +460,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const float4 k = sc[q];
-        // -inf * 0 (a page left out) would be NaN
-        const float kf = __float_as_int(k.w) < 0 ? 1.f : qscale * k.x, kx = k.y - ref;
+        // never 0, where a page is left out or the product is below fp32: a hidden score is
+        // -inf, and times 0 it would be NaN
+        const float kf = fmaf(qscale, k.x, 0x1p-126f), kx = k.y - ref;
         const float2 f2 = make_float2(kf, kf), x2 = make_float2(kx, kx);
         float2 part = make_float2(0.f, 0.f);
         uint32_t* v = s[q >> 1] + (q & 1) * 16;

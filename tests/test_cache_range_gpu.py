@@ -1,11 +1,12 @@
 """Cache attention over the whole range that codes, scales and queries may have:
-values of very different size in one sequence.  Bounds are those of test_cache_gpu
-with the terms that grow here written out (exponents of the value scales)."""
+values of very different size in one sequence, factors that underflow.  Bounds are
+those of test_cache_gpu with the terms that grow here written out (exponents of the
+value scales)."""
 import numpy as np
 import pytest
 
 from block_sparse_masked_mask_gb300 import api
-from test_cache_gpu import Pair, cu_of, randn, run_attend
+from test_cache_gpu import Pair, check_attend, cu_of, randn, run_attend
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +66,20 @@ def test_values_of_very_different_size(order, dim, lens, new, group):
         assert (d <= slack[b] + 2.0 ** -22 * np.abs(L[:, s])).all(), f"LSE of {b}: {d.max()} vs {slack[b]}"
     err = np.abs(o.double().cpu().numpy() - O)
     assert (err <= tol).all(), f"O: worst ratio {(err / tol).max()}"
+
+
+@pytest.mark.parametrize("new", [1, 20, 140])
+def test_hidden_tokens_under_factors_that_underflow(new):
+    """Keys of zeros (page scale 2^-80) and queries near 2^-70: the factor of a
+    block's scores is 0 in fp32, and what is hidden stays hidden."""
+    lens = [500, 150]
+    p = Pair(lens, 1, 64, 32, seed=1)
+    k, v = randn(650, 1, 64, seed=1), randn(650, 1, 64, seed=2)
+    k[::2] = 0
+    k[64:96] = 0
+    k[480:] = 0
+    p.append(k, v, cu_of(lens), lens)
+    cu = cu_of([new, new])
+    for size, scale in ((2.0 ** -70, 0.0), (1.0, 2.0 ** -100)):
+        q = randn(2 * new, 2, 64, seed=3, scale=size)
+        check_attend(p, q, cu, lens, scale=scale)
