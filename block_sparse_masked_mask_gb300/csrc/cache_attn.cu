@@ -16,14 +16,16 @@
 //    interleaved byte by byte, the weights turned by movmatrix.
 // Scores s_j (base 2) are the product times the page's key scale.  The page's
 // value scale 2^x is folded into the exponent, w_j = 2^(s_j + x_j - m), with m
-// the running maximum of s_j + x_j: weights of all pages share one fp16 range
-// in which those that matter to O are near 1, and the sum of 2^(s_j - m) is that
-// of w_j 2^-x_j, one multiplication.  m moves only when it would grow by
-// more than 2^8.  That sum does not depend on the values, and its terms span more
+// 2^7 below the running maximum of s_j + x_j: weights of all pages share one fp16
+// range, and the sum of 2^(s_j - m) is that of w_j 2^-x_j, one multiplication.  m
+// moves only when a weight would pass 2^15, the top of that range: the largest is
+// between 2^7 and 2^15, and fp16's least step, 2^-24, is 2^-31 of it at most (with
+// the largest at 1, thousands of tokens below 2^-25 of it would be lost in O).
+// That sum does not depend on the values, and its terms span more
 // than an exponential: where exponents of pages lie more than kSpread apart (a page of
 // zeros has 2^-80) they are taken as squares of 2^((s_j - m) / 2), and so are the
 // factors of sums whose reference moves (half_factor).  fp32 holds them: the
-// largest sum is 2^118, and one that a page of 2^120 dominates is 2^-120.
+// largest sum, of 2^30 tokens, is 2^125, and one that a page of 2^120 dominates is 2^-113.
 // A (sequence, head) that lies in one CTA's piece is finished there; the others
 // meet in a second kernel through fp32 partial results, two per CTA at most.
 // Few or short sequences go another way: a cluster of up to eight CTAs takes each
@@ -41,7 +43,6 @@ namespace {
 constexpr int kAttnThreads = 32 * kWarps;
 constexpr int kStages = 4;  // of the queue, groups
 constexpr int kTeam = 8;    // CTAs of a cluster
-constexpr float kRaise = 8.f;
 constexpr float kLn2 = 0.69314718055994531f;
 
 template <int D>
@@ -278,7 +279,7 @@ __global__ void __launch_bounds__(kAttnThreads, 3) cache_attn_kernel(const Cache
             if (vs == 0.f || tok + g >= visible[nt][e]) s[nt][e] = -INFINITY;
             if (vs == 0.f || tok + g + 8 >= visible[nt][e]) s[nt][2 + e] = -INFINITY;
           }
-          raise |= fmaxf(s[nt][e], s[nt][2 + e]) > m[nt][e] + kRaise;
+          raise |= fmaxf(s[nt][e], s[nt][2 + e]) > m[nt][e] + kMostWeight;
         }
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
@@ -289,7 +290,7 @@ __global__ void __launch_bounds__(kAttnThreads, 3) cache_attn_kernel(const Cache
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            top = fmaxf(top, m[nt][e]);
+            top = fmaxf(top - kTopWeight, m[nt][e]);
             const float half = half_factor(m[nt][e], top), f = half * half;
             m[nt][e] = top;
             l[nt][e] = l[nt][e] * half * half;

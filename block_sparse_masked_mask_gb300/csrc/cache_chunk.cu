@@ -431,8 +431,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (t > -INFINITY) top = fmaxf(top, fmaf(t, qscale * sc[q].x, sc[q].y));
       }
       // the reference moves on the first visible token and when a weight would
-      // pass 2^8
-      const bool raise = top > mx + 8.f;
+      // pass 2^15
+      const bool raise = top > mx + kMostWeight;
+      top -= kTopWeight;
       if (__any_sync(0xffffffffu, raise || (odd & kFar))) {
         const float half = raise ? half_factor(mx, top) : 1.f, alpha = half * half;
         if (raise) mx = top;

@@ -201,14 +201,17 @@ __device__ __forceinline__ PageBatch with_scales(const CacheView& c, int h, int 
   return p;
 }
 
+// Weights as fp16, powers of two: the largest when the reference moves, and at most.
+constexpr float kTopWeight = 7.f, kMostWeight = 15.f;
+
 // A term of a softmax's sum is its weight without the value's exponent (cache_attn.cu).
 // A weight is lost below 2^-126 of the reference: with value exponents this far apart
-// that is at most 2^-46 of the sum; further apart its terms are formed without them.
+// that is at most 2^-53 of the sum; further apart its terms are formed without them.
 constexpr int kSpread = 80;
 constexpr float kSpreadScale = 0x1p-80f;
 
 // The square root of the factor that brings what refers to `m` to the reference `top`:
-// sums are multiplied by it twice, since one may be 2^118 and the factor itself below
+// sums are multiplied by it twice, since one may be 2^125 and the factor itself below
 // what fp32 holds.
 __device__ __forceinline__ float half_factor(float m, float top) {
   return m == -INFINITY ? 0.f : ptx::ex2(0.5f * (m - top));

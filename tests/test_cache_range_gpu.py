@@ -1,9 +1,12 @@
 """Cache attention over the whole range that codes, scales and queries may have:
-values of very different size in one sequence, factors that underflow.  Bounds are
-those of test_cache_gpu with the terms that grow here written out (exponents of the
-value scales)."""
+values of very different size in one sequence, factors that underflow, weights far
+below the largest.  Bounds are those of test_cache_gpu with the terms that grow here
+written out (exponents of the value scales)."""
+import math
+
 import numpy as np
 import pytest
+import torch
 
 from block_sparse_masked_mask_gb300 import api
 from test_cache_gpu import Pair, check_attend, cu_of, randn, run_attend
@@ -83,3 +86,29 @@ def test_hidden_tokens_under_factors_that_underflow(new):
     for size, scale in ((2.0 ** -70, 0.0), (1.0, 2.0 ** -100)):
         q = randn(2 * new, 2, 64, seed=3, scale=size)
         check_attend(p, q, cu, lens, scale=scale)
+
+
+@pytest.mark.parametrize("dim", [32, 128])
+@pytest.mark.parametrize("new", [1, 12, 40, 300])
+@pytest.mark.parametrize("length", [900, 9000])
+def test_many_small_weights_beside_large_ones(length, new, dim):
+    """Every 16th token takes almost all the weight and has no value; the others,
+    2^-26 of it each, are all that O consists of.  A weight is fp16: 2^-19 of the
+    reference, which the largest passes by 2^7, so off by 2^-25 / 2^-19 = 2^-6 of
+    itself at most."""
+    p = Pair([length], 1, dim, 64, seed=1)
+    k, v = torch.zeros(length, 1, dim), torch.ones(length, 1, dim)
+    k[::16, :, 0] = 1.0
+    v[::16] = 0.0
+    p.append(k.bfloat16(), v.bfloat16(), cu_of([length]), [length])
+    q = torch.zeros(new, 1, dim, dtype=torch.bfloat16)
+    q[..., 0] = 1.0
+    scale = 26 * math.log(2)
+    O, L, _, _ = p.ref.attend(q.double().numpy(), cu_of([new]), [length], scale=scale)
+    assert np.abs(O).max() < 2.0 ** -20
+    o, lse = run_attend(p, q, cu_of([new]), [length], scale=scale)
+    # a score of 26 (base 2), a sum over `length` tokens in fp32
+    slack = 2 * (dim + 4) * 2.0 ** -24 * 19 + 2.0 ** -22 + 2.0 ** -23 * (2 * 26 + 16) + length * 2.0 ** -24
+    assert (np.abs(lse.double().cpu().numpy() - L) <= slack + 2.0 ** -22 * np.abs(L)).all()
+    err = np.abs(o.double().cpu().numpy() - O)
+    assert (err <= (2.0 ** -6 + 2.0 ** -8 + 2.0 ** -9) * np.abs(O)).all(), (err / np.abs(O)).max()
