@@ -32,6 +32,7 @@
 // (sequence, head) and joins its results through shared memory (team_of).
 // Measured, 64 requests of 1024 to 16384 tokens, 8 heads, D = 128: 118 us, 84% of the
 // copy rate; 16 of 8192, 16 rows 62 us, 64%; a single one of 2049 tokens 8.4 us.
+#include <algorithm>
 #include <cmath>
 
 #include "cache_rows.cuh"
@@ -532,6 +533,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_many_kernel(const 
   join_row<D, 1>(p, max(1, (limit + p.chunk - 1) / p.chunk), at, token, head, 0, lane, nullptr);
 }
 
+constexpr int64_t kMostPartial = int64_t(512) << 20;
+
 // CTAs that take a (sequence, head) together, as one cluster whose results meet in
 // shared memory, with one launch and no workspace; 0: the line of all tokens is cut
 // and joined.  As many as the GPU holds at once (456), for up to 1024 tokens each:
@@ -562,6 +565,11 @@ int team_of(const CacheQueryArgs& a) {
 // 5 TB/s).  Measured against chunks of work / SMs tokens: 2 sequences of 4096,
 // 300 new, 4 heads 58 -> 43 us; 8 of up to 9000, up to 200 new, D = 64: 72 -> 46;
 // 1 of 32768, 512 new, 8 heads 303 -> 284.
+// However long the sequences, the partial results stay within kMostPartial bytes,
+// about what the backward of the masked attention takes at 32768 tokens: a call whose
+// rows need more has over 4000 CTAs (tiles of rows times chunks), 26 per SM, by then.
+// (32 / 8 heads, D = 128, behind a bound of 131072: 2048 new tokens 1.09 GB and 4.0
+// ms -> 0.51 GB and 3.6 ms; 16384 new 8.7 GB and 30.3 ms -> none and 24.9 ms.)
 // The number of SMs only sizes the work, and the size query runs without a
 // device, so it is that of the GPU this library is built for.
 void plan(CacheAttnParams* p) {
@@ -577,10 +585,12 @@ void plan(CacheAttnParams* p) {
   p->chunk = 256;
   p->splits = 1;
   if (!p->many || items == 0) return;
-  const int64_t least = (int64_t(a.max_seqlen) + 4095) / 4096;
+  const int64_t row_bytes = int64_t(a.total_tokens) * a.num_heads * (4 * a.cache.head_dim + 8);
+  const int64_t most = std::max<int64_t>(1, kMostPartial / row_bytes);  // (items > 0: there are rows)
+  const int64_t least = std::min((int64_t(a.max_seqlen) + 4095) / 4096, most);
   double best = INFINITY;
   for (int fill = 0; fill <= 4; ++fill) {
-    const int64_t n = fill == 0 ? least : fill * kSms / items;
+    const int64_t n = fill == 0 ? least : std::min<int64_t>(fill * kSms / items, most);
     if (n < least || n < 1) continue;
     int64_t chunk = (int64_t(a.max_seqlen) + n - 1) / n;
     chunk = (chunk + kTile - 1) / kTile * kTile;
