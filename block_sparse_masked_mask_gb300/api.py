@@ -356,7 +356,11 @@ class _Launch:
 _Tensor = torch.Tensor
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _ROW_DTYPES = tuple(DTYPES)
-_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _raw_stream(index: int) -> int:
+    # (looked up when called: a PyTorch without CUDA has none, and imports this module)
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _elsewhere(device: torch.device, stream):
