@@ -59,10 +59,11 @@ struct NewPages {
   }
 };
 
-// (Six CTAs per SM: 36.0 us for those 14000 tokens; five, as the compiler would have it,
-// 36.9, seven 38.4.)
+// CTAs per SM: bf16 six (36.0 us for those 14000 tokens; five, as the compiler would have
+// it, 36.9, seven 38.4); fp32 three, as many as its 64 KB of shared memory each allow
+// (the same tokens 68.8 us, floor 40; held to the registers of six 69.8).
 template <typename T>
-__global__ void __launch_bounds__(kAppendThreads, 6) append_kernel(const AppendArgs a, int team_log2) {
+__global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 4 ? 3 : 6) append_kernel(const AppendArgs a, int team_log2) {
   using C = Chunk<T>;
   extern __shared__ __align__(16) uint8_t smem[];
   const CacheView& c = a.cache;
