@@ -40,7 +40,9 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 
 // One row's dimensions of lane t (two pieces) as fp16 pairs, times a power of two
 // that puts the row's largest magnitude into [1, 2): w[2 s], w[2 s + 1] belong to
-// step s.  Returns that power's inverse.  A row past the last is zero.
+// step s.  (fp16's least step is 2^-24: with bf16's 8 bits, elements down to 2^-17 are
+// exact, and smaller ones off by 2^-25 at most.)  Returns that power's inverse.  A row
+// past the last is zero.
 template <int D>
 __device__ __forceinline__ float load_query(const CacheQueryArgs& a, const SeqRows& r, int h, int G, int row, int t,
                                             uint32_t (&w)[D / 8]) {

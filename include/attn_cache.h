@@ -180,10 +180,10 @@ ATTN_API attn_status attn_cache_fwd_workspace_size(const attn_kv_cache* cache, i
  *                bytes, for this call alone while it runs; NULL if that is 0
  * Cached numbers inside a sequence must be finite, as for attn_bwd(); what
  * lies behind its end may hold anything.  Cached numbers enter the products
- * exactly.  q is scaled by a power of two per row; up to 16 rows (max_new * G)
- * it is then exact in fp16 down to 2^-24 of its row's largest value, with more
- * rows it is the sum of two e4m3 numbers, exact down to 2^-9 of that value and
- * within 2^-17 of it below.  The weights (times their page's value scale) are
+ * exactly.  q is scaled by a power of two per row.  Up to 16 rows (max_new * G)
+ * it is then fp16: elements down to 2^-17 of their row's largest are exact,
+ * smaller ones within 2^-25 of that largest.  With more rows it is the sum of
+ * two e4m3 numbers: exact down to 2^-9 of the largest, within 2^-17 of it below.  The weights (times their page's value scale) are
  * rounded to fp16: by 2^-11 of themselves, and below 2^-21 of the row's largest
  * by 2^-32 of that.  Sums are fp32, and LSE does not depend on the values.
  * Repeated calls are bit-identical.  o may be q.

@@ -112,3 +112,29 @@ def test_many_small_weights_beside_large_ones(length, new, dim):
     assert (np.abs(lse.double().cpu().numpy() - L) <= slack + 2.0 ** -22 * np.abs(L)).all()
     err = np.abs(o.double().cpu().numpy() - O)
     assert (err <= (2.0 ** -6 + 2.0 ** -8 + 2.0 ** -9) * np.abs(O)).all(), (err / np.abs(O)).max()
+
+
+@pytest.mark.parametrize("rows", [1, 3, 16, 48, 200])
+def test_small_elements_beside_a_large_one(rows):
+    """The largest element of a query meets keys of 0, so that scores consist of
+    elements 2^-12 to 2^-24 of it.  As fp16 (up to 16 rows) an element below 2^-17 of
+    the largest, m, is off by 2^-25 m at most, as two e4m3 numbers one below 2^-9 by
+    2^-17 m; a score by scale times that times sum |k|."""
+    L, scale = 400, 2.0 ** (10 if rows <= 16 else 3)
+    p = Pair([L], 1, 64, 64, seed=2)
+    k, v = randn(L, 1, 64, seed=1), randn(L, 1, 64, seed=2)
+    k[..., 0] = 0
+    p.append(k, v, cu_of([L]), [L])
+    g = torch.Generator().manual_seed(3)
+    q = torch.randn((rows, 1, 64), generator=g) * 2.0 ** torch.randint(-24, -11, (rows, 1, 64), generator=g)
+    q[..., 0] = 1.5
+    q = q.to(torch.bfloat16)
+    o, lse = run_attend(p, q, cu_of([rows]), [L], scale=scale)
+    O, Z, terms, spread = p.ref.attend(q.double().numpy(), cu_of([rows]), [L], scale=scale)
+    K = np.abs(p.ref.numbers(0, 0, L)).sum(-1).max()
+    off = 2.0 ** (-25 if rows <= 16 else -17) * 1.5 * K * scale
+    A = terms[0].max()
+    rel = 2 * ((64 + 4) * 2.0 ** -24 * A) + 2.0 ** -22 + 2.0 ** -23 * (2 * A + 16) + L * 2.0 ** -24
+    assert (np.abs(lse.double().cpu().numpy() - Z) <= rel + off + 2.0 ** -22 * np.abs(Z)).all()
+    tol = (2.0 ** -11 + 3 * rel + 2 * np.expm1(2 * off)) * spread + 2.0 ** -32 * p.ref.code_sums(1, 0, L)[None]
+    assert (np.abs(o.double().cpu().numpy() - O) <= tol * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(O)).all()
