@@ -439,7 +439,8 @@ def attn_rope(q: torch.Tensor, k: Optional[torch.Tensor], plan: RopePlan,
 
     Positions are ``positions`` (int32 [T]), or follow from ``cu_seqlens``
     (int32 [B + 1]): the place in the own sequence, behind the
-    ``seq_lens[b] - n`` earlier tokens where ``seq_lens`` (int32 [B]) is given.
+    ``seq_lens[b] - n`` earlier tokens where ``seq_lens`` (int32 [B]) is given (as
+    long as no eviction has shortened the sequence).
     ``inverse`` turns back: applied to the gradients of the rotated q and k it
     gives those of q and k.  bf16 or fp32; the tokens of q and k may be apart
     (slices of one projection).  ``q_out=q`` rotates in place."""
@@ -727,6 +728,8 @@ def attn_cache_evict(weights: torch.Tensor, cache: KVCache, dst: KVCache, seq_le
     largest ``weights`` (fp32 [batch, heads, width]; ties to the lower index,
     -inf first to go), and copy them in order into ``dst``'s pages (a KVCache
     with a page table of its own; the pools may be the same, the pages not).
+    Keys stay as they were rotated, so that later tokens of a shortened sequence take
+    ``attn_rope``'s ``positions`` (their place in the whole text), not its ``seq_lens``.
 
     Returns (kept int32 [batch, heads, max_keep] with -1 behind the last,
     new_weights [batch, heads, max_keep or wider] with 0 behind the last,

@@ -108,8 +108,9 @@ ATTN_API attn_status attn_rope_plan_init(attn_rope_plan* plan, int32_t rotary_di
  *   positions    device int32[total_tokens], any value; or NULL, and then
  *   cu_seqlens   device int32[batch + 1]: row cu_seqlens[b] + i stands at
  *                position i, or, where seq_lens (device int32[batch]) is given,
- *                at seq_lens[b] - n + i.  Rows outside every sequence keep
- *                what they held.
+ *                at seq_lens[b] - n + i (not for a sequence that an eviction
+ *                has shortened).  Rows outside every sequence keep what they
+ *                held.
  * The angle is reduced exactly: position times the 64-bit turn fraction of the
  * plan, modulo 2^64, in integers; so far positions lose nothing.  Arithmetic
  * is fp32, rounded once.
@@ -225,6 +226,9 @@ ATTN_API attn_status attn_cache_weights(const void* q, const float* lse, attn_dt
  * are copied in order to slots 0 .. n_b - 1 of dst's pages; a dst page's scale
  * is the largest of its tokens' scales, and codes from pages with smaller ones
  * are re-scaled.
+ * Keys stay as they were rotated: n_b is the number of tokens held, no longer a
+ * position, so that later tokens are rotated by attn_rope's positions and not by
+ * its seq_lens (attn_cache_fwd's causal order is that of the slots, as before).
  *   weights      device fp32 [batch, num_kv_heads, weight_stride], weight_stride >= max_seqlen
  *   budgets      device int32[batch], 0 <= budgets[b]
  *   max_keep     at least every n_b
