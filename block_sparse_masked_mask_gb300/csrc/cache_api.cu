@@ -284,6 +284,10 @@ attn_status attn_cache_evict(const float* weights, int64_t weight_stride, const 
       int64_t(max_keep) > int64_t(dst->max_pages) * dst->page_size)
     return ATTN_ERR_INVALID_ARG;
   if ((weights && new_weights == weights) || new_lens == seq_lens) return ATTN_ERR_INVALID_ARG;
+  // one table over one pool: every page would be read and written in no order
+  if (max_keep > 0 && cache->page_table == dst->page_table &&
+      (cache->k_pages == dst->k_pages || cache->v_pages == dst->v_pages))
+    return ATTN_ERR_INVALID_ARG;
   for (const void* p : {static_cast<const void*>(weights), static_cast<const void*>(seq_lens),
                         static_cast<const void*>(budgets), static_cast<const void*>(kept),
                         static_cast<const void*>(new_weights), static_cast<const void*>(new_lens)})

@@ -239,7 +239,7 @@ ATTN_API attn_status attn_cache_weights(const void* q, const float* lse, attn_dt
  *   new_lens     device int32[batch]: n_b; not seq_lens itself
  *   cache, dst   the same heads, head_dim, page_size and batch; dst's pages of
  *                these sequences are none of the pages that they are read from
- *                (the pools may be one)
+ *                (the pools may be one; one table over one pool is refused)
  */
 ATTN_API attn_status attn_cache_evict(const float* weights, int64_t weight_stride,
                                       const int32_t* seq_lens, const int32_t* budgets,
