@@ -222,12 +222,12 @@ __global__ void __launch_bounds__(kAttnThreads, 3) cache_attn_kernel(const Cache
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) o[k][nt][0] = o[k][nt][1] = o[k][nt][2] = o[k][nt][3] = 0.f;
 
-    // Whether some pages of this batch may lie far below the largest exponent so far:
-    // never while all scales are in [2^-kSpread, 1], values up to 448.
-    bool far = false;
+    int x_top = 0;  // largest exponent of the values so far, if above that of values up to 448
+    bool far;       // some pages of this batch lie far below it
     auto compare = [&]() {
-      const float v = now.v_scale;  // (0: no page)
-      far = __any_sync(0xffffffffu, v > 1.f || (v < kSpreadScale && v > 0.f)) || far;
+      const int x = exponent_of(now.v_scale);  // (-127: no page)
+      if (__any_sync(0xffffffffu, x > x_top)) x_top = max(x_top, __reduce_max_sync(0xffffffffu, x));
+      far = __any_sync(0xffffffffu, now.v_scale > 0.f && x < x_top - kSpread);
     };
     compare();
     for (int i = 0; i < mine; ++i) {

@@ -210,7 +210,6 @@ constexpr float kTopWeight = 7.f, kMostWeight = 15.f;
 // A weight is lost below 2^-126 of the reference: with value exponents this far apart
 // that is at most 2^-53 of the sum; further apart its terms are formed without them.
 constexpr int kSpread = 80;
-constexpr float kSpreadScale = 0x1p-80f;
 
 // The square root of the factor that brings what refers to `m` to the reference `top`:
 // sums are multiplied by it twice, since one may be 2^125 and the factor itself below
