@@ -31,7 +31,7 @@
 // Few or short sequences go another way: a cluster of up to eight CTAs takes each
 // (sequence, head) and joins its results through shared memory (team_of).
 // Measured, 64 requests of 1024 to 16384 tokens, 8 heads, D = 128: 118 us, 84% of the
-// copy rate; 16 of 8192, 16 rows 62 us, 64%; a single one of 2049 tokens 8.4 us.
+// copy rate; 16 of 8192, 16 rows 63 us, 63%; a single one of 2049 tokens 8.4 us.
 #include <algorithm>
 #include <cmath>
 
@@ -542,7 +542,7 @@ constexpr int64_t kMostPartial = int64_t(512) << 20;
 // even.  Measured, line / cluster, D = 128, 8 heads: 1 sequence of 700 tokens 10.2 /
 // 7.2 us, 2049 10.9 / 8.4, 8192 13.4 / 13.3, 16384 16.7 / 20.8; with 16 rows, 2049 15.6 /
 // 10.8; 4 of 3000 14.0 / 9.9, of 6000 18.5 / 14.7; 8 of 3000 18.8 / 14.4; 16 of 2000 21.1 /
-// 17.1.  Short sequences are quickest by one CTA: 8 of 300 tokens, by 4 CTAs 7.9 us, by
+// 17.1.  (D = 32 and 64 follow the same numbers.)  Short sequences are quickest by one CTA: 8 of 300 tokens, by 4 CTAs 7.9 us, by
 // one 6.9; 16 of 700, by two 10.0, by one 9.7; 64 of 700, by one 23, the line 27.
 int team_of(const CacheQueryArgs& a) {
   const int64_t items = int64_t(a.cache.batch) * a.cache.heads;
@@ -556,7 +556,7 @@ int team_of(const CacheQueryArgs& a) {
 // Which kernel, and its cut.  More than 16 rows of a key / value head go to the
 // tcgen05 kernel (cache_chunk.cu), which reads the cache once for 256, one CTA per
 // SM: measured here / there, 16 sequences of 8192, 8 heads, 4 rows 54 / 88 us, 16 rows
-// 62 / 89 (there 20 rows 90, 32 rows 90, 128 rows 108); one of 8192, 16 rows 18 / 19.
+// 63 / 89 (there 20 rows 90, 32 rows 91, 128 rows 108); one of 8192, 16 rows 18 / 19.
 // Its chunks are of one size: the least number of chunks (of 4096 tokens at
 // most), or as many as fill the SMs one to four times, whichever is quickest in
 // this estimate, in tokens of a CTA's walk (11 to 20 ns each): a chunk with its

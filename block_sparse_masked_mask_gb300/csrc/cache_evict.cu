@@ -185,8 +185,9 @@ struct KeptPages {
 };
 
 // N: 16-byte pieces per thread of a page's keys (and as many of its values).
-// A CTA takes destination pages in turn; the kept tokens' numbers are read two
-// pages ahead and the source pages' one, so that a page waits for its own codes only.
+// A CTA takes destination pages in turn (one, up to 64 pages and heads per SM); the kept
+// tokens' numbers are read two pages ahead and the source pages' one, so that a page waits
+// for its own codes only.
 template <int N>
 __global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const EvictArgs a) {
   __shared__ uint4 moved[2 * N * kGatherThreads];  // each thread's own pieces
