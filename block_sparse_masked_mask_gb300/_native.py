@@ -1,5 +1,5 @@
-"""ctypes loader for libattnmask.so (the C ABI in include/attn_block_mask.h and
-include/attn_cache.h).
+"""ctypes loader for libattnmask.so (the C ABI in include/attn_block_mask.h,
+include/attn_cache.h and include/attn_tree.h).
 
 Argument marshalling only: every step of the computation runs in the CUDA
 library.  There is no fallback: if the library is missing this module raises.
@@ -134,8 +134,21 @@ def _configure(L: ctypes.CDLL) -> ctypes.CDLL:
         c_void_p, i64, c_void_p, c_void_p, c_int32, c_int32, c_int32, P(AttnKVCache), P(AttnKVCache),
         c_void_p, c_void_p, i64, c_void_p, c_void_p]
     L.attn_cache_get_status.argtypes = [P(AttnKVCache), c_void_p]
+    L.attn_cache_tree_build.argtypes = [
+        c_void_p, c_int32, c_void_p, c_void_p, c_int32, c_void_p, c_int32, c_void_p, P(AttnKVCache), c_void_p]
+    L.attn_cache_append_rope.argtypes = [
+        c_void_p, c_void_p, i64, i64, c_int32, c_void_p, c_void_p, i64, i64, ctypes.c_int, c_int32, c_void_p,
+        c_void_p, c_void_p, c_int32, P(AttnRopePlan), P(AttnKVCache), c_void_p]
+    L.attn_cache_tree_fwd_workspace_size.argtypes = L.attn_cache_fwd_workspace_size.argtypes
+    L.attn_cache_tree_fwd.argtypes = [
+        c_void_p, c_void_p, c_void_p, ctypes.c_int, c_int32, c_int32, ctypes.c_float, c_void_p, c_int32, c_void_p,
+        c_int32, c_void_p, c_int32, P(AttnKVCache), c_void_p, ctypes.c_size_t, c_void_p]
+    L.attn_cache_tree_keep.argtypes = [
+        c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_int32, c_void_p, P(AttnKVCache), c_void_p]
     for f in ("attn_rope_plan_init", "attn_rope", "attn_cache_append", "attn_cache_fwd_workspace_size",
-              "attn_cache_fwd", "attn_cache_weights", "attn_cache_evict", "attn_cache_get_status"):
+              "attn_cache_fwd", "attn_cache_weights", "attn_cache_evict", "attn_cache_get_status",
+              "attn_cache_tree_build", "attn_cache_append_rope", "attn_cache_tree_fwd_workspace_size",
+              "attn_cache_tree_fwd", "attn_cache_tree_keep"):
         getattr(L, f).restype = ctypes.c_int
     L.attn_get_status.argtypes = [P(AttnBlockMask), c_void_p]
     L.attn_get_status.restype = ctypes.c_int

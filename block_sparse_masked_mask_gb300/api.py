@@ -774,6 +774,208 @@ def attn_cache_evict(weights: torch.Tensor, cache: KVCache, dst: KVCache, seq_le
     return kept, new_weights, new_lens
 
 
+def attn_cache_tree_build(parents: torch.Tensor, cache: KVCache, cu_seqlens: torch.Tensor, seq_lens: torch.Tensor,
+                          max_new: int, bits: Optional[torch.Tensor] = None,
+                          positions: Optional[torch.Tensor] = None, stream=None):
+    """Masks and positions of drafted trees, whose nodes are the new tokens of each
+    sequence; once per step, for all layers.
+
+    ``parents`` (int32 [T]): each node's parent by its number in its own sequence, below
+    the node's own, or -1.  Returns (bits, positions): bit j % 32 of word j / 32 of
+    a row of ``bits`` (int32 [T, words], words = ceil(max_new / 32) in a new one) is set
+    for the node itself and its ancestors; ``positions`` (int32 [T]) are the length of
+    the text plus the number of ancestors.  Rows behind the last sequence are left as
+    they were."""
+    where = "attn_cache_tree_build"
+    _need_cache(cache, where)
+    dev, index = cache.device, cache.index
+    if parents is None:
+        raise AttnError(1, f"{where}: parents is required")
+    if not (isinstance(parents, _Tensor) and parents.dim() == 1 and _fits(parents, _I32, parents.shape, index)):
+        _need(parents, "parents", where, (_I32,), device=dev)
+        if parents.dim() != 1:
+            raise AttnError(1, f"{where}: parents must be [tokens]")
+    T = parents.shape[0]
+    if bits is not None:
+        _need_bits(bits, T, cache, where)
+    if positions is not None and not _fits(positions, _I32, (T,), index):
+        _need(positions, "positions", where, (_I32,), (T,), dev)
+    _need_seqs(cache, cu_seqlens, seq_lens, where)
+    at = _elsewhere(dev, stream)
+    s = _raw_stream(index) if at is None else at.__enter__()
+    try:
+        if bits is None:
+            bits = torch.empty((T, (int(max_new) + 31) // 32), dtype=_I32, device=dev)
+        if positions is None:
+            positions = torch.empty(T, dtype=_I32, device=dev)
+        _check(_native.lib().attn_cache_tree_build(
+            parents.data_ptr(), T, cu_seqlens.data_ptr(), seq_lens.data_ptr(), max_new, bits.data_ptr(),
+            bits.shape[1], positions.data_ptr(), cache._ref, s), where)
+    finally:
+        if at is not None:
+            at.__exit__()
+    return bits, positions
+
+
+def _need_bits(bits, T: int, cache: KVCache, where: str) -> None:
+    """32-bit words [T, any number]."""
+    if bits is None:
+        raise AttnError(1, f"{where}: bits is required")
+    if not (isinstance(bits, _Tensor) and bits.dim() == 2 and _fits(bits, _I32, (T, bits.shape[1]), cache.index)):
+        _need(bits, "bits", where, _WORD_DTYPES, device=cache.device)
+        if bits.dim() != 2 or bits.shape[0] != T:
+            raise AttnError(1, f"{where}: bits has shape {tuple(bits.shape)}, expected [{T}, words]")
+
+
+def attn_cache_append_rope(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, plan: RopePlan,
+                           cache: KVCache, cu_seqlens: torch.Tensor, seq_lens: torch.Tensor, max_new: int,
+                           positions: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                           stream=None) -> Optional[torch.Tensor]:
+    """``attn_rope`` and ``attn_cache_append`` in one: rotates q [T, H, D] and returns it,
+    and writes the rotated keys and the values [T, Hk, D] into the cache (a key goes
+    from fp32 to its code without a rounding to bf16 between).
+
+    ``positions`` (int32 [T]) are those of ``attn_cache_tree_build`` for a drafted tree; by
+    default new token i of a sequence's n stands at seq_lens[b] - n + i.  q, k and v
+    are bf16 or fp32 and may be slices of one projection; ``q_out=q`` rotates in
+    place; q may be None.  Rows behind the last sequence keep what ``q_out`` held."""
+    where = "attn_cache_append_rope"
+    _need_cache(cache, where)
+    index, dev = cache.index, cache.device
+    ks = _need_rows(k, "k", where, _ROW_DTYPES, index)
+    dtype = k.dtype
+    vs = _need_rows(v, "v", where, (dtype,), index)
+    T, h, d = k.shape
+    if k.shape != v.shape or h != cache.num_kv_heads or d != cache.head_dim:
+        raise AttnError(1, f"{where}: k and v must be [tokens, {cache.num_kv_heads}, {cache.head_dim}], got "
+                           f"{tuple(k.shape)} and {tuple(v.shape)}")
+    H = qs = qos = 0
+    if q is not None:
+        qs = _need_rows(q, "q", where, (dtype,), index)
+        n, H, qd = q.shape
+        if n != T or qd != d:
+            raise AttnError(1, f"{where}: q has shape {tuple(q.shape)}, expected [{T}, heads, {d}]")
+    elif q_out is not None:
+        raise AttnError(1, f"{where}: q_out without q")
+    if not isinstance(plan, RopePlan):
+        raise AttnError(1, f"{where}: plan must come from attn_rope_plan")
+    if positions is not None and not _fits(positions, _I32, (T,), index):
+        _need(positions, "positions", where, (_I32,), (T,), dev)
+    _need_seqs(cache, cu_seqlens, seq_lens, where)
+    at = _elsewhere(dev, stream)
+    s = _raw_stream(index) if at is None else at.__enter__()
+    try:
+        if q_out is not None:
+            qos = _need_rows(q_out, "q_out", where, (dtype,), index)
+            if q_out.shape != q.shape:
+                raise AttnError(1, f"{where}: q_out has shape {tuple(q_out.shape)}, expected {tuple(q.shape)}")
+        elif q is not None:
+            q_out, qos = torch.empty((T, H, d), dtype=dtype, device=dev), H * d
+        _check(_native.lib().attn_cache_append_rope(
+            q.data_ptr() if H else None, q_out.data_ptr() if H else None, qs, qos, H, k.data_ptr(), v.data_ptr(), ks,
+            vs, DTYPES[dtype], T, None if positions is None else positions.data_ptr(), cu_seqlens.data_ptr(),
+            seq_lens.data_ptr(), max_new, plan._ref, cache._ref, s), where)
+    finally:
+        if at is not None:
+            at.__exit__()
+    return q_out
+
+
+def attn_cache_tree_fwd_workspace_size(cache: KVCache, total_tokens: int, num_heads: int, max_new: int,
+                                       max_seqlen: int) -> int:
+    """Bytes of device workspace ``attn_cache_tree_fwd`` needs at these sizes."""
+    _need_cache(cache, "attn_cache_tree_fwd_workspace_size")
+    out = ctypes.c_size_t()
+    _check(_native.lib().attn_cache_tree_fwd_workspace_size(cache._ref, total_tokens, num_heads, max_new,
+                                                            max_seqlen, ctypes.byref(out)),
+           "attn_cache_tree_fwd_workspace_size")
+    return int(out.value)
+
+
+def attn_cache_tree_fwd(q: torch.Tensor, cache: KVCache, bits: torch.Tensor, cu_seqlens: torch.Tensor,
+                        seq_lens: torch.Tensor, max_new: int, max_seqlen: int, scale: float = 0.0,
+                        out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None, stream=None):
+    """Attention of drafted trees' queries q [T, H, D] (bf16) over the cache, which holds
+    their keys and values already (``attn_cache_append_rope``); returns
+    (O [T, H, D], LSE [H, T] fp32).
+
+    A node sees the seq_lens[b] - n tokens before its tree and those nodes of the tree
+    whose bits are set in its row of ``bits`` (``attn_cache_tree_build``, or any
+    other 32-bit words [T, words], 32 * words >= max_new).  The rest is as for
+    ``attn_cache_fwd``."""
+    where = "attn_cache_tree_fwd"
+    T, H, D = _need_queries(q, cache, where)
+    dev = cache.device
+    _need_bits(bits, T, cache, where)
+    if out is not None and not _fits(out, _BF16, q.shape, cache.index):
+        _need(out, "out", where, (q.dtype,), q.shape, dev)
+    if lse is not None and not _fits(lse, _F32, (H, T), cache.index):
+        _need(lse, "lse", where, (torch.float32,), (H, T), dev)
+    _need(workspace, "workspace", where, device=dev)
+    _need_seqs(cache, cu_seqlens, seq_lens, where)
+    at = _elsewhere(dev, stream)
+    s = _raw_stream(cache.index) if at is None else at.__enter__()
+    try:
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty((H, T), dtype=torch.float32, device=dev)
+        own = None
+        if workspace is not None:
+            ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        else:
+            ws, nbytes = None, attn_cache_tree_fwd_workspace_size(cache, T, H, max_new, max_seqlen)
+            if nbytes:
+                ws = own = torch._C._cuda_cudaCachingAllocator_raw_alloc(nbytes, s)
+        try:
+            _check(_native.lib().attn_cache_tree_fwd(
+                q.data_ptr(), out.data_ptr(), lse.data_ptr(), 0, T, H, scale, bits.data_ptr(), bits.shape[1],
+                cu_seqlens.data_ptr(), max_new, seq_lens.data_ptr(), max_seqlen, cache._ref, ws, nbytes, s), where)
+        finally:
+            if own is not None:  # reused in the order of the stream
+                torch._C._cuda_cudaCachingAllocator_raw_delete(own)
+    finally:
+        if at is not None:
+            at.__exit__()
+    return out, lse
+
+
+def attn_cache_tree_keep(path: torch.Tensor, counts: torch.Tensor, cache: KVCache, cu_seqlens: torch.Tensor,
+                         seq_lens: torch.Tensor, max_new: int, new_lens: Optional[torch.Tensor] = None,
+                         stream=None) -> torch.Tensor:
+    """Keep the accepted path of each drafted tree: of sequence b's n new tokens those of
+    the numbers path[b, :counts[b]] (int32 [B, width], ascending) move together behind
+    the text, and the others are given up.  Returns the new lengths
+    seq_lens[b] - n + counts[b] (int32 [B]; not ``seq_lens`` itself, which every layer's
+    cache still needs)."""
+    where = "attn_cache_tree_keep"
+    _need_cache(cache, where)
+    dev, index, B = cache.device, cache.index, cache.batch
+    if path is None or counts is None:
+        raise AttnError(1, f"{where}: path and counts are required")
+    if not (isinstance(path, _Tensor) and path.dim() == 2 and _fits(path, _I32, (B, path.shape[1]), index)):
+        _need(path, "path", where, (_I32,), device=dev)
+        if path.dim() != 2 or path.shape[0] != B:
+            raise AttnError(1, f"{where}: path has shape {tuple(path.shape)}, expected [{B}, width]")
+    for name, t in (("counts", counts), ("new_lens", new_lens)):
+        if t is not None and not _fits(t, _I32, (B,), index):
+            _need(t, name, where, (_I32,), (B,), dev)
+    _need_seqs(cache, cu_seqlens, seq_lens, where)
+    at = _elsewhere(dev, stream)
+    s = _raw_stream(index) if at is None else at.__enter__()
+    try:
+        if new_lens is None:
+            new_lens = torch.empty(B, dtype=_I32, device=dev)
+        _check(_native.lib().attn_cache_tree_keep(
+            path.data_ptr(), path.shape[1], counts.data_ptr(), cu_seqlens.data_ptr(), seq_lens.data_ptr(),
+            max_new, new_lens.data_ptr(), cache._ref, s), where)
+    finally:
+        if at is not None:
+            at.__exit__()
+    return new_lens
+
+
 def attn_cache_get_status(cache: KVCache, stream=None) -> int:
     """Synchronise, then return and clear the cache's device status code."""
     _need_cache(cache, "attn_cache_get_status")

@@ -21,7 +21,7 @@ LIB_PATH = os.path.join(PKG, LIB_NAME)
 
 SOURCES = ["api.cu", "blockmask.cu", "blockmask_noalloc.cu", "attn_fwd_bf16.cu", "attn_fwd_f32.cu",
            "attn_bwd_bf16.cu", "cache_api.cu", "rope.cu", "cache_append.cu", "cache_attn.cu", "cache_chunk.cu",
-           "cache_weights.cu", "cache_weights_many.cu", "cache_evict.cu"]
+           "cache_weights.cu", "cache_weights_many.cu", "cache_evict.cu", "cache_tree.cu", "tree.cu"]
 HEADERS = ["common.cuh", "ptx.cuh", "tile_pipeline.cuh", "cache.cuh", "cache_rows.cuh", "cache_tiles.cuh"]
 
 NVCC_FLAGS = [
@@ -42,7 +42,7 @@ def _nvcc() -> str:
 
 def _inputs():
     return ([os.path.join(CSRC, s) for s in SOURCES + HEADERS] +
-            [os.path.join(INCLUDE, h) for h in ("attn_block_mask.h", "attn_cache.h")] + [os.path.abspath(__file__)])
+            [os.path.join(INCLUDE, h) for h in ("attn_block_mask.h", "attn_cache.h", "attn_tree.h")] + [os.path.abspath(__file__)])
 
 
 def _stale() -> bool:

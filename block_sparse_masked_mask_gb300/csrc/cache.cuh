@@ -9,6 +9,7 @@
 #include <cuda_runtime.h>
 
 #include "attn_cache.h"
+#include "attn_tree.h"
 #include "common.cuh"
 
 namespace attnmask {
@@ -21,7 +22,8 @@ enum : int32_t {
   kErrTooManyNew = 1 << 5, // a sequence has more new tokens than max_new
   kErrHeld = 1 << 6,       // seq_lens negative, or below the new tokens of an append
   kErrBudget = 1 << 7,     // an eviction's budget negative or above max_keep
-  kErrCacheInput = kErrInputMask | kErrBadPage | kErrTooManyNew | kErrHeld | kErrBudget,
+  kErrTree = 1 << 20,      // a tree's parents, or the path kept of it (9 and up: the site of a wait)
+  kErrCacheInput = kErrInputMask | kErrBadPage | kErrTooManyNew | kErrHeld | kErrBudget | kErrTree,
 };
 
 // The cache as the kernels see it.
@@ -46,6 +48,13 @@ struct RopeArgs {
   const int32_t* cu;
   const int32_t* lens;
   bool inverse, bf16;
+};
+
+// attn_rope's queries on their way past the cache: the sequences are checked as an
+// append checks them, and rows of none that is used are left alone.
+struct RopeCheck {
+  int max_new, max_len;
+  int32_t* status;
 };
 
 struct AppendArgs {
@@ -74,6 +83,32 @@ struct CacheQueryArgs {
   const int32_t* lens;
   CacheView cache;
   float* workspace;
+};
+
+struct TreeBuildArgs {
+  const int32_t* parents;
+  uint32_t* bits;
+  int32_t* positions;
+  int words, total_tokens, max_new;
+  const int32_t* cu;
+  const int32_t* lens;
+  CacheView cache;
+};
+
+struct TreeAttnArgs {
+  CacheQueryArgs a;
+  const uint32_t* bits;
+  int words;
+};
+
+struct TreeKeepArgs {
+  const int32_t* path;
+  const int32_t* counts;
+  int32_t* new_lens;
+  int path_stride, max_new;
+  const int32_t* cu;
+  const int32_t* lens;
+  CacheView cache;
 };
 
 // How attn_cache_fwd cuts its work, and where the pieces' results meet: rows (new
@@ -108,14 +143,20 @@ struct EvictArgs {
   CacheView src, dst;
 };
 
-attn_status launch_rope(const RopeArgs& a, const attn_rope_plan& plan, cudaStream_t s);
+attn_status launch_rope(const RopeArgs& a, const attn_rope_plan& plan, cudaStream_t s, const RopeCheck* check = nullptr);
 attn_status launch_cache_append(const AppendArgs& a, cudaStream_t s);
+attn_status launch_cache_append_rope(const AppendArgs& a, const int32_t* positions, const attn_rope_plan& plan,
+                                     cudaStream_t s);
 uint64_t cache_fwd_workspace(const CacheView& c, int total_tokens, int num_heads, int max_new, int max_seqlen);
 attn_status launch_cache_fwd(const CacheQueryArgs& a, cudaStream_t s);
 attn_status launch_cache_chunk(const CacheAttnParams& p, cudaStream_t s);
 attn_status launch_cache_weights(const CacheQueryArgs& a, cudaStream_t s);
 attn_status launch_cache_weights_many(const CacheQueryArgs& a, int sms, cudaStream_t s);
 attn_status launch_cache_evict(const EvictArgs& a, cudaStream_t s);
+attn_status launch_tree_build(const TreeBuildArgs& a, cudaStream_t s);
+attn_status launch_tree_keep(const TreeKeepArgs& a, cudaStream_t s);
+uint64_t cache_tree_workspace(const CacheView& c, int total_tokens, int num_heads, int max_new, int max_seqlen);
+attn_status launch_cache_tree(const TreeAttnArgs& t, cudaStream_t s);
 
 // ---------------------------------------------------------------- device side
 

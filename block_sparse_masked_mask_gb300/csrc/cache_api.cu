@@ -1,5 +1,5 @@
-// C ABI of the rotary and cache operators (include/attn_cache.h): argument
-// checks and dispatch.
+// C ABI of the rotary and cache operators (include/attn_cache.h, include/attn_tree.h):
+// argument checks and dispatch.
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -54,6 +54,34 @@ attn_status check_sizes(const attn_kv_cache* c, int32_t total_tokens, int32_t nu
   if (int64_t(c->batch) * c->num_kv_heads * (int64_t(max_seqlen) / 64 + 1) > INT_MAX) return ATTN_ERR_UNSUPPORTED;
   const int64_t tiles = (int64_t(max_new) * (num_heads / c->num_kv_heads) + 15) / 16;
   if (tiles * ((int64_t(max_seqlen) + 255) / 256) > (int64_t(1) << 30)) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+// What the appends check alike; fills `a`.
+attn_status check_append(const void* k, const void* v, int64_t k_stride, int64_t v_stride, attn_dtype dtype,
+                         int32_t total_tokens, const int32_t* cu_seqlens, const int32_t* seq_lens, int32_t max_new,
+                         const attn_kv_cache* cache, AppendArgs* a) {
+  if (!cu_seqlens || !seq_lens || total_tokens < 0 || max_new < 0) return ATTN_ERR_INVALID_ARG;
+  if (total_tokens > 0 && (!k || !v)) return ATTN_ERR_INVALID_ARG;
+  const attn_status st = check_cache(cache, &a->cache);
+  if (st != ATTN_OK) return st;
+  if (dtype != ATTN_DTYPE_BF16 && dtype != ATTN_DTYPE_FP32) return ATTN_ERR_INVALID_ARG;
+  const int64_t size = dtype == ATTN_DTYPE_BF16 ? 2 : 4;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(cu_seqlens, 4) || !aligned(seq_lens, 4)) return ATTN_ERR_INVALID_ARG;
+  if (total_tokens > 1) {
+    const int64_t need = int64_t(cache->num_kv_heads) * cache->head_dim;
+    if (k_stride < need || v_stride < need || (k_stride * size) % 16 != 0 || (v_stride * size) % 16 != 0)
+      return ATTN_ERR_INVALID_ARG;
+  }
+  a->k = k;
+  a->v = v;
+  a->k_stride = k_stride;
+  a->v_stride = v_stride;
+  a->total_tokens = total_tokens;
+  a->max_new = max_new < total_tokens ? max_new : total_tokens;
+  a->cu = cu_seqlens;
+  a->lens = seq_lens;
+  a->bf16 = dtype == ATTN_DTYPE_BF16;
   return ATTN_OK;
 }
 
@@ -185,29 +213,11 @@ attn_status attn_rope(const void* q, void* q_out, int64_t q_stride, int64_t q_ou
 attn_status attn_cache_append(const void* k, const void* v, int64_t k_stride, int64_t v_stride, attn_dtype dtype,
                               int32_t total_tokens, const int32_t* cu_seqlens, const int32_t* seq_lens,
                               int32_t max_new, const attn_kv_cache* cache, attn_stream_t stream) {
-  if (!cu_seqlens || !seq_lens || total_tokens < 0 || max_new < 0) return ATTN_ERR_INVALID_ARG;
-  if (total_tokens > 0 && (!k || !v)) return ATTN_ERR_INVALID_ARG;
   AppendArgs a;
-  const attn_status st = check_cache(cache, &a.cache);
+  const attn_status st =
+      check_append(k, v, k_stride, v_stride, dtype, total_tokens, cu_seqlens, seq_lens, max_new, cache, &a);
   if (st != ATTN_OK) return st;
-  if (dtype != ATTN_DTYPE_BF16 && dtype != ATTN_DTYPE_FP32) return ATTN_ERR_INVALID_ARG;
-  const int64_t size = dtype == ATTN_DTYPE_BF16 ? 2 : 4;
-  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(cu_seqlens, 4) || !aligned(seq_lens, 4)) return ATTN_ERR_INVALID_ARG;
-  if (total_tokens > 1) {
-    const int64_t need = int64_t(cache->num_kv_heads) * cache->head_dim;
-    if (k_stride < need || v_stride < need || (k_stride * size) % 16 != 0 || (v_stride * size) % 16 != 0)
-      return ATTN_ERR_INVALID_ARG;
-  }
   if (total_tokens == 0 || max_new == 0) return ATTN_OK;
-  a.k = k;
-  a.v = v;
-  a.k_stride = k_stride;
-  a.v_stride = v_stride;
-  a.total_tokens = total_tokens;
-  a.max_new = max_new < total_tokens ? max_new : total_tokens;
-  a.cu = cu_seqlens;
-  a.lens = seq_lens;
-  a.bf16 = dtype == ATTN_DTYPE_BF16;
   return launch_cache_append(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -304,6 +314,134 @@ attn_status attn_cache_evict(const float* weights, int64_t weight_stride, const 
   a.new_weights = new_weights;
   a.new_lens = new_lens;
   return launch_cache_evict(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+attn_status attn_cache_tree_build(const int32_t* parents, int32_t total_tokens, const int32_t* cu_seqlens,
+                                  const int32_t* seq_lens, int32_t max_new, uint32_t* tree_bits, int32_t tree_words,
+                                  int32_t* positions, const attn_kv_cache* cache, attn_stream_t stream) {
+  if (!cu_seqlens || !seq_lens || total_tokens < 0 || max_new < 0) return ATTN_ERR_INVALID_ARG;
+  if (total_tokens > 0 && (!parents || (tree_words > 0 && !tree_bits))) return ATTN_ERR_INVALID_ARG;
+  TreeBuildArgs a;
+  const attn_status st = check_cache(cache, &a.cache);
+  if (st != ATTN_OK) return st;
+  if (tree_words < 0 || int64_t(tree_words) * 32 < max_new) return ATTN_ERR_INVALID_ARG;
+  for (const void* p : {static_cast<const void*>(parents), static_cast<const void*>(cu_seqlens),
+                        static_cast<const void*>(seq_lens), static_cast<const void*>(tree_bits),
+                        static_cast<const void*>(positions)})
+    if (!aligned(p, 4)) return ATTN_ERR_INVALID_ARG;
+  if (total_tokens == 0 || max_new == 0) return ATTN_OK;
+  a.parents = parents;
+  a.bits = tree_bits;
+  a.positions = positions;
+  a.words = tree_words;
+  a.total_tokens = total_tokens;
+  a.max_new = max_new < total_tokens ? max_new : total_tokens;
+  a.cu = cu_seqlens;
+  a.lens = seq_lens;
+  return launch_tree_build(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+attn_status attn_cache_append_rope(const void* q, void* q_out, int64_t q_stride, int64_t q_out_stride,
+                                   int32_t num_heads, const void* k, const void* v, int64_t k_stride,
+                                   int64_t v_stride, attn_dtype dtype, int32_t total_tokens, const int32_t* positions,
+                                   const int32_t* cu_seqlens, const int32_t* seq_lens, int32_t max_new,
+                                   const attn_rope_plan* plan, const attn_kv_cache* cache, attn_stream_t stream) {
+  if (!plan || plan->magic != kRopeMagic || num_heads < 0) return ATTN_ERR_INVALID_ARG;
+  AppendArgs a;
+  attn_status st = check_append(k, v, k_stride, v_stride, dtype, total_tokens, cu_seqlens, seq_lens, max_new, cache, &a);
+  if (st != ATTN_OK) return st;
+  if (plan->rotary_dim > cache->head_dim || !aligned(positions, 4)) return ATTN_ERR_INVALID_ARG;
+  if (num_heads > kMaxHeads) return ATTN_ERR_UNSUPPORTED;
+  const uintptr_t size = dtype == ATTN_DTYPE_BF16 ? 2 : 4;
+  if (num_heads > 0 && total_tokens > 0) {
+    if (!q || !q_out || !aligned(q, size) || !aligned(q_out, size)) return ATTN_ERR_INVALID_ARG;
+    // tokens must not overlap; in place, a token's row must be its own
+    const int64_t need = int64_t(num_heads) * cache->head_dim;
+    if (total_tokens > 1 && (q_stride < need || q_out_stride < need || (q == q_out && q_stride != q_out_stride)))
+      return ATTN_ERR_INVALID_ARG;
+  }
+  if (total_tokens == 0 || max_new == 0) return ATTN_OK;
+  if (num_heads > 0) {
+    RopeArgs r;
+    std::memset(&r, 0, sizeof(r));
+    r.q = q;
+    r.q_out = q_out;
+    r.q_stride = q_stride;
+    r.q_out_stride = q_out_stride;
+    r.num_heads = num_heads;
+    r.total_tokens = total_tokens;
+    r.head_dim = cache->head_dim;
+    r.batch = cache->batch;
+    r.positions = positions;
+    r.cu = cu_seqlens;
+    r.lens = seq_lens;
+    r.bf16 = dtype == ATTN_DTYPE_BF16;
+    const RopeCheck check{a.max_new, cache->max_pages * cache->page_size, cache->status};
+    st = launch_rope(r, *plan, reinterpret_cast<cudaStream_t>(stream), &check);
+    if (st != ATTN_OK) return st;
+  }
+  return launch_cache_append_rope(a, positions, *plan, reinterpret_cast<cudaStream_t>(stream));
+}
+
+attn_status attn_cache_tree_fwd_workspace_size(const attn_kv_cache* cache, int32_t total_tokens, int32_t num_heads,
+                                               int32_t max_new, int32_t max_seqlen, size_t* bytes) {
+  if (bytes == nullptr) return ATTN_ERR_INVALID_ARG;
+  CacheView v;
+  attn_status st = check_cache(cache, &v);
+  if (st == ATTN_OK) st = check_sizes(cache, total_tokens, num_heads, max_new, max_seqlen);
+  if (st != ATTN_OK) return st;
+  *bytes = size_t(cache_tree_workspace(v, total_tokens, num_heads, max_new < total_tokens ? max_new : total_tokens,
+                                       max_seqlen));
+  return ATTN_OK;
+}
+
+attn_status attn_cache_tree_fwd(const void* q, void* o, float* lse, attn_dtype dtype, int32_t total_tokens,
+                                int32_t num_heads, float scale, const uint32_t* tree_bits, int32_t tree_words,
+                                const int32_t* cu_seqlens, int32_t max_new, const int32_t* seq_lens,
+                                int32_t max_seqlen, const attn_kv_cache* cache, void* workspace,
+                                size_t workspace_bytes, attn_stream_t stream) {
+  TreeAttnArgs t;
+  std::memset(&t, 0, sizeof(t));
+  const attn_status st = check_queries(q, lse, dtype, total_tokens, num_heads, scale, cu_seqlens, max_new, seq_lens,
+                                       max_seqlen, ATTN_MASK_NONE, cache, &t.a);
+  if (st != ATTN_OK) return st;
+  if ((total_tokens > 0 && !o) || !aligned(o, 16)) return ATTN_ERR_INVALID_ARG;
+  if (tree_words < 0 || int64_t(tree_words) * 32 < max_new || !aligned(tree_bits, 4)) return ATTN_ERR_INVALID_ARG;
+  if (total_tokens > 0 && max_new > 0 && !tree_bits) return ATTN_ERR_INVALID_ARG;
+  const uint64_t need = cache_tree_workspace(t.a.cache, total_tokens, num_heads, t.a.max_new, max_seqlen);
+  if (need > 0 && (workspace == nullptr || !aligned(workspace, 256))) return ATTN_ERR_INVALID_ARG;
+  if (uint64_t(workspace_bytes) < need) return ATTN_ERR_WORKSPACE_TOO_SMALL;
+  if (total_tokens == 0 || max_new == 0) return ATTN_OK;
+  t.a.o = o;
+  t.a.lse = lse;
+  t.a.workspace = static_cast<float*>(workspace);
+  t.bits = tree_bits;
+  t.words = tree_words;
+  return launch_cache_tree(t, reinterpret_cast<cudaStream_t>(stream));
+}
+
+attn_status attn_cache_tree_keep(const int32_t* path, int32_t path_stride, const int32_t* counts,
+                                 const int32_t* cu_seqlens, const int32_t* seq_lens, int32_t max_new,
+                                 int32_t* new_lens, const attn_kv_cache* cache, attn_stream_t stream) {
+  if (!counts || !cu_seqlens || !seq_lens || !new_lens || max_new < 0 || path_stride < 0 || (path_stride > 0 && !path))
+    return ATTN_ERR_INVALID_ARG;
+  TreeKeepArgs a;
+  const attn_status st = check_cache(cache, &a.cache);
+  if (st != ATTN_OK) return st;
+  for (const void* p : {static_cast<const void*>(path), static_cast<const void*>(counts),
+                        static_cast<const void*>(cu_seqlens), static_cast<const void*>(seq_lens),
+                        static_cast<const void*>(new_lens)})
+    if (!aligned(p, 4)) return ATTN_ERR_INVALID_ARG;
+  // written while others still read the old ones
+  if (new_lens == seq_lens || new_lens == counts || new_lens == cu_seqlens) return ATTN_ERR_INVALID_ARG;
+  a.path = path;
+  a.counts = counts;
+  a.new_lens = new_lens;
+  a.path_stride = path_stride;
+  a.max_new = max_new;
+  a.cu = cu_seqlens;
+  a.lens = seq_lens;
+  return launch_tree_keep(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 attn_status attn_cache_get_status(const attn_kv_cache* cache, attn_stream_t stream) {

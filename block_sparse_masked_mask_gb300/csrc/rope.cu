@@ -29,6 +29,7 @@ struct RopeParams {
   int passes;      // passes of a warp over its heads (32 units each)
   float factor;
   uint64_t turn[ATTN_ROPE_MAX_PAIRS];
+  RopeCheck check;  // CHECKED only
 };
 
 // E elements of one memory access, E * sizeof(T) a power of two up to 16 bytes.
@@ -67,9 +68,12 @@ __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float
 __device__ __forceinline__ void from_f(float& d, float x) { d = x; }
 __device__ __forceinline__ void from_f(__nv_bfloat16& d, float x) { d = __float2bfloat16_rn(x); }
 
-// The position of row t and whether it has one.
-__device__ __forceinline__ bool position_of(const RopeArgs& a, int t, int& pos) {
-  if (a.positions) {
+// The position of row t and whether it has one.  CHECKED: only rows of sequences that
+// an append would use have one, positions given or not.
+template <bool CHECKED>
+__device__ __forceinline__ bool position_of(const RopeParams& p, int t, int& pos) {
+  const RopeArgs& a = p.a;
+  if (!CHECKED && a.positions) {
     pos = a.positions[t];
     return true;
   }
@@ -79,15 +83,24 @@ __device__ __forceinline__ bool position_of(const RopeArgs& a, int t, int& pos) 
     const int m = (b0 + b1) >> 1;
     if (a.cu[m] <= t) b0 = m; else b1 = m;
   }
+  if (CHECKED) {
+    SeqRows r;
+    if (!load_rows(a.cu, a.lens, b0, a.total_tokens, p.check.max_new, p.check.max_len, p.check.status, r, false) ||
+        r.len < r.n || t < r.q0 || t >= r.q0 + r.n)
+      return false;
+    pos = a.positions ? a.positions[t] : r.len - r.n + t - r.q0;
+    return true;
+  }
   const int s0 = a.cu[b0], s1 = a.cu[b0 + 1];
   pos = t - s0 + (a.lens ? a.lens[b0] - (s1 - s0) : 0);
   return t >= s0 && t < s1;
 }
 
 // The warp's table of (cos, sin) for row t, the factor multiplied in; false if the row has no position.
+template <bool CHECKED>
 __device__ __forceinline__ bool angles(const RopeParams& p, int t, int lane, float2* cs) {
   int pos;
-  if (!position_of(p.a, t, pos)) return false;
+  if (!position_of<CHECKED>(p, t, pos)) return false;
   for (int c = lane; c < p.rot / 2; c += 32) {
     const int64_t turn = int64_t(uint64_t(int64_t(pos)) * p.turn[c]);
     float sn, cn;
@@ -105,7 +118,7 @@ __device__ __forceinline__ bool angles(const RopeParams& p, int t, int lane, flo
 // wide accesses (rot = 50, 10400 tokens of 40 heads of 128 bf16: 37 us; by the
 // accesses that divide rot 133).
 // (Three CTAs per SM fit fp32 without spills and are 5% faster; bf16 needs the registers.)
-template <typename T, int VP, bool INTER, bool PART>
+template <typename T, int VP, bool INTER, bool PART, bool CHECKED>
 __global__ void __launch_bounds__(32 * kRopeWarps, sizeof(T) == 4 ? 3 : 1) rope_kernel(const __grid_constant__ RopeParams p) {
   __shared__ float2 cs[kRopeWarps][ATTN_ROPE_MAX_PAIRS];
   const RopeArgs& a = p.a;
@@ -150,7 +163,7 @@ __global__ void __launch_bounds__(32 * kRopeWarps, sizeof(T) == 4 ? 3 : 1) rope_
     };
 #pragma unroll
     for (int j = 0; j < kRopeUnroll; ++j) load(j, h0 + j * per_pass);
-    if (block == 0 && !angles(p, t, lane, cs[warp])) return;  // the whole warp
+    if (block == 0 && !angles<CHECKED>(p, t, lane, cs[warp])) return;  // the whole warp
     float2 c[VP];
 #pragma unroll
     for (int e = 0; e < VP; ++e) c[e] = (PART ? u * VP + e < p.rot / 2 : u < turned) ? cs[warp][u * VP + e] : make_float2(1.f, 0.f);
@@ -183,7 +196,7 @@ __global__ void __launch_bounds__(32 * kRopeWarps, sizeof(T) == 4 ? 3 : 1) rope_
 // The half layout where rot / 2 is no multiple of a wide access: a lane takes W
 // consecutive elements as they lie, and finds each one's partner, rot / 2 away, in
 // a copy of the warp's heads in shared memory.
-template <typename T, int W>
+template <typename T, int W, bool CHECKED>
 __global__ void __launch_bounds__(32 * kRopeWarps) rope_halves_kernel(const __grid_constant__ RopeParams p) {
   __shared__ float2 cs[kRopeWarps][ATTN_ROPE_MAX_PAIRS];
   __shared__ alignas(16) T copies[kRopeWarps][2][32 * W];
@@ -206,7 +219,7 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_halves_kernel(const __gr
   };
 #pragma unroll
   for (int j = 0; j < kRopeUnroll; ++j) load(j, h0 + j * per_pass);
-  if (!angles(p, t, lane, cs[warp])) return;  // the whole warp
+  if (!angles<CHECKED>(p, t, lane, cs[warp])) return;  // the whole warp
   float2 c[W];  // y = x c.x + partner c.y
   int from[W];  // the partner's place in the copy
 #pragma unroll
@@ -237,24 +250,24 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_halves_kernel(const __gr
   }
 }
 
-template <typename T, int W>
+template <typename T, int W, bool CHECKED>
 cudaError_t launch_halves(const RopeParams& p, cudaStream_t s) {
   const unsigned grid = unsigned((int64_t(p.a.total_tokens) * p.slices + kRopeWarps - 1) / kRopeWarps);
-  rope_halves_kernel<T, W><<<grid, 32 * kRopeWarps, 0, s>>>(p);
+  rope_halves_kernel<T, W, CHECKED><<<grid, 32 * kRopeWarps, 0, s>>>(p);
   return cudaGetLastError();
 }
 
-template <typename T, int VP>
+template <typename T, int VP, bool CHECKED>
 cudaError_t launch_vp(const RopeParams& p, bool interleaved, cudaStream_t s) {
   const unsigned grid = unsigned((int64_t(p.a.total_tokens) * p.slices + kRopeWarps - 1) / kRopeWarps);
   const bool part = p.rot % (2 * VP) != 0;
-  auto kernel = !interleaved ? rope_kernel<T, VP, false, false>
-                             : part ? rope_kernel<T, VP, true, VP != 1> : rope_kernel<T, VP, true, false>;
+  auto kernel = !interleaved ? rope_kernel<T, VP, false, false, CHECKED>
+                             : part ? rope_kernel<T, VP, true, VP != 1, CHECKED> : rope_kernel<T, VP, true, false, CHECKED>;
   kernel<<<grid, 32 * kRopeWarps, 0, s>>>(p);
   return cudaGetLastError();
 }
 
-template <typename T>
+template <typename T, bool CHECKED>
 cudaError_t launch_t(RopeParams& p, bool interleaved, cudaStream_t s) {
   const RopeArgs& a = p.a;
   // The widest access (up to 16 bytes) that the halves, addresses and strides allow.
@@ -289,27 +302,30 @@ cudaError_t launch_t(RopeParams& p, bool interleaved, cudaStream_t s) {
   p.slices = (all + p.passes - 1) / p.passes;
   if (halves) {
     if constexpr (kMost >= 8)
-      if (wide == 8) return launch_halves<T, 8>(p, s);
-    return launch_halves<T, 4>(p, s);
+      if (wide == 8) return launch_halves<T, 8, CHECKED>(p, s);
+    return launch_halves<T, 4, CHECKED>(p, s);
   }
   switch (vp) {
-    case 8: if constexpr (kMost >= 8) return launch_vp<T, 8>(p, interleaved, s);
-    case 4: return launch_vp<T, 4>(p, interleaved, s);
-    case 2: return launch_vp<T, 2>(p, interleaved, s);
-    default: return launch_vp<T, 1>(p, interleaved, s);
+    case 8: if constexpr (kMost >= 8) return launch_vp<T, 8, CHECKED>(p, interleaved, s);
+    case 4: return launch_vp<T, 4, CHECKED>(p, interleaved, s);
+    case 2: return launch_vp<T, 2, CHECKED>(p, interleaved, s);
+    default: return launch_vp<T, 1, CHECKED>(p, interleaved, s);
   }
 }
 
 }  // namespace
 
-attn_status launch_rope(const RopeArgs& a, const attn_rope_plan& plan, cudaStream_t s) {
+attn_status launch_rope(const RopeArgs& a, const attn_rope_plan& plan, cudaStream_t s, const RopeCheck* check) {
   RopeParams p;
   p.a = a;
   p.rot = plan.rotary_dim;
   p.factor = plan.result_factor;
   for (int i = 0; i < ATTN_ROPE_MAX_PAIRS; ++i) p.turn[i] = plan.turn[i];
-  const cudaError_t e = a.bf16 ? launch_t<__nv_bfloat16>(p, plan.interleaved != 0, s)
-                               : launch_t<float>(p, plan.interleaved != 0, s);
+  p.check = check ? *check : RopeCheck{};
+  const bool inter = plan.interleaved != 0;
+  const cudaError_t e =
+      check ? (a.bf16 ? launch_t<__nv_bfloat16, true>(p, inter, s) : launch_t<float, true>(p, inter, s))
+            : (a.bf16 ? launch_t<__nv_bfloat16, false>(p, inter, s) : launch_t<float, false>(p, inter, s));
   return e == cudaSuccess ? ATTN_OK : record_cuda_error(e, "attn_rope launch");
 }
 
