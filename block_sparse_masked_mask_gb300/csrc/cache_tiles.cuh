@@ -43,7 +43,8 @@ struct CodeTile {
 // tile of hi at `tiles` and of the tile of lo behind it (zeros if not `real`);
 // returns the scale's inverse, NaN for an infinite query, which has no scores.
 template <int D>
-__device__ __forceinline__ float split_query(const __nv_bfloat16* query, bool real, uint8_t* tiles, int row) {
+__device__ __forceinline__ float split_query(const __nv_bfloat16* query, bool real, uint8_t* tiles, int row,
+                                             int behind = CodeTile<D>::BYTES) {
   uint4 q[D / 8];
   float amax = 0.f;
   const uint4* src = reinterpret_cast<const uint4*>(query);
@@ -75,7 +76,7 @@ __device__ __forceinline__ float split_query(const __nv_bfloat16* query, bool re
     }
     const uint32_t at = CodeTile<D>::unit(row, i);
     *reinterpret_cast<uint4*>(tiles + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4*>(tiles + CodeTile<D>::BYTES + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    *reinterpret_cast<uint4*>(tiles + behind + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
   return amax < INFINITY ? pow2f(e - 7) : __int_as_float(0x7FC00000);
 }

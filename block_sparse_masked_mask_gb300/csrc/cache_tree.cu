@@ -1,146 +1,837 @@
-// Attention of trees of drafted tokens over the 8-bit cache.
+// Attention of trees of drafted tokens over the 8-bit cache, on the tcgen05 tensor
+// cores.
 //
-// A CTA takes eight rows of one sequence and key / value head and walks the tokens
-// 128 at a time: each thread scores one token against every row, each warp settles
-// the running maximum and sum of two rows, and each thread then adds up one
-// dimension of O.  All in fp32.
+// A tree has a few dozen nodes, so up to 128 rows (nodes times query heads of the
+// group) share each cached byte: enough for the tensor cores, too few to fill their
+// 128 lanes.  So the products are turned round: tokens are their M, rows their N,
+// padded to 16, 32, 64 or 128 only.
+//  * S^T = K Q^T on the codes as they lie (kind::f8f6f4), a query as the sum of two
+//    e4m3 numbers (cache_tiles.cuh).  A thread of the softmax owns one token: its
+//    page's scales are the thread's own, and every one has work whatever the rows.
+//  * O^T += V^T P^T in fp16: one warpgroup turns the values' codes into fp16 tiles in
+//    shared memory, the softmax writes its weights there too.
+//  * Scores, scales, references and far pages are those of cache_attn.cu: the weight is
+//    2^(s + x - m), x the exponent of the page's value scale.  m belongs to a row
+//    and so to all threads: they vote on every tile whether some weight would pass 2^15,
+//    and only then look for the rows' maxima and move the references.
+//  * A row's sum is kept by every token's thread and added up at a segment's end.
+//  * The masks matter in the tiles that hold the tree (and at the end of a sequence): a
+//    thread collects the bits of its token, one per row, while it waits for its scores.
+// Work: tiles of 128 tokens of all (sequence, head, tile of rows)s form one line that
+// is cut evenly among one CTA per SM; a CTA's piece is walked segment by segment
+// without a pause between them: the rings of tiles run on, queries and O have
+// two buffers each.  Segments that are not whole meet in a second kernel
+// (cache_join.cuh), two per CTA at most.
+// Warps (512 threads):
+//   0-3, 4-7   softmax of the first and second half of the rows, a thread per token
+//   8-11       queries; values: codes to fp16 tiles
+//   12         pages, scales and TMA of the codes
+//   13, 14     tcgen05 issuers of S^T and of O^T (which also owns TMEM)
+//   15         the line: the CTA's segments
+// Every wait is bounded and ends in ATTN_ERR_DEVICE_TIMEOUT in the cache's status word.
+// Each role waits only for an earlier tile's events of the others, or for this
+// tile's by a role that comes before it (line, pages, queries and keys, S^T, softmax,
+// values, O^T), so the order of tiles carries every wait to its end.  Warps of the softmax
+// meet at barriers without a bound: a wait that ran out counts in the vote behind it, and
+// they leave together.
+#include <algorithm>
 #include <cmath>
 
-#include "cache_rows.cuh"
+#include "cache_join.cuh"
+#include "cache_tiles.cuh"
 
 namespace attnmask {
 namespace {
 
-constexpr int kTreeThreads = 128, kTreeRows = 8;
+constexpr int kTreeThreads = 512;
+constexpr int kWarpConvert = 8, kWarpPages = 12, kWarpS = 13, kWarpO = 14, kWarpLine = 15;
+constexpr int kNoPage = INT_MIN, kFar = 1;  // of a block of 16 tokens, as in cache_chunk.cu
+constexpr int kTreeSms = 152;
+constexpr float kNoReference = -0x1p100f;   // of a row that has seen nothing yet
+
+struct TreeParams {
+  CacheQueryArgs a;
+  const uint32_t* bits;
+  int words;
+  int G;
+  int ctas, least;  // least: tiles of a CTA's piece
+  float scale_log2;
+  float* part_o;    // [2 * ctas][N] rows of head_dim, as for few rows in cache_attn.cu
+  float2* part_m;
+};
+
+// A piece of the line in one (sequence, head, tile of rows).
+struct Segment {
+  int tiles;  // 0: there is no further one
+  int b, h, row0, rows, q0, n, len, token, slot;  // slot of the partial result, -1: whole
+};
+
+__device__ __forceinline__ int row_tiles(const SeqRows& r, int G, int N) { return (r.n * G + N - 1) / N; }
+__device__ __forceinline__ int tiles_of(const SeqRows& r) { return r.n == 0 ? 0 : (r.len + kTile - 1) / kTile; }
+
+template <int N>
+struct TreeUnits {
+  const TreeParams& p;
+  bool note;
+  __device__ int operator()(int b) const {
+    const CacheQueryArgs& a = p.a;
+    SeqRows r;
+    if (!load_rows(a.cu, a.lens, b, a.total_tokens, a.max_new, a.max_seqlen, a.cache.status, r, note)) return 0;
+    if (r.len < r.n) {
+      if (note) atomicOr(a.cache.status, kErrHeld);
+      return 0;
+    }
+    return tiles_of(r) * row_tiles(r, p.G, N) * a.cache.heads;
+  }
+};
+__device__ __forceinline__ int tree_share(int total, const TreeParams& p) {
+  return max(p.least, (total + p.ctas - 1) / p.ctas);
+}
+
+// N 16-bit rows of 128 tokens (P^T), or D dimensions of 64 tokens (V): MN-major, rows of 128
+// bytes at most, swizzled over their width.
+template <int E, int TOKENS>
+struct WideTile {
+  static constexpr int CE = E < 64 ? E : 64, ROWB = CE * 2, CHUNK = TOKENS * ROWB, BYTES = E / CE * CHUNK;
+  static constexpr uint32_t SW = ROWB == 128 ? ptx::kSwizzle128B : ROWB == 64 ? ptx::kSwizzle64B : ptx::kSwizzle32B;
+  __device__ static uint32_t unit(int token, int u) {  // byte offset of 16-byte unit u of the token
+    const int x = ROWB == 128 ? (token & 7) : ROWB == 64 ? ((token >> 1) & 3) : ((token >> 2) & 1);
+    constexpr int PER = ROWB / 16;
+    return uint32_t(u / PER * CHUNK + token * ROWB + (((u % PER) ^ x) << 4));
+  }
+  __device__ static uint64_t desc(uint32_t addr) { return ptx::smem_desc(addr, CHUNK, 8 * ROWB, SW); }
+  __host__ __device__ static constexpr uint64_t step(int kk) { return uint64_t(kk * 16 * ROWB) >> 4; }
+};
+
+template <int D, int N>
+struct TreeCfg {
+  using V = WideTile<D, 64>;    // half a tile of tokens
+  using P = WideTile<N, kTile>;
+  static constexpr int KT = CodeTile<D>::BYTES;   // a tile of codes
+  static constexpr int QT = 2 * N * D;            // queries: hi, lo
+  static constexpr int NQ = N == 128 ? 1 : 2;
+  static constexpr int NK = N <= 32 ? 4 : N == 64 ? 3 : 2, NR = NK;
+  static constexpr int NV = N == 16 ? 4 : 3;      // halves
+  static constexpr int NSCL = 8, NSEG = 4;
+  // (For D < 128 a product's A operand, 128 dimensions wide, reaches past the fp16 tile,
+  // whose rows past D are lanes of O^T that nobody reads: into what lies behind it.)
+  static constexpr int OFF_V = 0;
+  static constexpr int OFF_P = OFF_V + NV * V::BYTES;
+  static constexpr int OFF_Q = OFF_P + 2 * P::BYTES;
+  static constexpr int OFF_K = OFF_Q + (NQ * QT + 1023) / 1024 * 1024;
+  static constexpr int OFF_R = OFF_K + NK * KT;
+  static constexpr int OFF_SCL = OFF_R + NR * KT;          // as in cache_chunk.cu
+  static constexpr int OFF_ROWS = OFF_SCL + NSCL * 8 * 16; // [2][N / 2]: factor of two rows, their references
+  static constexpr int OFF_MAX = OFF_ROWS + 2 * N * 8;     // [2][4 warps][N / 2]: maxima, then sums
+  static constexpr int OFF_OUT = OFF_MAX + 4 * N * 4;      // [N]: 1 / sum, place in the outputs
+  static constexpr int OFF_SEG = OFF_OUT + N * 8;
+  static constexpr int OFF_BAR = OFF_SEG + NSEG * 48;
+  static constexpr int B_SEGFULL = 0, B_SEGFREE = B_SEGFULL + NSEG, B_QFULL = B_SEGFREE + NSEG, B_QFREE = B_QFULL + 2,
+                       B_KFULL = B_QFREE + NQ, B_KFREE = B_KFULL + NK, B_RFULL = B_KFREE + NK, B_RFREE = B_RFULL + NR,
+                       B_VFULL = B_RFREE + NR, B_VFREE = B_VFULL + NV, B_SCLFULL = B_VFREE + NV,
+                       B_SCLFREE = B_SCLFULL + NSCL, B_SFULL = B_SCLFREE + NSCL, B_PFULL = B_SFULL + 2,
+                       B_PDONE = B_PFULL + 2, B_OFREE = B_PDONE + 2, B_DRAIN = B_OFREE + 2, NBAR = B_DRAIN + 2;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int USED = OFF_MISC + 16 + 1024;        // the base is aligned to 1024
+  // one CTA per SM: it takes all of TMEM
+  static constexpr int SMEM = USED > 116 * 1024 ? USED : 116 * 1024;
+  static_assert(SMEM <= 232448, "shared memory budget");
+  static_assert(OFF_K - OFF_P + NK * KT >= 4 * V::CHUNK, "what the A operand reaches past V");
+  // TMEM columns
+  static constexpr int S = 0, O = 2 * N;  // two buffers each
+};
+
+// v[i] of all lanes: lane c (modulo C) returns op over the lanes of v[c].
+template <int C, typename Op>
+__device__ __forceinline__ float across_lanes(float (&v)[C], int lane, const Op& op) {
+#pragma unroll
+  for (int step = C / 2; step > 0; step >>= 1) {
+    const bool up = lane & step;
+#pragma unroll
+    for (int i = 0; i < step; ++i) {
+      const float send = up ? v[i] : v[i + step], keep = up ? v[i + step] : v[i];
+      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, step));
+    }
+  }
+  float x = v[0];
+#pragma unroll
+  for (int step = C; step < 32; step <<= 1) x = op(x, __shfl_xor_sync(0xffffffffu, x, step));
+  return x;
+}
+
+template <int C>
+__device__ __forceinline__ void load_columns(uint32_t taddr, uint32_t (&r)[C]) {
+  if constexpr (C == 32) ptx::tmem_ld32(taddr, r);
+  else if constexpr (C == 16) ptx::tmem_ld16(taddr, r);
+  else ptx::tmem_ld8(taddr, r);
+}
+template <int C>
+__device__ __forceinline__ void store_columns(uint32_t taddr, const uint32_t (&r)[C]) {
+  if constexpr (C == 32) ptx::tmem_st32(taddr, r);
+  else if constexpr (C == 16) ptx::tmem_st16(taddr, r);
+  else ptx::tmem_st8(taddr, r);
+}
+
+template <int D, int N>
+__global__ void __launch_bounds__(kTreeThreads, 1)
+    cache_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                      const __grid_constant__ TreeParams p) {
+  using C = TreeCfg<D, N>;
+  extern __shared__ uint8_t smem_raw[];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const CacheQueryArgs& a = p.a;
+  const CacheView& c = a.cache;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int32_t* err = c.status;
+
+  const uint32_t raw = ptx::smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* sbase = smem_raw + (base - raw);
+  const uint32_t bars = base + C::OFF_BAR;
+  auto bar = [&](int i) { return bars + 8u * uint32_t(i); };
+  uint32_t* misc = reinterpret_cast<uint32_t*>(sbase + C::OFF_MISC);
+  volatile uint32_t* abort_flag = misc + 1;
+  float4* scl = reinterpret_cast<float4*>(sbase + C::OFF_SCL);
+
+  if (threadIdx.x == 0) {
+    auto init = [&](int first, int n, int count) {
+      for (int i = 0; i < n; ++i) ptx::mbar_init(bar(first + i), count);
+    };
+    init(C::B_SEGFULL, C::NSEG, 1);
+    init(C::B_SEGFREE, C::NSEG, 15);  // the warps 0 to 14
+    init(C::B_QFULL, 2, 4);
+    init(C::B_QFREE, C::NQ, 1);
+    init(C::B_KFULL, C::NK, 1);
+    init(C::B_KFREE, C::NK, 1);
+    init(C::B_RFULL, C::NR, 1);
+    init(C::B_RFREE, C::NR, 4);
+    init(C::B_VFULL, C::NV, 4);
+    init(C::B_VFREE, C::NV, 1);
+    init(C::B_SCLFULL, C::NSCL, 1);
+    init(C::B_SCLFREE, C::NSCL, 12);  // softmax and value warps
+    init(C::B_SFULL, 2, 1);
+    init(C::B_PFULL, 2, 8);
+    init(C::B_PDONE, 2, 1);
+    init(C::B_OFREE, 2, 8);
+    init(C::B_DRAIN, 2, 1);
+    // (the second word decides alone whether warps start: see cache_chunk.cu)
+    misc[2] = *abort_flag = (*reinterpret_cast<volatile int32_t*>(err) & kErrTimeout) ? 1u : 0u;
+    ptx::fence_mbar_init();
+  }
+  if (warp == kWarpO) {
+    ptx::tmem_alloc(ptx::smem_addr(misc), 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = misc[0];
+  const bool skip = misc[2] != 0u;
+
+  // The s-th segment, copied from its place in the ring; one arrival frees that.
+  auto segment = [&](int s, Segment& g, bool single) {
+    const int at = s % C::NSEG;
+    const bool ok = single ? wait_lane(bar(C::B_SEGFULL + at), uint32_t(s / C::NSEG) & 1u, abort_flag, err, 1)
+                           : wait_warp(bar(C::B_SEGFULL + at), uint32_t(s / C::NSEG) & 1u, abort_flag, err, 1);
+    g.tiles = 0;
+    if (!ok) return false;
+    const int4* w = reinterpret_cast<const int4*>(sbase + C::OFF_SEG + at * 48);
+    const int4 x = w[0], y = w[1], z = w[2];
+    g = Segment{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, z.x, z.y};
+    if (single) ptx::mbar_arrive(bar(C::B_SEGFREE + at));
+    else warp_arrive(bar(C::B_SEGFREE + at), lane);
+    return true;
+  };
+
+  if (skip) {
+    // nothing issued, nothing to drain
+  } else if (warp == kWarpLine) {
+    // -------------------------------------------------------------- segments
+    const TreeUnits<N> units{p, blockIdx.x == 0};
+    const UnitLine line(units, c.batch, lane);
+    const int piece = tree_share(line.total, p);
+    int pos = int(min(int64_t(blockIdx.x) * piece, int64_t(line.total)));
+    const int stop = min(pos + piece, line.total);
+    int b = 0, before = 0;
+    if (pos < stop) b = line.find(units, c.batch, lane, pos, before);
+    for (int s = 0;; ++s) {
+      Segment g{};
+      while (pos < stop) {
+        SeqRows r;
+        const bool good = load_rows(a.cu, a.lens, b, a.total_tokens, a.max_new, a.max_seqlen, err, r, false);
+        const int U = good && r.len >= r.n ? tiles_of(r) : 0, RT = U ? row_tiles(r, p.G, N) : 0;
+        if (pos >= before + U * RT * c.heads) {
+          before += U * RT * c.heads;
+          ++b;
+          continue;
+        }
+        const int item = (pos - before) / U, u0 = (pos - before) % U, u1 = min(U, u0 + stop - pos);
+        g.tiles = u1 - u0;
+        g.b = b;
+        g.h = item / RT;
+        g.row0 = item % RT * N;
+        g.rows = min(N, r.n * p.G - g.row0);
+        g.q0 = r.q0;
+        g.n = r.n;
+        g.len = r.len;
+        g.token = u0 * kTile;
+        g.slot = u0 == 0 && u1 == U ? -1 : 2 * int(blockIdx.x) + (u0 > 0 ? 0 : 1);
+        pos += u1 - u0;
+        break;
+      }
+      const int at = s % C::NSEG;
+      if (s >= C::NSEG && !wait_warp(bar(C::B_SEGFREE + at), uint32_t(s / C::NSEG - 1) & 1u, abort_flag, err, 2)) break;
+      if (lane == 0) {
+        int4* w = reinterpret_cast<int4*>(sbase + C::OFF_SEG + at * 48);
+        w[0] = make_int4(g.tiles, g.b, g.h, g.row0);
+        w[1] = make_int4(g.rows, g.q0, g.n, g.len);
+        w[2] = make_int4(g.token, g.slot, 0, 0);
+        ptx::mbar_arrive(bar(C::B_SEGFULL + at));
+      }
+      __syncwarp();
+      if (g.tiles == 0) break;
+    }
+  } else if (warp == kWarpPages) {
+    // -------------------------------------------------------------- pages, scales, codes
+    // Eight lanes a tile, one per 16 tokens: lanes 8 q .. 8 q + 7 look up the q-th
+    // tile of four.  Page numbers are read two fours ahead, scales one.
+    const int step = (1 << c.page_log2) / 16;  // lanes per page
+    const uint32_t bytes = uint32_t(D) << c.page_log2;  // of a page's keys
+    if (lane == 0) {
+      ptx::prefetch_tensormap(&tmK);
+      ptx::prefetch_tensormap(&tmV);
+    }
+    Segment g;
+    int T = 0, done = 0, done_v = 0;
+    bool ok = true;
+    for (int s = 0; ok && segment(s, g, false) && g.tiles; ++s) {
+      const int end = min(g.token + g.tiles * kTile, g.len);
+      auto token = [&](int j) { return g.token + j * kTile + lane * 16; };  // of the four from j
+      auto number = [&](int j) { return page_number(c, g.b, token(j), token(j) < end); };
+      auto scales = [&](int j, int id) {
+        const bool fine = token(j) < end && in_pool(c, id);
+        const int64_t at = fine ? int64_t(id) * c.heads + g.h : 0;
+        return make_float2(fine ? __ldg(c.k_scale + at) : 0.f, fine ? __ldg(c.v_scale + at) : 0.f);
+      };
+      int id = 0, id_next = number(0), id_after = number(4);
+      float2 sc = make_float2(0.f, 0.f), sc_next = scales(0, id_next);
+      int x_top = 0;  // largest exponent of the values so far, if above that of values up to 448
+      for (int j = 0; j < g.tiles; ++j, ++T) {
+        if ((j & 3) == 0) {
+          id = id_next;
+          id_next = id_after;
+          id_after = number(j + 8);
+          sc = sc_next;
+          sc_next = scales(j + 4, id_next);
+        }
+        const int ss = T % C::NSCL, ks = T % C::NK, rs = T % C::NR;
+        const bool mine = lane >> 3 == (j & 3), here = mine && token(j & ~3) < end, fine = here && in_pool(c, id);
+        if (here && !fine) atomicOr(err, kErrBadPage);
+        if (T >= C::NSCL && !wait_warp(bar(C::B_SCLFREE + ss), uint32_t(T / C::NSCL - 1) & 1u, abort_flag, err, 3)) { ok = false; break; }
+        const int x = exponent_of(sc.y);
+        if (__any_sync(0xffffffffu, fine && x > x_top)) x_top = max(x_top, __reduce_max_sync(0xffffffffu, fine ? x : 0));
+        if (mine) {
+          const bool far = x < x_top - kSpread;
+          scl[ss * 8 + (lane & 7)] =
+              fine ? make_float4(sc.x, float(x), far ? 0.f : pow2f(max(-126, -x)), __int_as_float(far ? kFar : 0))
+                   : make_float4(0.f, 0.f, 0.f, __int_as_float(kNoPage));
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(C::B_SCLFULL + ss));
+        if (T >= C::NK && !wait_warp(bar(C::B_KFREE + ks), uint32_t(T / C::NK - 1) & 1u, abort_flag, err, 4)) { ok = false; break; }
+        const bool load = fine && lane % step == 0;  // one lane per page (eight lanes are whole pages)
+        const uint32_t loads = __popc(__ballot_sync(0xffffffffu, load));
+        if (lane == 0) ptx::mbar_arrive_expect_tx(bar(C::B_KFULL + ks), bytes * loads);
+        __syncwarp();
+        if (load)
+          ptx::tma_load_4d(base + C::OFF_K + ks * C::KT + (lane & 7) * 16 * D, &tmK, bar(C::B_KFULL + ks), 0, 0, g.h, id);
+        done = T + 1;
+        if (T >= C::NR && !wait_warp(bar(C::B_RFREE + rs), uint32_t(T / C::NR - 1) & 1u, abort_flag, err, 5)) { ok = false; break; }
+        if (lane == 0) ptx::mbar_arrive_expect_tx(bar(C::B_RFULL + rs), bytes * loads);
+        __syncwarp();
+        if (load)
+          ptx::tma_load_4d(base + C::OFF_R + rs * C::KT + (lane & 7) * 16 * D, &tmV, bar(C::B_RFULL + rs), 0, 0, g.h, id);
+        done_v = T + 1;
+      }
+    }
+    // do not leave while a copy may still be writing shared memory
+    if (lane == 0) {
+      for (int i = 0; i < C::NK; ++i) {
+        if (done <= i) continue;
+        const int last = i + C::NK * ((done - 1 - i) / C::NK);
+        drain_bar(bar(C::B_KFULL + i), uint32_t(last / C::NK) & 1u, err);
+      }
+      for (int i = 0; i < C::NR; ++i) {
+        if (done_v <= i) continue;
+        const int last = i + C::NR * ((done_v - 1 - i) / C::NR);
+        drain_bar(bar(C::B_RFULL + i), uint32_t(last / C::NR) & 1u, err);
+      }
+    }
+    __syncwarp();
+  } else if (warp == kWarpS) {
+    // -------------------------------------------------------------- S^T issuer
+    if (lane == 0) {
+      constexpr uint32_t IDESC = ptx::idesc_e4m3_f32(128, N);
+      const uint64_t qd = ptx::smem_desc(base + C::OFF_Q, 16u, 8 * D, CodeTile<D>::SW);
+      const uint64_t kd = ptx::smem_desc(base + C::OFF_K, 16u, 8 * D, CodeTile<D>::SW);
+      Segment g;
+      int T = 0;
+      bool ok = true;
+      for (int s = 0; ok && segment(s, g, true) && g.tiles; ++s) {
+        ok = wait_lane(bar(C::B_QFULL + (s & 1)), uint32_t(s >> 1) & 1u, abort_flag, err, 6);
+        const uint64_t qhi = qd + uint64_t((s % C::NQ) * C::QT >> 4), qlo = qhi + uint64_t(N * D >> 4);
+        for (int j = 0; ok && j < g.tiles; ++j, ++T) {
+          const int ks = T % C::NK, f = T & 1;
+          ok = wait_lane(bar(C::B_KFULL + ks), uint32_t(T / C::NK) & 1u, abort_flag, err, 7) &&
+               // the softmax has read the scores that lie there
+               (T < 2 || wait_lane(bar(C::B_PFULL + f), uint32_t((T >> 1) - 1) & 1u, abort_flag, err, 8));
+          if (!ok) break;
+          ptx::tc_fence_after();
+          const uint64_t ki = kd + uint64_t(ks * C::KT >> 4);
+          const uint32_t s_tmem = tmem + uint32_t(C::S + f * N);
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk) ptx::mma_f8_ss(s_tmem, ki + 2 * kk, qhi + 2 * kk, IDESC, kk > 0);
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk) ptx::mma_f8_ss(s_tmem, ki + 2 * kk, qlo + 2 * kk, IDESC, 1);
+          ptx::mma_commit(bar(C::B_SFULL + f));
+          ptx::mma_commit(bar(C::B_KFREE + ks));
+          if (j == g.tiles - 1) ptx::mma_commit(bar(C::B_QFREE + s % C::NQ));
+        }
+      }
+      // every product this thread issued has finished once this arrives
+      ptx::mma_commit(bar(C::B_DRAIN));
+      drain_bar(bar(C::B_DRAIN), 0, err);
+    }
+    __syncwarp();
+  } else if (warp == kWarpO) {
+    // -------------------------------------------------------------- O^T issuer
+    if (lane == 0) {
+      constexpr uint32_t IDESC = ptx::idesc_f16_f32(128, N, true, true);
+      const uint64_t vd = C::V::desc(base + C::OFF_V), pd = C::P::desc(base + C::OFF_P);
+      Segment g;
+      int T = 0;
+      bool ok = true;
+      for (int s = 0; ok && segment(s, g, true) && g.tiles; ++s) {
+        if (s >= 2) ok = wait_lane(bar(C::B_OFREE + (s & 1)), uint32_t((s >> 1) - 1) & 1u, abort_flag, err, 9);
+        const uint32_t o_tmem = tmem + uint32_t(C::O + (s & 1) * N);
+        for (int j = 0; ok && j < g.tiles; ++j, ++T) {
+          const int f = T & 1;
+          ok = wait_lane(bar(C::B_PFULL + f), uint32_t(T >> 1) & 1u, abort_flag, err, 10);
+          const uint64_t pi = pd + uint64_t(f * C::P::BYTES >> 4);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int x = 2 * T + half, vs = x % C::NV;
+            ok = ok && wait_lane(bar(C::B_VFULL + vs), uint32_t(x / C::NV) & 1u, abort_flag, err, 11);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            const uint64_t vi = vd + uint64_t(vs * C::V::BYTES >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              ptx::mma_ss(o_tmem, vi + C::V::step(kk), pi + C::P::step(4 * half + kk), IDESC, (j > 0 || half > 0 || kk > 0) ? 1u : 0u);
+            ptx::mma_commit(bar(C::B_VFREE + vs));
+          }
+          if (ok) ptx::mma_commit(bar(C::B_PDONE + f));
+        }
+      }
+      ptx::mma_commit(bar(C::B_DRAIN + 1));
+      drain_bar(bar(C::B_DRAIN + 1), 0, err);
+    }
+    __syncwarp();
+  } else if (warp >= kWarpConvert) {
+    // -------------------------------------------------------------- queries, values
+    constexpr int PPT = D / 16;        // 16-byte pieces of codes per token = pieces per thread of a tile
+    const int ct = threadIdx.x - kWarpConvert * 32;
+    Segment g;
+    int T = 0;
+    bool ok = true;
+    for (int s = 0; ok && segment(s, g, false) && g.tiles; ++s) {
+      // the queries two segments back are used, and so are their factors
+      if (s >= C::NQ) ok = wait_warp(bar(C::B_QFREE + s % C::NQ), uint32_t(s / C::NQ - 1) & 1u, abort_flag, err, 12);
+      if (ok && s >= 2) ok = wait_warp(bar(C::B_OFREE + (s & 1)), uint32_t((s >> 1) - 1) & 1u, abort_flag, err, 13);
+      if (!ok) break;
+      if (ct < N) {
+        const bool real = ct < g.rows;
+        const int rg = g.row0 + (real ? ct : 0);
+        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) +
+                                 (int64_t(g.q0 + rg / p.G) * a.num_heads + g.h * p.G + rg % p.G) * D;
+        const float f = p.scale_log2 * split_query<D>(q, real, sbase + C::OFF_Q + (s % C::NQ) * C::QT, ct, N * D);
+        reinterpret_cast<float*>(sbase + C::OFF_ROWS)[(s & 1) * 2 * N + ct / 2 * 4 + (ct & 1)] = f;
+      }
+      ptx::fence_proxy_async_smem();
+      warp_arrive(bar(C::B_QFULL + (s & 1)), lane);
+      const int end = min(g.token + g.tiles * kTile, g.len);
+      for (int j = 0; j < g.tiles; ++j, ++T) {
+        const int rs = T % C::NR, ss = T % C::NSCL;
+        // (the scales' slot was written before this arrived)
+        if (!wait_warp(bar(C::B_RFULL + rs), uint32_t(T / C::NR) & 1u, abort_flag, err, 14)) { ok = false; break; }
+        uint4 next[PPT];
+#pragma unroll
+        for (int i = 0; i < PPT; ++i)
+          next[i] = *reinterpret_cast<const uint4*>(sbase + C::OFF_R + rs * C::KT + (i * 128 + ct) * 16);
+        const bool gone = __float_as_int(scl[ss * 8 + (lane & 7)].w) < 0;
+        if (__any_sync(0xffffffffu, gone) || g.token + (j + 1) * kTile > end) {
+          // behind the end, or without a page: weights of 0 times 0
+#pragma unroll
+          for (int i = 0; i < PPT; ++i) {
+            const int row = (i * 128 + ct) / PPT;
+            if (g.token + j * kTile + row >= end || __float_as_int(scl[ss * 8 + row / 16].w) < 0)
+              next[i] = make_uint4(0, 0, 0, 0);
+          }
+        }
+        warp_arrive(bar(C::B_RFREE + rs), lane);
+        if (lane == 0) ptx::mbar_arrive(bar(C::B_SCLFREE + ss));
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int x = 2 * T + half, vs = x % C::NV;
+          if (x >= C::NV && !wait_warp(bar(C::B_VFREE + vs), uint32_t(x / C::NV - 1) & 1u, abort_flag, err, 15)) { ok = false; break; }
+          uint8_t* tile = sbase + C::OFF_V + vs * C::V::BYTES;
+#pragma unroll
+          for (int i = half * PPT / 2; i < (half + 1) * PPT / 2; ++i) {
+            const int y = i * 128 + ct, row = y / PPT - 64 * half, piece = y % PPT;
+            const uint4 w = next[i];
+            const uint4 lo = make_uint4(half2_of(w.x), half2_of_high(w.x), half2_of(w.y), half2_of_high(w.y));
+            const uint4 hi = make_uint4(half2_of(w.z), half2_of_high(w.z), half2_of(w.w), half2_of_high(w.w));
+            // pieces of the second row chunk store their halves the other way
+            // round: eight lanes of a token then meet eight different bank groups
+            const bool flip = piece * 16 >= C::V::CE;
+            *reinterpret_cast<uint4*>(tile + C::V::unit(row, 2 * piece + (flip ? 1 : 0))) = flip ? hi : lo;
+            *reinterpret_cast<uint4*>(tile + C::V::unit(row, 2 * piece + (flip ? 0 : 1))) = flip ? lo : hi;
+          }
+          ptx::fence_proxy_async_smem();
+          warp_arrive(bar(C::B_VFULL + vs), lane);
+        }
+        if (!ok) break;
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- softmax
+    constexpr int HALF = N / 2, CH = HALF < 32 ? HALF : 32, CHUNKS = HALF / CH;
+    const int wg = warp >> 2, w4 = warp & 3, tid = threadIdx.x & 127;  // tid: the token, a lane of TMEM
+    const uint32_t lanes = tmem + (uint32_t(w4 * 32) << 16) + uint32_t(wg * HALF);
+    float* const maxima = reinterpret_cast<float*>(sbase + C::OFF_MAX) + wg * 4 * HALF;
+    float2* const out = reinterpret_cast<float2*>(sbase + C::OFF_OUT) + wg * HALF;
+    auto meet = [&](bool x) { return ptx::named_barrier_or(1 + wg, 128, x); };
+    Segment g;
+    int T = 0;
+    for (int s = 0;; ++s) {
+      bool ok = segment(s, g, false);
+      float4* const rows = reinterpret_cast<float4*>(sbase + C::OFF_ROWS) + (s & 1) * HALF + wg * HALF / 2;
+      if (ok && g.tiles) ok = wait_warp(bar(C::B_QFULL + (s & 1)), uint32_t(s >> 1) & 1u, abort_flag, err, 16);
+      if (ok && tid < HALF) reinterpret_cast<float*>(rows)[tid / 2 * 4 + 2 + (tid & 1)] = kNoReference;
+      if (meet(!ok) || g.tiles == 0) break;
+      const int text = g.len - g.n;
+      const uint32_t o_col = lanes + uint32_t(C::O + (s & 1) * N);
+      float2 l2[HALF / 2];
+#pragma unroll
+      for (int i = 0; i < HALF / 2; ++i) l2[i] = make_float2(0.f, 0.f);
+
+      int j = 0;
+      for (; j < g.tiles; ++j, ++T) {
+        const int ss = T % C::NSCL, f = T & 1;
+        const int token = g.token + j * kTile + tid;
+        ok = wait_warp(bar(C::B_SCLFULL + ss), uint32_t(T / C::NSCL) & 1u, abort_flag, err, 17);
+        const float4 k = scl[ss * 8 + tid / 16];
+        const int flag = __float_as_int(k.w);
+        // which rows see the token
+        uint32_t seen[CHUNKS];
+        const bool masked = __any_sync(0xffffffffu, token >= text || flag < 0);
+        if (masked) {
+          const bool here = token < g.len && flag >= 0;
+          uint64_t see = here && token < text ? ~0ull : 0ull;
+          if (here && token >= text) {
+            const int node = token - text, first = g.row0 + wg * HALF, last = min(first + HALF, g.row0 + g.rows);
+            for (int i = first / p.G; i * p.G < last; ++i) {
+              if (!(__ldg(p.bits + int64_t(g.q0 + i) * p.words + (node >> 5)) >> (node & 31) & 1u)) continue;
+              const int from = max(i * p.G - first, 0), to = min((i + 1) * p.G, last) - first;  // columns
+              see |= (to >= 64 ? ~0ull : (1ull << to) - 1) & ~((1ull << from) - 1);
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < CHUNKS; ++q) seen[q] = uint32_t(see >> (q * 32));
+        }
+        ok = ok && wait_warp(bar(C::B_SFULL + f), uint32_t(T >> 1) & 1u, abort_flag, err, 18) &&
+             (T < 2 || wait_warp(bar(C::B_PDONE + f), uint32_t((T >> 1) - 1) & 1u, abort_flag, err, 19));
+        ptx::tc_fence_after();
+        const uint32_t s_col = lanes + uint32_t(C::S + f * N);
+        uint8_t* const weights = sbase + C::OFF_P + f * C::P::BYTES;
+        const float ks = k.x, x = k.y, inv = k.z;
+        bool left = false;  // the warps leave together
+#pragma unroll
+        for (int q = 0; q < CHUNKS; ++q) {
+          const float4* const row = rows + q * CH / 2;
+          uint32_t v[CH];
+          float top = -INFINITY;
+          // the base-2 logarithms of the weights
+          auto score = [&]() {
+            load_columns<CH>(s_col + q * CH, v);
+            ptx::tmem_wait_ld();
+            top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < CH / 2; ++i) {
+              const float4 r = row[i];
+              const float2 by = ptx::fmul2(make_float2(r.x, r.y), make_float2(ks, ks));
+              const float2 at = ptx::fadd2(make_float2(x, x), make_float2(-r.z, -r.w));
+              float2 y = ptx::ffma2(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), by, at);
+              if (masked) {
+                if (!(seen[q] >> (2 * i) & 1u)) y.x = -INFINITY;
+                if (!(seen[q] >> (2 * i + 1) & 1u)) y.y = -INFINITY;
+              }
+              top = ptx::fmax3(top, y.x, y.y);
+              v[2 * i] = __float_as_uint(y.x);
+              v[2 * i + 1] = __float_as_uint(y.y);
+            }
+          };
+          score();
+          if (meet(!ok || top > kMostWeight)) {
+            if (meet(!ok)) {
+              left = true;
+              break;
+            }
+            // the rows' maxima, over the tile
+            float z[CH];
+            load_columns<CH>(s_col + q * CH, v);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+              const float4 r = row[i / 2];
+              z[i] = fmaf(__uint_as_float(v[i]), (i & 1 ? r.y : r.x) * ks, x);
+              if (masked && !(seen[q] >> i & 1u)) z[i] = -INFINITY;
+            }
+            const float most = across_lanes<CH>(z, lane, [](float y, float w) { return fmaxf(y, w); });
+            const int col = lane % CH;
+            const float was = reinterpret_cast<const float*>(row)[col / 2 * 4 + 2 + (col & 1)];
+            if (lane < CH) maxima[w4 * HALF + col] = most;
+            bool fine = true;
+            if (j > 0) fine = wait_warp(bar(C::B_PDONE + (f ^ 1)), uint32_t((T - 1) >> 1) & 1u, abort_flag, err, 20);
+            if (meet(!fine)) {
+              left = true;
+              break;
+            }
+            float now = maxima[col];
+#pragma unroll
+            for (int w = 1; w < 4; ++w) now = fmaxf(now, maxima[w * HALF + col]);
+            const bool raise = now > was + kMostWeight;
+            now = raise ? now - kTopWeight : was;
+            const float half = raise ? half_factor(was, now) : 1.f;
+            if (w4 == 0 && lane < CH)
+              reinterpret_cast<float*>(rows)[(q * CH + col) / 2 * 4 + 2 + (col & 1)] = now;
+            if (j > 0) {  // O holds the earlier tiles' products, which have ended
+              ptx::tc_fence_after();
+              load_columns<CH>(o_col + q * CH, v);
+              ptx::tmem_wait_ld();
+            }
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+              const float h = __shfl_sync(0xffffffffu, half, i);
+              float& l = i & 1 ? l2[q * CH / 2 + i / 2].y : l2[q * CH / 2 + i / 2].x;
+              l = l * h * h;
+              if (j > 0) v[i] = __float_as_uint(__uint_as_float(v[i]) * (h * h));
+            }
+            if (j > 0) {
+              store_columns<CH>(o_col + q * CH, v);
+              ptx::tmem_wait_st();
+            }
+            meet(false);  // the references are written
+            score();
+          }
+          if (__any_sync(0xffffffffu, flag == kFar)) {  // sums that do not go through the weights
+#pragma unroll
+            for (int i = 0; i < CH / 2; ++i) {
+              const float y = ptx::ex2(0.5f * (__uint_as_float(v[2 * i]) - x)), z = ptx::ex2(0.5f * (__uint_as_float(v[2 * i + 1]) - x));
+              if (flag == kFar) l2[q * CH / 2 + i] = ptx::ffma2(make_float2(y, z), make_float2(y, z), l2[q * CH / 2 + i]);
+            }
+          }
+          uint32_t pk[CH / 2];
+#pragma unroll
+          for (int i = 0; i < CH / 2; ++i) {
+            const float2 w = make_float2(ptx::ex2(__uint_as_float(v[2 * i])), ptx::ex2(__uint_as_float(v[2 * i + 1])));
+            l2[q * CH / 2 + i] = ptx::ffma2(w, make_float2(inv, inv), l2[q * CH / 2 + i]);
+            pk[i] = pack_half2(w.x, w.y);
+          }
+#pragma unroll
+          for (int u = 0; u < CH / 8; ++u)
+            *reinterpret_cast<uint4*>(weights + C::P::unit(tid, (wg * HALF + q * CH) / 8 + u)) =
+                make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
+        }
+        if (left) break;
+        ptx::fence_proxy_async_smem();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          ptx::mbar_arrive(bar(C::B_PFULL + f));
+          ptx::mbar_arrive(bar(C::B_SCLFREE + ss));
+        }
+      }
+      if (j < g.tiles) break;
+
+      // ---- the segment's end: sums over the tokens, O
+      ok = wait_warp(bar(C::B_PDONE + ((T - 1) & 1)), uint32_t((T - 1) >> 1) & 1u, abort_flag, err, 21);
+#pragma unroll
+      for (int q = 0; q < CHUNKS; ++q) {
+        float z[CH];
+#pragma unroll
+        for (int i = 0; i < CH; ++i) z[i] = i & 1 ? l2[q * CH / 2 + i / 2].y : l2[q * CH / 2 + i / 2].x;
+        const float sum = across_lanes<CH>(z, lane, [](float y, float w) { return y + w; });
+        if (lane < CH) maxima[w4 * HALF + q * CH + lane] = sum;
+      }
+      if (meet(!ok)) break;
+      const int first = wg * HALF;  // of the tile's rows
+      if (tid < HALF) {
+        const float sum = (maxima[tid] + maxima[HALF + tid]) + (maxima[2 * HALF + tid] + maxima[3 * HALF + tid]);
+        const float m = reinterpret_cast<const float*>(rows)[tid / 2 * 4 + 2 + (tid & 1)];
+        const int row = first + tid, rg = g.row0 + row, head = g.h * p.G + rg % p.G, token = g.q0 + rg / p.G;
+        const bool whole = g.slot < 0;
+        if (row < g.rows) {
+          if (whole)
+            a.lse[int64_t(head) * a.total_tokens + token] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+          else
+            p.part_m[int64_t(g.slot) * N + row] = make_float2(m == kNoReference ? -INFINITY : m, sum);
+        }
+        out[tid] = make_float2(!whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum,
+                               __int_as_float(whole ? token * a.num_heads + head : g.slot * N + row));
+      }
+      meet(false);
+      ptx::tc_fence_after();
+#pragma unroll
+      for (int q = 0; q < CHUNKS; ++q) {
+        uint32_t v[CH];
+        load_columns<CH>(o_col + q * CH, v);
+        ptx::tmem_wait_ld();
+        if (q == CHUNKS - 1) {
+          ptx::tc_fence_before();
+          warp_arrive(bar(C::B_OFREE + (s & 1)), lane);
+        }
+        if (w4 * 32 < D) {
+#pragma unroll
+          for (int i = 0; i < CH; ++i) {
+            if (first + q * CH + i >= g.rows) break;
+            const float2 to = out[q * CH + i];
+            const int64_t at = int64_t(__float_as_int(to.y)) * D + tid;
+            if (g.slot < 0) static_cast<__nv_bfloat16*>(a.o)[at] = __float2bfloat16_rn(__uint_as_float(v[i]) * to.x);
+            else p.part_o[at] = __uint_as_float(v[i]);
+          }
+        }
+        __syncwarp();
+      }
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpO) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+constexpr int kJoinWarps = 8;  // per CTA
+
+// Starts while the first kernel ends; every CTA waits for its end, those with nothing to
+// join too, so that what follows on the stream does.  W warps per row.
+template <int D, int N, int W>
+__global__ void __launch_bounds__(32 * kJoinWarps) cache_tree_join_kernel(const __grid_constant__ TreeParams p) {
+  __shared__ float shared[W > 1 ? W * (D + 2) : 1];
+  const CacheQueryArgs& a = p.a;
+  const int b = blockIdx.y, w = (threadIdx.x >> 5) % W, lane = threadIdx.x & 31;
+  const int i = blockIdx.x * (kJoinWarps / W) + (threadIdx.x >> 5) / W;  // of the sequence: token, head
+  SeqRows r;
+  const bool good = load_rows(a.cu, a.lens, b, a.total_tokens, a.max_new, a.max_seqlen, a.cache.status, r, false);
+  const bool mine = good && r.len >= r.n && i < r.n * a.num_heads;
+  const int head = i % a.num_heads, row = (i / a.num_heads) * p.G + head % p.G;
+  const int U = mine ? tiles_of(r) : 0;
+  // the line before this (sequence, head, tile of rows); the division is the other kernel's
+  const TreeUnits<N> units{p, false};
+  int all = 0, first = 0;
+#pragma unroll 4
+  for (int s = lane; s < a.cache.batch; s += 32) {
+    const int n = units(s);
+    all += n;
+    first += s < b ? n : 0;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+    first += __shfl_xor_sync(0xffffffffu, first, o);
+  }
+  if (mine) first += (head / p.G * row_tiles(r, p.G, N) + row / N) * U;
+  const int piece = tree_share(all, p);
+  const int c0 = first / piece, c1 = (first + U - 1) / piece;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!mine || c0 == c1) return;  // finished by its CTA
+  auto at = [&](int j) { return int64_t(2 * (c0 + j) + (j == 0 ? 1 : 0)) * N + row % N; };
+  join_row<D, W>(p, c1 - c0 + 1, at, r.q0 + i / a.num_heads, head, w, lane, shared);
+}
+
+// Rows of a tile: the least that takes them all, or 128.
+int tile_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+
+uint64_t partial_rows(const CacheView& c, int num_heads, int max_new) {
+  return 2ull * kTreeSms * tile_rows(int64_t(max_new) * (num_heads / c.heads));
+}
+
+template <int D, int N>
+attn_status launch_dn(TreeParams& p, cudaStream_t s) {
+  using C = TreeCfg<D, N>;
+  const CacheView& c = p.a.cache;
+  CUtensorMap map, map_v;
+  if (!encode_pages<D>(&map, c, c.k_pages, true) || !encode_pages<D>(&map_v, c, c.v_pages, false))
+    return record_cuda_error(cudaErrorInvalidValue, "attn_cache_tree_fwd tensor map encoding");
+  cudaError_t e = cudaFuncSetAttribute(cache_tree_kernel<D, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return record_cuda_error(e, "attn_cache_tree_fwd configure");
+  cache_tree_kernel<D, N><<<unsigned(p.ctas), kTreeThreads, C::SMEM, s>>>(map, map_v, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return record_cuda_error(e, "attn_cache_tree_fwd launch");
+  // One warp or a CTA joins a row, as in cache_attn.cu.
+  const int64_t rows = int64_t(p.a.max_new) * p.a.num_heads;
+  const bool wide = int64_t(p.ctas) > 8 * int64_t(c.batch) * c.heads;
+  const int per_cta = wide ? 1 : kJoinWarps;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned((rows + per_cta - 1) / per_cta), unsigned(c.batch));
+  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, wide ? cache_tree_join_kernel<D, N, kJoinWarps> : cache_tree_join_kernel<D, N, 1>, p);
+  return e == cudaSuccess ? ATTN_OK : record_cuda_error(e, "attn_cache_tree_fwd join launch");
+}
 
 template <int D>
-__global__ void __launch_bounds__(kTreeThreads) cache_tree_kernel(const TreeAttnArgs t) {
-  __shared__ float q[kTreeRows][D], w[kTreeRows][kTreeThreads], factor[kTreeRows], sum[kTreeRows], top[kTreeRows];
-  const CacheQueryArgs& a = t.a;
-  const CacheView& c = a.cache;
-  const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int G = a.num_heads / c.heads;
-  SeqRows r;
-  if (!load_rows(a.cu, a.lens, b, a.total_tokens, a.max_new, a.max_seqlen, c.status, r, tid == 0)) return;
-  if (r.len < r.n) {
-    if (tid == 0) atomicOr(c.status, kErrHeld);
-    return;
-  }
-  const int row0 = blockIdx.x * kTreeRows, rows = min(kTreeRows, r.n * G - row0), base = r.len - r.n;
-  if (rows <= 0) return;
-  for (int x = tid; x < kTreeRows * D; x += kTreeThreads) {
-    const int row = row0 + x / D;
-    q[x / D][x % D] = x / D < rows ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[
-        (int64_t(r.q0 + row / G) * a.num_heads + h * G + row % G) * D + x % D]) * a.scale * 1.4426950408889634f : 0.f;
-  }
-  if (tid < kTreeRows) {
-    top[tid] = -INFINITY;
-    sum[tid] = 0.f;
-  }
-  float o[kTreeRows];
-#pragma unroll
-  for (int i = 0; i < kTreeRows; ++i) o[i] = 0.f;
-  for (int t0 = 0; t0 < r.len; t0 += kTreeThreads) {
-    __syncthreads();
-    const int token = t0 + tid;
-    const int number = page_number(c, b, token, token < r.len);
-    const bool here = token < r.len && in_pool(c, number);
-    if (token < r.len && !here) atomicOr(c.status, kErrBadPage);
-    float s[kTreeRows];
-#pragma unroll
-    for (int i = 0; i < kTreeRows; ++i) s[i] = 0.f;
-    if (here) {
-      const int64_t at = int64_t(number) * c.heads + h;
-      const uint32_t* k = reinterpret_cast<const uint32_t*>(
-          c.k_pages + ((at << c.page_log2) + (token & ((1 << c.page_log2) - 1))) * D);
-      for (int x = 0; x < D / 4; ++x) {
-        const uint32_t codes = k[x];
-        uint32_t lo = half2_of(codes), hi = half2_of_high(codes);
-        const float2 y = __half22float2(*reinterpret_cast<__half2*>(&lo)), z = __half22float2(*reinterpret_cast<__half2*>(&hi));
-#pragma unroll
-        for (int i = 0; i < kTreeRows; ++i)
-          s[i] += q[i][4 * x] * y.x + q[i][4 * x + 1] * y.y + q[i][4 * x + 2] * z.x + q[i][4 * x + 3] * z.y;
-      }
-      const float ks = c.k_scale[at];
-#pragma unroll
-      for (int i = 0; i < kTreeRows; ++i) s[i] *= ks;
-    }
-    const int node = token - base;
-#pragma unroll
-    for (int i = 0; i < kTreeRows; ++i) {
-      bool seen = here && i < rows;
-      if (seen && node >= 0) seen = t.bits[int64_t(r.q0 + (row0 + i) / G) * t.words + (node >> 5)] >> (node & 31) & 1u;
-      w[i][tid] = seen ? s[i] : -INFINITY;
-    }
-    __syncthreads();
-    for (int i = warp; i < kTreeRows; i += kTreeThreads / 32) {
-      float x[4], m = top[i];
-#pragma unroll
-      for (int y = 0; y < 4; ++y) m = fmaxf(m, x[y] = w[i][32 * y + lane]);
-#pragma unroll
-      for (int y = 16; y > 0; y >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, y));
-      const float ref = m == -INFINITY ? 0.f : m;
-      float l = 0.f;
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        x[y] = exp2f(x[y] - ref);
-        l += x[y];
-        w[i][32 * y + lane] = x[y];
-      }
-#pragma unroll
-      for (int y = 16; y > 0; y >>= 1) l += __shfl_xor_sync(0xffffffffu, l, y);
-      const float f = exp2f(top[i] - ref);
-      __syncwarp();
-      if (lane == 0) {
-        factor[i] = f;
-        sum[i] = sum[i] * f + l;
-        top[i] = m;
-      }
-    }
-    __syncthreads();
-    if (tid < D) {
-#pragma unroll
-      for (int i = 0; i < kTreeRows; ++i) o[i] *= factor[i];
-      for (int x = 0; x < min(kTreeThreads, r.len - t0); ++x) {
-        const int page = page_number(c, b, t0 + x, true);
-        if (!in_pool(c, page)) continue;
-        const int64_t at = int64_t(page) * c.heads + h;
-        uint32_t y = half2_of(c.v_pages[((at << c.page_log2) + ((t0 + x) & ((1 << c.page_log2) - 1))) * D + tid]);
-        const float v = __half22float2(*reinterpret_cast<__half2*>(&y)).x * c.v_scale[at];
-#pragma unroll
-        for (int i = 0; i < kTreeRows; ++i) o[i] = fmaf(w[i][x], v, o[i]);
-      }
-    }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kTreeRows; ++i) {
-    if (i >= rows) break;
-    const int row = row0 + i, head = h * G + row % G;
-    const int64_t token = r.q0 + row / G;
-    const float l = sum[i];
-    if (tid < D)
-      static_cast<__nv_bfloat16*>(a.o)[(token * a.num_heads + head) * D + tid] = __float2bfloat16_rn(l == 0.f ? 0.f : o[i] / l);
-    if (tid == 0)
-      a.lse[int64_t(head) * a.total_tokens + token] = l == 0.f ? -INFINITY : (top[i] + log2f(l)) * 0.69314718055994531f;
+attn_status launch_d(TreeParams& p, int N, cudaStream_t s) {
+  switch (N) {
+    case 16: return launch_dn<D, 16>(p, s);
+    case 32: return launch_dn<D, 32>(p, s);
+    case 64: return launch_dn<D, 64>(p, s);
+    default: return launch_dn<D, 128>(p, s);
   }
 }
 
 }  // namespace
 
-uint64_t cache_tree_workspace(const CacheView&, int, int, int, int) { return 0; }
+uint64_t cache_tree_workspace(const CacheView& c, int total_tokens, int num_heads, int max_new, int max_seqlen) {
+  if (total_tokens == 0 || max_new == 0 || max_seqlen == 0) return 0;
+  return partial_rows(c, num_heads, max_new) * (uint64_t(c.head_dim) * 4 + 8);
+}
 
 attn_status launch_cache_tree(const TreeAttnArgs& t, cudaStream_t s) {
-  const CacheQueryArgs& a = t.a;
-  const int64_t rows = int64_t(a.max_new) * (a.num_heads / a.cache.heads);
-  const dim3 grid(unsigned((rows + kTreeRows - 1) / kTreeRows), unsigned(a.cache.heads), unsigned(a.cache.batch));
-  switch (a.cache.head_dim) {
-    case 32: cache_tree_kernel<32><<<grid, kTreeThreads, 0, s>>>(t); break;
-    case 64: cache_tree_kernel<64><<<grid, kTreeThreads, 0, s>>>(t); break;
-    default: cache_tree_kernel<128><<<grid, kTreeThreads, 0, s>>>(t); break;
+  TreeParams p;
+  p.a = t.a;
+  p.bits = t.bits;
+  p.words = t.words;
+  p.G = t.a.num_heads / t.a.cache.heads;
+  p.ctas = kTreeSms;
+  p.least = 1;
+  p.scale_log2 = t.a.scale * 1.4426950408889634f;
+  const int N = tile_rows(int64_t(t.a.max_new) * p.G);
+  p.part_o = t.a.workspace;
+  p.part_m = reinterpret_cast<float2*>(t.a.workspace + partial_rows(t.a.cache, t.a.num_heads, t.a.max_new) * t.a.cache.head_dim);
+  switch (t.a.cache.head_dim) {
+    case 32: return launch_d<32>(p, N, s);
+    case 64: return launch_d<64>(p, N, s);
+    default: return launch_d<128>(p, N, s);
   }
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? ATTN_OK : record_cuda_error(e, "attn_cache_tree_fwd launch");
 }
 
 }  // namespace attnmask
