@@ -42,24 +42,28 @@ struct CodeTile {
 // to 2^-9 of that magnitude, and within 2^-17 of it below.  Writes `row` of the
 // tile of hi at `tiles` and of the tile of lo behind it (zeros if not `real`);
 // returns the scale's inverse, NaN for an infinite query, which has no scores.
-template <int D>
+// PARTS neighbouring lanes share a row, each with its part of the dimensions.
+template <int D, int PARTS = 1>
 __device__ __forceinline__ float split_query(const __nv_bfloat16* query, bool real, uint8_t* tiles, int row,
-                                             int behind = CodeTile<D>::BYTES) {
-  uint4 q[D / 8];
+                                             int behind = CodeTile<D>::BYTES, int part = 0) {
+  constexpr int W = D / PARTS;
+  uint4 q[W / 8];
   float amax = 0.f;
-  const uint4* src = reinterpret_cast<const uint4*>(query);
+  const uint4* src = reinterpret_cast<const uint4*>(query + part * W);
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) {
+  for (int i = 0; i < W / 8; ++i) {
     q[i] = real ? src[i] : make_uint4(0, 0, 0, 0);
     const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
   }
+#pragma unroll
+  for (int o = PARTS / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   const int e = amax > 0.f ? max(-119, min(126, exponent_of(amax))) : 0;
   const float f = pow2f(7 - e);
 #pragma unroll
-  for (int i = 0; i < D / 16; ++i) {
+  for (int i = 0; i < W / 16; ++i) {
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int e4 = 0; e4 < 4; ++e4) {
@@ -74,7 +78,7 @@ __device__ __forceinline__ float split_query(const __nv_bfloat16* query, bool re
       hi[e4] = h0 | (h1 << 16);
       lo[e4] = e4m3_pair(x0 - z0.x, x1 - z0.y) | (e4m3_pair(x2 - z1.x, x3 - z1.y) << 16);
     }
-    const uint32_t at = CodeTile<D>::unit(row, i);
+    const uint32_t at = CodeTile<D>::unit(row, part * (W / 16) + i);
     *reinterpret_cast<uint4*>(tiles + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     *reinterpret_cast<uint4*>(tiles + behind + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }

@@ -121,8 +121,8 @@ struct TreeCfg {
   static constexpr int OFF_K = OFF_Q + (NQ * QT + 1023) / 1024 * 1024;
   static constexpr int OFF_R = OFF_K + NK * KT;
   static constexpr int OFF_SCL = OFF_R + NR * KT;          // as in cache_chunk.cu
-  static constexpr int OFF_ROWS = OFF_SCL + NSCL * 8 * 16; // [2][N / 2]: factor of two rows, their references
-  static constexpr int OFF_MAX = OFF_ROWS + 2 * N * 8;     // [2][4 warps][N / 2]: maxima, then sums
+  static constexpr int OFF_ROWS = OFF_SCL + NSCL * 8 * 16; // [2][N]: the rows' factors
+  static constexpr int OFF_MAX = OFF_ROWS + 2 * N * 4;     // [2][4 warps][N / 2]: maxima, then sums
   static constexpr int OFF_OUT = OFF_MAX + 4 * N * 4;      // [N]: 1 / sum, place in the outputs
   static constexpr int OFF_SEG = OFF_OUT + N * 8;
   static constexpr int OFF_BAR = OFF_SEG + NSEG * 48;
@@ -141,37 +141,12 @@ struct TreeCfg {
   static constexpr int S = 0, O = 2 * N;  // two buffers each
 };
 
-// v[i] of all lanes: lane c (modulo C) returns op over the lanes of v[c].
-template <int C, typename Op>
-__device__ __forceinline__ float across_lanes(float (&v)[C], int lane, const Op& op) {
-#pragma unroll
-  for (int step = C / 2; step > 0; step >>= 1) {
-    const bool up = lane & step;
-#pragma unroll
-    for (int i = 0; i < step; ++i) {
-      const float send = up ? v[i] : v[i + step], keep = up ? v[i + step] : v[i];
-      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, step));
-    }
-  }
-  float x = v[0];
-#pragma unroll
-  for (int step = C; step < 32; step <<= 1) x = op(x, __shfl_xor_sync(0xffffffffu, x, step));
-  return x;
-}
-
 template <int C>
 __device__ __forceinline__ void load_columns(uint32_t taddr, uint32_t (&r)[C]) {
   if constexpr (C == 32) ptx::tmem_ld32(taddr, r);
   else if constexpr (C == 16) ptx::tmem_ld16(taddr, r);
   else ptx::tmem_ld8(taddr, r);
 }
-template <int C>
-__device__ __forceinline__ void store_columns(uint32_t taddr, const uint32_t (&r)[C]) {
-  if constexpr (C == 32) ptx::tmem_st32(taddr, r);
-  else if constexpr (C == 16) ptx::tmem_st16(taddr, r);
-  else ptx::tmem_st8(taddr, r);
-}
-
 template <int D, int N>
 __global__ void __launch_bounds__(kTreeThreads, 1)
     cache_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -449,13 +424,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       if (s >= C::NQ) ok = wait_warp(bar(C::B_QFREE + s % C::NQ), uint32_t(s / C::NQ - 1) & 1u, abort_flag, err, 12);
       if (ok && s >= 2) ok = wait_warp(bar(C::B_OFREE + (s & 1)), uint32_t((s >> 1) - 1) & 1u, abort_flag, err, 13);
       if (!ok) break;
-      if (ct < N) {
-        const bool real = ct < g.rows;
-        const int rg = g.row0 + (real ? ct : 0);
-        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) +
-                                 (int64_t(g.q0 + rg / p.G) * a.num_heads + g.h * p.G + rg % p.G) * D;
-        const float f = p.scale_log2 * split_query<D>(q, real, sbase + C::OFF_Q + (s % C::NQ) * C::QT, ct, N * D);
-        reinterpret_cast<float*>(sbase + C::OFF_ROWS)[(s & 1) * 2 * N + ct / 2 * 4 + (ct & 1)] = f;
+      {
+        constexpr int PARTS = 128 / N < D / 16 ? 128 / N : D / 16;  // threads of a row
+        const int row = ct / PARTS;
+        if (row < N) {
+          const bool real = row < g.rows;
+          const int rg = g.row0 + (real ? row : 0);
+          const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) +
+                                   (int64_t(g.q0 + rg / p.G) * a.num_heads + g.h * p.G + rg % p.G) * D;
+          const float f = p.scale_log2 * split_query<D, PARTS>(q, real, sbase + C::OFF_Q + (s % C::NQ) * C::QT, row, N * D, ct % PARTS);
+          if (ct % PARTS == 0) reinterpret_cast<float*>(sbase + C::OFF_ROWS)[(s & 1) * N + row] = f;
+        }
       }
       ptx::fence_proxy_async_smem();
       warp_arrive(bar(C::B_QFULL + (s & 1)), lane);
@@ -505,155 +484,228 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     }
   } else {
     // -------------------------------------------------------------- softmax
-    constexpr int HALF = N / 2, CH = HALF < 32 ? HALF : 32, CHUNKS = HALF / CH;
-    const int wg = warp >> 2, w4 = warp & 3, tid = threadIdx.x & 127;  // tid: the token, a lane of TMEM
+    // A warp takes 32 tokens, in two blocks of 16 (of one page each), and half of the rows;
+    // of a block, lane 4 g + i holds tokens g and g + 8 and rows 8 k + 2 i, + 1.
+    // The weights are formed and stored before the vote on the references, piece by piece, so
+    // that few scores are in registers at once; a tile whose references move repeats them.
+    constexpr int HALF = N / 2, K = HALF / 8, KL = K < 4 ? K : 4;
+    const int wg = warp >> 2, w4 = warp & 3, g4 = lane >> 2, i4 = lane & 3;
     const uint32_t lanes = tmem + (uint32_t(w4 * 32) << 16) + uint32_t(wg * HALF);
-    float* const maxima = reinterpret_cast<float*>(sbase + C::OFF_MAX) + wg * 4 * HALF;
+    float* const warps = reinterpret_cast<float*>(sbase + C::OFF_MAX) + wg * 4 * HALF;  // [warp][row]: maxima, then sums
     float2* const out = reinterpret_cast<float2*>(sbase + C::OFF_OUT) + wg * HALF;
-    auto meet = [&](bool x) { return ptx::named_barrier_or(1 + wg, 128, x); };
+    auto meet = [&](bool x) { return wg == 0 ? ptx::named_barrier_or(1, 128, x) : ptx::named_barrier_or(2, 128, x); };
+    // Scores of this warp's tokens to -inf where the row does not see the token, for which
+    // `see` of the token's lane has no bit.  In tensor memory, and rolled up: few tiles have any, and
+    // the loop over the others is the faster for being short.
+    auto hide = [&](uint32_t s_col, uint64_t see) {
+#pragma unroll 1
+      for (int x = 0; x < 2 * K; ++x) {
+        const uint32_t at = s_col + (uint32_t(16 * (x / K)) << 16) + uint32_t(8 * (x % K));
+        uint32_t v[4];
+        ptx::tmem_ld16x256(at, v);
+        ptx::tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint64_t seen = __shfl_sync(0xffffffffu, see, 16 * (x / K) + 8 * e + g4) >> (8 * (x % K) + 2 * i4);
+          if (!(seen & 1u)) v[2 * e] = 0xFF800000u;
+          if (!(seen & 2u)) v[2 * e + 1] = 0xFF800000u;
+        }
+        ptx::tmem_st16x256(at, v);
+      }
+      ptx::tmem_wait_st();
+    };
+    // (never 0, where a page is left out or the product is below fp32: a hidden score is -inf, and
+    // times 0 it would be NaN)
+    auto factor = [](float2 f, float2 ks) { return ptx::ffma2(f, ks, make_float2(0x1p-126f, 0x1p-126f)); };
+    // Half the exponent of the factor that a row's sums take; `minus` is the negative reference.
+    auto move_reference = [](float most, float& minus) {
+      const float was = -minus;
+      if (!(most > was + kMostWeight)) return 1.f;
+      minus = kTopWeight - most;
+      return half_factor(was, -minus);
+    };
+    // where this lane's row of a matrix of weights goes: a token, and the first or second
+    // eight rows of the query of sixteen
+    const int to_token = w4 * 32 + (lane & 15), to_unit = wg * (HALF / 8) + (lane >> 4);
     Segment g;
     int T = 0;
     for (int s = 0;; ++s) {
       bool ok = segment(s, g, false);
-      float4* const rows = reinterpret_cast<float4*>(sbase + C::OFF_ROWS) + (s & 1) * HALF + wg * HALF / 2;
       if (ok && g.tiles) ok = wait_warp(bar(C::B_QFULL + (s & 1)), uint32_t(s >> 1) & 1u, abort_flag, err, 16);
-      if (ok && tid < HALF) reinterpret_cast<float*>(rows)[tid / 2 * 4 + 2 + (tid & 1)] = kNoReference;
       if (meet(!ok) || g.tiles == 0) break;
       const int text = g.len - g.n;
       const uint32_t o_col = lanes + uint32_t(C::O + (s & 1) * N);
-      float2 l2[HALF / 2];
+      const float* factors = reinterpret_cast<const float*>(sbase + C::OFF_ROWS) + (s & 1) * N + wg * HALF;
+      float2 f2[K], m2[K], l2[K];  // of the rows: factor, negative reference, sum
 #pragma unroll
-      for (int i = 0; i < HALF / 2; ++i) l2[i] = make_float2(0.f, 0.f);
+      for (int k = 0; k < K; ++k) {
+        f2[k] = *reinterpret_cast<const float2*>(factors + 8 * k + 2 * i4);
+        m2[k] = make_float2(-kNoReference, -kNoReference);
+        l2[k] = make_float2(0.f, 0.f);
+      }
 
       int j = 0;
       for (; j < g.tiles; ++j, ++T) {
         const int ss = T % C::NSCL, f = T & 1;
-        const int token = g.token + j * kTile + tid;
+        const int token = g.token + j * kTile + w4 * 32 + lane;
         ok = wait_warp(bar(C::B_SCLFULL + ss), uint32_t(T / C::NSCL) & 1u, abort_flag, err, 17);
-        const float4 k = scl[ss * 8 + tid / 16];
-        const int flag = __float_as_int(k.w);
-        // which rows see the token
-        uint32_t seen[CHUNKS];
-        const bool masked = __any_sync(0xffffffffu, token >= text || flag < 0);
+        const float4 of[2] = {scl[ss * 8 + w4 * 2], scl[ss * 8 + w4 * 2 + 1]};  // of the two blocks
+        const int flags = __float_as_int(of[0].w) | __float_as_int(of[1].w);
+        // which rows see this lane's token
+        const bool masked = __any_sync(0xffffffffu, token >= text) || flags < 0;
+        uint64_t see = ~0ull;
         if (masked) {
-          const bool here = token < g.len && flag >= 0;
-          uint64_t see = here && token < text ? ~0ull : 0ull;
+          const bool here = token < g.len && __float_as_int(lane < 16 ? of[0].w : of[1].w) >= 0;
+          see = here && token < text ? ~0ull : 0ull;
           if (here && token >= text) {
             const int node = token - text, first = g.row0 + wg * HALF, last = min(first + HALF, g.row0 + g.rows);
-            for (int i = first / p.G; i * p.G < last; ++i) {
-              if (!(__ldg(p.bits + int64_t(g.q0 + i) * p.words + (node >> 5)) >> (node & 31) & 1u)) continue;
-              const int from = max(i * p.G - first, 0), to = min((i + 1) * p.G, last) - first;  // columns
-              see |= (to >= 64 ? ~0ull : (1ull << to) - 1) & ~((1ull << from) - 1);
+#pragma unroll 4
+            for (int i = first / p.G; i < (last + p.G - 1) / p.G; ++i) {
+              const uint32_t bit = __ldg(p.bits + int64_t(g.q0 + i) * p.words + (node >> 5)) >> (node & 31) & 1u;
+              const int from = max(i * p.G - first, 0), to = min((i + 1) * p.G, last) - first;  // rows of the half
+              const uint64_t span = (to >= 64 ? ~0ull : (1ull << to) - 1) & ~((1ull << from) - 1);
+              see |= bit ? span : 0ull;
             }
           }
-#pragma unroll
-          for (int q = 0; q < CHUNKS; ++q) seen[q] = uint32_t(see >> (q * 32));
         }
         ok = ok && wait_warp(bar(C::B_SFULL + f), uint32_t(T >> 1) & 1u, abort_flag, err, 18) &&
              (T < 2 || wait_warp(bar(C::B_PDONE + f), uint32_t((T >> 1) - 1) & 1u, abort_flag, err, 19));
         ptx::tc_fence_after();
         const uint32_t s_col = lanes + uint32_t(C::S + f * N);
-        uint8_t* const weights = sbase + C::OFF_P + f * C::P::BYTES;
-        const float ks = k.x, x = k.y, inv = k.z;
-        bool left = false;  // the warps leave together
+        const uint32_t weights = base + C::OFF_P + f * C::P::BYTES;
+        if (masked) hide(s_col, see);
+        float2 lt[K];  // the tile's sums
+        float top;
+        // The weights under the present references, into shared memory, and the largest of
+        // their base-2 logarithms.
+        auto weigh = [&]() {
+          top = -INFINITY;
 #pragma unroll
-        for (int q = 0; q < CHUNKS; ++q) {
-          const float4* const row = rows + q * CH / 2;
-          uint32_t v[CH];
-          float top = -INFINITY;
-          // the base-2 logarithms of the weights
-          auto score = [&]() {
-            load_columns<CH>(s_col + q * CH, v);
-            ptx::tmem_wait_ld();
-            top = -INFINITY;
+          for (int z = 0; z < 2; ++z) {
+            const float2 ks = make_float2(of[z].x, of[z].x), x = make_float2(of[z].y, of[z].y);
+            const float2 inv = make_float2(of[z].z, of[z].z);
 #pragma unroll
-            for (int i = 0; i < CH / 2; ++i) {
-              const float4 r = row[i];
-              const float2 by = ptx::fmul2(make_float2(r.x, r.y), make_float2(ks, ks));
-              const float2 at = ptx::fadd2(make_float2(x, x), make_float2(-r.z, -r.w));
-              float2 y = ptx::ffma2(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), by, at);
-              if (masked) {
-                if (!(seen[q] >> (2 * i) & 1u)) y.x = -INFINITY;
-                if (!(seen[q] >> (2 * i + 1) & 1u)) y.y = -INFINITY;
-              }
-              top = ptx::fmax3(top, y.x, y.y);
-              v[2 * i] = __float_as_uint(y.x);
-              v[2 * i + 1] = __float_as_uint(y.y);
-            }
-          };
-          score();
-          if (meet(!ok || top > kMostWeight)) {
-            if (meet(!ok)) {
-              left = true;
-              break;
-            }
-            // the rows' maxima, over the tile
-            float z[CH];
-            load_columns<CH>(s_col + q * CH, v);
-            ptx::tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < CH; ++i) {
-              const float4 r = row[i / 2];
-              z[i] = fmaf(__uint_as_float(v[i]), (i & 1 ? r.y : r.x) * ks, x);
-              if (masked && !(seen[q] >> i & 1u)) z[i] = -INFINITY;
-            }
-            const float most = across_lanes<CH>(z, lane, [](float y, float w) { return fmaxf(y, w); });
-            const int col = lane % CH;
-            const float was = reinterpret_cast<const float*>(row)[col / 2 * 4 + 2 + (col & 1)];
-            if (lane < CH) maxima[w4 * HALF + col] = most;
-            bool fine = true;
-            if (j > 0) fine = wait_warp(bar(C::B_PDONE + (f ^ 1)), uint32_t((T - 1) >> 1) & 1u, abort_flag, err, 20);
-            if (meet(!fine)) {
-              left = true;
-              break;
-            }
-            float now = maxima[col];
-#pragma unroll
-            for (int w = 1; w < 4; ++w) now = fmaxf(now, maxima[w * HALF + col]);
-            const bool raise = now > was + kMostWeight;
-            now = raise ? now - kTopWeight : was;
-            const float half = raise ? half_factor(was, now) : 1.f;
-            if (w4 == 0 && lane < CH)
-              reinterpret_cast<float*>(rows)[(q * CH + col) / 2 * 4 + 2 + (col & 1)] = now;
-            if (j > 0) {  // O holds the earlier tiles' products, which have ended
-              ptx::tc_fence_after();
-              load_columns<CH>(o_col + q * CH, v);
+            for (int k0 = 0; k0 < K; k0 += KL) {
+              uint32_t v[4 * KL], pk[2 * KL];
+              ptx::tmem_ld16x256(s_col + (uint32_t(16 * z) << 16) + uint32_t(8 * k0), v);
               ptx::tmem_wait_ld();
-            }
 #pragma unroll
-            for (int i = 0; i < CH; ++i) {
-              const float h = __shfl_sync(0xffffffffu, half, i);
-              float& l = i & 1 ? l2[q * CH / 2 + i / 2].y : l2[q * CH / 2 + i / 2].x;
-              l = l * h * h;
-              if (j > 0) v[i] = __float_as_uint(__uint_as_float(v[i]) * (h * h));
+              for (int kk = 0; kk < KL; ++kk) {
+                const int k = k0 + kk;
+                const float2 by = factor(f2[k], ks), at = ptx::fadd2(m2[k], x);
+                float2 y[2];  // of tokens g and g + 8
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const uint32_t* const w = v + 4 * kk + 2 * e;
+                  y[e] = ptx::ffma2(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), by, at);
+                  top = ptx::fmax3(top, y[e].x, y[e].y);
+                  y[e] = make_float2(ptx::ex2(y[e].x), ptx::ex2(y[e].y));
+                  pk[2 * kk + e] = pack_half2(y[e].x, y[e].y);
+                }
+                const float2 sum = ptx::fadd2(y[0], y[1]);
+                lt[k] = z == 0 ? ptx::fmul2(sum, inv) : ptx::ffma2(sum, inv, lt[k]);
+              }
+              if constexpr (KL == 1) {
+                ptx::stmatrix(weights + C::P::unit(to_token + 16 * z, wg * (HALF / 8)), pk[0], pk[1]);
+              } else {
+#pragma unroll
+                for (int kk = 0; kk < KL; kk += 2)
+                  ptx::stmatrix(weights + C::P::unit(to_token + 16 * z, to_unit + k0 + kk), pk[2 * kk], pk[2 * kk + 1],
+                                pk[2 * kk + 2], pk[2 * kk + 3]);
+              }
             }
-            if (j > 0) {
-              store_columns<CH>(o_col + q * CH, v);
-              ptx::tmem_wait_st();
-            }
-            meet(false);  // the references are written
-            score();
           }
-          if (__any_sync(0xffffffffu, flag == kFar)) {  // sums that do not go through the weights
+        };
+        bool left = false;
+        for (bool moved = false;; moved = true) {
+          // (the first tile sets the references)
+          if (j > 0 || moved) {
+            weigh();
+            if (moved || !meet(!ok || top > kMostWeight)) break;
+          }
+          // a weight would pass 2^15 (or a wait ran out): the references of such rows move
 #pragma unroll
-            for (int i = 0; i < CH / 2; ++i) {
-              const float y = ptx::ex2(0.5f * (__uint_as_float(v[2 * i]) - x)), z = ptx::ex2(0.5f * (__uint_as_float(v[2 * i + 1]) - x));
-              if (flag == kFar) l2[q * CH / 2 + i] = ptx::ffma2(make_float2(y, z), make_float2(y, z), l2[q * CH / 2 + i]);
+          for (int k0 = 0; k0 < K; k0 += KL) {
+            uint32_t v[2][4 * KL];
+#pragma unroll
+            for (int z = 0; z < 2; ++z) ptx::tmem_ld16x256(s_col + (uint32_t(16 * z) << 16) + uint32_t(8 * k0), v[z]);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int kk = 0; kk < KL; ++kk) {
+              const int k = k0 + kk;
+              float2 most = make_float2(-INFINITY, -INFINITY);
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                const float2 by = factor(f2[k], make_float2(of[z].x, of[z].x)), x = make_float2(of[z].y, of[z].y);
+#pragma unroll
+                for (int e = 4 * kk; e < 4 * kk + 4; e += 2) {
+                  const float2 y = ptx::ffma2(make_float2(__uint_as_float(v[z][e]), __uint_as_float(v[z][e + 1])), by, x);
+                  most = make_float2(fmaxf(most.x, y.x), fmaxf(most.y, y.y));
+                }
+              }
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) {
+                most.x = fmaxf(most.x, __shfl_xor_sync(0xffffffffu, most.x, o));
+                most.y = fmaxf(most.y, __shfl_xor_sync(0xffffffffu, most.y, o));
+              }
+              if (g4 == 0) *reinterpret_cast<float2*>(warps + w4 * HALF + 8 * k + 2 * i4) = most;
             }
           }
-          uint32_t pk[CH / 2];
-#pragma unroll
-          for (int i = 0; i < CH / 2; ++i) {
-            const float2 w = make_float2(ptx::ex2(__uint_as_float(v[2 * i])), ptx::ex2(__uint_as_float(v[2 * i + 1])));
-            l2[q * CH / 2 + i] = ptx::ffma2(w, make_float2(inv, inv), l2[q * CH / 2 + i]);
-            pk[i] = pack_half2(w.x, w.y);
+          if (j > 0) ok = ok && wait_warp(bar(C::B_PDONE + (f ^ 1)), uint32_t((T - 1) >> 1) & 1u, abort_flag, err, 20);
+          if (meet(!ok)) {
+            left = true;  // all of them
+            break;
           }
+          ptx::tc_fence_after();
 #pragma unroll
-          for (int u = 0; u < CH / 8; ++u)
-            *reinterpret_cast<uint4*>(weights + C::P::unit(tid, (wg * HALF + q * CH) / 8 + u)) =
-                make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
+          for (int k = 0; k < K; ++k) {
+            float2 now = make_float2(-INFINITY, -INFINITY), h;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const float2 y = *reinterpret_cast<const float2*>(warps + w * HALF + 8 * k + 2 * i4);
+              now = make_float2(fmaxf(now.x, y.x), fmaxf(now.y, y.y));
+            }
+            h.x = move_reference(now.x, m2[k].x);
+            h.y = move_reference(now.y, m2[k].y);
+            l2[k] = ptx::fmul2(ptx::fmul2(l2[k], h), h);
+            if (j > 0) {  // O holds the earlier tiles' products, which have ended
+              h = ptx::fmul2(h, h);
+              uint32_t w[2][4];
+#pragma unroll
+              for (int z = 0; z < 2; ++z) ptx::tmem_ld16x256(o_col + (uint32_t(16 * z) << 16) + uint32_t(8 * k), w[z]);
+              ptx::tmem_wait_ld();
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[z][e] = __float_as_uint(__uint_as_float(w[z][e]) * (e & 1 ? h.y : h.x));
+                ptx::tmem_st16x256(o_col + (uint32_t(16 * z) << 16) + uint32_t(8 * k), w[z]);
+              }
+            }
+          }
+          ptx::tmem_wait_st();
         }
         if (left) break;
+        if (flags & kFar) {  // sums that do not go through the weights
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            if (__float_as_int(of[z].w) != kFar) continue;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+              uint32_t v[4];
+              ptx::tmem_ld16x256(s_col + (uint32_t(16 * z) << 16) + uint32_t(8 * k), v);
+              ptx::tmem_wait_ld();
+              const float2 by = factor(f2[k], make_float2(of[z].x, of[z].x));
+#pragma unroll
+              for (int e = 0; e < 4; e += 2) {
+                float2 y = ptx::ffma2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), by, m2[k]);
+                y = make_float2(ptx::ex2(0.5f * y.x), ptx::ex2(0.5f * y.y));
+                lt[k] = ptx::ffma2(y, y, lt[k]);
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) l2[k] = ptx::fadd2(l2[k], lt[k]);
         ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
         __syncwarp();
@@ -667,35 +719,40 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       // ---- the segment's end: sums over the tokens, O
       ok = wait_warp(bar(C::B_PDONE + ((T - 1) & 1)), uint32_t((T - 1) >> 1) & 1u, abort_flag, err, 21);
 #pragma unroll
-      for (int q = 0; q < CHUNKS; ++q) {
-        float z[CH];
+      for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int i = 0; i < CH; ++i) z[i] = i & 1 ? l2[q * CH / 2 + i / 2].y : l2[q * CH / 2 + i / 2].x;
-        const float sum = across_lanes<CH>(z, lane, [](float y, float w) { return y + w; });
-        if (lane < CH) maxima[w4 * HALF + q * CH + lane] = sum;
-      }
+        for (int e = 0; e < 2; ++e) {
+          float y = e ? l2[k].y : l2[k].x;
+          y += __shfl_xor_sync(0xffffffffu, y, 4);
+          y += __shfl_xor_sync(0xffffffffu, y, 8);
+          y += __shfl_xor_sync(0xffffffffu, y, 16);
+          const int row = 8 * k + 2 * i4 + e;
+          if (g4 == 0) warps[w4 * HALF + row] = y;
+          if (g4 == 0 && w4 == 0) out[row].x = e ? m2[k].y : m2[k].x;
+        }
       if (meet(!ok)) break;
-      const int first = wg * HALF;  // of the tile's rows
+      const int first = wg * HALF, tid = w4 * 32 + lane;  // first: of the tile's rows
       if (tid < HALF) {
-        const float sum = (maxima[tid] + maxima[HALF + tid]) + (maxima[2 * HALF + tid] + maxima[3 * HALF + tid]);
-        const float m = reinterpret_cast<const float*>(rows)[tid / 2 * 4 + 2 + (tid & 1)];
-        const int row = first + tid, rg = g.row0 + row, head = g.h * p.G + rg % p.G, token = g.q0 + rg / p.G;
+        const float sum = (warps[tid] + warps[HALF + tid]) + (warps[2 * HALF + tid] + warps[3 * HALF + tid]);
+        const float m = -out[tid].x;
+        const int row = first + tid, rg = g.row0 + row, head = g.h * p.G + rg % p.G, at = g.q0 + rg / p.G;
         const bool whole = g.slot < 0;
         if (row < g.rows) {
           if (whole)
-            a.lse[int64_t(head) * a.total_tokens + token] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+            a.lse[int64_t(head) * a.total_tokens + at] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
           else
             p.part_m[int64_t(g.slot) * N + row] = make_float2(m == kNoReference ? -INFINITY : m, sum);
         }
         out[tid] = make_float2(!whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum,
-                               __int_as_float(whole ? token * a.num_heads + head : g.slot * N + row));
+                               __int_as_float(whole ? at * a.num_heads + head : g.slot * N + row));
       }
       meet(false);
       ptx::tc_fence_after();
-#pragma unroll
+      constexpr int CH = HALF < 32 ? HALF : 32, CHUNKS = HALF / CH;
+#pragma unroll 1
       for (int q = 0; q < CHUNKS; ++q) {
-        uint32_t v[CH];
-        load_columns<CH>(o_col + q * CH, v);
+        uint32_t w[CH];
+        load_columns<CH>(o_col + q * CH, w);
         ptx::tmem_wait_ld();
         if (q == CHUNKS - 1) {
           ptx::tc_fence_before();
@@ -707,8 +764,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             if (first + q * CH + i >= g.rows) break;
             const float2 to = out[q * CH + i];
             const int64_t at = int64_t(__float_as_int(to.y)) * D + tid;
-            if (g.slot < 0) static_cast<__nv_bfloat16*>(a.o)[at] = __float2bfloat16_rn(__uint_as_float(v[i]) * to.x);
-            else p.part_o[at] = __uint_as_float(v[i]);
+            if (g.slot < 0) static_cast<__nv_bfloat16*>(a.o)[at] = __float2bfloat16_rn(__uint_as_float(w[i]) * to.x);
+            else p.part_o[at] = __uint_as_float(w[i]);
           }
         }
         __syncwarp();
