@@ -88,8 +88,8 @@ __device__ __forceinline__ int tree_share(int total, const TreeParams& p) {
   return max(p.least, (total + p.ctas - 1) / p.ctas);
 }
 
-// N 16-bit rows of 128 tokens (P^T), or D dimensions of 64 tokens (V): MN-major, rows of 128
-// bytes at most, swizzled over their width.
+// E 16-bit rows of 128 tokens (P^T): MN-major, rows of 128 bytes at most, swizzled over their
+// width.
 template <int E, int TOKENS>
 struct WideTile {
   static constexpr int CE = E < 64 ? E : 64, ROWB = CE * 2, CHUNK = TOKENS * ROWB, BYTES = E / CE * CHUNK;
@@ -105,48 +105,42 @@ struct WideTile {
 
 template <int D, int N>
 struct TreeCfg {
-  using V = WideTile<D, 64>;    // half a tile of tokens
   using P = WideTile<N, kTile>;
   static constexpr int KT = CodeTile<D>::BYTES;   // a tile of codes
   static constexpr int QT = 2 * N * D;            // queries: hi, lo
+  static constexpr bool TURNS = N <= 64;          // the warpgroups of the softmax take tiles in turn, or half the rows each
   static constexpr int NQ = N == 128 ? 1 : 2;
-  static constexpr int NK = N <= 32 ? 4 : N == 64 ? 3 : 2, NR = NK;
-  static constexpr int NV = N == 16 ? 4 : 3;      // halves
+  static constexpr int NB = N <= 32 ? 3 : 2;      // of scores and of weights
+  static constexpr int NO = N == 128 ? 1 : 2;     // segments' O
+  static constexpr int NK = N <= 32 ? 5 : N == 64 ? 4 : 3, NR = NK;
   static constexpr int NSCL = 8, NSEG = 4;
-  // (For D < 128 a product's A operand, 128 dimensions wide, reaches past the fp16 tile,
-  // whose rows past D are lanes of O^T that nobody reads: into what lies behind it.)
-  static constexpr int OFF_V = 0;
-  static constexpr int OFF_P = OFF_V + NV * V::BYTES;
-  static constexpr int OFF_Q = OFF_P + 2 * P::BYTES;
+  static constexpr int OFF_P = 0;
+  static constexpr int OFF_Q = OFF_P + NB * P::BYTES;
   static constexpr int OFF_K = OFF_Q + (NQ * QT + 1023) / 1024 * 1024;
   static constexpr int OFF_R = OFF_K + NK * KT;
   static constexpr int OFF_SCL = OFF_R + NR * KT;          // as in cache_chunk.cu
   static constexpr int OFF_ROWS = OFF_SCL + NSCL * 8 * 16; // [2][N]: the rows' factors
-  static constexpr int OFF_MAX = OFF_ROWS + 2 * N * 4;     // [2][4 warps][N / 2]: maxima, then sums
-  static constexpr int OFF_OUT = OFF_MAX + 4 * N * 4;      // [N]: 1 / sum, place in the outputs
-  static constexpr int OFF_SEG = OFF_OUT + N * 8;
+  static constexpr int OFF_MAX = OFF_ROWS + 2 * N * 4;     // [2][4 warps][rows of a warpgroup]: maxima, then sums
+  static constexpr int OFF_REF = OFF_MAX + 8 * N * 4;      // [2][N]: negative references
+  static constexpr int OFF_OUT = OFF_REF + 2 * N * 4;      // [N]: factors of the two warpgroups' O, place in the outputs
+  static constexpr int OFF_SEG = OFF_OUT + N * 16;
   static constexpr int OFF_BAR = OFF_SEG + NSEG * 48;
   static constexpr int B_SEGFULL = 0, B_SEGFREE = B_SEGFULL + NSEG, B_QFULL = B_SEGFREE + NSEG, B_QFREE = B_QFULL + 2,
                        B_KFULL = B_QFREE + NQ, B_KFREE = B_KFULL + NK, B_RFULL = B_KFREE + NK, B_RFREE = B_RFULL + NR,
-                       B_VFULL = B_RFREE + NR, B_VFREE = B_VFULL + NV, B_SCLFULL = B_VFREE + NV,
-                       B_SCLFREE = B_SCLFULL + NSCL, B_SFULL = B_SCLFREE + NSCL, B_PFULL = B_SFULL + 2,
-                       B_PDONE = B_PFULL + 2, B_OFREE = B_PDONE + 2, B_DRAIN = B_OFREE + 2, NBAR = B_DRAIN + 2;
+                       B_VFULL = B_RFREE + NR, B_VFREE = B_VFULL + 2, B_SCLFULL = B_VFREE + 2,
+                       B_SCLFREE = B_SCLFULL + NSCL, B_SFULL = B_SCLFREE + NSCL, B_PFULL = B_SFULL + NB,
+                       B_PDONE = B_PFULL + NB, B_OFREE = B_PDONE + NB, B_USED = B_OFREE + NO,
+                       B_DRAIN = B_USED + 2, NBAR = B_DRAIN + 2;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int USED = OFF_MISC + 16 + 1024;        // the base is aligned to 1024
   // one CTA per SM: it takes all of TMEM
   static constexpr int SMEM = USED > 116 * 1024 ? USED : 116 * 1024;
   static_assert(SMEM <= 232448, "shared memory budget");
-  static_assert(OFF_K - OFF_P + NK * KT >= 4 * V::CHUNK, "what the A operand reaches past V");
   // TMEM columns
-  static constexpr int S = 0, O = 2 * N;  // two buffers each
+  static constexpr int S = 0, O = NB * N, OSEG = TURNS ? 2 * N : N, V = O + NO * OSEG;
+  static_assert(V + 2 * 64 <= 512, "tensor memory");
 };
 
-template <int C>
-__device__ __forceinline__ void load_columns(uint32_t taddr, uint32_t (&r)[C]) {
-  if constexpr (C == 32) ptx::tmem_ld32(taddr, r);
-  else if constexpr (C == 16) ptx::tmem_ld16(taddr, r);
-  else ptx::tmem_ld8(taddr, r);
-}
 template <int D, int N>
 __global__ void __launch_bounds__(kTreeThreads, 1)
     cache_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -180,14 +174,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     init(C::B_KFREE, C::NK, 1);
     init(C::B_RFULL, C::NR, 1);
     init(C::B_RFREE, C::NR, 4);
-    init(C::B_VFULL, C::NV, 4);
-    init(C::B_VFREE, C::NV, 1);
+    init(C::B_VFULL, 2, 4);
+    init(C::B_VFREE, 2, 1);
     init(C::B_SCLFULL, C::NSCL, 1);
-    init(C::B_SCLFREE, C::NSCL, 12);  // softmax and value warps
-    init(C::B_SFULL, 2, 1);
-    init(C::B_PFULL, 2, 8);
-    init(C::B_PDONE, 2, 1);
-    init(C::B_OFREE, 2, 8);
+    init(C::B_SCLFREE, C::NSCL, 4 + (C::TURNS ? 4 : 8));  // value and softmax warps
+    init(C::B_SFULL, C::NB, 1);
+    init(C::B_PFULL, C::NB, C::TURNS ? 4 : 8);
+    init(C::B_PDONE, C::NB, 1);
+    init(C::B_OFREE, C::NO, 8);
+    init(C::B_USED, 2, 8);
     init(C::B_DRAIN, 2, 1);
     // (the second word decides alone whether warps start: see cache_chunk.cu)
     misc[2] = *abort_flag = (*reinterpret_cast<volatile int32_t*>(err) & kErrTimeout) ? 1u : 0u;
@@ -206,8 +201,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   // The s-th segment, copied from its place in the ring; one arrival frees that.
   auto segment = [&](int s, Segment& g, bool single) {
     const int at = s % C::NSEG;
-    const bool ok = single ? wait_lane(bar(C::B_SEGFULL + at), uint32_t(s / C::NSEG) & 1u, abort_flag, err, 1)
-                           : wait_warp(bar(C::B_SEGFULL + at), uint32_t(s / C::NSEG) & 1u, abort_flag, err, 1);
+    const bool ok = single ? wait_bar(bar(C::B_SEGFULL + at), uint32_t(s / C::NSEG) & 1u, abort_flag, err, 1)
+                           : warp_wait(bar(C::B_SEGFULL + at), uint32_t(s / C::NSEG) & 1u, abort_flag, err, 1);
     g.tiles = 0;
     if (!ok) return false;
     const int4* w = reinterpret_cast<const int4*>(sbase + C::OFF_SEG + at * 48);
@@ -218,9 +213,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     return true;
   };
 
+  // Registers: of the launch's 128 for each thread the softmax takes 168, the conversion 104,
+  // the others 72.  (Set in each branch: where they meet, the least would hold for all.)
   if (skip) {
     // nothing issued, nothing to drain
-  } else if (warp == kWarpLine) {
+  } else if (warp >= kWarpPages) {
+   ptx::regs_dec<72>();
+   if (warp == kWarpLine) {
     // -------------------------------------------------------------- segments
     const TreeUnits<N> units{p, blockIdx.x == 0};
     const UnitLine line(units, c.batch, lane);
@@ -255,7 +254,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         break;
       }
       const int at = s % C::NSEG;
-      if (s >= C::NSEG && !wait_warp(bar(C::B_SEGFREE + at), uint32_t(s / C::NSEG - 1) & 1u, abort_flag, err, 2)) break;
+      if (s >= C::NSEG && !warp_wait(bar(C::B_SEGFREE + at), uint32_t(s / C::NSEG - 1) & 1u, abort_flag, err, 2)) break;
       if (lane == 0) {
         int4* w = reinterpret_cast<int4*>(sbase + C::OFF_SEG + at * 48);
         w[0] = make_int4(g.tiles, g.b, g.h, g.row0);
@@ -302,7 +301,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const int ss = T % C::NSCL, ks = T % C::NK, rs = T % C::NR;
         const bool mine = lane >> 3 == (j & 3), here = mine && token(j & ~3) < end, fine = here && in_pool(c, id);
         if (here && !fine) atomicOr(err, kErrBadPage);
-        if (T >= C::NSCL && !wait_warp(bar(C::B_SCLFREE + ss), uint32_t(T / C::NSCL - 1) & 1u, abort_flag, err, 3)) { ok = false; break; }
+        if (T >= C::NSCL && !warp_wait(bar(C::B_SCLFREE + ss), uint32_t(T / C::NSCL - 1) & 1u, abort_flag, err, 3)) { ok = false; break; }
         const int x = exponent_of(sc.y);
         if (__any_sync(0xffffffffu, fine && x > x_top)) x_top = max(x_top, __reduce_max_sync(0xffffffffu, fine ? x : 0));
         if (mine) {
@@ -313,7 +312,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(C::B_SCLFULL + ss));
-        if (T >= C::NK && !wait_warp(bar(C::B_KFREE + ks), uint32_t(T / C::NK - 1) & 1u, abort_flag, err, 4)) { ok = false; break; }
+        if (T >= C::NK && !warp_wait(bar(C::B_KFREE + ks), uint32_t(T / C::NK - 1) & 1u, abort_flag, err, 4)) { ok = false; break; }
         const bool load = fine && lane % step == 0;  // one lane per page (eight lanes are whole pages)
         const uint32_t loads = __popc(__ballot_sync(0xffffffffu, load));
         if (lane == 0) ptx::mbar_arrive_expect_tx(bar(C::B_KFULL + ks), bytes * loads);
@@ -321,7 +320,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (load)
           ptx::tma_load_4d(base + C::OFF_K + ks * C::KT + (lane & 7) * 16 * D, &tmK, bar(C::B_KFULL + ks), 0, 0, g.h, id);
         done = T + 1;
-        if (T >= C::NR && !wait_warp(bar(C::B_RFREE + rs), uint32_t(T / C::NR - 1) & 1u, abort_flag, err, 5)) { ok = false; break; }
+        if (T >= C::NR && !warp_wait(bar(C::B_RFREE + rs), uint32_t(T / C::NR - 1) & 1u, abort_flag, err, 5)) { ok = false; break; }
         if (lane == 0) ptx::mbar_arrive_expect_tx(bar(C::B_RFULL + rs), bytes * loads);
         __syncwarp();
         if (load)
@@ -353,13 +352,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       int T = 0;
       bool ok = true;
       for (int s = 0; ok && segment(s, g, true) && g.tiles; ++s) {
-        ok = wait_lane(bar(C::B_QFULL + (s & 1)), uint32_t(s >> 1) & 1u, abort_flag, err, 6);
+        ok = wait_bar(bar(C::B_QFULL + (s & 1)), uint32_t(s >> 1) & 1u, abort_flag, err, 6);
         const uint64_t qhi = qd + uint64_t((s % C::NQ) * C::QT >> 4), qlo = qhi + uint64_t(N * D >> 4);
         for (int j = 0; ok && j < g.tiles; ++j, ++T) {
-          const int ks = T % C::NK, f = T & 1;
-          ok = wait_lane(bar(C::B_KFULL + ks), uint32_t(T / C::NK) & 1u, abort_flag, err, 7) &&
+          const int ks = T % C::NK, f = T % C::NB;
+          ok = wait_bar(bar(C::B_KFULL + ks), uint32_t(T / C::NK) & 1u, abort_flag, err, 7) &&
                // the softmax has read the scores that lie there
-               (T < 2 || wait_lane(bar(C::B_PFULL + f), uint32_t((T >> 1) - 1) & 1u, abort_flag, err, 8));
+               (T < C::NB || wait_bar(bar(C::B_PFULL + f), uint32_t(T / C::NB - 1) & 1u, abort_flag, err, 8));
           if (!ok) break;
           ptx::tc_fence_after();
           const uint64_t ki = kd + uint64_t(ks * C::KT >> 4);
@@ -378,51 +377,48 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       drain_bar(bar(C::B_DRAIN), 0, err);
     }
     __syncwarp();
-  } else if (warp == kWarpO) {
+  } else {
     // -------------------------------------------------------------- O^T issuer
     if (lane == 0) {
-      constexpr uint32_t IDESC = ptx::idesc_f16_f32(128, N, true, true);
-      const uint64_t vd = C::V::desc(base + C::OFF_V), pd = C::P::desc(base + C::OFF_P);
+      constexpr uint32_t IDESC = ptx::idesc_f16_f32(128, N, false, true);
+      const uint64_t pd = C::P::desc(base + C::OFF_P);
       Segment g;
       int T = 0;
       bool ok = true;
       for (int s = 0; ok && segment(s, g, true) && g.tiles; ++s) {
-        if (s >= 2) ok = wait_lane(bar(C::B_OFREE + (s & 1)), uint32_t((s >> 1) - 1) & 1u, abort_flag, err, 9);
-        const uint32_t o_tmem = tmem + uint32_t(C::O + (s & 1) * N);
+        if (s >= C::NO) ok = wait_bar(bar(C::B_OFREE + s % C::NO), uint32_t(s / C::NO - 1) & 1u, abort_flag, err, 9);
+        const uint32_t o_seg = tmem + uint32_t(C::O + s % C::NO * C::OSEG);
         for (int j = 0; ok && j < g.tiles; ++j, ++T) {
-          const int f = T & 1;
-          ok = wait_lane(bar(C::B_PFULL + f), uint32_t(T >> 1) & 1u, abort_flag, err, 10);
+          const int f = T % C::NB, vs = T & 1;
+          ok = wait_bar(bar(C::B_VFULL + vs), uint32_t(T >> 1) & 1u, abort_flag, err, 11) &&
+               wait_bar(bar(C::B_PFULL + f), uint32_t(T / C::NB) & 1u, abort_flag, err, 10);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          const uint32_t o_tmem = o_seg + (C::TURNS ? uint32_t(T & 1) * N : 0u), v_tmem = tmem + uint32_t(C::V + vs * 64);
           const uint64_t pi = pd + uint64_t(f * C::P::BYTES >> 4);
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int x = 2 * T + half, vs = x % C::NV;
-            ok = ok && wait_lane(bar(C::B_VFULL + vs), uint32_t(x / C::NV) & 1u, abort_flag, err, 11);
-            if (!ok) break;
-            ptx::tc_fence_after();
-            const uint64_t vi = vd + uint64_t(vs * C::V::BYTES >> 4);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              ptx::mma_ss(o_tmem, vi + C::V::step(kk), pi + C::P::step(4 * half + kk), IDESC, (j > 0 || half > 0 || kk > 0) ? 1u : 0u);
-            ptx::mma_commit(bar(C::B_VFREE + vs));
-          }
-          if (ok) ptx::mma_commit(bar(C::B_PDONE + f));
+          for (int kk = 0; kk < 8; ++kk)
+            ptx::mma_ts(o_tmem, v_tmem + uint32_t(kk) * 8u, pi + C::P::step(kk), IDESC, (j > (C::TURNS ? 1 : 0) || kk > 0) ? 1u : 0u);
+          ptx::mma_commit(bar(C::B_PDONE + f));
+          ptx::mma_commit(bar(C::B_VFREE + vs));
         }
       }
       ptx::mma_commit(bar(C::B_DRAIN + 1));
       drain_bar(bar(C::B_DRAIN + 1), 0, err);
     }
     __syncwarp();
+   }
   } else if (warp >= kWarpConvert) {
+    ptx::regs_dec<104>();
     // -------------------------------------------------------------- queries, values
-    constexpr int PPT = D / 16;        // 16-byte pieces of codes per token = pieces per thread of a tile
-    const int ct = threadIdx.x - kWarpConvert * 32;
+    const int ct = threadIdx.x - kWarpConvert * 32, cw = warp - kWarpConvert;
     Segment g;
     int T = 0;
     bool ok = true;
     for (int s = 0; ok && segment(s, g, false) && g.tiles; ++s) {
       // the queries two segments back are used, and so are their factors
-      if (s >= C::NQ) ok = wait_warp(bar(C::B_QFREE + s % C::NQ), uint32_t(s / C::NQ - 1) & 1u, abort_flag, err, 12);
-      if (ok && s >= 2) ok = wait_warp(bar(C::B_OFREE + (s & 1)), uint32_t((s >> 1) - 1) & 1u, abort_flag, err, 13);
+      if (s >= C::NQ) ok = warp_wait(bar(C::B_QFREE + s % C::NQ), uint32_t(s / C::NQ - 1) & 1u, abort_flag, err, 12);
+      if (ok && s >= 2) ok = warp_wait(bar(C::B_USED + (s & 1)), uint32_t((s >> 1) - 1) & 1u, abort_flag, err, 13);
       if (!ok) break;
       {
         constexpr int PARTS = 128 / N < D / 16 ? 128 / N : D / 16;  // threads of a row
@@ -432,7 +428,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           const int rg = g.row0 + (real ? row : 0);
           const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) +
                                    (int64_t(g.q0 + rg / p.G) * a.num_heads + g.h * p.G + rg % p.G) * D;
-          const float f = p.scale_log2 * split_query<D, PARTS>(q, real, sbase + C::OFF_Q + (s % C::NQ) * C::QT, row, N * D, ct % PARTS);
+          const float f = p.scale_log2 * split_query<D, PARTS, true>(q, real, sbase + C::OFF_Q + (s % C::NQ) * C::QT, row, N * D, ct % PARTS);
           if (ct % PARTS == 0) reinterpret_cast<float*>(sbase + C::OFF_ROWS)[(s & 1) * N + row] = f;
         }
       }
@@ -442,58 +438,70 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       for (int j = 0; j < g.tiles; ++j, ++T) {
         const int rs = T % C::NR, ss = T % C::NSCL;
         // (the scales' slot was written before this arrived)
-        if (!wait_warp(bar(C::B_RFULL + rs), uint32_t(T / C::NR) & 1u, abort_flag, err, 14)) { ok = false; break; }
-        uint4 next[PPT];
-#pragma unroll
-        for (int i = 0; i < PPT; ++i)
-          next[i] = *reinterpret_cast<const uint4*>(sbase + C::OFF_R + rs * C::KT + (i * 128 + ct) * 16);
+        if (!warp_wait(bar(C::B_RFULL + rs), uint32_t(T / C::NR) & 1u, abort_flag, err, 14)) { ok = false; break; }
         const bool gone = __float_as_int(scl[ss * 8 + (lane & 7)].w) < 0;
-        if (__any_sync(0xffffffffu, gone) || g.token + (j + 1) * kTile > end) {
-          // behind the end, or without a page: weights of 0 times 0
+        const bool ragged = __any_sync(0xffffffffu, gone) || g.token + (j + 1) * kTile > end;
+        if (T >= 2 && !warp_wait(bar(C::B_VFREE + (T & 1)), uint32_t((T >> 1) - 1) & 1u, abort_flag, err, 15)) { ok = false; break; }
 #pragma unroll
-          for (int i = 0; i < PPT; ++i) {
-            const int row = (i * 128 + ct) / PPT;
-            if (g.token + j * kTile + row >= end || __float_as_int(scl[ss * 8 + row / 16].w) < 0)
-              next[i] = make_uint4(0, 0, 0, 0);
+        for (int z = 0; z < 2; ++z) {
+          const int u = 2 * cw + z;  // 16 dimensions
+          if (u >= D / 16) break;
+          uint32_t w[16];  // tokens 16 b + 4 i .. + 3 of dimensions g and g + 8, i and g of the lane
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            ptx::ldmatrix_bytes(base + C::OFF_R + rs * C::KT + CodeTile<D>::unit(32 * x + lane, u), w[4 * x], w[4 * x + 1],
+                                w[4 * x + 2], w[4 * x + 3]);
+          if (ragged) {
+            // behind the end, or without a page: weights of 0 times 0
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              const int first = g.token + j * kTile + 16 * x + 4 * (lane & 3);
+              const int n = __float_as_int(scl[ss * 8 + x].w) < 0 ? 0 : min(max(end - first, 0), 4);
+              const uint32_t keep = n == 4 ? ~0u : (1u << (8 * n)) - 1u;
+              w[2 * x] &= keep;
+              w[2 * x + 1] &= keep;
+            }
+          }
+          const uint32_t to = tmem + (uint32_t(16 * u) << 16) + uint32_t(C::V + (T & 1) * 64);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            uint32_t v[16];
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+              v[2 * y] = half2_of(w[8 * x + y]);
+              v[2 * y + 1] = half2_of_high(w[8 * x + y]);
+            }
+            ptx::tmem_st16x256(to + uint32_t(32 * x), v);
           }
         }
-        warp_arrive(bar(C::B_RFREE + rs), lane);
-        if (lane == 0) ptx::mbar_arrive(bar(C::B_SCLFREE + ss));
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int x = 2 * T + half, vs = x % C::NV;
-          if (x >= C::NV && !wait_warp(bar(C::B_VFREE + vs), uint32_t(x / C::NV - 1) & 1u, abort_flag, err, 15)) { ok = false; break; }
-          uint8_t* tile = sbase + C::OFF_V + vs * C::V::BYTES;
-#pragma unroll
-          for (int i = half * PPT / 2; i < (half + 1) * PPT / 2; ++i) {
-            const int y = i * 128 + ct, row = y / PPT - 64 * half, piece = y % PPT;
-            const uint4 w = next[i];
-            const uint4 lo = make_uint4(half2_of(w.x), half2_of_high(w.x), half2_of(w.y), half2_of_high(w.y));
-            const uint4 hi = make_uint4(half2_of(w.z), half2_of_high(w.z), half2_of(w.w), half2_of_high(w.w));
-            // pieces of the second row chunk store their halves the other way
-            // round: eight lanes of a token then meet eight different bank groups
-            const bool flip = piece * 16 >= C::V::CE;
-            *reinterpret_cast<uint4*>(tile + C::V::unit(row, 2 * piece + (flip ? 1 : 0))) = flip ? hi : lo;
-            *reinterpret_cast<uint4*>(tile + C::V::unit(row, 2 * piece + (flip ? 0 : 1))) = flip ? lo : hi;
-          }
-          ptx::fence_proxy_async_smem();
-          warp_arrive(bar(C::B_VFULL + vs), lane);
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        warp_arrive(bar(C::B_VFULL + (T & 1)), lane);
+        if (lane == 0) {
+          ptx::mbar_arrive(bar(C::B_RFREE + rs));
+          ptx::mbar_arrive(bar(C::B_SCLFREE + ss));
         }
-        if (!ok) break;
       }
     }
   } else {
+    ptx::regs_inc<168>();
     // -------------------------------------------------------------- softmax
-    // A warp takes 32 tokens, in two blocks of 16 (of one page each), and half of the rows;
-    // of a block, lane 4 g + i holds tokens g and g + 8 and rows 8 k + 2 i, + 1.
-    // The weights are formed and stored before the vote on the references, piece by piece, so
-    // that few scores are in registers at once; a tile whose references move repeats them.
-    constexpr int HALF = N / 2, K = HALF / 8, KL = K < 4 ? K : 4;
+    // A warp takes 32 tokens, in two blocks of 16 (of one page each); of a block, lane
+    // 4 g + i holds tokens g and g + 8 and rows 8 k + 2 i, + 1.  Up to 64 rows the warpgroups
+    // take tiles in turn, each with references, sums and O of its own, which meet at a
+    // segment's end: what a tile costs besides its scores (waits, the vote) is then paid
+    // by each for every other one.  Of 128 rows each takes half.
+    // The weights are formed and stored before the vote on the references; a tile whose
+    // references move repeats them.
+    constexpr int ROWS = C::TURNS ? N : N / 2, K = ROWS / 8, KL = K < 4 ? K : 4, STRIDE = C::TURNS ? 2 : 1;
     const int wg = warp >> 2, w4 = warp & 3, g4 = lane >> 2, i4 = lane & 3;
-    const uint32_t lanes = tmem + (uint32_t(w4 * 32) << 16) + uint32_t(wg * HALF);
-    float* const warps = reinterpret_cast<float*>(sbase + C::OFF_MAX) + wg * 4 * HALF;  // [warp][row]: maxima, then sums
-    float2* const out = reinterpret_cast<float2*>(sbase + C::OFF_OUT) + wg * HALF;
+    const int row_base = C::TURNS ? 0 : wg * ROWS;
+    const uint32_t lanes = tmem + (uint32_t(w4 * 32) << 16);
+    float* const warps = reinterpret_cast<float*>(sbase + C::OFF_MAX) + wg * 4 * ROWS;  // [warp][row]: maxima, then sums
+    float* const refs = reinterpret_cast<float*>(sbase + C::OFF_REF);                   // [warpgroup][row]
+    float4* const out = reinterpret_cast<float4*>(sbase + C::OFF_OUT);
     auto meet = [&](bool x) { return wg == 0 ? ptx::named_barrier_or(1, 128, x) : ptx::named_barrier_or(2, 128, x); };
+    auto meet_all = [&](bool x) { return C::TURNS ? ptx::named_barrier_or(3, 256, x) : meet(x); };
     // Scores of this warp's tokens to -inf where the row does not see the token, for which
     // `see` of the token's lane has no bit.  In tensor memory, and rolled up: few tiles have any, and
     // the loop over the others is the faster for being short.
@@ -524,18 +532,27 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       minus = kTopWeight - most;
       return half_factor(was, -minus);
     };
+    // The scales of this warp's two blocks of tile T, which has no further use for its slot.
+    float4 of[2];
+    auto scales = [&](int T) {
+      const int ss = T % C::NSCL;
+      if (!warp_wait(bar(C::B_SCLFULL + ss), uint32_t(T / C::NSCL) & 1u, abort_flag, err, 17)) return false;
+      of[0] = scl[ss * 8 + w4 * 2];
+      of[1] = scl[ss * 8 + w4 * 2 + 1];
+      warp_arrive(bar(C::B_SCLFREE + ss), lane);
+      return true;
+    };
     // where this lane's row of a matrix of weights goes: a token, and the first or second
     // eight rows of the query of sixteen
-    const int to_token = w4 * 32 + (lane & 15), to_unit = wg * (HALF / 8) + (lane >> 4);
+    const int to_token = w4 * 32 + (lane & 15), to_unit = row_base / 8 + (lane >> 4);
     Segment g;
-    int T = 0;
-    for (int s = 0;; ++s) {
+    for (int s = 0, T0 = 0;; ++s, T0 += g.tiles) {
       bool ok = segment(s, g, false);
-      if (ok && g.tiles) ok = wait_warp(bar(C::B_QFULL + (s & 1)), uint32_t(s >> 1) & 1u, abort_flag, err, 16);
-      if (meet(!ok) || g.tiles == 0) break;
+      if (ok && g.tiles) ok = warp_wait(bar(C::B_QFULL + (s & 1)), uint32_t(s >> 1) & 1u, abort_flag, err, 16);
+      if (meet_all(!ok) || g.tiles == 0) break;
       const int text = g.len - g.n;
-      const uint32_t o_col = lanes + uint32_t(C::O + (s & 1) * N);
-      const float* factors = reinterpret_cast<const float*>(sbase + C::OFF_ROWS) + (s & 1) * N + wg * HALF;
+      const uint32_t o_seg = lanes + uint32_t(C::O + s % C::NO * C::OSEG), o_col = o_seg + uint32_t(C::TURNS ? wg * N : row_base);
+      const float* factors = reinterpret_cast<const float*>(sbase + C::OFF_ROWS) + (s & 1) * N + row_base;
       float2 f2[K], m2[K], l2[K];  // of the rows: factor, negative reference, sum
 #pragma unroll
       for (int k = 0; k < K; ++k) {
@@ -544,12 +561,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         l2[k] = make_float2(0.f, 0.f);
       }
 
-      int j = 0;
-      for (; j < g.tiles; ++j, ++T) {
-        const int ss = T % C::NSCL, f = T & 1;
+      const int mine = C::TURNS ? (T0 ^ wg) & 1 : 0;  // the first tile of this warpgroup's
+      if (mine < g.tiles) ok = scales(T0 + mine);
+      bool left = false;
+      for (int j = mine; j < g.tiles; j += STRIDE) {
+        const int T = T0 + j, f = T % C::NB;
+        const uint32_t s_col = lanes + uint32_t(C::S + f * N + row_base), weights = base + C::OFF_P + f * C::P::BYTES;
         const int token = g.token + j * kTile + w4 * 32 + lane;
-        ok = wait_warp(bar(C::B_SCLFULL + ss), uint32_t(T / C::NSCL) & 1u, abort_flag, err, 17);
-        const float4 of[2] = {scl[ss * 8 + w4 * 2], scl[ss * 8 + w4 * 2 + 1]};  // of the two blocks
         const int flags = __float_as_int(of[0].w) | __float_as_int(of[1].w);
         // which rows see this lane's token
         const bool masked = __any_sync(0xffffffffu, token >= text) || flags < 0;
@@ -558,118 +576,119 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           const bool here = token < g.len && __float_as_int(lane < 16 ? of[0].w : of[1].w) >= 0;
           see = here && token < text ? ~0ull : 0ull;
           if (here && token >= text) {
-            const int node = token - text, first = g.row0 + wg * HALF, last = min(first + HALF, g.row0 + g.rows);
+            const int node = token - text, first = g.row0 + row_base, last = min(first + ROWS, g.row0 + g.rows);
 #pragma unroll 4
             for (int i = first / p.G; i < (last + p.G - 1) / p.G; ++i) {
               const uint32_t bit = __ldg(p.bits + int64_t(g.q0 + i) * p.words + (node >> 5)) >> (node & 31) & 1u;
-              const int from = max(i * p.G - first, 0), to = min((i + 1) * p.G, last) - first;  // rows of the half
+              const int from = max(i * p.G - first, 0), to = min((i + 1) * p.G, last) - first;  // of this warpgroup's
               const uint64_t span = (to >= 64 ? ~0ull : (1ull << to) - 1) & ~((1ull << from) - 1);
               see |= bit ? span : 0ull;
             }
           }
         }
-        ok = ok && wait_warp(bar(C::B_SFULL + f), uint32_t(T >> 1) & 1u, abort_flag, err, 18) &&
-             (T < 2 || wait_warp(bar(C::B_PDONE + f), uint32_t((T >> 1) - 1) & 1u, abort_flag, err, 19));
+        // the scores, and room for the weights
+        ok = ok && warp_wait(bar(C::B_SFULL + f), uint32_t(T / C::NB) & 1u, abort_flag, err, 18) &&
+             (T < C::NB || warp_wait(bar(C::B_PDONE + f), uint32_t(T / C::NB - 1) & 1u, abort_flag, err, 19));
         ptx::tc_fence_after();
-        const uint32_t s_col = lanes + uint32_t(C::S + f * N);
-        const uint32_t weights = base + C::OFF_P + f * C::P::BYTES;
         if (masked) hide(s_col, see);
-        float2 lt[K];  // the tile's sums
+        float2 lt[K];  // the tile's sums (before them, factors of the earlier ones)
         float top;
         // The weights under the present references, into shared memory, and the largest of
         // their base-2 logarithms.
         auto weigh = [&]() {
+          constexpr int PIECES = 2 * K / KL;  // (the next one is on its way while one is worked on)
+          uint32_t v[2][4 * KL];
+          auto load = [&](int i) {
+            ptx::tmem_ld16x256(s_col + (uint32_t(16 * (i / (K / KL))) << 16) + uint32_t(8 * KL * (i % (K / KL))), v[i & 1]);
+          };
+          load(0);
           top = -INFINITY;
 #pragma unroll
-          for (int z = 0; z < 2; ++z) {
+          for (int i = 0; i < PIECES; ++i) {
+            const int z = i / (K / KL), k0 = i % (K / KL) * KL;
+            ptx::tmem_wait_ld();
+            if (i + 1 < PIECES) load(i + 1);
             const float2 ks = make_float2(of[z].x, of[z].x), x = make_float2(of[z].y, of[z].y);
             const float2 inv = make_float2(of[z].z, of[z].z);
+            uint32_t pk[2 * KL];
 #pragma unroll
-            for (int k0 = 0; k0 < K; k0 += KL) {
-              uint32_t v[4 * KL], pk[2 * KL];
-              ptx::tmem_ld16x256(s_col + (uint32_t(16 * z) << 16) + uint32_t(8 * k0), v);
-              ptx::tmem_wait_ld();
+            for (int kk = 0; kk < KL; ++kk) {
+              const int k = k0 + kk;
+              const float2 by = factor(f2[k], ks), at = ptx::fadd2(m2[k], x);
+              float2 y[2];  // of tokens g and g + 8
 #pragma unroll
-              for (int kk = 0; kk < KL; ++kk) {
-                const int k = k0 + kk;
-                const float2 by = factor(f2[k], ks), at = ptx::fadd2(m2[k], x);
-                float2 y[2];  // of tokens g and g + 8
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const uint32_t* const w = v + 4 * kk + 2 * e;
-                  y[e] = ptx::ffma2(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), by, at);
-                  top = ptx::fmax3(top, y[e].x, y[e].y);
-                  y[e] = make_float2(ptx::ex2(y[e].x), ptx::ex2(y[e].y));
-                  pk[2 * kk + e] = pack_half2(y[e].x, y[e].y);
-                }
-                const float2 sum = ptx::fadd2(y[0], y[1]);
-                lt[k] = z == 0 ? ptx::fmul2(sum, inv) : ptx::ffma2(sum, inv, lt[k]);
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t* const w = v[i & 1] + 4 * kk + 2 * e;
+                y[e] = ptx::ffma2(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), by, at);
+                top = ptx::fmax3(top, y[e].x, y[e].y);
+                y[e] = make_float2(ptx::ex2(y[e].x), ptx::ex2(y[e].y));
+                pk[2 * kk + e] = pack_half2(y[e].x, y[e].y);
               }
-              if constexpr (KL == 1) {
-                ptx::stmatrix(weights + C::P::unit(to_token + 16 * z, wg * (HALF / 8)), pk[0], pk[1]);
-              } else {
-#pragma unroll
-                for (int kk = 0; kk < KL; kk += 2)
-                  ptx::stmatrix(weights + C::P::unit(to_token + 16 * z, to_unit + k0 + kk), pk[2 * kk], pk[2 * kk + 1],
-                                pk[2 * kk + 2], pk[2 * kk + 3]);
-              }
+              const float2 sum = ptx::fadd2(y[0], y[1]);
+              lt[k] = z == 0 ? ptx::fmul2(sum, inv) : ptx::ffma2(sum, inv, lt[k]);
             }
+#pragma unroll
+            for (int kk = 0; kk < KL; kk += 2)
+              ptx::stmatrix(weights + C::P::unit(to_token + 16 * z, to_unit + k0 + kk), pk[2 * kk], pk[2 * kk + 1],
+                            pk[2 * kk + 2], pk[2 * kk + 3]);
           }
         };
-        bool left = false;
         for (bool moved = false;; moved = true) {
           // (the first tile sets the references)
-          if (j > 0 || moved) {
+          if (j >= STRIDE || moved) {
             weigh();
             if (moved || !meet(!ok || top > kMostWeight)) break;
           }
           // a weight would pass 2^15 (or a wait ran out): the references of such rows move
+#pragma unroll 1
+          for (int k = 0; k < K; ++k) {
+            uint32_t v[2][4];
 #pragma unroll
-          for (int k0 = 0; k0 < K; k0 += KL) {
-            uint32_t v[2][4 * KL];
-#pragma unroll
-            for (int z = 0; z < 2; ++z) ptx::tmem_ld16x256(s_col + (uint32_t(16 * z) << 16) + uint32_t(8 * k0), v[z]);
+            for (int z = 0; z < 2; ++z) ptx::tmem_ld16x256(s_col + (uint32_t(16 * z) << 16) + uint32_t(8 * k), v[z]);
             ptx::tmem_wait_ld();
+            const float2 row = *reinterpret_cast<const float2*>(factors + 8 * k + 2 * i4);
+            float2 most = make_float2(-INFINITY, -INFINITY);
 #pragma unroll
-            for (int kk = 0; kk < KL; ++kk) {
-              const int k = k0 + kk;
-              float2 most = make_float2(-INFINITY, -INFINITY);
+            for (int z = 0; z < 2; ++z) {
+              const float2 by = factor(row, make_float2(of[z].x, of[z].x)), x = make_float2(of[z].y, of[z].y);
 #pragma unroll
-              for (int z = 0; z < 2; ++z) {
-                const float2 by = factor(f2[k], make_float2(of[z].x, of[z].x)), x = make_float2(of[z].y, of[z].y);
-#pragma unroll
-                for (int e = 4 * kk; e < 4 * kk + 4; e += 2) {
-                  const float2 y = ptx::ffma2(make_float2(__uint_as_float(v[z][e]), __uint_as_float(v[z][e + 1])), by, x);
-                  most = make_float2(fmaxf(most.x, y.x), fmaxf(most.y, y.y));
-                }
+              for (int e = 0; e < 4; e += 2) {
+                const float2 y = ptx::ffma2(make_float2(__uint_as_float(v[z][e]), __uint_as_float(v[z][e + 1])), by, x);
+                most = make_float2(fmaxf(most.x, y.x), fmaxf(most.y, y.y));
               }
-#pragma unroll
-              for (int o = 4; o < 32; o <<= 1) {
-                most.x = fmaxf(most.x, __shfl_xor_sync(0xffffffffu, most.x, o));
-                most.y = fmaxf(most.y, __shfl_xor_sync(0xffffffffu, most.y, o));
-              }
-              if (g4 == 0) *reinterpret_cast<float2*>(warps + w4 * HALF + 8 * k + 2 * i4) = most;
             }
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+              most.x = fmaxf(most.x, __shfl_xor_sync(0xffffffffu, most.x, o));
+              most.y = fmaxf(most.y, __shfl_xor_sync(0xffffffffu, most.y, o));
+            }
+            if (g4 == 0) *reinterpret_cast<float2*>(warps + w4 * ROWS + 8 * k + 2 * i4) = most;
           }
-          if (j > 0) ok = ok && wait_warp(bar(C::B_PDONE + (f ^ 1)), uint32_t((T - 1) >> 1) & 1u, abort_flag, err, 20);
+          const int before = T - STRIDE;  // this warpgroup's last tile
+          if (j >= STRIDE)
+            ok = ok && warp_wait(bar(C::B_PDONE + before % C::NB), uint32_t(before / C::NB) & 1u, abort_flag, err, 20);
           if (meet(!ok)) {
             left = true;  // all of them
             break;
           }
           ptx::tc_fence_after();
+          // (every warp for itself, with the same result)
 #pragma unroll
           for (int k = 0; k < K; ++k) {
             float2 now = make_float2(-INFINITY, -INFINITY), h;
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-              const float2 y = *reinterpret_cast<const float2*>(warps + w * HALF + 8 * k + 2 * i4);
+              const float2 y = *reinterpret_cast<const float2*>(warps + w * ROWS + 8 * k + 2 * i4);
               now = make_float2(fmaxf(now.x, y.x), fmaxf(now.y, y.y));
             }
             h.x = move_reference(now.x, m2[k].x);
             h.y = move_reference(now.y, m2[k].y);
             l2[k] = ptx::fmul2(ptx::fmul2(l2[k], h), h);
-            if (j > 0) {  // O holds the earlier tiles' products, which have ended
-              h = ptx::fmul2(h, h);
+            lt[k] = ptx::fmul2(h, h);
+          }
+          if (j >= STRIDE) {  // O holds the earlier tiles' products, which have ended
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
               uint32_t w[2][4];
 #pragma unroll
               for (int z = 0; z < 2; ++z) ptx::tmem_ld16x256(o_col + (uint32_t(16 * z) << 16) + uint32_t(8 * k), w[z]);
@@ -677,7 +696,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
               for (int z = 0; z < 2; ++z) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) w[z][e] = __float_as_uint(__uint_as_float(w[z][e]) * (e & 1 ? h.y : h.x));
+                for (int e = 0; e < 4; ++e) w[z][e] = __float_as_uint(__uint_as_float(w[z][e]) * (e & 1 ? lt[k].y : lt[k].x));
                 ptx::tmem_st16x256(o_col + (uint32_t(16 * z) << 16) + uint32_t(8 * k), w[z]);
               }
             }
@@ -704,68 +723,91 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             }
           }
         }
-#pragma unroll
-        for (int k = 0; k < K; ++k) l2[k] = ptx::fadd2(l2[k], lt[k]);
         ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          ptx::mbar_arrive(bar(C::B_PFULL + f));
-          ptx::mbar_arrive(bar(C::B_SCLFREE + ss));
-        }
+        warp_arrive(bar(C::B_PFULL + f), lane);
+#pragma unroll
+        for (int k = 0; k < K; ++k) l2[k] = ptx::fadd2(l2[k], lt[k]);
+        if (j + STRIDE < g.tiles) ok = scales(T + STRIDE);
       }
-      if (j < g.tiles) break;
-
       // ---- the segment's end: sums over the tokens, O
-      ok = wait_warp(bar(C::B_PDONE + ((T - 1) & 1)), uint32_t((T - 1) >> 1) & 1u, abort_flag, err, 21);
+      if (!C::TURNS && left) break;
+      const int end = T0 + g.tiles - 1, last = C::TURNS ? end - ((end ^ wg) & 1) : end;  // this warpgroup's last tile
+      if (last >= T0) ok = ok && !left && warp_wait(bar(C::B_PDONE + last % C::NB), uint32_t(last / C::NB) & 1u, abort_flag, err, 21);
 #pragma unroll
-      for (int k = 0; k < K; ++k)
+      for (int k = 0; k < K; ++k) {
+        float2 y = l2[k];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float y = e ? l2[k].y : l2[k].x;
-          y += __shfl_xor_sync(0xffffffffu, y, 4);
-          y += __shfl_xor_sync(0xffffffffu, y, 8);
-          y += __shfl_xor_sync(0xffffffffu, y, 16);
-          const int row = 8 * k + 2 * i4 + e;
-          if (g4 == 0) warps[w4 * HALF + row] = y;
-          if (g4 == 0 && w4 == 0) out[row].x = e ? m2[k].y : m2[k].x;
+        for (int o = 4; o < 32; o <<= 1) {
+          y.x += __shfl_xor_sync(0xffffffffu, y.x, o);
+          y.y += __shfl_xor_sync(0xffffffffu, y.y, o);
         }
-      if (meet(!ok)) break;
-      const int first = wg * HALF, tid = w4 * 32 + lane;  // first: of the tile's rows
-      if (tid < HALF) {
-        const float sum = (warps[tid] + warps[HALF + tid]) + (warps[2 * HALF + tid] + warps[3 * HALF + tid]);
-        const float m = -out[tid].x;
-        const int row = first + tid, rg = g.row0 + row, head = g.h * p.G + rg % p.G, at = g.q0 + rg / p.G;
-        const bool whole = g.slot < 0;
+        if (g4 == 0) *reinterpret_cast<float2*>(warps + w4 * ROWS + 8 * k + 2 * i4) = y;
+        if (g4 == 0 && w4 == 0) *reinterpret_cast<float2*>(refs + wg * ROWS + 8 * k + 2 * i4) = m2[k];
+      }
+      if (meet_all(!ok)) break;
+      const bool whole = g.slot < 0;
+      const int tid = w4 * 32 + lane, row = (C::TURNS ? wg * N / 2 : row_base) + tid;  // of the tile, for the first N / 2 threads
+      if (tid < N / 2) {
+        float m = -INFINITY, sum = 0.f, part[2] = {0.f, 0.f};
+        const float* const all = reinterpret_cast<const float*>(sbase + C::OFF_MAX);
+        if constexpr (C::TURNS) {
+          float its[2], half[2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const bool some = g.tiles > 1 || ((T0 ^ x) & 1) == 0;  // (else there is nothing in O)
+            const float* const w = all + x * 4 * N + row;
+            its[x] = (w[0] + w[N]) + (w[2 * N] + w[3 * N]);
+            half[x] = some ? -refs[x * N + row] : -INFINITY;
+            m = fmaxf(m, half[x]);
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            half[x] = half_factor(half[x], m);
+            sum += half[x] > 0.f ? its[x] * half[x] * half[x] : 0.f;
+            part[x] = half[x] * half[x];
+          }
+        } else {
+          const float* const w = all + wg * 4 * ROWS + tid;
+          sum = (w[0] + w[ROWS]) + (w[2 * ROWS] + w[3 * ROWS]);
+          m = -refs[wg * ROWS + tid];
+          part[0] = 1.f;
+        }
+        const int rg = g.row0 + row, head = g.h * p.G + rg % p.G, at = g.q0 + rg / p.G;
         if (row < g.rows) {
           if (whole)
             a.lse[int64_t(head) * a.total_tokens + at] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
           else
             p.part_m[int64_t(g.slot) * N + row] = make_float2(m == kNoReference ? -INFINITY : m, sum);
         }
-        out[tid] = make_float2(!whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum,
-                               __int_as_float(whole ? at * a.num_heads + head : g.slot * N + row));
+        const float inv = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+        out[row] = make_float4(part[0] * inv, part[1] * inv, __int_as_float(whole ? at * a.num_heads + head : g.slot * N + row), 0.f);
       }
-      meet(false);
+      meet(false);  // (a warpgroup reads the rows that it wrote)
+      if (lane == 0) ptx::mbar_arrive(bar(C::B_USED + (s & 1)));
       ptx::tc_fence_after();
-      constexpr int CH = HALF < 32 ? HALF : 32, CHUNKS = HALF / CH;
+      const int first = row - tid;
 #pragma unroll 1
-      for (int q = 0; q < CHUNKS; ++q) {
-        uint32_t w[CH];
-        load_columns<CH>(o_col + q * CH, w);
+      for (int q = first; q < first + N / 2; q += 8) {
+        uint32_t w[2][8];
+        ptx::tmem_ld8(o_seg + q, w[0]);
+        if (C::TURNS) ptx::tmem_ld8(o_seg + N + q, w[1]);
         ptx::tmem_wait_ld();
-        if (q == CHUNKS - 1) {
+        if (q + 8 == first + N / 2) {
           ptx::tc_fence_before();
-          warp_arrive(bar(C::B_OFREE + (s & 1)), lane);
+          warp_arrive(bar(C::B_OFREE + s % C::NO), lane);
         }
         if (w4 * 32 < D) {
 #pragma unroll
-          for (int i = 0; i < CH; ++i) {
-            if (first + q * CH + i >= g.rows) break;
-            const float2 to = out[q * CH + i];
-            const int64_t at = int64_t(__float_as_int(to.y)) * D + tid;
-            if (g.slot < 0) static_cast<__nv_bfloat16*>(a.o)[at] = __float2bfloat16_rn(__uint_as_float(w[i]) * to.x);
-            else p.part_o[at] = __uint_as_float(w[i]);
+          for (int i = 0; i < 8; ++i) {
+            if (q + i >= g.rows) break;
+            const float4 to = out[q + i];
+            // (times 0 is not taken: there may be nothing)
+            float y = to.x != 0.f ? __uint_as_float(w[0][i]) * to.x : 0.f;
+            if (C::TURNS && to.y != 0.f) y = fmaf(__uint_as_float(w[1][i]), to.y, y);
+            const int64_t at = int64_t(__float_as_int(to.z)) * D + tid;
+            if (whole) static_cast<__nv_bfloat16*>(a.o)[at] = __float2bfloat16_rn(y);
+            else p.part_o[at] = y;
           }
         }
         __syncwarp();
@@ -831,7 +873,7 @@ attn_status launch_dn(TreeParams& p, cudaStream_t s) {
   using C = TreeCfg<D, N>;
   const CacheView& c = p.a.cache;
   CUtensorMap map, map_v;
-  if (!encode_pages<D>(&map, c, c.k_pages, true) || !encode_pages<D>(&map_v, c, c.v_pages, false))
+  if (!encode_pages<D>(&map, c, c.k_pages, true) || !encode_pages<D>(&map_v, c, c.v_pages, true))
     return record_cuda_error(cudaErrorInvalidValue, "attn_cache_tree_fwd tensor map encoding");
   cudaError_t e = cudaFuncSetAttribute(cache_tree_kernel<D, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return record_cuda_error(e, "attn_cache_tree_fwd configure");

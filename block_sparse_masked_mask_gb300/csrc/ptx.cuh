@@ -336,16 +336,27 @@ __device__ __forceinline__ void tmem_st16x256(uint32_t taddr, const uint32_t (&r
                : "memory");
 }
 
-// Four (two) 8 x 8 matrices of 16-bit numbers into shared memory: register k of lane
+__device__ __forceinline__ void tmem_st16x256(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// Two 16 x 16 matrices of bytes, transposed: lane l gives the address of row l % 16 of matrix l / 16;
+// lane 4 g + i gets rows 4 i .. 4 i + 3 of columns g and g + 8 of the first (r0, r1) and of the second.
+__device__ __forceinline__ void ldmatrix_bytes(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3) : "r"(addr) : "memory");
+}
+
+// Four 8 x 8 matrices of 16-bit numbers into shared memory: register k of lane
 // 4 g + i holds columns 2i, 2i + 1 of row g of matrix k, and lane 8 k + g its address.
 __device__ __forceinline__ void stmatrix(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
                : "memory");
 }
-__device__ __forceinline__ void stmatrix(uint32_t addr, uint32_t r0, uint32_t r1) {
-  asm volatile("stmatrix.sync.aligned.m8n8.x2.shared.b16 [%0], {%1,%2};" ::"r"(addr), "r"(r0), "r"(r1) : "memory");
-}
-
 __device__ __forceinline__ void tmem_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
