@@ -39,21 +39,17 @@ struct CodeTile {
 
 // A bf16 query as the sum of two e4m3 numbers.  Scaled by a power of two to a
 // largest magnitude in [128, 256), its 8 significant bits are hi + lo exactly down
-// to 2^-9 of that magnitude, and within 2^-17 of it below.  Writes `row` of the
-// tile of hi at `tiles` and of the tile of lo behind it (zeros if not `real`);
+// to 2^-9 of that magnitude, and within 2^-17 of it below.  PARTS neighbouring lanes
+// share a row, each with its part q of the dimensions.  Writes `row` of the
+// tile of hi at `tiles` and of the tile of lo `behind` it;
 // returns the scale's inverse, NaN for an infinite query, which has no scores.
-// PARTS neighbouring lanes share a row, each with its part of the dimensions.  AGAIN: the row is
-// read a second time, in a loop of little code, and not held in registers.
-template <int D, int PARTS = 1, bool AGAIN = false>
-__device__ __forceinline__ float split_query(const __nv_bfloat16* query, bool real, uint8_t* tiles, int row,
-                                             int behind = CodeTile<D>::BYTES, int part = 0) {
+template <int D, int PARTS>
+__device__ __forceinline__ float split_held(const uint4 (&q)[D / PARTS / 8], uint8_t* tiles, int row, int behind,
+                                            int part) {
   constexpr int W = D / PARTS;
-  uint4 q[W / 8];
   float amax = 0.f;
-  const uint4* src = reinterpret_cast<const uint4*>(query + part * W);
 #pragma unroll
   for (int i = 0; i < W / 8; ++i) {
-    q[i] = real ? src[i] : make_uint4(0, 0, 0, 0);
     const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
 #pragma unroll
     for (int e = 0; e < 4; ++e)
@@ -63,15 +59,12 @@ __device__ __forceinline__ float split_query(const __nv_bfloat16* query, bool re
   for (int o = PARTS / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   const int e = amax > 0.f ? max(-119, min(126, exponent_of(amax))) : 0;
   const float f = pow2f(7 - e);
-#pragma unroll(AGAIN ? 1 : W / 16)
-  for (int i = 0; i < W / 16; ++i) {
-    uint4 two[2];
 #pragma unroll
-    for (int x = 0; x < 2; ++x) two[x] = !AGAIN ? q[2 * i + x] : real ? src[2 * i + x] : make_uint4(0, 0, 0, 0);
+  for (int i = 0; i < W / 16; ++i) {
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int e4 = 0; e4 < 4; ++e4) {
-      const uint4 v = two[e4 >> 1];
+      const uint4 v = q[2 * i + (e4 >> 1)];
       const uint32_t w0 = (e4 & 1) ? v.z : v.x, w1 = (e4 & 1) ? v.w : v.y;
       const float x0 = __uint_as_float(w0 << 16) * f, x1 = __uint_as_float(w0 & 0xFFFF0000u) * f;
       const float x2 = __uint_as_float(w1 << 16) * f, x3 = __uint_as_float(w1 & 0xFFFF0000u) * f;
@@ -87,6 +80,15 @@ __device__ __forceinline__ float split_query(const __nv_bfloat16* query, bool re
     *reinterpret_cast<uint4*>(tiles + behind + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
   return amax < INFINITY ? pow2f(e - 7) : __int_as_float(0x7FC00000);
+}
+// A whole row by one lane, from memory (zeros if not `real`).
+template <int D>
+__device__ __forceinline__ float split_query(const __nv_bfloat16* query, bool real, uint8_t* tiles, int row) {
+  uint4 q[D / 8];
+  const uint4* src = reinterpret_cast<const uint4*>(query);
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) q[i] = real ? src[i] : make_uint4(0, 0, 0, 0);
+  return split_held<D, 1>(q, tiles, row, CodeTile<D>::BYTES, 0);
 }
 
 // Pages as rows of D bytes, (dimension, slot, head, page), one page and head per copy.

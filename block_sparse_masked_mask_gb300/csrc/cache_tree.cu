@@ -49,6 +49,36 @@ constexpr int kNoPage = INT_MIN, kFar = 1;  // of a block of 16 tokens, as in ca
 constexpr int kTreeSms = 152;
 constexpr float kNoReference = -0x1p100f;   // of a row that has seen nothing yet
 
+// A constant that the compiler does not see: it would else copy a loop's body for its first turn.
+__device__ __forceinline__ uint32_t opaque(uint32_t x) {
+  asm volatile("" : "+r"(x));
+  return x;
+}
+
+// The bounded waits of tile_pipeline.cuh in the few instructions that five roles at once
+// leave room for: with 100 KB of code in all, warps waited for instructions more than for
+// anything else.  What runs out is left in *abort_flag, the site plus 1, and
+// becomes the status at the kernel's end.
+__device__ __forceinline__ bool tree_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, int site) {
+  bool ok = ptx::mbar_try_wait(bar, parity);
+  if (__builtin_expect(!ok, 0)) {
+    const uint32_t t0 = ptx::globaltimer_lo();
+    while (true) {
+      ok = ptx::mbar_try_wait(bar, parity);
+      if (ok || *abort_flag) break;
+      if (ptx::globaltimer_lo() - t0 > uint32_t(kWaitTimeoutNs)) {
+        *abort_flag = uint32_t(site) + 1u;
+        break;
+      }
+    }
+  }
+  return ok;
+}
+static_assert(kWaitTimeoutNs < (1ull << 32), "of a 32-bit clock");
+__device__ __forceinline__ bool tree_warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, int site) {
+  return __all_sync(0xffffffffu, tree_wait(bar, parity, abort_flag, site));
+}
+
 struct TreeParams {
   CacheQueryArgs a;
   const uint32_t* bits;
@@ -69,21 +99,16 @@ struct Segment {
 __device__ __forceinline__ int row_tiles(const SeqRows& r, int G, int N) { return (r.n * G + N - 1) / N; }
 __device__ __forceinline__ int tiles_of(const SeqRows& r) { return r.n == 0 ? 0 : (r.len + kTile - 1) / kTile; }
 
+// Tiles of sequence b, all heads and tiles of rows; 0 where its numbers cannot be used.
 template <int N>
-struct TreeUnits {
-  const TreeParams& p;
-  bool note;
-  __device__ int operator()(int b) const {
-    const CacheQueryArgs& a = p.a;
-    SeqRows r;
-    if (!load_rows(a.cu, a.lens, b, a.total_tokens, a.max_new, a.max_seqlen, a.cache.status, r, note)) return 0;
-    if (r.len < r.n) {
-      if (note) atomicOr(a.cache.status, kErrHeld);
-      return 0;
-    }
-    return tiles_of(r) * row_tiles(r, p.G, N) * a.cache.heads;
-  }
-};
+__device__ __forceinline__ int units_of(const TreeParams& p, int b) {
+  const CacheQueryArgs& a = p.a;
+  if (b >= a.cache.batch) return 0;
+  const int q0 = a.cu[b], q1 = a.cu[b + 1], len = a.lens[b], n = q1 - q0;
+  const bool good = q0 >= 0 && q1 >= q0 && q1 <= a.total_tokens && (b > 0 || q0 == 0) && n <= a.max_new && len >= n &&
+                    len <= a.max_seqlen;
+  return good ? (len + kTile - 1) / kTile * ((n * p.G + N - 1) / N) * a.cache.heads : 0;
+}
 __device__ __forceinline__ int tree_share(int total, const TreeParams& p) {
   return max(p.least, (total + p.ctas - 1) / p.ctas);
 }
@@ -122,7 +147,8 @@ struct TreeCfg {
   static constexpr int OFF_ROWS = OFF_SCL + NSCL * 8 * 16; // [2][N]: the rows' factors
   static constexpr int OFF_MAX = OFF_ROWS + 2 * N * 4;     // [2][4 warps][rows of a warpgroup]: maxima, then sums
   static constexpr int OFF_REF = OFF_MAX + 8 * N * 4;      // [2][N]: negative references
-  static constexpr int OFF_OUT = OFF_REF + 2 * N * 4;      // [N]: factors of the two warpgroups' O, place in the outputs
+  static constexpr int OFF_MOVE = OFF_REF + 2 * N * 4;     // [8 warps][rows of a warpgroup]: negative reference, half the factor's exponent
+  static constexpr int OFF_OUT = OFF_MOVE + 8 * (TURNS ? N : N / 2) * 8;      // [N]: factors of the two warpgroups' O, place in the outputs
   static constexpr int OFF_SEG = OFF_OUT + N * 16;
   static constexpr int OFF_BAR = OFF_SEG + NSEG * 48;
   static constexpr int B_SEGFULL = 0, B_SEGFREE = B_SEGFULL + NSEG, B_QFULL = B_SEGFREE + NSEG, B_QFREE = B_QFULL + 2,
@@ -131,6 +157,18 @@ struct TreeCfg {
                        B_SCLFREE = B_SCLFULL + NSCL, B_SFULL = B_SCLFREE + NSCL, B_PFULL = B_SFULL + NB,
                        B_PDONE = B_PFULL + NB, B_OFREE = B_PDONE + NB, B_USED = B_OFREE + NO,
                        B_DRAIN = B_USED + 2, NBAR = B_DRAIN + 2;
+  static_assert(NBAR <= kTreeThreads, "a thread for each");
+  __device__ static int arrivals(int i) {
+    return i >= B_USED ? (i >= B_DRAIN ? 1 : 8)
+           : i >= B_OFREE ? 8
+           : i >= B_PFULL ? (i >= B_PDONE ? 1 : TURNS ? 4 : 8)
+           : i >= B_SCLFREE ? (i >= B_SFULL ? 1 : 4 + (TURNS ? 4 : 8))  // value and softmax warps
+           : i >= B_SCLFULL ? 1
+           : i >= B_VFULL ? (i >= B_VFREE ? 1 : 4)
+           : i >= B_RFREE ? 4
+           : i >= B_QFULL ? (i >= B_QFREE ? 1 : 4)
+           : i >= B_SEGFREE ? 15 : 1;  // the warps 0 to 14
+  }
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int USED = OFF_MISC + 16 + 1024;        // the base is aligned to 1024
   // one CTA per SM: it takes all of TMEM
@@ -162,32 +200,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   volatile uint32_t* abort_flag = misc + 1;
   float4* scl = reinterpret_cast<float4*>(sbase + C::OFF_SCL);
 
-  if (threadIdx.x == 0) {
-    auto init = [&](int first, int n, int count) {
-      for (int i = 0; i < n; ++i) ptx::mbar_init(bar(first + i), count);
-    };
-    init(C::B_SEGFULL, C::NSEG, 1);
-    init(C::B_SEGFREE, C::NSEG, 15);  // the warps 0 to 14
-    init(C::B_QFULL, 2, 4);
-    init(C::B_QFREE, C::NQ, 1);
-    init(C::B_KFULL, C::NK, 1);
-    init(C::B_KFREE, C::NK, 1);
-    init(C::B_RFULL, C::NR, 1);
-    init(C::B_RFREE, C::NR, 4);
-    init(C::B_VFULL, 2, 4);
-    init(C::B_VFREE, 2, 1);
-    init(C::B_SCLFULL, C::NSCL, 1);
-    init(C::B_SCLFREE, C::NSCL, 4 + (C::TURNS ? 4 : 8));  // value and softmax warps
-    init(C::B_SFULL, C::NB, 1);
-    init(C::B_PFULL, C::NB, C::TURNS ? 4 : 8);
-    init(C::B_PDONE, C::NB, 1);
-    init(C::B_OFREE, C::NO, 8);
-    init(C::B_USED, 2, 8);
-    init(C::B_DRAIN, 2, 1);
-    // (the second word decides alone whether warps start: see cache_chunk.cu)
-    misc[2] = *abort_flag = (*reinterpret_cast<volatile int32_t*>(err) & kErrTimeout) ? 1u : 0u;
+  if (threadIdx.x < C::NBAR) {
+    ptx::mbar_init(bar(threadIdx.x), C::arrivals(threadIdx.x));
     ptx::fence_mbar_init();
   }
+  if (threadIdx.x == 0) *abort_flag = 0u;
   if (warp == kWarpO) {
     ptx::tmem_alloc(ptx::smem_addr(misc), 512);
     ptx::tmem_relinquish();
@@ -196,13 +213,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = misc[0];
-  const bool skip = misc[2] != 0u;
 
   // The s-th segment, copied from its place in the ring; one arrival frees that.
   auto segment = [&](int s, Segment& g, bool single) {
     const int at = s % C::NSEG;
-    const bool ok = single ? wait_bar(bar(C::B_SEGFULL + at), uint32_t(s / C::NSEG) & 1u, abort_flag, err, 1)
-                           : warp_wait(bar(C::B_SEGFULL + at), uint32_t(s / C::NSEG) & 1u, abort_flag, err, 1);
+    const bool ok = single ? tree_wait(bar(C::B_SEGFULL + at), uint32_t(s / C::NSEG) & 1u, abort_flag, 1)
+                           : tree_warp_wait(bar(C::B_SEGFULL + at), uint32_t(s / C::NSEG) & 1u, abort_flag, 1);
     g.tiles = 0;
     if (!ok) return false;
     const int4* w = reinterpret_cast<const int4*>(sbase + C::OFF_SEG + at * 48);
@@ -215,30 +231,61 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 
   // Registers: of the launch's 128 for each thread the softmax takes 168, the conversion 104,
   // the others 72.  (Set in each branch: where they meet, the least would hold for all.)
-  if (skip) {
-    // nothing issued, nothing to drain
-  } else if (warp >= kWarpPages) {
+  if (warp >= kWarpPages) {
    ptx::regs_dec<72>();
    if (warp == kWarpLine) {
     // -------------------------------------------------------------- segments
-    const TreeUnits<N> units{p, blockIdx.x == 0};
-    const UnitLine line(units, c.batch, lane);
-    const int piece = tree_share(line.total, p);
-    int pos = int(min(int64_t(blockIdx.x) * piece, int64_t(line.total)));
-    const int stop = min(pos + piece, line.total);
-    int b = 0, before = 0;
-    if (pos < stop) b = line.find(units, c.batch, lane, pos, before);
+    // 64 sequences at a time, two neighbours per lane
+    int total = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < c.batch; b0 += 64) total += units_of<N>(p, b0 + 2 * lane) + units_of<N>(p, b0 + 2 * lane + 1);
+    total = __reduce_add_sync(0xffffffffu, total);
+    const int piece = tree_share(total, p);
+    int pos = int(min(int64_t(blockIdx.x) * piece, int64_t(total)));
+    const int stop = min(pos + piece, total);
+    // (after a wait that ran out in an earlier CTA there is nothing to do)
+    if (*reinterpret_cast<volatile int32_t*>(err) & kErrTimeout) pos = stop;
+    int b = 0, before = 0;  // the sequence that pos belongs to, and the line before it
+#pragma unroll 1
+    while (pos < stop) {
+      const int n0 = units_of<N>(p, b + 2 * lane), n1 = units_of<N>(p, b + 2 * lane + 1);
+      int sum = n0 + n1;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += y;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, before + sum > pos);
+      if (past == 0) {
+        b += 64;
+        before += __shfl_sync(0xffffffffu, sum, 31);
+        continue;
+      }
+      const int at = __ffs(past) - 1, skip = __shfl_sync(0xffffffffu, sum - n0 - n1, at), half = __shfl_sync(0xffffffffu, n0, at);
+      before += skip;
+      b += 2 * at;
+      if (before + half <= pos) {
+        before += half;
+        ++b;
+      }
+      break;
+    }
+#pragma unroll 1
     for (int s = 0;; ++s) {
       Segment g{};
+#pragma unroll 1
       while (pos < stop) {
-        SeqRows r;
-        const bool good = load_rows(a.cu, a.lens, b, a.total_tokens, a.max_new, a.max_seqlen, err, r, false);
-        const int U = good && r.len >= r.n ? tiles_of(r) : 0, RT = U ? row_tiles(r, p.G, N) : 0;
-        if (pos >= before + U * RT * c.heads) {
-          before += U * RT * c.heads;
+        const int all = units_of<N>(p, b);
+        if (pos >= before + all) {
+          before += all;
           ++b;
           continue;
         }
+        SeqRows r;
+        r.q0 = a.cu[b];
+        r.n = a.cu[b + 1] - r.q0;
+        r.len = a.lens[b];
+        const int U = tiles_of(r), RT = row_tiles(r, p.G, N);
         const int item = (pos - before) / U, u0 = (pos - before) % U, u1 = min(U, u0 + stop - pos);
         g.tiles = u1 - u0;
         g.b = b;
@@ -254,7 +301,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         break;
       }
       const int at = s % C::NSEG;
-      if (s >= C::NSEG && !warp_wait(bar(C::B_SEGFREE + at), uint32_t(s / C::NSEG - 1) & 1u, abort_flag, err, 2)) break;
+      if (s >= C::NSEG && !tree_warp_wait(bar(C::B_SEGFREE + at), uint32_t(s / C::NSEG - 1) & 1u, abort_flag, 2)) break;
       if (lane == 0) {
         int4* w = reinterpret_cast<int4*>(sbase + C::OFF_SEG + at * 48);
         w[0] = make_int4(g.tiles, g.b, g.h, g.row0);
@@ -264,6 +311,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       }
       __syncwarp();
       if (g.tiles == 0) break;
+    }
+    // what is wrong with the sequences is noted once, when nobody waits for it
+    if (blockIdx.x == 0) {
+#pragma unroll 1
+      for (int x = lane; x < c.batch; x += 32) {
+        SeqRows r;
+        if (load_rows(a.cu, a.lens, x, a.total_tokens, a.max_new, a.max_seqlen, err, r) && r.len < r.n) atomicOr(err, kErrHeld);
+      }
     }
   } else if (warp == kWarpPages) {
     // -------------------------------------------------------------- pages, scales, codes
@@ -278,6 +333,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     Segment g;
     int T = 0, done = 0, done_v = 0;
     bool ok = true;
+#pragma unroll 1
     for (int s = 0; ok && segment(s, g, false) && g.tiles; ++s) {
       const int end = min(g.token + g.tiles * kTile, g.len);
       auto token = [&](int j) { return g.token + j * kTile + lane * 16; };  // of the four from j
@@ -290,6 +346,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       int id = 0, id_next = number(0), id_after = number(4);
       float2 sc = make_float2(0.f, 0.f), sc_next = scales(0, id_next);
       int x_top = 0;  // largest exponent of the values so far, if above that of values up to 448
+#pragma unroll 1
       for (int j = 0; j < g.tiles; ++j, ++T) {
         if ((j & 3) == 0) {
           id = id_next;
@@ -301,7 +358,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const int ss = T % C::NSCL, ks = T % C::NK, rs = T % C::NR;
         const bool mine = lane >> 3 == (j & 3), here = mine && token(j & ~3) < end, fine = here && in_pool(c, id);
         if (here && !fine) atomicOr(err, kErrBadPage);
-        if (T >= C::NSCL && !warp_wait(bar(C::B_SCLFREE + ss), uint32_t(T / C::NSCL - 1) & 1u, abort_flag, err, 3)) { ok = false; break; }
+        // keys first: they need no scales yet
+        if (T >= C::NK && !tree_warp_wait(bar(C::B_KFREE + ks), uint32_t(T / C::NK - 1) & 1u, abort_flag, 4)) { ok = false; break; }
+        const bool load = fine && lane % step == 0;  // one lane per page (eight lanes are whole pages)
+        const uint32_t loads = __popc(__ballot_sync(0xffffffffu, load));
+        if (lane == 0) ptx::mbar_arrive_expect_tx(bar(C::B_KFULL + ks), bytes * loads);
+        __syncwarp();
+        if (load)
+          ptx::tma_load_4d(base + C::OFF_K + ks * C::KT + (lane & 7) * 16 * D, &tmK, bar(C::B_KFULL + ks), 0, 0, g.h, id);
+        done = T + 1;
+        if (T >= C::NSCL && !tree_warp_wait(bar(C::B_SCLFREE + ss), uint32_t(T / C::NSCL - 1) & 1u, abort_flag, 3)) { ok = false; break; }
         const int x = exponent_of(sc.y);
         if (__any_sync(0xffffffffu, fine && x > x_top)) x_top = max(x_top, __reduce_max_sync(0xffffffffu, fine ? x : 0));
         if (mine) {
@@ -312,15 +378,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(C::B_SCLFULL + ss));
-        if (T >= C::NK && !warp_wait(bar(C::B_KFREE + ks), uint32_t(T / C::NK - 1) & 1u, abort_flag, err, 4)) { ok = false; break; }
-        const bool load = fine && lane % step == 0;  // one lane per page (eight lanes are whole pages)
-        const uint32_t loads = __popc(__ballot_sync(0xffffffffu, load));
-        if (lane == 0) ptx::mbar_arrive_expect_tx(bar(C::B_KFULL + ks), bytes * loads);
-        __syncwarp();
-        if (load)
-          ptx::tma_load_4d(base + C::OFF_K + ks * C::KT + (lane & 7) * 16 * D, &tmK, bar(C::B_KFULL + ks), 0, 0, g.h, id);
-        done = T + 1;
-        if (T >= C::NR && !warp_wait(bar(C::B_RFREE + rs), uint32_t(T / C::NR - 1) & 1u, abort_flag, err, 5)) { ok = false; break; }
+        if (T >= C::NR && !tree_warp_wait(bar(C::B_RFREE + rs), uint32_t(T / C::NR - 1) & 1u, abort_flag, 5)) { ok = false; break; }
         if (lane == 0) ptx::mbar_arrive_expect_tx(bar(C::B_RFULL + rs), bytes * loads);
         __syncwarp();
         if (load)
@@ -330,11 +388,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     }
     // do not leave while a copy may still be writing shared memory
     if (lane == 0) {
+#pragma unroll 1
       for (int i = 0; i < C::NK; ++i) {
         if (done <= i) continue;
         const int last = i + C::NK * ((done - 1 - i) / C::NK);
         drain_bar(bar(C::B_KFULL + i), uint32_t(last / C::NK) & 1u, err);
       }
+#pragma unroll 1
       for (int i = 0; i < C::NR; ++i) {
         if (done_v <= i) continue;
         const int last = i + C::NR * ((done_v - 1 - i) / C::NR);
@@ -351,14 +411,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       Segment g;
       int T = 0;
       bool ok = true;
+#pragma unroll 1
       for (int s = 0; ok && segment(s, g, true) && g.tiles; ++s) {
-        ok = wait_bar(bar(C::B_QFULL + (s & 1)), uint32_t(s >> 1) & 1u, abort_flag, err, 6);
+        ok = tree_wait(bar(C::B_QFULL + (s & 1)), uint32_t(s >> 1) & 1u, abort_flag, 6);
         const uint64_t qhi = qd + uint64_t((s % C::NQ) * C::QT >> 4), qlo = qhi + uint64_t(N * D >> 4);
+#pragma unroll 1
         for (int j = 0; ok && j < g.tiles; ++j, ++T) {
           const int ks = T % C::NK, f = T % C::NB;
-          ok = wait_bar(bar(C::B_KFULL + ks), uint32_t(T / C::NK) & 1u, abort_flag, err, 7) &&
+          ok = tree_wait(bar(C::B_KFULL + ks), uint32_t(T / C::NK) & 1u, abort_flag, 7) &&
                // the softmax has read the scores that lie there
-               (T < C::NB || wait_bar(bar(C::B_PFULL + f), uint32_t(T / C::NB - 1) & 1u, abort_flag, err, 8));
+               (T < C::NB || tree_wait(bar(C::B_PFULL + f), uint32_t(T / C::NB - 1) & 1u, abort_flag, 8));
           if (!ok) break;
           ptx::tc_fence_after();
           const uint64_t ki = kd + uint64_t(ks * C::KT >> 4);
@@ -385,13 +447,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       Segment g;
       int T = 0;
       bool ok = true;
+#pragma unroll 1
       for (int s = 0; ok && segment(s, g, true) && g.tiles; ++s) {
-        if (s >= C::NO) ok = wait_bar(bar(C::B_OFREE + s % C::NO), uint32_t(s / C::NO - 1) & 1u, abort_flag, err, 9);
+        if (s >= C::NO) ok = tree_wait(bar(C::B_OFREE + s % C::NO), uint32_t(s / C::NO - 1) & 1u, abort_flag, 9);
         const uint32_t o_seg = tmem + uint32_t(C::O + s % C::NO * C::OSEG);
+#pragma unroll 1
         for (int j = 0; ok && j < g.tiles; ++j, ++T) {
           const int f = T % C::NB, vs = T & 1;
-          ok = wait_bar(bar(C::B_VFULL + vs), uint32_t(T >> 1) & 1u, abort_flag, err, 11) &&
-               wait_bar(bar(C::B_PFULL + f), uint32_t(T / C::NB) & 1u, abort_flag, err, 10);
+          ok = tree_wait(bar(C::B_VFULL + vs), uint32_t(T >> 1) & 1u, abort_flag, 11) &&
+               tree_wait(bar(C::B_PFULL + f), uint32_t(T / C::NB) & 1u, abort_flag, 10);
           if (!ok) break;
           ptx::tc_fence_after();
           const uint32_t o_tmem = o_seg + (C::TURNS ? uint32_t(T & 1) * N : 0u), v_tmem = tmem + uint32_t(C::V + vs * 64);
@@ -415,33 +479,51 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     Segment g;
     int T = 0;
     bool ok = true;
+#pragma unroll 1
     for (int s = 0; ok && segment(s, g, false) && g.tiles; ++s) {
       // the queries two segments back are used, and so are their factors
-      if (s >= C::NQ) ok = warp_wait(bar(C::B_QFREE + s % C::NQ), uint32_t(s / C::NQ - 1) & 1u, abort_flag, err, 12);
-      if (ok && s >= 2) ok = warp_wait(bar(C::B_USED + (s & 1)), uint32_t((s >> 1) - 1) & 1u, abort_flag, err, 13);
+      if (s >= C::NQ) ok = tree_warp_wait(bar(C::B_QFREE + s % C::NQ), uint32_t(s / C::NQ - 1) & 1u, abort_flag, 12);
+      if (ok && s >= 2) ok = tree_warp_wait(bar(C::B_USED + (s & 1)), uint32_t((s >> 1) - 1) & 1u, abort_flag, 13);
       if (!ok) break;
-      {
-        constexpr int PARTS = 128 / N < D / 16 ? 128 / N : D / 16;  // threads of a row
-        const int row = ct / PARTS;
-        if (row < N) {
-          const bool real = row < g.rows;
-          const int rg = g.row0 + (real ? row : 0);
-          const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) +
-                                   (int64_t(g.q0 + rg / p.G) * a.num_heads + g.h * p.G + rg % p.G) * D;
-          const float f = p.scale_log2 * split_query<D, PARTS, true>(q, real, sbase + C::OFF_Q + (s % C::NQ) * C::QT, row, N * D, ct % PARTS);
-          if (ct % PARTS == 0) reinterpret_cast<float*>(sbase + C::OFF_ROWS)[(s & 1) * N + row] = f;
+      // D / 16 lanes per row, rows on their way two turns ahead
+      constexpr int PARTS = D / 16, STEP = 128 / PARTS;
+      auto fetch = [&](int row, uint4 (&q)[2]) {
+        if (row < g.rows) {
+          const int rg = g.row0 + row;
+          const uint4* src = reinterpret_cast<const uint4*>(
+              static_cast<const __nv_bfloat16*>(a.q) +
+              (int64_t(g.q0 + rg / p.G) * a.num_heads + g.h * p.G + rg % p.G) * D) + 2 * (ct % PARTS);
+          q[0] = src[0];
+          q[1] = src[1];
+        } else {
+          q[0] = q[1] = make_uint4(0, 0, 0, 0);
+        }
+      };
+      uint4 q[3][2];
+      fetch(ct / PARTS, q[0]);
+      fetch(ct / PARTS + STEP, q[1]);
+#pragma unroll 1
+      for (int row = ct / PARTS; row < N; row += STEP) {  // (whole warps)
+        fetch(row + 2 * STEP, q[2]);
+        const float f = p.scale_log2 * split_held<D, PARTS>(q[0], sbase + C::OFF_Q + (s % C::NQ) * C::QT, row, N * D, ct % PARTS);
+        if (ct % PARTS == 0) reinterpret_cast<float*>(sbase + C::OFF_ROWS)[(s & 1) * N + row] = f;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          q[0][x] = q[1][x];
+          q[1][x] = q[2][x];
         }
       }
       ptx::fence_proxy_async_smem();
       warp_arrive(bar(C::B_QFULL + (s & 1)), lane);
       const int end = min(g.token + g.tiles * kTile, g.len);
+#pragma unroll 1
       for (int j = 0; j < g.tiles; ++j, ++T) {
         const int rs = T % C::NR, ss = T % C::NSCL;
         // (the scales' slot was written before this arrived)
-        if (!warp_wait(bar(C::B_RFULL + rs), uint32_t(T / C::NR) & 1u, abort_flag, err, 14)) { ok = false; break; }
+        if (!tree_warp_wait(bar(C::B_RFULL + rs), uint32_t(T / C::NR) & 1u, abort_flag, 14)) { ok = false; break; }
         const bool gone = __float_as_int(scl[ss * 8 + (lane & 7)].w) < 0;
         const bool ragged = __any_sync(0xffffffffu, gone) || g.token + (j + 1) * kTile > end;
-        if (T >= 2 && !warp_wait(bar(C::B_VFREE + (T & 1)), uint32_t((T >> 1) - 1) & 1u, abort_flag, err, 15)) { ok = false; break; }
+        if (T >= 2 && !tree_warp_wait(bar(C::B_VFREE + (T & 1)), uint32_t((T >> 1) - 1) & 1u, abort_flag, 15)) { ok = false; break; }
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
           const int u = 2 * cw + z;  // 16 dimensions
@@ -451,7 +533,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           for (int x = 0; x < 4; ++x)
             ptx::ldmatrix_bytes(base + C::OFF_R + rs * C::KT + CodeTile<D>::unit(32 * x + lane, u), w[4 * x], w[4 * x + 1],
                                 w[4 * x + 2], w[4 * x + 3]);
-          if (ragged) {
+          if (__builtin_expect(ragged, 0)) {
             // behind the end, or without a page: weights of 0 times 0
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
@@ -525,18 +607,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     // (never 0, where a page is left out or the product is below fp32: a hidden score is -inf, and
     // times 0 it would be NaN)
     auto factor = [](float2 f, float2 ks) { return ptx::ffma2(f, ks, make_float2(0x1p-126f, 0x1p-126f)); };
-    // Half the exponent of the factor that a row's sums take; `minus` is the negative reference.
-    auto move_reference = [](float most, float& minus) {
-      const float was = -minus;
-      if (!(most > was + kMostWeight)) return 1.f;
-      minus = kTopWeight - most;
-      return half_factor(was, -minus);
-    };
+    float2* const move = reinterpret_cast<float2*>(sbase + C::OFF_MOVE) + warp * ROWS;
     // The scales of this warp's two blocks of tile T, which has no further use for its slot.
     float4 of[2];
     auto scales = [&](int T) {
       const int ss = T % C::NSCL;
-      if (!warp_wait(bar(C::B_SCLFULL + ss), uint32_t(T / C::NSCL) & 1u, abort_flag, err, 17)) return false;
+      if (!tree_warp_wait(bar(C::B_SCLFULL + ss), uint32_t(T / C::NSCL) & 1u, abort_flag, 17)) return false;
       of[0] = scl[ss * 8 + w4 * 2];
       of[1] = scl[ss * 8 + w4 * 2 + 1];
       warp_arrive(bar(C::B_SCLFREE + ss), lane);
@@ -545,11 +621,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     // where this lane's row of a matrix of weights goes: a token, and the first or second
     // eight rows of the query of sixteen
     const int to_token = w4 * 32 + (lane & 15), to_unit = row_base / 8 + (lane >> 4);
-    Segment g;
-    for (int s = 0, T0 = 0;; ++s, T0 += g.tiles) {
-      bool ok = segment(s, g, false);
-      if (ok && g.tiles) ok = warp_wait(bar(C::B_QFULL + (s & 1)), uint32_t(s >> 1) & 1u, abort_flag, err, 16);
-      if (meet_all(!ok) || g.tiles == 0) break;
+    // Before the first segment is there, one tile of nothing (on what lies in this warpgroup's O):
+    // the instructions of the loop arrive while the first keys do, and not after them.
+    Segment g{(C::TURNS ? wg : 0) + 1, 0, 0, 0, 0, 0, 0, 1 << 30, 0, 0};
+    of[0] = of[1] = make_float4(1.f, 0.f, 1.f, 0.f);
+    bool dry = opaque(1) != 0;
+#pragma unroll 1
+    for (int s = 0, T0 = 0;;) {
+      bool ok = true;
+      if (!dry) {
+        ok = segment(s, g, false);
+        if (ok && g.tiles) ok = tree_warp_wait(bar(C::B_QFULL + (s & 1)), uint32_t(s >> 1) & 1u, abort_flag, 16);
+        if (meet_all(!ok) || g.tiles == 0) break;
+      }
       const int text = g.len - g.n;
       const uint32_t o_seg = lanes + uint32_t(C::O + s % C::NO * C::OSEG), o_col = o_seg + uint32_t(C::TURNS ? wg * N : row_base);
       const float* factors = reinterpret_cast<const float*>(sbase + C::OFF_ROWS) + (s & 1) * N + row_base;
@@ -562,17 +646,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       }
 
       const int mine = C::TURNS ? (T0 ^ wg) & 1 : 0;  // the first tile of this warpgroup's
-      if (mine < g.tiles) ok = scales(T0 + mine);
+      if (mine < g.tiles && !dry) ok = scales(T0 + mine);
       bool left = false;
+#pragma unroll 1
       for (int j = mine; j < g.tiles; j += STRIDE) {
         const int T = T0 + j, f = T % C::NB;
-        const uint32_t s_col = lanes + uint32_t(C::S + f * N + row_base), weights = base + C::OFF_P + f * C::P::BYTES;
+        const uint32_t s_col = dry ? o_col : lanes + uint32_t(C::S + f * N + row_base), weights = base + C::OFF_P + f * C::P::BYTES;
         const int token = g.token + j * kTile + w4 * 32 + lane;
         const int flags = __float_as_int(of[0].w) | __float_as_int(of[1].w);
         // which rows see this lane's token
         const bool masked = __any_sync(0xffffffffu, token >= text) || flags < 0;
         uint64_t see = ~0ull;
-        if (masked) {
+        if (__builtin_expect(masked, 0)) {
           const bool here = token < g.len && __float_as_int(lane < 16 ? of[0].w : of[1].w) >= 0;
           see = here && token < text ? ~0ull : 0ull;
           if (here && token >= text) {
@@ -587,11 +672,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           }
         }
         // the scores, and room for the weights
-        ok = ok && warp_wait(bar(C::B_SFULL + f), uint32_t(T / C::NB) & 1u, abort_flag, err, 18) &&
-             (T < C::NB || warp_wait(bar(C::B_PDONE + f), uint32_t(T / C::NB - 1) & 1u, abort_flag, err, 19));
+        ok = ok && (dry || tree_warp_wait(bar(C::B_SFULL + f), uint32_t(T / C::NB) & 1u, abort_flag, 18)) &&
+             (T < C::NB || tree_warp_wait(bar(C::B_PDONE + f), uint32_t(T / C::NB - 1) & 1u, abort_flag, 19));
         ptx::tc_fence_after();
-        if (masked) hide(s_col, see);
-        float2 lt[K];  // the tile's sums (before them, factors of the earlier ones)
+        if (__builtin_expect(masked, 0)) hide(s_col, see);
+        float2 lt[K];  // the tile's sums
         float top;
         // The weights under the present references, into shared memory, and the largest of
         // their base-2 logarithms.
@@ -633,14 +718,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                             pk[2 * kk + 2], pk[2 * kk + 3]);
           }
         };
-        for (bool moved = false;; moved = true) {
+#pragma unroll 1
+        for (bool moved = opaque(0) != 0;; moved = true) {
           // (the first tile sets the references)
           if (j >= STRIDE || moved) {
             weigh();
-            if (moved || !meet(!ok || top > kMostWeight)) break;
+            if (__builtin_expect(moved || !meet(!ok || top > kMostWeight), 1)) break;
           }
           // a weight would pass 2^15 (or a wait ran out): the references of such rows move
-#pragma unroll 1
+#pragma unroll 2
           for (int k = 0; k < K; ++k) {
             uint32_t v[2][4];
 #pragma unroll
@@ -666,29 +752,36 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           }
           const int before = T - STRIDE;  // this warpgroup's last tile
           if (j >= STRIDE)
-            ok = ok && warp_wait(bar(C::B_PDONE + before % C::NB), uint32_t(before / C::NB) & 1u, abort_flag, err, 20);
+            ok = ok && tree_warp_wait(bar(C::B_PDONE + before % C::NB), uint32_t(before / C::NB) & 1u, abort_flag, 20);
           if (meet(!ok)) {
             left = true;  // all of them
             break;
           }
           ptx::tc_fence_after();
-          // (every warp for itself, with the same result)
+          // A lane per row, every warp for itself with the same result (in little code, as
+          // all that runs once a segment: instructions from far away cost more than their work)
+          if (lane < ROWS) {
+#pragma unroll 1
+            for (int x = lane; x < ROWS; x += 32) {
+              const float now = fmaxf(fmaxf(warps[x], warps[ROWS + x]), fmaxf(warps[2 * ROWS + x], warps[3 * ROWS + x]));
+              const float was = j >= STRIDE ? -move[x].x : kNoReference;
+              const bool raise = now > was + kMostWeight;
+              move[x] = make_float2(raise ? kTopWeight - now : -was, raise ? half_factor(was, now - kTopWeight) : 1.f);
+            }
+          }
+          __syncwarp();
 #pragma unroll
           for (int k = 0; k < K; ++k) {
-            float2 now = make_float2(-INFINITY, -INFINITY), h;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const float2 y = *reinterpret_cast<const float2*>(warps + w * ROWS + 8 * k + 2 * i4);
-              now = make_float2(fmaxf(now.x, y.x), fmaxf(now.y, y.y));
-            }
-            h.x = move_reference(now.x, m2[k].x);
-            h.y = move_reference(now.y, m2[k].y);
+            const float4 y = *reinterpret_cast<const float4*>(move + 8 * k + 2 * i4);
+            const float2 h = make_float2(y.y, y.w);
+            m2[k] = make_float2(y.x, y.z);
             l2[k] = ptx::fmul2(ptx::fmul2(l2[k], h), h);
-            lt[k] = ptx::fmul2(h, h);
           }
           if (j >= STRIDE) {  // O holds the earlier tiles' products, which have ended
-#pragma unroll
+#pragma unroll 1
             for (int k = 0; k < K; ++k) {
+              const float4 y = *reinterpret_cast<const float4*>(move + 8 * k + 2 * i4);
+              const float2 h = make_float2(y.y * y.y, y.w * y.w);
               uint32_t w[2][4];
 #pragma unroll
               for (int z = 0; z < 2; ++z) ptx::tmem_ld16x256(o_col + (uint32_t(16 * z) << 16) + uint32_t(8 * k), w[z]);
@@ -696,15 +789,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
               for (int z = 0; z < 2; ++z) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) w[z][e] = __float_as_uint(__uint_as_float(w[z][e]) * (e & 1 ? lt[k].y : lt[k].x));
+                for (int e = 0; e < 4; ++e) w[z][e] = __float_as_uint(__uint_as_float(w[z][e]) * (e & 1 ? h.y : h.x));
                 ptx::tmem_st16x256(o_col + (uint32_t(16 * z) << 16) + uint32_t(8 * k), w[z]);
               }
             }
           }
+          __syncwarp();  // the table is read before it changes again
           ptx::tmem_wait_st();
         }
         if (left) break;
-        if (flags & kFar) {  // sums that do not go through the weights
+        if (__builtin_expect(flags & kFar, 0)) {  // sums that do not go through the weights
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
             if (__float_as_int(of[z].w) != kFar) continue;
@@ -725,15 +819,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
         ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
-        warp_arrive(bar(C::B_PFULL + f), lane);
+        __syncwarp();
+        if (lane == 0 && !dry) ptx::mbar_arrive(bar(C::B_PFULL + f));
 #pragma unroll
         for (int k = 0; k < K; ++k) l2[k] = ptx::fadd2(l2[k], lt[k]);
         if (j + STRIDE < g.tiles) ok = scales(T + STRIDE);
       }
+      if (dry) {
+        dry = false;
+        continue;
+      }
       // ---- the segment's end: sums over the tokens, O
       if (!C::TURNS && left) break;
       const int end = T0 + g.tiles - 1, last = C::TURNS ? end - ((end ^ wg) & 1) : end;  // this warpgroup's last tile
-      if (last >= T0) ok = ok && !left && warp_wait(bar(C::B_PDONE + last % C::NB), uint32_t(last / C::NB) & 1u, abort_flag, err, 21);
+      if (last >= T0) ok = ok && !left && tree_warp_wait(bar(C::B_PDONE + last % C::NB), uint32_t(last / C::NB) & 1u, abort_flag, 21);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         float2 y = l2[k];
@@ -755,16 +854,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           float its[2], half[2];
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const bool some = g.tiles > 1 || ((T0 ^ x) & 1) == 0;  // (else there is nothing in O)
             const float* const w = all + x * 4 * N + row;
             its[x] = (w[0] + w[N]) + (w[2 * N] + w[3 * N]);
-            half[x] = some ? -refs[x * N + row] : -INFINITY;
+            half[x] = -refs[x * N + row];
             m = fmaxf(m, half[x]);
           }
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             half[x] = half_factor(half[x], m);
-            sum += half[x] > 0.f ? its[x] * half[x] * half[x] : 0.f;
+            sum += its[x] * half[x] * half[x];
             part[x] = half[x] * half[x];
           }
         } else {
@@ -773,50 +871,54 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           m = -refs[wg * ROWS + tid];
           part[0] = 1.f;
         }
-        const int rg = g.row0 + row, head = g.h * p.G + rg % p.G, at = g.q0 + rg / p.G;
+        const int rg = g.row0 + row, node = rg / p.G, head = g.h * p.G + rg - node * p.G, at = g.q0 + node;
         if (row < g.rows) {
           if (whole)
             a.lse[int64_t(head) * a.total_tokens + at] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
           else
             p.part_m[int64_t(g.slot) * N + row] = make_float2(m == kNoReference ? -INFINITY : m, sum);
         }
-        const float inv = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
-        out[row] = make_float4(part[0] * inv, part[1] * inv, __int_as_float(whole ? at * a.num_heads + head : g.slot * N + row), 0.f);
+        const float inv = !whole ? 1.f : sum == 0.f ? 0.f : __fdividef(1.f, sum);
+        const uint64_t to = whole ? (uint64_t(at) * a.num_heads + head) * (2 * D) : uint64_t(g.slot * N + row) * (4 * D);  // bytes
+        out[row] = make_float4(part[0] * inv, part[1] * inv, __uint_as_float(uint32_t(to)), __uint_as_float(uint32_t(to >> 32)));
       }
       meet(false);  // (a warpgroup reads the rows that it wrote)
       if (lane == 0) ptx::mbar_arrive(bar(C::B_USED + (s & 1)));
       ptx::tc_fence_after();
       const int first = row - tid;
+      // (the other warpgroup's O, of which its factor is 0 where it had no tile and there is nothing)
+      const uint32_t o_mine = o_seg + (C::TURNS ? uint32_t((T0 & 1) * N) : 0u);
+      const uint32_t o_other = o_seg + (C::TURNS ? uint32_t(((T0 + (g.tiles > 1)) & 1) * N) : 0u);
+      uint8_t* const to = (whole ? static_cast<uint8_t*>(a.o) : reinterpret_cast<uint8_t*>(p.part_o)) + tid * (whole ? 2 : 4);
 #pragma unroll 1
-      for (int q = first; q < first + N / 2; q += 8) {
-        uint32_t w[2][8];
-        ptx::tmem_ld8(o_seg + q, w[0]);
-        if (C::TURNS) ptx::tmem_ld8(o_seg + N + q, w[1]);
+      for (int q = first; q < first + N / 2; q += 4) {
+        uint32_t w[2][4];
+        ptx::tmem_ld4(o_mine + q, w[0]);
+        if (C::TURNS) ptx::tmem_ld4(o_other + q, w[1]);
         ptx::tmem_wait_ld();
-        if (q + 8 == first + N / 2) {
+        if (q + 4 == first + N / 2) {
           ptx::tc_fence_before();
           warp_arrive(bar(C::B_OFREE + s % C::NO), lane);
         }
-        if (w4 * 32 < D) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (q + i >= g.rows) break;
-            const float4 to = out[q + i];
-            // (times 0 is not taken: there may be nothing)
-            float y = to.x != 0.f ? __uint_as_float(w[0][i]) * to.x : 0.f;
-            if (C::TURNS && to.y != 0.f) y = fmaf(__uint_as_float(w[1][i]), to.y, y);
-            const int64_t at = int64_t(__float_as_int(to.z)) * D + tid;
-            if (whole) static_cast<__nv_bfloat16*>(a.o)[at] = __float2bfloat16_rn(y);
-            else p.part_o[at] = y;
-          }
+        for (int i = 0; i < 4; ++i) {
+          const float4 x = out[q + i];
+          float y = __uint_as_float(w[0][i]) * ((T0 & 1) && C::TURNS ? x.y : x.x);
+          if (C::TURNS) y = fmaf(__uint_as_float(w[1][i]), g.tiles == 1 ? 0.f : (T0 & 1) ? x.x : x.y, y);
+          uint8_t* const at = to + (uint64_t(__float_as_uint(x.w)) << 32 | __float_as_uint(x.z));
+          const bool on = q + i < g.rows && w4 * 32 < D;
+          if (on && whole) *reinterpret_cast<__nv_bfloat16*>(at) = __float2bfloat16_rn(y);
+          if (on && !whole) *reinterpret_cast<float*>(at) = y;
         }
-        __syncwarp();
       }
+      ++s;
+      T0 += g.tiles;
     }
   }
 
   ptx::tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) atomicOr(err, kErrTimeout | int(*abort_flag - 1u) << 9);
   if (warp == kWarpO) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, 512);
@@ -839,19 +941,15 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_tree_join_kernel(const 
   const int head = i % a.num_heads, row = (i / a.num_heads) * p.G + head % p.G;
   const int U = mine ? tiles_of(r) : 0;
   // the line before this (sequence, head, tile of rows); the division is the other kernel's
-  const TreeUnits<N> units{p, false};
   int all = 0, first = 0;
-#pragma unroll 4
-  for (int s = lane; s < a.cache.batch; s += 32) {
-    const int n = units(s);
-    all += n;
-    first += s < b ? n : 0;
+#pragma unroll 1
+  for (int x = 2 * lane; x < a.cache.batch; x += 64) {
+    const int n0 = units_of<N>(p, x), n1 = units_of<N>(p, x + 1);
+    all += n0 + n1;
+    first += (x < b ? n0 : 0) + (x + 1 < b ? n1 : 0);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    all += __shfl_xor_sync(0xffffffffu, all, o);
-    first += __shfl_xor_sync(0xffffffffu, first, o);
-  }
+  all = __reduce_add_sync(0xffffffffu, all);
+  first = __reduce_add_sync(0xffffffffu, first);
   if (mine) first += (head / p.G * row_tiles(r, p.G, N) + row / N) * U;
   const int piece = tree_share(all, p);
   const int c0 = first / piece, c1 = (first + U - 1) / piece;
