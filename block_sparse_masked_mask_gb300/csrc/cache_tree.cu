@@ -43,8 +43,6 @@
 namespace attnmask {
 namespace {
 
-constexpr int kTreeThreads = 512;
-constexpr int kWarpConvert = 8, kWarpPages = 12, kWarpS = 13, kWarpO = 14, kWarpLine = 15;
 constexpr int kNoPage = INT_MIN, kFar = 1;  // of a block of 16 tokens, as in cache_chunk.cu
 constexpr int kTreeSms = 152;
 constexpr float kNoReference = -0x1p100f;   // of a row that has seen nothing yet
@@ -131,9 +129,17 @@ struct WideTile {
 template <int D, int N>
 struct TreeCfg {
   using P = WideTile<N, kTile>;
+  // Warpgroups of the softmax, and the warps behind them
+  static constexpr int GROUPS = N == 128 ? 4 : 2, THREADS = 128 * GROUPS + 256;
+  static constexpr int CONVERT = 4 * GROUPS, PAGES = CONVERT + 4, ISSUE_S = PAGES + 1, ISSUE_O = PAGES + 2, LINE = PAGES + 3;
+  // Registers for each thread of the softmax, the conversion and the others: of what the launch
+  // has for all (128 with 512 threads, 80 with 768)
+  static constexpr int REG_SOFTMAX = N == 128 ? 88 : 168, REG_CONVERT = N == 128 ? 72 : 104, REG_OTHERS = N == 128 ? 56 : 72;
+  static_assert(GROUPS * REG_SOFTMAX + REG_CONVERT + REG_OTHERS == (GROUPS + 2) * (N == 128 ? 80 : 128), "registers");
   static constexpr int KT = CodeTile<D>::BYTES;   // a tile of codes
   static constexpr int QT = 2 * N * D;            // queries: hi, lo
-  static constexpr bool TURNS = N <= 64;          // the warpgroups of the softmax take tiles in turn, or half the rows each
+  static constexpr bool TURNS = N <= 64;          // the warpgroups of the softmax take tiles in turn, or a part of the rows each
+  static constexpr int ROWS = TURNS ? N : N / GROUPS;  // of a warpgroup
   static constexpr int NQ = N == 128 ? 1 : 2;
   static constexpr int NB = N <= 32 ? 3 : 2;      // of scores and of weights
   static constexpr int NO = N == 128 ? 1 : 2;     // segments' O
@@ -145,10 +151,10 @@ struct TreeCfg {
   static constexpr int OFF_R = OFF_K + NK * KT;
   static constexpr int OFF_SCL = OFF_R + NR * KT;          // as in cache_chunk.cu
   static constexpr int OFF_ROWS = OFF_SCL + NSCL * 8 * 16; // [2][N]: the rows' factors
-  static constexpr int OFF_MAX = OFF_ROWS + 2 * N * 4;     // [2][4 warps][rows of a warpgroup]: maxima, then sums
-  static constexpr int OFF_REF = OFF_MAX + 8 * N * 4;      // [2][N]: negative references
-  static constexpr int OFF_MOVE = OFF_REF + 2 * N * 4;     // [8 warps][rows of a warpgroup]: negative reference, half the factor's exponent
-  static constexpr int OFF_OUT = OFF_MOVE + 8 * (TURNS ? N : N / 2) * 8;      // [N]: factors of the two warpgroups' O, place in the outputs
+  static constexpr int OFF_MAX = OFF_ROWS + 2 * N * 4;     // [warpgroup][4 warps][ROWS]: maxima, then sums
+  static constexpr int OFF_REF = OFF_MAX + GROUPS * 4 * ROWS * 4;  // [warpgroup][ROWS]: negative references
+  static constexpr int OFF_MOVE = OFF_REF + GROUPS * ROWS * 4;     // [warp][ROWS]: negative reference, half the factor's exponent
+  static constexpr int OFF_OUT = OFF_MOVE + GROUPS * 4 * ROWS * 8;      // [N]: factors of the two warpgroups' O, place in the outputs
   static constexpr int OFF_SEG = OFF_OUT + N * 16;
   static constexpr int OFF_BAR = OFF_SEG + NSEG * 48;
   static constexpr int B_SEGFULL = 0, B_SEGFREE = B_SEGFULL + NSEG, B_QFULL = B_SEGFREE + NSEG, B_QFREE = B_QFULL + 2,
@@ -157,17 +163,17 @@ struct TreeCfg {
                        B_SCLFREE = B_SCLFULL + NSCL, B_SFULL = B_SCLFREE + NSCL, B_PFULL = B_SFULL + NB,
                        B_PDONE = B_PFULL + NB, B_OFREE = B_PDONE + NB, B_USED = B_OFREE + NO,
                        B_DRAIN = B_USED + 2, NBAR = B_DRAIN + 2;
-  static_assert(NBAR <= kTreeThreads, "a thread for each");
+  static_assert(NBAR <= THREADS, "a thread for each");
   __device__ static int arrivals(int i) {
-    return i >= B_USED ? (i >= B_DRAIN ? 1 : 8)
-           : i >= B_OFREE ? 8
-           : i >= B_PFULL ? (i >= B_PDONE ? 1 : TURNS ? 4 : 8)
-           : i >= B_SCLFREE ? (i >= B_SFULL ? 1 : 4 + (TURNS ? 4 : 8))  // value and softmax warps
+    constexpr int ALL = 4 * GROUPS, EACH = TURNS ? 4 : ALL;  // warps of the softmax, and of those with a tile
+    return i >= B_OFREE ? (i >= B_DRAIN ? 1 : ALL)
+           : i >= B_PFULL ? (i >= B_PDONE ? 1 : EACH)
+           : i >= B_SCLFREE ? (i >= B_SFULL ? 1 : 4 + EACH)  // value and softmax warps
            : i >= B_SCLFULL ? 1
            : i >= B_VFULL ? (i >= B_VFREE ? 1 : 4)
            : i >= B_RFREE ? 4
            : i >= B_QFULL ? (i >= B_QFREE ? 1 : 4)
-           : i >= B_SEGFREE ? 15 : 1;  // the warps 0 to 14
+           : i >= B_SEGFREE ? LINE : 1;  // the warps before that one
   }
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int USED = OFF_MISC + 16 + 1024;        // the base is aligned to 1024
@@ -180,7 +186,7 @@ struct TreeCfg {
 };
 
 template <int D, int N>
-__global__ void __launch_bounds__(kTreeThreads, 1)
+__global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
     cache_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ TreeParams p) {
   using C = TreeCfg<D, N>;
@@ -205,7 +211,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     ptx::fence_mbar_init();
   }
   if (threadIdx.x == 0) *abort_flag = 0u;
-  if (warp == kWarpO) {
+  if (warp == C::ISSUE_O) {
     ptx::tmem_alloc(ptx::smem_addr(misc), 512);
     ptx::tmem_relinquish();
   }
@@ -229,11 +235,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     return true;
   };
 
-  // Registers: of the launch's 128 for each thread the softmax takes 168, the conversion 104,
-  // the others 72.  (Set in each branch: where they meet, the least would hold for all.)
-  if (warp >= kWarpPages) {
-   ptx::regs_dec<72>();
-   if (warp == kWarpLine) {
+  // (the registers are split in each branch: where they meet, the least would hold for all)
+  if (warp >= C::PAGES) {
+   ptx::regs_dec<C::REG_OTHERS>();
+   if (warp == C::LINE) {
     // -------------------------------------------------------------- segments
     // 64 sequences at a time, two neighbours per lane
     int total = 0;
@@ -320,7 +325,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (load_rows(a.cu, a.lens, x, a.total_tokens, a.max_new, a.max_seqlen, err, r) && r.len < r.n) atomicOr(err, kErrHeld);
       }
     }
-  } else if (warp == kWarpPages) {
+  } else if (warp == C::PAGES) {
     // -------------------------------------------------------------- pages, scales, codes
     // Eight lanes a tile, one per 16 tokens: lanes 8 q .. 8 q + 7 look up the q-th
     // tile of four.  Page numbers are read two fours ahead, scales one.
@@ -402,7 +407,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == kWarpS) {
+  } else if (warp == C::ISSUE_S) {
     // -------------------------------------------------------------- S^T issuer
     if (lane == 0) {
       constexpr uint32_t IDESC = ptx::idesc_e4m3_f32(128, N);
@@ -472,10 +477,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     }
     __syncwarp();
    }
-  } else if (warp >= kWarpConvert) {
-    ptx::regs_dec<104>();
+  } else if (warp >= C::CONVERT) {
+    ptx::regs_dec<C::REG_CONVERT>();
     // -------------------------------------------------------------- queries, values
-    const int ct = threadIdx.x - kWarpConvert * 32, cw = warp - kWarpConvert;
+    const int ct = threadIdx.x - C::CONVERT * 32, cw = warp - C::CONVERT;
     Segment g;
     int T = 0;
     bool ok = true;
@@ -566,24 +571,24 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       }
     }
   } else {
-    ptx::regs_inc<168>();
+    ptx::regs_inc<C::REG_SOFTMAX>();
     // -------------------------------------------------------------- softmax
     // A warp takes 32 tokens, in two blocks of 16 (of one page each); of a block, lane
     // 4 g + i holds tokens g and g + 8 and rows 8 k + 2 i, + 1.  Up to 64 rows the warpgroups
     // take tiles in turn, each with references, sums and O of its own, which meet at a
     // segment's end: what a tile costs besides its scores (waits, the vote) is then paid
-    // by each for every other one.  Of 128 rows each takes half.
+    // by each for every other one.  Of 128 rows each of four takes a quarter.
     // The weights are formed and stored before the vote on the references; a tile whose
     // references move repeats them.
-    constexpr int ROWS = C::TURNS ? N : N / 2, K = ROWS / 8, KL = K < 4 ? K : 4, STRIDE = C::TURNS ? 2 : 1;
+    constexpr int ROWS = C::ROWS, K = ROWS / 8, KL = N == 128 || K < 4 ? 2 : 4, STRIDE = C::TURNS ? 2 : 1;
     const int wg = warp >> 2, w4 = warp & 3, g4 = lane >> 2, i4 = lane & 3;
     const int row_base = C::TURNS ? 0 : wg * ROWS;
     const uint32_t lanes = tmem + (uint32_t(w4 * 32) << 16);
     float* const warps = reinterpret_cast<float*>(sbase + C::OFF_MAX) + wg * 4 * ROWS;  // [warp][row]: maxima, then sums
     float* const refs = reinterpret_cast<float*>(sbase + C::OFF_REF);                   // [warpgroup][row]
     float4* const out = reinterpret_cast<float4*>(sbase + C::OFF_OUT);
-    auto meet = [&](bool x) { return wg == 0 ? ptx::named_barrier_or(1, 128, x) : ptx::named_barrier_or(2, 128, x); };
-    auto meet_all = [&](bool x) { return C::TURNS ? ptx::named_barrier_or(3, 256, x) : meet(x); };
+    auto meet = [&](bool x) { return ptx::named_barrier_or(1 + wg, 128, x); };
+    auto meet_all = [&](bool x) { return C::TURNS ? ptx::named_barrier_or(5, 256, x) : meet(x); };
     // Scores of this warp's tokens to -inf where the row does not see the token, for which
     // `see` of the token's lane has no bit.  In tensor memory, and rolled up: few tiles have any, and
     // the loop over the others is the faster for being short.
@@ -845,9 +850,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (g4 == 0 && w4 == 0) *reinterpret_cast<float2*>(refs + wg * ROWS + 8 * k + 2 * i4) = m2[k];
       }
       if (meet_all(!ok)) break;
+      constexpr int OUT = N / C::GROUPS;  // rows that a warpgroup writes
       const bool whole = g.slot < 0;
-      const int tid = w4 * 32 + lane, row = (C::TURNS ? wg * N / 2 : row_base) + tid;  // of the tile, for the first N / 2 threads
-      if (tid < N / 2) {
+      const int tid = w4 * 32 + lane, row = wg * OUT + tid;  // of the tile, for the first OUT threads
+      if (tid < OUT) {
         float m = -INFINITY, sum = 0.f, part[2] = {0.f, 0.f};
         const float* const all = reinterpret_cast<const float*>(sbase + C::OFF_MAX);
         if constexpr (C::TURNS) {
@@ -891,12 +897,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       const uint32_t o_other = o_seg + (C::TURNS ? uint32_t(((T0 + (g.tiles > 1)) & 1) * N) : 0u);
       uint8_t* const to = (whole ? static_cast<uint8_t*>(a.o) : reinterpret_cast<uint8_t*>(p.part_o)) + tid * (whole ? 2 : 4);
 #pragma unroll 1
-      for (int q = first; q < first + N / 2; q += 4) {
+      for (int q = first; q < first + OUT; q += 4) {
         uint32_t w[2][4];
         ptx::tmem_ld4(o_mine + q, w[0]);
         if (C::TURNS) ptx::tmem_ld4(o_other + q, w[1]);
         ptx::tmem_wait_ld();
-        if (q + 4 == first + N / 2) {
+        if (q + 4 == first + OUT) {
           ptx::tc_fence_before();
           warp_arrive(bar(C::B_OFREE + s % C::NO), lane);
         }
@@ -919,7 +925,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0 && *abort_flag) atomicOr(err, kErrTimeout | int(*abort_flag - 1u) << 9);
-  if (warp == kWarpO) {
+  if (warp == C::ISSUE_O) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, 512);
   }
@@ -975,7 +981,7 @@ attn_status launch_dn(TreeParams& p, cudaStream_t s) {
     return record_cuda_error(cudaErrorInvalidValue, "attn_cache_tree_fwd tensor map encoding");
   cudaError_t e = cudaFuncSetAttribute(cache_tree_kernel<D, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return record_cuda_error(e, "attn_cache_tree_fwd configure");
-  cache_tree_kernel<D, N><<<unsigned(p.ctas), kTreeThreads, C::SMEM, s>>>(map, map_v, p);
+  cache_tree_kernel<D, N><<<unsigned(p.ctas), C::THREADS, C::SMEM, s>>>(map, map_v, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return record_cuda_error(e, "attn_cache_tree_fwd launch");
   // One warp or a CTA joins a row, as in cache_attn.cu.
