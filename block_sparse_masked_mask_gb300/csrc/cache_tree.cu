@@ -185,6 +185,12 @@ struct TreeCfg {
   static_assert(V + 2 * 64 <= 512, "tensor memory");
 };
 
+// 8 K columns of 16 tokens' scores.
+template <int K>
+__device__ __forceinline__ void load_scores(uint32_t taddr, uint32_t (&v)[4 * K]) {
+  ptx::tmem_ld16x256(taddr, v);
+}
+
 template <int D, int N>
 __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
     cache_tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -580,7 +586,7 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
     // by each for every other one.  Of 128 rows each of four takes a quarter.
     // The weights are formed and stored before the vote on the references; a tile whose
     // references move repeats them.
-    constexpr int ROWS = C::ROWS, K = ROWS / 8, KL = N == 128 || K < 4 ? 2 : 4, STRIDE = C::TURNS ? 2 : 1;
+    constexpr int ROWS = C::ROWS, K = ROWS / 8, STRIDE = C::TURNS ? 2 : 1;
     const int wg = warp >> 2, w4 = warp & 3, g4 = lane >> 2, i4 = lane & 3;
     const int row_base = C::TURNS ? 0 : wg * ROWS;
     const uint32_t lanes = tmem + (uint32_t(w4 * 32) << 16);
@@ -686,41 +692,40 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
         // The weights under the present references, into shared memory, and the largest of
         // their base-2 logarithms.
         auto weigh = [&]() {
-          constexpr int PIECES = 2 * K / KL;  // (the next one is on its way while one is worked on)
-          uint32_t v[2][4 * KL];
-          auto load = [&](int i) {
-            ptx::tmem_ld16x256(s_col + (uint32_t(16 * (i / (K / KL))) << 16) + uint32_t(8 * KL * (i % (K / KL))), v[i & 1]);
-          };
-          load(0);
           top = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < PIECES; ++i) {
-            const int z = i / (K / KL), k0 = i % (K / KL) * KL;
+          for (int k = 0; k < K; ++k) lt[k] = make_float2(0.f, 0.f);
+          // (rolled up: the second block's instructions are still at hand)
+#pragma unroll 1
+          for (int z = 0; z < 2; ++z) {
+            const uint32_t s_at = s_col + (uint32_t(16 * z) << 16);
+            uint32_t v[4 * K];
+            load_scores<K>(s_at, v);
+            const float2 ks = z ? make_float2(of[1].x, of[1].x) : make_float2(of[0].x, of[0].x);
+            const float2 x = z ? make_float2(of[1].y, of[1].y) : make_float2(of[0].y, of[0].y);
+            const float2 inv = z ? make_float2(of[1].z, of[1].z) : make_float2(of[0].z, of[0].z);
             ptx::tmem_wait_ld();
-            if (i + 1 < PIECES) load(i + 1);
-            const float2 ks = make_float2(of[z].x, of[z].x), x = make_float2(of[z].y, of[z].y);
-            const float2 inv = make_float2(of[z].z, of[z].z);
-            uint32_t pk[2 * KL];
 #pragma unroll
-            for (int kk = 0; kk < KL; ++kk) {
-              const int k = k0 + kk;
-              const float2 by = factor(f2[k], ks), at = ptx::fadd2(m2[k], x);
-              float2 y[2];  // of tokens g and g + 8
+            for (int k0 = 0; k0 < K; k0 += 2) {
+              uint32_t pk[4];
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const uint32_t* const w = v[i & 1] + 4 * kk + 2 * e;
-                y[e] = ptx::ffma2(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), by, at);
-                top = ptx::fmax3(top, y[e].x, y[e].y);
-                y[e] = make_float2(ptx::ex2(y[e].x), ptx::ex2(y[e].y));
-                pk[2 * kk + e] = pack_half2(y[e].x, y[e].y);
+              for (int kk = 0; kk < 2; ++kk) {
+                const int k = k0 + kk;
+                const float2 by = factor(f2[k], ks), at = ptx::fadd2(m2[k], x);
+                float2 y[2];  // of tokens g and g + 8
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const uint32_t* const w = v + 4 * k + 2 * e;
+                  y[e] = ptx::ffma2(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), by, at);
+                  top = ptx::fmax3(top, y[e].x, y[e].y);
+                  y[e] = make_float2(ptx::ex2(y[e].x), ptx::ex2(y[e].y));
+                  pk[2 * kk + e] = pack_half2(y[e].x, y[e].y);
+                }
+                lt[k] = ptx::ffma2(ptx::fadd2(y[0], y[1]), inv, lt[k]);
               }
-              const float2 sum = ptx::fadd2(y[0], y[1]);
-              lt[k] = z == 0 ? ptx::fmul2(sum, inv) : ptx::ffma2(sum, inv, lt[k]);
+              // (the 16 tokens of the second block are 16 rows on, whatever the swizzle)
+              ptx::stmatrix(weights + C::P::unit(to_token, to_unit + k0) + z * 16 * C::P::ROWB, pk[0], pk[1], pk[2], pk[3]);
             }
-#pragma unroll
-            for (int kk = 0; kk < KL; kk += 2)
-              ptx::stmatrix(weights + C::P::unit(to_token + 16 * z, to_unit + k0 + kk), pk[2 * kk], pk[2 * kk + 1],
-                            pk[2 * kk + 2], pk[2 * kk + 3]);
           }
         };
 #pragma unroll 1
