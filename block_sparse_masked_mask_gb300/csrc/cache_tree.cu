@@ -130,12 +130,12 @@ template <int D, int N>
 struct TreeCfg {
   using P = WideTile<N, kTile>;
   // Warpgroups of the softmax, and the warps behind them
-  static constexpr int GROUPS = N == 128 ? 4 : 2, THREADS = 128 * GROUPS + 256;
+  static constexpr int GROUPS = 2, THREADS = 128 * GROUPS + 256;
   static constexpr int CONVERT = 4 * GROUPS, PAGES = CONVERT + 4, ISSUE_S = PAGES + 1, ISSUE_O = PAGES + 2, LINE = PAGES + 3;
   // Registers for each thread of the softmax, the conversion and the others: of what the launch
   // has for all (128 with 512 threads, 80 with 768)
-  static constexpr int REG_SOFTMAX = N == 128 ? 88 : 168, REG_CONVERT = N == 128 ? 72 : 104, REG_OTHERS = N == 128 ? 56 : 72;
-  static_assert(GROUPS * REG_SOFTMAX + REG_CONVERT + REG_OTHERS == (GROUPS + 2) * (N == 128 ? 80 : 128), "registers");
+  static constexpr int REG_SOFTMAX = 168, REG_CONVERT = 104, REG_OTHERS = 72;
+  static_assert(GROUPS * REG_SOFTMAX + REG_CONVERT + REG_OTHERS == (GROUPS + 2) * 128, "registers");
   static constexpr int KT = CodeTile<D>::BYTES;   // a tile of codes
   static constexpr int QT = 2 * N * D;            // queries: hi, lo
   static constexpr bool TURNS = N <= 64;          // the warpgroups of the softmax take tiles in turn, or a part of the rows each
@@ -184,12 +184,6 @@ struct TreeCfg {
   static constexpr int S = 0, O = NB * N, OSEG = TURNS ? 2 * N : N, V = O + NO * OSEG;
   static_assert(V + 2 * 64 <= 512, "tensor memory");
 };
-
-// 8 K columns of 16 tokens' scores.
-template <int K>
-__device__ __forceinline__ void load_scores(uint32_t taddr, uint32_t (&v)[4 * K]) {
-  ptx::tmem_ld16x256(taddr, v);
-}
 
 template <int D, int N>
 __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
@@ -687,20 +681,18 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
              (T < C::NB || tree_warp_wait(bar(C::B_PDONE + f), uint32_t(T / C::NB - 1) & 1u, abort_flag, 19));
         ptx::tc_fence_after();
         if (__builtin_expect(masked, 0)) hide(s_col, see);
-        float2 lt[K];  // the tile's sums
+        float2 lt[K];  // the sums with this tile's
         float top;
-        // The weights under the present references, into shared memory, and the largest of
-        // their base-2 logarithms.
+        // The weights under the present references, into shared memory, and the largest sum of two.
         auto weigh = [&]() {
-          top = -INFINITY;
+          top = 0.f;
 #pragma unroll
-          for (int k = 0; k < K; ++k) lt[k] = make_float2(0.f, 0.f);
+          for (int k = 0; k < K; ++k) lt[k] = l2[k];
           // (rolled up: the second block's instructions are still at hand)
 #pragma unroll 1
           for (int z = 0; z < 2; ++z) {
-            const uint32_t s_at = s_col + (uint32_t(16 * z) << 16);
             uint32_t v[4 * K];
-            load_scores<K>(s_at, v);
+            ptx::tmem_ld16x256(s_col + (uint32_t(16 * z) << 16), v);
             const float2 ks = z ? make_float2(of[1].x, of[1].x) : make_float2(of[0].x, of[0].x);
             const float2 x = z ? make_float2(of[1].y, of[1].y) : make_float2(of[0].y, of[0].y);
             const float2 inv = z ? make_float2(of[1].z, of[1].z) : make_float2(of[0].z, of[0].z);
@@ -717,11 +709,12 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
                 for (int e = 0; e < 2; ++e) {
                   const uint32_t* const w = v + 4 * k + 2 * e;
                   y[e] = ptx::ffma2(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), by, at);
-                  top = ptx::fmax3(top, y[e].x, y[e].y);
                   y[e] = make_float2(ptx::ex2(y[e].x), ptx::ex2(y[e].y));
                   pk[2 * kk + e] = pack_half2(y[e].x, y[e].y);
                 }
-                lt[k] = ptx::ffma2(ptx::fadd2(y[0], y[1]), inv, lt[k]);
+                const float2 sum = ptx::fadd2(y[0], y[1]);
+                top = ptx::fmax3(top, sum.x, sum.y);
+                lt[k] = ptx::ffma2(sum, inv, lt[k]);
               }
               // (the 16 tokens of the second block are 16 rows on, whatever the swizzle)
               ptx::stmatrix(weights + C::P::unit(to_token, to_unit + k0) + z * 16 * C::P::ROWB, pk[0], pk[1], pk[2], pk[3]);
@@ -733,9 +726,9 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
           // (the first tile sets the references)
           if (j >= STRIDE || moved) {
             weigh();
-            if (__builtin_expect(moved || !meet(!ok || top > kMostWeight), 1)) break;
+            if (__builtin_expect(moved || !meet(!ok || top > 0x1p15f), 1)) break;
           }
-          // a weight would pass 2^15 (or a wait ran out): the references of such rows move
+          // two weights together pass 2^15 (or a wait ran out): references move where one may have
 #pragma unroll 2
           for (int k = 0; k < K; ++k) {
             uint32_t v[2][4];
@@ -775,7 +768,7 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
             for (int x = lane; x < ROWS; x += 32) {
               const float now = fmaxf(fmaxf(warps[x], warps[ROWS + x]), fmaxf(warps[2 * ROWS + x], warps[3 * ROWS + x]));
               const float was = j >= STRIDE ? -move[x].x : kNoReference;
-              const bool raise = now > was + kMostWeight;
+              const bool raise = now > was + (kMostWeight - 1.f);
               move[x] = make_float2(raise ? kTopWeight - now : -was, raise ? half_factor(was, now - kTopWeight) : 1.f);
             }
           }
@@ -832,7 +825,7 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
         __syncwarp();
         if (lane == 0 && !dry) ptx::mbar_arrive(bar(C::B_PFULL + f));
 #pragma unroll
-        for (int k = 0; k < K; ++k) l2[k] = ptx::fadd2(l2[k], lt[k]);
+        for (int k = 0; k < K; ++k) l2[k] = lt[k];
         if (j + STRIDE < g.tiles) ok = scales(T + STRIDE);
       }
       if (dry) {
