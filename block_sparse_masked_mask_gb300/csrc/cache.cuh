@@ -95,10 +95,10 @@ struct TreeBuildArgs {
   CacheView cache;
 };
 
-struct TreeAttnArgs {
-  CacheQueryArgs a;
+// Which nodes of its tree a node sees: a row of `words` words per new token.
+struct TreeMasks {
   const uint32_t* bits;
-  int words;
+  int64_t words;
 };
 
 struct TreeKeepArgs {
@@ -149,14 +149,17 @@ attn_status launch_cache_append_rope(const AppendArgs& a, const int32_t* positio
                                      cudaStream_t s);
 uint64_t cache_fwd_workspace(const CacheView& c, int total_tokens, int num_heads, int max_new, int max_seqlen);
 attn_status launch_cache_fwd(const CacheQueryArgs& a, cudaStream_t s);
-attn_status launch_cache_chunk(const CacheAttnParams& p, cudaStream_t s);
+attn_status launch_cache_chunk(const CacheAttnParams& p, const TreeMasks* tree, cudaStream_t s);
 attn_status launch_cache_weights(const CacheQueryArgs& a, cudaStream_t s);
 attn_status launch_cache_weights_many(const CacheQueryArgs& a, int sms, cudaStream_t s);
 attn_status launch_cache_evict(const EvictArgs& a, cudaStream_t s);
 attn_status launch_tree_build(const TreeBuildArgs& a, cudaStream_t s);
 attn_status launch_tree_keep(const TreeKeepArgs& a, cudaStream_t s);
 uint64_t cache_tree_workspace(const CacheView& c, int total_tokens, int num_heads, int max_new, int max_seqlen);
-attn_status launch_cache_tree(const TreeAttnArgs& t, cudaStream_t s);
+attn_status launch_cache_tree(const CacheQueryArgs& a, const TreeMasks& tree, cudaStream_t s);
+// The same by the kernel of many rows.
+uint64_t cache_tree_many_workspace(const CacheView& c, int total_tokens, int num_heads, int max_new, int max_seqlen);
+attn_status launch_cache_tree_many(const CacheQueryArgs& a, const TreeMasks& tree, cudaStream_t s);
 
 // ---------------------------------------------------------------- device side
 

@@ -400,24 +400,22 @@ attn_status attn_cache_tree_fwd(const void* q, void* o, float* lse, attn_dtype d
                                 const int32_t* cu_seqlens, int32_t max_new, const int32_t* seq_lens,
                                 int32_t max_seqlen, const attn_kv_cache* cache, void* workspace,
                                 size_t workspace_bytes, attn_stream_t stream) {
-  TreeAttnArgs t;
-  std::memset(&t, 0, sizeof(t));
+  CacheQueryArgs a;
+  std::memset(&a, 0, sizeof(a));
   const attn_status st = check_queries(q, lse, dtype, total_tokens, num_heads, scale, cu_seqlens, max_new, seq_lens,
-                                       max_seqlen, ATTN_MASK_NONE, cache, &t.a);
+                                       max_seqlen, ATTN_MASK_NONE, cache, &a);
   if (st != ATTN_OK) return st;
   if ((total_tokens > 0 && !o) || !aligned(o, 16)) return ATTN_ERR_INVALID_ARG;
   if (tree_words < 0 || int64_t(tree_words) * 32 < max_new || !aligned(tree_bits, 4)) return ATTN_ERR_INVALID_ARG;
   if (total_tokens > 0 && max_new > 0 && !tree_bits) return ATTN_ERR_INVALID_ARG;
-  const uint64_t need = cache_tree_workspace(t.a.cache, total_tokens, num_heads, t.a.max_new, max_seqlen);
+  const uint64_t need = cache_tree_workspace(a.cache, total_tokens, num_heads, a.max_new, max_seqlen);
   if (need > 0 && (workspace == nullptr || !aligned(workspace, 256))) return ATTN_ERR_INVALID_ARG;
   if (uint64_t(workspace_bytes) < need) return ATTN_ERR_WORKSPACE_TOO_SMALL;
   if (total_tokens == 0 || max_new == 0) return ATTN_OK;
-  t.a.o = o;
-  t.a.lse = lse;
-  t.a.workspace = static_cast<float*>(workspace);
-  t.bits = tree_bits;
-  t.words = tree_words;
-  return launch_cache_tree(t, reinterpret_cast<cudaStream_t>(stream));
+  a.o = o;
+  a.lse = lse;
+  a.workspace = static_cast<float*>(workspace);
+  return launch_cache_tree(a, TreeMasks{tree_bits, tree_words}, reinterpret_cast<cudaStream_t>(stream));
 }
 
 attn_status attn_cache_tree_keep(const int32_t* path, int32_t path_stride, const int32_t* counts,

@@ -79,8 +79,7 @@ __device__ __forceinline__ bool tree_warp_wait(uint32_t bar, uint32_t parity, vo
 
 struct TreeParams {
   CacheQueryArgs a;
-  const uint32_t* bits;
-  int words;
+  TreeMasks tree;
   int G;
   int ctas, least;  // least: tiles of a CTA's piece
   float scale_log2;
@@ -669,7 +668,7 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
             const int node = token - text, first = g.row0 + row_base, last = min(first + ROWS, g.row0 + g.rows);
 #pragma unroll 4
             for (int i = first / p.G; i < (last + p.G - 1) / p.G; ++i) {
-              const uint32_t bit = __ldg(p.bits + int64_t(g.q0 + i) * p.words + (node >> 5)) >> (node & 31) & 1u;
+              const uint32_t bit = __ldg(p.tree.bits + (g.q0 + i) * p.tree.words + (node >> 5)) >> (node & 31) & 1u;
               const int from = max(i * p.G - first, 0), to = min((i + 1) * p.G, last) - first;  // of this warpgroup's
               const uint64_t span = (to >= 64 ? ~0ull : (1ull << to) - 1) & ~((1ull << from) - 1);
               see |= bit ? span : 0ull;
@@ -963,12 +962,15 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_tree_join_kernel(const 
   join_row<D, W>(p, c1 - c0 + 1, at, r.q0 + i / a.num_heads, head, w, lane, shared);
 }
 
-// Rows of a tile: the least that takes them all, or 128.
-int tile_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
-
-uint64_t partial_rows(const CacheView& c, int num_heads, int max_new) {
-  return 2ull * kTreeSms * tile_rows(int64_t(max_new) * (num_heads / c.heads));
+// Rows are padded to the least of these; 0: cache_chunk.cu takes them, 128 or 256 rows of a
+// sequence and head at a time (16 sequences of 8192 tokens, 8 heads, here / there: 16 rows 54 / 64 us, 32
+// 60 / 100, 64 70 / 108; in tiles of 128 rows, 128 112 / 121, 256 203 / 181; 32 of 1024 to 16384, 68 to 128
+// rows 196 / 159: with that many rows, the ones that pad them out cost more than is saved).
+int padded_rows(const CacheView& c, int num_heads, int max_new) {
+  const int64_t rows = int64_t(max_new) * (num_heads / c.heads);
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 0;
 }
+uint64_t partial_rows(int N) { return 2ull * kTreeSms * N; }
 
 template <int D, int N>
 attn_status launch_dn(TreeParams& p, cudaStream_t s) {
@@ -1004,31 +1006,32 @@ attn_status launch_d(TreeParams& p, int N, cudaStream_t s) {
   switch (N) {
     case 16: return launch_dn<D, 16>(p, s);
     case 32: return launch_dn<D, 32>(p, s);
-    case 64: return launch_dn<D, 64>(p, s);
-    default: return launch_dn<D, 128>(p, s);
+    default: return launch_dn<D, 64>(p, s);
   }
 }
 
 }  // namespace
 
 uint64_t cache_tree_workspace(const CacheView& c, int total_tokens, int num_heads, int max_new, int max_seqlen) {
-  if (total_tokens == 0 || max_new == 0 || max_seqlen == 0) return 0;
-  return partial_rows(c, num_heads, max_new) * (uint64_t(c.head_dim) * 4 + 8);
+  if (total_tokens == 0 || max_new == 0) return 0;
+  const int N = padded_rows(c, num_heads, max_new);
+  if (N == 0) return cache_tree_many_workspace(c, total_tokens, num_heads, max_new, max_seqlen);
+  return partial_rows(N) * (uint64_t(c.head_dim) * 4 + 8);
 }
 
-attn_status launch_cache_tree(const TreeAttnArgs& t, cudaStream_t s) {
+attn_status launch_cache_tree(const CacheQueryArgs& a, const TreeMasks& tree, cudaStream_t s) {
+  const int N = padded_rows(a.cache, a.num_heads, a.max_new);
+  if (N == 0) return launch_cache_tree_many(a, tree, s);
   TreeParams p;
-  p.a = t.a;
-  p.bits = t.bits;
-  p.words = t.words;
-  p.G = t.a.num_heads / t.a.cache.heads;
+  p.a = a;
+  p.tree = tree;
+  p.G = a.num_heads / a.cache.heads;
   p.ctas = kTreeSms;
   p.least = 1;
-  p.scale_log2 = t.a.scale * 1.4426950408889634f;
-  const int N = tile_rows(int64_t(t.a.max_new) * p.G);
-  p.part_o = t.a.workspace;
-  p.part_m = reinterpret_cast<float2*>(t.a.workspace + partial_rows(t.a.cache, t.a.num_heads, t.a.max_new) * t.a.cache.head_dim);
-  switch (t.a.cache.head_dim) {
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.part_o = a.workspace;
+  p.part_m = reinterpret_cast<float2*>(a.workspace + partial_rows(N) * a.cache.head_dim);
+  switch (a.cache.head_dim) {
     case 32: return launch_d<32>(p, N, s);
     case 64: return launch_d<64>(p, N, s);
     default: return launch_d<128>(p, N, s);
