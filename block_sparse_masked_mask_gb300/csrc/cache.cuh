@@ -143,10 +143,10 @@ struct EvictArgs {
   CacheView src, dst;
 };
 
-attn_status launch_rope(const RopeArgs& a, const attn_rope_plan& plan, cudaStream_t s, const RopeCheck* check = nullptr);
+attn_status launch_rope(const RopeArgs& a, const attn_rope_plan& plan, cudaStream_t s);
 attn_status launch_cache_append(const AppendArgs& a, cudaStream_t s);
-attn_status launch_cache_append_rope(const AppendArgs& a, const int32_t* positions, const attn_rope_plan& plan,
-                                     cudaStream_t s);
+// (q.num_heads may be 0)
+attn_status launch_cache_append_rope(const AppendArgs& kv, const RopeArgs& q, const attn_rope_plan& plan, cudaStream_t s);
 uint64_t cache_fwd_workspace(const CacheView& c, int total_tokens, int num_heads, int max_new, int max_seqlen);
 attn_status launch_cache_fwd(const CacheQueryArgs& a, cudaStream_t s);
 attn_status launch_cache_chunk(const CacheAttnParams& p, const TreeMasks* tree, cudaStream_t s);

@@ -352,6 +352,10 @@ attn_status attn_cache_append_rope(const void* q, void* q_out, int64_t q_stride,
   if (st != ATTN_OK) return st;
   if (plan->rotary_dim > cache->head_dim || !aligned(positions, 4)) return ATTN_ERR_INVALID_ARG;
   if (num_heads > kMaxHeads) return ATTN_ERR_UNSUPPORTED;
+  // a launch's blocks fit 31 bits
+  if ((int64_t(total_tokens) / cache->page_size + 2ll * cache->batch) * 2 * cache->num_kv_heads +
+          int64_t(total_tokens) * (num_heads + 1) / 8 > INT_MAX)
+    return ATTN_ERR_UNSUPPORTED;
   const uintptr_t size = dtype == ATTN_DTYPE_BF16 ? 2 : 4;
   if (num_heads > 0 && total_tokens > 0) {
     if (!q || !q_out || !aligned(q, size) || !aligned(q_out, size)) return ATTN_ERR_INVALID_ARG;
@@ -361,26 +365,21 @@ attn_status attn_cache_append_rope(const void* q, void* q_out, int64_t q_stride,
       return ATTN_ERR_INVALID_ARG;
   }
   if (total_tokens == 0 || max_new == 0) return ATTN_OK;
-  if (num_heads > 0) {
-    RopeArgs r;
-    std::memset(&r, 0, sizeof(r));
-    r.q = q;
-    r.q_out = q_out;
-    r.q_stride = q_stride;
-    r.q_out_stride = q_out_stride;
-    r.num_heads = num_heads;
-    r.total_tokens = total_tokens;
-    r.head_dim = cache->head_dim;
-    r.batch = cache->batch;
-    r.positions = positions;
-    r.cu = cu_seqlens;
-    r.lens = seq_lens;
-    r.bf16 = dtype == ATTN_DTYPE_BF16;
-    const RopeCheck check{a.max_new, cache->max_pages * cache->page_size, cache->status};
-    st = launch_rope(r, *plan, reinterpret_cast<cudaStream_t>(stream), &check);
-    if (st != ATTN_OK) return st;
-  }
-  return launch_cache_append_rope(a, positions, *plan, reinterpret_cast<cudaStream_t>(stream));
+  RopeArgs r;
+  std::memset(&r, 0, sizeof(r));
+  r.q = q;
+  r.q_out = q_out;
+  r.q_stride = q_stride;
+  r.q_out_stride = q_out_stride;
+  r.num_heads = num_heads;
+  r.total_tokens = total_tokens;
+  r.head_dim = cache->head_dim;
+  r.batch = cache->batch;
+  r.positions = positions;
+  r.cu = cu_seqlens;
+  r.lens = seq_lens;
+  r.bf16 = a.bf16;
+  return launch_cache_append_rope(a, r, *plan, reinterpret_cast<cudaStream_t>(stream));
 }
 
 attn_status attn_cache_tree_fwd_workspace_size(const attn_kv_cache* cache, int32_t total_tokens, int32_t num_heads,

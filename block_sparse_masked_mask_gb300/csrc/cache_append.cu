@@ -13,8 +13,6 @@
 // for 14000 tokens of 16 heads.)  The pages of all
 // sequences form one line (cache_rows.cuh), a CTA per page, so that ragged
 // batches launch few empty CTAs.
-#include <type_traits>
-
 #include "cache_rows.cuh"
 
 namespace attnmask {
@@ -24,21 +22,17 @@ constexpr int kAppendThreads = 256;
 constexpr int kChunk = 8;   // elements of one access
 constexpr int kChunks = 8;  // accesses per thread
 
-__device__ __forceinline__ float to_float(float x) { return x; }
-__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-
 // Eight elements (a chunk) in shared memory: 16-byte piece p of a thread's j-th
 // chunk at ((j * PIECES + p) * kAppendThreads + thread) * 16.
 template <typename T>
 struct Chunk {
   static constexpr int PIECES = sizeof(T) * kChunk / 16;
   static constexpr int SMEM = kChunks * PIECES * kAppendThreads * 16;
-  __device__ static void get(const uint8_t* smem, int j, float (&f)[kChunk]) { get(smem, j, threadIdx.x, f); }
-  __device__ static void get(const uint8_t* smem, int j, int thread, float (&f)[kChunk]) {
+  __device__ static void get(const uint8_t* smem, int j, float (&f)[kChunk]) {
     uint32_t w[4 * PIECES];
 #pragma unroll
     for (int p = 0; p < PIECES; ++p) {
-      const uint4 v = *reinterpret_cast<const uint4*>(smem + ((j * PIECES + p) * kAppendThreads + thread) * 16);
+      const uint4 v = *reinterpret_cast<const uint4*>(smem + ((j * PIECES + p) * kAppendThreads + threadIdx.x) * 16);
       w[4 * p] = v.x; w[4 * p + 1] = v.y; w[4 * p + 2] = v.z; w[4 * p + 3] = v.w;
     }
 #pragma unroll
@@ -48,58 +42,6 @@ struct Chunk {
     }
   }
 };
-
-// The keys' rotation on their way into the cache.
-struct NoTurn {};
-struct Turn {
-  const int32_t* positions;  // of the packed tokens, or NULL
-  int rot;
-  bool interleaved;
-  float factor;
-  uint64_t turn[ATTN_ROPE_MAX_PAIRS];
-};
-
-// The rotated elements of a chunk, dimensions d .. d + 7 of a token whose (cos, sin) are at
-// `cs`.  A partner rot / 2 dimensions away is in the chunk of another thread of the team.
-template <typename T>
-__device__ __forceinline__ void turned(const uint8_t* smem, int j, int d, const Turn& p, const float2* cs,
-                                       float (&f)[kChunk]) {
-  using C = Chunk<T>;
-  C::get(smem, j, f);
-  if (d >= p.rot) return;
-  if (p.interleaved) {
-#pragma unroll
-    for (int e = 0; e < kChunk; e += 2) {
-      if (d + e >= p.rot) continue;
-      const float2 c = cs[(d + e) / 2];
-      const float x = f[e], y = f[e + 1];
-      f[e] = x * c.x - y * c.y;
-      f[e + 1] = y * c.x + x * c.y;
-    }
-    return;
-  }
-  const int half = p.rot / 2;
-  if (half % kChunk == 0) {
-    const bool low = d < half;
-    float other[kChunk];
-    C::get(smem, j, threadIdx.x + (low ? half : -half) / kChunk, other);
-    cs += low ? d : d - half;
-#pragma unroll
-    for (int e = 0; e < kChunk; ++e) f[e] = low ? f[e] * cs[e].x - other[e] * cs[e].y : f[e] * cs[e].x + other[e] * cs[e].y;
-    return;
-  }
-#pragma unroll
-  for (int e = 0; e < kChunk; ++e) {
-    if (d + e >= p.rot) continue;
-    const bool low = d + e < half;
-    const int at = d + e + (low ? half : -half), by = (at & -kChunk) - d;  // the partner, its chunk less this one
-    const float y = to_float(reinterpret_cast<const T*>(smem)[
-        ((j * C::PIECES + at % kChunk * int(sizeof(T)) / 16) * kAppendThreads + int(threadIdx.x) + by / kChunk) * (16 / int(sizeof(T))) +
-        at % (16 / int(sizeof(T)))]);
-    const float2 c = cs[low ? d + e : d + e - half];
-    f[e] = low ? f[e] * c.x - y * c.y : f[e] * c.x + y * c.y;
-  }
-}
 
 // Pages that a sequence's new tokens touch.
 struct NewPages {
@@ -120,11 +62,9 @@ struct NewPages {
 // CTAs per SM: bf16 six (36.0 us for those 14000 tokens; five, as the compiler would have
 // it, 36.9, seven 38.4); fp32 three, as many as its 64 KB of shared memory each allow
 // (the same tokens 68.8 us, floor 40; held to the registers of six 69.8).
-template <typename T, typename P>
-__global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 4 ? 3 : 6)
-    append_kernel(const __grid_constant__ AppendArgs a, int team_log2, const __grid_constant__ P turn) {
+template <typename T>
+__global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 4 ? 3 : 6) append_kernel(const AppendArgs a, int team_log2) {
   using C = Chunk<T>;
-  constexpr bool kTurn = !std::is_same<P, NoTurn>::value;
   extern __shared__ __align__(16) uint8_t smem[];
   const CacheView& c = a.cache;
   const NewPages pages{a, blockIdx.x == 0 && blockIdx.y == 0};
@@ -169,32 +109,11 @@ __global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 4 ? 3 : 6)
   }
   uint8_t* codes = (values ? c.v_pages : c.k_pages) + ((int64_t(number) * c.heads + h) << c.page_log2) * c.head_dim;
   float* scale = (values ? c.v_scale : c.k_scale) + int64_t(number) * c.heads + h;
-  float2* const cs = reinterpret_cast<float2*>(smem + C::SMEM);  // [new slot][pair]
-  if constexpr (kTurn) {
-    const int pairs = turn.rot / 2;
-    for (int x = threadIdx.x; x < (last - first) * pairs; x += kAppendThreads) {
-      const int token = (i << c.page_log2) + first + x / pairs, pair = x % pairs;  // of the sequence
-      const int at = turn.positions ? turn.positions[q0 + token - held] : token;
-      const int64_t angle = int64_t(uint64_t(int64_t(at)) * turn.turn[pair]);
-      float sn, cn;
-      sincospif(float(int32_t(angle >> 32)) * 0x1p-31f, &sn, &cn);
-      cs[x] = make_float2(cn * turn.factor, sn * turn.factor);
-    }
-  }
-  auto get = [&](int j, float (&f)[kChunk]) {
-    if constexpr (kTurn) {
-      const int ch = (j << team_log2) + tid, slot = ch / per_row;
-      if (!values && slot >= first && slot < last)
-        return turned<T>(smem, j, (ch % per_row) * kChunk, turn, cs + (slot - first) * (turn.rot / 2), f);
-    }
-    C::get(smem, j, f);
-  };
   asm volatile("cp.async.wait_all;" ::: "memory");
-  if constexpr (kTurn) __syncthreads();  // partners and angles are other threads'
 #pragma unroll
   for (int j = 0; j < kChunks; ++j) {
     float f[kChunk];
-    get(j, f);
+    C::get(smem, j, f);
 #pragma unroll
     for (int e = 0; e < kChunk; ++e) {
       const float m = fabsf(f[e]);
@@ -233,7 +152,7 @@ __global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 4 ? 3 : 6)
     const int slot = ch / per_row;
     if (slot < first || slot >= last) continue;
     float f[kChunk];
-    get(j, f);
+    C::get(smem, j, f);
     uint2 w;
     w.x = e4m3_pair(f[0] * inv, f[1] * inv) | (e4m3_pair(f[2] * inv, f[3] * inv) << 16);
     w.y = e4m3_pair(f[4] * inv, f[5] * inv) | (e4m3_pair(f[6] * inv, f[7] * inv) << 16);
@@ -242,8 +161,8 @@ __global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 4 ? 3 : 6)
   if (tid == 0) *scale = pow2f(e);
 }
 
-template <typename T, typename P>
-cudaError_t launch_t(const AppendArgs& a, const P& turn, int pairs, cudaStream_t s) {
+template <typename T>
+cudaError_t launch_t(const AppendArgs& a, cudaStream_t s) {
   const int page_size = 1 << a.cache.page_log2;
   int team_log2 = 5;  // threads of a team: a page's elements, 64 each
   while ((kChunks * kChunk << team_log2) < page_size * a.cache.head_dim) ++team_log2;
@@ -254,30 +173,18 @@ cudaError_t launch_t(const AppendArgs& a, const P& turn, int pairs, cudaStream_t
   const int64_t most = a.total_tokens / page_size + 2ll * a.cache.batch;
   const int64_t pages = each * a.cache.batch < most ? each * a.cache.batch : most;
   const dim3 grid(unsigned(pages), unsigned((2 * a.cache.heads + teams - 1) / teams));
-  const int smem = Chunk<T>::SMEM + (page_size < a.max_new ? page_size : a.max_new) * pairs * int(sizeof(float2));
-  const cudaError_t e = cudaFuncSetAttribute(append_kernel<T, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e =
+      cudaFuncSetAttribute(append_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, Chunk<T>::SMEM);
   if (e != cudaSuccess) return e;
-  append_kernel<T, P><<<grid, kAppendThreads, smem, s>>>(a, team_log2, turn);
+  append_kernel<T><<<grid, kAppendThreads, Chunk<T>::SMEM, s>>>(a, team_log2);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 attn_status launch_cache_append(const AppendArgs& a, cudaStream_t s) {
-  const cudaError_t e = a.bf16 ? launch_t<__nv_bfloat16>(a, NoTurn{}, 0, s) : launch_t<float>(a, NoTurn{}, 0, s);
+  const cudaError_t e = a.bf16 ? launch_t<__nv_bfloat16>(a, s) : launch_t<float>(a, s);
   return e == cudaSuccess ? ATTN_OK : record_cuda_error(e, "attn_cache_append launch");
-}
-
-attn_status launch_cache_append_rope(const AppendArgs& a, const int32_t* positions, const attn_rope_plan& plan,
-                                     cudaStream_t s) {
-  Turn t;
-  t.positions = positions;
-  t.rot = plan.rotary_dim;
-  t.interleaved = plan.interleaved != 0;
-  t.factor = plan.result_factor;
-  for (int i = 0; i < ATTN_ROPE_MAX_PAIRS; ++i) t.turn[i] = plan.turn[i];
-  const cudaError_t e = a.bf16 ? launch_t<__nv_bfloat16>(a, t, t.rot / 2, s) : launch_t<float>(a, t, t.rot / 2, s);
-  return e == cudaSuccess ? ATTN_OK : record_cuda_error(e, "attn_cache_append_rope launch");
 }
 
 }  // namespace attnmask

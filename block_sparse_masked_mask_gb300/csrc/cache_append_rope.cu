@@ -1,0 +1,315 @@
+// Rotation and append in one launch: queries are turned (rope.cuh), new keys are turned
+// and become e4m3 codes, new values become codes (cache_append.cu).
+//
+// The queries are most of the bytes, 4 per element against 3 of a key or value, and
+// none of them waits for a page; so the launch has two kinds of CTAs.  The first ones take
+// pages: their lookups, one behind the other, then go on under the stream of the rotated
+// queries, the others' work.
+// Pages: a team of threads owns the new tokens of one page and head, staged once in shared
+// memory; the CTA's teams take different heads and share the sines and cosines of the
+// page's tokens, a table in shared memory.  A team turns its keys twice, for their
+// largest magnitude and for their codes, from the raw elements: kept in between
+// in 32 bits they would take twice the room.  A key goes from fp32 to its code without a
+// rounding to bf16 between.
+// Loops are rolled up: all of a call's CTAs run their code once or a few times, and what
+// has to be fetched first costs more than what is executed (cache_tree.cu).
+#include <type_traits>
+
+#include "cache_rows.cuh"
+#include "rope.cuh"
+
+namespace attnmask {
+namespace {
+
+constexpr int kThreads = 32 * kRopeWarps;
+constexpr int kPiece = 8;    // elements of a chunk, a thread's unit
+constexpr int kPieces = 8;   // chunks of a thread, at most
+
+struct AppendRopeParams {
+  RopeParams rope;  // of the queries; the keys' too
+  AppendArgs kv;
+  bool interleaved;
+  int team_log2, pieces;   // threads of a team, chunks of each
+  int groups, key_groups;  // CTAs of a page: those of its keys, then of its values
+  int loops;               // heads that a team takes in turn
+  int page_ctas;
+};
+
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// Eight elements in shared memory: 16-byte part p of a thread's j-th chunk at
+// ((j * PARTS + p) * kThreads + thread) * 16.
+template <typename T>
+struct Staged {
+  static constexpr int PARTS = sizeof(T) * kPiece / 16, PER = 16 / sizeof(T);
+  __device__ static int at(int j, int thread, int e) {  // element e, in elements
+    return ((j * PARTS + e / PER) * kThreads + thread) * PER + e % PER;
+  }
+  __device__ static void get(const T* staged, int j, int thread, float (&f)[kPiece]) {
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) {
+      const uint4 v = *reinterpret_cast<const uint4*>(staged + at(j, thread, p * PER));
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < PER; ++e) {
+        if constexpr (sizeof(T) == 4) f[p * PER + e] = __uint_as_float(w[e]);
+        else f[p * PER + e] = __uint_as_float(e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
+      }
+    }
+  }
+  // The same turned: dimensions d .. d + 7 of a token whose (cos, sin) are at `cs`.  A partner
+  // half the rotated dimensions away lies in the chunk of another thread of the team.
+  __device__ static void turned(const T* staged, int j, int d, int rot, bool interleaved, const float2* cs,
+                                float (&f)[kPiece]) {
+    get(staged, j, threadIdx.x, f);
+    if (d >= rot) return;
+    const int half = rot / 2;
+    if (interleaved) {
+#pragma unroll
+      for (int e = 0; e < kPiece; e += 2) {
+        if (d + e >= rot) continue;
+        const float2 c = cs[(d + e) / 2];
+        const float x = f[e], y = f[e + 1];
+        f[e] = x * c.x - y * c.y;
+        f[e + 1] = y * c.x + x * c.y;
+      }
+    } else if (half % kPiece == 0) {
+      const bool low = d < half;
+      float other[kPiece];
+      get(staged, j, int(threadIdx.x) + (low ? half : -half) / kPiece, other);
+      cs += low ? d : d - half;
+#pragma unroll
+      for (int e = 0; e < kPiece; ++e)
+        f[e] = low ? f[e] * cs[e].x - other[e] * cs[e].y : f[e] * cs[e].x + other[e] * cs[e].y;
+    } else {
+#pragma unroll
+      for (int e = 0; e < kPiece; ++e) {
+        if (d + e >= rot) continue;
+        const bool low = d + e < half;
+        const int to = d + e + (low ? half : -half);
+        const float y = to_float(staged[at(j, int(threadIdx.x) + ((to & -kPiece) - d) / kPiece, to % kPiece)]);
+        const float2 c = cs[low ? d + e : d + e - half];
+        f[e] = low ? f[e] * c.x - y * c.y : f[e] * c.x + y * c.y;
+      }
+    }
+  }
+};
+
+// Pages that sequence b's new tokens touch; 0 where its numbers cannot be used.
+__device__ __forceinline__ int new_pages(const AppendArgs& a, int b) {
+  const CacheView& c = a.cache;
+  if (b >= c.batch) return 0;
+  const int q0 = a.cu[b], q1 = a.cu[b + 1], len = a.lens[b], n = q1 - q0;
+  const bool good = q0 >= 0 && q1 > q0 && q1 <= a.total_tokens && (b > 0 || q0 == 0) && n <= a.max_new && len >= n &&
+                    len <= c.max_pages << c.page_log2;
+  return good ? ((len - 1) >> c.page_log2) - ((len - n) >> c.page_log2) + 1 : 0;
+}
+
+template <typename T>
+__device__ __forceinline__ void append_pages(const AppendRopeParams& p) {
+  using S = Staged<T>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float warp_max[kRopeWarps];
+  const AppendArgs& a = p.kv;
+  const CacheView& c = a.cache;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int pos = blockIdx.x / p.groups, group = blockIdx.x % p.groups;
+  // what is wrong with the sequences is noted by one warp that has little else to do
+  if (blockIdx.x == p.page_ctas - 1 && warp == 0) {
+#pragma unroll 1
+    for (int x = lane; x < c.batch; x += 32) {
+      SeqRows r;
+      if (load_rows(a.cu, a.lens, x, a.total_tokens, a.max_new, c.max_pages << c.page_log2, c.status, r) && r.len < r.n)
+        atomicOr(c.status, kErrHeld);
+    }
+  }
+  // the sequence that this page of the line belongs to, 64 at a time, two neighbours per lane
+  int b = 0, before = 0;
+#pragma unroll 1
+  while (true) {
+    if (b >= c.batch) return;
+    const int n0 = new_pages(a, b + 2 * lane), n1 = new_pages(a, b + 2 * lane + 1);
+    int sum = n0 + n1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += y;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, before + sum > pos);
+    if (past) {
+      const int at = __ffs(past) - 1;
+      before += __shfl_sync(0xffffffffu, sum - n0 - n1, at);
+      const int skip = __shfl_sync(0xffffffffu, n0, at);
+      b += 2 * at;
+      if (before + skip <= pos) {
+        before += skip;
+        ++b;
+      }
+      break;
+    }
+    before += __shfl_sync(0xffffffffu, sum, 31);
+    b += 64;
+  }
+  const int q0 = a.cu[b], len = a.lens[b], held = len - (a.cu[b + 1] - q0);
+  const int i = (held >> c.page_log2) + pos - before;  // this CTA's page of the sequence
+  const int start = i << c.page_log2;                  // its first token
+  const int first = max(held - start, 0), last = min(len - start, 1 << c.page_log2);  // slots [first, last) are new
+  const int number = __ldg(c.table + int64_t(b) * c.max_pages + i);  // needed only behind the loads
+  const int row_log2 = 31 - __clz(c.head_dim / kPiece), mask = (1 << row_log2) - 1;  // chunks of a token
+  const int team = threadIdx.x >> p.team_log2, tid = threadIdx.x & ((1 << p.team_log2) - 1), teams = kThreads >> p.team_log2;
+  const bool keys = group < p.key_groups;
+  const int head0 = (keys ? group : group - p.key_groups) * p.loops * teams + team;
+  const int fill = ((last - first) << row_log2);                         // chunks of a head
+  const int turns = (fill + (1 << p.team_log2) - 1) >> p.team_log2;      // of the team
+  const T* src = static_cast<const T*>(keys ? a.k : a.v);
+  const int64_t stride = keys ? a.k_stride : a.v_stride;
+  T* const staged = reinterpret_cast<T*>(smem);
+  float2* const cs = reinterpret_cast<float2*>(smem + p.pieces * S::PARTS * kThreads * 16);  // [new slot][pair]
+  const int pairs = p.rope.rot / 2;
+  const bool fine = in_pool(c, number);
+
+#pragma unroll 1
+  for (int l = 0; l < p.loops; ++l) {
+    const int h = head0 + l * teams;
+    const bool on = h < c.heads;
+    if (l > 0) __syncthreads();  // the last head's elements have been read
+#pragma unroll 1
+    for (int j = 0; j < turns; ++j) {
+      const int ch = (j << p.team_log2) + tid;
+      const bool here = on && ch < fill;
+      const T* from = src + (here ? (q0 + start + first - held + (ch >> row_log2)) * stride + int64_t(h) * c.head_dim + (ch & mask) * kPiece : 0);
+#pragma unroll
+      for (int x = 0; x < S::PARTS; ++x)
+        copy16_async(uint32_t(__cvta_generic_to_shared(staged + S::at(j, threadIdx.x, x * S::PER))), from + x * S::PER, here);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (l == 0 && keys) {
+      // 64 threads a token, four tokens at a time
+      const int pair = threadIdx.x & 63;
+#pragma unroll 1
+      for (int x = threadIdx.x >> 6; x < last - first; x += kThreads / 64) {
+        const int at = p.rope.a.positions ? p.rope.a.positions[q0 + start + first - held + x] : start + first + x;
+        if (pair >= pairs) continue;
+        const int64_t turn = int64_t(uint64_t(int64_t(at)) * p.rope.turn[pair]);
+        float sn, cn;
+        sincospif(float(int32_t(turn >> 32)) * 0x1p-31f, &sn, &cn);
+        cs[x * pairs + pair] = make_float2(cn * p.rope.factor, sn * p.rope.factor);
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();  // partners and angles are other threads'
+    if (!fine) {
+      if (threadIdx.x == 0) atomicOr(c.status, kErrBadPage);
+      return;
+    }
+    const int64_t at = int64_t(number) * c.heads + (on ? h : 0);
+    uint8_t* const codes = (keys ? c.k_pages : c.v_pages) + (at << c.page_log2) * c.head_dim;
+    float* const scale = (keys ? c.k_scale : c.v_scale) + at;
+    auto get = [&](int j, float (&f)[kPiece]) {
+      const int ch = (j << p.team_log2) + tid;
+      if (keys && ch < fill) S::turned(staged, j, (ch & mask) * kPiece, p.rope.rot, p.interleaved, cs + (ch >> row_log2) * pairs, f);
+      else S::get(staged, j, threadIdx.x, f);
+    };
+    float amax = 0.f;
+#pragma unroll 1
+    for (int j = 0; j < turns; ++j) {
+      float f[kPiece];
+      get(j, f);
+#pragma unroll
+      for (int e = 0; e < kPiece; ++e) {
+        const float m = fabsf(f[e]);
+        if (m < INFINITY) amax = fmaxf(amax, m);  // false for NaN too
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if (lane == 0) warp_max[warp] = amax;
+    const float was = first > 0 ? *scale : 0.f;  // read before the team's first thread replaces it
+    __syncthreads();
+    const int warps = 1 << (p.team_log2 - 5);  // of the team
+    for (int w = 0; w < warps; ++w) amax = fmaxf(amax, warp_max[team * warps + w]);
+    int e = scale_exponent(amax);
+    if (first > 0) {
+      // a scale outside the range (the caller's memory) is taken into it
+      const int e0 = max(kScaleExpMin, min(kScaleExpMax, exponent_of(was)));
+      if (e0 < e && on) {
+        const int bytes = first * c.head_dim;  // codes of the earlier tokens
+#pragma unroll 1
+        for (int x = tid * 8; x < bytes; x += 8 << p.team_log2) {
+          uint2 w = *reinterpret_cast<uint2*>(codes + x);
+          w.x = rescale4(w.x, e - e0);
+          w.y = rescale4(w.y, e - e0);
+          *reinterpret_cast<uint2*>(codes + x) = w;
+        }
+      }
+      e = max(e, e0);
+    }
+    const float inv = pow2f(-e);
+#pragma unroll 1
+    for (int j = 0; j < turns; ++j) {
+      const int ch = (j << p.team_log2) + tid;
+      if (!on || ch >= fill) break;
+      float f[kPiece];
+      get(j, f);
+      uint2 w;
+      w.x = e4m3_pair(f[0] * inv, f[1] * inv) | (e4m3_pair(f[2] * inv, f[3] * inv) << 16);
+      w.y = e4m3_pair(f[4] * inv, f[5] * inv) | (e4m3_pair(f[6] * inv, f[7] * inv) << 16);
+      *reinterpret_cast<uint2*>(codes + int64_t((first << row_log2) + ch) * kPiece) = w;
+    }
+    if (tid == 0 && on) *scale = pow2f(e);
+  }
+}
+
+template <typename WAY>
+__global__ void __launch_bounds__(kThreads, sizeof(typename WAY::T) == 4 ? 3 : 4)
+    append_rope_kernel(const __grid_constant__ AppendRopeParams p) {
+  if (int(blockIdx.x) < p.page_ctas) append_pages<typename WAY::T>(p);
+  else WAY::run(p.rope, int(blockIdx.x) - p.page_ctas);
+}
+
+template <typename T>
+cudaError_t launch_t(AppendRopeParams& p, cudaStream_t s) {
+  const AppendArgs& a = p.kv;
+  const CacheView& c = a.cache;
+  const int page_size = 1 << c.page_log2, most = a.max_new < page_size ? a.max_new : page_size;  // new tokens of a page
+  p.team_log2 = 5;
+  while ((kPieces * kPiece << p.team_log2) < most * c.head_dim) ++p.team_log2;
+  p.pieces = (most * c.head_dim / kPiece + (1 << p.team_log2) - 1) >> p.team_log2;
+  const int teams = kThreads >> p.team_log2;
+  // n tokens touch at most (n + page_size - 2) / page_size + 1 pages; all of them
+  // together at most T / page_size whole ones and two more per sequence
+  const int64_t each = (int64_t(a.max_new) + page_size - 2) / page_size + 1;
+  const int64_t bound = a.total_tokens / page_size + 2ll * c.batch;
+  const int64_t pages = each * c.batch < bound ? each * c.batch : bound;
+  // Heads in turn share a table of angles; as many as leave eight CTAs for each SM.
+  p.loops = 1;
+  while (p.loops * teams < c.heads && pages * ((c.heads + 2 * p.loops * teams - 1) / (2 * p.loops * teams)) * 2 >= 8 * 152) p.loops *= 2;
+  p.key_groups = (c.heads + p.loops * teams - 1) / (p.loops * teams);
+  p.groups = 2 * p.key_groups;
+  p.page_ctas = int(pages * p.groups);
+  const int smem = p.pieces * Staged<T>::PARTS * kThreads * 16 + most * (p.rope.rot / 2) * int(sizeof(float2));
+  auto launch = [&](auto way, int64_t ctas) {
+    auto kernel = append_rope_kernel<decltype(way)>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<unsigned(p.page_ctas + ctas), kThreads, smem, s>>>(p);
+    return cudaGetLastError();
+  };
+  if (p.rope.a.num_heads == 0) return launch(RopeWay<T, 0, 4, true>{}, 0);
+  return with_way<T, true>(p.rope, p.interleaved, launch);
+}
+
+}  // namespace
+
+attn_status launch_cache_append_rope(const AppendArgs& kv, const RopeArgs& q, const attn_rope_plan& plan, cudaStream_t s) {
+  AppendRopeParams p;
+  p.rope = rope_params(q, plan);
+  p.rope.check = RopeCheck{kv.max_new, kv.cache.max_pages << kv.cache.page_log2, kv.cache.status};
+  p.kv = kv;
+  p.interleaved = plan.interleaved != 0;
+  const cudaError_t e = kv.bf16 ? launch_t<__nv_bfloat16>(p, s) : launch_t<float>(p, s);
+  return e == cudaSuccess ? ATTN_OK : record_cuda_error(e, "attn_cache_append_rope launch");
+}
+
+}  // namespace attnmask
