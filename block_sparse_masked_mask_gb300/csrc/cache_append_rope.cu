@@ -2,8 +2,8 @@
 // and become e4m3 codes, new values become codes (cache_append.cu).
 //
 // The queries are most of the bytes, 4 per element against 3 of a key or value, and
-// none of them waits for a page; so the launch has two kinds of CTAs.  The first ones take
-// pages: their lookups, one behind the other, then go on under the stream of the rotated
+// none of them waits for a page; so the launch has two kinds of CTAs, in turn: those that
+// take pages have their lookups, one behind the other, under the stream of the rotated
 // queries, the others' work.
 // Pages: a team of threads owns the new tokens of one page and head, staged once in shared
 // memory; the CTA's teams take different heads and share the sines and cosines of the
@@ -23,7 +23,7 @@ namespace {
 
 constexpr int kThreads = 32 * kRopeWarps;
 constexpr int kPiece = 8;    // elements of a chunk, a thread's unit
-constexpr int kPieces = 8;   // chunks of a thread, at most
+constexpr int kPieces = 4;   // chunks of a thread, while a team has room to grow
 
 struct AppendRopeParams {
   RopeParams rope;  // of the queries; the keys' too
@@ -71,8 +71,8 @@ struct Staged {
         if (d + e >= rot) continue;
         const float2 c = cs[(d + e) / 2];
         const float x = f[e], y = f[e + 1];
-        f[e] = x * c.x - y * c.y;
-        f[e + 1] = y * c.x + x * c.y;
+        f[e] = turned_x(x, y, c);
+        f[e + 1] = turned_y(x, y, c);
       }
     } else if (half % kPiece == 0) {
       const bool low = d < half;
@@ -81,7 +81,7 @@ struct Staged {
       cs += low ? d : d - half;
 #pragma unroll
       for (int e = 0; e < kPiece; ++e)
-        f[e] = low ? f[e] * cs[e].x - other[e] * cs[e].y : f[e] * cs[e].x + other[e] * cs[e].y;
+        f[e] = low ? turned_x(f[e], other[e], cs[e]) : turned_y(other[e], f[e], cs[e]);
     } else {
 #pragma unroll
       for (int e = 0; e < kPiece; ++e) {
@@ -90,7 +90,7 @@ struct Staged {
         const int to = d + e + (low ? half : -half);
         const float y = to_float(staged[at(j, int(threadIdx.x) + ((to & -kPiece) - d) / kPiece, to % kPiece)]);
         const float2 c = cs[low ? d + e : d + e - half];
-        f[e] = low ? f[e] * c.x - y * c.y : f[e] * c.x + y * c.y;
+        f[e] = low ? turned_x(f[e], y, c) : turned_y(y, f[e], c);
       }
     }
   }
@@ -107,16 +107,16 @@ __device__ __forceinline__ int new_pages(const AppendArgs& a, int b) {
 }
 
 template <typename T>
-__device__ __forceinline__ void append_pages(const AppendRopeParams& p) {
+__device__ __forceinline__ void append_pages(const AppendRopeParams& p, int block) {
   using S = Staged<T>;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float warp_max[kRopeWarps];
   const AppendArgs& a = p.kv;
   const CacheView& c = a.cache;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int pos = blockIdx.x / p.groups, group = blockIdx.x % p.groups;
+  const int pos = block / p.groups, group = block % p.groups;
   // what is wrong with the sequences is noted by one warp that has little else to do
-  if (blockIdx.x == p.page_ctas - 1 && warp == 0) {
+  if (block == p.page_ctas - 1 && warp == 0) {
 #pragma unroll 1
     for (int x = lane; x < c.batch; x += 32) {
       SeqRows r;
@@ -187,11 +187,12 @@ __device__ __forceinline__ void append_pages(const AppendRopeParams& p) {
     if (l == 0 && keys) {
       // 64 threads a token, four tokens at a time
       const int pair = threadIdx.x & 63;
+      const uint64_t theta = p.rope.turn[min(pair, pairs - 1)];
 #pragma unroll 1
       for (int x = threadIdx.x >> 6; x < last - first; x += kThreads / 64) {
         const int at = p.rope.a.positions ? p.rope.a.positions[q0 + start + first - held + x] : start + first + x;
         if (pair >= pairs) continue;
-        const int64_t turn = int64_t(uint64_t(int64_t(at)) * p.rope.turn[pair]);
+        const int64_t turn = int64_t(uint64_t(int64_t(at)) * theta);
         float sn, cn;
         sincospif(float(int32_t(turn >> 32)) * 0x1p-31f, &sn, &cn);
         cs[x * pairs + pair] = make_float2(cn * p.rope.factor, sn * p.rope.factor);
@@ -264,8 +265,12 @@ __device__ __forceinline__ void append_pages(const AppendRopeParams& p) {
 template <typename WAY>
 __global__ void __launch_bounds__(kThreads, sizeof(typename WAY::T) == 4 ? 3 : 4)
     append_rope_kernel(const __grid_constant__ AppendRopeParams p) {
-  if (int(blockIdx.x) < p.page_ctas) append_pages<typename WAY::T>(p);
-  else WAY::run(p.rope, int(blockIdx.x) - p.page_ctas);
+  // one of each kind in turn, then the rest of the longer kind
+  const int x = blockIdx.x, pages = p.page_ctas, rows = int(gridDim.x) - pages, both = 2 * min(pages, rows);
+  const bool page = x < both ? (x & 1) == 0 : pages > rows;
+  const int mine = x < both ? x >> 1 : x - both / 2;
+  if (page) append_pages<typename WAY::T>(p, mine);
+  else WAY::run(p.rope, mine);
 }
 
 template <typename T>
@@ -274,7 +279,7 @@ cudaError_t launch_t(AppendRopeParams& p, cudaStream_t s) {
   const CacheView& c = a.cache;
   const int page_size = 1 << c.page_log2, most = a.max_new < page_size ? a.max_new : page_size;  // new tokens of a page
   p.team_log2 = 5;
-  while ((kPieces * kPiece << p.team_log2) < most * c.head_dim) ++p.team_log2;
+  while (p.team_log2 < 8 && (kPieces * kPiece << p.team_log2) < most * c.head_dim) ++p.team_log2;
   p.pieces = (most * c.head_dim / kPiece + (1 << p.team_log2) - 1) >> p.team_log2;
   const int teams = kThreads >> p.team_log2;
   // n tokens touch at most (n + page_size - 2) / page_size + 1 pages; all of them

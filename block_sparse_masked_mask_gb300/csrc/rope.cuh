@@ -70,6 +70,11 @@ __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float
 __device__ __forceinline__ void from_f(float& d, float x) { d = x; }
 __device__ __forceinline__ void from_f(__nv_bfloat16& d, float x) { d = __float2bfloat16_rn(x); }
 
+// A turned pair, c = (cos, sin), with the roundings fixed: what goes into the cache does not depend on
+// how it was read.
+__device__ __forceinline__ float turned_x(float x, float y, float2 c) { return __fmaf_rn(x, c.x, -__fmul_rn(y, c.y)); }
+__device__ __forceinline__ float turned_y(float x, float y, float2 c) { return __fmaf_rn(y, c.x, __fmul_rn(x, c.y)); }
+
 // The position of row t and whether it has one.  CHECKED: only rows of sequences that
 // an append would use have one, positions given or not.
 template <bool CHECKED>
@@ -182,8 +187,8 @@ __device__ __forceinline__ void rope_rows(const RopeParams& p, int block_of_jobs
             T* py = INTER ? (2 * e + 1 < VP ? &x[j].x[2 * e + 1] : &y[j].x[2 * e + 1 - VP]) : &y[j].x[e];
             if (PART && u * VP + e >= p.rot / 2) continue;  // copied
             const float fx = to_f(*px), fy = to_f(*py);
-            from_f(*px, fx * c[e].x - fy * c[e].y);
-            from_f(*py, fy * c[e].x + fx * c[e].y);
+            from_f(*px, CHECKED ? turned_x(fx, fy, c[e]) : fx * c[e].x - fy * c[e].y);
+            from_f(*py, CHECKED ? turned_y(fx, fy, c[e]) : fy * c[e].x + fx * c[e].y);
           }
         }
         T* dst = i < a.num_heads ? qo + i * a.head_dim : ko + (i - a.num_heads) * a.head_dim;
@@ -244,7 +249,10 @@ __device__ __forceinline__ void rope_halves(const RopeParams& p, int block_of_jo
 #pragma unroll
       for (int e = 0; e < W; ++e) {
         y.x[e] = x[j].x[e];
-        if (d0 + e < p.rot) from_f(y.x[e], to_f(x[j].x[e]) * c[e].x + to_f(copy[from[e]]) * c[e].y);
+        if (d0 + e < p.rot) {
+          const float a = to_f(x[j].x[e]), b = to_f(copy[from[e]]);
+          from_f(y.x[e], CHECKED ? turned_y(b, a, c[e]) : a * c[e].x + b * c[e].y);
+        }
       }
       if (i < last) store_vec(i < a.num_heads ? qo + i * a.head_dim : ko + (i - a.num_heads) * a.head_dim, y);
       load(j, i + kRopeUnroll * per_pass);
