@@ -5,14 +5,11 @@
 // none of them waits for a page; so the launch has two kinds of CTAs, in turn: those that
 // take pages have their lookups, one behind the other, under the stream of the rotated
 // queries, the others' work.
-// Pages: a team of threads owns the new tokens of one page and head, staged once in shared
-// memory; the CTA's teams take different heads and share the sines and cosines of the
-// page's tokens, a table in shared memory.  A team turns its keys twice, for their
-// largest magnitude and for their codes, from the raw elements: kept in between
-// in 32 bits they would take twice the room.  A key goes from fp32 to its code without a
-// rounding to bf16 between.
-// Loops are rolled up: all of a call's CTAs run their code once or a few times, and what
-// has to be fetched first costs more than what is executed (cache_tree.cu).
+// Pages: a team of threads owns the new tokens of one page and head, staged in shared
+// memory, since a key's partner may be another thread's; the CTA's teams take different heads and
+// share the sines and cosines of the page's tokens, a table in shared memory.  The turned
+// elements stay in registers, 32 bits each, for their largest magnitude and their codes, so that
+// a key goes from fp32 to its code without a rounding to bf16 between.
 #include <type_traits>
 
 #include "cache_rows.cuh"
@@ -114,9 +111,40 @@ __device__ __forceinline__ void append_pages(const AppendRopeParams& p, int bloc
   const AppendArgs& a = p.kv;
   const CacheView& c = a.cache;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ int found[2], place[128];  // place: the new tokens' positions
   const int pos = block / p.groups, group = block % p.groups;
-  // what is wrong with the sequences is noted by one warp that has little else to do
-  if (block == p.page_ctas - 1 && warp == 0) {
+  if (warp == 0) {
+    // the sequence that this page of the line belongs to, 64 at a time, two neighbours per lane
+    int b = 0, before = 0;
+#pragma unroll 1
+    for (; b < c.batch; b += 64) {
+      const int n0 = new_pages(a, b + 2 * lane), n1 = new_pages(a, b + 2 * lane + 1);
+      int sum = n0 + n1;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += y;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, before + sum > pos);
+      if (past) {
+        const int at = __ffs(past) - 1;
+        before += __shfl_sync(0xffffffffu, sum - n0 - n1, at);
+        const int skip = __shfl_sync(0xffffffffu, n0, at);
+        b += 2 * at;
+        if (before + skip <= pos) {
+          before += skip;
+          ++b;
+        }
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (lane == 0) {
+      found[0] = b;
+      found[1] = pos - before;
+    }
+  } else if (block == p.page_ctas - 1 && warp == 1) {
+    // what is wrong with the sequences is noted once
 #pragma unroll 1
     for (int x = lane; x < c.batch; x += 32) {
       SeqRows r;
@@ -124,35 +152,11 @@ __device__ __forceinline__ void append_pages(const AppendRopeParams& p, int bloc
         atomicOr(c.status, kErrHeld);
     }
   }
-  // the sequence that this page of the line belongs to, 64 at a time, two neighbours per lane
-  int b = 0, before = 0;
-#pragma unroll 1
-  while (true) {
-    if (b >= c.batch) return;
-    const int n0 = new_pages(a, b + 2 * lane), n1 = new_pages(a, b + 2 * lane + 1);
-    int sum = n0 + n1;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += y;
-    }
-    const uint32_t past = __ballot_sync(0xffffffffu, before + sum > pos);
-    if (past) {
-      const int at = __ffs(past) - 1;
-      before += __shfl_sync(0xffffffffu, sum - n0 - n1, at);
-      const int skip = __shfl_sync(0xffffffffu, n0, at);
-      b += 2 * at;
-      if (before + skip <= pos) {
-        before += skip;
-        ++b;
-      }
-      break;
-    }
-    before += __shfl_sync(0xffffffffu, sum, 31);
-    b += 64;
-  }
+  __syncthreads();
+  const int b = found[0];
+  if (b >= c.batch) return;
   const int q0 = a.cu[b], len = a.lens[b], held = len - (a.cu[b + 1] - q0);
-  const int i = (held >> c.page_log2) + pos - before;  // this CTA's page of the sequence
+  const int i = (held >> c.page_log2) + found[1];      // this CTA's page of the sequence
   const int start = i << c.page_log2;                  // its first token
   const int first = max(held - start, 0), last = min(len - start, 1 << c.page_log2);  // slots [first, last) are new
   const int number = __ldg(c.table + int64_t(b) * c.max_pages + i);  // needed only behind the loads
@@ -185,17 +189,20 @@ __device__ __forceinline__ void append_pages(const AppendRopeParams& p, int bloc
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     if (l == 0 && keys) {
+      if (int(threadIdx.x) < last - first)
+        place[threadIdx.x] = p.rope.a.positions ? p.rope.a.positions[q0 + start + first - held + threadIdx.x] : start + first + int(threadIdx.x);
+      __syncthreads();
       // 64 threads a token, four tokens at a time
       const int pair = threadIdx.x & 63;
       const uint64_t theta = p.rope.turn[min(pair, pairs - 1)];
-#pragma unroll 1
-      for (int x = threadIdx.x >> 6; x < last - first; x += kThreads / 64) {
-        const int at = p.rope.a.positions ? p.rope.a.positions[q0 + start + first - held + x] : start + first + x;
-        if (pair >= pairs) continue;
-        const int64_t turn = int64_t(uint64_t(int64_t(at)) * theta);
-        float sn, cn;
-        sincospif(float(int32_t(turn >> 32)) * 0x1p-31f, &sn, &cn);
-        cs[x * pairs + pair] = make_float2(cn * p.rope.factor, sn * p.rope.factor);
+      if (pair < pairs) {
+#pragma unroll 2
+        for (int x = threadIdx.x >> 6; x < last - first; x += kThreads / 64) {
+          const int64_t turn = int64_t(uint64_t(int64_t(place[x])) * theta);
+          float sn, cn;
+          sincospif(float(int32_t(turn >> 32)) * 0x1p-31f, &sn, &cn);
+          cs[x * pairs + pair] = make_float2(cn * p.rope.factor, sn * p.rope.factor);
+        }
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -207,20 +214,29 @@ __device__ __forceinline__ void append_pages(const AppendRopeParams& p, int bloc
     const int64_t at = int64_t(number) * c.heads + (on ? h : 0);
     uint8_t* const codes = (keys ? c.k_pages : c.v_pages) + (at << c.page_log2) * c.head_dim;
     float* const scale = (keys ? c.k_scale : c.v_scale) + at;
-    auto get = [&](int j, float (&f)[kPiece]) {
-      const int ch = (j << p.team_log2) + tid;
-      if (keys && ch < fill) S::turned(staged, j, (ch & mask) * kPiece, p.rope.rot, p.interleaved, cs + (ch >> row_log2) * pairs, f);
-      else S::get(staged, j, threadIdx.x, f);
+    // The elements of kPieces turns from j0 on, turned.
+    float f[kPieces][kPiece];
+    auto get = [&](int j0) {
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) {
+        if (j0 + j >= turns) break;
+        const int ch = ((j0 + j) << p.team_log2) + tid;
+        if (keys && ch < fill) S::turned(staged, j0 + j, (ch & mask) * kPiece, p.rope.rot, p.interleaved, cs + (ch >> row_log2) * pairs, f[j]);
+        else S::get(staged, j0 + j, threadIdx.x, f[j]);
+      }
     };
     float amax = 0.f;
 #pragma unroll 1
-    for (int j = 0; j < turns; ++j) {
-      float f[kPiece];
-      get(j, f);
+    for (int j0 = 0; j0 < turns; j0 += kPieces) {
+      get(j0);
 #pragma unroll
-      for (int e = 0; e < kPiece; ++e) {
-        const float m = fabsf(f[e]);
-        if (m < INFINITY) amax = fmaxf(amax, m);  // false for NaN too
+      for (int j = 0; j < kPieces; ++j) {
+        if (j0 + j >= turns) break;
+#pragma unroll
+        for (int e = 0; e < kPiece; ++e) {
+          const float m = fabsf(f[j][e]);
+          if (m < INFINITY) amax = fmaxf(amax, m);  // false for NaN too
+        }
       }
     }
 #pragma unroll
@@ -248,15 +264,17 @@ __device__ __forceinline__ void append_pages(const AppendRopeParams& p, int bloc
     }
     const float inv = pow2f(-e);
 #pragma unroll 1
-    for (int j = 0; j < turns; ++j) {
-      const int ch = (j << p.team_log2) + tid;
-      if (!on || ch >= fill) break;
-      float f[kPiece];
-      get(j, f);
-      uint2 w;
-      w.x = e4m3_pair(f[0] * inv, f[1] * inv) | (e4m3_pair(f[2] * inv, f[3] * inv) << 16);
-      w.y = e4m3_pair(f[4] * inv, f[5] * inv) | (e4m3_pair(f[6] * inv, f[7] * inv) << 16);
-      *reinterpret_cast<uint2*>(codes + int64_t((first << row_log2) + ch) * kPiece) = w;
+    for (int j0 = 0; j0 < turns; j0 += kPieces) {
+      if (turns > kPieces) get(j0);  // (a page of 128 x 128: turned again)
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) {
+        const int ch = ((j0 + j) << p.team_log2) + tid;
+        if (!on || ch >= fill) break;
+        uint2 w;
+        w.x = e4m3_pair(f[j][0] * inv, f[j][1] * inv) | (e4m3_pair(f[j][2] * inv, f[j][3] * inv) << 16);
+        w.y = e4m3_pair(f[j][4] * inv, f[j][5] * inv) | (e4m3_pair(f[j][6] * inv, f[j][7] * inv) << 16);
+        *reinterpret_cast<uint2*>(codes + int64_t((first << row_log2) + ch) * kPiece) = w;
+      }
     }
     if (tid == 0 && on) *scale = pow2f(e);
   }
@@ -287,9 +305,9 @@ cudaError_t launch_t(AppendRopeParams& p, cudaStream_t s) {
   const int64_t each = (int64_t(a.max_new) + page_size - 2) / page_size + 1;
   const int64_t bound = a.total_tokens / page_size + 2ll * c.batch;
   const int64_t pages = each * c.batch < bound ? each * c.batch : bound;
-  // Heads in turn share a table of angles; as many as leave eight CTAs for each SM.
+  // Heads in turn share a table of angles; as many as leave four CTAs for each SM.
   p.loops = 1;
-  while (p.loops * teams < c.heads && pages * ((c.heads + 2 * p.loops * teams - 1) / (2 * p.loops * teams)) * 2 >= 8 * 152) p.loops *= 2;
+  while (p.loops * teams < c.heads && pages * ((c.heads + 2 * p.loops * teams - 1) / (2 * p.loops * teams)) * 2 >= 4 * 152) p.loops *= 2;
   p.key_groups = (c.heads + p.loops * teams - 1) / (p.loops * teams);
   p.groups = 2 * p.key_groups;
   p.page_ctas = int(pages * p.groups);
