@@ -296,14 +296,16 @@ cudaError_t with_way(RopeParams& p, bool interleaved, const F& launch) {
   p.unit_log2 = 0;
   while ((unit << p.unit_log2) < a.head_dim) ++p.unit_log2;
   // Warps per token: one, or more while there are fewer warps than the GPU
-  // holds (32 per SM), down to one pass each.
+  // holds (32 per SM), down to one pass each.  Beside an append's pages (CHECKED) 8 per SM: a
+  // warp's start costs more than a pass of its loop there (32 trees of 17 to 64 tokens, 32 heads of 128:
+  // 17.3 / 13.9 us).
   const int units = 1 << p.unit_log2, heads = a.num_heads + a.num_kv_heads;
   const int all = units > 32 ? heads : int((int64_t(heads) * units + 31) / 32);  // passes over a token
   int sms = 0, dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const int want = (32 * sms + a.total_tokens - 1) / a.total_tokens;
+  const int want = ((CHECKED ? 8 : 32) * sms + a.total_tokens - 1) / a.total_tokens;
   p.passes = (all + want - 1) / want;
   p.slices = (all + p.passes - 1) / p.passes;
   const int64_t ctas = (int64_t(a.total_tokens) * p.slices + kRopeWarps - 1) / kRopeWarps;
