@@ -1,34 +1,40 @@
 // Trees of drafted tokens: their ancestor masks and positions, and the accepted
 // path moved together in the cache.
 //
-// Masks.  A warp takes a node and walks up to its root; lane w collects word w of
-// the node's row.  A parent's number is below the node's own, which every
-// CTA checks for the whole sequence first, so every walk ends.
+// Masks.  A thread takes a node and walks up to its root; the words of its row are collected
+// in shared memory, eight at a time from the last down, since a parent's number is below
+// the node's own, and a CTA's rows are written together.  Every CTA checks the parents of the
+// whole sequence first, so every walk ends.  What bounds it is the walk, one load behind the
+// other, and with few nodes the launch.  (A warp per node, a lane per word: the
+// walks of a warp's nodes came one behind the other.)
 //
-// Path.  A CTA owns one (sequence, head) of the keys or of the values and takes the
-// pages that receive tokens in their order: the node of a path's j-th token is at
-// least j, so what a page receives lies in it or behind it and has not been written
-// yet.  All of a page's loads are in flight at once, and a barrier
-// stands between them and the page's stores.
+// Path.  A warp owns one (sequence, head) of the keys or of the values and takes the
+// tokens in their order: the node of a path's j-th token is at least j, so what a slot
+// receives lies in it or behind it and has not been written yet, whatever number of slots
+// is loaded at once, as long as their stores come behind.  No thread waits for another warp;
+// the lookups of a page (path, table) are all that stands before its loads, and the scales
+// arrive with the tokens.
 #include "cache_rows.cuh"
 
 namespace attnmask {
 namespace {
 
-constexpr int kBuildThreads = 256, kBuildWarps = kBuildThreads / 32;
-constexpr int kBuildNodes = 64;  // of one CTA
+constexpr int kBuildThreads = 128;  // a node each
+constexpr int kBuildWords = 8;      // of a row at a time
 
 __global__ void __launch_bounds__(kBuildThreads) tree_build_kernel(const TreeBuildArgs a) {
-  const int b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ uint32_t rows[kBuildThreads][kBuildWords + 1];
+  const int b = blockIdx.y, tid = threadIdx.x;
   const CacheView& c = a.cache;
   SeqRows r;
-  const bool note = blockIdx.x == 0 && threadIdx.x == 0;
+  const bool note = blockIdx.x == 0 && tid == 0;
   if (!load_rows(a.cu, a.lens, b, a.total_tokens, a.max_new, c.max_pages << c.page_log2, c.status, r, note)) return;
-  const int first = blockIdx.x * kBuildNodes, last = min(r.n, first + kBuildNodes);
-  if (first >= r.n) return;
+  const int first = blockIdx.x * kBuildThreads, nodes = min(r.n - first, kBuildThreads);
+  if (nodes <= 0) return;
   const int32_t* parents = a.parents + r.q0;
   bool bad = r.len < r.n;
-  for (int i = threadIdx.x; i < r.n; i += kBuildThreads) {
+#pragma unroll 4
+  for (int i = tid; i < r.n; i += kBuildThreads) {
     const int p = __ldg(parents + i);
     bad |= p < -1 || p >= i;
   }
@@ -36,123 +42,167 @@ __global__ void __launch_bounds__(kBuildThreads) tree_build_kernel(const TreeBui
     if (note) atomicOr(c.status, r.len < r.n ? kErrHeld : kErrTree);
     return;
   }
-  for (int i = first + warp; i < last; i += kBuildWarps) {
-    for (int w0 = 0; w0 < a.words; w0 += 32) {
-      uint32_t word = 0;
-      int depth = -1;
-      for (int p = i; p >= 0; p = __ldg(parents + p)) {
-        if ((p >> 5) - w0 == lane) word |= 1u << (p & 31);
-        ++depth;
-      }
-      if (w0 + lane < a.words) a.bits[int64_t(r.q0 + i) * a.words + w0 + lane] = word;
-      if (w0 == 0 && lane == 0 && a.positions) a.positions[r.q0 + i] = r.len - r.n + depth;
+  int p = tid < nodes ? first + tid : -1, depth = -1;
+  uint32_t* const bits = a.bits + int64_t(r.q0 + first) * a.words;
+  for (int w0 = (a.words - 1) / kBuildWords * kBuildWords; w0 >= 0; w0 -= kBuildWords) {
+    const int width = min(kBuildWords, a.words - w0);
+#pragma unroll
+    for (int w = 0; w < kBuildWords; ++w) rows[tid][w] = 0;
+    while (p >= w0 * 32) {
+      rows[tid][(p >> 5) - w0] |= 1u << (p & 31);
+      p = __ldg(parents + p);
+      ++depth;
     }
+    __syncthreads();
+    for (int x = tid; x < nodes * kBuildWords; x += kBuildThreads) {
+      const int row = x / kBuildWords, w = x % kBuildWords;
+      if (w < width) bits[int64_t(row) * a.words + w0 + w] = rows[row][w];
+    }
+    __syncthreads();
   }
+  if (tid < nodes && a.positions) a.positions[r.q0 + first + tid] = r.len - r.n + depth;
 }
 
-constexpr int kKeepThreads = 128;
+constexpr int kKeepWarps = 4, kKeepThreads = 32 * kKeepWarps;
 
-// N: 16-byte pieces per thread of a page.
-template <int N>
 __global__ void __launch_bounds__(kKeepThreads) tree_keep_kernel(const TreeKeepArgs a) {
-  __shared__ int src_page[128], src_slot[128], shift[128];
-  __shared__ int top;
+  __shared__ __align__(16) uint4 staged[kKeepWarps][32 * 128 / 16];  // 32 rows
   const CacheView& c = a.cache;
-  const int h = blockIdx.x >> 1, values = blockIdx.x & 1, b = blockIdx.y, tid = threadIdx.x;
-  const int log2 = c.page_log2, page_size = 1 << log2, D = c.head_dim, per_row = D / 16;
+  const int b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int log2 = c.page_log2, page_size = 1 << log2, D = c.head_dim;
+  const int row_log2 = 31 - __clz(D / 16);  // pieces of 16 bytes of a row
   const bool note = blockIdx.x == 0 && tid == 0;
   SeqRows r;
+  const int m = __ldg(a.counts + b);
   if (!load_rows(a.cu, a.lens, b, INT_MAX, a.max_new, c.max_pages << c.page_log2, c.status, r, note)) return;
-  const int m = a.counts[b], base = r.len - r.n;
+  const int base = r.len - r.n;
   const int32_t* path = a.path + int64_t(b) * a.path_stride;
   bool bad = base < 0 || m < 0 || m > r.n || m > a.path_stride;
-  if (!bad)
+  if (!bad) {
+#pragma unroll 1
     for (int j = tid; j < m; j += kKeepThreads) {
       const int p = __ldg(path + j);
       bad |= p < 0 || p >= r.n || (j > 0 && __ldg(path + j - 1) >= p);
     }
+  }
   if (__syncthreads_or(bad)) {
     if (note) atomicOr(c.status, base < 0 ? kErrHeld : kErrTree);
     return;
   }
   if (note) a.new_lens[b] = base + m;
-  uint8_t* pages = values ? c.v_pages : c.k_pages;
-  float* scales = values ? c.v_scale : c.k_scale;
+  const int head = blockIdx.x * kKeepWarps + warp, h = head >> 1, values = head & 1;
+  if (h >= c.heads) return;
+  uint4* const pages = reinterpret_cast<uint4*>(values ? c.v_pages : c.k_pages);
+  float* const scales = values ? c.v_scale : c.k_scale;
   const int32_t* table = c.table + int64_t(b) * c.max_pages;
+  uint4* const stage = staged[warp];
+  const uint32_t stage_at = smem_addr(stage);
+  const int mask = (1 << row_log2) - 1;
+#pragma unroll 1
   for (int i = base >> log2; i << log2 < base + m; ++i) {
     const int number = __ldg(table + i);
-    const bool fine = in_pool(c, number);
-    const int t0 = i << log2, live = min(page_size, r.len - t0);  // its slots that hold tokens
-    const int64_t at = int64_t(fine ? number : 0) * c.heads + h;
-    const int own = fine ? exponent_of(scales[at]) : 0;
-    if (tid == 0) top = own;
-    __syncthreads();
+    if (!in_pool(c, number)) {
+      if (lane == 0) atomicOr(c.status, kErrBadPage);
+      continue;
+    }
+    const int64_t at = int64_t(number) * c.heads + h;
+    const int t0 = i << log2;                     // its first token
+    const int j0 = max(t0 - base, 0), j1 = min(t0 + page_size - base, m);  // of the path, its new tokens
+    const int own = exponent_of(scales[at]);
+    // The row that token j comes from, or -1 if it stays where it is or has no page; its exponent.
     int e = own;
-    if (tid < live) {
-      // slot tid receives a token, or keeps its own
-      const int j = t0 + tid - base;
-      const bool moves = j >= 0 && j < m;
-      const int src = moves ? base + __ldg(path + j) : t0 + tid;
-      const int from = moves ? __ldg(table + (src >> log2)) : number;
-      const bool good = fine && in_pool(c, from);
-      if (!good) atomicOr(c.status, kErrBadPage);
-      src_page[tid] = good ? from : -1;
-      src_slot[tid] = src & (page_size - 1);
-      if (good && from != number) {
-        e = exponent_of(scales[int64_t(from) * c.heads + h]);
-        atomicMax(&top, e);
+    auto source = [&](int j) -> int64_t {
+      e = own;
+      if (j >= j1) return -1;
+      const int src = base + __ldg(path + j);
+      if (src == base + j) return -1;
+      const int from = __ldg(table + (src >> log2));
+      if (!in_pool(c, from)) {
+        atomicOr(c.status, kErrBadPage);
+        return -1;
       }
-    }
-    __syncthreads();
-    const int to = top;
-    if (tid < live) {
-      shift[tid] = to - e;
-      if (src_page[tid] == number && src_slot[tid] == tid && to == e) src_page[tid] = -1;  // stays as it is
-    }
-    __syncthreads();
-    uint4 w[N];
-#pragma unroll
-    for (int y = 0; y < N; ++y) {
-      const int x = y * kKeepThreads + tid, slot = x / per_row, piece = x % per_row;
-      if (slot < live && src_page[slot] >= 0)
-        w[y] = *reinterpret_cast<const uint4*>(
-            pages + (((int64_t(src_page[slot]) * c.heads + h) << log2) + src_slot[slot]) * D + piece * 16);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int y = 0; y < N; ++y) {
-      const int x = y * kKeepThreads + tid, slot = x / per_row, piece = x % per_row;
-      if (slot >= live || src_page[slot] < 0) continue;
-      if (shift[slot] > 0) {
-        w[y].x = rescale4(w[y].x, shift[slot]);
-        w[y].y = rescale4(w[y].y, shift[slot]);
-        w[y].z = rescale4(w[y].z, shift[slot]);
-        w[y].w = rescale4(w[y].w, shift[slot]);
+      const int64_t row = int64_t(from) * c.heads + h;
+      if (from != number) e = exponent_of(scales[row]);
+      return (row << log2) + (src & (page_size - 1));
+    };
+    auto fetch = [&](int j, int64_t row) {
+      const int n = min(32, j1 - j) << row_log2;
+#pragma unroll 1
+      for (int x = lane; x < ((n + 31) & ~31); x += 32) {
+        const int64_t from = __shfl_sync(0xffffffffu, row, x >> row_log2);
+        copy16_async(stage_at + x * 16, pages + ((from < 0 ? 0 : from) << row_log2) + (x & mask), from >= 0);
       }
-      *reinterpret_cast<uint4*>(pages + ((at << log2) + slot) * D + piece * 16) = w[y];
+    };
+    int64_t row = source(j0 + lane);
+    fetch(j0, row);
+    int to = max(own, e);
+    const int e0 = e;
+#pragma unroll 1
+    for (int j = j0 + 32; j < j1; j += 32) {
+      source(j + lane);
+      to = max(to, e);
     }
-    if (tid == 0 && fine && to > own) scales[at] = pow2f(to);
-    __syncthreads();  // before the next page's numbers, and its reads of what was written here
+    to = __reduce_max_sync(0xffffffffu, to);
+#pragma unroll 1
+    for (int j = j0; j < j1; j += 32) {
+      if (j > j0) {
+        row = source(j + lane);
+        fetch(j, row);
+      } else {
+        e = e0;
+      }
+      asm volatile("cp.async.commit_group;\n\tcp.async.wait_all;" ::: "memory");
+      __syncwarp();
+      const int n = min(32, j1 - j) << row_log2;
+      uint4* const out = pages + (((at << log2) + base + j - t0) << row_log2);
+#pragma unroll 1
+      for (int x = lane; x < ((n + 31) & ~31); x += 32) {
+        const int down = __shfl_sync(0xffffffffu, row < 0 ? -1 : to - e, x >> row_log2);
+        if (down < 0) continue;
+        uint4 w = stage[x];
+        if (down > 0) {
+          w.x = rescale4(w.x, down);
+          w.y = rescale4(w.y, down);
+          w.z = rescale4(w.z, down);
+          w.w = rescale4(w.w, down);
+        }
+        out[x] = w;
+      }
+      __syncwarp();
+    }
+    if (__builtin_expect(to > own, 0)) {
+      // the page's other tokens take the new scale
+      uint4* const all = pages + (at << log2 << row_log2);
+      const int n = min(page_size, r.len - t0) << row_log2;
+#pragma unroll 1
+      for (int x = lane; x < n; x += 32) {
+        const int j = (x >> row_log2) + t0 - base;
+        if (j >= 0 && j < m && __ldg(path + j) != j) continue;
+        uint4 w = all[x];
+        w.x = rescale4(w.x, to - own);
+        w.y = rescale4(w.y, to - own);
+        w.z = rescale4(w.z, to - own);
+        w.w = rescale4(w.w, to - own);
+        all[x] = w;
+      }
+      if (lane == 0) scales[at] = pow2f(to);
+    }
+    __syncwarp();  // before the reads of what was written here
   }
 }
 
 }  // namespace
 
 attn_status launch_tree_build(const TreeBuildArgs& a, cudaStream_t s) {
-  const dim3 grid(unsigned((a.max_new + kBuildNodes - 1) / kBuildNodes), unsigned(a.cache.batch));
+  const dim3 grid(unsigned((a.max_new + kBuildThreads - 1) / kBuildThreads), unsigned(a.cache.batch));
   tree_build_kernel<<<grid, kBuildThreads, 0, s>>>(a);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? ATTN_OK : record_cuda_error(e, "attn_cache_tree_build launch");
 }
 
 attn_status launch_tree_keep(const TreeKeepArgs& a, cudaStream_t s) {
-  const dim3 grid(unsigned(2 * a.cache.heads), unsigned(a.cache.batch));
-  switch ((a.cache.head_dim << a.cache.page_log2) / 16 / kKeepThreads) {
-    case 8: tree_keep_kernel<8><<<grid, kKeepThreads, 0, s>>>(a); break;
-    case 4: tree_keep_kernel<4><<<grid, kKeepThreads, 0, s>>>(a); break;
-    case 2: tree_keep_kernel<2><<<grid, kKeepThreads, 0, s>>>(a); break;
-    default: tree_keep_kernel<1><<<grid, kKeepThreads, 0, s>>>(a); break;
-  }
+  const dim3 grid(unsigned((2 * a.cache.heads + kKeepWarps - 1) / kKeepWarps), unsigned(a.cache.batch));
+  tree_keep_kernel<<<grid, kKeepThreads, 0, s>>>(a);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? ATTN_OK : record_cuda_error(e, "attn_cache_tree_keep launch");
 }
