@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kKeepThreads) tree_keep_kernel(const TreeKeepA
   float* const scales = values ? c.v_scale : c.k_scale;
   const int32_t* table = c.table + int64_t(b) * c.max_pages;
   uint4* const stage = staged[warp];
-  const uint32_t stage_at = smem_addr(stage);
+  const uint32_t stage_at = ptx::smem_addr(stage);
   const int mask = (1 << row_log2) - 1;
 #pragma unroll 1
   for (int i = base >> log2; i << log2 < base + m; ++i) {
