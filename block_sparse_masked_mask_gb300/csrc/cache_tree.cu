@@ -1,33 +1,43 @@
 // Attention of trees of drafted tokens over the 8-bit cache, on the tcgen05 tensor
-// cores.
+// cores: up to 64 rows (nodes times query heads of the group) share each cached byte.
 //
-// A tree has a few dozen nodes, so up to 128 rows (nodes times query heads of the
-// group) share each cached byte: enough for the tensor cores, too few to fill their
-// 128 lanes.  So the products are turned round: tokens are their M, rows their N,
-// padded to 16, 32, 64 or 128 only.
+// That is too few to fill the 128 lanes of a product, so the products are turned round: tokens are
+// their M, rows their N, padded to 16, 32 or 64 only.
 //  * S^T = K Q^T on the codes as they lie (kind::f8f6f4), a query as the sum of two
-//    e4m3 numbers (cache_tiles.cuh).  A thread of the softmax owns one token: its
-//    page's scales are the thread's own, and every one has work whatever the rows.
-//  * O^T += V^T P^T in fp16: one warpgroup turns the values' codes into fp16 tiles in
-//    shared memory, the softmax writes its weights there too.
+//    e4m3 numbers (cache_tiles.cuh).
+//  * O^T += V^T P^T in fp16.  One warpgroup turns the values' codes into fp16 in tensor memory,
+//    dimensions in its lanes (a transposed load of bytes); the softmax writes its weights to
+//    shared memory, rows along the tokens (stmatrix).
 //  * Scores, scales, references and far pages are those of cache_attn.cu: the weight is
-//    2^(s + x - m), x the exponent of the page's value scale.  m belongs to a row
-//    and so to all threads: they vote on every tile whether some weight would pass 2^15,
-//    and only then look for the rows' maxima and move the references.
-//  * A row's sum is kept by every token's thread and added up at a segment's end.
-//  * The masks matter in the tiles that hold the tree (and at the end of a sequence): a
-//    thread collects the bits of its token, one per row, while it waits for its scores.
-// Work: tiles of 128 tokens of all (sequence, head, tile of rows)s form one line that
-// is cut evenly among one CTA per SM; a CTA's piece is walked segment by segment
-// without a pause between them: the rings of tiles run on, queries and O have
-// two buffers each.  Segments that are not whole meet in a second kernel
-// (cache_join.cuh), two per CTA at most.
+//    2^(s + x - m), x the exponent of the page's value scale.  A page has one scale for 16 tokens at
+//    least, which a warp's loads from tensor memory are arranged by, so it is uniform there; m, the
+//    row's factor and its sum stay in the registers of the lanes that hold the row.
+//  * References move when the sum of two weights of any row passes 2^15.  The warps vote on that with
+//    a barrier's OR, once a tile, behind the weights; a tile that moves them repeats its weights.
+//  * Two warpgroups take tiles in turn, each with references, sums and O of its own, which meet
+//    at a segment's end.
+//  * The masks matter in the tiles that hold the tree (and at the end of a sequence): only there
+//    hidden scores are overwritten, in tensor memory, before the loop that all tiles share.
+// Work: tiles of 128 tokens of all (sequence, head)s form one line that is cut evenly among one
+// CTA per SM; a CTA's piece is walked segment by segment without a pause between them: the
+// rings of tiles run on, queries and O have two buffers each.  Segments that are
+// not whole meet in a second kernel (cache_join.cuh), two per CTA at most.
 // Warps (512 threads):
-//   0-3, 4-7   softmax of the first and second half of the rows, a thread per token
-//   8-11       queries; values: codes to fp16 tiles
+//   0-3, 4-7   softmax of every other tile
+//   8-11       queries; values: codes to fp16
 //   12         pages, scales and TMA of the codes
 //   13, 14     tcgen05 issuers of S^T and of O^T (which also owns TMEM)
 //   15         the line: the CTA's segments
+//
+// What bounds it: 64 trees of 4 to 8 nodes behind 1024 to 16384 tokens, 32 query and 8 key heads of
+// 128, take 166 us where the bytes take 108 at the rate of a copy; 16 sequences of 8192 tokens, 16 / 32 / 64
+// rows a head, 54 / 61 / 70 us (40).  It is the instructions'
+// supply more than their issue: with five roles' loops at once, warps wait for instructions
+// more than for anything else, and each step that made the code shorter (loops rolled up, one form of
+// waits, rare paths out of line) was worth more than one that took operations out.  Four
+// warpgroups for the softmax, or factors held ready across its loop, were no faster.
+// One tree of 16 nodes behind 2049 tokens takes 17 us: the kernels' start, one tile, the join.
+//
 // Every wait is bounded and ends in ATTN_ERR_DEVICE_TIMEOUT in the cache's status word.
 // Each role waits only for an earlier tile's events of the others, or for this
 // tile's by a role that comes before it (line, pages, queries and keys, S^T, softmax,
@@ -87,84 +97,76 @@ struct TreeParams {
   float2* part_m;
 };
 
-// A piece of the line in one (sequence, head, tile of rows).
+// A piece of the line in one (sequence, head).
 struct Segment {
   int tiles;  // 0: there is no further one
-  int b, h, row0, rows, q0, n, len, token, slot;  // slot of the partial result, -1: whole
+  int b, h, rows, q0, n, len, token, slot;  // slot of the partial result, -1: whole
 };
 
-__device__ __forceinline__ int row_tiles(const SeqRows& r, int G, int N) { return (r.n * G + N - 1) / N; }
 __device__ __forceinline__ int tiles_of(const SeqRows& r) { return r.n == 0 ? 0 : (r.len + kTile - 1) / kTile; }
 
-// Tiles of sequence b, all heads and tiles of rows; 0 where its numbers cannot be used.
-template <int N>
+// Tiles of sequence b, all heads; 0 where its numbers cannot be used.
 __device__ __forceinline__ int units_of(const TreeParams& p, int b) {
   const CacheQueryArgs& a = p.a;
   if (b >= a.cache.batch) return 0;
   const int q0 = a.cu[b], q1 = a.cu[b + 1], len = a.lens[b], n = q1 - q0;
   const bool good = q0 >= 0 && q1 >= q0 && q1 <= a.total_tokens && (b > 0 || q0 == 0) && n <= a.max_new && len >= n &&
                     len <= a.max_seqlen;
-  return good ? (len + kTile - 1) / kTile * ((n * p.G + N - 1) / N) * a.cache.heads : 0;
+  return good && n > 0 ? (len + kTile - 1) / kTile * a.cache.heads : 0;
 }
 __device__ __forceinline__ int tree_share(int total, const TreeParams& p) {
   return max(p.least, (total + p.ctas - 1) / p.ctas);
 }
 
-// E 16-bit rows of 128 tokens (P^T): MN-major, rows of 128 bytes at most, swizzled over their
-// width.
-template <int E, int TOKENS>
-struct WideTile {
-  static constexpr int CE = E < 64 ? E : 64, ROWB = CE * 2, CHUNK = TOKENS * ROWB, BYTES = E / CE * CHUNK;
+// E 16-bit rows of 128 tokens (P^T): MN-major, swizzled over a token's width.
+template <int E>
+struct WeightTile {
+  static constexpr int ROWB = E * 2, BYTES = kTile * ROWB;
   static constexpr uint32_t SW = ROWB == 128 ? ptx::kSwizzle128B : ROWB == 64 ? ptx::kSwizzle64B : ptx::kSwizzle32B;
   __device__ static uint32_t unit(int token, int u) {  // byte offset of 16-byte unit u of the token
     const int x = ROWB == 128 ? (token & 7) : ROWB == 64 ? ((token >> 1) & 3) : ((token >> 2) & 1);
-    constexpr int PER = ROWB / 16;
-    return uint32_t(u / PER * CHUNK + token * ROWB + (((u % PER) ^ x) << 4));
+    return uint32_t(token * ROWB + ((u ^ x) << 4));
   }
-  __device__ static uint64_t desc(uint32_t addr) { return ptx::smem_desc(addr, CHUNK, 8 * ROWB, SW); }
+  __device__ static uint64_t desc(uint32_t addr) { return ptx::smem_desc(addr, BYTES, 8 * ROWB, SW); }
   __host__ __device__ static constexpr uint64_t step(int kk) { return uint64_t(kk * 16 * ROWB) >> 4; }
 };
 
 template <int D, int N>
 struct TreeCfg {
-  using P = WideTile<N, kTile>;
+  using P = WeightTile<N>;
   // Warpgroups of the softmax, and the warps behind them
   static constexpr int GROUPS = 2, THREADS = 128 * GROUPS + 256;
   static constexpr int CONVERT = 4 * GROUPS, PAGES = CONVERT + 4, ISSUE_S = PAGES + 1, ISSUE_O = PAGES + 2, LINE = PAGES + 3;
-  // Registers for each thread of the softmax, the conversion and the others: of what the launch
-  // has for all (128 with 512 threads, 80 with 768)
+  // Registers for each thread of the softmax, the conversion and the others, of the launch's 128 for all
   static constexpr int REG_SOFTMAX = 168, REG_CONVERT = 104, REG_OTHERS = 72;
   static_assert(GROUPS * REG_SOFTMAX + REG_CONVERT + REG_OTHERS == (GROUPS + 2) * 128, "registers");
   static constexpr int KT = CodeTile<D>::BYTES;   // a tile of codes
   static constexpr int QT = 2 * N * D;            // queries: hi, lo
-  static constexpr bool TURNS = N <= 64;          // the warpgroups of the softmax take tiles in turn, or a part of the rows each
-  static constexpr int ROWS = TURNS ? N : N / GROUPS;  // of a warpgroup
-  static constexpr int NQ = N == 128 ? 1 : 2;
   static constexpr int NB = N <= 32 ? 3 : 2;      // of scores and of weights
-  static constexpr int NO = N == 128 ? 1 : 2;     // segments' O
-  static constexpr int NK = N <= 32 ? 5 : N == 64 ? 4 : 3, NR = NK;
+  static constexpr int NO = 2;                    // segments' O
+  static constexpr int NK = N <= 32 ? 5 : 4, NR = NK;
   static constexpr int NSCL = 8, NSEG = 4;
   static constexpr int OFF_P = 0;
   static constexpr int OFF_Q = OFF_P + NB * P::BYTES;
-  static constexpr int OFF_K = OFF_Q + (NQ * QT + 1023) / 1024 * 1024;
+  static constexpr int OFF_K = OFF_Q + (2 * QT + 1023) / 1024 * 1024;
   static constexpr int OFF_R = OFF_K + NK * KT;
   static constexpr int OFF_SCL = OFF_R + NR * KT;          // as in cache_chunk.cu
   static constexpr int OFF_ROWS = OFF_SCL + NSCL * 8 * 16; // [2][N]: the rows' factors
-  static constexpr int OFF_MAX = OFF_ROWS + 2 * N * 4;     // [warpgroup][4 warps][ROWS]: maxima, then sums
-  static constexpr int OFF_REF = OFF_MAX + GROUPS * 4 * ROWS * 4;  // [warpgroup][ROWS]: negative references
-  static constexpr int OFF_MOVE = OFF_REF + GROUPS * ROWS * 4;     // [warp][ROWS]: negative reference, half the factor's exponent
-  static constexpr int OFF_OUT = OFF_MOVE + GROUPS * 4 * ROWS * 8;      // [N]: factors of the two warpgroups' O, place in the outputs
+  static constexpr int OFF_MAX = OFF_ROWS + 2 * N * 4;     // [warpgroup][4 warps][N]: maxima, then sums
+  static constexpr int OFF_REF = OFF_MAX + GROUPS * 4 * N * 4;  // [warpgroup][N]: negative references
+  static constexpr int OFF_MOVE = OFF_REF + GROUPS * N * 4;     // [warp][N]: negative reference, half the factor's exponent
+  static constexpr int OFF_OUT = OFF_MOVE + GROUPS * 4 * N * 8;      // [N]: factors of the two warpgroups' O, place in the outputs
   static constexpr int OFF_SEG = OFF_OUT + N * 16;
   static constexpr int OFF_BAR = OFF_SEG + NSEG * 48;
   static constexpr int B_SEGFULL = 0, B_SEGFREE = B_SEGFULL + NSEG, B_QFULL = B_SEGFREE + NSEG, B_QFREE = B_QFULL + 2,
-                       B_KFULL = B_QFREE + NQ, B_KFREE = B_KFULL + NK, B_RFULL = B_KFREE + NK, B_RFREE = B_RFULL + NR,
+                       B_KFULL = B_QFREE + 2, B_KFREE = B_KFULL + NK, B_RFULL = B_KFREE + NK, B_RFREE = B_RFULL + NR,
                        B_VFULL = B_RFREE + NR, B_VFREE = B_VFULL + 2, B_SCLFULL = B_VFREE + 2,
                        B_SCLFREE = B_SCLFULL + NSCL, B_SFULL = B_SCLFREE + NSCL, B_PFULL = B_SFULL + NB,
                        B_PDONE = B_PFULL + NB, B_OFREE = B_PDONE + NB, B_USED = B_OFREE + NO,
                        B_DRAIN = B_USED + 2, NBAR = B_DRAIN + 2;
   static_assert(NBAR <= THREADS, "a thread for each");
   __device__ static int arrivals(int i) {
-    constexpr int ALL = 4 * GROUPS, EACH = TURNS ? 4 : ALL;  // warps of the softmax, and of those with a tile
+    constexpr int ALL = 4 * GROUPS, EACH = 4;  // warps of the softmax, and of those with a tile
     return i >= B_OFREE ? (i >= B_DRAIN ? 1 : ALL)
            : i >= B_PFULL ? (i >= B_PDONE ? 1 : EACH)
            : i >= B_SCLFREE ? (i >= B_SFULL ? 1 : 4 + EACH)  // value and softmax warps
@@ -180,7 +182,7 @@ struct TreeCfg {
   static constexpr int SMEM = USED > 116 * 1024 ? USED : 116 * 1024;
   static_assert(SMEM <= 232448, "shared memory budget");
   // TMEM columns
-  static constexpr int S = 0, O = NB * N, OSEG = TURNS ? 2 * N : N, V = O + NO * OSEG;
+  static constexpr int S = 0, O = NB * N, OSEG = GROUPS * N, V = O + NO * OSEG;
   static_assert(V + 2 * 64 <= 512, "tensor memory");
 };
 
@@ -227,8 +229,9 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
     g.tiles = 0;
     if (!ok) return false;
     const int4* w = reinterpret_cast<const int4*>(sbase + C::OFF_SEG + at * 48);
-    const int4 x = w[0], y = w[1], z = w[2];
-    g = Segment{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, z.x, z.y};
+    const int4 x = w[0], y = w[1];
+    const int slot = w[2].x;
+    g = Segment{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, slot};
     if (single) ptx::mbar_arrive(bar(C::B_SEGFREE + at));
     else warp_arrive(bar(C::B_SEGFREE + at), lane);
     return true;
@@ -242,7 +245,7 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
     // 64 sequences at a time, two neighbours per lane
     int total = 0;
 #pragma unroll 1
-    for (int b0 = 0; b0 < c.batch; b0 += 64) total += units_of<N>(p, b0 + 2 * lane) + units_of<N>(p, b0 + 2 * lane + 1);
+    for (int b0 = 0; b0 < c.batch; b0 += 64) total += units_of(p, b0 + 2 * lane) + units_of(p, b0 + 2 * lane + 1);
     total = __reduce_add_sync(0xffffffffu, total);
     const int piece = tree_share(total, p);
     int pos = int(min(int64_t(blockIdx.x) * piece, int64_t(total)));
@@ -252,7 +255,7 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
     int b = 0, before = 0;  // the sequence that pos belongs to, and the line before it
 #pragma unroll 1
     while (pos < stop) {
-      const int n0 = units_of<N>(p, b + 2 * lane), n1 = units_of<N>(p, b + 2 * lane + 1);
+      const int n0 = units_of(p, b + 2 * lane), n1 = units_of(p, b + 2 * lane + 1);
       int sum = n0 + n1;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -279,7 +282,7 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
       Segment g{};
 #pragma unroll 1
       while (pos < stop) {
-        const int all = units_of<N>(p, b);
+        const int all = units_of(p, b);
         if (pos >= before + all) {
           before += all;
           ++b;
@@ -289,13 +292,12 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
         r.q0 = a.cu[b];
         r.n = a.cu[b + 1] - r.q0;
         r.len = a.lens[b];
-        const int U = tiles_of(r), RT = row_tiles(r, p.G, N);
+        const int U = tiles_of(r);
         const int item = (pos - before) / U, u0 = (pos - before) % U, u1 = min(U, u0 + stop - pos);
         g.tiles = u1 - u0;
         g.b = b;
-        g.h = item / RT;
-        g.row0 = item % RT * N;
-        g.rows = min(N, r.n * p.G - g.row0);
+        g.h = item;
+        g.rows = r.n * p.G;
         g.q0 = r.q0;
         g.n = r.n;
         g.len = r.len;
@@ -308,9 +310,9 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
       if (s >= C::NSEG && !tree_warp_wait(bar(C::B_SEGFREE + at), uint32_t(s / C::NSEG - 1) & 1u, abort_flag, 2)) break;
       if (lane == 0) {
         int4* w = reinterpret_cast<int4*>(sbase + C::OFF_SEG + at * 48);
-        w[0] = make_int4(g.tiles, g.b, g.h, g.row0);
-        w[1] = make_int4(g.rows, g.q0, g.n, g.len);
-        w[2] = make_int4(g.token, g.slot, 0, 0);
+        w[0] = make_int4(g.tiles, g.b, g.h, g.rows);
+        w[1] = make_int4(g.q0, g.n, g.len, g.token);
+        w[2].x = g.slot;
         ptx::mbar_arrive(bar(C::B_SEGFULL + at));
       }
       __syncwarp();
@@ -418,7 +420,7 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
 #pragma unroll 1
       for (int s = 0; ok && segment(s, g, true) && g.tiles; ++s) {
         ok = tree_wait(bar(C::B_QFULL + (s & 1)), uint32_t(s >> 1) & 1u, abort_flag, 6);
-        const uint64_t qhi = qd + uint64_t((s % C::NQ) * C::QT >> 4), qlo = qhi + uint64_t(N * D >> 4);
+        const uint64_t qhi = qd + uint64_t((s & 1) * C::QT >> 4), qlo = qhi + uint64_t(N * D >> 4);
 #pragma unroll 1
         for (int j = 0; ok && j < g.tiles; ++j, ++T) {
           const int ks = T % C::NK, f = T % C::NB;
@@ -435,7 +437,7 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
           for (int kk = 0; kk < D / 32; ++kk) ptx::mma_f8_ss(s_tmem, ki + 2 * kk, qlo + 2 * kk, IDESC, 1);
           ptx::mma_commit(bar(C::B_SFULL + f));
           ptx::mma_commit(bar(C::B_KFREE + ks));
-          if (j == g.tiles - 1) ptx::mma_commit(bar(C::B_QFREE + s % C::NQ));
+          if (j == g.tiles - 1) ptx::mma_commit(bar(C::B_QFREE + (s & 1)));
         }
       }
       // every product this thread issued has finished once this arrives
@@ -462,11 +464,11 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
                tree_wait(bar(C::B_PFULL + f), uint32_t(T / C::NB) & 1u, abort_flag, 10);
           if (!ok) break;
           ptx::tc_fence_after();
-          const uint32_t o_tmem = o_seg + (C::TURNS ? uint32_t(T & 1) * N : 0u), v_tmem = tmem + uint32_t(C::V + vs * 64);
+          const uint32_t o_tmem = o_seg + uint32_t(T & 1) * N, v_tmem = tmem + uint32_t(C::V + vs * 64);
           const uint64_t pi = pd + uint64_t(f * C::P::BYTES >> 4);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            ptx::mma_ts(o_tmem, v_tmem + uint32_t(kk) * 8u, pi + C::P::step(kk), IDESC, (j > (C::TURNS ? 1 : 0) || kk > 0) ? 1u : 0u);
+            ptx::mma_ts(o_tmem, v_tmem + uint32_t(kk) * 8u, pi + C::P::step(kk), IDESC, (j > 1 || kk > 0) ? 1u : 0u);
           ptx::mma_commit(bar(C::B_PDONE + f));
           ptx::mma_commit(bar(C::B_VFREE + vs));
         }
@@ -486,17 +488,16 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
 #pragma unroll 1
     for (int s = 0; ok && segment(s, g, false) && g.tiles; ++s) {
       // the queries two segments back are used, and so are their factors
-      if (s >= C::NQ) ok = tree_warp_wait(bar(C::B_QFREE + s % C::NQ), uint32_t(s / C::NQ - 1) & 1u, abort_flag, 12);
+      if (s >= 2) ok = tree_warp_wait(bar(C::B_QFREE + (s & 1)), uint32_t((s >> 1) - 1) & 1u, abort_flag, 12);
       if (ok && s >= 2) ok = tree_warp_wait(bar(C::B_USED + (s & 1)), uint32_t((s >> 1) - 1) & 1u, abort_flag, 13);
       if (!ok) break;
       // D / 16 lanes per row, rows on their way two turns ahead
       constexpr int PARTS = D / 16, STEP = 128 / PARTS;
       auto fetch = [&](int row, uint4 (&q)[2]) {
         if (row < g.rows) {
-          const int rg = g.row0 + row;
           const uint4* src = reinterpret_cast<const uint4*>(
               static_cast<const __nv_bfloat16*>(a.q) +
-              (int64_t(g.q0 + rg / p.G) * a.num_heads + g.h * p.G + rg % p.G) * D) + 2 * (ct % PARTS);
+              (int64_t(g.q0 + row / p.G) * a.num_heads + g.h * p.G + row % p.G) * D) + 2 * (ct % PARTS);
           q[0] = src[0];
           q[1] = src[1];
         } else {
@@ -509,7 +510,7 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
 #pragma unroll 1
       for (int row = ct / PARTS; row < N; row += STEP) {  // (whole warps)
         fetch(row + 2 * STEP, q[2]);
-        const float f = p.scale_log2 * split_held<D, PARTS>(q[0], sbase + C::OFF_Q + (s % C::NQ) * C::QT, row, N * D, ct % PARTS);
+        const float f = p.scale_log2 * split_held<D, PARTS>(q[0], sbase + C::OFF_Q + (s & 1) * C::QT, row, N * D, ct % PARTS);
         if (ct % PARTS == 0) reinterpret_cast<float*>(sbase + C::OFF_ROWS)[(s & 1) * N + row] = f;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -573,21 +574,18 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
     ptx::regs_inc<C::REG_SOFTMAX>();
     // -------------------------------------------------------------- softmax
     // A warp takes 32 tokens, in two blocks of 16 (of one page each); of a block, lane
-    // 4 g + i holds tokens g and g + 8 and rows 8 k + 2 i, + 1.  Up to 64 rows the warpgroups
-    // take tiles in turn, each with references, sums and O of its own, which meet at a
-    // segment's end: what a tile costs besides its scores (waits, the vote) is then paid
-    // by each for every other one.  Of 128 rows each of four takes a quarter.
+    // 4 g + i holds tokens g and g + 8 and rows 8 k + 2 i, + 1.  What a tile costs besides its
+    // scores (waits, the vote) is paid by each warpgroup for every other one.
     // The weights are formed and stored before the vote on the references; a tile whose
     // references move repeats them.
-    constexpr int ROWS = C::ROWS, K = ROWS / 8, STRIDE = C::TURNS ? 2 : 1;
+    constexpr int K = N / 8, STRIDE = C::GROUPS;
     const int wg = warp >> 2, w4 = warp & 3, g4 = lane >> 2, i4 = lane & 3;
-    const int row_base = C::TURNS ? 0 : wg * ROWS;
     const uint32_t lanes = tmem + (uint32_t(w4 * 32) << 16);
-    float* const warps = reinterpret_cast<float*>(sbase + C::OFF_MAX) + wg * 4 * ROWS;  // [warp][row]: maxima, then sums
+    float* const warps = reinterpret_cast<float*>(sbase + C::OFF_MAX) + wg * 4 * N;  // [warp][row]: maxima, then sums
     float* const refs = reinterpret_cast<float*>(sbase + C::OFF_REF);                   // [warpgroup][row]
     float4* const out = reinterpret_cast<float4*>(sbase + C::OFF_OUT);
     auto meet = [&](bool x) { return ptx::named_barrier_or(1 + wg, 128, x); };
-    auto meet_all = [&](bool x) { return C::TURNS ? ptx::named_barrier_or(5, 256, x) : meet(x); };
+    auto meet_all = [&](bool x) { return ptx::named_barrier_or(5, 256, x); };
     // Scores of this warp's tokens to -inf where the row does not see the token, for which
     // `see` of the token's lane has no bit.  In tensor memory, and rolled up: few tiles have any, and
     // the loop over the others is the faster for being short.
@@ -611,7 +609,7 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
     // (never 0, where a page is left out or the product is below fp32: a hidden score is -inf, and
     // times 0 it would be NaN)
     auto factor = [](float2 f, float2 ks) { return ptx::ffma2(f, ks, make_float2(0x1p-126f, 0x1p-126f)); };
-    float2* const move = reinterpret_cast<float2*>(sbase + C::OFF_MOVE) + warp * ROWS;
+    float2* const move = reinterpret_cast<float2*>(sbase + C::OFF_MOVE) + warp * N;
     // The scales of this warp's two blocks of tile T, which has no further use for its slot.
     float4 of[2];
     auto scales = [&](int T) {
@@ -624,10 +622,10 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
     };
     // where this lane's row of a matrix of weights goes: a token, and the first or second
     // eight rows of the query of sixteen
-    const int to_token = w4 * 32 + (lane & 15), to_unit = row_base / 8 + (lane >> 4);
+    const int to_token = w4 * 32 + (lane & 15), to_unit = lane >> 4;
     // Before the first segment is there, one tile of nothing (on what lies in this warpgroup's O):
     // the instructions of the loop arrive while the first keys do, and not after them.
-    Segment g{(C::TURNS ? wg : 0) + 1, 0, 0, 0, 0, 0, 0, 1 << 30, 0, 0};
+    Segment g{wg + 1, 0, 0, 0, 0, 0, 1 << 30, 0, 0};
     of[0] = of[1] = make_float4(1.f, 0.f, 1.f, 0.f);
     bool dry = opaque(1) != 0;
 #pragma unroll 1
@@ -639,8 +637,8 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
         if (meet_all(!ok) || g.tiles == 0) break;
       }
       const int text = g.len - g.n;
-      const uint32_t o_seg = lanes + uint32_t(C::O + s % C::NO * C::OSEG), o_col = o_seg + uint32_t(C::TURNS ? wg * N : row_base);
-      const float* factors = reinterpret_cast<const float*>(sbase + C::OFF_ROWS) + (s & 1) * N + row_base;
+      const uint32_t o_seg = lanes + uint32_t(C::O + s % C::NO * C::OSEG), o_col = o_seg + uint32_t(wg * N);
+      const float* factors = reinterpret_cast<const float*>(sbase + C::OFF_ROWS) + (s & 1) * N;
       float2 f2[K], m2[K], l2[K];  // of the rows: factor, negative reference, sum
 #pragma unroll
       for (int k = 0; k < K; ++k) {
@@ -649,13 +647,13 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
         l2[k] = make_float2(0.f, 0.f);
       }
 
-      const int mine = C::TURNS ? (T0 ^ wg) & 1 : 0;  // the first tile of this warpgroup's
+      const int mine = (T0 ^ wg) & 1;  // the first tile of this warpgroup's
       if (mine < g.tiles && !dry) ok = scales(T0 + mine);
       bool left = false;
 #pragma unroll 1
       for (int j = mine; j < g.tiles; j += STRIDE) {
         const int T = T0 + j, f = T % C::NB;
-        const uint32_t s_col = dry ? o_col : lanes + uint32_t(C::S + f * N + row_base), weights = base + C::OFF_P + f * C::P::BYTES;
+        const uint32_t s_col = dry ? o_col : lanes + uint32_t(C::S + f * N), weights = base + C::OFF_P + f * C::P::BYTES;
         const int token = g.token + j * kTile + w4 * 32 + lane;
         const int flags = __float_as_int(of[0].w) | __float_as_int(of[1].w);
         // which rows see this lane's token
@@ -665,12 +663,13 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
           const bool here = token < g.len && __float_as_int(lane < 16 ? of[0].w : of[1].w) >= 0;
           see = here && token < text ? ~0ull : 0ull;
           if (here && token >= text) {
-            const int node = token - text, first = g.row0 + row_base, last = min(first + ROWS, g.row0 + g.rows);
+            const int node = token - text;
+            const uint32_t* word = p.tree.bits + int64_t(g.q0) * p.tree.words + (node >> 5);
 #pragma unroll 4
-            for (int i = first / p.G; i < (last + p.G - 1) / p.G; ++i) {
-              const uint32_t bit = __ldg(p.tree.bits + (g.q0 + i) * p.tree.words + (node >> 5)) >> (node & 31) & 1u;
-              const int from = max(i * p.G - first, 0), to = min((i + 1) * p.G, last) - first;  // of this warpgroup's
-              const uint64_t span = (to >= 64 ? ~0ull : (1ull << to) - 1) & ~((1ull << from) - 1);
+            for (int i = 0; i < g.n; ++i) {
+              const uint32_t bit = __ldg(word + int64_t(i) * p.tree.words) >> (node & 31) & 1u;
+              // (the last row may be the 64th)
+              const uint64_t span = (i + 1) * p.G >= 64 ? ~0ull << i * p.G : ((1ull << p.G) - 1) << i * p.G;
               see |= bit ? span : 0ull;
             }
           }
@@ -750,7 +749,7 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
               most.x = fmaxf(most.x, __shfl_xor_sync(0xffffffffu, most.x, o));
               most.y = fmaxf(most.y, __shfl_xor_sync(0xffffffffu, most.y, o));
             }
-            if (g4 == 0) *reinterpret_cast<float2*>(warps + w4 * ROWS + 8 * k + 2 * i4) = most;
+            if (g4 == 0) *reinterpret_cast<float2*>(warps + w4 * N + 8 * k + 2 * i4) = most;
           }
           const int before = T - STRIDE;  // this warpgroup's last tile
           if (j >= STRIDE)
@@ -762,10 +761,10 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
           ptx::tc_fence_after();
           // A lane per row, every warp for itself with the same result (in little code, as
           // all that runs once a segment: instructions from far away cost more than their work)
-          if (lane < ROWS) {
+          if (lane < N) {
 #pragma unroll 1
-            for (int x = lane; x < ROWS; x += 32) {
-              const float now = fmaxf(fmaxf(warps[x], warps[ROWS + x]), fmaxf(warps[2 * ROWS + x], warps[3 * ROWS + x]));
+            for (int x = lane; x < N; x += 32) {
+              const float now = fmaxf(fmaxf(warps[x], warps[N + x]), fmaxf(warps[2 * N + x], warps[3 * N + x]));
               const float was = j >= STRIDE ? -move[x].x : kNoReference;
               const bool raise = now > was + (kMostWeight - 1.f);
               move[x] = make_float2(raise ? kTopWeight - now : -was, raise ? half_factor(was, now - kTopWeight) : 1.f);
@@ -832,8 +831,7 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
         continue;
       }
       // ---- the segment's end: sums over the tokens, O
-      if (!C::TURNS && left) break;
-      const int end = T0 + g.tiles - 1, last = C::TURNS ? end - ((end ^ wg) & 1) : end;  // this warpgroup's last tile
+      const int end = T0 + g.tiles - 1, last = end - ((end ^ wg) & 1);  // this warpgroup's last tile
       if (last >= T0) ok = ok && !left && tree_warp_wait(bar(C::B_PDONE + last % C::NB), uint32_t(last / C::NB) & 1u, abort_flag, 21);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
@@ -843,38 +841,31 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
           y.x += __shfl_xor_sync(0xffffffffu, y.x, o);
           y.y += __shfl_xor_sync(0xffffffffu, y.y, o);
         }
-        if (g4 == 0) *reinterpret_cast<float2*>(warps + w4 * ROWS + 8 * k + 2 * i4) = y;
-        if (g4 == 0 && w4 == 0) *reinterpret_cast<float2*>(refs + wg * ROWS + 8 * k + 2 * i4) = m2[k];
+        if (g4 == 0) *reinterpret_cast<float2*>(warps + w4 * N + 8 * k + 2 * i4) = y;
+        if (g4 == 0 && w4 == 0) *reinterpret_cast<float2*>(refs + wg * N + 8 * k + 2 * i4) = m2[k];
       }
       if (meet_all(!ok)) break;
       constexpr int OUT = N / C::GROUPS;  // rows that a warpgroup writes
       const bool whole = g.slot < 0;
       const int tid = w4 * 32 + lane, row = wg * OUT + tid;  // of the tile, for the first OUT threads
       if (tid < OUT) {
-        float m = -INFINITY, sum = 0.f, part[2] = {0.f, 0.f};
+        float m = -INFINITY, sum = 0.f, part[2];
         const float* const all = reinterpret_cast<const float*>(sbase + C::OFF_MAX);
-        if constexpr (C::TURNS) {
-          float its[2], half[2];
+        float its[2], half[2];
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const float* const w = all + x * 4 * N + row;
-            its[x] = (w[0] + w[N]) + (w[2 * N] + w[3 * N]);
-            half[x] = -refs[x * N + row];
-            m = fmaxf(m, half[x]);
-          }
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            half[x] = half_factor(half[x], m);
-            sum += its[x] * half[x] * half[x];
-            part[x] = half[x] * half[x];
-          }
-        } else {
-          const float* const w = all + wg * 4 * ROWS + tid;
-          sum = (w[0] + w[ROWS]) + (w[2 * ROWS] + w[3 * ROWS]);
-          m = -refs[wg * ROWS + tid];
-          part[0] = 1.f;
+        for (int x = 0; x < 2; ++x) {
+          const float* const w = all + x * 4 * N + row;
+          its[x] = (w[0] + w[N]) + (w[2 * N] + w[3 * N]);
+          half[x] = -refs[x * N + row];
+          m = fmaxf(m, half[x]);
         }
-        const int rg = g.row0 + row, node = rg / p.G, head = g.h * p.G + rg - node * p.G, at = g.q0 + node;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          half[x] = half_factor(half[x], m);
+          sum += its[x] * half[x] * half[x];
+          part[x] = half[x] * half[x];
+        }
+        const int node = row / p.G, head = g.h * p.G + row - node * p.G, at = g.q0 + node;
         if (row < g.rows) {
           if (whole)
             a.lse[int64_t(head) * a.total_tokens + at] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
@@ -890,14 +881,14 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
       ptx::tc_fence_after();
       const int first = row - tid;
       // (the other warpgroup's O, of which its factor is 0 where it had no tile and there is nothing)
-      const uint32_t o_mine = o_seg + (C::TURNS ? uint32_t((T0 & 1) * N) : 0u);
-      const uint32_t o_other = o_seg + (C::TURNS ? uint32_t(((T0 + (g.tiles > 1)) & 1) * N) : 0u);
+      const uint32_t o_mine = o_seg + uint32_t((T0 & 1) * N);
+      const uint32_t o_other = o_seg + uint32_t(((T0 + (g.tiles > 1)) & 1) * N);
       uint8_t* const to = (whole ? static_cast<uint8_t*>(a.o) : reinterpret_cast<uint8_t*>(p.part_o)) + tid * (whole ? 2 : 4);
 #pragma unroll 1
       for (int q = first; q < first + OUT; q += 4) {
         uint32_t w[2][4];
         ptx::tmem_ld4(o_mine + q, w[0]);
-        if (C::TURNS) ptx::tmem_ld4(o_other + q, w[1]);
+        ptx::tmem_ld4(o_other + q, w[1]);
         ptx::tmem_wait_ld();
         if (q + 4 == first + OUT) {
           ptx::tc_fence_before();
@@ -906,8 +897,8 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float4 x = out[q + i];
-          float y = __uint_as_float(w[0][i]) * ((T0 & 1) && C::TURNS ? x.y : x.x);
-          if (C::TURNS) y = fmaf(__uint_as_float(w[1][i]), g.tiles == 1 ? 0.f : (T0 & 1) ? x.x : x.y, y);
+          float y = __uint_as_float(w[0][i]) * (T0 & 1 ? x.y : x.x);
+          y = fmaf(__uint_as_float(w[1][i]), g.tiles == 1 ? 0.f : (T0 & 1) ? x.x : x.y, y);
           uint8_t* const at = to + (uint64_t(__float_as_uint(x.w)) << 32 | __float_as_uint(x.z));
           const bool on = q + i < g.rows && w4 * 32 < D;
           if (on && whole) *reinterpret_cast<__nv_bfloat16*>(at) = __float2bfloat16_rn(y);
@@ -943,22 +934,22 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_tree_join_kernel(const 
   const bool mine = good && r.len >= r.n && i < r.n * a.num_heads;
   const int head = i % a.num_heads, row = (i / a.num_heads) * p.G + head % p.G;
   const int U = mine ? tiles_of(r) : 0;
-  // the line before this (sequence, head, tile of rows); the division is the other kernel's
+  // the line before this (sequence, head); the division is the other kernel's
   int all = 0, first = 0;
 #pragma unroll 1
   for (int x = 2 * lane; x < a.cache.batch; x += 64) {
-    const int n0 = units_of<N>(p, x), n1 = units_of<N>(p, x + 1);
+    const int n0 = units_of(p, x), n1 = units_of(p, x + 1);
     all += n0 + n1;
     first += (x < b ? n0 : 0) + (x + 1 < b ? n1 : 0);
   }
   all = __reduce_add_sync(0xffffffffu, all);
   first = __reduce_add_sync(0xffffffffu, first);
-  if (mine) first += (head / p.G * row_tiles(r, p.G, N) + row / N) * U;
+  if (mine) first += head / p.G * U;
   const int piece = tree_share(all, p);
   const int c0 = first / piece, c1 = (first + U - 1) / piece;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!mine || c0 == c1) return;  // finished by its CTA
-  auto at = [&](int j) { return int64_t(2 * (c0 + j) + (j == 0 ? 1 : 0)) * N + row % N; };
+  auto at = [&](int j) { return int64_t(2 * (c0 + j) + (j == 0 ? 1 : 0)) * N + row; };
   join_row<D, W>(p, c1 - c0 + 1, at, r.q0 + i / a.num_heads, head, w, lane, shared);
 }
 
