@@ -21,8 +21,10 @@ LIB_PATH = os.path.join(PKG, LIB_NAME)
 
 SOURCES = ["api.cu", "blockmask.cu", "blockmask_noalloc.cu", "attn_fwd_bf16.cu", "attn_fwd_f32.cu",
            "attn_bwd_bf16.cu", "cache_api.cu", "rope.cu", "cache_append.cu", "cache_attn.cu", "cache_chunk.cu",
-           "cache_weights.cu", "cache_weights_many.cu", "cache_evict.cu", "cache_append_rope.cu", "cache_tree.cu", "tree.cu"]
-HEADERS = ["common.cuh", "ptx.cuh", "tile_pipeline.cuh", "cache.cuh", "cache_rows.cuh", "cache_tiles.cuh", "cache_join.cuh", "rope.cuh"]
+           "cache_weights.cu", "cache_weights_many.cu", "cache_evict.cu", "cache_append_rope.cu", "cache_tree.cu",
+           "cache_tree_many.cu", "tree.cu"]
+HEADERS = ["common.cuh", "ptx.cuh", "tile_pipeline.cuh", "cache.cuh", "cache_rows.cuh", "cache_tiles.cuh", "cache_join.cuh", "cache_tree.cuh",
+           "rope.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",

@@ -149,7 +149,7 @@ attn_status launch_cache_append(const AppendArgs& a, cudaStream_t s);
 attn_status launch_cache_append_rope(const AppendArgs& kv, const RopeArgs& q, const attn_rope_plan& plan, cudaStream_t s);
 uint64_t cache_fwd_workspace(const CacheView& c, int total_tokens, int num_heads, int max_new, int max_seqlen);
 attn_status launch_cache_fwd(const CacheQueryArgs& a, cudaStream_t s);
-attn_status launch_cache_chunk(const CacheAttnParams& p, const TreeMasks* tree, cudaStream_t s);
+attn_status launch_cache_chunk(const CacheAttnParams& p, cudaStream_t s);
 attn_status launch_cache_weights(const CacheQueryArgs& a, cudaStream_t s);
 attn_status launch_cache_weights_many(const CacheQueryArgs& a, int sms, cudaStream_t s);
 attn_status launch_cache_evict(const EvictArgs& a, cudaStream_t s);
@@ -158,7 +158,7 @@ attn_status launch_tree_keep(const TreeKeepArgs& a, cudaStream_t s);
 uint64_t cache_tree_workspace(const CacheView& c, int total_tokens, int num_heads, int max_new, int max_seqlen);
 attn_status launch_cache_tree(const CacheQueryArgs& a, const TreeMasks& tree, cudaStream_t s);
 // The same by the kernel of many rows.
-uint64_t cache_tree_many_workspace(const CacheView& c, int total_tokens, int num_heads, int max_new, int max_seqlen);
+uint64_t cache_tree_many_workspace(const CacheView& c);
 attn_status launch_cache_tree_many(const CacheQueryArgs& a, const TreeMasks& tree, cudaStream_t s);
 
 // ---------------------------------------------------------------- device side

@@ -503,12 +503,12 @@ int team_of(const CacheQueryArgs& a) {
 // ms -> 0.51 GB and 3.6 ms; 16384 new 8.7 GB and 30.3 ms -> none and 24.9 ms.)
 // The number of SMs only sizes the work, and the size query runs without a
 // device, so it is that of the GPU this library is built for.
-void plan(CacheAttnParams* p, bool many_anyway = false) {
+void plan(CacheAttnParams* p) {
   constexpr int kSms = 152;
   const CacheQueryArgs& a = p->a;
   p->G = a.num_heads / a.cache.heads;
   const int64_t rows = int64_t(a.max_new) * p->G;
-  p->many = many_anyway || rows > kFewRows;
+  p->many = rows > kFewRows;
   p->team = team_of(a);
   p->ctas = p->team ? a.cache.batch * a.cache.heads * p->team : 3 * kSms;  // (three per SM are resident at once)
   p->row_tiles = int((rows + kManyRows - 1) / kManyRows);
@@ -610,7 +610,7 @@ attn_status launch_cache_fwd(const CacheQueryArgs& a, cudaStream_t s) {
   const int d = a.cache.head_dim;
   cudaError_t e = cudaSuccess;
   if (p.many) {
-    const attn_status st = launch_cache_chunk(p, nullptr, s);
+    const attn_status st = launch_cache_chunk(p, s);
     if (st != ATTN_OK) return st;
   } else {
     e = d == 32 ? launch_few<32>(p, s) : d == 64 ? launch_few<64>(p, s) : launch_few<128>(p, s);
@@ -618,33 +618,6 @@ attn_status launch_cache_fwd(const CacheQueryArgs& a, cudaStream_t s) {
   if (e == cudaSuccess && partial > 0)
     e = d == 32 ? launch_join<32>(p, s) : d == 64 ? launch_join<64>(p, s) : launch_join<128>(p, s);
   return e == cudaSuccess ? ATTN_OK : record_cuda_error(e, "attn_cache_fwd launch");
-}
-
-// Trees of more rows than cache_tree.cu takes.
-uint64_t cache_tree_many_workspace(const CacheView& c, int total_tokens, int num_heads, int max_new, int max_seqlen) {
-  CacheAttnParams p;
-  p.a.cache = c;
-  p.a.total_tokens = total_tokens;
-  p.a.num_heads = num_heads;
-  p.a.max_new = max_new;
-  p.a.max_seqlen = max_seqlen;
-  plan(&p, true);
-  return partial_rows(p) * (uint64_t(c.head_dim) * 4 + 8);
-}
-
-attn_status launch_cache_tree_many(const CacheQueryArgs& a, const TreeMasks& tree, cudaStream_t s) {
-  CacheAttnParams p;
-  p.a = a;
-  plan(&p, true);
-  p.scale_log2 = a.scale * 1.4426950408889634f;
-  const uint64_t partial = partial_rows(p);
-  p.part_o = a.workspace;
-  p.part_m = reinterpret_cast<float2*>(a.workspace + partial * uint64_t(a.cache.head_dim));
-  const attn_status st = launch_cache_chunk(p, &tree, s);
-  if (st != ATTN_OK || partial == 0) return st;
-  const int d = a.cache.head_dim;
-  const cudaError_t e = d == 32 ? launch_join<32>(p, s) : d == 64 ? launch_join<64>(p, s) : launch_join<128>(p, s);
-  return e == cudaSuccess ? ATTN_OK : record_cuda_error(e, "attn_cache_tree_fwd join launch");
 }
 
 }  // namespace attnmask

@@ -46,14 +46,11 @@
 // an earlier step's events of the others, or for this step's by a role that
 // comes before it (pages, keys / values, S, softmax, P V), so the order of steps
 // carries every wait to its end.
-#include <type_traits>
-
 #include "cache_tiles.cuh"
 
 namespace attnmask {
 namespace {
 
-struct NoTree {};
 constexpr int kChunkThreads = 512;
 constexpr int kWarpValues = 8, kWarpKeys = 12, kWarpS = 13, kWarpPV = 15;
 constexpr int kStep = 64;  // tokens per step
@@ -92,7 +89,7 @@ struct ChunkCfg {
 
 // The sums of a step's far blocks, from the scores as they lie; not inlined, to keep
 // the softmax's loop short.
-__device__ __noinline__ float far_sums(uint32_t s_col, const float4* sc, float qscale, float ref, uint64_t seen) {
+__device__ __noinline__ float far_sums(uint32_t s_col, const float4* sc, float qscale, float ref, int seen) {
   float sum = 0.f;
 #pragma unroll 1
   for (int q = 0; q < 4; ++q) {
@@ -104,33 +101,16 @@ __device__ __noinline__ float far_sums(uint32_t s_col, const float4* sc, float q
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
       const float y = ptx::ex2(0.5f * fmaf(__uint_as_float(v[e]), f, -ref));
-      if (seen >> (16 * q + e) & 1u) sum = fmaf(y, y, sum);
+      if (16 * q + e < seen) sum = fmaf(y, y, sum);
     }
   }
   return sum;
 }
 
-// A drafted tree's masks (cache_tree.cu): which of the 64 tokens from `first` on a row sees.
-// The text is seen, and of the nodes, numbers from first - text on, those of its bits.
-__device__ __forceinline__ uint64_t tree_step(const uint32_t* bits, int first, int text, int nodes) {
-  uint64_t seen = first >= text ? 0ull : text - first >= kStep ? ~0ull : (1ull << (text - first)) - 1;
-  const int node = first - text;  // of the first token; negative in the text
-#pragma unroll 1
-  for (int w = max(node, 0) / 32; 32 * w < min(node + kStep, nodes); ++w) {
-    uint64_t x = __ldg(bits + w);
-    if (nodes - 32 * w < 32) x &= (1ull << (nodes - 32 * w)) - 1;
-    const int to = 32 * w - node;  // its first bit's place
-    seen |= to >= 0 ? x << to : x >> -to;
-  }
-  return seen;
-}
-
-// MASK: NoTree, or the masks of a drafted tree, whose rows a.causal is not set for.
-template <int D, typename MASK>
+template <int D>
 __global__ void __launch_bounds__(kChunkThreads, 1)
     cache_chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                       const __grid_constant__ CacheAttnParams p, const __grid_constant__ MASK mask) {
-  constexpr bool kTree = std::is_same<MASK, TreeMasks>::value;
+                       const __grid_constant__ CacheAttnParams p) {
   using C = ChunkCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -141,10 +121,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const int h = blockIdx.y, b = blockIdx.z;
   SeqRows r;
   if (!load_rows(a.cu, a.lens, b, a.total_tokens, a.max_new, a.max_seqlen, c.status, r)) return;
-  if (kTree && r.len < r.n) {
-    if (threadIdx.x == 0) atomicOr(c.status, kErrHeld);
-    return;
-  }
   const int rows = min(kManyRows, r.n * p.G - row0);
   if (rows <= 0) return;
   const int limit = visible_tokens(r, p.G, row0 + rows - 1, a.causal);
@@ -396,7 +372,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const int head = h * p.G + (real ? rg % p.G : 0);
     // (a lane without a row hides nothing: one hidden score sends its warp the slow way)
     const int visible = real ? visible_tokens(r, p.G, rg, a.causal) : limit;
-    const int text = kTree ? r.len - r.n : 0;
     const bool idle = rg - lane >= r.n * p.G;     // a warp without rows only keeps the steps' order
 
     const float qscale =
@@ -432,22 +407,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       ptx::tmem_ld32(s_col + 32, s[1]);
       const float4* sc = scl + ss * 8 + 4 * f;
       const int seen = visible - (begin + i * kStep);  // columns [0, seen) are visible
-      const int whole = kTree ? text - (begin + i * kStep) : seen;  // those that hide nothing from any row
       const int odd = __float_as_int(sc[0].w) | __float_as_int(sc[1].w) | __float_as_int(sc[2].w) | __float_as_int(sc[3].w);
       ptx::tmem_wait_ld();
-      if (kTree && (whole < kStep || odd < 0)) {
-        uint64_t see = real ? 0ull : ~0ull;
-        if constexpr (kTree) {
-          if (real) see = tree_step(mask.bits + token * mask.words, begin + i * kStep, text, r.n);
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t part = __float_as_int(sc[q].w) < 0 ? 0u : uint32_t(see >> (16 * q)) & 0xFFFFu;
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (!(part >> e & 1u)) s[q >> 1][(q & 1) * 16 + e] = 0xFF800000u;  // -inf
-        }
-      } else if (!kTree && (__any_sync(0xffffffffu, seen < kStep) || odd < 0)) {
+      if (__any_sync(0xffffffffu, seen < kStep) || odd < 0) {
         // hidden: the lowest score, whatever lay there
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -493,13 +455,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             ptx::tmem_st16(o_col + q * 16, v);
           }
         }
-        if (odd & kFar) {
-          uint64_t see = seen <= 0 ? 0ull : seen >= kStep ? ~0ull : (1ull << seen) - 1;
-          if constexpr (kTree) {
-            if (real) see = tree_step(mask.bits + token * mask.words, begin + i * kStep, text, r.n);
-          }
-          l2.x += far_sums(s_col, sc, qscale, mx == -INFINITY ? 0.f : mx, see);
-        }
+        if (odd & kFar) l2.x += far_sums(s_col, sc, qscale, mx == -INFINITY ? 0.f : mx, seen);
       }
       const float ref = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
@@ -632,35 +588,30 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   }
 }
 
-template <int D, typename MASK>
-attn_status launch_d(const CacheAttnParams& p, const MASK& mask, cudaStream_t s) {
+template <int D>
+attn_status launch_d(const CacheAttnParams& p, cudaStream_t s) {
   using C = ChunkCfg<D>;
   const CacheView& c = p.a.cache;
   CUtensorMap map, map_v;
   if (!encode_pages<D>(&map, c, c.k_pages, true) || !encode_pages<D>(&map_v, c, c.v_pages, false))
     return record_cuda_error(cudaErrorInvalidValue, "attn_cache_fwd tensor map encoding");
-  cudaError_t e = cudaFuncSetAttribute(cache_chunk_kernel<D, MASK>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  cudaError_t e = cudaFuncSetAttribute(cache_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return record_cuda_error(e, "attn_cache_fwd configure");
   const dim3 grid(unsigned(p.splits) * unsigned(p.row_tiles), unsigned(c.heads), unsigned(c.batch));
-  cache_chunk_kernel<D, MASK><<<grid, kChunkThreads, C::SMEM, s>>>(map, map_v, p, mask);
+  cache_chunk_kernel<D><<<grid, kChunkThreads, C::SMEM, s>>>(map, map_v, p);
   e = cudaGetLastError();
   return e == cudaSuccess ? ATTN_OK : record_cuda_error(e, "attn_cache_fwd launch");
 }
 
-template <typename MASK>
-attn_status launch(const CacheAttnParams& p, const MASK& mask, cudaStream_t s) {
-  switch (p.a.cache.head_dim) {
-    case 32: return launch_d<32>(p, mask, s);
-    case 64: return launch_d<64>(p, mask, s);
-    case 128: return launch_d<128>(p, mask, s);
-  }
-  return ATTN_ERR_UNSUPPORTED;
-}
-
 }  // namespace
 
-attn_status launch_cache_chunk(const CacheAttnParams& p, const TreeMasks* tree, cudaStream_t s) {
-  return tree ? launch(p, *tree, s) : launch(p, NoTree{}, s);
+attn_status launch_cache_chunk(const CacheAttnParams& p, cudaStream_t s) {
+  switch (p.a.cache.head_dim) {
+    case 32: return launch_d<32>(p, s);
+    case 64: return launch_d<64>(p, s);
+    case 128: return launch_d<128>(p, s);
+  }
+  return ATTN_ERR_UNSUPPORTED;
 }
 
 }  // namespace attnmask

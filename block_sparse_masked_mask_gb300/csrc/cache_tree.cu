@@ -48,54 +48,12 @@
 #include <cmath>
 
 #include "cache_join.cuh"
-#include "cache_tiles.cuh"
+#include "cache_tree.cuh"
 
 namespace attnmask {
 namespace {
 
-constexpr int kNoPage = INT_MIN, kFar = 1;  // of a block of 16 tokens, as in cache_chunk.cu
-constexpr int kTreeSms = 152;
 constexpr float kNoReference = -0x1p100f;   // of a row that has seen nothing yet
-
-// A constant that the compiler does not see: it would else copy a loop's body for its first turn.
-__device__ __forceinline__ uint32_t opaque(uint32_t x) {
-  asm volatile("" : "+r"(x));
-  return x;
-}
-
-// The bounded waits of tile_pipeline.cuh in the few instructions that five roles at once
-// leave room for: with 100 KB of code in all, warps waited for instructions more than for
-// anything else.  What runs out is left in *abort_flag, the site plus 1, and
-// becomes the status at the kernel's end.
-__device__ __forceinline__ bool tree_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, int site) {
-  bool ok = ptx::mbar_try_wait(bar, parity);
-  if (__builtin_expect(!ok, 0)) {
-    const uint32_t t0 = ptx::globaltimer_lo();
-    while (true) {
-      ok = ptx::mbar_try_wait(bar, parity);
-      if (ok || *abort_flag) break;
-      if (ptx::globaltimer_lo() - t0 > uint32_t(kWaitTimeoutNs)) {
-        *abort_flag = uint32_t(site) + 1u;
-        break;
-      }
-    }
-  }
-  return ok;
-}
-static_assert(kWaitTimeoutNs < (1ull << 32), "of a 32-bit clock");
-__device__ __forceinline__ bool tree_warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, int site) {
-  return __all_sync(0xffffffffu, tree_wait(bar, parity, abort_flag, site));
-}
-
-struct TreeParams {
-  CacheQueryArgs a;
-  TreeMasks tree;
-  int G;
-  int ctas, least;  // least: tiles of a CTA's piece
-  float scale_log2;
-  float* part_o;    // [2 * ctas][N] rows of head_dim, as for few rows in cache_attn.cu
-  float2* part_m;
-};
 
 // A piece of the line in one (sequence, head).
 struct Segment {
@@ -115,7 +73,7 @@ __device__ __forceinline__ int units_of(const TreeParams& p, int b) {
   return good && n > 0 ? (len + kTile - 1) / kTile * a.cache.heads : 0;
 }
 __device__ __forceinline__ int tree_share(int total, const TreeParams& p) {
-  return max(p.least, (total + p.ctas - 1) / p.ctas);
+  return max(1, (total + p.ctas - 1) / p.ctas);
 }
 
 // E 16-bit rows of 128 tokens (P^T): MN-major, swizzled over a token's width.
@@ -1006,7 +964,7 @@ attn_status launch_d(TreeParams& p, int N, cudaStream_t s) {
 uint64_t cache_tree_workspace(const CacheView& c, int total_tokens, int num_heads, int max_new, int max_seqlen) {
   if (total_tokens == 0 || max_new == 0) return 0;
   const int N = padded_rows(c, num_heads, max_new);
-  if (N == 0) return cache_tree_many_workspace(c, total_tokens, num_heads, max_new, max_seqlen);
+  if (N == 0) return cache_tree_many_workspace(c);
   return partial_rows(N) * (uint64_t(c.head_dim) * 4 + 8);
 }
 
@@ -1018,7 +976,6 @@ attn_status launch_cache_tree(const CacheQueryArgs& a, const TreeMasks& tree, cu
   p.tree = tree;
   p.G = a.num_heads / a.cache.heads;
   p.ctas = kTreeSms;
-  p.least = 1;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.part_o = a.workspace;
   p.part_m = reinterpret_cast<float2*>(a.workspace + partial_rows(N) * a.cache.head_dim);
