@@ -152,7 +152,7 @@ struct ManyCfg {
   static constexpr int KT = CodeTile<D>::BYTES;  // a tile of codes: keys, values or half a query
   static constexpr int VT = V::TILE;
   static constexpr int NK = 2, NR = 2, NV = 2, NSCL = 8, NSEG = 4;
-  static constexpr int OFF_Q = 0;                // [M tile][hi, lo]; at a segment's end half of each one's O
+  static constexpr int OFF_Q = 0;                // [M tile][hi, lo]
   static constexpr int OFF_K = OFF_Q + 4 * KT;
   static constexpr int OFF_R = OFF_K + NK * KT;  // the values' codes
   static constexpr int OFF_V = OFF_R + NR * KT;
@@ -165,10 +165,10 @@ struct ManyCfg {
                        B_KFREE = B_KFULL + NK, B_RFULL = B_KFREE + NK, B_RFREE = B_RFULL + NR, B_VFULL = B_RFREE + NR,
                        B_VFREE = B_VFULL + NV, B_SCLFULL = B_VFREE + NV, B_SCLFREE = B_SCLFULL + NSCL,
                        B_SFULL = B_SCLFREE + NSCL, B_PFULL = B_SFULL + 4, B_PDONE = B_PFULL + 4, B_OFREE = B_PDONE + 4,
-                       B_DRAIN = B_OFREE + 2, NBAR = B_DRAIN + 3;
+                       B_DRAIN = B_OFREE + 1, NBAR = B_DRAIN + 3;
   static_assert(NBAR <= THREADS, "a thread for each");
   __device__ static int arrivals(int i) {
-    return i >= B_OFREE ? (i >= B_DRAIN ? 1 : 4)
+    return i >= B_OFREE ? (i >= B_DRAIN ? 1 : 8)
            : i >= B_PFULL ? (i >= B_PDONE ? 1 : 4)
            : i >= B_SCLFREE ? (i >= B_SFULL ? 1 : 12)  // softmax (twice by those of one M tile alone) and value warps
            : i >= B_SCLFULL ? 1
@@ -291,6 +291,16 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
         }
         __syncwarp();
         if (g.tiles == 0) break;
+        // queries and masks on their way to L2
+#pragma unroll 1
+        for (int x = lane; x < g.rows; x += 32) {
+          const int rg = g.row0 + x, node = rg / p.G;
+          const int64_t token = g.q0 + node;
+          const char* row = static_cast<const char*>(a.q) + (token * a.num_heads + g.h * p.G + rg - node * p.G) * (2 * D);
+#pragma unroll
+          for (int y = 0; y < 2 * D; y += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + y));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(p.tree.bits + token * p.tree.words));
+        }
       }
       // what is wrong with the sequences is noted once, when nobody waits for it
       if (blockIdx.x == 0) {
@@ -438,9 +448,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
         for (int s = 0; ok && segment(s, g, true) && g.tiles; ++s) {
           const bool twin = g.rows <= kTile;
           // the segment before has read its O
-          if (s > 0)
-            ok = tree_wait(bar(C::B_OFREE), uint32_t(s - 1) & 1u, abort_flag, 9) &&
-                 tree_wait(bar(C::B_OFREE + 1), uint32_t(s - 1) & 1u, abort_flag, 9);
+          if (s > 0) ok = tree_wait(bar(C::B_OFREE), uint32_t(s - 1) & 1u, abort_flag, 9);
 #pragma unroll 1
           for (int j = 0; ok && j < g.tiles; ++j, ++T) {
             const int vs = T % C::NV, first = twin ? j & 1 : 0, last = twin ? first : 1;
@@ -539,7 +547,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
 #pragma unroll 1
     for (int s = 0;; ++s) {
       ok = ok && segment(s, g, false);
-      // (and nobody reads the other M tile's place of the queries any more)
+      // (and both M tiles' products have used the queries)
       if (meet(!ok) || g.tiles == 0) break;
       const bool twin = g.rows <= kTile;
       const int mine = (twin ? 0 : m * kTile) + row;  // of the segment's rows
@@ -723,28 +731,12 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
       ok = ok && (!had || tree_warp_wait(bar(C::B_PDONE + 2 * m + 1), uint32_t(turn - 1) & 1u, abort_flag, 17));
       ptx::tc_fence_after();
       float l = l2.x + l2.y;
-      // Of rows that both M tiles hold, each ends half of the dimensions, and leaves the other half of its
-      // O where the queries were, once both have used them.  Lanes are rows.
-      float4* const own = reinterpret_cast<float4*>(sbase + C::OFF_Q + 2 * m * C::KT);
-      const float4* const other = reinterpret_cast<const float4*>(sbase + C::OFF_Q + 2 * (1 - m) * C::KT);
+      // Of rows that both M tiles hold, in the same lanes of tensor memory, each ends half of the dimensions.
       float ours = 1.f, theirs = 0.f;  // factors of the two
       if (twin) {
-        if (meet(!ok)) break;
         stats[m * kTile + row] = make_float2(mx, l);
-        if (had) {
-#pragma unroll 1
-          for (int q = 0; q < D / 32; ++q) {
-            uint32_t v[16];
-            ptx::tmem_ld16(o_col + uint32_t((1 - m) * (D / 2) + q * 16), v);
-            ptx::tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              own[(4 * q + e) * kTile + row] =
-                  make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]), __uint_as_float(v[4 * e + 2]),
-                              __uint_as_float(v[4 * e + 3]));
-          }
-        }
-        meet(false);
+        if (meet(!ok)) break;
+        ptx::tc_fence_after();
         const float2 ml = stats[(1 - m) * kTile + row];
         const float top = fmaxf(mx, ml.x);
         const float half = half_factor(mx, top), other_half = half_factor(ml.x, top);
@@ -762,33 +754,28 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
       const int from = twin ? m * (D / 2) : 0, count = twin ? D / 32 : D / 16;
 #pragma unroll 1
       for (int q = 0; q < count; ++q) {
-        uint32_t v[16];
+        uint32_t v[16], y[16];
         ptx::tmem_ld16(o_col + uint32_t(from + q * 16), v);
+        if (twin) ptx::tmem_ld16((o_col ^ 128u) + uint32_t(from + q * 16), y);
         ptx::tmem_wait_ld();
         if (q == count - 1) {
           ptx::tc_fence_before();
-          warp_arrive(bar(C::B_OFREE + m), lane);
+          warp_arrive(bar(C::B_OFREE), lane);
         }
         // (nothing has been written where an M tile had no tile, or has no weight yet)
 #pragma unroll
         for (int e = 0; e < 16; ++e) v[e] = had && ours != 0.f ? __float_as_uint(__uint_as_float(v[e]) * ours) : 0u;
         if (twin && theirs != 0.f && 1 - m < g.tiles) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float4 x = other[(4 * q + e) * kTile + row];
-            v[4 * e] = __float_as_uint(fmaf(x.x, theirs, __uint_as_float(v[4 * e])));
-            v[4 * e + 1] = __float_as_uint(fmaf(x.y, theirs, __uint_as_float(v[4 * e + 1])));
-            v[4 * e + 2] = __float_as_uint(fmaf(x.z, theirs, __uint_as_float(v[4 * e + 2])));
-            v[4 * e + 3] = __float_as_uint(fmaf(x.w, theirs, __uint_as_float(v[4 * e + 3])));
-          }
+          for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(fmaf(__uint_as_float(y[e]), theirs, __uint_as_float(v[e])));
         }
         if (real && whole) {
           uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + (token * a.num_heads + head) * D + from + q * 16);
-          uint32_t y[8];
+          uint32_t w[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = ptx::pack_bf16(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-          out[0] = make_uint4(y[0], y[1], y[2], y[3]);
-          out[1] = make_uint4(y[4], y[5], y[6], y[7]);
+          for (int i = 0; i < 8; ++i) w[i] = ptx::pack_bf16(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+          out[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          out[1] = make_uint4(w[4], w[5], w[6], w[7]);
         } else if (real) {
           // four dimensions of all rows together
           uint4* out = reinterpret_cast<uint4*>(p.part_o) + (int64_t(g.slot) * (D / 4) + from / 4 + q * 4) * kTreeRows + mine;
