@@ -19,7 +19,7 @@
 //  * The masks matter in the tiles that hold the tree (and at the end of a sequence): only there
 //    hidden scores are overwritten, in tensor memory, before the loop that all tiles share.
 // Work: tiles of 128 tokens of all (sequence, head)s form one line that is cut evenly among one
-// CTA per SM; a CTA's piece is walked segment by segment without a pause between them: the
+// CTA per SM (TreeLine in cache_tree.cuh); a CTA's piece is walked segment by segment without a pause between them: the
 // rings of tiles run on, queries and O have two buffers each.  Segments that are
 // not whole meet in a second kernel (cache_join.cuh), two per CTA at most.
 // Warps (512 threads):
@@ -30,8 +30,8 @@
 //   15         the line: the CTA's segments
 //
 // What bounds it: 64 trees of 4 to 8 nodes behind 1024 to 16384 tokens, 32 query and 8 key heads of
-// 128, take 166 us where the bytes take 108 at the rate of a copy; 16 sequences of 8192 tokens, 16 / 32 / 64
-// rows a head, 54 / 61 / 70 us (40).  It is the instructions'
+// 128, take 139 us where the bytes take 108 at the rate of a copy; 16 sequences of 8192 tokens, 16 / 32 / 64
+// rows a head, 55 / 58 / 73 us (40).  It is the instructions'
 // supply more than their issue: with five roles' loops at once, warps wait for instructions
 // more than for anything else, and each step that made the code shorter (loops rolled up, one form of
 // waits, rare paths out of line) was worth more than one that took operations out.  Four
@@ -61,20 +61,11 @@ struct Segment {
   int b, h, rows, q0, n, len, token, slot;  // slot of the partial result, -1: whole
 };
 
-__device__ __forceinline__ int tiles_of(const SeqRows& r) { return r.n == 0 ? 0 : (r.len + kTile - 1) / kTile; }
-
-// Tiles of sequence b, all heads; 0 where its numbers cannot be used.
-__device__ __forceinline__ int units_of(const TreeParams& p, int b) {
-  const CacheQueryArgs& a = p.a;
-  if (b >= a.cache.batch) return 0;
-  const int q0 = a.cu[b], q1 = a.cu[b + 1], len = a.lens[b], n = q1 - q0;
-  const bool good = q0 >= 0 && q1 >= q0 && q1 <= a.total_tokens && (b > 0 || q0 == 0) && n <= a.max_new && len >= n &&
-                    len <= a.max_seqlen;
-  return good && n > 0 ? (len + kTile - 1) / kTile * a.cache.heads : 0;
-}
-__device__ __forceinline__ int tree_share(int total, const TreeParams& p) {
-  return max(1, (total + p.ctas - 1) / p.ctas);
-}
+// A segment's start and end cost as much as three tiles (64 trees of 4 to 8 nodes: taken for 0 156 us, 2 139, 4 140,
+// 7 145, 11 152); pieces of less than two tiles' cost gain nothing (a tree of 16 nodes behind 1024
+// tokens: from 1 17.4 us, 2 16.5, 4 17.9, 6 19.4).
+template <int N>
+using Line = TreeLine<N, 1, 1, 3, 2>;
 
 // E 16-bit rows of 128 tokens (P^T): MN-major, swizzled over a token's width.
 template <int E>
@@ -200,68 +191,39 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
    ptx::regs_dec<C::REG_OTHERS>();
    if (warp == C::LINE) {
     // -------------------------------------------------------------- segments
-    // 64 sequences at a time, two neighbours per lane
-    int total = 0;
-#pragma unroll 1
-    for (int b0 = 0; b0 < c.batch; b0 += 64) total += units_of(p, b0 + 2 * lane) + units_of(p, b0 + 2 * lane + 1);
-    total = __reduce_add_sync(0xffffffffu, total);
-    const int piece = tree_share(total, p);
-    int pos = int(min(int64_t(blockIdx.x) * piece, int64_t(total)));
-    const int stop = min(pos + piece, total);
+    const int64_t total = Line<N>::total(p, lane), piece = Line<N>::share(total, p);
+    int64_t pos = min(int64_t(blockIdx.x) * piece, total);
+    const int64_t stop = min(pos + piece, total);
     // (after a wait that ran out in an earlier CTA there is nothing to do)
     if (*reinterpret_cast<volatile int32_t*>(err) & kErrTimeout) pos = stop;
-    int b = 0, before = 0;  // the sequence that pos belongs to, and the line before it
-#pragma unroll 1
-    while (pos < stop) {
-      const int n0 = units_of(p, b + 2 * lane), n1 = units_of(p, b + 2 * lane + 1);
-      int sum = n0 + n1;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += y;
-      }
-      const uint32_t past = __ballot_sync(0xffffffffu, before + sum > pos);
-      if (past == 0) {
-        b += 64;
-        before += __shfl_sync(0xffffffffu, sum, 31);
-        continue;
-      }
-      const int at = __ffs(past) - 1, skip = __shfl_sync(0xffffffffu, sum - n0 - n1, at), half = __shfl_sync(0xffffffffu, n0, at);
-      before += skip;
-      b += 2 * at;
-      if (before + half <= pos) {
-        before += half;
-        ++b;
-      }
-      break;
-    }
+    int64_t before = 0;
+    int b = pos < stop ? Line<N>::find(p, pos, lane, before) : 0;
 #pragma unroll 1
     for (int s = 0;; ++s) {
       Segment g{};
 #pragma unroll 1
       while (pos < stop) {
-        const int all = units_of(p, b);
+        const int64_t all = Line<N>::of(p, b);
         if (pos >= before + all) {
           before += all;
           ++b;
           continue;
         }
-        SeqRows r;
-        r.q0 = a.cu[b];
-        r.n = a.cu[b + 1] - r.q0;
-        r.len = a.lens[b];
-        const int U = tiles_of(r);
-        const int item = (pos - before) / U, u0 = (pos - before) % U, u1 = min(U, u0 + stop - pos);
+        const int q0 = a.cu[b], n = a.cu[b + 1] - q0, len = a.lens[b];
+        const typename Line<N>::Seq l(n, p.G, len);
+        const typename Line<N>::Item it(l, before, pos);
+        const int u0 = it.tiles(pos, l.U), u1 = it.tiles(stop, l.U);
+        pos = min(stop, it.end);
+        if (u1 <= u0) continue;
         g.tiles = u1 - u0;
         g.b = b;
-        g.h = item;
-        g.rows = r.n * p.G;
-        g.q0 = r.q0;
-        g.n = r.n;
-        g.len = r.len;
+        g.h = it.h;
+        g.rows = n * p.G;
+        g.q0 = q0;
+        g.n = n;
+        g.len = len;
         g.token = u0 * kTile;
-        g.slot = u0 == 0 && u1 == U ? -1 : 2 * int(blockIdx.x) + (u0 > 0 ? 0 : 1);
-        pos += u1 - u0;
+        g.slot = u0 == 0 && u1 == l.U ? -1 : 2 * int(blockIdx.x) + (u0 > 0 ? 0 : 1);
         break;
       }
       const int at = s % C::NSEG;
@@ -891,30 +853,36 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_tree_join_kernel(const 
   const bool good = load_rows(a.cu, a.lens, b, a.total_tokens, a.max_new, a.max_seqlen, a.cache.status, r, false);
   const bool mine = good && r.len >= r.n && i < r.n * a.num_heads;
   const int head = i % a.num_heads, row = (i / a.num_heads) * p.G + head % p.G;
-  const int U = mine ? tiles_of(r) : 0;
   // the line before this (sequence, head); the division is the other kernel's
-  int all = 0, first = 0;
+  int64_t all = 0, first = 0;
 #pragma unroll 1
-  for (int x = 2 * lane; x < a.cache.batch; x += 64) {
-    const int n0 = units_of(p, x), n1 = units_of(p, x + 1);
-    all += n0 + n1;
-    first += (x < b ? n0 : 0) + (x + 1 < b ? n1 : 0);
+  for (int x = lane; x < a.cache.batch; x += 32) {
+    const int64_t n = Line<N>::of(p, x);
+    all += n;
+    first += x < b ? n : 0;
   }
-  all = __reduce_add_sync(0xffffffffu, all);
-  first = __reduce_add_sync(0xffffffffu, first);
-  if (mine) first += head / p.G * U;
-  const int piece = tree_share(all, p);
-  const int c0 = first / piece, c1 = (first + U - 1) / piece;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+    first += __shfl_xor_sync(0xffffffffu, first, o);
+  }
+  const int64_t piece = Line<N>::share(all, p);
+  int c0 = 0, c1 = 0;
+  if (mine) {
+    const typename Line<N>::Seq l(r.n, p.G, r.len);
+    const typename Line<N>::Item it(l, 0, head / p.G * l.head());
+    c0 = int((first + it.first) / piece);
+    c1 = int((first + it.end - 1) / piece);
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!mine || c0 == c1) return;  // finished by its CTA
+  if (c0 == c1) return;  // finished by its CTA
   auto at = [&](int j) { return int64_t(2 * (c0 + j) + (j == 0 ? 1 : 0)) * N + row; };
   join_row<D, W>(p, c1 - c0 + 1, at, r.q0 + i / a.num_heads, head, w, lane, shared);
 }
 
-// Rows are padded to the least of these; 0: cache_chunk.cu takes them, 128 or 256 rows of a
-// sequence and head at a time (16 sequences of 8192 tokens, 8 heads, here / there: 16 rows 54 / 64 us, 32
-// 60 / 100, 64 70 / 108; in tiles of 128 rows, 128 112 / 121, 256 203 / 181; 32 of 1024 to 16384, 68 to 128
-// rows 196 / 159: with that many rows, the ones that pad them out cost more than is saved).
+// Rows are padded to the least of these; 0: cache_tree_many.cu takes them, 128 or 256 rows of a sequence
+// and head at a time (16 sequences of 8192 tokens, 8 heads: 64 rows 73 us here, 128 rows 89 us there; 128 rows
+// as N of the products here took 112).
 int padded_rows(const CacheView& c, int num_heads, int max_new) {
   const int64_t rows = int64_t(max_new) * (num_heads / c.heads);
   return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 0;

@@ -8,11 +8,15 @@
 // of the softmax owns a row, with its maximum and sum; scales and far pages are those of
 // cache_attn.cu.
 // What differs is the division.  Tiles of 128 tokens of all (sequence, head, 256 rows)s form one
-// line, a tile counted by what it costs, that is cut evenly among one CTA per SM.  A CTA walks
-// its piece segment by segment: page numbers, keys and values of the next one are under way while
-// the last one ends.  (With a CTA for each 4096 tokens, as in cache_chunk.cu, starts and ends took
-// a quarter of the time, and half of that again was uneven.)  Segments that are not
-// whole meet in a second kernel, two per CTA at most.
+// line, counted by what they cost, that is cut evenly among one CTA per SM (TreeLine in cache_tree.cuh).  A CTA
+// walks its piece segment by segment: page numbers, keys and values of the next one are under way while
+// the last one ends.  Segments that are not whole meet in a second kernel, two per CTA at most.
+// 32 trees of 17 to 32 nodes behind 1024 to 16384 tokens, 32 query and 8 key heads of 128, take 115 us, and
+// 8 trees of 48 to 64 nodes, 64 and 8 heads, behind 4096 to 16384 tokens 129 us (the kernel of
+// cache_chunk.cu with these masks, a CTA for 4096 tokens, took 155 and 157: starts and ends were a quarter of
+// it, and uneven).  Products of 128 rows fill the tensor cores to a half there; a tile takes about 1.4 us, most of it
+// the softmax's, which waits for its scores, its exponentials and the other warps' instructions in
+// turn; a segment's start and end about 9 us (queries as two numbers, O, the first scores).
 // Every tile is two steps of 64 tokens, whatever lies behind a sequence's end (weights of 0
 // times 0), so that each barrier's phases go on by one a tile.
 // Warps (640 threads):
@@ -37,93 +41,15 @@ namespace attnmask {
 namespace {
 
 constexpr int kTreeRows = 256;          // of a segment
-// What a tile of tokens costs, with up to 256 rows and with up to 128, and what a segment's start and end do
-constexpr int kTileCost = 5, kHalfCost = 3, kItemCost = 10;
+// What a tile of tokens costs, with up to 256 rows and with up to 128, and a segment's start and end
+// (32 trees of 17 to 32 nodes: 6 141 us, 10 129, 16 119, 20 115, 26 118, 34 122).
+using Line = TreeLine<kTreeRows, 5, 3, 20, 5>;
 constexpr int kStep = 64;
 
 // A piece of the line in one (sequence, head, 256 rows).
 struct Segment {
   int tiles;  // 0: there is no further one
   int b, h, row0, rows, q0, n, len, token, slot;  // slot of the partial result, -1: whole
-};
-
-// One sequence's part of the line.
-struct SeqLine {
-  int U, row_tiles, last;  // tiles of tokens, of rows; the last one's cost
-
-  __device__ __forceinline__ SeqLine(int n, int G, int len) {
-    const int64_t rows = int64_t(n) * G;
-    U = (len + kTile - 1) / kTile;
-    row_tiles = int((rows + kTreeRows - 1) / kTreeRows);
-    last = rows - int64_t(row_tiles - 1) * kTreeRows <= kTile ? kHalfCost : kTileCost;
-  }
-  // of one tile of rows but the last, and of one head
-  __device__ __forceinline__ int64_t item() const { return int64_t(U) * kTileCost + kItemCost; }
-  __device__ __forceinline__ int64_t head() const { return (row_tiles - 1) * item() + int64_t(U) * last + kItemCost; }
-  __device__ __forceinline__ int cost(int rt) const { return rt == row_tiles - 1 ? last : kTileCost; }
-};
-
-// Sequence b's, all heads; 0 where its numbers cannot be used.
-__device__ __forceinline__ int64_t line_of(const TreeParams& p, int b) {
-  const CacheQueryArgs& a = p.a;
-  if (b >= a.cache.batch) return 0;
-  const int q0 = a.cu[b], q1 = a.cu[b + 1], len = a.lens[b], n = q1 - q0;
-  const bool good = q0 >= 0 && q1 > q0 && q1 <= a.total_tokens && (b > 0 || q0 == 0) && n <= a.max_new && len >= n &&
-                    len <= a.max_seqlen;
-  return good ? SeqLine(n, p.G, len).head() * a.cache.heads : 0;
-}
-// The line's length, by whole warps, and a CTA's piece of it (at least a tile begins in each piece of an item
-// that goes on behind it).
-__device__ __forceinline__ int64_t line_total(const TreeParams& p, int lane) {
-  int64_t total = 0;
-#pragma unroll 1
-  for (int b = lane; b < p.a.cache.batch; b += 32) total += line_of(p, b);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  return total;
-}
-__device__ __forceinline__ int64_t line_share(int64_t total, const TreeParams& p) {
-  return max(int64_t(kTileCost), (total + p.ctas - 1) / p.ctas);
-}
-// The sequence that `pos` (below the total) belongs to, and the line before it.
-__device__ __forceinline__ int line_find(const TreeParams& p, int64_t pos, int lane, int64_t& before) {
-  before = 0;
-#pragma unroll 1
-  for (int b = 0;; b += 32) {
-    const int64_t n = line_of(p, b + lane);
-    int64_t sum = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += y;
-    }
-    const uint32_t past = __ballot_sync(0xffffffffu, before + sum > pos);
-    if (past || b + 32 >= p.a.cache.batch) {
-      const int at = past ? __ffs(past) - 1 : 31;
-      before += __shfl_sync(0xffffffffu, sum - n, at);
-      return b + at;
-    }
-    before += __shfl_sync(0xffffffffu, sum, 31);
-  }
-}
-// One (head, tile of rows) of a sequence on the line: where its first tile of tokens begins.
-struct Item {
-  int h, rt, w;   // w: cost of a tile
-  int64_t first, end;
-
-  __device__ __forceinline__ Item(const SeqLine& l, int64_t before, int64_t pos) {
-    h = int((pos - before) / l.head());
-    int64_t start = before + h * l.head();
-    rt = int(min((pos - start) / l.item(), int64_t(l.row_tiles - 1)));
-    start += rt * l.item();
-    w = l.cost(rt);
-    first = start + kItemCost;
-    end = first + int64_t(l.U) * w;
-  }
-  // The tiles that begin before `pos`.
-  __device__ __forceinline__ int tiles(int64_t pos, int U) const {
-    return pos <= first ? 0 : int(min(int64_t(U), (pos - first + w - 1) / w));
-  }
 };
 
 // The tokens of a step of 64 from `first` on that a row sees: the text, and of the nodes, numbers
@@ -244,27 +170,27 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
     ptx::regs_dec<C::REG_OTHERS>();
     if (warp == C::LINE) {
       // ------------------------------------------------------------ segments
-      const int64_t total = line_total(p, lane), piece = line_share(total, p);
+      const int64_t total = Line::total(p, lane), piece = Line::share(total, p);
       int64_t pos = min(int64_t(blockIdx.x) * piece, total);
       const int64_t stop = min(pos + piece, total);
       // (after a wait that ran out in an earlier CTA there is nothing to do)
       if (*reinterpret_cast<volatile int32_t*>(err) & kErrTimeout) pos = stop;
       int64_t before = 0;
-      int b = pos < stop ? line_find(p, pos, lane, before) : 0;
+      int b = pos < stop ? Line::find(p, pos, lane, before) : 0;
 #pragma unroll 1
       for (int s = 0;; ++s) {
         Segment g{};
 #pragma unroll 1
         while (pos < stop) {
-          const int64_t all = line_of(p, b);
+          const int64_t all = Line::of(p, b);
           if (pos >= before + all) {
             before += all;
             ++b;
             continue;
           }
           const int q0 = a.cu[b], n = a.cu[b + 1] - q0, len = a.lens[b];
-          const SeqLine l(n, p.G, len);
-          const Item it(l, before, pos);
+          const Line::Seq l(n, p.G, len);
+          const Line::Item it(l, before, pos);
           const int u0 = it.tiles(pos, l.U), u1 = it.tiles(stop, l.U);
           pos = min(stop, it.end);
           if (u1 <= u0) continue;
@@ -811,14 +737,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_tree_many_join_kernel(c
   constexpr int E = D / kJoinWarps / 4;  // of four dimensions
   const CacheQueryArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, x = blockIdx.x, row = blockIdx.y * kJoinRows + lane;
-  const int64_t total = line_total(p, lane), piece = line_share(total, p), pos = (x + 1) * piece;
+  const int64_t total = Line::total(p, lane), piece = Line::share(total, p), pos = (x + 1) * piece;
   int64_t before = 0;
-  const int b = pos < total ? line_find(p, pos, lane, before) : 0;
+  const int b = pos < total ? Line::find(p, pos, lane, before) : 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (pos >= total) return;
   const int q0 = a.cu[b], n = a.cu[b + 1] - q0;
-  const SeqLine l(n, p.G, a.lens[b]);
-  const Item it(l, before, pos);
+  const Line::Seq l(n, p.G, a.lens[b]);
+  const Line::Item it(l, before, pos);
   const int parts = int((it.first + int64_t(l.U - 1) * it.w) / piece) - x + 1;
   const int64_t rg = int64_t(it.rt) * kTreeRows + row;
   if (it.first / piece != x || parts < 2 || rg >= int64_t(n) * p.G) return;
