@@ -198,6 +198,7 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
     if (*reinterpret_cast<volatile int32_t*>(err) & kErrTimeout) pos = stop;
     int64_t before = 0;
     int b = pos < stop ? Line<N>::find(p, pos, lane, before) : 0;
+    TreeCut cut{};
 #pragma unroll 1
     for (int s = 0;; ++s) {
       Segment g{};
@@ -224,6 +225,8 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
         g.len = len;
         g.token = u0 * kTile;
         g.slot = u0 == 0 && u1 == l.U ? -1 : 2 * int(blockIdx.x) + (u0 > 0 ? 0 : 1);
+        if (u0 == 0 && u1 < l.U)
+          cut = TreeCut{int((it.end - it.w) / piece) - int(blockIdx.x) + 1, g.h, 0, g.rows, g.q0};
         break;
       }
       const int at = s % C::NSEG;
@@ -238,6 +241,7 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
       __syncwarp();
       if (g.tiles == 0) break;
     }
+    if (lane == 0) p.cuts[blockIdx.x] = cut;
     // what is wrong with the sequences is noted once, when nobody waits for it
     if (blockIdx.x == 0) {
 #pragma unroll 1
@@ -841,43 +845,27 @@ __global__ void __launch_bounds__(TreeCfg<D, N>::THREADS, 1)
 
 constexpr int kJoinWarps = 8;  // per CTA
 
-// Starts while the first kernel ends; every CTA waits for its end, those with nothing to
-// join too, so that what follows on the stream does.  W warps per row.
+// Starts while the first kernel ends, and waits for it.  W warps per row of a cut segment; where few sequences
+// are cut often, a CTA per row for every eight CTAs of the line (one for each: 16 nodes behind 2049 tokens 18 us, 22).
+constexpr int kCutsWide = 8;
+
 template <int D, int N, int W>
 __global__ void __launch_bounds__(32 * kJoinWarps) cache_tree_join_kernel(const __grid_constant__ TreeParams p) {
   __shared__ float shared[W > 1 ? W * (D + 2) : 1];
-  const CacheQueryArgs& a = p.a;
-  const int b = blockIdx.y, w = (threadIdx.x >> 5) % W, lane = threadIdx.x & 31;
-  const int i = blockIdx.x * (kJoinWarps / W) + (threadIdx.x >> 5) / W;  // of the sequence: token, head
-  SeqRows r;
-  const bool good = load_rows(a.cu, a.lens, b, a.total_tokens, a.max_new, a.max_seqlen, a.cache.status, r, false);
-  const bool mine = good && r.len >= r.n && i < r.n * a.num_heads;
-  const int head = i % a.num_heads, row = (i / a.num_heads) * p.G + head % p.G;
-  // the line before this (sequence, head); the division is the other kernel's
-  int64_t all = 0, first = 0;
-#pragma unroll 1
-  for (int x = lane; x < a.cache.batch; x += 32) {
-    const int64_t n = Line<N>::of(p, x);
-    all += n;
-    first += x < b ? n : 0;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    all += __shfl_xor_sync(0xffffffffu, all, o);
-    first += __shfl_xor_sync(0xffffffffu, first, o);
-  }
-  const int64_t piece = Line<N>::share(all, p);
-  int c0 = 0, c1 = 0;
-  if (mine) {
-    const typename Line<N>::Seq l(r.n, p.G, r.len);
-    const typename Line<N>::Item it(l, 0, head / p.G * l.head());
-    c0 = int((first + it.first) / piece);
-    c1 = int((first + it.end - 1) / piece);
-  }
+  constexpr int CUTS = W > 1 ? kCutsWide : 1;
+  const int w = (threadIdx.x >> 5) % W, lane = threadIdx.x & 31, x0 = blockIdx.x * CUTS;
+  const int row = blockIdx.y * (kJoinWarps / W) + (threadIdx.x >> 5) / W;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (c0 == c1) return;  // finished by its CTA
-  auto at = [&](int j) { return int64_t(2 * (c0 + j) + (j == 0 ? 1 : 0)) * N + row; };
-  join_row<D, W>(p, c1 - c0 + 1, at, r.q0 + i / a.num_heads, head, w, lane, shared);
+  const bool here = lane < CUTS && x0 + lane < p.ctas && p.cuts[x0 + lane].parts >= 2 && row < p.cuts[x0 + lane].rows;
+#pragma unroll 1
+  for (uint32_t left = __ballot_sync(0xffffffffu, here); left; left &= left - 1) {
+    const int x = x0 + __ffs(left) - 1;
+    const TreeCut cut = p.cuts[x];
+    const int node = row / p.G;
+    auto at = [&](int j) { return int64_t(2 * (x + j) + (j == 0 ? 1 : 0)) * N + row; };
+    join_row<D, W>(p, cut.parts, at, cut.q0 + node, cut.h * p.G + row - node * p.G, w, lane, shared);
+    if (W > 1) __syncthreads();
+  }
 }
 
 // Rows are padded to the least of these; 0: cache_tree_many.cu takes them, 128 or 256 rows of a sequence
@@ -888,6 +876,7 @@ int padded_rows(const CacheView& c, int num_heads, int max_new) {
   return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 0;
 }
 uint64_t partial_rows(int N) { return 2ull * kTreeSms * N; }
+uint64_t partial_bytes(int N, int D) { return partial_rows(N) * (uint64_t(D) * 4 + 8); }
 
 template <int D, int N>
 attn_status launch_dn(TreeParams& p, cudaStream_t s) {
@@ -902,11 +891,11 @@ attn_status launch_dn(TreeParams& p, cudaStream_t s) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return record_cuda_error(e, "attn_cache_tree_fwd launch");
   // One warp or a CTA joins a row, as in cache_attn.cu.
-  const int64_t rows = int64_t(p.a.max_new) * p.a.num_heads;
   const bool wide = int64_t(p.ctas) > 8 * int64_t(c.batch) * c.heads;
   const int per_cta = wide ? 1 : kJoinWarps;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned((rows + per_cta - 1) / per_cta), unsigned(c.batch));
+  const int cuts = wide ? kCutsWide : 1;
+  cfg.gridDim = dim3(unsigned((p.ctas + cuts - 1) / cuts), unsigned(N / per_cta));
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -933,7 +922,7 @@ uint64_t cache_tree_workspace(const CacheView& c, int total_tokens, int num_head
   if (total_tokens == 0 || max_new == 0) return 0;
   const int N = padded_rows(c, num_heads, max_new);
   if (N == 0) return cache_tree_many_workspace(c);
-  return partial_rows(N) * (uint64_t(c.head_dim) * 4 + 8);
+  return partial_bytes(N, c.head_dim) + kTreeSms * sizeof(TreeCut);
 }
 
 attn_status launch_cache_tree(const CacheQueryArgs& a, const TreeMasks& tree, cudaStream_t s) {
@@ -947,6 +936,7 @@ attn_status launch_cache_tree(const CacheQueryArgs& a, const TreeMasks& tree, cu
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.part_o = a.workspace;
   p.part_m = reinterpret_cast<float2*>(a.workspace + partial_rows(N) * a.cache.head_dim);
+  p.cuts = reinterpret_cast<TreeCut*>(a.workspace + partial_bytes(N, a.cache.head_dim) / 4);
   switch (a.cache.head_dim) {
     case 32: return launch_d<32>(p, N, s);
     case 64: return launch_d<64>(p, N, s);

@@ -47,6 +47,14 @@ struct TreeParams {
   float scale_log2;
   float* part_o;    // [2 * ctas][rows of a segment] of head_dim, as for few rows in cache_attn.cu
   float2* part_m;
+  struct TreeCut* cuts;  // [ctas]
+};
+
+// What the line of a CTA leaves for the second kernel: the segment that begins in its piece and ends in
+// a later one's.
+struct alignas(16) TreeCut {
+  int parts;  // CTAs that hold a part of it, this one the first; 0: there is no such segment
+  int h, row0, rows, q0, unused[3];
 };
 
 // The line of work: tiles of tokens of all (sequence, head, ROWS rows)s, one behind the other, in units

@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
       if (*reinterpret_cast<volatile int32_t*>(err) & kErrTimeout) pos = stop;
       int64_t before = 0;
       int b = pos < stop ? Line::find(p, pos, lane, before) : 0;
+      TreeCut cut{};
 #pragma unroll 1
       for (int s = 0;; ++s) {
         Segment g{};
@@ -204,6 +205,8 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
           g.len = len;
           g.token = u0 * kTile;
           g.slot = u0 == 0 && u1 == l.U ? -1 : 2 * int(blockIdx.x) + (u0 > 0 ? 0 : 1);
+          if (u0 == 0 && u1 < l.U)
+            cut = TreeCut{int((it.end - it.w) / piece) - int(blockIdx.x) + 1, g.h, g.row0, g.rows, g.q0};
           break;
         }
         const int at = s % C::NSEG;
@@ -228,6 +231,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
           asm volatile("prefetch.global.L2 [%0];" ::"l"(p.tree.bits + token * p.tree.words));
         }
       }
+      if (lane == 0) p.cuts[blockIdx.x] = cut;
       // what is wrong with the sequences is noted once, when nobody waits for it
       if (blockIdx.x == 0) {
 #pragma unroll 1
@@ -729,31 +733,21 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
 
 constexpr int kJoinWarps = 8, kJoinRows = 32;  // per CTA: a lane per row, a warp per eighth of the dimensions
 
-// The item that is cut for the first time where the pieces of CTAs x and x + 1 meet, if there is one: its
-// partial results become one, in their order.  Starts while the first kernel ends; every CTA waits
-// for its end, those with nothing to join too, so that what follows on the stream does.
+// Starts while the first kernel ends, and waits for it.
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) cache_tree_many_join_kernel(const __grid_constant__ TreeParams p) {
   constexpr int E = D / kJoinWarps / 4;  // of four dimensions
   const CacheQueryArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, x = blockIdx.x, row = blockIdx.y * kJoinRows + lane;
-  const int64_t total = Line::total(p, lane), piece = Line::share(total, p), pos = (x + 1) * piece;
-  int64_t before = 0;
-  const int b = pos < total ? Line::find(p, pos, lane, before) : 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (pos >= total) return;
-  const int q0 = a.cu[b], n = a.cu[b + 1] - q0;
-  const Line::Seq l(n, p.G, a.lens[b]);
-  const Line::Item it(l, before, pos);
-  const int parts = int((it.first + int64_t(l.U - 1) * it.w) / piece) - x + 1;
-  const int64_t rg = int64_t(it.rt) * kTreeRows + row;
-  if (it.first / piece != x || parts < 2 || rg >= int64_t(n) * p.G) return;
+  const TreeCut cut = p.cuts[x];
+  if (cut.parts < 2 || row >= cut.rows) return;
   float m = -INFINITY, sum = 0.f;
   float4 o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
-  for (int i = 0; i < parts; ++i) {
+  for (int i = 0; i < cut.parts; ++i) {
     const int64_t slot = 2 * (x + i) + (i == 0 ? 1 : 0);
     const float2 s = p.part_m[slot * kTreeRows + row];
     float4 v[E];
@@ -769,8 +763,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_tree_many_join_kernel(c
                          fmaf(v[e].w, f, o[e].w * old));
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int node = int(rg / p.G), head = it.h * p.G + int(rg - int64_t(node) * p.G);
-  const int64_t at = q0 + node;
+  const int rg = cut.row0 + row, node = rg / p.G, head = cut.h * p.G + rg - node * p.G;
+  const int64_t at = cut.q0 + node;
   uint2* out = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + (at * a.num_heads + head) * D + warp * (E * 4));
 #pragma unroll
   for (int e = 0; e < E; ++e)
@@ -791,7 +785,7 @@ attn_status launch_d(const TreeParams& p, cudaStream_t s) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return record_cuda_error(e, "attn_cache_tree_fwd launch");
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(p.ctas - 1), kTreeRows / kJoinRows);
+  cfg.gridDim = dim3(unsigned(p.ctas), kTreeRows / kJoinRows);
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -803,10 +797,12 @@ attn_status launch_d(const TreeParams& p, cudaStream_t s) {
   return e == cudaSuccess ? ATTN_OK : record_cuda_error(e, "attn_cache_tree_fwd join launch");
 }
 
+uint64_t partial_bytes(int D) { return 2ull * kTreeSms * kTreeRows * (uint64_t(D) * 4 + 8); }
+
 }  // namespace
 
 uint64_t cache_tree_many_workspace(const CacheView& c) {
-  return 2ull * kTreeSms * kTreeRows * (uint64_t(c.head_dim) * 4 + 8);
+  return partial_bytes(c.head_dim) + kTreeSms * sizeof(TreeCut);
 }
 
 attn_status launch_cache_tree_many(const CacheQueryArgs& a, const TreeMasks& tree, cudaStream_t s) {
@@ -818,6 +814,7 @@ attn_status launch_cache_tree_many(const CacheQueryArgs& a, const TreeMasks& tre
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.part_o = a.workspace;
   p.part_m = reinterpret_cast<float2*>(a.workspace + 2ull * kTreeSms * kTreeRows * a.cache.head_dim);
+  p.cuts = reinterpret_cast<TreeCut*>(a.workspace + partial_bytes(a.cache.head_dim) / 4);
   switch (a.cache.head_dim) {
     case 32: return launch_d<32>(p, s);
     case 64: return launch_d<64>(p, s);
