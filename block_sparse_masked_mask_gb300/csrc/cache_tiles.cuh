@@ -81,14 +81,44 @@ __device__ __forceinline__ float split_held(const uint4 (&q)[D / PARTS / 8], uin
   }
   return amax < INFINITY ? pow2f(e - 7) : __int_as_float(0x7FC00000);
 }
-// A whole row by one lane, from memory (zeros if not `real`).
+// The same of a whole row by one lane, from memory (zeros if not `real`), lo behind hi.  (By the form above with one part
+// a window of 8 x 32 queries, 16 heads, was weighed in 19.8 us instead of 18.8.)
 template <int D>
 __device__ __forceinline__ float split_query(const __nv_bfloat16* query, bool real, uint8_t* tiles, int row) {
   uint4 q[D / 8];
+  float amax = 0.f;
   const uint4* src = reinterpret_cast<const uint4*>(query);
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) q[i] = real ? src[i] : make_uint4(0, 0, 0, 0);
-  return split_held<D, 1>(q, tiles, row, CodeTile<D>::BYTES, 0);
+  for (int i = 0; i < D / 8; ++i) {
+    q[i] = real ? src[i] : make_uint4(0, 0, 0, 0);
+    const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
+  }
+  const int e = amax > 0.f ? max(-119, min(126, exponent_of(amax))) : 0;
+  const float f = pow2f(7 - e);
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) {
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int e4 = 0; e4 < 4; ++e4) {
+      const uint4 v = q[2 * i + (e4 >> 1)];
+      const uint32_t w0 = (e4 & 1) ? v.z : v.x, w1 = (e4 & 1) ? v.w : v.y;
+      const float x0 = __uint_as_float(w0 << 16) * f, x1 = __uint_as_float(w0 & 0xFFFF0000u) * f;
+      const float x2 = __uint_as_float(w1 << 16) * f, x3 = __uint_as_float(w1 & 0xFFFF0000u) * f;
+      const uint32_t h0 = e4m3_pair(x0, x1), h1 = e4m3_pair(x2, x3);
+      uint32_t y0 = half2_of(h0), y1 = half2_of(h1);
+      const float2 z0 = __half22float2(*reinterpret_cast<__half2*>(&y0));
+      const float2 z1 = __half22float2(*reinterpret_cast<__half2*>(&y1));
+      hi[e4] = h0 | (h1 << 16);
+      lo[e4] = e4m3_pair(x0 - z0.x, x1 - z0.y) | (e4m3_pair(x2 - z1.x, x3 - z1.y) << 16);
+    }
+    const uint32_t at = CodeTile<D>::unit(row, i);
+    *reinterpret_cast<uint4*>(tiles + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(tiles + CodeTile<D>::BYTES + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  }
+  return amax < INFINITY ? pow2f(e - 7) : __int_as_float(0x7FC00000);
 }
 
 // Pages as rows of D bytes, (dimension, slot, head, page), one page and head per copy.
