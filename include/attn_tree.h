@@ -86,7 +86,10 @@ ATTN_API attn_status attn_cache_tree_fwd_workspace_size(const attn_kv_cache* cac
  *   tree_bits    device uint32 [total_tokens, tree_words], 32 * tree_words >=
  *                max_new; bits of nodes that the sequence does not have are ignored
  * q, o, lse, scale, bounds and workspace are attn_cache_fwd()'s, and so is what is
- * said there of finite numbers, of empty rows, of repeats and of o being q.
+ * said there of finite numbers, of empty rows, of repeats and of o being q.  A query
+ * enters as the sum of two e4m3 numbers whatever the number of rows: with m the
+ * largest magnitude of a row, its elements down to 2^-9 m are exact, and smaller ones
+ * are off by 2^-17 m at most.
  */
 ATTN_API attn_status attn_cache_tree_fwd(const void* q, void* o, float* lse, attn_dtype dtype,
                                          int32_t total_tokens, int32_t num_heads, float scale,
