@@ -53,8 +53,6 @@
 namespace attnmask {
 namespace {
 
-constexpr float kNoReference = -0x1p100f;   // of a row that has seen nothing yet
-
 // A piece of the line in one (sequence, head).
 struct Segment {
   int tiles;  // 0: there is no further one

@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
              tree_warp_wait(bar(C::B_Q + 1), uint32_t(s) & 1u, abort_flag, 18);
       const float qscale = factors[row];
 
-      float mx = -INFINITY;                    // running maximum (of score + value exponent)
+      float mx = kNoReference;                 // the weights' reference (a score + value exponent)
       float2 l2 = make_float2(0.f, 0.f);       // two halves of the sum
       bool some = false;                       // O holds products of this segment
 #pragma unroll 1
@@ -570,78 +570,90 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
             ptx::tmem_ld32(s_col, w[0]);
             ptx::tmem_ld32(s_col + 32, w[1]);
             ptx::tmem_wait_ld();
-            // a block's largest score: its factor is not negative, so the largest product
-            float top = -INFINITY;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint32_t* v = w[q >> 1] + (q & 1) * 16;
-              float t = ptx::fmax3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
-#pragma unroll
-              for (int e = 3; e < 15; e += 2) t = ptx::fmax3(t, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-              t = fmaxf(t, __uint_as_float(v[15]));
-              if (t > -INFINITY) top = fmaxf(top, fmaf(t, qscale * sc[q].x, sc[q].y));
-            }
-            // the reference moves on the first visible token and when a weight would pass 2^15
-            const bool raise = top > mx + kMostWeight;
-            top -= kTopWeight;
-            if (__builtin_expect(__any_sync(0xffffffffu, raise || (odd & kFar)), 0)) {
-              const float half = raise ? half_factor(mx, top) : 1.f, alpha = half * half;
-              if (raise) mx = top;
-              l2.x = l2.x * half * half;
-              l2.y = l2.y * half * half;
-              if (some) {  // O holds the earlier steps' products once the last of them has ended
-                ok = tree_warp_wait(bar(C::B_PDONE + 2 * m + (f ^ 1)), uint32_t(turn - (f ^ 1)) & 1u, abort_flag, 16);
-                if (!ok) break;
-                ptx::tc_fence_after();
+            // The weights under the present reference, and the sum with them.  Eight of them together above
+            // 2^15 (or a segment's first step, or a far page) send the warp to the rows' maxima, and the
+            // weights are repeated: scores without a maximum to wait for come through that much sooner.
+            float2 lt;
 #pragma unroll 1
-                for (int q = 0; q < D / 16; ++q) {
-                  uint32_t v[16];
-                  ptx::tmem_ld16(o_col + q * 16, v);
-                  ptx::tmem_wait_ld();
+            for (bool need = !some || (odd & kFar);;) {
+              if (__builtin_expect(need, 0)) {
+                // a block's largest score: its factor is not negative, so the largest product
+                float top = -INFINITY;
 #pragma unroll
-                  for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
-                  ptx::tmem_st16(o_col + q * 16, v);
-                }
-              }
-              if (odd & kFar) {  // sums that do not go through the weights, from the scores as they lie
-                const float ref = mx == -INFINITY ? 0.f : mx;
-#pragma unroll 1
                 for (int q = 0; q < 4; ++q) {
-                  if (__float_as_int(sc[q].w) != kFar) continue;
-                  const float by = qscale * sc[q].x;
-                  uint32_t v[16];
-                  ptx::tmem_ld16(s_col + 16 * q, v);
-                  ptx::tmem_wait_ld();
+                  const uint32_t* v = w[q >> 1] + (q & 1) * 16;
+                  float t = ptx::fmax3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
 #pragma unroll
-                  for (int e = 0; e < 16; ++e) {
-                    const float y = ptx::ex2(0.5f * fmaf(__uint_as_float(v[e]), by, -ref));
-                    l2.x = fmaf(y, y, l2.x);
+                  for (int e = 3; e < 15; e += 2) t = ptx::fmax3(t, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+                  t = fmaxf(t, __uint_as_float(v[15]));
+                  if (t > -INFINITY) top = fmaxf(top, fmaf(t, qscale * sc[q].x, sc[q].y));
+                }
+                // (eight weights of 2^12 do not come here again)
+                const bool raise = top > mx + (kMostWeight - 3.f);
+                top -= kTopWeight;
+                const float half = raise ? half_factor(mx, top) : 1.f, alpha = half * half;
+                if (raise) mx = top;
+                l2.x = l2.x * half * half;
+                l2.y = l2.y * half * half;
+                if (some) {  // O holds the earlier steps' products once the last of them has ended
+                  ok = tree_warp_wait(bar(C::B_PDONE + 2 * m + (f ^ 1)), uint32_t(turn - (f ^ 1)) & 1u, abort_flag, 16);
+                  if (!ok) break;
+                  ptx::tc_fence_after();
+#pragma unroll 1
+                  for (int q = 0; q < D / 16; ++q) {
+                    uint32_t v[16];
+                    ptx::tmem_ld16(o_col + q * 16, v);
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+                    ptx::tmem_st16(o_col + q * 16, v);
+                  }
+                }
+                if (odd & kFar) {  // sums that do not go through the weights, from the scores as they lie
+#pragma unroll 1
+                  for (int q = 0; q < 4; ++q) {
+                    if (__float_as_int(sc[q].w) != kFar) continue;
+                    const float by = fmaf(qscale, sc[q].x, 0x1p-126f);
+                    uint32_t v[16];
+                    ptx::tmem_ld16(s_col + 16 * q, v);
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                      const float y = ptx::ex2(0.5f * fmaf(__uint_as_float(v[e]), by, -mx));
+                      l2.x = fmaf(y, y, l2.x);
+                    }
                   }
                 }
               }
-            }
-            const float ref = mx == -INFINITY ? 0.f : mx;
+              lt = l2;
+              float hot = 0.f;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float4 k = sc[q];
-              // never 0, where a page is left out or the product is below fp32: a hidden score is
-              // -inf, and times 0 it would be NaN
-              const float kf = fmaf(qscale, k.x, 0x1p-126f), kx = k.y - ref;
-              const float2 f2 = make_float2(kf, kf), x2 = make_float2(kx, kx);
-              float2 part = make_float2(0.f, 0.f);
-              uint32_t* v = w[q >> 1] + (q & 1) * 16;
-              uint32_t pk[8];
+              for (int q = 0; q < 4; ++q) {
+                const float4 k = sc[q];
+                // never 0, where a page is left out or the product is below fp32: a hidden score is
+                // -inf, and times 0 it would be NaN
+                const float kf = fmaf(qscale, k.x, 0x1p-126f), kx = k.y - mx;
+                const float2 f2 = make_float2(kf, kf), x2 = make_float2(kx, kx);
+                float2 part = make_float2(0.f, 0.f);
+                uint32_t* v = w[q >> 1] + (q & 1) * 16;
+                uint32_t pk[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                float2 y = ptx::ffma2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), f2, x2);
-                y.x = ptx::ex2(y.x);
-                y.y = ptx::ex2(y.y);
-                part = ptx::fadd2(part, y);
-                pk[e] = pack_half2(y.x, y.y);
+                for (int e = 0; e < 8; ++e) {
+                  float2 y = ptx::ffma2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), f2, x2);
+                  y.x = ptx::ex2(y.x);
+                  y.y = ptx::ex2(y.y);
+                  part = ptx::fadd2(part, y);
+                  pk[e] = pack_half2(y.x, y.y);
+                }
+                lt = ptx::ffma2(part, make_float2(k.z, k.z), lt);
+                hot = ptx::fmax3(hot, part.x, part.y);
+                ptx::tmem_st8(s_col + 8 * q, pk);  // over S columns read already
               }
-              l2 = ptx::ffma2(part, make_float2(k.z, k.z), l2);
-              ptx::tmem_st8(s_col + 8 * q, pk);  // over S columns read already
+              if (__builtin_expect(need || !__any_sync(0xffffffffu, hot > 0x1p15f), 1)) break;
+              need = true;
             }
+            if (!ok) break;
+            l2 = lt;
             ptx::tmem_wait_st();
             ptx::tc_fence_before();
             some = true;
