@@ -525,3 +525,33 @@ def test_append_rope_of_many_heads_and_long_pages():
         far = (one.dev.k_pages.int() - two.dev.k_pages.int()).abs()
         assert (one.dev.k_scale == two.dev.k_scale).float().mean() >= 0.99
         assert (far <= 1).float().mean() >= 0.99 and api.attn_cache_get_status(one.dev) == api.ATTN_OK
+
+
+@pytest.mark.parametrize("n", [4, 40])
+def test_attention_behind_copies_and_kernels(n):
+    """What was written just before the call, by a copy or a kernel, is what it reads, in a captured graph too."""
+    p = filled([900, 2000], 2, 64, 32, seed=n)
+    masks = trees([n, n])
+    sources = [randn(2 * n, 8, 64, seed=i).cuda() for i in range(6)]
+    args = (p.dev, device_bits(words_of(masks)), dev(cu_of([n, n])), dev([900, 2000]), n, 2000)
+    want = [[x.clone() for x in api.attn_cache_tree_fwd(q, *args)] for q in sources]
+    q = torch.empty_like(sources[0])
+
+    def calls():
+        got = []
+        for i, x in enumerate(sources):
+            if i % 2:
+                torch.mul(x, 1, out=q)
+            else:
+                q.copy_(x)
+            got.append(api.attn_cache_tree_fwd(q, *args))
+        return got
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = calls()
+    for _ in range(3):
+        graph.replay()
+        for got in (captured, calls()):
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for x, y in zip(want, got) for a, b in zip(x, y))
