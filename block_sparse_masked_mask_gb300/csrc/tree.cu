@@ -14,7 +14,7 @@
 // is loaded at once, as long as their stores come behind.  No thread waits for another warp;
 // the lookups of a page (path, table) are all that stands before its loads, and the scales
 // arrive with the tokens.  Tokens go through shared memory by copies that need no registers, in loops of
-// little code.  256 sequences of 16 heads of 128, 16 to 64 of their 128 to 256 nodes kept, take 22 us where
+// little code.  256 sequences of 16 heads of 128, 16 to 64 of their 128 to 256 nodes kept, take 21 us where
 // the bytes take 12.5: rows of 128 bytes, scattered.  (A CTA per head and side, a barrier between a page's loads and
 // stores: 39 us.)
 #include "cache_rows.cuh"
@@ -101,9 +101,12 @@ __global__ void __launch_bounds__(kKeepThreads) tree_keep_kernel(const TreeKeepA
   uint4* const stage = staged[warp];
   const uint32_t stage_at = ptx::smem_addr(stage);
   const int mask = (1 << row_log2) - 1;
+  auto number_of = [&](int i) { return i << log2 < base + m ? __ldg(table + i) : 0; };
+  int next = number_of(base >> log2);
 #pragma unroll 1
   for (int i = base >> log2; i << log2 < base + m; ++i) {
-    const int number = __ldg(table + i);
+    const int number = next;
+    next = number_of(i + 1);
     if (!in_pool(c, number)) {
       if (lane == 0) atomicOr(c.status, kErrBadPage);
       continue;
@@ -111,11 +114,12 @@ __global__ void __launch_bounds__(kKeepThreads) tree_keep_kernel(const TreeKeepA
     const int64_t at = int64_t(number) * c.heads + h;
     const int t0 = i << log2;                     // its first token
     const int j0 = max(t0 - base, 0), j1 = min(t0 + page_size - base, m);  // of the path, its new tokens
-    const int own = exponent_of(scales[at]);
-    // The row that token j comes from, or -1 if it stays where it is or has no page; its exponent.
-    int e = own;
+    const float own_scale = scales[at];
+    // The row that token j comes from, or -1 if it stays where it is or has no page; its scale (which is looked
+    // at only once the tokens are on their way).
+    float scale;
     auto source = [&](int j) -> int64_t {
-      e = own;
+      scale = own_scale;
       if (j >= j1) return -1;
       const int src = base + __ldg(path + j);
       if (src == base + j) return -1;
@@ -125,7 +129,7 @@ __global__ void __launch_bounds__(kKeepThreads) tree_keep_kernel(const TreeKeepA
         return -1;
       }
       const int64_t row = int64_t(from) * c.heads + h;
-      if (from != number) e = exponent_of(scales[row]);
+      scale = scales[row];
       return (row << log2) + (src & (page_size - 1));
     };
     auto fetch = [&](int j, int64_t row) {
@@ -138,12 +142,12 @@ __global__ void __launch_bounds__(kKeepThreads) tree_keep_kernel(const TreeKeepA
     };
     int64_t row = source(j0 + lane);
     fetch(j0, row);
-    int to = max(own, e);
-    const int e0 = e;
+    const int own = exponent_of(own_scale), e0 = exponent_of(scale);
+    int to = max(own, e0), e = e0;
 #pragma unroll 1
     for (int j = j0 + 32; j < j1; j += 32) {
       source(j + lane);
-      to = max(to, e);
+      to = max(to, exponent_of(scale));
     }
     to = __reduce_max_sync(0xffffffffu, to);
 #pragma unroll 1
@@ -151,8 +155,7 @@ __global__ void __launch_bounds__(kKeepThreads) tree_keep_kernel(const TreeKeepA
       if (j > j0) {
         row = source(j + lane);
         fetch(j, row);
-      } else {
-        e = e0;
+        e = exponent_of(scale);
       }
       asm volatile("cp.async.commit_group;\n\tcp.async.wait_all;" ::: "memory");
       __syncwarp();
