@@ -335,6 +335,8 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
 #pragma unroll 1
         for (int s = 0; ok && segment(s, g, true) && g.tiles; ++s) {
           const bool twin = g.rows <= kTile;
+          // (Behind both M tiles' end of the segment before.  Sooner, the tile two places before this one's first, the
+          // other issuer's, may be on its way still, and a wait for a phase's parity would not tell it from it.)
           ok = tree_wait(bar(C::B_Q + m), uint32_t(s) & 1u, abort_flag, 6) &&
                (!twin || tree_wait(bar(C::B_Q + 1 - m), uint32_t(s) & 1u, abort_flag, 6));
           const uint64_t qhi = qd + (twin ? 0 : uint64_t(m) * (2 * C::KT >> 4)), qlo = qhi + (C::KT >> 4);

@@ -555,3 +555,14 @@ def test_attention_behind_copies_and_kernels(n):
         for got in (captured, calls()):
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for x, y in zip(want, got) for a, b in zip(x, y))
+
+
+@pytest.mark.parametrize("sizes", [[20, 17, 32, 26], [33, 64, 40], [20, 64, 3, 33, 1, 17, 90]], ids=str)
+@pytest.mark.parametrize("dim,heads,lengths", [(64, 8, 500), (32, 3, 1300), (128, 8, 130)])
+def test_several_segments_of_a_cta(dim, heads, lengths, sizes):
+    """More (sequence, head)s than three for each SM, of up to 128 rows, of more, and of both in turn."""
+    batch = -(-152 * 7 // (2 * heads))
+    n = [sizes[b % len(sizes)] for b in range(batch)]
+    lens = [x + (b * 277) % lengths for b, x in enumerate(n)]
+    p = filled(lens, heads, dim, 32, seed=batch)
+    check_tree(p, randn(sum(n), heads * 4, dim, seed=2), cu_of(n), lens, trees(n))
