@@ -8,7 +8,7 @@ namespace {
 
 constexpr int kNoPage = INT_MIN, kFar = 1;  // of a block of 16 tokens, as in cache_chunk.cu
 constexpr int kTreeSms = 152;
-constexpr float kNoReference = -0x1p100f;   // of a row that has seen nothing yet
+constexpr float kNoReference = -0x1.8p127f;  // of a row that has seen nothing yet: any score moves it
 
 // A constant that the compiler does not see: it would else copy a loop's body for its first turn.
 __device__ __forceinline__ uint32_t opaque(uint32_t x) {

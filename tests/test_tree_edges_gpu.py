@@ -566,3 +566,30 @@ def test_several_segments_of_a_cta(dim, heads, lengths, sizes):
     lens = [x + (b * 277) % lengths for b, x in enumerate(n)]
     p = filled(lens, heads, dim, 32, seed=batch)
     check_tree(p, randn(sum(n), heads * 4, dim, seed=2), cu_of(n), lens, trees(n))
+
+
+@pytest.mark.parametrize("n", [1, 4, 40])
+@pytest.mark.parametrize("scale", [1.0, 1e20, 1e28, 1e33])
+def test_scores_far_below_zero(n, scale):
+    """Equal scores of -64 scale, whatever that is: no row is lost, LSE is the score (off by fp32's roundings of it
+    and, where the exponents of the values' scales, up to 2^4, are below those, by 2^4 and ln of the tokens), and at
+    scale 1 O is the mean of the visible values.  (From scale 2^19 on a score's rounding is more than the
+    exponents that go with it: pages' shares are then no better known than the scores.)"""
+    length = 700 + n
+    p = Pair([length], 1, 64, 32, seed=1)
+    k, v = torch.ones(length, 1, 64).bfloat16(), randn(length, 1, 64, seed=2)
+    p.append(k, v, cu_of([length]), [length])
+    masks = trees([n])
+    q = -torch.ones(n, 4, 64, dtype=torch.bfloat16)
+    o, lse = api.attn_cache_tree_fwd(q.cuda(), p.dev, device_bits(words_of(masks)), dev([0, n]), dev([length]), n, length, scale=scale)
+    assert api.attn_cache_get_status(p.dev) == api.ATTN_OK
+    V = p.ref.numbers(1, 0, length)[0]
+    for i in range(n):
+        seen = np.concatenate([np.ones(length - n, bool), masks[0][i]])
+        want, size = V[seen].mean(0), np.abs(V[seen]).mean(0)
+        # (weights are equal and exact; sums of `length` terms in fp32, a rounding to bf16)
+        err = np.abs(o[i].double().cpu().numpy() - want)
+        assert torch.isfinite(o[i]).all() and (o[i] != 0).any()
+        assert scale > 1 or (err <= 2.0 ** -8 * np.abs(want) + (length + 8) * 2.0 ** -23 * size).all()
+        exact = -64.0 * scale + math.log(seen.sum())
+        assert (np.abs(lse[:, i].double().cpu().numpy() - exact) <= 2.0 ** -20 * abs(exact)).all()
