@@ -178,11 +178,9 @@ __device__ __forceinline__ void append_pages(const AppendRopeParams& p, int bloc
   const int pairs = p.rope.rot / 2;
   const bool fine = in_pool(c, number);
 
-#pragma unroll 1
-  for (int l = 0; l < p.loops; ++l) {
+  auto stage = [&](int l) {
     const int h = head0 + l * teams;
     const bool on = h < c.heads;
-    if (l > 0) __syncthreads();  // the last head's elements have been read
 #pragma unroll 1
     for (int j = 0; j < turns; ++j) {
       const int ch = (j << p.team_log2) + tid;
@@ -193,6 +191,12 @@ __device__ __forceinline__ void append_pages(const AppendRopeParams& p, int bloc
         copy16_async(uint32_t(__cvta_generic_to_shared(staged + S::at(j, threadIdx.x, x * S::PER))), from + x * S::PER, here);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  stage(0);
+#pragma unroll 1
+  for (int l = 0; l < p.loops; ++l) {
+    const int h = head0 + l * teams;
+    const bool on = h < c.heads;
     if (l == 0 && keys) {
       if (int(threadIdx.x) < last - first)
         place[threadIdx.x] = p.rope.a.positions ? p.rope.a.positions[q0 + start + first - held + threadIdx.x] : start + first + int(threadIdx.x);
@@ -249,6 +253,8 @@ __device__ __forceinline__ void append_pages(const AppendRopeParams& p, int bloc
     if (lane == 0) warp_max[warp] = amax;
     const float was = first > 0 ? *scale : 0.f;  // read before the team's first thread replaces it
     __syncthreads();
+    // the next head's elements, while this one's, held in registers, are rounded and stored
+    if (turns <= kPieces && l + 1 < p.loops) stage(l + 1);
     const int warps = 1 << (p.team_log2 - 5);  // of the team
     for (int w = 0; w < warps; ++w) amax = fmaxf(amax, warp_max[team * warps + w]);
     int e = scale_exponent(amax);
@@ -282,6 +288,10 @@ __device__ __forceinline__ void append_pages(const AppendRopeParams& p, int bloc
       }
     }
     if (tid == 0 && on) *scale = pow2f(e);
+    if (turns > kPieces && l + 1 < p.loops) {
+      __syncthreads();  // this head's elements have been read
+      stage(l + 1);
+    }
   }
 }
 
