@@ -12,9 +12,9 @@
 // a key goes from fp32 to its code without a rounding to bf16 between.
 // Measured, 32 query and 8 key / value heads of 128: 64 single tokens 4.8 us, 32 trees of 17 to 64
 // nodes 14 us (4.2 at the rate of a copy), 12 prompts of 257 to 2048 tokens, half of each head turned, pages of 32,
-// 56 us (42); 5 prompts of 900 to 4001 in fp32, 16 and 16 heads of 64, 60 us (35).  Small calls are lookups one behind
+// 55 us (42); 5 prompts of 900 to 4001 in fp32, 16 and 16 heads of 64, 57 us (35).  Small calls are lookups one behind
 // the other; large ones issue in half of their cycles: sines, roundings and the maximum beside the copies, with
-// 32 warps per SM (24 in fp32).
+// 24 warps per SM.
 #include <type_traits>
 
 #include "cache_rows.cuh"
@@ -296,7 +296,7 @@ __device__ __forceinline__ void append_pages(const AppendRopeParams& p, int bloc
 }
 
 template <typename WAY>
-__global__ void __launch_bounds__(kThreads, sizeof(typename WAY::T) == 4 ? 3 : 4)
+__global__ void __launch_bounds__(kThreads, 3)  // (with 4 registers are spilled: prompts 54.9 us, 54.6)
     append_rope_kernel(const __grid_constant__ AppendRopeParams p) {
   // one of each kind in turn, then the rest of the longer kind
   const int x = blockIdx.x, pages = p.page_ctas, rows = int(gridDim.x) - pages, both = 2 * min(pages, rows);
