@@ -29,8 +29,9 @@
 // TMEM columns: S of M tile m, step f of a tile at 128 m + 64 f; O at 256 + 128 m.
 // Waits are those of cache_tree.cuh; each role waits only for an earlier tile's events of the
 // others, or for this tile's by a role that comes before it (line, pages, queries and keys, S,
-// softmax, values, P V).  Warps of the softmax meet without a bound at a segment's beginning and end:
-// all come there, whatever ran out, and leave together.
+// softmax, values, P V).  No barrier's phase ends a second time before all who wait for it have seen the
+// first: they bring something, or free a place, that the second one needs.  Warps of the softmax meet
+// without a bound at a segment's beginning and end: all come there, whatever ran out, and leave together.
 #include <algorithm>
 #include <cmath>
 
@@ -87,7 +88,7 @@ struct ManyCfg {
   static constexpr int OFF_ROWS = OFF_STATS + 2 * kTile * 8;  // [M tile][row]: the queries' factors
   static constexpr int OFF_SEG = OFF_ROWS + 2 * kTile * 4;
   static constexpr int OFF_BAR = OFF_SEG + NSEG * 48;
-  static constexpr int B_SEGFULL = 0, B_SEGFREE = B_SEGFULL + NSEG, B_Q = B_SEGFREE + NSEG, B_KFULL = B_Q + 2,
+  static constexpr int B_SEGFULL = 0, B_SEGFREE = B_SEGFULL + NSEG, B_Q = B_SEGFREE + NSEG, B_KFULL = B_Q + 2 * NSEG,
                        B_KFREE = B_KFULL + NK, B_RFULL = B_KFREE + NK, B_RFREE = B_RFULL + NR, B_VFULL = B_RFREE + NR,
                        B_VFREE = B_VFULL + NV, B_SCLFULL = B_VFREE + NV, B_SCLFREE = B_SCLFULL + NSCL,
                        B_SFULL = B_SCLFREE + NSCL, B_PFULL = B_SFULL + 4, B_PDONE = B_PFULL + 4, B_OFREE = B_PDONE + 4,
@@ -104,6 +105,11 @@ struct ManyCfg {
            : i >= B_Q ? 4
            : i >= B_SEGFREE ? LINE : 1;  // the warps before that one
   }
+  // The queries of segment s and M tile m: a barrier for each place of the segments' ring.  An issuer frees the
+  // place only once it has seen them, so that no phase can end twice while it looks for it, in a segment
+  // without a tile of its own too.
+  __device__ static int queries(int s, int m) { return B_Q + 2 * (s % NSEG) + m; }
+  __device__ static uint32_t queries_parity(int s) { return uint32_t(s / NSEG) & 1u; }
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int USED = OFF_MISC + 16 + 1024;        // the base is aligned to 1024
   // one CTA per SM: it takes all of TMEM
@@ -150,8 +156,8 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = misc[0];
 
-  // The s-th segment, copied from its place in the ring; one arrival frees that.
-  auto segment = [&](int s, Segment& g, bool single) {
+  // The s-th segment, copied from its place in the ring; one arrival frees that (an issuer of S brings it later).
+  auto segment = [&](int s, Segment& g, bool single, bool later = false) {
     const int at = s % C::NSEG;
     const bool ok = single ? tree_wait(bar(C::B_SEGFULL + at), uint32_t(s / C::NSEG) & 1u, abort_flag, 1)
                            : tree_warp_wait(bar(C::B_SEGFULL + at), uint32_t(s / C::NSEG) & 1u, abort_flag, 1);
@@ -160,6 +166,7 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
     const int4* w = reinterpret_cast<const int4*>(sbase + C::OFF_SEG + at * 48);
     const int4 x = w[0], y = w[1], z = w[2];
     g = Segment{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, z.x, z.y};
+    if (later) return true;
     if (single) ptx::mbar_arrive(bar(C::B_SEGFREE + at));
     else warp_arrive(bar(C::B_SEGFREE + at), lane);
     return true;
@@ -333,12 +340,19 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
         int T0 = 0, turn = 0;  // turn: this M tile's tiles so far
         bool ok = true;
 #pragma unroll 1
-        for (int s = 0; ok && segment(s, g, true) && g.tiles; ++s) {
+        for (int s = 0; ok && segment(s, g, true, true) && g.tiles; ++s) {
           const bool twin = g.rows <= kTile;
+          // (A build may hold back the second M tile's issuer in every segment, to test that the others do not
+          // get ahead of a phase that it still waits for.)
+#ifdef ATTN_TREE_LATE_NS
+          for (const uint64_t t0 = ptx::globaltimer(); m == 1 && ptx::globaltimer() - t0 < ATTN_TREE_LATE_NS;) {
+          }
+#endif
           // (Behind both M tiles' end of the segment before.  Sooner, the tile two places before this one's first, the
           // other issuer's, may be on its way still, and a wait for a phase's parity would not tell it from it.)
-          ok = tree_wait(bar(C::B_Q + m), uint32_t(s) & 1u, abort_flag, 6) &&
-               (!twin || tree_wait(bar(C::B_Q + 1 - m), uint32_t(s) & 1u, abort_flag, 6));
+          ok = tree_wait(bar(C::queries(s, m)), C::queries_parity(s), abort_flag, 6) &&
+               (!twin || tree_wait(bar(C::queries(s, 1 - m)), C::queries_parity(s), abort_flag, 6));
+          if (ok) ptx::mbar_arrive(bar(C::B_SEGFREE + s % C::NSEG));
           const uint64_t qhi = qd + (twin ? 0 : uint64_t(m) * (2 * C::KT >> 4)), qlo = qhi + (C::KT >> 4);
 #pragma unroll 1
           for (int j = twin ? m : 0; ok && j < g.tiles; j += twin ? 2 : 1, ++turn) {
@@ -526,11 +540,11 @@ __global__ void __launch_bounds__(ManyCfg<D>::THREADS, 1)
         }
       }
       ptx::fence_proxy_async_smem();
-      warp_arrive(bar(C::B_Q + m), lane);
+      warp_arrive(bar(C::queries(s, m)), lane);
       // (brought by other warps)
       if (twin)
-        ok = tree_warp_wait(bar(C::B_Q), uint32_t(s) & 1u, abort_flag, 18) &&
-             tree_warp_wait(bar(C::B_Q + 1), uint32_t(s) & 1u, abort_flag, 18);
+        ok = tree_warp_wait(bar(C::queries(s, 0)), C::queries_parity(s), abort_flag, 18) &&
+             tree_warp_wait(bar(C::queries(s, 1)), C::queries_parity(s), abort_flag, 18);
       const float qscale = factors[row];
 
       float mx = kNoReference;                 // the weights' reference (a score + value exponent)
