@@ -785,7 +785,7 @@ def attn_cache_tree_build(parents: torch.Tensor, cache: KVCache, cu_seqlens: tor
     a row of ``bits`` (int32 [T, words], words = ceil(max_new / 32) in a new one) is set
     for the node itself and its ancestors; ``positions`` (int32 [T]) are the length of
     the text plus the number of ancestors.  Rows behind the last sequence are left as
-    they were."""
+    they were; results that overlap the inputs or each other are refused."""
     where = "attn_cache_tree_build"
     _need_cache(cache, where)
     dev, index = cache.device, cache.index
@@ -947,8 +947,8 @@ def attn_cache_tree_keep(path: torch.Tensor, counts: torch.Tensor, cache: KVCach
     """Keep the accepted path of each drafted tree: of sequence b's n new tokens those of
     the numbers path[b, :counts[b]] (int32 [B, width], ascending) move together behind
     the text, and the others are given up.  Returns the new lengths
-    seq_lens[b] - n + counts[b] (int32 [B]; not ``seq_lens`` itself, which every layer's
-    cache still needs)."""
+    seq_lens[b] - n + counts[b] (int32 [B]; ``new_lens`` overlaps none of the inputs: every
+    layer's cache still needs ``seq_lens``)."""
     where = "attn_cache_tree_keep"
     _need_cache(cache, where)
     dev, index, B = cache.device, cache.index, cache.batch

@@ -3,6 +3,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <utility>
 
 #include "cache.cuh"
 
@@ -14,6 +15,12 @@ constexpr double kPi = 3.14159265358979323846;
 constexpr int kMaxBatch = 65535, kMaxHeads = 32767;
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Arrays of m and n 32-bit numbers that share some.
+bool overlap(const void* a, int64_t m, const void* b, int64_t n) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && m > 0 && n > 0 && x < y + uintptr_t(n) * 4 && y < x + uintptr_t(m) * 4;
+}
 
 // The cache's own fields, and the view the kernels take.
 attn_status check_cache(const attn_kv_cache* c, CacheView* v) {
@@ -330,6 +337,12 @@ attn_status attn_cache_tree_build(const int32_t* parents, int32_t total_tokens, 
                         static_cast<const void*>(positions)})
     if (!aligned(p, 4)) return ATTN_ERR_INVALID_ARG;
   if (total_tokens == 0 || max_new == 0) return ATTN_OK;
+  // results over what other CTAs still read: a walk would go by them
+  const int64_t words = int64_t(total_tokens) * tree_words, batch = cache->batch;
+  if (overlap(tree_bits, words, positions, total_tokens)) return ATTN_ERR_INVALID_ARG;
+  for (const auto& in : {std::pair<const void*, int64_t>(parents, total_tokens), {cu_seqlens, batch + 1}, {seq_lens, batch}})
+    if (overlap(tree_bits, words, in.first, in.second) || overlap(positions, total_tokens, in.first, in.second))
+      return ATTN_ERR_INVALID_ARG;
   a.parents = parents;
   a.bits = tree_bits;
   a.positions = positions;
@@ -430,7 +443,10 @@ attn_status attn_cache_tree_keep(const int32_t* path, int32_t path_stride, const
                         static_cast<const void*>(new_lens)})
     if (!aligned(p, 4)) return ATTN_ERR_INVALID_ARG;
   // written while others still read the old ones
-  if (new_lens == seq_lens || new_lens == counts || new_lens == cu_seqlens) return ATTN_ERR_INVALID_ARG;
+  const int64_t batch = cache->batch;
+  for (const auto& in : {std::pair<const void*, int64_t>(path, batch * path_stride), {counts, batch},
+                         {cu_seqlens, batch + 1}, {seq_lens, batch}})
+    if (overlap(new_lens, batch, in.first, in.second)) return ATTN_ERR_INVALID_ARG;
   a.path = path;
   a.counts = counts;
   a.new_lens = new_lens;

@@ -42,6 +42,7 @@ extern "C" {
  *                of the node's ancestors, for attn_cache_append_rope and attn_rope
  *   cu_seqlens, seq_lens, max_new   as for attn_cache_append(); of the cache only
  *                its sizes and status word are used
+ * The results overlap neither each other nor the inputs (refused).
  */
 ATTN_API attn_status attn_cache_tree_build(const int32_t* parents, int32_t total_tokens,
                                            const int32_t* cu_seqlens, const int32_t* seq_lens,
@@ -108,7 +109,7 @@ ATTN_API attn_status attn_cache_tree_fwd(const void* q, void* o, float* lse, att
  *                entries from counts[b] on are not read.  A sequence whose path is
  *                not ascending or names nodes it does not have is left out.
  *   counts       device int32[batch], 0 <= counts[b] <= n and path_stride
- *   new_lens     device int32[batch]; not seq_lens, counts or cu_seqlens themselves
+ *   new_lens     device int32[batch]; overlaps none of the inputs (refused)
  *   max_new      at least every sequence's number of new tokens
  * A page that receives tokens from pages with a larger scale takes the largest of
  * them, and all its codes of tokens are re-scaled (rounded only where they fall below
