@@ -76,7 +76,8 @@ __device__ __forceinline__ float turned_x(float x, float y, float2 c) { return _
 __device__ __forceinline__ float turned_y(float x, float y, float2 c) { return __fmaf_rn(y, c.x, __fmul_rn(x, c.y)); }
 
 // The position of row t and whether it has one.  CHECKED: only rows of sequences that
-// an append would use have one, positions given or not.
+// an append would use have one, positions given or not, and all of those do, whatever stands
+// beside them in a malformed cu.  Called by whole warps.
 template <bool CHECKED>
 __device__ __forceinline__ bool position_of(const RopeParams& p, int t, int& pos) {
   const RopeArgs& a = p.a;
@@ -91,11 +92,25 @@ __device__ __forceinline__ bool position_of(const RopeParams& p, int t, int& pos
     if (a.cu[m] <= t) b0 = m; else b1 = m;
   }
   if (CHECKED) {
-    SeqRows r;
-    if (!load_rows(a.cu, a.lens, b0, a.total_tokens, p.check.max_new, p.check.max_len, p.check.status, r, false) ||
-        r.len < r.n || t < r.q0 || t >= r.q0 + r.n)
-      return false;
-    pos = a.positions ? a.positions[t] : r.len - r.n + t - r.q0;
+    int slot;  // of the row's token, -1 where the sequence is not used or does not hold the row
+    auto look = [&](int b) {
+      SeqRows r;
+      const bool mine = load_rows(a.cu, a.lens, b, a.total_tokens, p.check.max_new, p.check.max_len, p.check.status, r, false) &&
+                        r.len >= r.n && t >= r.q0 && t < r.q0 + r.n;
+      slot = mine ? r.len - r.n + t - r.q0 : -1;
+    };
+    look(b0);
+    if (__builtin_expect(slot < 0, 0)) {
+      // a row of no sequence, or a cu that does not ascend and led the search astray: look at every one
+#pragma unroll 1
+      for (int b = int(threadIdx.x & 31u); b < ((a.batch + 31) & ~31); b += 32) {
+        if (b < a.batch) look(b);
+        slot = __reduce_max_sync(0xffffffffu, slot);
+        if (slot >= 0) break;
+      }
+      if (slot < 0) return false;
+    }
+    pos = a.positions ? a.positions[t] : slot;
     return true;
   }
   const int s0 = a.cu[b0], s1 = a.cu[b0 + 1];
