@@ -92,22 +92,20 @@ __device__ __forceinline__ bool position_of(const RopeParams& p, int t, int& pos
     if (a.cu[m] <= t) b0 = m; else b1 = m;
   }
   if (CHECKED) {
-    int slot;  // of the row's token, -1 where the sequence is not used or does not hold the row
+    // the slot of the row's token, -1 where the sequence is not used or does not hold the row
     auto look = [&](int b) {
       SeqRows r;
       const bool mine = load_rows(a.cu, a.lens, b, a.total_tokens, p.check.max_new, p.check.max_len, p.check.status, r, false) &&
                         r.len >= r.n && t >= r.q0 && t < r.q0 + r.n;
-      slot = mine ? r.len - r.n + t - r.q0 : -1;
+      return mine ? r.len - r.n + t - r.q0 : -1;
     };
-    look(b0);
+    int slot = look(b0);
     if (__builtin_expect(slot < 0, 0)) {
-      // a row of no sequence, or a cu that does not ascend and led the search astray: look at every one
-#pragma unroll 1
-      for (int b = int(threadIdx.x & 31u); b < ((a.batch + 31) & ~31); b += 32) {
-        if (b < a.batch) look(b);
-        slot = __reduce_max_sync(0xffffffffu, slot);
-        if (slot >= 0) break;
-      }
+      // a row of no sequence, or a cu that does not ascend and led the search astray: look at all that may hold it
+#pragma unroll 4
+      for (int b = int(threadIdx.x & 31u); b < a.batch; b += 32)
+        if (__ldg(a.cu + b) <= t && t < __ldg(a.cu + b + 1)) slot = max(slot, look(b));
+      slot = __reduce_max_sync(0xffffffffu, slot);
       if (slot < 0) return false;
     }
     pos = a.positions ? a.positions[t] : slot;
