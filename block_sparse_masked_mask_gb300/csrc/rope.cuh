@@ -75,6 +75,30 @@ __device__ __forceinline__ void from_f(__nv_bfloat16& d, float x) { d = __float2
 __device__ __forceinline__ float turned_x(float x, float y, float2 c) { return __fmaf_rn(x, c.x, -__fmul_rn(y, c.y)); }
 __device__ __forceinline__ float turned_y(float x, float y, float2 c) { return __fmaf_rn(y, c.x, __fmul_rn(x, c.y)); }
 
+// The slot of row t's token in sequence b; -1 where that is not used or does not hold the row.
+__device__ __forceinline__ int slot_of(const int32_t* cu, const int32_t* lens, int t, int b, int total_tokens, int max_new,
+                                       int max_len) {
+  SeqRows r;
+  const bool mine = load_rows(cu, lens, b, total_tokens, max_new, max_len, nullptr, r, false) && r.len >= r.n && t >= r.q0 &&
+                    t < r.q0 + r.n;
+  return mine ? r.len - r.n + t - r.q0 : -1;
+}
+
+// The same in any of them, by a whole warp: for a row of none, and where a cu that does not ascend leads a search
+// astray.  (Out of line: 12 prompts 55 us, 58 with its code among what all run.)
+__device__ __noinline__ int slot_of_any(const int32_t* cu, const int32_t* lens, int t, int batch, int total_tokens, int max_new,
+                                        int max_len) {
+  const int lane = int(threadIdx.x & 31u);
+  bool some = false;  // most often none
+#pragma unroll 8
+  for (int b = lane; b < batch; b += 32) some |= __ldg(cu + b) <= t && t < __ldg(cu + b + 1);
+  if (!__any_sync(0xffffffffu, some)) return -1;
+  int slot = -1;
+#pragma unroll 1
+  for (int b = lane; b < batch; b += 32) slot = max(slot, slot_of(cu, lens, t, b, total_tokens, max_new, max_len));
+  return __reduce_max_sync(0xffffffffu, slot);
+}
+
 // The position of row t and whether it has one.  CHECKED: only rows of sequences that
 // an append would use have one, positions given or not, and all of those do, whatever stands
 // beside them in a malformed cu.  Called by whole warps.
@@ -92,22 +116,10 @@ __device__ __forceinline__ bool position_of(const RopeParams& p, int t, int& pos
     if (a.cu[m] <= t) b0 = m; else b1 = m;
   }
   if (CHECKED) {
-    // the slot of the row's token, -1 where the sequence is not used or does not hold the row
-    auto look = [&](int b) {
-      SeqRows r;
-      const bool mine = load_rows(a.cu, a.lens, b, a.total_tokens, p.check.max_new, p.check.max_len, p.check.status, r, false) &&
-                        r.len >= r.n && t >= r.q0 && t < r.q0 + r.n;
-      return mine ? r.len - r.n + t - r.q0 : -1;
-    };
-    int slot = look(b0);
-    if (__builtin_expect(slot < 0, 0)) {
-      // a row of no sequence, or a cu that does not ascend and led the search astray: look at all that may hold it
-#pragma unroll 4
-      for (int b = int(threadIdx.x & 31u); b < a.batch; b += 32)
-        if (__ldg(a.cu + b) <= t && t < __ldg(a.cu + b + 1)) slot = max(slot, look(b));
-      slot = __reduce_max_sync(0xffffffffu, slot);
-      if (slot < 0) return false;
-    }
+    int slot = slot_of(a.cu, a.lens, t, b0, a.total_tokens, p.check.max_new, p.check.max_len);
+    if (__builtin_expect(slot < 0, 0))
+      slot = slot_of_any(a.cu, a.lens, t, a.batch, a.total_tokens, p.check.max_new, p.check.max_len);
+    if (slot < 0) return false;
     pos = a.positions ? a.positions[t] : slot;
     return true;
   }
