@@ -327,9 +327,12 @@ cudaError_t launch_t(AppendRopeParams& p, cudaStream_t s) {
   p.groups = 2 * p.key_groups;
   p.page_ctas = int(pages * p.groups);
   const int smem = p.pieces * Staged<T>::PARTS * kThreads * 16 + most * (p.rope.rot / 2) * int(sizeof(float2));
+  // The limit is the kernel's, so every call sets the same one, the most that any asks for: by its own need, another host
+  // thread could lower it between here and the launch.
+  constexpr int kMostSmem = 128 * 128 * int(sizeof(T)) + 128 * ATTN_ROPE_MAX_PAIRS * int(sizeof(float2));
   auto launch = [&](auto way, int64_t ctas) {
     auto kernel = append_rope_kernel<decltype(way)>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
     if (e != cudaSuccess) return e;
     kernel<<<unsigned(p.page_ctas + ctas), kThreads, smem, s>>>(p);
     return cudaGetLastError();

@@ -1,5 +1,5 @@
-"""The rotated append where its parts have to agree: batches in which good sequences
-stand behind bad ones."""
+"""The rotated append where its parts have to agree (batches in which good sequences
+stand behind bad ones), and from several host threads."""
 import numpy as np
 import pytest
 import torch
@@ -50,3 +50,45 @@ def test_queries_and_keys_of_the_same_sequences(cu, T, rot, inter, given):
     for i in good:
         mine[cu[i]:cu[i + 1]] = True
     assert torch.equal(again[mine], want[mine]) and torch.equal(again[~mine], q[~mine])
+
+
+def test_host_threads_of_very_different_calls():
+    """Calls of one kernel from several host threads, each on a stream and a cache of its own, that ask for very
+    different amounts of shared memory: none is refused, and all store what a call alone stores."""
+    import ctypes
+    import threading
+
+    from block_sparse_masked_mask_gb300 import _native
+    plan, heads, dim, ps = api.attn_rope_plan(128), 2, 128, 128
+    fn, sides = _native.lib().attn_cache_append_rope, []
+    for n in (1, 128, 20):
+        stream, p = torch.cuda.Stream(), Pair([n], heads, dim, ps, seed=n)
+        q, k, v = (randn(n, h, dim, seed=h).cuda() for h in (4, heads, heads))
+        x = dict(n=n, p=p, q=q, k=k, v=v, cu=dev([0, n]), lens=dev([n]), out=torch.empty_like(q), stream=stream, bad=[])
+        x["want"] = api.attn_cache_append_rope(q, k, v, plan, p.dev, x["cu"], x["lens"], n)
+        x["state"] = [getattr(p.dev, name).clone() for name in STATE]
+        x["args"] = (q.data_ptr(), x["out"].data_ptr(), 4 * dim, 4 * dim, 4, k.data_ptr(), v.data_ptr(), heads * dim, heads * dim, 0, n,
+                     None, x["cu"].data_ptr(), x["lens"].data_ptr(), n, ctypes.byref(plan.struct), p.dev._ref, stream.cuda_stream)
+        sides.append(x)
+    torch.cuda.synchronize()
+    start = threading.Barrier(len(sides))
+
+    def calls(x):
+        start.wait()
+        for i in range(6000):
+            status = fn(*x["args"])
+            if status != api.ATTN_OK:
+                x["bad"].append((i, status))
+            if i % 64 == 63:
+                x["stream"].synchronize()
+
+    threads = [threading.Thread(target=calls, args=(x,)) for x in sides]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for x in sides:
+        assert not x["bad"], (x["n"], len(x["bad"]), x["bad"][0])
+        assert torch.equal(x["out"], x["want"]) and api.attn_cache_get_status(x["p"].dev) == api.ATTN_OK
+        assert all(torch.equal(getattr(x["p"].dev, name), y) for name, y in zip(STATE, x["state"]))
