@@ -784,7 +784,8 @@ def attn_cache_tree_build(parents: torch.Tensor, cache: KVCache, cu_seqlens: tor
     the node's own, or -1.  Returns (bits, positions): bit j % 32 of word j / 32 of
     a row of ``bits`` (int32 [T, words], words = ceil(max_new / 32) in a new one) is set
     for the node itself and its ancestors; ``positions`` (int32 [T]) are the length of
-    the text plus the number of ancestors.  Rows behind the last sequence are left as
+    the text that is held plus the number of ancestors (behind an eviction the caller adds
+    the number of tokens dropped).  Rows behind the last sequence are left as
     they were; results that overlap the inputs or each other are refused."""
     where = "attn_cache_tree_build"
     _need_cache(cache, where)

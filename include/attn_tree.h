@@ -18,6 +18,9 @@
  *   tree_bits stands for node j.  attn_cache_tree_build sets those of the node
  *   and of its ancestors; any other masks serve as well.
  *
+ * attn_cache_weights has no tree masks: tokens are weighed for an eviction by
+ * queries that see a chain, such as those of plain steps.
+ *
  * Conventions are those of attn_cache.h: device pointers owned by the caller,
  * packed batches, no allocation, asynchronous calls, status codes, and what the
  * device finds wrong in the cache's status word, with the sequence left out.
@@ -39,7 +42,9 @@ extern "C" {
  *   tree_bits    device uint32 [total_tokens, tree_words], all words written;
  *                32 * tree_words >= max_new
  *   positions    device int32[total_tokens] or NULL: seq_lens[b] - n + the number
- *                of the node's ancestors, for attn_cache_append_rope and attn_rope
+ *                of the node's ancestors, for attn_cache_append_rope and attn_rope.
+ *                Where an eviction has shortened the sequence, that is not where it
+ *                stands in its text: the caller adds the number of tokens dropped
  *   cu_seqlens, seq_lens, max_new   as for attn_cache_append(); of the cache only
  *                its sizes and status word are used
  * The results overlap neither each other nor the inputs (refused).
