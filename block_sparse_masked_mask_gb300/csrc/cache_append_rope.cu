@@ -10,11 +10,16 @@
 // share the sines and cosines of the page's tokens, a table in shared memory.  The turned
 // elements stay in registers, 32 bits each, for their largest magnitude and their codes, so that
 // a key goes from fp32 to its code without a rounding to bf16 between.
-// Measured, 32 query and 8 key / value heads of 128: 64 single tokens 4.8 us, 32 trees of 17 to 64
+// Measured, 32 query and 8 key / value heads of 128: 64 single tokens 4.7 us, 32 trees of 17 to 64
 // nodes 14 us (4.2 at the rate of a copy), 12 prompts of 257 to 2048 tokens, half of each head turned, pages of 32,
-// 55 us (42); 5 prompts of 900 to 4001 in fp32, 16 and 16 heads of 64, 57 us (35).  Small calls are lookups one behind
-// the other; large ones issue in half of their cycles: sines, roundings and the maximum beside the copies, with
-// 24 warps per SM.
+// 55 us (42); 5 prompts of 900 to 4001 in fp32, 16 and 16 heads of 64, 57 us (35).  One token each is lookups one
+// behind the other.  The trees are 1024 CTAs for pages, of which 456 run at a time (and 224 find no page), each with that
+// chain and its loads, turns, maximum and stores once, beside 160 for the queries; fewer CTAs of longer chains
+// take longer (launch_t).  Prompts issue in half of their cycles (58%, fp32 47%): sines, roundings and the
+// maximum beside the copies, with 24 warps per SM, where three CTAs fit its shared memory.  They do not with
+// pages of 128 x 128 turned whole, whose angles take 64 KB beside 32 KB of elements (fp32 64): two CTAs per SM, or
+// one, the queries' among them, and keys are turned twice (the 12 prompts turned whole, pages of 32 / 64 / 128:
+// 59 / 61 / 86 us; 128 in fp32 163, 81 at the rate of a copy).
 #include <type_traits>
 
 #include "cache_rows.cuh"
@@ -320,7 +325,9 @@ cudaError_t launch_t(AppendRopeParams& p, cudaStream_t s) {
   const int64_t each = (int64_t(a.max_new) + page_size - 2) / page_size + 1;
   const int64_t bound = a.total_tokens / page_size + 2ll * c.batch;
   const int64_t pages = each * c.batch < bound ? each * c.batch : bound;
-  // Heads in turn share a table of angles; as many as leave four CTAs for each SM.
+  // Heads in turn share a table of angles, and one's elements are fetched while another's are stored; but few CTAs of
+  // long chains begin and end unevenly.  As many as leave 608 CTAs for the pages (by 1 / 2 / 4 / 8: 32 trees
+  // 14.3 / 15.3 / 18.6 / 26.4 us, 12 prompts 60.8 / 56.7 / 54.7 / 54.8, 5 in fp32 70.6 / 63.2 / 57.1 / 56.3).
   p.loops = 1;
   while (p.loops * teams < c.heads && pages * ((c.heads + 2 * p.loops * teams - 1) / (2 * p.loops * teams)) * 2 >= 4 * 152) p.loops *= 2;
   p.key_groups = (c.heads + p.loops * teams - 1) / (p.loops * teams);

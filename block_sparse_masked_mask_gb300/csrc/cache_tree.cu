@@ -30,13 +30,14 @@
 //   15         the line: the CTA's segments
 //
 // What bounds it: 64 trees of 4 to 8 nodes behind 1024 to 16384 tokens, 32 query and 8 key heads of
-// 128, take 139 us where the bytes take 108 at the rate of a copy; 16 sequences of 8192 tokens, 16 / 32 / 64
-// rows a head, 55 / 58 / 73 us (40).  It is the instructions'
+// 128, take 137 us where the bytes take 108 at the rate of a copy; 16 sequences of 8192 tokens, 16 / 32 / 64
+// rows a head, 55 / 59 / 71 us (40).  Heads of 64 or 32 take as long as those of 128 (139 us both): it is
+// not the bytes but the softmax, a score as dear as any other, and the instructions'
 // supply more than their issue: with five roles' loops at once, warps wait for instructions
 // more than for anything else, and each step that made the code shorter (loops rolled up, one form of
 // waits, rare paths out of line) was worth more than one that took operations out.  Four
 // warpgroups for the softmax, or factors held ready across its loop, were no faster.
-// One tree of 16 nodes behind 2049 tokens takes 17 us: the kernels' start, one tile, the join.
+// One tree of 16 nodes behind 2049 tokens takes 18 us: the kernels' start, one tile, the join.
 //
 // Every wait is bounded and ends in ATTN_ERR_DEVICE_TIMEOUT in the cache's status word.
 // Each role waits only for an earlier tile's events of the others, or for this
@@ -59,8 +60,8 @@ struct Segment {
   int b, h, rows, q0, n, len, token, slot;  // slot of the partial result, -1: whole
 };
 
-// A segment's start and end cost as much as three tiles (64 trees of 4 to 8 nodes: taken for 0 156 us, 2 139, 4 140,
-// 7 145, 11 152); pieces of less than two tiles' cost gain nothing (a tree of 16 nodes behind 1024
+// A segment's start and end cost as much as three tiles (64 trees of 4 to 8 nodes, heads of 128 / 64 / 32: taken for 0
+// 154 / 154 / 152 us, 2 137 / 143 / 140, 3 137 / 139 / 139, 4 138 / 141 / 141, 7 144 / 146 / 145); pieces of less than two tiles' cost gain nothing (a tree of 16 nodes behind 1024
 // tokens: from 1 17.4 us, 2 16.5, 4 17.9, 6 19.4).
 template <int N>
 using Line = TreeLine<N, 1, 1, 3, 2>;
@@ -867,7 +868,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_tree_join_kernel(const 
 }
 
 // Rows are padded to the least of these; 0: cache_tree_many.cu takes them, 128 or 256 rows of a sequence
-// and head at a time (16 sequences of 8192 tokens, 8 heads: 64 rows 73 us here, 128 rows 89 us there; 128 rows
+// and head at a time (16 sequences of 8192 tokens, 8 heads: 64 rows 71 us here, 128 rows 87 us there; 128 rows
 // as N of the products here took 112).
 int padded_rows(const CacheView& c, int num_heads, int max_new) {
   const int64_t rows = int64_t(max_new) * (num_heads / c.heads);

@@ -11,8 +11,8 @@
 // line, counted by what they cost, that is cut evenly among one CTA per SM (TreeLine in cache_tree.cuh).  A CTA
 // walks its piece segment by segment: page numbers, keys and values of the next one are under way while
 // the last one ends.  Segments that are not whole meet in a second kernel, two per CTA at most.
-// 32 trees of 17 to 32 nodes behind 1024 to 16384 tokens, 32 query and 8 key heads of 128, take 115 us, and
-// 8 trees of 48 to 64 nodes, 64 and 8 heads, behind 4096 to 16384 tokens 129 us (the kernel of
+// 32 trees of 17 to 32 nodes behind 1024 to 16384 tokens, 32 query and 8 key heads of 128, take 114 us, and
+// 8 trees of 48 to 64 nodes, 64 and 8 heads, behind 4096 to 16384 tokens 126 us (the kernel of
 // cache_chunk.cu with these masks, a CTA for 4096 tokens, took 155 and 157: starts and ends were a quarter of
 // it, and uneven).  Products of 128 rows fill the tensor cores to a half there; a tile takes about 1.4 us, most of it
 // the softmax's, which waits for its scores, its exponentials and the other warps' instructions in
@@ -43,7 +43,8 @@ namespace {
 
 constexpr int kTreeRows = 256;          // of a segment
 // What a tile of tokens costs, with up to 256 rows and with up to 128, and a segment's start and end
-// (32 trees of 17 to 32 nodes: 6 141 us, 10 129, 16 119, 20 115, 26 118, 34 122).
+// (32 trees of 17 to 32 nodes, heads of 128 / 64 / 32: 10 128 / 93 / 83 us, 16 119 / 88 / 81, 20 114 / 88 / 83,
+// 26 115 / 91 / 86).
 using Line = TreeLine<kTreeRows, 5, 3, 20, 5>;
 constexpr int kStep = 64;
 
@@ -72,7 +73,8 @@ template <int D>
 struct ManyCfg {
   static constexpr int THREADS = 640;
   static constexpr int VALUES = 8, PAGES = 12, ISSUE_S = 13, ISSUE_O = 15, LINE = 16;
-  // Registers for each thread of the softmax, the values and the others, of the launch's 96 for all
+  // Registers for each thread of the softmax, the values and the others, of the launch's 96 for all (with which
+  // the compiler spills 72 bytes a thread)
   static constexpr int REG_SOFTMAX = 144, REG_VALUES = 80, REG_OTHERS = 56;
   static_assert(2 * REG_SOFTMAX + REG_VALUES + 2 * REG_OTHERS == 5 * 96, "registers");
   using V = TileLayout<D>;                       // fp16 value tile: the 16-bit layout

@@ -65,7 +65,7 @@ ATTN_API attn_status attn_cache_tree_build(const int32_t* parents, int32_t total
  *   k, v, cu_seqlens, seq_lens, max_new   as for attn_cache_append()
  *   dtype        of q, k, v and q_out: bf16 or fp32
  *   positions    device int32[total_tokens], any value; or NULL: new token i of n
- *                stands at seq_lens[b] - n + i
+ *                stands at seq_lens[b] - n + i (not behind an eviction)
  *   plan         rotary_dim at most the cache's head_dim
  * Rows behind the last sequence and those of a sequence that is left out keep what
  * q_out held.
@@ -96,6 +96,10 @@ ATTN_API attn_status attn_cache_tree_fwd_workspace_size(const attn_kv_cache* cac
  * enters as the sum of two e4m3 numbers whatever the number of rows: with m the
  * largest magnitude of a row, its elements down to 2^-9 m are exact, and smaller ones
  * are off by 2^-17 m at most.
+ * max_new settles which kernel runs and how its rows are padded, for the lengths are
+ * the device's alone: a bound near the largest tree is faster than a wide one (64 trees of 4
+ * to 8 nodes with 4 query heads a group: 137 us with a bound of 8, 191 with 16, 198 with 64).
+ * Above 64 rows (max_new * G) the workspace is 40 MB at a head_dim of 128, whatever the batch.
  */
 ATTN_API attn_status attn_cache_tree_fwd(const void* q, void* o, float* lse, attn_dtype dtype,
                                          int32_t total_tokens, int32_t num_heads, float scale,
