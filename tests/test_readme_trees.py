@@ -54,7 +54,7 @@ def test_the_step_over_two_layers():
     rng = np.random.default_rng(1)
     pairs = [filled(list(text + 40), heads, dim, 32, seed=7 * i) for i in range(2)]
     plan, cu = api.attn_rope_plan(dim), cu_of(n)
-    for round_ in range(2):
+    for turn in range(2):
         lens = text + n
         parents = [random_parents(int(x), rng) for x in n]
         masks = [R.ancestors(x) for x in parents]
@@ -62,7 +62,7 @@ def test_the_step_over_two_layers():
         path = np.zeros((3, max(map(len, paths))), np.int32)
         for b, x in enumerate(paths):
             path[b, :len(x)] = x
-        qkv = [[randn(int(n.sum()), h, dim, seed=10 * round_ + 3 * i + j).cuda() for j, h in enumerate((4, heads, heads))] for i in range(2)]
+        qkv = [[randn(int(n.sum()), h, dim, seed=10 * turn + 3 * i + j).cuda() for j, h in enumerate((4, heads, heads))] for i in range(2)]
         seen = []
 
         def rest(layer, x, o):
